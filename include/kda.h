@@ -9,6 +9,10 @@
  *   kda_decode_conv_step      the decode step with its causal conv1d + SiLU fused in front
  *   kda_recurrent_step        T tokens per row (T <= 64) on a slot pool: speculative / extend steps
  *   kda_head_rmsnorm          output-side per-head RMSNorm of attention outputs
+ *   kda_add_rmsnorm           residual addition + RMSNorm of whole rows, optionally to 8 bits with scales
+ *   kda_linear                matrix product with scales, bias, activation and residual in its epilogue
+ *   kda_scan_fwd / _bwd       gated linear recurrence (one state per channel) and its gradients
+ *   kda_scan_step             the recurrence's single-token step on a slot pool
  *   kda_chunk_fwd_noalloc     kda_chunk_fwd on a library-owned scratch buffer (no allocation)
  *   kda_version               library version string
  *   kda_selftest_*            diagnostics: bounded-wait failure path, tcgen05 round trip
@@ -65,7 +69,9 @@ typedef enum {
 
 typedef enum {
   KDA_DTYPE_BF16 = 0,  /* q, k, v, beta/b and o in bfloat16; tensor-core path */
-  KDA_DTYPE_FP32 = 1   /* q, k, v, beta/b and o in float32; CUDA-core fp32 path */
+  KDA_DTYPE_FP32 = 1,  /* q, k, v, beta/b and o in float32; CUDA-core fp32 path */
+  KDA_DTYPE_E4M3 = 2   /* 8-bit floats (4 exponent, 3 mantissa bits, largest 448, no inf):
+                          kda_add_rmsnorm's output and kda_linear's operands only */
 } kda_dtype;
 
 typedef enum {
@@ -338,6 +344,175 @@ typedef struct kda_rmsnorm_args {
   void* y;
 } kda_rmsnorm_args;
 kda_status kda_head_rmsnorm(const kda_rmsnorm_args* args, kda_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The layer around the attention: residual + norm, projections, and a gated
+ * recurrence with one state per channel. These calls take row strides (in
+ * elements; the last axis is contiguous) and only need the natural alignment of
+ * an element: rows that start on 16-byte boundaries take wider accesses.
+ * No counterpart in the method's description; plain definitions below.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Residual addition and root-mean-square norm of R rows of D values:
+ *   r = x + residual                          (r = x without residual)
+ *   y = r / sqrt(mean(r^2) + eps) * weight
+ * and with y_dtype KDA_DTYPE_E4M3
+ *   m = max |y| of the row;  y_scale = m / 448 (at least 2^-126; 1 where m is 0 or NaN)
+ *   y stored = y / y_scale rounded to e4m3, so that y ~ stored * y_scale.
+ *   x, residual, residual_out  [R, D]  dtype (bf16 or fp32); residual and
+ *                              residual_out may be NULL. residual_out receives r
+ *                              rounded to dtype; y is formed from the unrounded r.
+ *   weight                     [D]     fp32
+ *   y                          [R, D]  y_dtype (bf16, fp32 or e4m3)
+ *   y_scale                    [R]     fp32, e4m3 only
+ * residual_out may be residual or x, and y may be x (same dtype and stride):
+ * a row is read whole before any of it is written. A NaN in a row makes that
+ * row's y NaN. 1 <= D <= KDA_NORM_MAX_D (KDA_ERR_UNSUPPORTED above). R = 0 is
+ * accepted and does nothing.
+ */
+#define KDA_NORM_MAX_D 32768
+typedef struct kda_add_rmsnorm_args {
+  int64_t R;
+  int32_t D;
+  int32_t dtype, y_dtype;  /* kda_dtype */
+  float eps;
+  int64_t x_stride, residual_stride, residual_out_stride, y_stride;
+  const void* x;
+  const void* residual;
+  const float* weight;
+  void* residual_out;
+  void* y;
+  float* y_scale;
+} kda_add_rmsnorm_args;
+kda_status kda_add_rmsnorm(const kda_add_rmsnorm_args* args, kda_stream_t stream);
+
+typedef enum {
+  KDA_ACT_NONE = 0,
+  KDA_ACT_SILU = 1,     /* v / (1 + e^-v) */
+  KDA_ACT_GELU = 2,     /* v (1 + erf(v / sqrt 2)) / 2 */
+  KDA_ACT_SIGMOID = 3,  /* 1 / (1 + e^-v) */
+  KDA_ACT_RELU = 4      /* max(v, 0), NaN kept */
+} kda_activation;
+
+/*
+ * Projection: y = act((x w^T) * x_scale[m] * w_scale[n] + bias[n]) + residual.
+ *   x         [M, K]  dtype, row stride ldx
+ *   w         [N, K]  dtype, row stride ldw (a row per output)
+ *   x_scale   [M]     fp32, w_scale [N] fp32: required for e4m3, must be NULL for bf16
+ *   bias      [N]     fp32 or NULL
+ *   residual  [M, N]  y_dtype, row stride ld_residual, or NULL; may be y (same stride)
+ *   y         [M, N]  y_dtype (bf16 or fp32), row stride ldy
+ * dtype is bf16 or e4m3 (both operands); products and sums are fp32, everything
+ * after them is fp32, and y is rounded once. M = 0 does nothing; N, K >= 1.
+ * A bounded wait that runs out writes KDA_ERR_TIMEOUT to err.
+ */
+typedef struct kda_linear_args {
+  int32_t M, N, K;
+  int32_t dtype, y_dtype;  /* kda_dtype */
+  int32_t activation;      /* kda_activation */
+  int64_t ldx, ldw, ld_residual, ldy;
+  const void* x;
+  const void* w;
+  const float* x_scale;
+  const float* w_scale;
+  const float* bias;
+  const void* residual;
+  void* y;
+  int32_t* err;            /* optional device status word */
+} kda_linear_args;
+kda_status kda_linear(const kda_linear_args* args, kda_stream_t stream);
+
+typedef enum {
+  KDA_SCAN_LOG_DECAY = 0,  /* a = exp(gate) */
+  KDA_SCAN_LOGITS = 1      /* a = sigmoid(gate) */
+} kda_scan_gate;
+#define KDA_SCAN_FLAG_COMPLEMENT 0x1u  /* input weighted by 1 - a */
+
+/*
+ * Gated linear recurrence, one fp32 state h per sequence and channel:
+ *   h_t = a_t h_{t-1} + u_t,   u_t = x_t, or (1 - a_t) x_t with KDA_SCAN_FLAG_COMPLEMENT
+ *   y_t = h_t
+ *   x, y        [B, T, D]  dtype (bf16 or fp32)
+ *   gate        [B, T, D]  gate_dtype (fp32, or bf16 when dtype is bf16)
+ *   h0, hT      [N, D]     fp32, either may be NULL
+ *   cu_seqlens  [N + 1]    as for kda_chunk_fwd (N = B without it)
+ *   h_chunks    [chunks, D] fp32 or NULL: the state entering every 16-token
+ *                          chunk, numbered as kda_chunk_fwd's (kda_scan_bwd reads it);
+ *                          h_chunks_rows says how many there is room for
+ * Strides are those of a token; the tokens of the batch follow one another.
+ * Sequences of length 0 are allowed (hT = h0, or 0 without h0).
+ * A cu_seqlens that does not start at 0, decreases or does not end at T, or one
+ * whose chunks h_chunks has no room for, writes KDA_ERR_INVALID_ARG to err and
+ * skips the call's work.
+ */
+typedef struct kda_scan_args {
+  int32_t dtype, gate_dtype;  /* kda_dtype */
+  int32_t B, T, D, N;
+  int32_t gate_mode;          /* kda_scan_gate */
+  uint32_t flags;             /* KDA_SCAN_FLAG_* */
+  int64_t x_stride, gate_stride, y_stride;
+  int64_t h_chunks_rows;      /* states that h_chunks has room for */
+  const void* x;
+  const void* gate;
+  const float* h0;
+  const int32_t* cu_seqlens;
+  void* y;
+  float* hT;
+  float* h_chunks;
+  int32_t* err;               /* optional device status word */
+} kda_scan_args;
+kda_status kda_scan_fwd(const kda_scan_args* args, kda_stream_t stream);
+
+/*
+ * Gradients of the recurrence from dy (of y) and dhT (of hT, NULL for zero):
+ *   d_t = dy_t + a_{t+1} d_{t+1}   (after the last token: dhT)
+ *   dx_t = d_t, or (1 - a_t) d_t;  dh0 = a_1 d_1
+ *   da_t = d_t h_{t-1}, or d_t (h_{t-1} - x_t)
+ *   dgate_t = a_t da_t (log decay), a_t (1 - a_t) da_t (logits)
+ * fwd holds the forward's arguments; fwd.h_chunks (required when there are
+ * tokens) is what kda_scan_fwd wrote for them, and fwd.h0, fwd.y and fwd.hT are
+ * ignored.
+ *   dy, dx  [B, T, D] dtype;  dgate [B, T, D] gate_dtype;  dhT, dh0 [N, D] fp32
+ * dh0 may be NULL. dx may be dy or x, and dgate may be gate (same strides).
+ */
+typedef struct kda_scan_bwd_args {
+  kda_scan_args fwd;
+  int64_t dy_stride, dx_stride, dgate_stride;
+  const void* dy;
+  const float* dhT;
+  void* dx;
+  void* dgate;
+  float* dh0;
+} kda_scan_bwd_args;
+kda_status kda_scan_bwd(const kda_scan_bwd_args* args, kda_stream_t stream);
+
+/*
+ * One token per row on a pool of states: row b with slot s = indices[b] computes
+ *   h = a h_in + u (as above),  state_out[s] = h,  y[b] = h
+ *   x, y       [B, D]          dtype;  gate [B, D] gate_dtype
+ *   state_in   [num_slots, D]  fp32; state_out may be state_in (in place); only
+ *                              the valid rows' slots of state_out are written
+ *   indices    [B]             int32, negative = padding row
+ * A padding row writes y = 0 and touches no state. An index >= num_slots writes
+ * KDA_ERR_INVALID_ARG to err and is treated as padding. Valid indices must be
+ * distinct (KDA_FLAG_CHECK_INDICES in flags checks it, and needs err).
+ */
+typedef struct kda_scan_step_args {
+  int32_t dtype, gate_dtype;  /* kda_dtype */
+  int32_t B, D, num_slots;
+  int32_t gate_mode;          /* kda_scan_gate */
+  uint32_t flags;             /* KDA_SCAN_FLAG_COMPLEMENT, KDA_FLAG_CHECK_INDICES */
+  int64_t x_stride, gate_stride, y_stride;
+  const void* x;
+  const void* gate;
+  const float* state_in;
+  float* state_out;
+  const int32_t* indices;
+  void* y;
+  int32_t* err;               /* optional device status word */
+} kda_scan_step_args;
+kda_status kda_scan_step(const kda_scan_step_args* args, kda_stream_t stream);
 
 /*
  * Chunk forward for callers that cannot allocate device memory.

@@ -11,13 +11,18 @@ from ._lib import (  # noqa: F401
     KdaError,
     chunk_count,
     chunk_workspace_size,
+    kda_add_rmsnorm,
     kda_chunk_fwd,
     kda_chunk_output,
     kda_chunk_fwd_noalloc,
     kda_decode_conv_step,
     kda_decode_step,
     kda_head_rmsnorm,
+    kda_linear,
     kda_recurrent_step,
+    kda_scan_bwd,
+    kda_scan_fwd,
+    kda_scan_step,
     lib_path,
     load,
     make_chunk_args,

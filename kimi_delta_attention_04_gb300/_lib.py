@@ -8,6 +8,7 @@ tensor is not on a CUDA device, the call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import threading
 from pathlib import Path
@@ -30,11 +31,16 @@ KDA_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 KDA_DTYPE_BF16 = 0
 KDA_DTYPE_FP32 = 1
+KDA_DTYPE_E4M3 = 2
 KDA_GATE_NONE, KDA_GATE_G, KDA_GATE_INPUTS, KDA_GATE_HEAD_G = 0, 1, 2, 3
 KDA_BETA_VALUES, KDA_BETA_LOGITS = 0, 1
 KDA_FLAG_L2NORM_QK = 0x1
 KDA_FLAG_DELTA_OFF = 0x2
 KDA_FLAG_CHECK_INDICES = 0x4
+KDA_NORM_MAX_D = 32768
+KDA_ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "sigmoid": 3, "relu": 4}
+KDA_SCAN_GATES = {"log": 0, "logits": 1}
+KDA_SCAN_FLAG_COMPLEMENT = 0x1
 
 
 class KdaError(RuntimeError):
@@ -97,6 +103,54 @@ class RmsNormArgs(ctypes.Structure):
     ]
 
 
+class AddRmsNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("R", ctypes.c_int64), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+        ("residual_out_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("x", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("residual_out", ctypes.c_void_p),
+        ("y", ctypes.c_void_p), ("y_scale", ctypes.c_void_p),
+    ]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64),
+        ("ld_residual", ctypes.c_int64), ("ldy", ctypes.c_int64), ("x", ctypes.c_void_p), ("w", ctypes.c_void_p),
+        ("x_scale", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p), ("y", ctypes.c_void_p), ("err", ctypes.c_void_p),
+    ]
+
+
+class ScanArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("T", ctypes.c_int32),
+        ("D", ctypes.c_int32), ("N", ctypes.c_int32), ("gate_mode", ctypes.c_int32), ("flags", ctypes.c_uint32),
+        ("x_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+        ("h_chunks_rows", ctypes.c_int64), ("x", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("h0", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p),
+        ("y", ctypes.c_void_p), ("hT", ctypes.c_void_p), ("h_chunks", ctypes.c_void_p), ("err", ctypes.c_void_p),
+    ]
+
+
+class ScanBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("fwd", ScanArgs), ("dy_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+        ("dgate_stride", ctypes.c_int64), ("dy", ctypes.c_void_p), ("dhT", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+        ("dgate", ctypes.c_void_p), ("dh0", ctypes.c_void_p),
+    ]
+
+
+class ScanStepArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("num_slots", ctypes.c_int32), ("gate_mode", ctypes.c_int32), ("flags", ctypes.c_uint32),
+        ("x_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("state_in", ctypes.c_void_p),
+        ("state_out", ctypes.c_void_p), ("indices", ctypes.c_void_p), ("y", ctypes.c_void_p), ("err", ctypes.c_void_p),
+    ]
+
+
 class Tcgen05ProbeArgs(ctypes.Structure):
     _fields_ = [
         ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("layout", ctypes.c_int32), ("a_from_tmem", ctypes.c_int32),
@@ -106,7 +160,8 @@ class Tcgen05ProbeArgs(ctypes.Structure):
 
 
 EXPORTS = ("kda_chunk_fwd", "kda_chunk_output", "kda_chunk_fwd_noalloc", "kda_chunk_workspace_size", "kda_decode_step",
-           "kda_decode_conv_step", "kda_recurrent_step", "kda_head_rmsnorm", "kda_version",
+           "kda_decode_conv_step", "kda_recurrent_step", "kda_head_rmsnorm", "kda_add_rmsnorm", "kda_linear", "kda_scan_fwd",
+           "kda_scan_bwd", "kda_scan_step", "kda_version",
            "kda_selftest_bounded_wait", "kda_selftest_tcgen05")
 
 
@@ -139,6 +194,10 @@ def load() -> ctypes.CDLL:
         lib.kda_decode_conv_step.argtypes = [ctypes.POINTER(DecodeConvArgs), ctypes.c_void_p]
         lib.kda_head_rmsnorm.restype = ctypes.c_int
         lib.kda_head_rmsnorm.argtypes = [ctypes.POINTER(RmsNormArgs), ctypes.c_void_p]
+        for name, struct in (("kda_add_rmsnorm", AddRmsNormArgs), ("kda_linear", LinearArgs), ("kda_scan_fwd", ScanArgs),
+                             ("kda_scan_bwd", ScanBwdArgs), ("kda_scan_step", ScanStepArgs)):
+            getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name).argtypes = [ctypes.POINTER(struct), ctypes.c_void_p]
         lib.kda_chunk_fwd_noalloc.restype = ctypes.c_int
         lib.kda_chunk_fwd_noalloc.argtypes = [ctypes.POINTER(ChunkArgs), ctypes.c_void_p]
         lib.kda_version.restype = ctypes.c_char_p
@@ -466,3 +525,247 @@ def kda_chunk_output(q, k, v, h_chunks, *, scale, g=None, a=None, dt_bias=None, 
     if st != KDA_OK:
         raise KdaError(st, "kda_chunk_output")
     return o
+
+
+# --- the layer around the attention: norm, projections, gated recurrence ---
+
+
+def _any_dtype_code(dt: torch.dtype) -> int:
+    return KDA_DTYPE_E4M3 if dt == torch.float8_e4m3fn else _dtype_code(dt)
+
+
+def _rows(t, name, dtype=None, shape=None):
+    """(pointer, row stride) of a tensor taken as rows of its last axis: CUDA, that
+    axis contiguous, the leading axes evenly spaced. None gives (None, 0)."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if not t.is_cuda:
+        raise ValueError("libkda works on CUDA tensors only (no CPU fallback)")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() < 1:
+        raise ValueError(f"{name}: needs at least one axis")
+    if t.numel() == 0:
+        return t.data_ptr() or None, int(t.shape[-1])
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    step, span = None, None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != span:
+            raise ValueError(f"{name}: the leading axes must be evenly spaced rows")
+        span = stride * size
+    return t.data_ptr(), int(t.shape[-1] if step is None else step)
+
+
+def _vec(t, name, shape, dtype=torch.float32):
+    """Pointer of a contiguous tensor of the given shape, or None."""
+    if t is None:
+        return None
+    p = _ptr(t)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return p
+
+
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, x on {ref.device}")
+
+
+def _outputs_on(stream):
+    """Context in which a call allocates its outputs: the stream that writes them,
+    so the caching allocator does not hand their memory on too early."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _call(name, args, x, stream):
+    with _on_device(x):
+        st = getattr(load(), name)(ctypes.byref(args), _stream_ptr(stream, x.device))
+    if st != KDA_OK:
+        raise KdaError(st, name)
+
+
+def kda_add_rmsnorm(x, weight, *, eps, residual=None, residual_out=None, out=None, out_scale=None, out_dtype=None,
+                    stream=None):
+    """r = x + residual; y = r / sqrt(mean(r^2) + eps) * weight over the last axis.
+
+    x, residual (optional): bf16 or fp32 [..., D], rows evenly spaced; weight fp32
+    [D]. out_dtype (default x.dtype) is torch.bfloat16, torch.float32 or
+    torch.float8_e4m3fn; the last stores y / scale with one fp32 scale per row
+    (largest |y| / 448). residual_out may be residual or x (in place).
+    Returns (y, scale or None, residual_out or None): residual_out is made when
+    there is a residual, or when it is given."""
+    xp, xs = _rows(x, "x")
+    lead, D = tuple(x.shape[:-1]), int(x.shape[-1])
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out: expected {out_dtype}, got {out.dtype}")
+    out_dtype = out.dtype if out is not None else (out_dtype or x.dtype)
+    q8 = out_dtype == torch.float8_e4m3fn
+    if out_scale is not None and not q8:
+        raise ValueError("out_scale goes with an 8-bit output")
+    with _outputs_on(stream):
+        if residual_out is None and residual is not None:
+            residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if out is None:
+            out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+        if out_scale is None and q8:
+            out_scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+    _same_device(x, weight=weight, residual=residual, residual_out=residual_out, out=out, out_scale=out_scale)
+    args = AddRmsNormArgs()
+    args.D, args.R = D, x.numel() // max(D, 1)
+    args.dtype, args.y_dtype, args.eps = _dtype_code(x.dtype), _any_dtype_code(out_dtype), float(eps)
+    args.x, args.x_stride = xp, xs
+    args.residual, args.residual_stride = _rows(residual, "residual", x.dtype, x.shape)
+    args.residual_out, args.residual_out_stride = _rows(residual_out, "residual_out", x.dtype, x.shape)
+    args.y, args.y_stride = _rows(out, "out", shape=x.shape)
+    args.weight, args.y_scale = _vec(weight, "weight", (D,)), _vec(out_scale, "out_scale", lead)
+    _call("kda_add_rmsnorm", args, x, stream)
+    return out, out_scale, residual_out
+
+
+def kda_linear(x, w, *, bias=None, activation="none", residual=None, x_scale=None, w_scale=None, out=None,
+               out_dtype=None, err=None, stream=None):
+    """y = act((x w^T) * x_scale * w_scale + bias) + residual.
+
+    x [..., K] and w [N, K], both bf16, or both torch.float8_e4m3fn with fp32
+    scales x_scale [...] (one per row) and w_scale [N]. bias fp32 [N]; activation
+    "none", "silu", "gelu", "sigmoid" or "relu"; residual [..., N] in the output's
+    dtype, bf16 (default) or fp32; out may be residual. Returns y [..., N]."""
+    if activation not in KDA_ACTIVATIONS:
+        raise ValueError(f"activation: expected one of {sorted(KDA_ACTIVATIONS)}, got {activation!r}")
+    args = LinearArgs()
+    args.x, args.ldx = _rows(x, "x")
+    lead, K = tuple(x.shape[:-1]), int(x.shape[-1])
+    if w.dim() != 2:
+        raise ValueError("w: expected [N, K]")
+    N = int(w.shape[0])
+    args.w, args.ldw = _rows(w, "w", x.dtype, (N, K))
+    shape = lead + (N,)
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out: expected {out_dtype}, got {out.dtype}")
+    out_dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
+    if out is None:
+        with _outputs_on(stream):
+            out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    _same_device(x, w=w, bias=bias, residual=residual, x_scale=x_scale, w_scale=w_scale, out=out, err=err)
+    args.M, args.N, args.K = x.numel() // max(K, 1), N, K
+    args.dtype, args.y_dtype = _any_dtype_code(x.dtype), _any_dtype_code(out_dtype)
+    args.activation = KDA_ACTIVATIONS[activation]
+    args.x_scale, args.w_scale = _vec(x_scale, "x_scale", lead), _vec(w_scale, "w_scale", (N,))
+    args.bias = _vec(bias, "bias", (N,))
+    args.residual, args.ld_residual = _rows(residual, "residual", out_dtype, shape)
+    args.y, args.ldy = _rows(out, "out", out_dtype, shape)
+    args.err = _ptr(err)
+    _call("kda_linear", args, x, stream)
+    return out
+
+
+def _scan_args(x, gate, gate_mode, complement, h0, cu_seqlens, h_chunks, err):
+    if gate_mode not in KDA_SCAN_GATES:
+        raise ValueError(f"gate_mode: expected one of {sorted(KDA_SCAN_GATES)}, got {gate_mode!r}")
+    if x.dim() != 3:
+        raise ValueError("x: expected [B, T, D]")
+    B, T, D = (int(v) for v in x.shape)
+    args = ScanArgs()
+    args.x, args.x_stride = _rows(x, "x")
+    args.gate, args.gate_stride = _rows(gate, "gate", shape=x.shape)
+    args.dtype, args.gate_dtype = _dtype_code(x.dtype), _dtype_code(gate.dtype)
+    args.B, args.T, args.D = B, T, D
+    args.N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    args.gate_mode, args.flags = KDA_SCAN_GATES[gate_mode], KDA_SCAN_FLAG_COMPLEMENT if complement else 0
+    args.h0 = _vec(h0, "h0", (args.N, D))
+    args.cu_seqlens = _vec(cu_seqlens, "cu_seqlens", (args.N + 1,), torch.int32)
+    if h_chunks is not None and (h_chunks.dtype != torch.float32 or h_chunks.dim() != 2 or h_chunks.shape[1] != D):
+        raise ValueError(f"h_chunks: expected fp32 [chunks, {D}]")
+    if h_chunks is not None:
+        args.h_chunks, args.h_chunks_rows = _ptr(h_chunks), int(h_chunks.shape[0])
+    args.err = _ptr(err)
+    _same_device(x, gate=gate, h0=h0, cu_seqlens=cu_seqlens, h_chunks=h_chunks, err=err)
+    return args
+
+
+def kda_scan_fwd(x, gate, *, gate_mode="log", complement=False, h0=None, cu_seqlens=None, y=None, hT=None,
+                 h_chunks=None, output_final_state=True, err=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + u_t over x [B, T, D], y_t = h_t.
+
+    a = exp(gate) (gate_mode "log") or sigmoid(gate) ("logits"); u = x, or
+    (1 - a) x with complement. x bf16 with a bf16 or fp32 gate, or both fp32; rows
+    evenly spaced (views of one packed projection will do). h0, hT fp32 [N, D];
+    cu_seqlens as for kda_chunk_fwd. h_chunks (fp32 [chunk_count(B, T,
+    cu_seqlens), D]) receives the state entering every 16-token chunk, which
+    kda_scan_bwd reads. Returns (y, hT), hT None when output_final_state is False."""
+    args = _scan_args(x, gate, gate_mode, complement, h0, cu_seqlens, h_chunks, err)
+    with _outputs_on(stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if hT is None and output_final_state:
+            hT = torch.empty(args.N, args.D, dtype=torch.float32, device=x.device)
+    _same_device(x, y=y, hT=hT)
+    args.y, args.y_stride = _rows(y, "y", x.dtype, x.shape)
+    args.hT = _vec(hT, "hT", (args.N, args.D))
+    _call("kda_scan_fwd", args, x, stream)
+    return y, hT
+
+
+def kda_scan_bwd(x, gate, dy, h_chunks, *, gate_mode="log", complement=False, dhT=None, cu_seqlens=None, dx=None,
+                 dgate=None, dh0=None, output_dh0=True, err=None, stream=None):
+    """Gradients of kda_scan_fwd from dy (of y) and dhT (of hT; None for zero), with
+    the h_chunks that the forward wrote. Returns (dx, dgate, dh0), dh0 None when
+    output_dh0 is False. dx may be dy or x, and dgate may be gate."""
+    args = ScanBwdArgs()
+    args.fwd = _scan_args(x, gate, gate_mode, complement, None, cu_seqlens, h_chunks, err)
+    N, D = args.fwd.N, args.fwd.D
+    with _outputs_on(stream):
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if dgate is None:
+            dgate = torch.empty(x.shape, dtype=gate.dtype, device=x.device)
+        if dh0 is None and output_dh0:
+            dh0 = torch.empty(N, D, dtype=torch.float32, device=x.device)
+    _same_device(x, dy=dy, dhT=dhT, dx=dx, dgate=dgate, dh0=dh0)
+    args.dy, args.dy_stride = _rows(dy, "dy", x.dtype, x.shape)
+    args.dx, args.dx_stride = _rows(dx, "dx", x.dtype, x.shape)
+    args.dgate, args.dgate_stride = _rows(dgate, "dgate", gate.dtype, x.shape)
+    args.dhT, args.dh0 = _vec(dhT, "dhT", (N, D)), _vec(dh0, "dh0", (N, D))
+    _call("kda_scan_bwd", args, x, stream)
+    return dx, dgate, dh0
+
+
+def kda_scan_step(x, gate, state_pool, indices, *, gate_mode="log", complement=False, state_out=None, y=None,
+                  err=None, stream=None, check_indices=False):
+    """One token of the recurrence for each row of x [B, D] on a pool of states
+    (fp32 [slots, D]): row b uses slot indices[b] (int32; negative = padding, y = 0).
+    state_out defaults to state_pool (in place); only the valid rows' slots are
+    written. check_indices (needs err): a debug check that the valid slots are
+    distinct. Returns y [B, D]."""
+    if gate_mode not in KDA_SCAN_GATES:
+        raise ValueError(f"gate_mode: expected one of {sorted(KDA_SCAN_GATES)}, got {gate_mode!r}")
+    if x.dim() != 2:
+        raise ValueError("x: expected [B, D]")
+    B, D = int(x.shape[0]), int(x.shape[1])
+    if y is None:
+        with _outputs_on(stream):
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    state_out = state_pool if state_out is None else state_out
+    _same_device(x, gate=gate, state_pool=state_pool, state_out=state_out, indices=indices, y=y, err=err)
+    args = ScanStepArgs()
+    args.dtype, args.gate_dtype, args.B, args.D = _dtype_code(x.dtype), _dtype_code(gate.dtype), B, D
+    args.num_slots, args.gate_mode = int(state_pool.shape[0]), KDA_SCAN_GATES[gate_mode]
+    args.flags = (KDA_SCAN_FLAG_COMPLEMENT if complement else 0) | (KDA_FLAG_CHECK_INDICES if check_indices else 0)
+    args.x, args.x_stride = _rows(x, "x")
+    args.gate, args.gate_stride = _rows(gate, "gate", shape=x.shape)
+    args.y, args.y_stride = _rows(y, "y", x.dtype, x.shape)
+    args.state_in = _vec(state_pool, "state_pool", (args.num_slots, D))
+    args.state_out = _vec(state_out, "state_out", (args.num_slots, D))
+    args.indices, args.err = _vec(indices, "indices", (B,), torch.int32), _ptr(err)
+    _call("kda_scan_step", args, x, stream)
+    return y

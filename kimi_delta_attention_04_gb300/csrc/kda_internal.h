@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/kda.h"
+
 namespace kda {
 
 // Where the chunks of a call are. Without cu_seqlens the batch is N sequences
@@ -98,6 +100,14 @@ struct RmsNormCall {
   const float* weight;
   void* y;
 };
+
+// The layer operators' calls are their argument structs, validated on the host
+// (kda_layer_api.cpp).
+cudaError_t launch_add_rmsnorm(const kda_add_rmsnorm_args& a, cudaStream_t s);
+cudaError_t launch_linear(const kda_linear_args& a, cudaStream_t s);
+cudaError_t launch_scan_fwd(const kda_scan_args& a, cudaStream_t s);
+cudaError_t launch_scan_bwd(const kda_scan_bwd_args& a, cudaStream_t s);
+cudaError_t launch_scan_step(const kda_scan_step_args& a, cudaStream_t s);
 
 // Bytes of one (chunk, head) prep record.
 size_t record_bytes_tc(int d);           // bf16 tensor-core path, dk = dv = d
