@@ -2,14 +2,28 @@
 //   h_t = a_t h_{t-1} + u_t,  u_t = x_t or (1 - a_t) x_t,  a_t = exp(g) or sigmoid(f),
 // its gradients, and the single-token step on a pool of states.
 //
-// One thread per (sequence, channel) walks the tokens in order.
+// Split. A warp holds one chunk of 16 tokens x 64 channels (two a lane) in
+// registers; the kWarps warps of a CTA and the S CTAs of a cluster hold
+// consecutive chunks, so a cluster advances S * kWarps * 16 tokens at a time and
+// no token is read twice. Each warp reduces its chunk to the pair (A, B) of
+// h_out = A h_in + B (A the product of the decays, B the state from zero); the
+// pairs meet in shared memory, the CTAs' totals in every CTA of the cluster
+// (distributed shared memory), and each warp composes the pairs before it with
+// the carried state and runs its chunk again from the state that enters it.
+// Nothing waits on memory flags: two barriers per advance, in a fixed order, so
+// results do not vary from run to run.
+#include "kda_cluster.cuh"
 #include "kda_elem.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kScanChunk = 16;  // tokens between the states of h_chunks
+constexpr int kScanChunk = 16;    // tokens between the states of h_chunks, and of a warp's tile
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kBlockCh = 64;      // channels of a CTA
+constexpr int kMaxCluster = 8;
+constexpr int kStepThreads = 128;
 
 // sigmoid without overflow: e^-f = inf gives 0
 __device__ __forceinline__ float decay_of(float f, int mode) {
@@ -31,6 +45,7 @@ __device__ __forceinline__ bool find_sequence(const kda_scan_args& p, int n, Seq
     return true;
   }
   __shared__ unsigned long long base, total;  // chunks before sequence n, of all
+  __syncthreads();  // the previous sequence's have been read
   if (threadIdx.x == 0) base = total = 0;
   bool bad = threadIdx.x == 0 && (p.cu_seqlens[0] != 0 || p.cu_seqlens[p.N] != p.T);
   unsigned long long mine = 0, all = 0;
@@ -56,65 +71,269 @@ __device__ __forceinline__ bool find_sequence(const kda_scan_args& p, int n, Seq
   return true;
 }
 
-template <typename X, typename G>
-__global__ void __launch_bounds__(kThreads) kda_scan_fwd_kernel(const kda_scan_args p) {
-  const int n = blockIdx.y, c = blockIdx.x * kThreads + threadIdx.x;
-  SeqPos pos;
-  if (!find_sequence(p, n, pos) || c >= p.D) return;
-  const bool comp = p.flags & KDA_SCAN_FLAG_COMPLEMENT;
-  float h = p.h0 ? p.h0[static_cast<long long>(n) * p.D + c] : 0.f;
-  for (int t = pos.start; t < pos.end; ++t) {
-    const int i = t - pos.start;
-    if (p.h_chunks && i % kScanChunk == 0) p.h_chunks[(pos.chunk_base + i / kScanChunk) * p.D + c] = h;
-    const float a = decay_of(load_f(static_cast<const G*>(p.gate) + t * p.gate_stride + c), p.gate_mode);
-    const float x = load_f(static_cast<const X*>(p.x) + t * p.x_stride + c);
-    h = a * h + (comp ? (1.f - a) * x : x);
-    store_f(static_cast<X*>(p.y) + t * p.y_stride + c, h);
+// Two channels of one token. VEC: a lane's channels are 2 lane and 2 lane + 1
+// (even D and strides, aligned pointers), one access; otherwise lane and
+// lane + 32, two accesses, whatever the alignment.
+template <typename T>
+struct Raw2;
+template <>
+struct Raw2<__nv_bfloat16> {
+  uint32_t v;
+  __device__ __forceinline__ void zero() { v = 0; }
+  __device__ __forceinline__ float2 get() const {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
   }
-  if (p.hT) p.hT[static_cast<long long>(n) * p.D + c] = h;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint32_t*>(p); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
+    const uint32_t lo = p ? *reinterpret_cast<const uint16_t*>(p) : 0u;
+    const uint32_t hi = q ? *reinterpret_cast<const uint16_t*>(q) : 0u;
+    v = lo | (hi << 16);
+  }
+};
+template <>
+struct Raw2<float> {
+  float2 v;
+  __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
+  __device__ __forceinline__ float2 get() const { return v; }
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
+  __device__ __forceinline__ void load(const float* p, const float* q) { v = make_float2(p ? *p : 0.f, q ? *q : 0.f); }
+};
+
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v) { *reinterpret_cast<uint32_t*>(p) = Bf16::pack(v.x, v.y); }
+__device__ __forceinline__ void store2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+
+// A lane's two channels and which of them exist.
+struct Lane {
+  int c0, c1;
+  bool p0, p1;
+};
+
+template <bool VEC>
+__device__ __forceinline__ Lane lane_channels(int block_ch, int D) {
+  const int lane = threadIdx.x & 31;
+  Lane l;
+  l.c0 = block_ch + (VEC ? 2 * lane : lane);
+  l.c1 = block_ch + (VEC ? 2 * lane + 1 : lane + 32);
+  l.p0 = l.c0 < D;
+  l.p1 = l.c1 < D;
+  return l;
 }
 
-template <typename X, typename G>
-__global__ void __launch_bounds__(kThreads) kda_scan_bwd_kernel(const kda_scan_bwd_args q) {
+template <bool VEC, typename T>
+__device__ __forceinline__ Raw2<T> load_pair(const T* row, const Lane& l) {
+  Raw2<T> r;
+  if (VEC) {
+    if (l.p0) r.load(row + l.c0);
+    else r.zero();
+  } else {
+    r.load(l.p0 ? row + l.c0 : nullptr, l.p1 ? row + l.c1 : nullptr);
+  }
+  return r;
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_pair(T* row, const Lane& l, float2 v) {
+  if (VEC) {
+    if (l.p0) store2(row + l.c0, v);
+  } else {
+    if (l.p0) store_f(row + l.c0, v.x);
+    if (l.p1) store_f(row + l.c1, v.y);
+  }
+}
+
+// States are [.., D] fp32 rows: no alignment is assumed of them.
+__device__ __forceinline__ float2 load_state(const float* base, long long row, int D, const Lane& l) {
+  if (base == nullptr) return make_float2(0.f, 0.f);
+  base += row * D;
+  return make_float2(l.p0 ? base[l.c0] : 0.f, l.p1 ? base[l.c1] : 0.f);
+}
+__device__ __forceinline__ void store_state(float* base, long long row, int D, const Lane& l, float2 v) {
+  base += row * D;
+  if (l.p0) base[l.c0] = v.x;
+  if (l.p1) base[l.c1] = v.y;
+}
+
+__device__ __forceinline__ float2 decay2(float2 f, int mode) { return make_float2(decay_of(f.x, mode), decay_of(f.y, mode)); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+
+// The map h -> A h + B of some consecutive tokens, for a lane's two channels.
+struct Map {
+  float2 A, B;
+};
+__device__ __forceinline__ Map then(const Map& first, const Map& second) {
+  return Map{mul2(first.A, second.A), fma2(second.A, first.B, second.B)};
+}
+
+struct ScanSmem {
+  Map warp[kWarps][32];                  // this advance's maps, by warp
+  Map cta[2][kMaxCluster][32];           // the CTAs' maps, by parity of the advance
+};
+
+__device__ __forceinline__ void st_cluster_map(uint32_t addr, const Map& m) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(m.A.x), "f"(m.A.y), "f"(m.B.x),
+               "f"(m.B.y)
+               : "memory");
+}
+
+// From this warp's map of the advance and the state `carry` that enters the
+// advance (the same in every warp of the cluster): the state that enters this
+// warp's chunk; carry becomes the state after the advance. All threads of the
+// cluster call it.
+__device__ __forceinline__ float2 enter_state(ScanSmem& sm, const Map& mine, float2& carry, int parity, int S, int rank) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  sm.warp[warp][lane] = mine;
+  __syncthreads();
+  Map before{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
+  for (int w = 0; w < warp; ++w) before = then(before, sm.warp[w][lane]);
+  if (warp == kWarps - 1) {
+    const Map total = then(before, mine);
+    const uint32_t at = smem_u32(&sm.cta[parity][rank][lane]);
+    for (int r = 0; r < S; ++r) st_cluster_map(mapa_shared(at, r), total);
+  }
+  if (S > 1) cluster_sync_all();
+  else __syncthreads();
+  float2 h = carry, in = carry;
+  for (int r = 0; r < S; ++r) {
+    if (r == rank) in = h;
+    const Map& m = sm.cta[parity][r][lane];
+    h = fma2(m.A, h, m.B);
+  }
+  carry = h;
+  return fma2(before.A, in, before.B);
+}
+
+// Forward. Grid (S * channel blocks, sequences), cluster (S, 1, 1).
+template <typename X, typename G, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) kda_scan_fwd_kernel(const kda_scan_args p, int S) {
+  __shared__ ScanSmem sm;
+  const int warp = threadIdx.x >> 5, rank = blockIdx.x % S;
+  const Lane l = lane_channels<VEC>(blockIdx.x / S * kBlockCh, p.D);
+  const bool comp = p.flags & KDA_SCAN_FLAG_COMPLEMENT;
+  if (S > 1) cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written
+  int parity = 0;
+  for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
+    SeqPos pos;
+    if (!find_sequence(p, n, pos)) return;  // (the same answer in every CTA)
+    const int len = pos.end - pos.start;
+    float2 carry = load_state(p.h0, n, p.D, l);
+    for (int base = 0; base < len; base += S * kWarps * kScanChunk, parity ^= 1) {
+      const int i0 = base + (rank * kWarps + warp) * kScanChunk;  // first token of this warp's chunk
+      const int m = min(kScanChunk, len - i0);
+      const X* x = static_cast<const X*>(p.x) + (pos.start + static_cast<long long>(i0)) * p.x_stride;
+      const G* gate = static_cast<const G*>(p.gate) + (pos.start + static_cast<long long>(i0)) * p.gate_stride;
+      Raw2<X> rx[kScanChunk];
+      Raw2<G> rg[kScanChunk];
+#pragma unroll
+      for (int i = 0; i < kScanChunk; ++i) {
+        rx[i].zero();
+        rg[i].zero();
+        if (i < m) {
+          rx[i] = load_pair<VEC>(x + i * p.x_stride, l);
+          rg[i] = load_pair<VEC>(gate + i * p.gate_stride, l);
+        }
+      }
+      float2 a[kScanChunk], u[kScanChunk];
+      Map mine{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int i = 0; i < kScanChunk; ++i) {
+        a[i] = decay2(rg[i].get(), p.gate_mode);
+        u[i] = rx[i].get();
+        if (comp) u[i] = make_float2((1.f - a[i].x) * u[i].x, (1.f - a[i].y) * u[i].y);
+        if (i < m) mine = then(mine, Map{a[i], u[i]});
+      }
+      float2 h = enter_state(sm, mine, carry, parity, S, rank);
+      if (m > 0) {
+        if (p.h_chunks) store_state(p.h_chunks, pos.chunk_base + i0 / kScanChunk, p.D, l, h);
+        X* y = static_cast<X*>(p.y) + (pos.start + static_cast<long long>(i0)) * p.y_stride;
+#pragma unroll
+        for (int i = 0; i < kScanChunk; ++i) {
+          if (i < m) {
+            h = fma2(a[i], h, u[i]);
+            store_pair<VEC>(y + i * p.y_stride, l, h);
+          }
+        }
+      }
+    }
+    if (p.hT && rank == 0 && warp == 0) store_state(p.hT, n, p.D, l, carry);
+  }
+}
+
+// Backward: the same over the chunks from the last to the first, with the map of
+// d (the gradient of a state) over a chunk; the states within a chunk come from
+// h_chunks, so the forward direction needs no exchange.
+template <typename X, typename G, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_scan_bwd_args q, int S) {
+  __shared__ ScanSmem sm;
   const kda_scan_args& p = q.fwd;
-  const int n = blockIdx.y, c = blockIdx.x * kThreads + threadIdx.x;
-  SeqPos pos;
-  if (!find_sequence(p, n, pos) || c >= p.D) return;
-  const bool comp = p.flags & KDA_SCAN_FLAG_COMPLEMENT;
-  const int len = pos.end - pos.start;
-  float d = q.dhT ? q.dhT[static_cast<long long>(n) * p.D + c] : 0.f;
-  for (int k = (len + kScanChunk - 1) / kScanChunk - 1; k >= 0; --k) {
-    const int t0 = pos.start + k * kScanChunk, m = min(kScanChunk, len - k * kScanChunk);
-    float a[kScanChunk], x[kScanChunk], hp[kScanChunk];  // decay, input, state before the token
-    float h = p.h_chunks[(pos.chunk_base + k) * p.D + c];
+  const int warp = threadIdx.x >> 5, rank = blockIdx.x % S;
+  const Lane l = lane_channels<VEC>(blockIdx.x / S * kBlockCh, p.D);
+  const bool comp = p.flags & KDA_SCAN_FLAG_COMPLEMENT, logits = p.gate_mode == KDA_SCAN_LOGITS;
+  if (S > 1) cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written
+  int parity = 0;
+  for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
+    SeqPos pos;
+    if (!find_sequence(p, n, pos)) return;
+    const int len = pos.end - pos.start, chunks = (len + kScanChunk - 1) / kScanChunk;
+    float2 carry = load_state(q.dhT, n, p.D, l);
+    for (int base = 0; base < chunks; base += S * kWarps, parity ^= 1) {
+      const int k = chunks - 1 - (base + rank * kWarps + warp);  // this warp's chunk (negative: none left)
+      const int m = k < 0 ? 0 : min(kScanChunk, len - k * kScanChunk);
+      const long long t0 = pos.start + static_cast<long long>(k) * kScanChunk;
+      const X* x = static_cast<const X*>(p.x) + t0 * p.x_stride;
+      const G* gate = static_cast<const G*>(p.gate) + t0 * p.gate_stride;
+      const X* dy = static_cast<const X*>(q.dy) + t0 * q.dy_stride;
+      Raw2<X> rx[kScanChunk], rd[kScanChunk];
+      Raw2<G> rg[kScanChunk];
 #pragma unroll
-    for (int i = 0; i < kScanChunk; ++i) {
-      if (i < m) {
-        a[i] = decay_of(load_f(static_cast<const G*>(p.gate) + (t0 + i) * p.gate_stride + c), p.gate_mode);
-        x[i] = load_f(static_cast<const X*>(p.x) + (t0 + i) * p.x_stride + c);
-        hp[i] = h;
-        h = a[i] * h + (comp ? (1.f - a[i]) * x[i] : x[i]);
+      for (int i = 0; i < kScanChunk; ++i) {
+        rx[i].zero();
+        rg[i].zero();
+        rd[i].zero();
+        if (i < m) {
+          rx[i] = load_pair<VEC>(x + i * p.x_stride, l);
+          rg[i] = load_pair<VEC>(gate + i * p.gate_stride, l);
+          rd[i] = load_pair<VEC>(dy + i * q.dy_stride, l);
+        }
+      }
+      float2 h = m > 0 ? load_state(p.h_chunks, pos.chunk_base + k, p.D, l) : make_float2(0.f, 0.f);
+      float2 a[kScanChunk], w[kScanChunk];  // decay; what d multiplies in the decay's gradient
+#pragma unroll
+      for (int i = 0; i < kScanChunk; ++i) {
+        a[i] = decay2(rg[i].get(), p.gate_mode);
+        const float2 xv = rx[i].get();
+        w[i] = comp ? make_float2(h.x - xv.x, h.y - xv.y) : h;
+        h = comp ? fma2(a[i], w[i], xv) : fma2(a[i], h, xv);  // a h + (1 - a) x = x + a (h - x)
+      }
+      Map mine{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};  // d -> a (d + dy), last token first
+#pragma unroll
+      for (int i = kScanChunk - 1; i >= 0; --i)
+        if (i < m) mine = then(mine, Map{a[i], mul2(a[i], rd[i].get())});
+      float2 d = enter_state(sm, mine, carry, parity, S, rank);
+      X* dx = static_cast<X*>(q.dx) + t0 * q.dx_stride;
+      G* dg = static_cast<G*>(q.dgate) + t0 * q.dgate_stride;
+#pragma unroll
+      for (int i = kScanChunk - 1; i >= 0; --i) {
+        if (i < m) {
+          const float2 dyv = rd[i].get(), b = make_float2(1.f - a[i].x, 1.f - a[i].y);
+          d = make_float2(d.x + dyv.x, d.y + dyv.y);
+          store_pair<VEC>(dx + i * q.dx_stride, l, comp ? mul2(b, d) : d);
+          d = mul2(a[i], d);
+          float2 g = mul2(d, w[i]);
+          if (logits) g = mul2(b, g);
+          store_pair<VEC>(dg + i * q.dgate_stride, l, g);
+        }
       }
     }
-#pragma unroll
-    for (int i = kScanChunk - 1; i >= 0; --i) {
-      if (i < m) {
-        const long long t = t0 + i;
-        d += load_f(static_cast<const X*>(q.dy) + t * q.dy_stride + c);
-        const float da = comp ? d * (hp[i] - x[i]) : d * hp[i];
-        store_f(static_cast<X*>(q.dx) + t * q.dx_stride + c, comp ? (1.f - a[i]) * d : d);
-        d *= a[i];
-        store_f(static_cast<G*>(q.dgate) + t * q.dgate_stride + c,
-                a[i] * (p.gate_mode == KDA_SCAN_LOG_DECAY ? da : (1.f - a[i]) * da));
-      }
-    }
+    if (q.dh0 && rank == 0 && warp == 0) store_state(q.dh0, n, p.D, l, carry);
   }
-  if (q.dh0) q.dh0[static_cast<long long>(n) * p.D + c] = d;
 }
 
 template <typename X, typename G>
-__global__ void __launch_bounds__(kThreads) kda_scan_step_kernel(const kda_scan_step_args p) {
-  const int c = blockIdx.x * kThreads + threadIdx.x;
+__global__ void __launch_bounds__(kStepThreads) kda_scan_step_kernel(const kda_scan_step_args p) {
+  const int c = blockIdx.x * kStepThreads + threadIdx.x;
   const long long b = blockIdx.y;
   if (c >= p.D) return;
   const int slot = p.indices[b];
@@ -132,36 +351,69 @@ __global__ void __launch_bounds__(kThreads) kda_scan_step_kernel(const kda_scan_
   store_f(y, h);
 }
 
+// CTAs of a cluster: enough that the grid fills the 152 SMs twice over (two CTAs
+// are resident on each), no more than the sequences (their mean length, where
+// they are packed) have advances for.
+int cluster_size(const kda_scan_args& a) {
+  const long long blocks = (a.D + kBlockCh - 1) / kBlockCh * static_cast<long long>(a.N);
+  const long long mean = a.cu_seqlens ? (a.T + a.N - 1) / a.N : a.T;
+  int S = 1;
+  while (S < kMaxCluster && blocks * S < 2 * 152 && mean > S * kWarps * kScanChunk) S *= 2;
+  return S;
+}
+
+// Whether pairs of channels can be read as one access of 2 * elem bytes.
+bool pairs_ok(const void* p, int64_t stride, size_t elem) {
+  return reinterpret_cast<uintptr_t>(p) % (2 * elem) == 0 && stride % 2 == 0;
+}
+size_t elem_bytes(int32_t dt) { return dt == KDA_DTYPE_FP32 ? 4 : 2; }
+
+template <typename Args>
+cudaError_t launch_clusters(void (*kernel)(Args, int), const Args& a, const kda_scan_args& f, cudaStream_t s) {
+  const int S = cluster_size(f);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((f.D + kBlockCh - 1) / kBlockCh * S), static_cast<unsigned>(f.N < 65535 ? f.N : 65535));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = S;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, S);
+}
+
 }  // namespace
 
-// The kernels' instances by tensor types: x bf16 with a bf16 or fp32 gate, or both fp32.
-#define KDA_SCAN_LAUNCH(kernel, args, xt, gt, grid, s)                                                 \
-  do {                                                                                                 \
-    if ((xt) == KDA_DTYPE_FP32) kernel<float, float><<<grid, kThreads, 0, s>>>(args);                  \
-    else if ((gt) == KDA_DTYPE_FP32) kernel<__nv_bfloat16, float><<<grid, kThreads, 0, s>>>(args);     \
-    else kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kThreads, 0, s>>>(args);                         \
-  } while (0)
-
-static unsigned blocks_of(int D) { return static_cast<unsigned>((D + kThreads - 1) / kThreads); }
+// The instances by tensor types: x bf16 with a bf16 or fp32 gate, or both fp32.
+#define KDA_SCAN_KERNEL(kernel, vec, xt, gt)                                                            \
+  ((xt) == KDA_DTYPE_FP32   ? ((vec) ? kernel<float, float, true> : kernel<float, float, false>)        \
+   : (gt) == KDA_DTYPE_FP32 ? ((vec) ? kernel<__nv_bfloat16, float, true> : kernel<__nv_bfloat16, float, false>) \
+                            : ((vec) ? kernel<__nv_bfloat16, __nv_bfloat16, true> : kernel<__nv_bfloat16, __nv_bfloat16, false>))
 
 cudaError_t launch_scan_fwd(const kda_scan_args& a, cudaStream_t s) {
-  if (a.N > 65535) return cudaErrorNotSupported;
-  const dim3 grid(blocks_of(a.D), a.N);
-  KDA_SCAN_LAUNCH(kda_scan_fwd_kernel, a, a.dtype, a.gate_dtype, grid, s);
-  return cudaGetLastError();
+  const size_t xe = elem_bytes(a.dtype), ge = elem_bytes(a.gate_dtype);
+  const bool vec = a.D % 2 == 0 && pairs_ok(a.x, a.x_stride, xe) && pairs_ok(a.gate, a.gate_stride, ge) &&
+                   pairs_ok(a.y, a.y_stride, xe);
+  return launch_clusters(KDA_SCAN_KERNEL(kda_scan_fwd_kernel, vec, a.dtype, a.gate_dtype), a, a, s);
 }
 
 cudaError_t launch_scan_bwd(const kda_scan_bwd_args& a, cudaStream_t s) {
-  if (a.fwd.N > 65535) return cudaErrorNotSupported;
-  const dim3 grid(blocks_of(a.fwd.D), a.fwd.N);
-  KDA_SCAN_LAUNCH(kda_scan_bwd_kernel, a, a.fwd.dtype, a.fwd.gate_dtype, grid, s);
-  return cudaGetLastError();
+  const kda_scan_args& f = a.fwd;
+  const size_t xe = elem_bytes(f.dtype), ge = elem_bytes(f.gate_dtype);
+  const bool vec = f.D % 2 == 0 && pairs_ok(f.x, f.x_stride, xe) && pairs_ok(f.gate, f.gate_stride, ge) &&
+                   pairs_ok(a.dy, a.dy_stride, xe) && pairs_ok(a.dx, a.dx_stride, xe) &&
+                   pairs_ok(a.dgate, a.dgate_stride, ge);
+  return launch_clusters(KDA_SCAN_KERNEL(kda_scan_bwd_kernel, vec, f.dtype, f.gate_dtype), a, f, s);
 }
 
 cudaError_t launch_scan_step(const kda_scan_step_args& a, cudaStream_t s) {
   if (a.B > 65535) return cudaErrorNotSupported;
-  const dim3 grid(blocks_of(a.D), a.B);
-  KDA_SCAN_LAUNCH(kda_scan_step_kernel, a, a.dtype, a.gate_dtype, grid, s);
+  const dim3 grid(static_cast<unsigned>((a.D + kStepThreads - 1) / kStepThreads), static_cast<unsigned>(a.B));
+  if (a.dtype == KDA_DTYPE_FP32) kda_scan_step_kernel<float, float><<<grid, kStepThreads, 0, s>>>(a);
+  else if (a.gate_dtype == KDA_DTYPE_FP32) kda_scan_step_kernel<__nv_bfloat16, float><<<grid, kStepThreads, 0, s>>>(a);
+  else kda_scan_step_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kStepThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
