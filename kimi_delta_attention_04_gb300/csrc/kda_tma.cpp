@@ -36,6 +36,20 @@ bool encode3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, size_t e
 
 }  // namespace
 
+bool encode_rows(CUtensorMap* m, const void* base, size_t elem, long long cols, long long rows, long long ld,
+                 unsigned box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const long long pitch = rows == 1 ? (cols * static_cast<long long>(elem) + 15) / 16 * 16 : ld * static_cast<long long>(elem);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), box_rows};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return fn(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t encode_input_maps(const ChunkCall& c, TmaInputMaps* m) {
   const long long tokens = c.geo.cu_seqlens ? static_cast<long long>(c.geo.T)
                                             : static_cast<long long>(c.geo.N) * c.geo.T;
