@@ -8,7 +8,6 @@ tensor is not on a CUDA device, the call raises.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import threading
 from pathlib import Path
@@ -530,68 +529,126 @@ def kda_chunk_output(q, k, v, h_chunks, *, scale, g=None, a=None, dt_bias=None, 
 # --- the layer around the attention: norm, projections, gated recurrence ---
 
 
-def _any_dtype_code(dt: torch.dtype) -> int:
-    return KDA_DTYPE_E4M3 if dt == torch.float8_e4m3fn else _dtype_code(dt)
+_DTYPE_CODES = {torch.bfloat16: KDA_DTYPE_BF16, torch.float32: KDA_DTYPE_FP32, torch.float8_e4m3fn: KDA_DTYPE_E4M3}
 
 
-def _rows(t, name, dtype=None, shape=None):
-    """(pointer, row stride) of a tensor taken as rows of its last axis: CUDA, that
-    axis contiguous, the leading axes evenly spaced. None gives (None, 0)."""
-    if t is None:
-        return None, 0
+# These calls are short next to a launch (a decode step's norm takes 3 us), so the
+# marshalling below avoids what costs microseconds: device contexts where the
+# device is current already, stream objects, tuples of shapes.
+
+def _code(dt):
+    code = _DTYPE_CODES.get(dt)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dt}; use torch.bfloat16, torch.float32 or torch.float8_e4m3fn")
+    return code
+
+
+def _device_of(x):
+    """Device index of a call's first tensor."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"expected a torch.Tensor, got {type(x).__name__}")
+    if not x.is_cuda:
+        raise ValueError("libkda works on CUDA tensors only (no CPU fallback)")
+    return x.get_device()
+
+
+def _refuse(t, name, dev, dtype, shape):
+    """Says what is wrong with a tensor that is not as expected (_rows and _vec ask)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if not t.is_cuda:
-        raise ValueError("libkda works on CUDA tensors only (no CPU fallback)")
-    if dtype is not None and t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev} (libkda works on CUDA tensors only)")
+    if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dim() < 1:
-        raise ValueError(f"{name}: needs at least one axis")
+    raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(t, name, dev, dtype, shape):
+    """(pointer, row stride) of a tensor taken as rows of its last axis: that axis
+    contiguous, the leading axes evenly spaced. None gives (None, 0)."""
+    if t is None:
+        return None, 0
+    # (a CPU tensor's device index is -1)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        _refuse(t, name, dev, dtype, shape)
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    return _spaced_rows(t, name)
+
+
+def _spaced_rows(t, name):
+    size = t.shape
     if t.numel() == 0:
-        return t.data_ptr() or None, int(t.shape[-1])
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        return t.data_ptr(), size[-1]
+    if size[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
     step, span = None, None
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        if size == 1:
+    for n, stride in zip(reversed(size[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
             continue
         if step is None:
             step = stride
         elif stride != span:
             raise ValueError(f"{name}: the leading axes must be evenly spaced rows")
-        span = stride * size
-    return t.data_ptr(), int(t.shape[-1] if step is None else step)
+        span = stride * n
+    return t.data_ptr(), size[-1] if step is None else step
 
 
-def _vec(t, name, shape, dtype=torch.float32):
+def _vec(t, name, dev, shape, dtype=torch.float32):
     """Pointer of a contiguous tensor of the given shape, or None."""
     if t is None:
         return None
-    p = _ptr(t)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    return p
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        _refuse(t, name, dev, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
 
 
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, x on {ref.device}")
+def _err_word(err, dev):
+    if err is None:
+        return None
+    if not isinstance(err, torch.Tensor) or err.get_device() != dev or err.dtype != torch.int32 or err.numel() < 1:
+        _refuse(err, "err", dev, torch.int32, (1,))
+    return err.data_ptr()
 
 
-def _outputs_on(stream):
-    """Context in which a call allocates its outputs: the stream that writes them,
-    so the caching allocator does not hand their memory on too early."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty(x, stream, shape, dtype):
+    """An output on x's device, allocated on the stream that writes it, so that the
+    caching allocator does not hand its memory on too early."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=x.get_device())
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=x.get_device())
 
 
-def _call(name, args, x, stream):
-    with _on_device(x):
-        st = getattr(load(), name)(ctypes.byref(args), _stream_ptr(stream, x.device))
+def _output(t, name, x, stream, shape, dtype):
+    """(tensor, pointer, row stride) of an output: the caller's, checked, or a new one."""
+    if t is not None:
+        return t, *_rows(t, name, x.get_device(), dtype, shape)
+    t = _empty(x, stream, shape, dtype)
+    return t, t.data_ptr(), shape[-1]
+
+
+def _state_output(t, name, x, stream, shape, wanted):
+    """(tensor or None, pointer) of an fp32 state output."""
+    if t is not None:
+        return t, _vec(t, name, x.get_device(), shape)
+    if not wanted:
+        return None, None
+    t = _empty(x, stream, shape, torch.float32)
+    return t, t.data_ptr()
+
+
+def _call(fn, args, dev, stream):
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(args, handle)
     if st != KDA_OK:
-        raise KdaError(st, name)
+        raise KdaError(st, fn.__name__)
 
 
 def kda_add_rmsnorm(x, weight, *, eps, residual=None, residual_out=None, out=None, out_scale=None, out_dtype=None,
@@ -604,31 +661,27 @@ def kda_add_rmsnorm(x, weight, *, eps, residual=None, residual_out=None, out=Non
     (largest |y| / 448). residual_out may be residual or x (in place).
     Returns (y, scale or None, residual_out or None): residual_out is made when
     there is a residual, or when it is given."""
-    xp, xs = _rows(x, "x")
-    lead, D = tuple(x.shape[:-1]), int(x.shape[-1])
+    lib = _lib or load()
+    dev = _device_of(x)
+    shape, dtype = x.shape, x.dtype
+    lead, D = shape[:-1], shape[-1]
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out: expected {out_dtype}, got {out.dtype}")
     out_dtype = out.dtype if out is not None else (out_dtype or x.dtype)
     q8 = out_dtype == torch.float8_e4m3fn
     if out_scale is not None and not q8:
         raise ValueError("out_scale goes with an 8-bit output")
-    with _outputs_on(stream):
-        if residual_out is None and residual is not None:
-            residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if out is None:
-            out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-        if out_scale is None and q8:
-            out_scale = torch.empty(lead, dtype=torch.float32, device=x.device)
-    _same_device(x, weight=weight, residual=residual, residual_out=residual_out, out=out, out_scale=out_scale)
     args = AddRmsNormArgs()
-    args.D, args.R = D, x.numel() // max(D, 1)
-    args.dtype, args.y_dtype, args.eps = _dtype_code(x.dtype), _any_dtype_code(out_dtype), float(eps)
-    args.x, args.x_stride = xp, xs
-    args.residual, args.residual_stride = _rows(residual, "residual", x.dtype, x.shape)
-    args.residual_out, args.residual_out_stride = _rows(residual_out, "residual_out", x.dtype, x.shape)
-    args.y, args.y_stride = _rows(out, "out", shape=x.shape)
-    args.weight, args.y_scale = _vec(weight, "weight", (D,)), _vec(out_scale, "out_scale", lead)
-    _call("kda_add_rmsnorm", args, x, stream)
+    args.R, args.D = x.numel() // max(D, 1), D
+    args.dtype, args.y_dtype, args.eps = _code(dtype), _code(out_dtype), eps
+    args.x, args.x_stride = _rows(x, "x", dev, dtype, shape)
+    args.weight = _vec(weight, "weight", dev, (D,))
+    if residual is not None or residual_out is not None:
+        args.residual, args.residual_stride = _rows(residual, "residual", dev, dtype, shape)
+        residual_out, args.residual_out, args.residual_out_stride = _output(residual_out, "residual_out", x, stream, shape, dtype)
+    out, args.y, args.y_stride = _output(out, "out", x, stream, shape, out_dtype)
+    out_scale, args.y_scale = _state_output(out_scale, "out_scale", x, stream, lead, q8)
+    _call(lib.kda_add_rmsnorm, args, dev, stream)
     return out, out_scale, residual_out
 
 
@@ -642,54 +695,49 @@ def kda_linear(x, w, *, bias=None, activation="none", residual=None, x_scale=Non
     dtype, bf16 (default) or fp32; out may be residual. Returns y [..., N]."""
     if activation not in KDA_ACTIVATIONS:
         raise ValueError(f"activation: expected one of {sorted(KDA_ACTIVATIONS)}, got {activation!r}")
-    args = LinearArgs()
-    args.x, args.ldx = _rows(x, "x")
-    lead, K = tuple(x.shape[:-1]), int(x.shape[-1])
+    lib = _lib or load()
+    dev = _device_of(x)
+    dtype, lead, K = x.dtype, x.shape[:-1], x.shape[-1]
     if w.dim() != 2:
         raise ValueError("w: expected [N, K]")
-    N = int(w.shape[0])
-    args.w, args.ldw = _rows(w, "w", x.dtype, (N, K))
+    N = w.shape[0]
     shape = lead + (N,)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out: expected {out_dtype}, got {out.dtype}")
     out_dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)
-    if out is None:
-        with _outputs_on(stream):
-            out = torch.empty(shape, dtype=out_dtype, device=x.device)
-    _same_device(x, w=w, bias=bias, residual=residual, x_scale=x_scale, w_scale=w_scale, out=out, err=err)
+    args = LinearArgs()
+    args.x, args.ldx = _rows(x, "x", dev, dtype, x.shape)
+    args.w, args.ldw = _rows(w, "w", dev, dtype, (N, K))
     args.M, args.N, args.K = x.numel() // max(K, 1), N, K
-    args.dtype, args.y_dtype = _any_dtype_code(x.dtype), _any_dtype_code(out_dtype)
+    args.dtype, args.y_dtype = _code(dtype), _code(out_dtype)
     args.activation = KDA_ACTIVATIONS[activation]
-    args.x_scale, args.w_scale = _vec(x_scale, "x_scale", lead), _vec(w_scale, "w_scale", (N,))
-    args.bias = _vec(bias, "bias", (N,))
-    args.residual, args.ld_residual = _rows(residual, "residual", out_dtype, shape)
-    args.y, args.ldy = _rows(out, "out", out_dtype, shape)
-    args.err = _ptr(err)
-    _call("kda_linear", args, x, stream)
+    args.x_scale, args.w_scale = _vec(x_scale, "x_scale", dev, lead), _vec(w_scale, "w_scale", dev, (N,))
+    args.bias, args.err = _vec(bias, "bias", dev, (N,)), _err_word(err, dev)
+    args.residual, args.ld_residual = _rows(residual, "residual", dev, out_dtype, shape)
+    out, args.y, args.ldy = _output(out, "out", x, stream, shape, out_dtype)
+    _call(lib.kda_linear, args, dev, stream)
     return out
 
 
-def _scan_args(x, gate, gate_mode, complement, h0, cu_seqlens, h_chunks, err):
-    if gate_mode not in KDA_SCAN_GATES:
-        raise ValueError(f"gate_mode: expected one of {sorted(KDA_SCAN_GATES)}, got {gate_mode!r}")
-    if x.dim() != 3:
+def _scan_args(x, gate, gate_mode, complement, h0, cu_seqlens, h_chunks, err, dev):
+    if len(x.shape) != 3:
         raise ValueError("x: expected [B, T, D]")
-    B, T, D = (int(v) for v in x.shape)
+    B, T, D = shape = x.shape
     args = ScanArgs()
-    args.x, args.x_stride = _rows(x, "x")
-    args.gate, args.gate_stride = _rows(gate, "gate", shape=x.shape)
-    args.dtype, args.gate_dtype = _dtype_code(x.dtype), _dtype_code(gate.dtype)
+    args.x, args.x_stride = _rows(x, "x", dev, x.dtype, shape)
+    args.gate, args.gate_stride = _rows(gate, "gate", dev, gate.dtype, shape)
+    args.dtype, args.gate_dtype = _code(x.dtype), _code(gate.dtype)
     args.B, args.T, args.D = B, T, D
-    args.N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    args.N = N = B if cu_seqlens is None else cu_seqlens.numel() - 1
     args.gate_mode, args.flags = KDA_SCAN_GATES[gate_mode], KDA_SCAN_FLAG_COMPLEMENT if complement else 0
-    args.h0 = _vec(h0, "h0", (args.N, D))
-    args.cu_seqlens = _vec(cu_seqlens, "cu_seqlens", (args.N + 1,), torch.int32)
-    if h_chunks is not None and (h_chunks.dtype != torch.float32 or h_chunks.dim() != 2 or h_chunks.shape[1] != D):
-        raise ValueError(f"h_chunks: expected fp32 [chunks, {D}]")
+    args.h0 = _vec(h0, "h0", dev, (N, D))
+    args.cu_seqlens = _vec(cu_seqlens, "cu_seqlens", dev, (N + 1,), torch.int32)
     if h_chunks is not None:
-        args.h_chunks, args.h_chunks_rows = _ptr(h_chunks), int(h_chunks.shape[0])
-    args.err = _ptr(err)
-    _same_device(x, gate=gate, h0=h0, cu_seqlens=cu_seqlens, h_chunks=h_chunks, err=err)
+        if h_chunks.dim() != 2:
+            raise ValueError(f"h_chunks: expected [chunks, {D}]")
+        args.h_chunks = _vec(h_chunks, "h_chunks", dev, (h_chunks.shape[0], D))
+        args.h_chunks_rows = h_chunks.shape[0]
+    args.err = _err_word(err, dev)
     return args
 
 
@@ -703,16 +751,14 @@ def kda_scan_fwd(x, gate, *, gate_mode="log", complement=False, h0=None, cu_seql
     cu_seqlens as for kda_chunk_fwd. h_chunks (fp32 [chunk_count(B, T,
     cu_seqlens), D]) receives the state entering every 16-token chunk, which
     kda_scan_bwd reads. Returns (y, hT), hT None when output_final_state is False."""
-    args = _scan_args(x, gate, gate_mode, complement, h0, cu_seqlens, h_chunks, err)
-    with _outputs_on(stream):
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if hT is None and output_final_state:
-            hT = torch.empty(args.N, args.D, dtype=torch.float32, device=x.device)
-    _same_device(x, y=y, hT=hT)
-    args.y, args.y_stride = _rows(y, "y", x.dtype, x.shape)
-    args.hT = _vec(hT, "hT", (args.N, args.D))
-    _call("kda_scan_fwd", args, x, stream)
+    if gate_mode not in KDA_SCAN_GATES:
+        raise ValueError(f"gate_mode: expected one of {sorted(KDA_SCAN_GATES)}, got {gate_mode!r}")
+    lib = _lib or load()
+    dev = _device_of(x)
+    args = _scan_args(x, gate, gate_mode, complement, h0, cu_seqlens, h_chunks, err, dev)
+    y, args.y, args.y_stride = _output(y, "y", x, stream, x.shape, x.dtype)
+    hT, args.hT = _state_output(hT, "hT", x, stream, (args.N, args.D), output_final_state)
+    _call(lib.kda_scan_fwd, args, dev, stream)
     return y, hT
 
 
@@ -721,22 +767,20 @@ def kda_scan_bwd(x, gate, dy, h_chunks, *, gate_mode="log", complement=False, dh
     """Gradients of kda_scan_fwd from dy (of y) and dhT (of hT; None for zero), with
     the h_chunks that the forward wrote. Returns (dx, dgate, dh0), dh0 None when
     output_dh0 is False. dx may be dy or x, and dgate may be gate."""
+    if gate_mode not in KDA_SCAN_GATES:
+        raise ValueError(f"gate_mode: expected one of {sorted(KDA_SCAN_GATES)}, got {gate_mode!r}")
+    lib = _lib or load()
+    dev = _device_of(x)
+    shape, dtype = x.shape, x.dtype
     args = ScanBwdArgs()
-    args.fwd = _scan_args(x, gate, gate_mode, complement, None, cu_seqlens, h_chunks, err)
+    args.fwd = _scan_args(x, gate, gate_mode, complement, None, cu_seqlens, h_chunks, err, dev)
     N, D = args.fwd.N, args.fwd.D
-    with _outputs_on(stream):
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if dgate is None:
-            dgate = torch.empty(x.shape, dtype=gate.dtype, device=x.device)
-        if dh0 is None and output_dh0:
-            dh0 = torch.empty(N, D, dtype=torch.float32, device=x.device)
-    _same_device(x, dy=dy, dhT=dhT, dx=dx, dgate=dgate, dh0=dh0)
-    args.dy, args.dy_stride = _rows(dy, "dy", x.dtype, x.shape)
-    args.dx, args.dx_stride = _rows(dx, "dx", x.dtype, x.shape)
-    args.dgate, args.dgate_stride = _rows(dgate, "dgate", gate.dtype, x.shape)
-    args.dhT, args.dh0 = _vec(dhT, "dhT", (N, D)), _vec(dh0, "dh0", (N, D))
-    _call("kda_scan_bwd", args, x, stream)
+    args.dy, args.dy_stride = _rows(dy, "dy", dev, dtype, shape)
+    args.dhT = _vec(dhT, "dhT", dev, (N, D))
+    dx, args.dx, args.dx_stride = _output(dx, "dx", x, stream, shape, dtype)
+    dgate, args.dgate, args.dgate_stride = _output(dgate, "dgate", x, stream, shape, gate.dtype)
+    dh0, args.dh0 = _state_output(dh0, "dh0", x, stream, (N, D), output_dh0)
+    _call(lib.kda_scan_bwd, args, dev, stream)
     return dx, dgate, dh0
 
 
@@ -749,23 +793,21 @@ def kda_scan_step(x, gate, state_pool, indices, *, gate_mode="log", complement=F
     distinct. Returns y [B, D]."""
     if gate_mode not in KDA_SCAN_GATES:
         raise ValueError(f"gate_mode: expected one of {sorted(KDA_SCAN_GATES)}, got {gate_mode!r}")
-    if x.dim() != 2:
+    lib = _lib or load()
+    dev = _device_of(x)
+    if len(x.shape) != 2:
         raise ValueError("x: expected [B, D]")
-    B, D = int(x.shape[0]), int(x.shape[1])
-    if y is None:
-        with _outputs_on(stream):
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    state_out = state_pool if state_out is None else state_out
-    _same_device(x, gate=gate, state_pool=state_pool, state_out=state_out, indices=indices, y=y, err=err)
+    B, D = shape = x.shape
+    slots = state_pool.shape[0]
     args = ScanStepArgs()
-    args.dtype, args.gate_dtype, args.B, args.D = _dtype_code(x.dtype), _dtype_code(gate.dtype), B, D
-    args.num_slots, args.gate_mode = int(state_pool.shape[0]), KDA_SCAN_GATES[gate_mode]
+    args.dtype, args.gate_dtype, args.B, args.D = _code(x.dtype), _code(gate.dtype), B, D
+    args.num_slots, args.gate_mode = slots, KDA_SCAN_GATES[gate_mode]
     args.flags = (KDA_SCAN_FLAG_COMPLEMENT if complement else 0) | (KDA_FLAG_CHECK_INDICES if check_indices else 0)
-    args.x, args.x_stride = _rows(x, "x")
-    args.gate, args.gate_stride = _rows(gate, "gate", shape=x.shape)
-    args.y, args.y_stride = _rows(y, "y", x.dtype, x.shape)
-    args.state_in = _vec(state_pool, "state_pool", (args.num_slots, D))
-    args.state_out = _vec(state_out, "state_out", (args.num_slots, D))
-    args.indices, args.err = _vec(indices, "indices", (B,), torch.int32), _ptr(err)
-    _call("kda_scan_step", args, x, stream)
+    args.x, args.x_stride = _rows(x, "x", dev, x.dtype, shape)
+    args.gate, args.gate_stride = _rows(gate, "gate", dev, gate.dtype, shape)
+    y, args.y, args.y_stride = _output(y, "y", x, stream, shape, x.dtype)
+    args.state_in = _vec(state_pool, "state_pool", dev, (slots, D))
+    args.state_out = args.state_in if state_out is None else _vec(state_out, "state_out", dev, (slots, D))
+    args.indices, args.err = _vec(indices, "indices", dev, (B,), torch.int32), _err_word(err, dev)
+    _call(lib.kda_scan_step, args, dev, stream)
     return y
