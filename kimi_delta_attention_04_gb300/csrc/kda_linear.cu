@@ -16,76 +16,23 @@
 // K of one tile: each sums its share, puts it into its own shared memory, and
 // finishes 1/S of the tokens from all S (distributed shared memory), in the
 // order of the ranks, so results do not vary from run to run.
-#include "kda_cluster.cuh"
-#include "kda_elem.cuh"
-#include "kda_tcgen05.cuh"
-#include "kda_tma.h"
+#include "kda_linear.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kOut = 128;       // outputs per tile (tensor-memory lanes)
-constexpr int kKBytes = 128;    // bytes of K per block: one row of the swizzle atom
+using namespace linear;
+
 constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;
 constexpr int kEpiThreads = 128;
 constexpr int kTmaThreads = kEpiThreads + 64;       // + MMA warp, TMA warp
 constexpr int kCopyThreads = kEpiThreads + 32 + 256;  // + MMA warp, two groups of loaders
-constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct LinearHead {
   uint64_t full[kMaxStages], empty[kMaxStages], acc;
   uint32_t tmem_base;
   int failed;
-};
-
-// One MMA of the 8-bit kind (e4m3 x e4m3, 32 values of K); its instruction
-// descriptor is kind::f16's with operand formats 0 (e4m3).
-__device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t smem, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case KDA_ACT_SILU: return v / (1.f + expf(-v));
-    case KDA_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678f));
-    case KDA_ACT_SIGMOID: return 1.f / (1.f + expf(-v));
-    case KDA_ACT_RELU: return v < 0.f ? 0.f : v;
-    default: return v;
-  }
-}
-
-// What one thread needs to finish its output n of a token m.
-template <typename Y>
-struct Epilogue {
-  const kda_linear_args& p;
-  int n;
-  float ws, bias;
-  __device__ __forceinline__ Epilogue(const kda_linear_args& args, int out) : p(args), n(out), ws(1.f), bias(0.f) {
-    if (n < p.N) {
-      if (p.w_scale) ws = p.w_scale[n];
-      if (p.bias) bias = p.bias[n];
-    }
-  }
-  __device__ __forceinline__ void operator()(float v, long long m) const {
-    if (m >= p.M || n >= p.N) return;
-    if (p.x_scale) v *= p.x_scale[m] * ws;
-    v = activate(v + bias, p.activation);
-    if (p.residual) v += load_f(static_cast<const Y*>(p.residual) + m * p.ld_residual + n);
-    store_f(static_cast<Y*>(p.y) + m * p.ldy + n, v);
-  }
 };
 
 // 16 bytes of a row at byte offset `off` of [0, row_bytes): bytes past the row are
@@ -207,7 +154,7 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
       bool ok = true;
       for (int i = 0; i < nkb && ok; ++i) {
         const int s = i % stages;
-        ok = mbar_wait_bounded(smem_u32(&sm.full[s]), (i / stages) & 1, kWaitNs);
+        ok = mbar_wait_bounded(smem_u32(&sm.full[s]), (i / stages) & 1, kLinearWaitNs);
         if (!ok) break;
         tc05::fence_after_sync();
         const uint32_t w = smem_u32(ring + s * kStage), x = w + kWBytes;
@@ -229,7 +176,7 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
       int i = 0;
       for (; i < nkb; ++i) {
         const int s = i % stages;
-        if (i >= stages) ok = mbar_wait_bounded(smem_u32(&sm.empty[s]), (i / stages - 1) & 1, kWaitNs);
+        if (i >= stages) ok = mbar_wait_bounded(smem_u32(&sm.empty[s]), (i / stages - 1) & 1, kLinearWaitNs);
         if (!ok) break;
         const uint32_t w = smem_u32(ring + s * kStage), bar = smem_u32(&sm.full[s]);
         mbar_arrive_expect_tx_local(&sm.full[s], kStage);
@@ -239,14 +186,14 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
       if (!ok) sm.failed = 1;
       // no copy is left in flight when the CTA ends
       for (int j = i > stages ? i - stages : 0; j < i; ++j)
-        mbar_wait_bounded(smem_u32(&sm.full[j % stages]), (j / stages) & 1, kWaitNs);
+        mbar_wait_bounded(smem_u32(&sm.full[j % stages]), (j / stages) & 1, kLinearWaitNs);
     }
   } else if (!TMA && warp >= 5) {
     const int group = (warp - 5) >> 2, t = tid - kEpiThreads - 32 - 128 * group;
     bool ok = true;
     for (int i = group; i < nkb && ok; i += 2) {
       const int s = i % stages;
-      if (i >= stages) ok = mbar_wait_bounded(smem_u32(&sm.empty[s]), (i / stages - 1) & 1, kWaitNs);
+      if (i >= stages) ok = mbar_wait_bounded(smem_u32(&sm.empty[s]), (i / stages - 1) & 1, kLinearWaitNs);
       if (!ok) break;
       unsigned char* w = ring + s * kStage;
       copy_tile<E, kOut>(w, p.w, p.ldw, n0, p.N, kb0 + i, p.K, t);
@@ -259,7 +206,7 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
   __syncwarp();
 
   bool ok = true;
-  if (warp < 4) ok = mbar_wait_bounded(smem_u32(&sm.acc), 0, kWaitNs);
+  if (warp < 4) ok = mbar_wait_bounded(smem_u32(&sm.acc), 0, kLinearWaitNs);
   if (!ok) sm.failed = 1;
   tc05::fence_after_sync();
   const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
@@ -267,10 +214,9 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
     if (warp < 4 && __all_sync(0xffffffffu, ok)) {
       const Epilogue<Y> finish(p, n0 + tid);
       for (int c0 = 0; c0 < TOK && m0 + c0 < p.M; c0 += 16) {
-        uint32_t r[16];
-        tc05::ld16_wait(tlane + c0, r);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) finish(__uint_as_float(r[j]), static_cast<long long>(m0) + c0 + j);
+        float v[16];
+        tmem_load(tlane + c0, v);
+        finish(v, static_cast<long long>(m0) + c0);
       }
     }
   } else {
@@ -278,10 +224,10 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
     float* part = reinterpret_cast<float*>(ring);
     if (warp < 4 && __all_sync(0xffffffffu, ok)) {
       for (int c0 = 0; c0 < TOK; c0 += 16) {
-        uint32_t r[16];
-        tc05::ld16_wait(tlane + c0, r);
+        float v[16];
+        tmem_load(tlane + c0, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c0 + j) * kOut + tid] = __uint_as_float(r[j]);
+        for (int j = 0; j < 16; ++j) part[(c0 + j) * kOut + tid] = v[j];
       }
     }
     cluster_sync_all();
@@ -290,8 +236,8 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
       const int per = TOK / S;
       for (int c = rank * per; c < (rank + 1) * per && m0 + c < p.M; ++c) {
         const uint32_t at = smem_u32(part + c * kOut + tid);
-        float v = 0.f;
-        for (int r = 0; r < S; ++r) v += ld_shared_cluster_f32(mapa_shared(at, r));
+        float v[1] = {0.f};
+        for (int r = 0; r < S; ++r) v[0] += ld_shared_cluster_f32(mapa_shared(at, r));
         finish(v, static_cast<long long>(m0) + c);
       }
     }
@@ -352,7 +298,8 @@ cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
   if (a.M <= 16) return launch_tile<E, Y, 16, true>(a, s);
   if (a.M <= 32) return launch_tile<E, Y, 32, true>(a, s);
   if (a.M <= 64) return launch_tile<E, Y, 64, true>(a, s);
-  return launch_tile<E, Y, 128, true>(a, s);
+  if (a.M <= 128) return launch_tile<E, Y, 128, true>(a, s);
+  return launch_linear_pair(a, s);
 }
 
 }  // namespace
