@@ -111,6 +111,29 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
   return v;
 }
 
+// Tokens c .. c_end - 1 of the tile from the sums of all S CTAs (part: [token][output]
+// in each one's shared memory), C tokens at a time so that their reads overlap.
+template <int C, typename Y>
+__device__ __forceinline__ void finish_shared(const Epilogue<Y>& finish, const float* part, int c, int c_end, int m0, int M,
+                                              int S, int out) {
+  for (; c < c_end && m0 + c < M; c += C) {
+    float v[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) v[j] = 0.f;
+    const uint32_t at = smem_u32(part + c * kOut + out);
+#pragma unroll 2
+    for (int r = 0; r < S; ++r) {
+      const uint32_t peer = mapa_shared(at, r);
+      float u[C];
+#pragma unroll
+      for (int j = 0; j < C; ++j) u[j] = ld_shared_cluster_f32(peer + j * kOut * 4);
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] += u[j];
+    }
+    finish(v, static_cast<long long>(m0) + c);
+  }
+}
+
 // Grid (S * output tiles, token tiles), cluster (S, 1, 1).
 // E: bits of an operand element (uint16_t bf16, uint8_t e4m3).
 template <typename E, typename Y, int TOK, bool TMA>
@@ -234,12 +257,8 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
     if (warp < 4) {
       const Epilogue<Y> finish(p, n0 + tid);
       const int per = TOK / S;
-      for (int c = rank * per; c < (rank + 1) * per && m0 + c < p.M; ++c) {
-        const uint32_t at = smem_u32(part + c * kOut + tid);
-        float v[1] = {0.f};
-        for (int r = 0; r < S; ++r) v[0] += ld_shared_cluster_f32(mapa_shared(at, r));
-        finish(v, static_cast<long long>(m0) + c);
-      }
+      if (per % 8 == 0) finish_shared<8>(finish, part, rank * per, (rank + 1) * per, m0, p.M, S, tid);
+      else finish_shared<2>(finish, part, rank * per, (rank + 1) * per, m0, p.M, S, tid);
     }
     cluster_sync_all();  // nobody reads this CTA's shared memory any more
   }

@@ -33,14 +33,26 @@ __device__ __forceinline__ void tma_load_2d(uint32_t smem, const CUtensorMap* ma
       : "memory");
 }
 
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case KDA_ACT_SILU: return v / (1.f + expf(-v));
-    case KDA_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678f));
-    case KDA_ACT_SIGMOID: return 1.f / (1.f + expf(-v));
-    case KDA_ACT_RELU: return v < 0.f ? 0.f : v;
-    default: return v;
-  }
+// 1 / (1 + e^-v) from the special-function unit (ex2, rcp: a few units in the last
+// place of fp32); e^-v = inf gives 0.
+__device__ __forceinline__ float fast_sigmoid(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-1.44269504f * v)));
+  return r;
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+  if (ACT == KDA_ACT_SILU) return v * fast_sigmoid(v);
+  if (ACT == KDA_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678f));
+  if (ACT == KDA_ACT_SIGMOID) return fast_sigmoid(v);
+  if (ACT == KDA_ACT_RELU) return v < 0.f ? 0.f : v;
+  return v;
+}
+template <int ACT, int C>
+__device__ __forceinline__ void activate_all(float (&v)[C]) {
+#pragma unroll
+  for (int j = 0; j < C; ++j) v[j] = activate<ACT>(v[j]);
 }
 
 // What one thread needs to finish its output n of a tile's tokens.
@@ -55,24 +67,44 @@ struct Epilogue {
       if (p.bias) bias = p.bias[n];
     }
   }
-  // Tokens m .. m + C - 1 (those below M). What the tokens need is read before
-  // anything is stored: y may be the residual, so no load passes a store.
+  // Tokens m .. m + C - 1 (those below M). The choices are made once for the C
+  // values, and all reads are issued before anything is stored (y may be the
+  // residual, so no load passes a store): 32 reads one by one had made the epilogue
+  // of 8192 x 4096 outputs 5 times the products' time.
   template <int C>
-  __device__ __forceinline__ void operator()(const float (&acc)[C], long long m) const {
+  __device__ __forceinline__ void operator()(float (&v)[C], long long m) const {
     const int live = n < p.N ? static_cast<int>(p.M - m < C ? p.M - m : C) : 0;
     if (live <= 0) return;
-    float xs[C], res[C];
-    const Y* r = static_cast<const Y*>(p.residual) + m * p.ld_residual + n;
+    float res[C];
+    if (p.residual) {
+      const Y* r = static_cast<const Y*>(p.residual) + m * p.ld_residual + n;
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      xs[j] = p.x_scale && j < live ? p.x_scale[m + j] : 1.f;
-      res[j] = p.residual && j < live ? load_f(r + j * p.ld_residual) : 0.f;
+      for (int j = 0; j < C; ++j) res[j] = load_f(r + (j < live ? j : 0) * p.ld_residual);
+    } else {
+#pragma unroll
+      for (int j = 0; j < C; ++j) res[j] = 0.f;
+    }
+    if (p.x_scale) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] *= p.x_scale[m + (j < live ? j : 0)] * ws;
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) v[j] += bias;
+    switch (p.activation) {
+      case KDA_ACT_SILU: activate_all<KDA_ACT_SILU>(v); break;
+      case KDA_ACT_GELU: activate_all<KDA_ACT_GELU>(v); break;
+      case KDA_ACT_SIGMOID: activate_all<KDA_ACT_SIGMOID>(v); break;
+      case KDA_ACT_RELU: activate_all<KDA_ACT_RELU>(v); break;
+      default: break;
     }
     Y* y = static_cast<Y*>(p.y) + m * p.ldy + n;
+    if (live == C) {
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const float v = activate(acc[j] * (xs[j] * ws) + bias, p.activation) + res[j];
-      if (j < live) store_f(y + j * p.ldy, v);
+      for (int j = 0; j < C; ++j) store_f(y + j * p.ldy, v[j] + res[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (j < live) store_f(y + j * p.ldy, v[j] + res[j]);
     }
   }
 };
