@@ -25,9 +25,14 @@ constexpr int kBlockCh = 64;      // channels of a CTA
 constexpr int kMaxCluster = 8;
 constexpr int kStepThreads = 128;
 
-// sigmoid without overflow: e^-f = inf gives 0
+// The decay, to about an fp32 step. Long memories multiply hundreds of decays near
+// 1, so exp keeps expf's accuracy; in the sigmoid the error of e^-f is scaled by
+// 1 - a, and the special-function unit's ex2 and rcp do. (e^-f = inf gives 0.)
 __device__ __forceinline__ float decay_of(float f, int mode) {
-  return mode == KDA_SCAN_LOG_DECAY ? expf(f) : 1.f / (1.f + expf(-f));
+  if (mode == KDA_SCAN_LOG_DECAY) return expf(f);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-1.44269504f * f)));
+  return r;
 }
 
 struct SeqPos {
@@ -102,6 +107,12 @@ struct Raw2<float> {
 __device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v) { *reinterpret_cast<uint32_t*>(p) = Bf16::pack(v.x, v.y); }
 __device__ __forceinline__ void store2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 
+// 4- or 8-byte asynchronous copy into shared memory.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(void* smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(smem)), "l"(gmem), "n"(BYTES) : "memory");
+}
+
 // A lane's two channels and which of them exist.
 struct Lane {
   int c0, c1;
@@ -130,6 +141,38 @@ __device__ __forceinline__ Raw2<T> load_pair(const T* row, const Lane& l) {
   }
   return r;
 }
+
+// One tensor's share of a warp's tile on its way in: the 16 tokens of this thread's
+// two channels, in slots of shared memory that only this thread touches, so a
+// thread waits for its own copies alone. fetch() starts the copies (where pairs
+// cannot be copied as one word it loads and stores them); get() reads a slot.
+template <typename T, bool VEC>
+struct Tile {
+  using Slot = Raw2<T>;
+  Slot* slots;  // [token][thread]
+  __device__ __forceinline__ void fetch(const T* rows, long long stride, int m, const Lane& l) const {
+    if (VEC) {
+      if (l.p0) {
+#pragma unroll
+        for (int i = 0; i < kScanChunk; ++i)
+          if (i < m) cp_async_small<sizeof(Slot)>(slots + i * kThreads + threadIdx.x, rows + i * stride + l.c0);
+      }
+    } else {
+      Slot r[kScanChunk];
+#pragma unroll
+      for (int i = 0; i < kScanChunk; ++i) {
+        r[i].zero();
+        if (i < m) r[i] = load_pair<VEC>(rows + i * stride, l);
+      }
+#pragma unroll
+      for (int i = 0; i < kScanChunk; ++i) slots[i * kThreads + threadIdx.x] = r[i];
+    }
+  }
+  // (a token or channel that does not exist reads what the slot held: its result is not used)
+  __device__ __forceinline__ float2 get(int i) const { return slots[i * kThreads + threadIdx.x].get(); }
+};
+template <typename T>
+constexpr size_t tile_bytes() { return sizeof(Raw2<T>) * kScanChunk * kThreads; }
 
 template <bool VEC, typename T>
 __device__ __forceinline__ void store_pair(T* row, const Lane& l, float2 v) {
@@ -205,11 +248,18 @@ __device__ __forceinline__ float2 enter_state(ScanSmem& sm, const Map& mine, flo
   return fma2(before.A, in, before.B);
 }
 
+// Stages of the ring of tiles: what leaves two CTAs on an SM (about 100 KB each),
+// at least two.
+constexpr int stages_for(size_t stage) { return 100 * 1024 / stage >= 3 ? 3 : 2; }
+
 // Forward. Grid (S * channel blocks, sequences), cluster (S, 1, 1).
 template <typename X, typename G, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) kda_scan_fwd_kernel(const kda_scan_args p, int S) {
+  extern __shared__ __align__(16) unsigned char ring[];
   __shared__ ScanSmem sm;
-  const int warp = threadIdx.x >> 5, rank = blockIdx.x % S;
+  constexpr size_t kStage = tile_bytes<X>() + tile_bytes<G>();
+  constexpr int kStages = stages_for(kStage);
+  const int warp = threadIdx.x >> 5, rank = blockIdx.x % S, advance = S * kWarps * kScanChunk;
   const Lane l = lane_channels<VEC>(blockIdx.x / S * kBlockCh, p.D);
   const bool comp = p.flags & KDA_SCAN_FLAG_COMPLEMENT;
   if (S > 1) cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written
@@ -218,29 +268,33 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_fwd_kernel(const kda_sca
     SeqPos pos;
     if (!find_sequence(p, n, pos)) return;  // (the same answer in every CTA)
     const int len = pos.end - pos.start;
-    float2 carry = load_state(p.h0, n, p.D, l);
-    for (int base = 0; base < len; base += S * kWarps * kScanChunk, parity ^= 1) {
-      const int i0 = base + (rank * kWarps + warp) * kScanChunk;  // first token of this warp's chunk
-      const int m = min(kScanChunk, len - i0);
-      const X* x = static_cast<const X*>(p.x) + (pos.start + static_cast<long long>(i0)) * p.x_stride;
-      const G* gate = static_cast<const G*>(p.gate) + (pos.start + static_cast<long long>(i0)) * p.gate_stride;
-      Raw2<X> rx[kScanChunk];
-      Raw2<G> rg[kScanChunk];
-#pragma unroll
-      for (int i = 0; i < kScanChunk; ++i) {
-        rx[i].zero();
-        rg[i].zero();
-        if (i < m) {
-          rx[i] = load_pair<VEC>(x + i * p.x_stride, l);
-          rg[i] = load_pair<VEC>(gate + i * p.gate_stride, l);
-        }
+    // the tiles of advance j, whose first token for this warp is i0
+    auto tile_x = [&](int j) { return Tile<X, VEC>{reinterpret_cast<Raw2<X>*>(ring + (j % kStages) * kStage)}; };
+    auto tile_g = [&](int j) { return Tile<G, VEC>{reinterpret_cast<Raw2<G>*>(ring + (j % kStages) * kStage + tile_bytes<X>())}; };
+    auto first = [&](int j) { return j * advance + (rank * kWarps + warp) * kScanChunk; };
+    auto fetch = [&](int j) {
+      const int i0 = first(j);
+      if (i0 < len) {
+        const long long t0 = pos.start + static_cast<long long>(i0);
+        tile_x(j).fetch(static_cast<const X*>(p.x) + t0 * p.x_stride, p.x_stride, len - i0, l);
+        tile_g(j).fetch(static_cast<const G*>(p.gate) + t0 * p.gate_stride, p.gate_stride, len - i0, l);
       }
+      cp_async_commit();
+    };
+    float2 carry = load_state(p.h0, n, p.D, l);
+    for (int j = 0; j < kStages - 1; ++j) fetch(j);
+    for (int j = 0; j * static_cast<long long>(advance) < len; ++j, parity ^= 1) {
+      fetch(j + kStages - 1);
+      cp_async_wait<kStages - 1>();
+      const int i0 = first(j), m = min(kScanChunk, len - i0);
+      const Tile<X, VEC> tx = tile_x(j);
+      const Tile<G, VEC> tg = tile_g(j);
       float2 a[kScanChunk], u[kScanChunk];
       Map mine{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int i = 0; i < kScanChunk; ++i) {
-        a[i] = decay2(rg[i].get(), p.gate_mode);
-        u[i] = rx[i].get();
+        a[i] = decay2(tg.get(i), p.gate_mode);
+        u[i] = tx.get(i);
         if (comp) u[i] = make_float2((1.f - a[i].x) * u[i].x, (1.f - a[i].y) * u[i].y);
         if (i < m) mine = then(mine, Map{a[i], u[i]});
       }
@@ -266,7 +320,10 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_fwd_kernel(const kda_sca
 // h_chunks, so the forward direction needs no exchange.
 template <typename X, typename G, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_scan_bwd_args q, int S) {
+  extern __shared__ __align__(16) unsigned char ring[];
   __shared__ ScanSmem sm;
+  constexpr size_t kStage = 2 * tile_bytes<X>() + tile_bytes<G>();
+  constexpr int kStages = stages_for(kStage);
   const kda_scan_args& p = q.fwd;
   const int warp = threadIdx.x >> 5, rank = blockIdx.x % S;
   const Lane l = lane_channels<VEC>(blockIdx.x / S * kBlockCh, p.D);
@@ -277,47 +334,51 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_sca
     SeqPos pos;
     if (!find_sequence(p, n, pos)) return;
     const int len = pos.end - pos.start, chunks = (len + kScanChunk - 1) / kScanChunk;
-    float2 carry = load_state(q.dhT, n, p.D, l);
-    for (int base = 0; base < chunks; base += S * kWarps, parity ^= 1) {
-      const int k = chunks - 1 - (base + rank * kWarps + warp);  // this warp's chunk (negative: none left)
-      const int m = k < 0 ? 0 : min(kScanChunk, len - k * kScanChunk);
-      const long long t0 = pos.start + static_cast<long long>(k) * kScanChunk;
-      const X* x = static_cast<const X*>(p.x) + t0 * p.x_stride;
-      const G* gate = static_cast<const G*>(p.gate) + t0 * p.gate_stride;
-      const X* dy = static_cast<const X*>(q.dy) + t0 * q.dy_stride;
-      Raw2<X> rx[kScanChunk], rd[kScanChunk];
-      Raw2<G> rg[kScanChunk];
-#pragma unroll
-      for (int i = 0; i < kScanChunk; ++i) {
-        rx[i].zero();
-        rg[i].zero();
-        rd[i].zero();
-        if (i < m) {
-          rx[i] = load_pair<VEC>(x + i * p.x_stride, l);
-          rg[i] = load_pair<VEC>(gate + i * p.gate_stride, l);
-          rd[i] = load_pair<VEC>(dy + i * q.dy_stride, l);
-        }
+    auto tile_x = [&](int j) { return Tile<X, VEC>{reinterpret_cast<Raw2<X>*>(ring + (j % kStages) * kStage)}; };
+    auto tile_d = [&](int j) { return Tile<X, VEC>{reinterpret_cast<Raw2<X>*>(ring + (j % kStages) * kStage + tile_bytes<X>())}; };
+    auto tile_g = [&](int j) { return Tile<G, VEC>{reinterpret_cast<Raw2<G>*>(ring + (j % kStages) * kStage + 2 * tile_bytes<X>())}; };
+    // this warp's chunk of advance j (negative: none left)
+    auto chunk_of = [&](int j) { return chunks - 1 - ((j * S + rank) * kWarps + warp); };
+    auto fetch = [&](int j) {
+      const int k = chunk_of(j);
+      if (k >= 0) {
+        const int m = len - k * kScanChunk;
+        const long long t0 = pos.start + static_cast<long long>(k) * kScanChunk;
+        tile_x(j).fetch(static_cast<const X*>(p.x) + t0 * p.x_stride, p.x_stride, m, l);
+        tile_g(j).fetch(static_cast<const G*>(p.gate) + t0 * p.gate_stride, p.gate_stride, m, l);
+        tile_d(j).fetch(static_cast<const X*>(q.dy) + t0 * q.dy_stride, q.dy_stride, m, l);
       }
+      cp_async_commit();
+    };
+    float2 carry = load_state(q.dhT, n, p.D, l);
+    for (int j = 0; j < kStages - 1; ++j) fetch(j);
+    for (int j = 0; j * S * kWarps < chunks; ++j, parity ^= 1) {
+      const int k = chunk_of(j), m = k < 0 ? 0 : min(kScanChunk, len - k * kScanChunk);
+      const long long t0 = pos.start + static_cast<long long>(k) * kScanChunk;
       float2 h = m > 0 ? load_state(p.h_chunks, pos.chunk_base + k, p.D, l) : make_float2(0.f, 0.f);
+      fetch(j + kStages - 1);
+      cp_async_wait<kStages - 1>();
+      const Tile<X, VEC> tx = tile_x(j), td = tile_d(j);
+      const Tile<G, VEC> tg = tile_g(j);
       float2 a[kScanChunk], w[kScanChunk];  // decay; what d multiplies in the decay's gradient
 #pragma unroll
       for (int i = 0; i < kScanChunk; ++i) {
-        a[i] = decay2(rg[i].get(), p.gate_mode);
-        const float2 xv = rx[i].get();
+        a[i] = decay2(tg.get(i), p.gate_mode);
+        const float2 xv = tx.get(i);
         w[i] = comp ? make_float2(h.x - xv.x, h.y - xv.y) : h;
         h = comp ? fma2(a[i], w[i], xv) : fma2(a[i], h, xv);  // a h + (1 - a) x = x + a (h - x)
       }
       Map mine{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};  // d -> a (d + dy), last token first
 #pragma unroll
       for (int i = kScanChunk - 1; i >= 0; --i)
-        if (i < m) mine = then(mine, Map{a[i], mul2(a[i], rd[i].get())});
+        if (i < m) mine = then(mine, Map{a[i], mul2(a[i], td.get(i))});
       float2 d = enter_state(sm, mine, carry, parity, S, rank);
       X* dx = static_cast<X*>(q.dx) + t0 * q.dx_stride;
       G* dg = static_cast<G*>(q.dgate) + t0 * q.dgate_stride;
 #pragma unroll
       for (int i = kScanChunk - 1; i >= 0; --i) {
         if (i < m) {
-          const float2 dyv = rd[i].get(), b = make_float2(1.f - a[i].x, 1.f - a[i].y);
+          const float2 dyv = td.get(i), b = make_float2(1.f - a[i].x, 1.f - a[i].y);
           d = make_float2(d.x + dyv.x, d.y + dyv.y);
           store_pair<VEC>(dx + i * q.dx_stride, l, comp ? mul2(b, d) : d);
           d = mul2(a[i], d);
@@ -351,14 +412,16 @@ __global__ void __launch_bounds__(kStepThreads) kda_scan_step_kernel(const kda_s
   store_f(y, h);
 }
 
-// CTAs of a cluster: enough that the grid fills the 152 SMs twice over (two CTAs
-// are resident on each), no more than the sequences (their mean length, where
-// they are packed) have advances for.
+// CTAs of a cluster: as many as leave the whole grid resident at once (two CTAs on
+// each of 152 SMs), no more than the sequences (their mean length, where they are
+// packed) have advances for. Packed sequences differ in length, so they get up to
+// four times as many, whose order of execution evens the lengths out.
 int cluster_size(const kda_scan_args& a) {
   const long long blocks = (a.D + kBlockCh - 1) / kBlockCh * static_cast<long long>(a.N);
   const long long mean = a.cu_seqlens ? (a.T + a.N - 1) / a.N : a.T;
+  const long long room = 2 * 152 * (a.cu_seqlens && a.N > 1 ? 4 : 1);
   int S = 1;
-  while (S < kMaxCluster && blocks * S < 2 * 152 && mean > S * kWarps * kScanChunk) S *= 2;
+  while (S < kMaxCluster && blocks * S * 2 <= room && mean > S * kWarps * kScanChunk) S *= 2;
   return S;
 }
 
@@ -368,12 +431,18 @@ bool pairs_ok(const void* p, int64_t stride, size_t elem) {
 }
 size_t elem_bytes(int32_t dt) { return dt == KDA_DTYPE_FP32 ? 4 : 2; }
 
+// One instance's launch. `done` is the instance's record of devices whose
+// shared-memory limit has been raised.
 template <typename Args>
-cudaError_t launch_clusters(void (*kernel)(Args, int), const Args& a, const kda_scan_args& f, cudaStream_t s) {
+cudaError_t launch_clusters(void (*kernel)(Args, int), std::atomic<uint64_t>& done, size_t smem, const Args& a,
+                            const kda_scan_args& f, cudaStream_t s) {
+  const cudaError_t e = set_smem_limit_once(kernel, smem, done);
+  if (e != cudaSuccess) return e;
   const int S = cluster_size(f);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((f.D + kBlockCh - 1) / kBlockCh * S), static_cast<unsigned>(f.N < 65535 ? f.N : 65535));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -384,19 +453,35 @@ cudaError_t launch_clusters(void (*kernel)(Args, int), const Args& a, const kda_
   return cudaLaunchKernelEx(&cfg, kernel, a, S);
 }
 
+template <typename X, typename G, bool VEC>
+cudaError_t launch_fwd(const kda_scan_args& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  constexpr size_t stage = tile_bytes<X>() + tile_bytes<G>();
+  return launch_clusters(kda_scan_fwd_kernel<X, G, VEC>, done, stages_for(stage) * stage, a, a, s);
+}
+
+template <typename X, typename G, bool VEC>
+cudaError_t launch_bwd(const kda_scan_bwd_args& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  constexpr size_t stage = 2 * tile_bytes<X>() + tile_bytes<G>();
+  return launch_clusters(kda_scan_bwd_kernel<X, G, VEC>, done, stages_for(stage) * stage, a, a.fwd, s);
+}
+
 }  // namespace
 
 // The instances by tensor types: x bf16 with a bf16 or fp32 gate, or both fp32.
-#define KDA_SCAN_KERNEL(kernel, vec, xt, gt)                                                            \
-  ((xt) == KDA_DTYPE_FP32   ? ((vec) ? kernel<float, float, true> : kernel<float, float, false>)        \
-   : (gt) == KDA_DTYPE_FP32 ? ((vec) ? kernel<__nv_bfloat16, float, true> : kernel<__nv_bfloat16, float, false>) \
-                            : ((vec) ? kernel<__nv_bfloat16, __nv_bfloat16, true> : kernel<__nv_bfloat16, __nv_bfloat16, false>))
+#define KDA_SCAN_LAUNCH(launch, vec, xt, gt, ...)                                                        \
+  ((xt) == KDA_DTYPE_FP32   ? ((vec) ? launch<float, float, true>(__VA_ARGS__) : launch<float, float, false>(__VA_ARGS__)) \
+   : (gt) == KDA_DTYPE_FP32 ? ((vec) ? launch<__nv_bfloat16, float, true>(__VA_ARGS__)                   \
+                                     : launch<__nv_bfloat16, float, false>(__VA_ARGS__))                 \
+                            : ((vec) ? launch<__nv_bfloat16, __nv_bfloat16, true>(__VA_ARGS__)           \
+                                     : launch<__nv_bfloat16, __nv_bfloat16, false>(__VA_ARGS__)))
 
 cudaError_t launch_scan_fwd(const kda_scan_args& a, cudaStream_t s) {
   const size_t xe = elem_bytes(a.dtype), ge = elem_bytes(a.gate_dtype);
   const bool vec = a.D % 2 == 0 && pairs_ok(a.x, a.x_stride, xe) && pairs_ok(a.gate, a.gate_stride, ge) &&
                    pairs_ok(a.y, a.y_stride, xe);
-  return launch_clusters(KDA_SCAN_KERNEL(kda_scan_fwd_kernel, vec, a.dtype, a.gate_dtype), a, a, s);
+  return KDA_SCAN_LAUNCH(launch_fwd, vec, a.dtype, a.gate_dtype, a, s);
 }
 
 cudaError_t launch_scan_bwd(const kda_scan_bwd_args& a, cudaStream_t s) {
@@ -405,7 +490,7 @@ cudaError_t launch_scan_bwd(const kda_scan_bwd_args& a, cudaStream_t s) {
   const bool vec = f.D % 2 == 0 && pairs_ok(f.x, f.x_stride, xe) && pairs_ok(f.gate, f.gate_stride, ge) &&
                    pairs_ok(a.dy, a.dy_stride, xe) && pairs_ok(a.dx, a.dx_stride, xe) &&
                    pairs_ok(a.dgate, a.dgate_stride, ge);
-  return launch_clusters(KDA_SCAN_KERNEL(kda_scan_bwd_kernel, vec, f.dtype, f.gate_dtype), a, f, s);
+  return KDA_SCAN_LAUNCH(launch_bwd, vec, f.dtype, f.gate_dtype, a, s);
 }
 
 cudaError_t launch_scan_step(const kda_scan_step_args& a, cudaStream_t s) {
