@@ -24,12 +24,14 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kBlockCh = 64;      // channels of a CTA
 constexpr int kMaxCluster = 8;
 constexpr int kStepThreads = 128;
+constexpr uint64_t kWaitNs = 2000000000ull;
 
 // The decay, to about an fp32 step. Long memories multiply hundreds of decays near
 // 1, so exp keeps expf's accuracy; in the sigmoid the error of e^-f is scaled by
 // 1 - a, and the special-function unit's ex2 and rcp do. (e^-f = inf gives 0.)
-__device__ __forceinline__ float decay_of(float f, int mode) {
-  if (mode == KDA_SCAN_LOG_DECAY) return expf(f);
+template <int MODE>
+__device__ __forceinline__ float decay_of(float f) {
+  if (MODE == KDA_SCAN_LOG_DECAY) return expf(f);
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-1.44269504f * f)));
   return r;
@@ -76,19 +78,20 @@ __device__ __forceinline__ bool find_sequence(const kda_scan_args& p, int n, Seq
   return true;
 }
 
-// Two channels of one token. VEC: a lane's channels are 2 lane and 2 lane + 1
-// (even D and strides, aligned pointers), one access; otherwise lane and
-// lane + 32, two accesses, whatever the alignment.
+// How a tile's rows are read and written, by their alignment: 16 bytes at a time,
+// a pair of channels at a time, or one.
+enum { kWide = 2, kPair = 1, kSingle = 0 };
+
+// Two channels of one token: 2 lane and 2 lane + 1 of the block, or with kSingle
+// lane and lane + 32.
 template <typename T>
 struct Raw2;
 template <>
 struct Raw2<__nv_bfloat16> {
   uint32_t v;
-  __device__ __forceinline__ void zero() { v = 0; }
   __device__ __forceinline__ float2 get() const {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
   }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint32_t*>(p); }
   __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
     const uint32_t lo = p ? *reinterpret_cast<const uint16_t*>(p) : 0u;
     const uint32_t hi = q ? *reinterpret_cast<const uint16_t*>(q) : 0u;
@@ -98,85 +101,81 @@ struct Raw2<__nv_bfloat16> {
 template <>
 struct Raw2<float> {
   float2 v;
-  __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
   __device__ __forceinline__ float2 get() const { return v; }
-  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
   __device__ __forceinline__ void load(const float* p, const float* q) { v = make_float2(p ? *p : 0.f, q ? *q : 0.f); }
 };
 
 __device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v) { *reinterpret_cast<uint32_t*>(p) = Bf16::pack(v.x, v.y); }
 __device__ __forceinline__ void store2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 
-// 4- or 8-byte asynchronous copy into shared memory.
 template <int BYTES>
-__device__ __forceinline__ void cp_async_small(void* smem, const void* gmem) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(smem)), "l"(gmem), "n"(BYTES) : "memory");
+__device__ __forceinline__ void cp_async_bytes(void* smem, const void* gmem) {
+  if (BYTES == 16) cp_async16(smem, gmem);
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(smem)), "l"(gmem), "n"(BYTES) : "memory");
 }
 
-// A lane's two channels and which of them exist.
+// A lane's two channels, and which of them exist.
 struct Lane {
-  int c0, c1;
+  int block_ch, c0, c1;
   bool p0, p1;
 };
 
-template <bool VEC>
+template <int ACC>
 __device__ __forceinline__ Lane lane_channels(int block_ch, int D) {
   const int lane = threadIdx.x & 31;
   Lane l;
-  l.c0 = block_ch + (VEC ? 2 * lane : lane);
-  l.c1 = block_ch + (VEC ? 2 * lane + 1 : lane + 32);
+  l.block_ch = block_ch;
+  l.c0 = block_ch + (ACC == kSingle ? lane : 2 * lane);
+  l.c1 = block_ch + (ACC == kSingle ? lane + 32 : 2 * lane + 1);
   l.p0 = l.c0 < D;
   l.p1 = l.c1 < D;
   return l;
 }
 
-template <bool VEC, typename T>
-__device__ __forceinline__ Raw2<T> load_pair(const T* row, const Lane& l) {
-  Raw2<T> r;
-  if (VEC) {
-    if (l.p0) r.load(row + l.c0);
-    else r.zero();
-  } else {
-    r.load(l.p0 ? row + l.c0 : nullptr, l.p1 ? row + l.c1 : nullptr);
-  }
-  return r;
-}
-
-// One tensor's share of a warp's tile on its way in: the 16 tokens of this thread's
-// two channels, in slots of shared memory that only this thread touches, so a
-// thread waits for its own copies alone. fetch() starts the copies (where pairs
-// cannot be copied as one word it loads and stores them); get() reads a slot.
-template <typename T, bool VEC>
+// One tensor's share of a warp's tile on its way in: 16 tokens x 64 channels,
+// token by token, in shared memory that only this warp touches. fetch() starts the
+// copies (kSingle loads and stores); once they have landed and the warp has
+// synchronised, get() reads a lane's pair. Tokens past m and channels past D are
+// not copied: what their slots held is read, and the results are not used.
+template <typename T, int ACC>
 struct Tile {
-  using Slot = Raw2<T>;
-  Slot* slots;  // [token][thread]
-  __device__ __forceinline__ void fetch(const T* rows, long long stride, int m, const Lane& l) const {
-    if (VEC) {
-      if (l.p0) {
+  Raw2<T>* pairs;  // this warp's
+  __device__ __forceinline__ void fetch(const T* rows, long long stride, int m, const Lane& l, int D) const {
+    const int lane = threadIdx.x & 31;
+    if (ACC == kWide) {
+      constexpr int PER = 16 / sizeof(T), LANES = kBlockCh / PER, TOK = 32 / LANES;  // lanes of a token, tokens a step
+      const int i0 = lane / LANES, c = lane % LANES * PER;
+      if (l.block_ch + c >= D) return;
+      const T* src = rows + i0 * stride + l.block_ch + c;
+      unsigned char* dst = reinterpret_cast<unsigned char*>(pairs) + (i0 * kBlockCh + c) * sizeof(T);
 #pragma unroll
-        for (int i = 0; i < kScanChunk; ++i)
-          if (i < m) cp_async_small<sizeof(Slot)>(slots + i * kThreads + threadIdx.x, rows + i * stride + l.c0);
-      }
+      for (int i = 0; i < kScanChunk / TOK; ++i, src += TOK * stride)
+        if (i * TOK + i0 < m) cp_async_bytes<16>(dst + i * TOK * kBlockCh * sizeof(T), src);
+    } else if (ACC == kPair) {
+      if (!l.p0) return;
+      const T* src = rows + l.c0;
+#pragma unroll
+      for (int i = 0; i < kScanChunk; ++i, src += stride)
+        if (i < m) cp_async_bytes<2 * sizeof(T)>(pairs + i * 32 + lane, src);
     } else {
-      Slot r[kScanChunk];
+      Raw2<T> r[kScanChunk];
 #pragma unroll
       for (int i = 0; i < kScanChunk; ++i) {
-        r[i].zero();
-        if (i < m) r[i] = load_pair<VEC>(rows + i * stride, l);
+        const T* row = rows + i * stride;
+        r[i].load(i < m && l.p0 ? row + l.c0 : nullptr, i < m && l.p1 ? row + l.c1 : nullptr);
       }
 #pragma unroll
-      for (int i = 0; i < kScanChunk; ++i) slots[i * kThreads + threadIdx.x] = r[i];
+      for (int i = 0; i < kScanChunk; ++i) pairs[i * 32 + lane] = r[i];
     }
   }
-  // (a token or channel that does not exist reads what the slot held: its result is not used)
-  __device__ __forceinline__ float2 get(int i) const { return slots[i * kThreads + threadIdx.x].get(); }
+  __device__ __forceinline__ float2 get(int i) const { return pairs[i * 32 + (threadIdx.x & 31)].get(); }
 };
 template <typename T>
-constexpr size_t tile_bytes() { return sizeof(Raw2<T>) * kScanChunk * kThreads; }
+constexpr size_t tile_bytes() { return sizeof(Raw2<T>) * 32 * kScanChunk; }  // of one warp
 
-template <bool VEC, typename T>
+template <int ACC, typename T>
 __device__ __forceinline__ void store_pair(T* row, const Lane& l, float2 v) {
-  if (VEC) {
+  if (ACC != kSingle) {
     if (l.p0) store2(row + l.c0, v);
   } else {
     if (l.p0) store_f(row + l.c0, v.x);
@@ -196,11 +195,50 @@ __device__ __forceinline__ void store_state(float* base, long long row, int D, c
   if (l.p1) base[l.c1] = v.y;
 }
 
-__device__ __forceinline__ float2 decay2(float2 f, int mode) { return make_float2(decay_of(f.x, mode), decay_of(f.y, mode)); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+// Two fp32 operations in one instruction (PTX f32x2).
+__device__ __forceinline__ uint64_t bits2(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+__device__ __forceinline__ float2 floats2(uint64_t b) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(b));
+  return v;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return floats2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return floats2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return floats2(r);
+}
+
+// The decays of a tile; the mode is looked at once.
+template <typename T, int ACC>
+__device__ __forceinline__ void decays(float2 (&a)[kScanChunk], const Tile<T, ACC>& gate, int mode) {
+  if (mode == KDA_SCAN_LOG_DECAY) {
+#pragma unroll
+    for (int i = 0; i < kScanChunk; ++i) {
+      const float2 g = gate.get(i);
+      a[i] = make_float2(decay_of<KDA_SCAN_LOG_DECAY>(g.x), decay_of<KDA_SCAN_LOG_DECAY>(g.y));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kScanChunk; ++i) {
+      const float2 f = gate.get(i);
+      a[i] = make_float2(decay_of<KDA_SCAN_LOGITS>(f.x), decay_of<KDA_SCAN_LOGITS>(f.y));
+    }
+  }
+}
 
 // The map h -> A h + B of some consecutive tokens, for a lane's two channels.
 struct Map {
@@ -209,116 +247,162 @@ struct Map {
 __device__ __forceinline__ Map then(const Map& first, const Map& second) {
   return Map{mul2(first.A, second.A), fma2(second.A, first.B, second.B)};
 }
+__device__ __forceinline__ Map identity_map() { return Map{make_float2(1.f, 1.f), make_float2(0.f, 0.f)}; }
 
 struct ScanSmem {
-  Map warp[kWarps][32];                  // this advance's maps, by warp
-  Map cta[2][kMaxCluster][32];           // the CTAs' maps, by parity of the advance
+  Map warp[2][kWarps][32];      // the warps' maps of an advance, by parity of the advance
+  Map cta[2][kMaxCluster][32];  // the CTAs' maps
+  uint64_t bar[2];              // all CTAs' maps of the advance have arrived
 };
 
-__device__ __forceinline__ void st_cluster_map(uint32_t addr, const Map& m) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(m.A.x), "f"(m.A.y), "f"(m.B.x),
-               "f"(m.B.y)
+// A lane's map into another CTA's shared memory, counted in bytes on its barrier.
+__device__ __forceinline__ void st_async_map(uint32_t addr, const Map& m, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+               "r"(__float_as_uint(m.A.x)), "r"(__float_as_uint(m.A.y)), "r"(__float_as_uint(m.B.x)),
+               "r"(__float_as_uint(m.B.y)), "r"(bar)
                : "memory");
 }
 
-// From this warp's map of the advance and the state `carry` that enters the
+// From this warp's map of advance number `it` and the state `carry` that enters the
 // advance (the same in every warp of the cluster): the state that enters this
 // warp's chunk; carry becomes the state after the advance. All threads of the
-// cluster call it.
-__device__ __forceinline__ float2 enter_state(ScanSmem& sm, const Map& mine, float2& carry, int parity, int S, int rank) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  sm.warp[warp][lane] = mine;
+// cluster call it. The buffers alternate: a CTA sends its map of advance it + 2 only
+// after every CTA's map of it + 1, which each sent after all its warps had read
+// those of it. A wait for the other CTAs that runs out clears `ok`; the thread then
+// goes on through the same barriers without waiting for them again, so that all
+// threads still reach the end (with results that the error word disowns).
+__device__ __forceinline__ float2 enter_state(ScanSmem& sm, const Map& mine, float2& carry, bool& ok, int it, int S, int rank) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, parity = it & 1;
+  sm.warp[parity][warp][lane] = mine;
   __syncthreads();
-  Map before{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
-  for (int w = 0; w < warp; ++w) before = then(before, sm.warp[w][lane]);
+  Map before = identity_map();
+  for (int w = 0; w < warp; ++w) before = then(before, sm.warp[parity][w][lane]);
+  if (S == 1) {
+    Map total = then(before, mine);
+    for (int w = warp + 1; w < kWarps; ++w) total = then(total, sm.warp[parity][w][lane]);
+    const float2 in = fma2(before.A, carry, before.B);
+    carry = fma2(total.A, carry, total.B);
+    return in;
+  }
+  const uint32_t bar = smem_u32(&sm.bar[parity]);
   if (warp == kWarps - 1) {
     const Map total = then(before, mine);
+    if (lane == 0) mbar_arrive_expect_tx_local(&sm.bar[parity], S * 32 * sizeof(Map));
     const uint32_t at = smem_u32(&sm.cta[parity][rank][lane]);
-    for (int r = 0; r < S; ++r) st_cluster_map(mapa_shared(at, r), total);
+    for (int r = 0; r < S; ++r) st_async_map(mapa_shared(at, r), total, mapa_shared(bar, r));
   }
-  if (S > 1) cluster_sync_all();
-  else __syncthreads();
-  float2 h = carry, in = carry;
+  if (ok) ok = mbar_wait_bounded(bar, (it >> 1) & 1, kWaitNs);
+  float2 h = carry, start = carry;
   for (int r = 0; r < S; ++r) {
-    if (r == rank) in = h;
+    if (r == rank) start = h;
     const Map& m = sm.cta[parity][r][lane];
     h = fma2(m.A, h, m.B);
   }
   carry = h;
-  return fma2(before.A, in, before.B);
+  return fma2(before.A, start, before.B);
 }
 
 // Stages of the ring of tiles: what leaves two CTAs on an SM (about 100 KB each),
 // at least two.
-constexpr int stages_for(size_t stage) { return 100 * 1024 / stage >= 3 ? 3 : 2; }
+constexpr int stages_for(size_t stage) { return 100 * 1024 / (kWarps * stage) >= 3 ? 3 : 2; }
+
+__device__ __forceinline__ void scan_prologue(ScanSmem& sm, int S) {
+  if (S == 1) return;
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.bar[0], 1);
+    mbar_init(&sm.bar[1], 1);
+    fence_mbarrier_init_cluster();
+  }
+  cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written
+}
 
 // Forward. Grid (S * channel blocks, sequences), cluster (S, 1, 1).
-template <typename X, typename G, bool VEC>
+template <typename X, typename G, int ACC>
 __global__ void __launch_bounds__(kThreads, 2) kda_scan_fwd_kernel(const kda_scan_args p, int S) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ ScanSmem sm;
-  constexpr size_t kStage = tile_bytes<X>() + tile_bytes<G>();
+  constexpr size_t kStage = tile_bytes<X>() + tile_bytes<G>();  // of one warp
   constexpr int kStages = stages_for(kStage);
   const int warp = threadIdx.x >> 5, rank = blockIdx.x % S, advance = S * kWarps * kScanChunk;
-  const Lane l = lane_channels<VEC>(blockIdx.x / S * kBlockCh, p.D);
+  const Lane l = lane_channels<ACC>(blockIdx.x / S * kBlockCh, p.D);
   const bool comp = p.flags & KDA_SCAN_FLAG_COMPLEMENT;
-  if (S > 1) cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written
-  int parity = 0;
+  unsigned char* mine_ring = ring + warp * kStages * kStage;
+  scan_prologue(sm, S);
+  int it = 0;
+  bool ok = true;
   for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
     SeqPos pos;
-    if (!find_sequence(p, n, pos)) return;  // (the same answer in every CTA)
+    if (!find_sequence(p, n, pos)) break;  // (the same answer in every CTA)
     const int len = pos.end - pos.start;
-    // the tiles of advance j, whose first token for this warp is i0
-    auto tile_x = [&](int j) { return Tile<X, VEC>{reinterpret_cast<Raw2<X>*>(ring + (j % kStages) * kStage)}; };
-    auto tile_g = [&](int j) { return Tile<G, VEC>{reinterpret_cast<Raw2<G>*>(ring + (j % kStages) * kStage + tile_bytes<X>())}; };
+    // the tiles of advance j, whose first token for this warp is first(j)
+    auto tile_x = [&](int j) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + (j % kStages) * kStage)}; };
+    auto tile_g = [&](int j) { return Tile<G, ACC>{reinterpret_cast<Raw2<G>*>(mine_ring + (j % kStages) * kStage + tile_bytes<X>())}; };
     auto first = [&](int j) { return j * advance + (rank * kWarps + warp) * kScanChunk; };
     auto fetch = [&](int j) {
       const int i0 = first(j);
       if (i0 < len) {
         const long long t0 = pos.start + static_cast<long long>(i0);
-        tile_x(j).fetch(static_cast<const X*>(p.x) + t0 * p.x_stride, p.x_stride, len - i0, l);
-        tile_g(j).fetch(static_cast<const G*>(p.gate) + t0 * p.gate_stride, p.gate_stride, len - i0, l);
+        tile_x(j).fetch(static_cast<const X*>(p.x) + t0 * p.x_stride, p.x_stride, len - i0, l, p.D);
+        tile_g(j).fetch(static_cast<const G*>(p.gate) + t0 * p.gate_stride, p.gate_stride, len - i0, l, p.D);
       }
       cp_async_commit();
     };
     float2 carry = load_state(p.h0, n, p.D, l);
     for (int j = 0; j < kStages - 1; ++j) fetch(j);
-    for (int j = 0; j * static_cast<long long>(advance) < len; ++j, parity ^= 1) {
+    for (int j = 0; j * static_cast<long long>(advance) < len; ++j, ++it) {
       fetch(j + kStages - 1);
       cp_async_wait<kStages - 1>();
-      const int i0 = first(j), m = min(kScanChunk, len - i0);
-      const Tile<X, VEC> tx = tile_x(j);
-      const Tile<G, VEC> tg = tile_g(j);
+      __syncwarp();
+      const int i0 = first(j), m = len - i0;
       float2 a[kScanChunk], u[kScanChunk];
-      Map mine{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
+      decays(a, tile_g(j), p.gate_mode);
+      const Tile<X, ACC> tx = tile_x(j);
 #pragma unroll
       for (int i = 0; i < kScanChunk; ++i) {
-        a[i] = decay2(tg.get(i), p.gate_mode);
         u[i] = tx.get(i);
-        if (comp) u[i] = make_float2((1.f - a[i].x) * u[i].x, (1.f - a[i].y) * u[i].y);
-        if (i < m) mine = then(mine, Map{a[i], u[i]});
+        if (comp) u[i] = make_float2(fmaf(-a[i].x, u[i].x, u[i].x), fmaf(-a[i].y, u[i].y, u[i].y));
       }
-      float2 h = enter_state(sm, mine, carry, parity, S, rank);
-      if (m > 0) {
-        if (p.h_chunks) store_state(p.h_chunks, pos.chunk_base + i0 / kScanChunk, p.D, l, h);
-        X* y = static_cast<X*>(p.y) + (pos.start + static_cast<long long>(i0)) * p.y_stride;
+      __syncwarp();  // the slots are free for the fetch of the next iteration
+      Map mine = identity_map();
+      if (m >= kScanChunk) {
 #pragma unroll
-        for (int i = 0; i < kScanChunk; ++i) {
+        for (int i = 0; i < kScanChunk; ++i) mine = then(mine, Map{a[i], u[i]});
+      } else {
+#pragma unroll
+        for (int i = 0; i < kScanChunk; ++i)
+          if (i < m) mine = then(mine, Map{a[i], u[i]});
+      }
+      float2 h = enter_state(sm, mine, carry, ok, it, S, rank);
+      if (m > 0 && p.h_chunks) store_state(p.h_chunks, pos.chunk_base + i0 / kScanChunk, p.D, l, h);
+      X* y = static_cast<X*>(p.y) + (pos.start + static_cast<long long>(i0)) * p.y_stride;
+      if (m >= kScanChunk) {
+#pragma unroll
+        for (int i = 0; i < kScanChunk; ++i, y += p.y_stride) {
+          h = fma2(a[i], h, u[i]);
+          store_pair<ACC>(y, l, h);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kScanChunk; ++i, y += p.y_stride) {
           if (i < m) {
             h = fma2(a[i], h, u[i]);
-            store_pair<VEC>(y + i * p.y_stride, l, h);
+            store_pair<ACC>(y, l, h);
           }
         }
       }
     }
     if (p.hT && rank == 0 && warp == 0) store_state(p.hT, n, p.D, l, carry);
   }
+  cp_async_wait<0>();
+  if (!ok) set_err(p.err, KDA_ERR_TIMEOUT);
+  __syncwarp();
+  if (S > 1) cluster_sync_all();  // no CTA ends while another may still write to it
 }
 
 // Backward: the same over the chunks from the last to the first, with the map of
 // d (the gradient of a state) over a chunk; the states within a chunk come from
 // h_chunks, so the forward direction needs no exchange.
-template <typename X, typename G, bool VEC>
+template <typename X, typename G, int ACC>
 __global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_scan_bwd_args q, int S) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ ScanSmem sm;
@@ -326,17 +410,19 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_sca
   constexpr int kStages = stages_for(kStage);
   const kda_scan_args& p = q.fwd;
   const int warp = threadIdx.x >> 5, rank = blockIdx.x % S;
-  const Lane l = lane_channels<VEC>(blockIdx.x / S * kBlockCh, p.D);
+  const Lane l = lane_channels<ACC>(blockIdx.x / S * kBlockCh, p.D);
   const bool comp = p.flags & KDA_SCAN_FLAG_COMPLEMENT, logits = p.gate_mode == KDA_SCAN_LOGITS;
-  if (S > 1) cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written
-  int parity = 0;
+  unsigned char* mine_ring = ring + warp * kStages * kStage;
+  scan_prologue(sm, S);
+  int it = 0;
+  bool ok = true;
   for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
     SeqPos pos;
-    if (!find_sequence(p, n, pos)) return;
+    if (!find_sequence(p, n, pos)) break;
     const int len = pos.end - pos.start, chunks = (len + kScanChunk - 1) / kScanChunk;
-    auto tile_x = [&](int j) { return Tile<X, VEC>{reinterpret_cast<Raw2<X>*>(ring + (j % kStages) * kStage)}; };
-    auto tile_d = [&](int j) { return Tile<X, VEC>{reinterpret_cast<Raw2<X>*>(ring + (j % kStages) * kStage + tile_bytes<X>())}; };
-    auto tile_g = [&](int j) { return Tile<G, VEC>{reinterpret_cast<Raw2<G>*>(ring + (j % kStages) * kStage + 2 * tile_bytes<X>())}; };
+    auto tile_x = [&](int j) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + (j % kStages) * kStage)}; };
+    auto tile_d = [&](int j) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + (j % kStages) * kStage + tile_bytes<X>())}; };
+    auto tile_g = [&](int j) { return Tile<G, ACC>{reinterpret_cast<Raw2<G>*>(mine_ring + (j % kStages) * kStage + 2 * tile_bytes<X>())}; };
     // this warp's chunk of advance j (negative: none left)
     auto chunk_of = [&](int j) { return chunks - 1 - ((j * S + rank) * kWarps + warp); };
     auto fetch = [&](int j) {
@@ -344,52 +430,79 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_sca
       if (k >= 0) {
         const int m = len - k * kScanChunk;
         const long long t0 = pos.start + static_cast<long long>(k) * kScanChunk;
-        tile_x(j).fetch(static_cast<const X*>(p.x) + t0 * p.x_stride, p.x_stride, m, l);
-        tile_g(j).fetch(static_cast<const G*>(p.gate) + t0 * p.gate_stride, p.gate_stride, m, l);
-        tile_d(j).fetch(static_cast<const X*>(q.dy) + t0 * q.dy_stride, q.dy_stride, m, l);
+        tile_x(j).fetch(static_cast<const X*>(p.x) + t0 * p.x_stride, p.x_stride, m, l, p.D);
+        tile_g(j).fetch(static_cast<const G*>(p.gate) + t0 * p.gate_stride, p.gate_stride, m, l, p.D);
+        tile_d(j).fetch(static_cast<const X*>(q.dy) + t0 * q.dy_stride, q.dy_stride, m, l, p.D);
       }
       cp_async_commit();
     };
-    float2 carry = load_state(q.dhT, n, p.D, l);
+    auto chunk_state = [&](int j) {
+      const int k = chunk_of(j);
+      return k >= 0 ? load_state(p.h_chunks, pos.chunk_base + k, p.D, l) : make_float2(0.f, 0.f);
+    };
+    float2 carry = load_state(q.dhT, n, p.D, l), next_h = chunk_state(0);
     for (int j = 0; j < kStages - 1; ++j) fetch(j);
-    for (int j = 0; j * S * kWarps < chunks; ++j, parity ^= 1) {
-      const int k = chunk_of(j), m = k < 0 ? 0 : min(kScanChunk, len - k * kScanChunk);
-      const long long t0 = pos.start + static_cast<long long>(k) * kScanChunk;
-      float2 h = m > 0 ? load_state(p.h_chunks, pos.chunk_base + k, p.D, l) : make_float2(0.f, 0.f);
+    for (int j = 0; j * S * kWarps < chunks; ++j, ++it) {
+      const int k = chunk_of(j), m = k < 0 ? 0 : len - k * kScanChunk;
+      float2 h = next_h;
+      next_h = chunk_state(j + 1);
       fetch(j + kStages - 1);
       cp_async_wait<kStages - 1>();
-      const Tile<X, VEC> tx = tile_x(j), td = tile_d(j);
-      const Tile<G, VEC> tg = tile_g(j);
+      __syncwarp();
+      const Tile<X, ACC> tx = tile_x(j), td = tile_d(j);
       float2 a[kScanChunk], w[kScanChunk];  // decay; what d multiplies in the decay's gradient
+      decays(a, tile_g(j), p.gate_mode);
+      if (comp) {
 #pragma unroll
-      for (int i = 0; i < kScanChunk; ++i) {
-        a[i] = decay2(tg.get(i), p.gate_mode);
-        const float2 xv = tx.get(i);
-        w[i] = comp ? make_float2(h.x - xv.x, h.y - xv.y) : h;
-        h = comp ? fma2(a[i], w[i], xv) : fma2(a[i], h, xv);  // a h + (1 - a) x = x + a (h - x)
-      }
-      Map mine{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};  // d -> a (d + dy), last token first
+        for (int i = 0; i < kScanChunk; ++i) {  // a h + (1 - a) x = x + a (h - x)
+          const float2 xv = tx.get(i);
+          w[i] = make_float2(h.x - xv.x, h.y - xv.y);
+          h = fma2(a[i], w[i], xv);
+        }
+      } else {
 #pragma unroll
-      for (int i = kScanChunk - 1; i >= 0; --i)
-        if (i < m) mine = then(mine, Map{a[i], mul2(a[i], td.get(i))});
-      float2 d = enter_state(sm, mine, carry, parity, S, rank);
-      X* dx = static_cast<X*>(q.dx) + t0 * q.dx_stride;
-      G* dg = static_cast<G*>(q.dgate) + t0 * q.dgate_stride;
-#pragma unroll
-      for (int i = kScanChunk - 1; i >= 0; --i) {
-        if (i < m) {
-          const float2 dyv = td.get(i), b = make_float2(1.f - a[i].x, 1.f - a[i].y);
-          d = make_float2(d.x + dyv.x, d.y + dyv.y);
-          store_pair<VEC>(dx + i * q.dx_stride, l, comp ? mul2(b, d) : d);
-          d = mul2(a[i], d);
-          float2 g = mul2(d, w[i]);
-          if (logits) g = mul2(b, g);
-          store_pair<VEC>(dg + i * q.dgate_stride, l, g);
+        for (int i = 0; i < kScanChunk; ++i) {
+          w[i] = h;
+          h = fma2(a[i], h, tx.get(i));
         }
       }
+      Map mine = identity_map();  // d -> a (d + dy), last token first
+      if (m >= kScanChunk) {
+#pragma unroll
+        for (int i = kScanChunk - 1; i >= 0; --i) mine = then(mine, Map{a[i], mul2(a[i], td.get(i))});
+      } else {
+#pragma unroll
+        for (int i = kScanChunk - 1; i >= 0; --i)
+          if (i < m) mine = then(mine, Map{a[i], mul2(a[i], td.get(i))});
+      }
+      float2 d = enter_state(sm, mine, carry, ok, it, S, rank);
+      const long long last = pos.start + static_cast<long long>(k) * kScanChunk + kScanChunk - 1;
+      X* dx = static_cast<X*>(q.dx) + last * q.dx_stride;
+      G* dg = static_cast<G*>(q.dgate) + last * q.dgate_stride;
+      auto token = [&](int i) {
+        const float2 b = make_float2(1.f - a[i].x, 1.f - a[i].y);
+        d = add2(d, td.get(i));
+        store_pair<ACC>(dx, l, comp ? mul2(b, d) : d);
+        d = mul2(a[i], d);
+        const float2 g = mul2(d, w[i]);
+        store_pair<ACC>(dg, l, logits ? mul2(b, g) : g);
+      };
+      if (m >= kScanChunk) {
+#pragma unroll
+        for (int i = kScanChunk - 1; i >= 0; --i, dx -= q.dx_stride, dg -= q.dgate_stride) token(i);
+      } else {
+#pragma unroll
+        for (int i = kScanChunk - 1; i >= 0; --i, dx -= q.dx_stride, dg -= q.dgate_stride)
+          if (i < m) token(i);
+      }
+      __syncwarp();  // the slots are free for the fetch of the next iteration
     }
     if (q.dh0 && rank == 0 && warp == 0) store_state(q.dh0, n, p.D, l, carry);
   }
+  cp_async_wait<0>();
+  if (!ok) set_err(p.err, KDA_ERR_TIMEOUT);
+  __syncwarp();
+  if (S > 1) cluster_sync_all();  // no CTA ends while another may still write to it
 }
 
 template <typename X, typename G>
@@ -404,7 +517,8 @@ __global__ void __launch_bounds__(kStepThreads) kda_scan_step_kernel(const kda_s
     store_f(y, 0.f);
     return;
   }
-  const float a = decay_of(load_f(static_cast<const G*>(p.gate) + b * p.gate_stride + c), p.gate_mode);
+  const float f = load_f(static_cast<const G*>(p.gate) + b * p.gate_stride + c);
+  const float a = p.gate_mode == KDA_SCAN_LOG_DECAY ? decay_of<KDA_SCAN_LOG_DECAY>(f) : decay_of<KDA_SCAN_LOGITS>(f);
   const float x = load_f(static_cast<const X*>(p.x) + b * p.x_stride + c);
   const long long at = static_cast<long long>(slot) * p.D + c;
   const float h = a * p.state_in[at] + (p.flags & KDA_SCAN_FLAG_COMPLEMENT ? (1.f - a) * x : x);
@@ -420,16 +534,21 @@ int cluster_size(const kda_scan_args& a) {
   const long long blocks = (a.D + kBlockCh - 1) / kBlockCh * static_cast<long long>(a.N);
   const long long mean = a.cu_seqlens ? (a.T + a.N - 1) / a.N : a.T;
   const long long room = 2 * 152 * (a.cu_seqlens && a.N > 1 ? 4 : 1);
-  int S = 1;
-  while (S < kMaxCluster && blocks * S * 2 <= room && mean > S * kWarps * kScanChunk) S *= 2;
-  return S;
+  const long long fit = room / blocks, advances = (mean + kWarps * kScanChunk - 1) / (kWarps * kScanChunk);
+  const long long S = fit < advances ? fit : advances;
+  return static_cast<int>(S < 1 ? 1 : S > kMaxCluster ? kMaxCluster : S);
 }
 
-// Whether pairs of channels can be read as one access of 2 * elem bytes.
-bool pairs_ok(const void* p, int64_t stride, size_t elem) {
-  return reinterpret_cast<uintptr_t>(p) % (2 * elem) == 0 && stride % 2 == 0;
-}
 size_t elem_bytes(int32_t dt) { return dt == KDA_DTYPE_FP32 ? 4 : 2; }
+
+// How rows of D channels at p can be accessed: the widest of 16 bytes, a pair, one
+// channel that D, the stride and the address are all multiples of.
+int access_of(const void* p, int64_t stride, int D, int32_t dt) {
+  const int64_t e = static_cast<int64_t>(elem_bytes(dt));
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  if (D * e % 16 == 0 && stride * e % 16 == 0 && at % 16 == 0) return kWide;
+  return D % 2 == 0 && stride % 2 == 0 && at % (2 * e) == 0 ? kPair : kSingle;
+}
 
 // One instance's launch. `done` is the instance's record of devices whose
 // shared-memory limit has been raised.
@@ -453,44 +572,55 @@ cudaError_t launch_clusters(void (*kernel)(Args, int), std::atomic<uint64_t>& do
   return cudaLaunchKernelEx(&cfg, kernel, a, S);
 }
 
-template <typename X, typename G, bool VEC>
+template <typename X, typename G, int ACC>
 cudaError_t launch_fwd(const kda_scan_args& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   constexpr size_t stage = tile_bytes<X>() + tile_bytes<G>();
-  return launch_clusters(kda_scan_fwd_kernel<X, G, VEC>, done, stages_for(stage) * stage, a, a, s);
+  return launch_clusters(kda_scan_fwd_kernel<X, G, ACC>, done, stages_for(stage) * kWarps * stage, a, a, s);
 }
 
-template <typename X, typename G, bool VEC>
+template <typename X, typename G, int ACC>
 cudaError_t launch_bwd(const kda_scan_bwd_args& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   constexpr size_t stage = 2 * tile_bytes<X>() + tile_bytes<G>();
-  return launch_clusters(kda_scan_bwd_kernel<X, G, VEC>, done, stages_for(stage) * stage, a, a.fwd, s);
+  return launch_clusters(kda_scan_bwd_kernel<X, G, ACC>, done, stages_for(stage) * kWarps * stage, a, a.fwd, s);
+}
+
+template <typename X, typename G>
+cudaError_t launch_any(const kda_scan_args& a, int acc, cudaStream_t s) {
+  return acc == kWide ? launch_fwd<X, G, kWide>(a, s) : acc == kPair ? launch_fwd<X, G, kPair>(a, s) : launch_fwd<X, G, kSingle>(a, s);
+}
+template <typename X, typename G>
+cudaError_t launch_any(const kda_scan_bwd_args& a, int acc, cudaStream_t s) {
+  return acc == kWide ? launch_bwd<X, G, kWide>(a, s) : acc == kPair ? launch_bwd<X, G, kPair>(a, s) : launch_bwd<X, G, kSingle>(a, s);
+}
+
+// The instance for a call's types: x bf16 with a bf16 or fp32 gate, or both fp32.
+template <typename Args>
+cudaError_t launch_types(const Args& a, const kda_scan_args& f, int acc, cudaStream_t s) {
+  if (f.dtype == KDA_DTYPE_FP32) return launch_any<float, float>(a, acc, s);
+  if (f.gate_dtype == KDA_DTYPE_FP32) return launch_any<__nv_bfloat16, float>(a, acc, s);
+  return launch_any<__nv_bfloat16, __nv_bfloat16>(a, acc, s);
 }
 
 }  // namespace
 
-// The instances by tensor types: x bf16 with a bf16 or fp32 gate, or both fp32.
-#define KDA_SCAN_LAUNCH(launch, vec, xt, gt, ...)                                                        \
-  ((xt) == KDA_DTYPE_FP32   ? ((vec) ? launch<float, float, true>(__VA_ARGS__) : launch<float, float, false>(__VA_ARGS__)) \
-   : (gt) == KDA_DTYPE_FP32 ? ((vec) ? launch<__nv_bfloat16, float, true>(__VA_ARGS__)                   \
-                                     : launch<__nv_bfloat16, float, false>(__VA_ARGS__))                 \
-                            : ((vec) ? launch<__nv_bfloat16, __nv_bfloat16, true>(__VA_ARGS__)           \
-                                     : launch<__nv_bfloat16, __nv_bfloat16, false>(__VA_ARGS__)))
-
 cudaError_t launch_scan_fwd(const kda_scan_args& a, cudaStream_t s) {
-  const size_t xe = elem_bytes(a.dtype), ge = elem_bytes(a.gate_dtype);
-  const bool vec = a.D % 2 == 0 && pairs_ok(a.x, a.x_stride, xe) && pairs_ok(a.gate, a.gate_stride, ge) &&
-                   pairs_ok(a.y, a.y_stride, xe);
-  return KDA_SCAN_LAUNCH(launch_fwd, vec, a.dtype, a.gate_dtype, a, s);
+  int acc = kWide;
+  for (const int v : {access_of(a.x, a.x_stride, a.D, a.dtype), access_of(a.gate, a.gate_stride, a.D, a.gate_dtype),
+                      access_of(a.y, a.y_stride, a.D, a.dtype)})
+    acc = v < acc ? v : acc;
+  return launch_types(a, a, acc, s);
 }
 
 cudaError_t launch_scan_bwd(const kda_scan_bwd_args& a, cudaStream_t s) {
   const kda_scan_args& f = a.fwd;
-  const size_t xe = elem_bytes(f.dtype), ge = elem_bytes(f.gate_dtype);
-  const bool vec = f.D % 2 == 0 && pairs_ok(f.x, f.x_stride, xe) && pairs_ok(f.gate, f.gate_stride, ge) &&
-                   pairs_ok(a.dy, a.dy_stride, xe) && pairs_ok(a.dx, a.dx_stride, xe) &&
-                   pairs_ok(a.dgate, a.dgate_stride, ge);
-  return KDA_SCAN_LAUNCH(launch_bwd, vec, f.dtype, f.gate_dtype, a, s);
+  int acc = kWide;
+  for (const int v : {access_of(f.x, f.x_stride, f.D, f.dtype), access_of(f.gate, f.gate_stride, f.D, f.gate_dtype),
+                      access_of(a.dy, a.dy_stride, f.D, f.dtype), access_of(a.dx, a.dx_stride, f.D, f.dtype),
+                      access_of(a.dgate, a.dgate_stride, f.D, f.gate_dtype)})
+    acc = v < acc ? v : acc;
+  return launch_types(a, f, acc, s);
 }
 
 cudaError_t launch_scan_step(const kda_scan_step_args& a, cudaStream_t s) {
