@@ -526,19 +526,6 @@ __global__ void __launch_bounds__(kStepThreads) kda_scan_step_kernel(const kda_s
   store_f(y, h);
 }
 
-// CTAs of a cluster: as many as leave the whole grid resident at once (two CTAs on
-// each of 152 SMs), no more than the sequences (their mean length, where they are
-// packed) have advances for. Packed sequences differ in length, so they get up to
-// four times as many, whose order of execution evens the lengths out.
-int cluster_size(const kda_scan_args& a) {
-  const long long blocks = (a.D + kBlockCh - 1) / kBlockCh * static_cast<long long>(a.N);
-  const long long mean = a.cu_seqlens ? (a.T + a.N - 1) / a.N : a.T;
-  const long long room = 2 * 152 * (a.cu_seqlens && a.N > 1 ? 4 : 1);
-  const long long fit = room / blocks, advances = (mean + kWarps * kScanChunk - 1) / (kWarps * kScanChunk);
-  const long long S = fit < advances ? fit : advances;
-  return static_cast<int>(S < 1 ? 1 : S > kMaxCluster ? kMaxCluster : S);
-}
-
 size_t elem_bytes(int32_t dt) { return dt == KDA_DTYPE_FP32 ? 4 : 2; }
 
 // How rows of D channels at p can be accessed: the widest of 16 bytes, a pair, one
@@ -550,40 +537,66 @@ int access_of(const void* p, int64_t stride, int D, int32_t dt) {
   return D % 2 == 0 && stride % 2 == 0 && at % (2 * e) == 0 ? kPair : kSingle;
 }
 
-// One instance's launch. `done` is the instance's record of devices whose
-// shared-memory limit has been raised.
+// What one instance of a kernel remembers of the device: where its shared-memory
+// limit has been raised, and how many of its clusters of each size are resident at
+// once (0: not asked yet).
+struct Instance {
+  std::atomic<uint64_t> smem_set{0};
+  std::atomic<int> resident[kMaxCluster + 1] = {};
+};
+
 template <typename Args>
-cudaError_t launch_clusters(void (*kernel)(Args, int), std::atomic<uint64_t>& done, size_t smem, const Args& a,
-                            const kda_scan_args& f, cudaStream_t s) {
-  const cudaError_t e = set_smem_limit_once(kernel, smem, done);
+cudaError_t launch_clusters(void (*kernel)(Args, int), Instance& inst, size_t smem, const Args& a, const kda_scan_args& f,
+                            cudaStream_t s) {
+  cudaError_t e = set_smem_limit_once(kernel, smem, inst.smem_set);
   if (e != cudaSuccess) return e;
-  const int S = cluster_size(f);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((f.D + kBlockCh - 1) / kBlockCh * S), static_cast<unsigned>(f.N < 65535 ? f.N : 65535));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = S;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  // The most CTAs a cluster that leave the whole grid resident at once, no more than
+  // the sequences (their mean length, where they are packed) have chunks for: with
+  // clusters of 7, which the GPU's groups of SMs hold 38 of, 40 channel blocks of
+  // 8192 tokens take two rounds and 54 us, with clusters of 5 one. Packed sequences
+  // differ in length, so they get up to four rounds, which even the lengths out.
+  const long long blocks = (f.D + kBlockCh - 1) / kBlockCh, work = blocks * f.N;
+  const long long mean = f.cu_seqlens ? (f.T + f.N - 1) / f.N : f.T;
+  const int rounds = f.cu_seqlens && f.N > 1 ? 4 : 1;
+  int S = kMaxCluster;
+  for (; S > 1; --S) {
+    if (mean <= static_cast<long long>(S - 1) * kWarps * kScanChunk) continue;
+    int fit = inst.resident[S].load(std::memory_order_relaxed);
+    if (fit == 0) {
+      attr.val.clusterDim.x = S;
+      cfg.gridDim = dim3(S);
+      e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      inst.resident[S].store(fit > 0 ? fit : -1, std::memory_order_relaxed);
+    }
+    if (work <= static_cast<long long>(fit) * rounds) break;
+  }
+  attr.val.clusterDim.x = S;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * S), static_cast<unsigned>(f.N < 65535 ? f.N : 65535));
   return cudaLaunchKernelEx(&cfg, kernel, a, S);
 }
 
 template <typename X, typename G, int ACC>
 cudaError_t launch_fwd(const kda_scan_args& a, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
+  static Instance inst;
   constexpr size_t stage = tile_bytes<X>() + tile_bytes<G>();
-  return launch_clusters(kda_scan_fwd_kernel<X, G, ACC>, done, stages_for(stage) * kWarps * stage, a, a, s);
+  return launch_clusters(kda_scan_fwd_kernel<X, G, ACC>, inst, stages_for(stage) * kWarps * stage, a, a, s);
 }
 
 template <typename X, typename G, int ACC>
 cudaError_t launch_bwd(const kda_scan_bwd_args& a, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
+  static Instance inst;
   constexpr size_t stage = 2 * tile_bytes<X>() + tile_bytes<G>();
-  return launch_clusters(kda_scan_bwd_kernel<X, G, ACC>, done, stages_for(stage) * kWarps * stage, a, a.fwd, s);
+  return launch_clusters(kda_scan_bwd_kernel<X, G, ACC>, inst, stages_for(stage) * kWarps * stage, a, a.fwd, s);
 }
 
 template <typename X, typename G>
