@@ -105,7 +105,7 @@ struct RmsNormCall {
 // (kda_layer_api.cpp).
 cudaError_t launch_add_rmsnorm(const kda_add_rmsnorm_args& a, cudaStream_t s);
 cudaError_t launch_linear(const kda_linear_args& a, cudaStream_t s);
-cudaError_t launch_linear_pair(const kda_linear_args& a, cudaStream_t s);  // more than 128 tokens, rows that TMA describes
+cudaError_t launch_linear_wide(const kda_linear_args& a, cudaStream_t s);  // many tokens, rows that TMA describes
 cudaError_t launch_scan_fwd(const kda_scan_args& a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const kda_scan_bwd_args& a, cudaStream_t s);
 cudaError_t launch_scan_step(const kda_scan_step_args& a, cudaStream_t s);

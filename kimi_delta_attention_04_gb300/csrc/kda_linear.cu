@@ -9,8 +9,8 @@
 //
 // Roles: warps 0-3 the epilogue, warp 4 issues the MMAs, warp 5 the TMA loads
 // through a ring of stages. Rows that TMA cannot describe (an address or a row
-// pitch that is no multiple of 16 bytes) are copied by eight loader warps
-// instead, two groups of four taking alternate blocks.
+// pitch that is no multiple of 16 bytes) are copied by sixteen loader warps
+// instead.
 //
 // Few tiles (small M) leave most SMs without work, so a cluster of S CTAs splits
 // K of one tile: each sums its share, puts it into its own shared memory, and
@@ -27,7 +27,9 @@ constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;
 constexpr int kEpiThreads = 128;
 constexpr int kTmaThreads = kEpiThreads + 64;       // + MMA warp, TMA warp
-constexpr int kCopyThreads = kEpiThreads + 32 + 256;  // + MMA warp, two groups of loaders
+constexpr int kLoaders = 16;
+constexpr int kRawStages = 4;
+constexpr int kCopyThreads = kEpiThreads + 32 + 32 * kLoaders;  // + MMA warp, loader warps
 
 struct LinearHead {
   uint64_t full[kMaxStages], empty[kMaxStages], acc;
@@ -35,75 +37,107 @@ struct LinearHead {
   int failed;
 };
 
-// 16 bytes of a row at byte offset `off` of [0, row_bytes): bytes past the row are
-// zero. `lo` and `hi` bound the matrix's memory: where the two aligned 16-byte
-// words that hold the bytes lie inside, they are read and shifted; at the
-// matrix's very ends the bytes are read one element at a time.
-template <typename E>
-__device__ __forceinline__ uint4 load_unaligned16(const unsigned char* row, long long off, long long row_bytes,
-                                                  const unsigned char* lo, const unsigned char* hi) {
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-  const long long left = row_bytes - off;
-  if (left <= 0) return make_uint4(0u, 0u, 0u, 0u);
-  const unsigned char* p = row + off;
-  const unsigned char* base = reinterpret_cast<const unsigned char*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t{15});
-  if (base >= lo && base + 32 <= hi) {
-    const uint4 a = *reinterpret_cast<const uint4*>(base), b = *reinterpret_cast<const uint4*>(base + 16);
-    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const int sh = static_cast<int>(p - base), words = sh >> 2;
-    const uint32_t bits = (sh & 3) * 8;
-    // word i + words of v for a run-time `words`: selects, no local memory
-    uint32_t u[5];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) {
-      const uint32_t a0 = v[i], a1 = v[i + 1 < 8 ? i + 1 : 7], a2 = v[i + 2 < 8 ? i + 2 : 7], a3 = v[i + 3 < 8 ? i + 3 : 7];
-      u[i] = words == 0 ? a0 : words == 1 ? a1 : words == 2 ? a2 : a3;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(u[i], u[i + 1], bits);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // zero what lies past the row
-      const long long keep = left - 4 * i;
-      if (keep < 4) w[i] = keep <= 0 ? 0u : w[i] & (0xffffffffu >> (8 * (4 - keep)));
-    }
-  } else {
-    constexpr int PER = 4 / sizeof(E);
-#pragma unroll
-    for (int i = 0; i < 16 / static_cast<int>(sizeof(E)); ++i)
-      if (i * static_cast<int>(sizeof(E)) < left)
-        w[i / PER] |= static_cast<uint32_t>(reinterpret_cast<const E*>(p)[i]) << (8 * sizeof(E) * (i % PER));
+// The operand rows of a tile for rows that start at any byte: warp `warp` of the 16
+// loaders brings rows warp, warp + 16, .. of the 128 + TOK (first w's, then x's).
+// fetch() starts copies of the aligned 4-byte words that hold a row's 128 bytes (33
+// of them; bytes past the row and rows past the end are zero-filled) into raw
+// shared memory that only this warp uses; place() shifts them into the swizzled
+// tile (16-byte chunk c of row r at chunk c ^ (r % 8)). What bounds it is the
+// instructions per row and block: 12 here, 96 in a first form that formed every
+// word's address and length anew (777 x 1001 -> 1111: 55 us, now 26).
+template <typename E, int TOK>
+struct RowLoader {
+  static constexpr int kPer = (kOut + TOK) / kLoaders;   // rows of a warp
+  static constexpr int kPitch = 33;                      // words of a raw row
+  static constexpr uint32_t kRawWords = kLoaders * kPer * kPitch;
+  const unsigned char* w;
+  const unsigned char* x;
+  long long w_pitch, x_pitch, row_bytes;
+  int n, m, n_end, m_end, warp;  // this warp's first rows
+  __device__ __forceinline__ RowLoader(const kda_linear_args& p, int n0, int m0, int loader)
+      : w_pitch(p.ldw * static_cast<long long>(sizeof(E))), x_pitch(p.ldx * static_cast<long long>(sizeof(E))),
+        row_bytes(p.K * static_cast<long long>(sizeof(E))), n(n0 + loader), m(m0 + loader), n_end(p.N), m_end(p.M), warp(loader) {
+    w = static_cast<const unsigned char*>(p.w) + n * w_pitch;
+    x = static_cast<const unsigned char*>(p.x) + m * x_pitch;
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Copies rows row0 .. row0 + ROWS - 1 of one K block into a swizzled tile (16-byte
-// chunk c of row r at chunk c ^ (r % 8)) with 128 threads; rows past row_end are zero.
-template <typename E, int ROWS>
-__device__ __forceinline__ void copy_tile(unsigned char* tile, const void* src, long long ld, int row0, int row_end,
-                                          int block, int K, int tid) {
-  const unsigned char* lo = static_cast<const unsigned char*>(src);
-  const long long pitch = ld * static_cast<long long>(sizeof(E)), bytes = static_cast<long long>(K) * sizeof(E);
-  const unsigned char* hi = lo + (row_end - 1) * pitch + bytes;
-  constexpr int STEP = 4;  // chunks in flight per thread
-  constexpr int CHUNKS = ROWS * 8;
-  static_assert(CHUNKS % 128 == 0, "");
+  // Row j of the warp: where it starts, and whether it exists. Rows that do not are
+  // left alone: what they put into the tile reaches outputs that are not stored.
+  __device__ __forceinline__ const unsigned char* row(int j) const {
+    return j < kOut / kLoaders ? w + j * kLoaders * w_pitch : x + (j - kOut / kLoaders) * kLoaders * x_pitch;
+  }
+  __device__ __forceinline__ bool live(int j) const {
+    return j < kOut / kLoaders ? n + j * kLoaders < n_end : m + (j - kOut / kLoaders) * kLoaders < m_end;
+  }
+  __device__ __forceinline__ bool first_of_matrix(int j) const {
+    return j < kOut / kLoaders ? n + j * kLoaders == 0 : m + (j - kOut / kLoaders) * kLoaders == 0;
+  }
+  __device__ __forceinline__ static uint32_t shift_of(const unsigned char* p) { return reinterpret_cast<uintptr_t>(p) & 3; }
+  // Word `word` of row j at byte `at`, where the row may end inside it or start
+  // after it. (The word that the first row of a matrix starts inside of would begin
+  // before the matrix; place() reads the row's first bytes by themselves.)
+  __device__ __forceinline__ void copy_edge_word(uint32_t* dst, int j, long long at, int word) const {
+    const unsigned char* p = row(j);
+    const long long off = at + 4 * word - shift_of(p), left = row_bytes - off;
+    if (!live(j) || (off < 0 && first_of_matrix(j))) return;
+    if (left <= 0) {
+      *dst = 0u;
+      return;
+    }
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(p + off),
+                 "r"(left < 4 ? static_cast<uint32_t>(left) : 4u)
+                 : "memory");
+  }
+  __device__ __forceinline__ static void copy_word(uint32_t* dst, const unsigned char* p) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uintptr_t>(p) & ~uintptr_t{3})
+                 : "memory");
+  }
+  __device__ __forceinline__ void fetch(uint32_t* raw, int block) const {
+    const int lane = threadIdx.x & 31;
+    const long long at = static_cast<long long>(block) * kKBytes;
+    raw += warp * kPer * kPitch;
+    if (block > 0 && at + 4 * kPitch <= row_bytes) {  // every word of the block lies inside its row
+      const unsigned char* p = w + at + 4 * lane;
+#pragma unroll
+      for (int j = 0; j < kOut / kLoaders; ++j, p += kLoaders * w_pitch)
+        if (live(j)) copy_word(raw + j * kPitch + lane, p);
+      p = x + at + 4 * lane;
+#pragma unroll
+      for (int j = kOut / kLoaders; j < kPer; ++j, p += kLoaders * x_pitch)
+        if (live(j)) copy_word(raw + j * kPitch + lane, p);
+      if (lane < kPer && live(lane)) copy_word(raw + lane * kPitch + 32, row(lane) + at + 4 * 32);
+    } else {
 #pragma unroll 1
-  for (int i0 = tid; i0 < CHUNKS; i0 += 128 * STEP) {
-    uint4 v[STEP];
-#pragma unroll
-    for (int j = 0; j < STEP; ++j) {
-      const int i = i0 + 128 * j, r = i >> 3, c = i & 7;
-      v[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < CHUNKS && row0 + r < row_end)
-        v[j] = load_unaligned16<E>(lo + (row0 + r) * pitch, static_cast<long long>(block) * kKBytes + 16 * c, bytes, lo, hi);
-    }
-#pragma unroll
-    for (int j = 0; j < STEP; ++j) {
-      const int i = i0 + 128 * j, r = i >> 3, c = i & 7;
-      if (i < CHUNKS) *reinterpret_cast<uint4*>(tile + r * kKBytes + (((c ^ r) & 7) << 4)) = v[j];
+      for (int j = 0; j < kPer; ++j) copy_edge_word(raw + j * kPitch + lane, j, at, lane);
+      if (lane < kPer) copy_edge_word(raw + lane * kPitch + 32, lane, at, 32);
     }
   }
-}
+  __device__ __forceinline__ void place(uint32_t* raw, unsigned char* tile, int block) const {
+    const int lane = threadIdx.x & 31;
+    raw += warp * kPer * kPitch;
+    if (block == 0) {  // the word a row starts inside of, element by element: lane j does row j
+      if (lane < kPer && live(lane)) {
+        const unsigned char* p = row(lane);
+        const int shift = static_cast<int>(shift_of(p)), E_ = static_cast<int>(sizeof(E));
+        uint32_t first = 0;
+        for (int i = 0; i * E_ + shift < 4 && i * E_ < row_bytes; ++i)
+          first |= static_cast<uint32_t>(reinterpret_cast<const E*>(p)[i]) << (8 * (shift + E_ * i));
+        raw[lane * kPitch] = first;
+      }
+      __syncwarp();
+    }
+    unsigned char* dst = tile + warp * kKBytes + (((lane >> 2) ^ (warp & 7)) << 4) + 4 * (lane & 3);
+    const uint32_t w_low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(w)), w_step = static_cast<uint32_t>(kLoaders * w_pitch);
+    const uint32_t x_low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x)), x_step = static_cast<uint32_t>(kLoaders * x_pitch);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint32_t low = j < kOut / kLoaders ? w_low + j * w_step : x_low + (j - kOut / kLoaders) * x_step;
+      // (the funnel shift takes the distance modulo 32: 8 * (address % 4))
+      *reinterpret_cast<uint32_t*>(dst + j * kLoaders * kKBytes) =
+          __funnelshift_r(raw[j * kPitch + lane], raw[j * kPitch + lane + 1], 8 * low);
+    }
+  }
+};
 
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
   float v;
@@ -153,13 +187,17 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
   const int kb0 = static_cast<int>(static_cast<long long>(blocks) * rank / S);
   const int nkb = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / S) - kb0;
 
+  if (TMA && warp == 5 && lane == 0) {
+    prefetch_map(&wmap);
+    prefetch_map(&xmap);
+  }
   if (warp == 0) {
     tc05::tmem_alloc(&sm.tmem_base, kCols);
     tc05::tmem_relinquish();
   }
   if (tid == kEpiThreads) {
     for (int i = 0; i < stages; ++i) {
-      mbar_init(&sm.full[i], TMA ? 1 : 128);
+      mbar_init(&sm.full[i], TMA ? 1 : kLoaders);
       mbar_init(&sm.empty[i], 1);
     }
     mbar_init(&sm.acc, 1);
@@ -212,18 +250,29 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
         mbar_wait_bounded(smem_u32(&sm.full[j % stages]), (j / stages) & 1, kLinearWaitNs);
     }
   } else if (!TMA && warp >= 5) {
-    const int group = (warp - 5) >> 2, t = tid - kEpiThreads - 32 - 128 * group;
+    const RowLoader<E, TOK> rows(p, n0, m0, warp - 5);
+    uint32_t* raws = reinterpret_cast<uint32_t*>(ring + stages * kStage);
+    auto raw = [&](int i) { return raws + (i % kRawStages) * RowLoader<E, TOK>::kRawWords; };
     bool ok = true;
-    for (int i = group; i < nkb && ok; i += 2) {
+    for (int i = 0; i < kRawStages - 1; ++i) {
+      if (i < nkb) rows.fetch(raw(i), kb0 + i);
+      cp_async_commit();
+    }
+    for (int i = 0; i < nkb; ++i) {
+      if (i + kRawStages - 1 < nkb) rows.fetch(raw(i + kRawStages - 1), kb0 + i + kRawStages - 1);
+      cp_async_commit();
+      cp_async_wait<kRawStages - 1>();
+      __syncwarp();
       const int s = i % stages;
       if (i >= stages) ok = mbar_wait_bounded(smem_u32(&sm.empty[s]), (i / stages - 1) & 1, kLinearWaitNs);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      unsigned char* w = ring + s * kStage;
-      copy_tile<E, kOut>(w, p.w, p.ldw, n0, p.N, kb0 + i, p.K, t);
-      copy_tile<E, TOK>(w + kWBytes, p.x, p.ldx, m0, p.M, kb0 + i, p.K, t);
+      rows.place(raw(i), ring + s * kStage, kb0 + i);
       fence_proxy_async_smem();
-      mbar_arrive_local(&sm.full[s]);
+      __syncwarp();  // (also: the raw words have been read before their next copies start)
+      if (lane == 0) mbar_arrive_local(&sm.full[s]);
     }
+    cp_async_wait<0>();
     if (!ok) sm.failed = 1;
   }
   __syncwarp();
@@ -277,18 +326,23 @@ cudaError_t launch_tile(const kda_linear_args& a, cudaStream_t s) {
   constexpr int EPB = kKBytes / sizeof(E);
   const long long gx = (static_cast<long long>(a.N) + kOut - 1) / kOut, gy = (static_cast<long long>(a.M) + TOK - 1) / TOK;
   if (gy > 65535 || gx * kMaxSplit > INT32_MAX) return cudaErrorNotSupported;
-  // two CTAs share an SM's 227 KB: ring of about 100 KB
-  const int stages = static_cast<int>(100 * 1024 / stage) < kMaxStages ? static_cast<int>(100 * 1024 / stage) : kMaxStages;
-  // split K while the CTAs still fit the SMs (two on each) and each keeps four blocks of K
+  // With TMA two CTAs share an SM's 227 KB: a ring of about 100 KB. The loaders' raw
+  // words leave one CTA an SM, and one stage to fill while another is read.
+  constexpr int kCtas = TMA ? 2 : 1;
+  constexpr size_t kRaw = TMA ? 0 : kRawStages * RowLoader<E, TOK>::kRawWords * sizeof(uint32_t);
+  constexpr int kFit = static_cast<int>(100 * 1024 / stage);
+  constexpr int stages = !TMA ? 2 : kFit < kMaxStages ? kFit : kMaxStages;
+  static_assert(stages * stage >= TOK * kOut * sizeof(float), "the ring holds a CTA's sums");
+  // split K while the CTAs still fit the SMs and each keeps four blocks of K
   const long long blocks = (a.K + EPB - 1) / EPB;
   int S = 1;
-  while (S < kMaxSplit && 2 * S <= TOK && gx * gy * S * 2 <= 2 * 152 && blocks >= 2 * S * 4) S *= 2;
+  while (S < kMaxSplit && 2 * S <= TOK && gx * gy * S * 2 <= kCtas * 152 && blocks >= 2 * S * 4) S *= 2;
   CUtensorMap wmap = {}, xmap = {};
   if (TMA && !(encode_rows(&wmap, a.w, sizeof(E), a.K, a.N, a.ldw, kOut) && encode_rows(&xmap, a.x, sizeof(E), a.K, a.M, a.ldx, TOK)))
     return cudaErrorInvalidValue;
-  const size_t smem = stages * stage + 1024;
+  constexpr size_t smem = stages * stage + kRaw + 1024;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = set_smem_limit_once(kda_linear_kernel<E, Y, TOK, TMA>, 104 * 1024, smem_set);
+  const cudaError_t e = set_smem_limit_once(kda_linear_kernel<E, Y, TOK, TMA>, smem, smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(gx * S), static_cast<unsigned>(gy));
@@ -313,12 +367,13 @@ bool tma_ok(const void* p, long long rows, long long ld, size_t elem) {
 template <typename E, typename Y>
 cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
   if (!tma_ok(a.x, a.M, a.ldx, sizeof(E)) || !tma_ok(a.w, a.N, a.ldw, sizeof(E)))
-    return a.M <= 16 ? launch_tile<E, Y, 16, false>(a, s) : launch_tile<E, Y, 64, false>(a, s);
+    return a.M <= 16   ? launch_tile<E, Y, 16, false>(a, s)
+           : a.M <= 64 ? launch_tile<E, Y, 64, false>(a, s)
+                       : launch_tile<E, Y, 128, false>(a, s);
   if (a.M <= 16) return launch_tile<E, Y, 16, true>(a, s);
   if (a.M <= 32) return launch_tile<E, Y, 32, true>(a, s);
   if (a.M <= 64) return launch_tile<E, Y, 64, true>(a, s);
-  if (a.M <= 128) return launch_tile<E, Y, 128, true>(a, s);
-  return launch_linear_pair(a, s);
+  return launch_linear_wide(a, s);
 }
 
 }  // namespace

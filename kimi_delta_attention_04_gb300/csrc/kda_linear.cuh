@@ -1,4 +1,4 @@
-// Device code shared by the projection's kernels (kda_linear.cu, kda_linear_pair.cu):
+// Device code shared by the projection's kernels (kda_linear.cu, kda_linear_wide.cu):
 // the 8-bit MMA, TMA loads of operand tiles, and the epilogue
 // y = act((x w^T) xs[m] ws[n] + bias[n]) + residual.
 #pragma once
@@ -31,6 +31,10 @@ __device__ __forceinline__ void tma_load_2d(uint32_t smem, const CUtensorMap* ma
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem),
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // 1 / (1 + e^-v) from the special-function unit (ex2, rcp: a few units in the last
