@@ -47,7 +47,7 @@ struct SeqPos {
 // on the way (all threads of the CTA call it; lens: kThreads ints of shared memory
 // that nothing else uses meanwhile). Up to kThreads packed sequences are
 // taken longest first, so that no long one starts when the others are done (16
-// sequences of 512 to 8192 tokens: 133 -> 108 us forward). Returns false, after
+// sequences of 512 to 8192 tokens: 133 -> 116 us forward). Returns false, after
 // reporting, where the array is bad.
 __device__ __forceinline__ bool find_packed_sequence(const kda_scan_args& p, int y, SeqPos& pos, int* lens) {
   __shared__ unsigned long long base, total;  // chunks before the sequence, of all
