@@ -12,6 +12,8 @@
 // the carried state and runs its chunk again from the state that enters it.
 // Nothing waits on memory flags: two barriers per advance, in a fixed order, so
 // results do not vary from run to run.
+#include <algorithm>
+
 #include "kda_cluster.cuh"
 #include "kda_elem.cuh"
 
@@ -37,28 +39,38 @@ __device__ __forceinline__ float decay_of(float f) {
   return r;
 }
 
-struct SeqPos {
-  int n;                 // the sequence
-  int start, end;        // tokens of the sequence
+// A CTA's sequences, one after another.
+struct Sequences {
+  int n, last;           // the present one, and the last that this CTA takes
+  int start, end;        // its tokens
   long long chunk_base;  // its first chunk in h_chunks
 };
 
-// Finds the sequence that the CTA's y'th turn takes, checking the whole of cu_seqlens
-// on the way (all threads of the CTA call it; lens: kThreads ints of shared memory
-// that nothing else uses meanwhile). Up to kThreads packed sequences are
-// taken longest first, so that no long one starts when the others are done (16
-// sequences of 512 to 8192 tokens: 133 -> 116 us forward). Returns false, after
+// The first sequence of a CTA, checking the whole of cu_seqlens on the way (all
+// threads of the CTA call it; lens: kThreads ints of shared memory that nothing else
+// uses meanwhile). Up to kThreads packed sequences take a CTA (or cluster) each,
+// longest first, so that no long one starts when the others are done (16 sequences
+// of 512 to 8192 tokens: 133 -> 116 us forward); more of them are shared out in runs
+// of neighbours, so that the check of all N is made once a CTA. Returns false, after
 // reporting, where the array is bad.
-__device__ __forceinline__ bool find_packed_sequence(const kda_scan_args& p, int y, SeqPos& pos, int* lens) {
+__device__ __forceinline__ bool first_sequence(const kda_scan_args& p, Sequences& q, int* lens) {
+  const int y = blockIdx.y, rows = gridDim.y, tid = threadIdx.x;
+  if (p.cu_seqlens == nullptr) {
+    const int per_seq = (p.T + kScanChunk - 1) / kScanChunk;
+    q.n = y;
+    q.last = p.N - 1;
+    q.start = y * p.T;
+    q.end = q.start + p.T;
+    q.chunk_base = static_cast<long long>(y) * per_seq;
+    return true;
+  }
   __shared__ unsigned long long base, total;  // chunks before the sequence, of all
   __shared__ int chosen;
-  const int tid = threadIdx.x;
-  __syncthreads();  // the previous turn's have been read
   if (tid == 0) base = total = 0;
   if (p.N <= kThreads) {
     if (tid < p.N) lens[tid] = p.cu_seqlens[tid + 1] - p.cu_seqlens[tid];
   } else if (tid == 0) {
-    chosen = y;
+    chosen = static_cast<int>(static_cast<long long>(p.N) * y / rows);
   }
   __syncthreads();
   if (p.N <= kThreads && tid < p.N) {
@@ -85,23 +97,23 @@ __device__ __forceinline__ bool find_packed_sequence(const kda_scan_args& p, int
     if (tid == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
     return false;
   }
-  pos.n = n;
-  pos.start = p.cu_seqlens[n];
-  pos.end = p.cu_seqlens[n + 1];
-  pos.chunk_base = static_cast<long long>(base);
+  q.n = n;
+  q.last = p.N <= kThreads ? n : static_cast<int>(static_cast<long long>(p.N) * (y + 1) / rows) - 1;
+  q.start = p.cu_seqlens[n];
+  q.end = p.cu_seqlens[n + 1];
+  q.chunk_base = static_cast<long long>(base);
   return true;
 }
 
-// The same without cu_seqlens, or with it.
-__device__ __forceinline__ bool find_sequence(const kda_scan_args& p, int y, SeqPos& pos, int* lens) {
-  if (p.cu_seqlens == nullptr) {
-    pos.n = y;
-    pos.start = y * p.T;
-    pos.end = pos.start + p.T;
-    pos.chunk_base = static_cast<long long>(y) * ((p.T + kScanChunk - 1) / kScanChunk);
-    return true;
-  }
-  return find_packed_sequence(p, y, pos, lens);
+// Moves to the CTA's next sequence; false when there is none.
+__device__ __forceinline__ bool next_sequence(const kda_scan_args& p, Sequences& q) {
+  const int step = p.cu_seqlens == nullptr ? static_cast<int>(gridDim.y) : 1;
+  if (q.n > q.last - step) return false;
+  q.chunk_base += static_cast<long long>(step) * ((q.end - q.start + kScanChunk - 1) / kScanChunk);
+  q.n += step;
+  q.start = p.cu_seqlens == nullptr ? q.n * p.T : q.end;
+  q.end = p.cu_seqlens == nullptr ? q.start + p.T : p.cu_seqlens[q.n + 1];
+  return true;
 }
 
 // How a tile's rows are read and written, by their alignment: 16 bytes at a time,
@@ -131,6 +143,19 @@ struct Raw2<float> {
   __device__ __forceinline__ void load(const float* p, const float* q) { v = make_float2(p ? *p : 0.f, q ? *q : 0.f); }
 };
 
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 r = *reinterpret_cast<const float4*>(p);
+  v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
+  const uint2 r = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(r.x << 16), v[1] = __uint_as_float(r.x & 0xffff0000u);
+  v[2] = __uint_as_float(r.y << 16), v[3] = __uint_as_float(r.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float* v) { *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3]));
+}
 __device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v) { *reinterpret_cast<uint32_t*>(p) = Bf16::pack(v.x, v.y); }
 __device__ __forceinline__ void store2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 
@@ -358,9 +383,9 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_fwd_kernel(const kda_sca
   scan_prologue(sm, S);
   int it = 0;
   bool ok = true;
-  for (int turn = blockIdx.y; turn < p.N; turn += gridDim.y) {
-    SeqPos pos;
-    if (!find_sequence(p, turn, pos, reinterpret_cast<int*>(sm.warp))) break;  // (the same answer in every CTA)
+  Sequences pos;
+  bool more = first_sequence(p, pos, reinterpret_cast<int*>(sm.warp));  // (the same answer in every CTA)
+  for (; more; more = next_sequence(p, pos)) {
     const int len = pos.end - pos.start;
     // the tiles of advance j, whose first token for this warp is first(j)
     auto tile_x = [&](int j) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + (j % kStages) * kStage)}; };
@@ -444,9 +469,9 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_sca
   scan_prologue(sm, S);
   int it = 0;
   bool ok = true;
-  for (int turn = blockIdx.y; turn < p.N; turn += gridDim.y) {
-    SeqPos pos;
-    if (!find_sequence(p, turn, pos, reinterpret_cast<int*>(sm.warp))) break;
+  Sequences pos;
+  bool more = first_sequence(p, pos, reinterpret_cast<int*>(sm.warp));
+  for (; more; more = next_sequence(p, pos)) {
     const int len = pos.end - pos.start, chunks = (len + kScanChunk - 1) / kScanChunk;
     auto tile_x = [&](int j) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + (j % kStages) * kStage)}; };
     auto tile_d = [&](int j) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + (j % kStages) * kStage + tile_bytes<X>())}; };
@@ -533,25 +558,44 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_sca
   if (S > 1) cluster_sync_all();  // no CTA ends while another may still write to it
 }
 
-template <typename X, typename G>
+// One token: C channels a thread (4 where the rows allow their accesses), rows of
+// the batch strided over the grid.
+template <typename X, typename G, int C>
 __global__ void __launch_bounds__(kStepThreads) kda_scan_step_kernel(const kda_scan_step_args p) {
-  const int c = blockIdx.x * kStepThreads + threadIdx.x;
-  const long long b = blockIdx.y;
+  const int c = (blockIdx.x * kStepThreads + threadIdx.x) * C;
   if (c >= p.D) return;
-  const int slot = p.indices[b];
-  X* y = static_cast<X*>(p.y) + b * p.y_stride + c;
-  if (slot < 0 || slot >= p.num_slots) {
-    if (slot >= 0 && c == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
-    store_f(y, 0.f);
-    return;
+  for (long long b = blockIdx.y; b < p.B; b += gridDim.y) {
+    const int slot = p.indices[b];
+    const bool live = slot >= 0 && slot < p.num_slots;
+    if (!live && slot >= 0 && c == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
+    const G* gate = static_cast<const G*>(p.gate) + b * p.gate_stride + c;
+    const X* x = static_cast<const X*>(p.x) + b * p.x_stride + c;
+    X* y = static_cast<X*>(p.y) + b * p.y_stride + c;
+    float f[C], u[C], h[C];
+    if (C == 4) {
+      load4(gate, f);
+      load4(x, u);
+    } else {
+      f[0] = load_f(gate);
+      u[0] = load_f(x);
+    }
+    const long long at = static_cast<long long>(live ? slot : 0) * p.D + c;
+#pragma unroll
+    for (int j = 0; j < C; ++j) h[j] = 0.f;
+    if (live) {
+      if (C == 4) load4(p.state_in + at, h);
+      else h[0] = p.state_in[at];
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const float a = p.gate_mode == KDA_SCAN_LOG_DECAY ? decay_of<KDA_SCAN_LOG_DECAY>(f[j]) : decay_of<KDA_SCAN_LOGITS>(f[j]);
+        h[j] = fmaf(a, h[j], p.flags & KDA_SCAN_FLAG_COMPLEMENT ? fmaf(-a, u[j], u[j]) : u[j]);
+      }
+      if (C == 4) store4(p.state_out + at, h);
+      else p.state_out[at] = h[0];
+    }
+    if (C == 4) store4(y, h);
+    else store_f(y, h[0]);
   }
-  const float f = load_f(static_cast<const G*>(p.gate) + b * p.gate_stride + c);
-  const float a = p.gate_mode == KDA_SCAN_LOG_DECAY ? decay_of<KDA_SCAN_LOG_DECAY>(f) : decay_of<KDA_SCAN_LOGITS>(f);
-  const float x = load_f(static_cast<const X*>(p.x) + b * p.x_stride + c);
-  const long long at = static_cast<long long>(slot) * p.D + c;
-  const float h = a * p.state_in[at] + (p.flags & KDA_SCAN_FLAG_COMPLEMENT ? (1.f - a) * x : x);
-  p.state_out[at] = h;
-  store_f(y, h);
 }
 
 size_t elem_bytes(int32_t dt) { return dt == KDA_DTYPE_FP32 ? 4 : 2; }
@@ -609,7 +653,10 @@ cudaError_t launch_clusters(void (*kernel)(Args, int), Instance& inst, size_t sm
     if (work <= static_cast<long long>(fit) * rounds) break;
   }
   attr.val.clusterDim.x = S;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks * S), static_cast<unsigned>(f.N < 65535 ? f.N : 65535));
+  long long rows = f.N < 65535 ? f.N : 65535;
+  // (many packed sequences: runs of them, eight rounds of CTAs in all)
+  if (f.cu_seqlens && f.N > kThreads) rows = std::min(rows, std::max<long long>(kThreads, 8 * 2 * 152 / blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * S), static_cast<unsigned>(rows));
   return cudaLaunchKernelEx(&cfg, kernel, a, S);
 }
 
@@ -664,13 +711,29 @@ cudaError_t launch_scan_bwd(const kda_scan_bwd_args& a, cudaStream_t s) {
   return launch_types(a, f, acc, s);
 }
 
-cudaError_t launch_scan_step(const kda_scan_step_args& a, cudaStream_t s) {
-  if (a.B > 65535) return cudaErrorNotSupported;
-  const dim3 grid(static_cast<unsigned>((a.D + kStepThreads - 1) / kStepThreads), static_cast<unsigned>(a.B));
-  if (a.dtype == KDA_DTYPE_FP32) kda_scan_step_kernel<float, float><<<grid, kStepThreads, 0, s>>>(a);
-  else if (a.gate_dtype == KDA_DTYPE_FP32) kda_scan_step_kernel<__nv_bfloat16, float><<<grid, kStepThreads, 0, s>>>(a);
-  else kda_scan_step_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kStepThreads, 0, s>>>(a);
+namespace {
+
+template <typename X, typename G>
+cudaError_t launch_step(const kda_scan_step_args& a, cudaStream_t s) {
+  // four channels an access: 16 bytes of fp32, 8 of bf16
+  auto fours = [&](const void* p, int64_t stride, size_t elem) {
+    return reinterpret_cast<uintptr_t>(p) % (4 * elem) == 0 && stride % 4 == 0;
+  };
+  const bool four = a.D % 4 == 0 && fours(a.x, a.x_stride, sizeof(X)) && fours(a.gate, a.gate_stride, sizeof(G)) &&
+                    fours(a.y, a.y_stride, sizeof(X)) && fours(a.state_in, 0, 4) && fours(a.state_out, 0, 4);
+  const int per = kStepThreads * (four ? 4 : 1);
+  const dim3 grid(static_cast<unsigned>((a.D + per - 1) / per), static_cast<unsigned>(std::min(a.B, 65535)));
+  if (four) kda_scan_step_kernel<X, G, 4><<<grid, kStepThreads, 0, s>>>(a);
+  else kda_scan_step_kernel<X, G, 1><<<grid, kStepThreads, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_scan_step(const kda_scan_step_args& a, cudaStream_t s) {
+  if (a.dtype == KDA_DTYPE_FP32) return launch_step<float, float>(a, s);
+  if (a.gate_dtype == KDA_DTYPE_FP32) return launch_step<__nv_bfloat16, float>(a, s);
+  return launch_step<__nv_bfloat16, __nv_bfloat16>(a, s);
 }
 
 }  // namespace kda

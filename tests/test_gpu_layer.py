@@ -227,6 +227,22 @@ def test_linear_repeats_bit_for_bit():
             assert torch.equal(kda.kda_linear(x, w), first)
 
 
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("M,N,K", [(100, 1024, 512), (128, 30000, 80), (3000, 5008, 64), (2500, 4999, 144), (200, 12288, 48),
+                                   (70, 20000, 33), (1300, 2100, 65)])
+def test_linear_many_tiles(dtype, M, N, K):
+    """Several tiles for each SM (both accumulators in turn), widths that divide nothing."""
+    gen = torch.Generator().manual_seed(M + N + K)
+    x, w, xs, ws = linear_inputs(gen, M, N, K, dtype)
+    res = randn(gen, M, N, dtype=BF)
+    cuda = lambda t: None if t is None else t.cuda()  # noqa: E731
+    cn = Canary()
+    y = cn.empty((M, N), BF, name="y")
+    kda.kda_linear(x.cuda(), w.cuda(), x_scale=cuda(xs), w_scale=cuda(ws), residual=res.cuda(), out=y)
+    cn.check()
+    check_linear(y, x, w, xs, ws, res=res)
+
+
 # --- recurrence ---
 
 def scan_inputs(gen, B, T, D, dtype, gate_dtype, mode):
@@ -338,6 +354,40 @@ def test_scan_packed(lens, D):
     assert err.item() == 0
     check_scan(y, hT, x, gate, "logits", True, h0, cu)
     check_scan_grad(dx, dg, dh0, x, gate, dy, "logits", True, h0, dhT, cu)
+
+
+@pytest.mark.parametrize("N,D", [(256, 24), (257, 70), (3000, 8)])
+def test_scan_many_sequences(N, D):
+    """More packed sequences than the CTAs that take them."""
+    gen = torch.Generator().manual_seed(N)
+    lens = [int(v) for v in torch.randint(0, 40, (N,), generator=gen)]
+    lens[N // 2] = 600
+    T = sum(lens)
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32)
+    x, gate = scan_inputs(gen, 1, T, D, BF, BF, "logits")
+    h0, dhT, dy = randn(gen, N, D), randn(gen, N, D), randn(gen, 1, T, D, dtype=BF)
+    how = dict(gate_mode="logits", cu_seqlens=cu.cuda())
+    states = torch.empty(kda.chunk_count(1, T, cu), D, device="cuda")
+    y, hT = kda.kda_scan_fwd(x.cuda(), gate.cuda(), h0=h0.cuda(), h_chunks=states, **how)
+    dx, dg, dh0 = kda.kda_scan_bwd(x.cuda(), gate.cuda(), dy.cuda(), states, dhT=dhT.cuda(), **how)
+    check_scan(y, hT, x, gate, "logits", False, h0, cu)
+    check_scan_grad(dx, dg, dh0, x, gate, dy, "logits", False, h0, dhT, cu)
+
+
+def test_scan_many_rows():
+    """More sequences of a batch, and more single tokens, than a grid's second axis."""
+    N, D = 65535 + 300, 4
+    x = torch.randn(N, 2, D, device="cuda")
+    gate = torch.full((N, 2, D), -0.5, device="cuda")
+    y, hT = kda.kda_scan_fwd(x, gate)
+    a = float(np.exp(-0.5))
+    # two tokens: one product, one sum
+    assert torch.allclose(hT, a * x[:, 0] + x[:, 1], rtol=0, atol=1e-5) and torch.equal(y[:, 1], hT) and torch.equal(y[:, 0], x[:, 0])
+    pool = torch.randn(N, D, device="cuda")
+    idx = torch.arange(N - 1, -1, -1, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(pool)
+    y = kda.kda_scan_step(x[:, 0].contiguous(), gate[:, 0].contiguous(), pool, idx, state_out=out)
+    assert torch.allclose(y, a * pool.flip(0) + x[:, 0], rtol=0, atol=1e-5) and torch.equal(out.flip(0), y)
 
 
 def test_scan_empty_batch_of_tokens():
