@@ -405,6 +405,7 @@ typedef enum {
  *   y         [M, N]  y_dtype (bf16 or fp32), row stride ldy
  * dtype is bf16 or e4m3 (both operands); products and sums are fp32, everything
  * after them is fp32, and y is rounded once. M = 0 does nothing; N, K >= 1.
+ * y overlaps neither x nor w.
  * A bounded wait that runs out writes KDA_ERR_TIMEOUT to err.
  */
 typedef struct kda_linear_args {
@@ -421,7 +422,12 @@ typedef struct kda_linear_args {
   void* y;
   int32_t* err;            /* optional device status word */
 } kda_linear_args;
-kda_status kda_linear(const kda_linear_args* args, kda_stream_t stream);
+/* Bytes of device scratch kda_linear needs: 0 where the rows of x and of w start on
+ * 16-byte boundaries (address and pitch; also for arguments it refuses), otherwise
+ * an aligned copy of the operand that does not. */
+size_t kda_linear_workspace_size(const kda_linear_args* args);
+/* `workspace` is device memory of at least that size, 256-byte aligned (NULL for 0). */
+kda_status kda_linear(const kda_linear_args* args, void* workspace, size_t workspace_bytes, kda_stream_t stream);
 
 typedef enum {
   KDA_SCAN_LOG_DECAY = 0,  /* a = exp(gate) */

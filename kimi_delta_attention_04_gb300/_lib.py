@@ -159,7 +159,8 @@ class Tcgen05ProbeArgs(ctypes.Structure):
 
 
 EXPORTS = ("kda_chunk_fwd", "kda_chunk_output", "kda_chunk_fwd_noalloc", "kda_chunk_workspace_size", "kda_decode_step",
-           "kda_decode_conv_step", "kda_recurrent_step", "kda_head_rmsnorm", "kda_add_rmsnorm", "kda_linear", "kda_scan_fwd",
+           "kda_decode_conv_step", "kda_recurrent_step", "kda_head_rmsnorm", "kda_add_rmsnorm", "kda_linear",
+           "kda_linear_workspace_size", "kda_scan_fwd",
            "kda_scan_bwd", "kda_scan_step", "kda_version",
            "kda_selftest_bounded_wait", "kda_selftest_tcgen05")
 
@@ -193,10 +194,13 @@ def load() -> ctypes.CDLL:
         lib.kda_decode_conv_step.argtypes = [ctypes.POINTER(DecodeConvArgs), ctypes.c_void_p]
         lib.kda_head_rmsnorm.restype = ctypes.c_int
         lib.kda_head_rmsnorm.argtypes = [ctypes.POINTER(RmsNormArgs), ctypes.c_void_p]
-        for name, struct in (("kda_add_rmsnorm", AddRmsNormArgs), ("kda_linear", LinearArgs), ("kda_scan_fwd", ScanArgs),
-                             ("kda_scan_bwd", ScanBwdArgs), ("kda_scan_step", ScanStepArgs)):
+        for name, struct in (("kda_add_rmsnorm", AddRmsNormArgs), ("kda_scan_fwd", ScanArgs), ("kda_scan_bwd", ScanBwdArgs), ("kda_scan_step", ScanStepArgs)):
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = [ctypes.POINTER(struct), ctypes.c_void_p]
+        lib.kda_linear.restype = ctypes.c_int
+        lib.kda_linear.argtypes = [ctypes.POINTER(LinearArgs), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        lib.kda_linear_workspace_size.restype = ctypes.c_size_t
+        lib.kda_linear_workspace_size.argtypes = [ctypes.POINTER(LinearArgs)]
         lib.kda_chunk_fwd_noalloc.restype = ctypes.c_int
         lib.kda_chunk_fwd_noalloc.argtypes = [ctypes.POINTER(ChunkArgs), ctypes.c_void_p]
         lib.kda_version.restype = ctypes.c_char_p
@@ -641,13 +645,13 @@ def _state_output(t, name, x, stream, shape, wanted):
     return t, t.data_ptr()
 
 
-def _call(fn, args, dev, stream):
+def _call(fn, args, dev, stream, *workspace):
     handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == dev:
-        st = fn(args, handle)
+        st = fn(args, *workspace, handle)
     else:
         with torch.cuda.device(dev):
-            st = fn(args, handle)
+            st = fn(args, *workspace, handle)
     if st != KDA_OK:
         raise KdaError(st, fn.__name__)
 
@@ -687,13 +691,15 @@ def kda_add_rmsnorm(x, weight, *, eps, residual=None, residual_out=None, out=Non
 
 
 def kda_linear(x, w, *, bias=None, activation="none", residual=None, x_scale=None, w_scale=None, out=None,
-               out_dtype=None, err=None, stream=None):
+               out_dtype=None, workspace=None, err=None, stream=None):
     """y = act((x w^T) * x_scale * w_scale + bias) + residual.
 
     x [..., K] and w [N, K], both bf16, or both torch.float8_e4m3fn with fp32
     scales x_scale [...] (one per row) and w_scale [N]. bias fp32 [N]; activation
     "none", "silu", "gelu", "sigmoid" or "relu"; residual [..., N] in the output's
-    dtype, bf16 (default) or fp32; out may be residual. Returns y [..., N]."""
+    dtype, bf16 (default) or fp32; out may be residual. Rows of x or w that do not
+    start on 16-byte boundaries are copied into workspace (a CUDA uint8 tensor of
+    kda_linear_workspace_size bytes, made here unless given). Returns y [..., N]."""
     if activation not in KDA_ACTIVATIONS:
         raise ValueError(f"activation: expected one of {sorted(KDA_ACTIVATIONS)}, got {activation!r}")
     lib = _lib or load()
@@ -716,7 +722,15 @@ def kda_linear(x, w, *, bias=None, activation="none", residual=None, x_scale=Non
     args.bias, args.err = _vec(bias, "bias", dev, (N,)), _err_word(err, dev)
     args.residual, args.ld_residual = _rows(residual, "residual", dev, out_dtype, shape)
     out, args.y, args.ldy = _output(out, "out", x, stream, shape, out_dtype)
-    _call(lib.kda_linear, args, dev, stream)
+    if ((args.x or 0) | (args.w or 0) | args.ldx * x.element_size() | args.ldw * x.element_size()) % 16 == 0:
+        _call(lib.kda_linear, args, dev, stream, None, 0)
+        return out
+    need = lib.kda_linear_workspace_size(args)
+    if need and workspace is None:
+        workspace = _empty(x, stream, (need,), torch.uint8)
+    elif need:
+        _vec(workspace, "workspace", dev, (max(need, workspace.numel()),), torch.uint8)
+    _call(lib.kda_linear, args, dev, stream, workspace.data_ptr() if need else None, need)
     return out
 
 

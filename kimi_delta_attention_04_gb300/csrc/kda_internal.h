@@ -104,7 +104,8 @@ struct RmsNormCall {
 // The layer operators' calls are their argument structs, validated on the host
 // (kda_layer_api.cpp).
 cudaError_t launch_add_rmsnorm(const kda_add_rmsnorm_args& a, cudaStream_t s);
-cudaError_t launch_linear(const kda_linear_args& a, cudaStream_t s);
+size_t linear_workspace_bytes(const kda_linear_args& a);  // aligned copies of operands that TMA cannot describe
+cudaError_t launch_linear(kda_linear_args a, void* workspace, cudaStream_t s);
 cudaError_t launch_linear_wide(const kda_linear_args& a, cudaStream_t s);  // many tokens, rows that TMA describes
 cudaError_t launch_scan_fwd(const kda_scan_args& a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const kda_scan_bwd_args& a, cudaStream_t s);

@@ -62,6 +62,23 @@ kda_status check_scan(const kda_scan_args* a, bool forward) {
   return KDA_OK;
 }
 
+kda_status check_linear(const kda_linear_args* a) {
+  if (a == nullptr || a->M < 0 || a->N < 1 || a->K < 1) return KDA_ERR_INVALID_ARG;
+  if (!is_dtype(a->dtype) || !is_dtype(a->y_dtype)) return KDA_ERR_INVALID_ARG;
+  if (a->activation < KDA_ACT_NONE || a->activation > KDA_ACT_RELU) return KDA_ERR_INVALID_ARG;
+  if (a->dtype == KDA_DTYPE_FP32 || a->y_dtype == KDA_DTYPE_E4M3) return KDA_ERR_UNSUPPORTED;
+  if (!aligned(a->err, 4)) return KDA_ERR_INVALID_ARG;
+  if (a->M == 0) return KDA_OK;
+  if (!matrix_ok(a->x, a->dtype, a->M, a->K, a->ldx) || !matrix_ok(a->w, a->dtype, a->N, a->K, a->ldw) ||
+      !matrix_ok(a->y, a->y_dtype, a->M, a->N, a->ldy))
+    return KDA_ERR_INVALID_ARG;
+  if (a->residual && !matrix_ok(a->residual, a->y_dtype, a->M, a->N, a->ld_residual)) return KDA_ERR_INVALID_ARG;
+  const bool scaled = a->dtype == KDA_DTYPE_E4M3;
+  if (scaled != (a->x_scale != nullptr) || scaled != (a->w_scale != nullptr)) return KDA_ERR_INVALID_ARG;
+  if (!aligned(a->x_scale, 4) || !aligned(a->w_scale, 4) || !aligned(a->bias, 4)) return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -82,21 +99,16 @@ kda_status kda_add_rmsnorm(const kda_add_rmsnorm_args* a, kda_stream_t stream) {
   return done(kda::launch_add_rmsnorm(*a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-kda_status kda_linear(const kda_linear_args* a, kda_stream_t stream) {
-  if (a == nullptr || a->M < 0 || a->N < 1 || a->K < 1) return KDA_ERR_INVALID_ARG;
-  if (!is_dtype(a->dtype) || !is_dtype(a->y_dtype)) return KDA_ERR_INVALID_ARG;
-  if (a->activation < KDA_ACT_NONE || a->activation > KDA_ACT_RELU) return KDA_ERR_INVALID_ARG;
-  if (a->dtype == KDA_DTYPE_FP32 || a->y_dtype == KDA_DTYPE_E4M3) return KDA_ERR_UNSUPPORTED;
-  if (!aligned(a->err, 4)) return KDA_ERR_INVALID_ARG;
-  if (a->M == 0) return KDA_OK;
-  if (!matrix_ok(a->x, a->dtype, a->M, a->K, a->ldx) || !matrix_ok(a->w, a->dtype, a->N, a->K, a->ldw) ||
-      !matrix_ok(a->y, a->y_dtype, a->M, a->N, a->ldy))
-    return KDA_ERR_INVALID_ARG;
-  if (a->residual && !matrix_ok(a->residual, a->y_dtype, a->M, a->N, a->ld_residual)) return KDA_ERR_INVALID_ARG;
-  const bool scaled = a->dtype == KDA_DTYPE_E4M3;
-  if (scaled != (a->x_scale != nullptr) || scaled != (a->w_scale != nullptr)) return KDA_ERR_INVALID_ARG;
-  if (!aligned(a->x_scale, 4) || !aligned(a->w_scale, 4) || !aligned(a->bias, 4)) return KDA_ERR_INVALID_ARG;
-  return done(kda::launch_linear(*a, reinterpret_cast<cudaStream_t>(stream)));
+size_t kda_linear_workspace_size(const kda_linear_args* a) {
+  return check_linear(a) == KDA_OK && a->M > 0 ? kda::linear_workspace_bytes(*a) : 0;
+}
+
+kda_status kda_linear(const kda_linear_args* a, void* workspace, size_t workspace_bytes, kda_stream_t stream) {
+  const kda_status st = check_linear(a);
+  if (st != KDA_OK || a->M == 0) return st;
+  const size_t need = kda::linear_workspace_bytes(*a);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))) return KDA_ERR_INVALID_ARG;
+  return done(kda::launch_linear(*a, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kda_status kda_scan_fwd(const kda_scan_args* a, kda_stream_t stream) {

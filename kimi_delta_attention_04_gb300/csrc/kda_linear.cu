@@ -8,9 +8,12 @@
 // bytes along K (64 bf16 or 128 e4m3 values), in the 128-byte swizzle.
 //
 // Roles: warps 0-3 the epilogue, warp 4 issues the MMAs, warp 5 the TMA loads
-// through a ring of stages. Rows that TMA cannot describe (an address or a row
-// pitch that is no multiple of 16 bytes) are copied by sixteen loader warps
-// instead.
+// through a ring of stages.
+//
+// Rows that TMA cannot describe (an address or a row pitch that is no multiple of 16
+// bytes) are first copied to a pitch that is one, in the caller's workspace: a pass
+// over the operand costs less than loads that shift every row on its way into every
+// tile (777 x 1001 -> 1111: 27 us in the best such form).
 //
 // Few tiles (small M) leave most SMs without work, so a cluster of S CTAs splits
 // K of one tile: each sums its share, puts it into its own shared memory, and
@@ -26,117 +29,12 @@ using namespace linear;
 constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;
 constexpr int kEpiThreads = 128;
-constexpr int kTmaThreads = kEpiThreads + 64;       // + MMA warp, TMA warp
-constexpr int kLoaders = 16;
-constexpr int kRawStages = 4;
-constexpr int kCopyThreads = kEpiThreads + 32 + 32 * kLoaders;  // + MMA warp, loader warps
+constexpr int kThreads = kEpiThreads + 64;  // + MMA warp, TMA warp
 
 struct LinearHead {
   uint64_t full[kMaxStages], empty[kMaxStages], acc;
   uint32_t tmem_base;
   int failed;
-};
-
-// The operand rows of a tile for rows that start at any byte: warp `warp` of the 16
-// loaders brings rows warp, warp + 16, .. of the 128 + TOK (first w's, then x's).
-// fetch() starts copies of the aligned 4-byte words that hold a row's 128 bytes (33
-// of them; bytes past the row and rows past the end are zero-filled) into raw
-// shared memory that only this warp uses; place() shifts them into the swizzled
-// tile (16-byte chunk c of row r at chunk c ^ (r % 8)). What bounds it is the
-// instructions per row and block: 12 here, 96 in a first form that formed every
-// word's address and length anew (777 x 1001 -> 1111: 55 us, now 26).
-template <typename E, int TOK>
-struct RowLoader {
-  static constexpr int kPer = (kOut + TOK) / kLoaders;   // rows of a warp
-  static constexpr int kPitch = 33;                      // words of a raw row
-  static constexpr uint32_t kRawWords = kLoaders * kPer * kPitch;
-  const unsigned char* w;
-  const unsigned char* x;
-  long long w_pitch, x_pitch, row_bytes;
-  int n, m, n_end, m_end, warp;  // this warp's first rows
-  __device__ __forceinline__ RowLoader(const kda_linear_args& p, int n0, int m0, int loader)
-      : w_pitch(p.ldw * static_cast<long long>(sizeof(E))), x_pitch(p.ldx * static_cast<long long>(sizeof(E))),
-        row_bytes(p.K * static_cast<long long>(sizeof(E))), n(n0 + loader), m(m0 + loader), n_end(p.N), m_end(p.M), warp(loader) {
-    w = static_cast<const unsigned char*>(p.w) + n * w_pitch;
-    x = static_cast<const unsigned char*>(p.x) + m * x_pitch;
-  }
-  // Row j of the warp: where it starts, and whether it exists. Rows that do not are
-  // left alone: what they put into the tile reaches outputs that are not stored.
-  __device__ __forceinline__ const unsigned char* row(int j) const {
-    return j < kOut / kLoaders ? w + j * kLoaders * w_pitch : x + (j - kOut / kLoaders) * kLoaders * x_pitch;
-  }
-  __device__ __forceinline__ bool live(int j) const {
-    return j < kOut / kLoaders ? n + j * kLoaders < n_end : m + (j - kOut / kLoaders) * kLoaders < m_end;
-  }
-  __device__ __forceinline__ bool first_of_matrix(int j) const {
-    return j < kOut / kLoaders ? n + j * kLoaders == 0 : m + (j - kOut / kLoaders) * kLoaders == 0;
-  }
-  __device__ __forceinline__ static uint32_t shift_of(const unsigned char* p) { return reinterpret_cast<uintptr_t>(p) & 3; }
-  // Word `word` of row j at byte `at`, where the row may end inside it or start
-  // after it. (The word that the first row of a matrix starts inside of would begin
-  // before the matrix; place() reads the row's first bytes by themselves.)
-  __device__ __forceinline__ void copy_edge_word(uint32_t* dst, int j, long long at, int word) const {
-    const unsigned char* p = row(j);
-    const long long off = at + 4 * word - shift_of(p), left = row_bytes - off;
-    if (!live(j) || (off < 0 && first_of_matrix(j))) return;
-    if (left <= 0) {
-      *dst = 0u;
-      return;
-    }
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(p + off),
-                 "r"(left < 4 ? static_cast<uint32_t>(left) : 4u)
-                 : "memory");
-  }
-  __device__ __forceinline__ static void copy_word(uint32_t* dst, const unsigned char* p) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)),
-                 "l"(reinterpret_cast<uintptr_t>(p) & ~uintptr_t{3})
-                 : "memory");
-  }
-  __device__ __forceinline__ void fetch(uint32_t* raw, int block) const {
-    const int lane = threadIdx.x & 31;
-    const long long at = static_cast<long long>(block) * kKBytes;
-    raw += warp * kPer * kPitch;
-    if (block > 0 && at + 4 * kPitch <= row_bytes) {  // every word of the block lies inside its row
-      const unsigned char* p = w + at + 4 * lane;
-#pragma unroll
-      for (int j = 0; j < kOut / kLoaders; ++j, p += kLoaders * w_pitch)
-        if (live(j)) copy_word(raw + j * kPitch + lane, p);
-      p = x + at + 4 * lane;
-#pragma unroll
-      for (int j = kOut / kLoaders; j < kPer; ++j, p += kLoaders * x_pitch)
-        if (live(j)) copy_word(raw + j * kPitch + lane, p);
-      if (lane < kPer && live(lane)) copy_word(raw + lane * kPitch + 32, row(lane) + at + 4 * 32);
-    } else {
-#pragma unroll 1
-      for (int j = 0; j < kPer; ++j) copy_edge_word(raw + j * kPitch + lane, j, at, lane);
-      if (lane < kPer) copy_edge_word(raw + lane * kPitch + 32, lane, at, 32);
-    }
-  }
-  __device__ __forceinline__ void place(uint32_t* raw, unsigned char* tile, int block) const {
-    const int lane = threadIdx.x & 31;
-    raw += warp * kPer * kPitch;
-    if (block == 0) {  // the word a row starts inside of, element by element: lane j does row j
-      if (lane < kPer && live(lane)) {
-        const unsigned char* p = row(lane);
-        const int shift = static_cast<int>(shift_of(p)), E_ = static_cast<int>(sizeof(E));
-        uint32_t first = 0;
-        for (int i = 0; i * E_ + shift < 4 && i * E_ < row_bytes; ++i)
-          first |= static_cast<uint32_t>(reinterpret_cast<const E*>(p)[i]) << (8 * (shift + E_ * i));
-        raw[lane * kPitch] = first;
-      }
-      __syncwarp();
-    }
-    unsigned char* dst = tile + warp * kKBytes + (((lane >> 2) ^ (warp & 7)) << 4) + 4 * (lane & 3);
-    const uint32_t w_low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(w)), w_step = static_cast<uint32_t>(kLoaders * w_pitch);
-    const uint32_t x_low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x)), x_step = static_cast<uint32_t>(kLoaders * x_pitch);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const uint32_t low = j < kOut / kLoaders ? w_low + j * w_step : x_low + (j - kOut / kLoaders) * x_step;
-      // (the funnel shift takes the distance modulo 32: 8 * (address % 4))
-      *reinterpret_cast<uint32_t*>(dst + j * kLoaders * kKBytes) =
-          __funnelshift_r(raw[j * kPitch + lane], raw[j * kPitch + lane + 1], 8 * low);
-    }
-  }
 };
 
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
@@ -170,8 +68,8 @@ __device__ __forceinline__ void finish_shared(const Epilogue<Y>& finish, const f
 
 // Grid (S * output tiles, token tiles), cluster (S, 1, 1).
 // E: bits of an operand element (uint16_t bf16, uint8_t e4m3).
-template <typename E, typename Y, int TOK, bool TMA>
-__global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
+template <typename E, typename Y, int TOK>
+__global__ void __launch_bounds__(kThreads)
     kda_linear_kernel(const kda_linear_args p, const __grid_constant__ CUtensorMap wmap,
                       const __grid_constant__ CUtensorMap xmap, int S, int stages) {
   extern __shared__ unsigned char raw[];
@@ -187,7 +85,7 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
   const int kb0 = static_cast<int>(static_cast<long long>(blocks) * rank / S);
   const int nkb = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / S) - kb0;
 
-  if (TMA && warp == 5 && lane == 0) {
+  if (warp == 5 && lane == 0) {
     prefetch_map(&wmap);
     prefetch_map(&xmap);
   }
@@ -197,7 +95,7 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
   }
   if (tid == kEpiThreads) {
     for (int i = 0; i < stages; ++i) {
-      mbar_init(&sm.full[i], TMA ? 1 : kLoaders);
+      mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
     }
     mbar_init(&sm.acc, 1);
@@ -231,7 +129,7 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
       if (ok) tc05::commit(&sm.acc);
       else sm.failed = 1;
     }
-  } else if (TMA && warp == 5) {
+  } else if (warp == 5) {
     if (lane == 0) {
       bool ok = true;
       int i = 0;
@@ -249,31 +147,6 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
       for (int j = i > stages ? i - stages : 0; j < i; ++j)
         mbar_wait_bounded(smem_u32(&sm.full[j % stages]), (j / stages) & 1, kLinearWaitNs);
     }
-  } else if (!TMA && warp >= 5) {
-    const RowLoader<E, TOK> rows(p, n0, m0, warp - 5);
-    uint32_t* raws = reinterpret_cast<uint32_t*>(ring + stages * kStage);
-    auto raw = [&](int i) { return raws + (i % kRawStages) * RowLoader<E, TOK>::kRawWords; };
-    bool ok = true;
-    for (int i = 0; i < kRawStages - 1; ++i) {
-      if (i < nkb) rows.fetch(raw(i), kb0 + i);
-      cp_async_commit();
-    }
-    for (int i = 0; i < nkb; ++i) {
-      if (i + kRawStages - 1 < nkb) rows.fetch(raw(i + kRawStages - 1), kb0 + i + kRawStages - 1);
-      cp_async_commit();
-      cp_async_wait<kRawStages - 1>();
-      __syncwarp();
-      const int s = i % stages;
-      if (i >= stages) ok = mbar_wait_bounded(smem_u32(&sm.empty[s]), (i / stages - 1) & 1, kLinearWaitNs);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      rows.place(raw(i), ring + s * kStage, kb0 + i);
-      fence_proxy_async_smem();
-      __syncwarp();  // (also: the raw words have been read before their next copies start)
-      if (lane == 0) mbar_arrive_local(&sm.full[s]);
-    }
-    cp_async_wait<0>();
-    if (!ok) sm.failed = 1;
   }
   __syncwarp();
 
@@ -320,33 +193,30 @@ __global__ void __launch_bounds__(TMA ? kTmaThreads : kCopyThreads)
   }
 }
 
-template <typename E, typename Y, int TOK, bool TMA>
+template <typename E, typename Y, int TOK>
 cudaError_t launch_tile(const kda_linear_args& a, cudaStream_t s) {
   constexpr size_t stage = (kOut + TOK) * kKBytes;
   constexpr int EPB = kKBytes / sizeof(E);
   const long long gx = (static_cast<long long>(a.N) + kOut - 1) / kOut, gy = (static_cast<long long>(a.M) + TOK - 1) / TOK;
   if (gy > 65535 || gx * kMaxSplit > INT32_MAX) return cudaErrorNotSupported;
-  // With TMA two CTAs share an SM's 227 KB: a ring of about 100 KB. The loaders' raw
-  // words leave one CTA an SM, and one stage to fill while another is read.
-  constexpr int kCtas = TMA ? 2 : 1;
-  constexpr size_t kRaw = TMA ? 0 : kRawStages * RowLoader<E, TOK>::kRawWords * sizeof(uint32_t);
+  // two CTAs share an SM's 227 KB: a ring of about 100 KB
   constexpr int kFit = static_cast<int>(100 * 1024 / stage);
-  constexpr int stages = !TMA ? 2 : kFit < kMaxStages ? kFit : kMaxStages;
+  constexpr int stages = kFit < kMaxStages ? kFit : kMaxStages;
   static_assert(stages * stage >= TOK * kOut * sizeof(float), "the ring holds a CTA's sums");
-  // split K while the CTAs still fit the SMs and each keeps four blocks of K
+  // split K while the CTAs still fit the SMs (two on each) and each keeps four blocks of K
   const long long blocks = (a.K + EPB - 1) / EPB;
   int S = 1;
-  while (S < kMaxSplit && 2 * S <= TOK && gx * gy * S * 2 <= kCtas * 152 && blocks >= 2 * S * 4) S *= 2;
-  CUtensorMap wmap = {}, xmap = {};
-  if (TMA && !(encode_rows(&wmap, a.w, sizeof(E), a.K, a.N, a.ldw, kOut) && encode_rows(&xmap, a.x, sizeof(E), a.K, a.M, a.ldx, TOK)))
+  while (S < kMaxSplit && 2 * S <= TOK && gx * gy * S * 2 <= 2 * 152 && blocks >= 2 * S * 4) S *= 2;
+  CUtensorMap wmap, xmap;
+  if (!encode_rows(&wmap, a.w, sizeof(E), a.K, a.N, a.ldw, kOut) || !encode_rows(&xmap, a.x, sizeof(E), a.K, a.M, a.ldx, TOK))
     return cudaErrorInvalidValue;
-  constexpr size_t smem = stages * stage + kRaw + 1024;
+  constexpr size_t smem = stages * stage + 1024;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = set_smem_limit_once(kda_linear_kernel<E, Y, TOK, TMA>, smem, smem_set);
+  const cudaError_t e = set_smem_limit_once(kda_linear_kernel<E, Y, TOK>, smem, smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(gx * S), static_cast<unsigned>(gy));
-  cfg.blockDim = dim3(TMA ? kTmaThreads : kCopyThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr;
@@ -355,7 +225,59 @@ cudaError_t launch_tile(const kda_linear_args& a, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kda_linear_kernel<E, Y, TOK, TMA>, a, wmap, xmap, S, stages);
+  return cudaLaunchKernelEx(&cfg, kda_linear_kernel<E, Y, TOK>, a, wmap, xmap, S, stages);
+}
+
+template <typename E, typename Y>
+cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
+  if (a.M <= 16) return launch_tile<E, Y, 16>(a, s);
+  if (a.M <= 32) return launch_tile<E, Y, 32>(a, s);
+  if (a.M <= 64) return launch_tile<E, Y, 64>(a, s);
+  return launch_linear_wide(a, s);
+}
+
+// ---- rows to a pitch that TMA describes ----
+
+struct Repitch {
+  const unsigned char* src;
+  unsigned char* dst;
+  long long src_pitch, dst_pitch, row_bytes;
+  int rows;
+};
+
+// A warp a row, 16 bytes a lane and step, from the aligned 4-byte words around them;
+// where those words may lie outside the row (its first and last bytes), element by
+// element. Bytes of the new pitch past the row are not written: no map reaches them.
+template <typename E>
+__global__ void __launch_bounds__(256) kda_linear_repitch_kernel(const Repitch x, const Repitch w) {
+  const int lane = threadIdx.x & 31;
+  const long long total = static_cast<long long>(x.rows) + w.rows;
+  for (long long r = (blockIdx.x * 256LL + threadIdx.x) >> 5; r < total; r += gridDim.x * 8LL) {
+    const bool of_x = r < x.rows;
+    const Repitch& m = of_x ? x : w;
+    const long long row = of_x ? r : r - x.rows;
+    const unsigned char* src = m.src + row * m.src_pitch;
+    unsigned char* dst = m.dst + row * m.dst_pitch;
+    for (long long b = 16 * lane; b < m.row_bytes; b += 512) {
+      const unsigned char* p = src + b;
+      if (b >= 4 && b + 20 <= m.row_bytes) {
+        const uint32_t shift = reinterpret_cast<uintptr_t>(p) & 3;
+        const uint32_t* at = reinterpret_cast<const uint32_t*>(p - shift);
+        uint32_t v[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) v[i] = at[i];
+        uint4 out;
+        out.x = __funnelshift_r(v[0], v[1], 8 * shift);
+        out.y = __funnelshift_r(v[1], v[2], 8 * shift);
+        out.z = __funnelshift_r(v[2], v[3], 8 * shift);
+        out.w = __funnelshift_r(v[3], v[4], 8 * shift);
+        *reinterpret_cast<uint4*>(dst + b) = out;
+      } else {
+        for (int i = 0; i < 16 && b + i < m.row_bytes; i += sizeof(E))
+          *reinterpret_cast<E*>(dst + b + i) = *reinterpret_cast<const E*>(p + i);
+      }
+    }
+  }
 }
 
 // Whether TMA can describe the rows: address and pitch on 16-byte boundaries
@@ -364,21 +286,42 @@ bool tma_ok(const void* p, long long rows, long long ld, size_t elem) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows == 1 || ld * static_cast<long long>(elem) % 16 == 0);
 }
 
-template <typename E, typename Y>
-cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
-  if (!tma_ok(a.x, a.M, a.ldx, sizeof(E)) || !tma_ok(a.w, a.N, a.ldw, sizeof(E)))
-    return a.M <= 16   ? launch_tile<E, Y, 16, false>(a, s)
-           : a.M <= 64 ? launch_tile<E, Y, 64, false>(a, s)
-                       : launch_tile<E, Y, 128, false>(a, s);
-  if (a.M <= 16) return launch_tile<E, Y, 16, true>(a, s);
-  if (a.M <= 32) return launch_tile<E, Y, 32, true>(a, s);
-  if (a.M <= 64) return launch_tile<E, Y, 64, true>(a, s);
-  return launch_linear_wide(a, s);
+size_t elem_of(const kda_linear_args& a) { return a.dtype == KDA_DTYPE_BF16 ? 2 : 1; }
+size_t pitch_of(const kda_linear_args& a) { return (a.K * elem_of(a) + 15) / 16 * 16; }
+size_t copy_bytes(const kda_linear_args& a, const void* p, long long rows, long long ld) {
+  return tma_ok(p, rows, ld, elem_of(a)) ? 0 : (rows * pitch_of(a) + 255) / 256 * 256;
+}
+
+// Operands that need it into the workspace; `a` then refers to the copies.
+cudaError_t repitch(kda_linear_args& a, void* workspace, cudaStream_t s) {
+  const size_t e = elem_of(a), pitch = pitch_of(a), xb = copy_bytes(a, a.x, a.M, a.ldx), wb = copy_bytes(a, a.w, a.N, a.ldw);
+  if (xb == 0 && wb == 0) return cudaSuccess;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  const long long bytes = static_cast<long long>(a.K) * e, dst_pitch = static_cast<long long>(pitch);
+  const Repitch x = {static_cast<const unsigned char*>(a.x), ws, a.ldx * static_cast<long long>(e), dst_pitch, bytes, xb ? a.M : 0};
+  const Repitch w = {static_cast<const unsigned char*>(a.w), ws + xb, a.ldw * static_cast<long long>(e), dst_pitch, bytes, wb ? a.N : 0};
+  const long long rows = static_cast<long long>(x.rows) + w.rows, grid = (rows + 7) / 8;
+  const unsigned ctas = static_cast<unsigned>(grid < 8 * 152 ? grid : 8 * 152);
+  if (e == 2) kda_linear_repitch_kernel<uint16_t><<<ctas, 256, 0, s>>>(x, w);
+  else kda_linear_repitch_kernel<uint8_t><<<ctas, 256, 0, s>>>(x, w);
+  if (xb) {
+    a.x = x.dst;
+    a.ldx = static_cast<int64_t>(pitch / e);
+  }
+  if (wb) {
+    a.w = w.dst;
+    a.ldw = static_cast<int64_t>(pitch / e);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_linear(const kda_linear_args& a, cudaStream_t s) {
+size_t linear_workspace_bytes(const kda_linear_args& a) { return copy_bytes(a, a.x, a.M, a.ldx) + copy_bytes(a, a.w, a.N, a.ldw); }
+
+cudaError_t launch_linear(kda_linear_args a, void* workspace, cudaStream_t s) {
+  const cudaError_t e = repitch(a, workspace, s);
+  if (e != cudaSuccess) return e;
   if (a.dtype == KDA_DTYPE_BF16)
     return a.y_dtype == KDA_DTYPE_BF16 ? launch<uint16_t, __nv_bfloat16>(a, s) : launch<uint16_t, float>(a, s);
   return a.y_dtype == KDA_DTYPE_BF16 ? launch<uint8_t, __nv_bfloat16>(a, s) : launch<uint8_t, float>(a, s);

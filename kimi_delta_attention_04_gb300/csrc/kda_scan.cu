@@ -46,61 +46,80 @@ struct Sequences {
   long long chunk_base;  // its first chunk in h_chunks
 };
 
+// Chunks of a sequence of a packed batch, and whether its two ends are in order.
+__device__ __forceinline__ unsigned chunks_of(int s, int e, int T, bool& bad) {
+  const bool wrong = e < s || s < 0 || e > T;
+  bad |= wrong;
+  return wrong ? 0u : static_cast<unsigned>(e - s + kScanChunk - 1) / kScanChunk;
+}
+
 // The first sequence of a CTA, checking the whole of cu_seqlens on the way (all
-// threads of the CTA call it; lens: kThreads ints of shared memory that nothing else
-// uses meanwhile). Up to kThreads packed sequences take a CTA (or cluster) each,
-// longest first, so that no long one starts when the others are done (16 sequences
-// of 512 to 8192 tokens: 133 -> 116 us forward); more of them are shared out in runs
-// of neighbours, so that the check of all N is made once a CTA. Returns false, after
-// reporting, where the array is bad.
-__device__ __forceinline__ bool first_sequence(const kda_scan_args& p, Sequences& q, int* lens) {
+// threads of the CTA call it; scratch: kThreads + 1 ints of shared memory that
+// nothing else uses meanwhile). Up to kThreads packed sequences take a CTA (or
+// cluster) each, longest first, so that no long one starts when the others are done
+// (16 sequences of 512 to 8192 tokens: 133 -> 116 us forward); more of them are
+// shared out in runs of neighbours, so that the check of all N is made once a CTA.
+// Returns false, after reporting, where the array is bad.
+__device__ __forceinline__ bool first_sequence(const kda_scan_args& p, Sequences& q, int* scratch) {
   const int y = blockIdx.y, rows = gridDim.y, tid = threadIdx.x;
   if (p.cu_seqlens == nullptr) {
-    const int per_seq = (p.T + kScanChunk - 1) / kScanChunk;
     q.n = y;
     q.last = p.N - 1;
     q.start = y * p.T;
     q.end = q.start + p.T;
-    q.chunk_base = static_cast<long long>(y) * per_seq;
+    q.chunk_base = static_cast<long long>(y) * ((p.T + kScanChunk - 1) / kScanChunk);
     return true;
   }
   __shared__ unsigned long long base, total;  // chunks before the sequence, of all
   __shared__ int chosen;
   if (tid == 0) base = total = 0;
-  if (p.N <= kThreads) {
-    if (tid < p.N) lens[tid] = p.cu_seqlens[tid + 1] - p.cu_seqlens[tid];
-  } else if (tid == 0) {
-    chosen = static_cast<int>(static_cast<long long>(p.N) * y / rows);
-  }
-  __syncthreads();
-  if (p.N <= kThreads && tid < p.N) {
-    int rank = 0;  // longer ones, and equal ones before
-    for (int i = 0; i < p.N; ++i) rank += lens[i] > lens[tid] || (lens[i] == lens[tid] && i < tid);
-    if (rank == y) chosen = tid;
-  }
-  __syncthreads();
-  const int n = chosen;
-  bool bad = tid == 0 && (p.cu_seqlens[0] != 0 || p.cu_seqlens[p.N] != p.T);
+  bool bad = false;
   unsigned long long mine = 0, all = 0;
-  for (int i = tid; i < p.N; i += kThreads) {
-    const int s = p.cu_seqlens[i], e = p.cu_seqlens[i + 1];
-    bad |= e < s || s < 0 || e > p.T;
-    const unsigned chunks = bad ? 0u : static_cast<unsigned>(e - s + kScanChunk - 1) / kScanChunk;
-    all += chunks;
-    if (i < n) mine += chunks;
+  int n;
+  if (p.N <= kThreads) {
+    for (int i = tid; i <= p.N; i += kThreads) scratch[i] = p.cu_seqlens[i];
+    __syncthreads();
+    if (tid < p.N) {
+      const int s = scratch[tid], e = scratch[tid + 1];
+      all = chunks_of(s, e, p.T, bad);
+      int rank = 0;  // longer ones, and equal ones before
+      for (int i = 0; i < p.N; ++i) {
+        const int len = scratch[i + 1] - scratch[i];
+        rank += len > e - s || (len == e - s && i < tid);
+      }
+      if (rank == y) chosen = tid;
+    }
+    bad |= tid == 0 && (scratch[0] != 0 || scratch[p.N] != p.T);
+    __syncthreads();
+    n = chosen;
+    if (tid < n) mine = all;
+    q.start = scratch[n];
+    q.end = scratch[n + 1];
+    q.last = n;
+  } else {
+    n = static_cast<int>(static_cast<long long>(p.N) * y / rows);
+    q.last = static_cast<int>(static_cast<long long>(p.N) * (y + 1) / rows) - 1;
+    q.start = p.cu_seqlens[n];
+    q.end = p.cu_seqlens[n + 1];
+    for (int i = tid; i < p.N; i += kThreads) {
+      const unsigned chunks = chunks_of(p.cu_seqlens[i], p.cu_seqlens[i + 1], p.T, bad);
+      all += chunks;
+      if (i < n) mine += chunks;
+    }
+    bad |= tid == 0 && (p.cu_seqlens[0] != 0 || p.cu_seqlens[p.N] != p.T);
+    __syncthreads();  // base and total are 0
   }
-  if (mine != 0) atomicAdd(&base, mine);
-  if (all != 0) atomicAdd(&total, all);
-  __syncthreads();
-  bad |= p.h_chunks != nullptr && total > static_cast<unsigned long long>(p.h_chunks_rows);
+  if (p.h_chunks != nullptr) {
+    if (mine != 0) atomicAdd(&base, mine);
+    if (all != 0) atomicAdd(&total, all);
+    __syncthreads();
+    bad |= total > static_cast<unsigned long long>(p.h_chunks_rows);
+  }
   if (__syncthreads_or(bad)) {
     if (tid == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
     return false;
   }
   q.n = n;
-  q.last = p.N <= kThreads ? n : static_cast<int>(static_cast<long long>(p.N) * (y + 1) / rows) - 1;
-  q.start = p.cu_seqlens[n];
-  q.end = p.cu_seqlens[n + 1];
   q.chunk_base = static_cast<long long>(base);
   return true;
 }

@@ -205,6 +205,19 @@ def test_linear_start_off_alignment():
     check_linear(y, base[:, 3:131].cpu(), w, None, None)
 
 
+def test_linear_workspace_of_the_caller():
+    gen = torch.Generator().manual_seed(15)
+    x, w = randn(gen, 40, 51, dtype=BF), randn(gen, 30, 51, dtype=BF)
+    cn = Canary()
+    need = 2 * (40 * 112 // 256 + 1) * 256
+    ws = cn.empty((need,), torch.uint8, name="workspace")
+    y = kda.kda_linear(x.cuda(), w.cuda(), workspace=ws)
+    cn.check()
+    check_linear(y, x, w, None, None)
+    with pytest.raises(ValueError, match="workspace"):
+        kda.kda_linear(x.cuda(), w.cuda(), workspace=ws[:256])
+
+
 def test_linear_nan_and_inf_stay_in_their_rows():
     gen = torch.Generator().manual_seed(6)
     for M in (20, 300):

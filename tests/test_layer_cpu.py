@@ -94,8 +94,25 @@ def _linear(**over):
     (dict(x_scale=FAKE, w_scale=FAKE), INVALID),                  # bf16 takes none
 ])
 def test_linear_refuses(lib, over, status):
-    assert lib.kda_linear(ctypes.byref(_linear(**over)), None) == status
-    assert lib.kda_linear(None, None) == INVALID
+    a = _linear(**over)
+    assert lib.kda_linear(ctypes.byref(a), ctypes.c_void_p(FAKE), 1 << 30, None) == status
+    assert lib.kda_linear_workspace_size(ctypes.byref(a)) == 0
+    assert lib.kda_linear(None, None, 0, None) == INVALID
+
+
+def test_linear_workspace(lib):
+    """Nothing for rows on 16-byte boundaries; otherwise a copy at a pitch of 16 bytes, each rounded to 256."""
+    def size(**over):
+        return lib.kda_linear_workspace_size(ctypes.byref(_linear(**over)))
+    assert size(K=40, ldx=40, ldw=48) == 0
+    assert size(K=40, ldx=41, ldw=48) == 512           # 5 rows of 80 bytes
+    assert size(K=40, ldx=40, ldw=41) == 768           # 7 rows of 80 bytes
+    assert size() == 512 + 768                         # 33 values: 66 bytes, a pitch of 80
+    assert size(M=1, K=40, ldx=41, ldw=40) == 0        # one row has no pitch
+    assert size(M=1, K=40, ldx=41, ldw=40, x=FAKE + 2) == 256
+    a = _linear()
+    call = lambda ws, n: lib.kda_linear(ctypes.byref(a), ctypes.c_void_p(ws), n, None)  # noqa: E731
+    assert call(None, 1 << 20) == INVALID and call(FAKE, 1279) == INVALID and call(FAKE + 16, 1 << 20) == INVALID
 
 
 def _scan(**over):
@@ -155,7 +172,7 @@ def test_scan_step_refuses(lib, over, status):
 def test_empty_calls_do_nothing(lib):
     """No rows: accepted on the host without a launch (there is no GPU here)."""
     assert lib.kda_add_rmsnorm(ctypes.byref(_norm(R=0, x=None, y=None)), None) == _lib.KDA_OK
-    assert lib.kda_linear(ctypes.byref(_linear(M=0, x=None, y=None)), None) == _lib.KDA_OK
+    assert lib.kda_linear(ctypes.byref(_linear(M=0, x=None, y=None)), None, 0, None) == _lib.KDA_OK
     a = _fill(_lib.ScanStepArgs(), dtype=BF16, gate_dtype=BF16, B=0, D=20, num_slots=5)
     assert lib.kda_scan_step(ctypes.byref(a), None) == _lib.KDA_OK
 
