@@ -101,15 +101,64 @@ __device__ __forceinline__ void tile_of(int t, int mt, int nt, int& m, int& n) {
   m = first + r % width;
 }
 
-__device__ __forceinline__ void store_block(__nv_bfloat16* y, const float (&v)[8]) {
+// 32 bytes at once (sm_100 and later).
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+
+// 16 consecutive values of a row, 32 bytes an access.
+__device__ __forceinline__ void store16(__nv_bfloat16* y, const float* v) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = Bf16::pack(v[2 * i], v[2 * i + 1]);
+  store32(y, w);
+}
+__device__ __forceinline__ void store16(float* y, const float* v) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+    store32(y + 8 * h, w);
+  }
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* v) {
+  uint32_t w[8];
+  load32(p, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load16(const float* p, float* v) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+    load32(p + 8 * h, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[8 * h + i] = __uint_as_float(w[i]);
+  }
+}
+
+// 8 consecutive values of a row, 16 bytes an access.
+__device__ __forceinline__ void store8(__nv_bfloat16* y, const float* v) {
   *reinterpret_cast<uint4*>(y) =
       make_uint4(Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3]), Bf16::pack(v[4], v[5]), Bf16::pack(v[6], v[7]));
 }
-__device__ __forceinline__ void store_block(float* y, const float (&v)[8]) {
+__device__ __forceinline__ void store8(float* y, const float* v) {
   reinterpret_cast<float4*>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ void load_block(const __nv_bfloat16* p, float (&v)[8]) {
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
   const uint4 r = *reinterpret_cast<const uint4*>(p);
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -118,14 +167,22 @@ __device__ __forceinline__ void load_block(const __nv_bfloat16* p, float (&v)[8]
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load_block(const float* p, float (&v)[8]) {
+__device__ __forceinline__ void load8(const float* p, float* v) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
-// Finishes 32 consecutive outputs n .. of one token whose rows of y and of the
-// residual allow 16-byte accesses (so N is a multiple of 8): those below `end`.
-template <typename Y>
+// How rows of y and of the residual can be accessed: 32 or 16 bytes at a time by one
+// thread, or (any alignment) through shared memory. A lane's rows are a pitch apart,
+// so each access of a warp is 32 separate pieces whatever its width: 32 bytes instead
+// of 16 took 5536 x 800 -> 5216 e4m3 from 37 to 29 us.
+// (An instance of the kernel each: with all three in one, its instructions no longer
+// fit the caches near the SM's schedulers, and every path took a third longer.)
+enum { kRows32 = 2, kRows16 = 1, kRowsAny = 0 };
+
+// Finishes 32 consecutive outputs n .. of one token: those below `end` (a multiple
+// of the access's values).
+template <typename Y, int ACCESS>
 __device__ __forceinline__ void finish_row(const kda_linear_args& p, float (&v)[32], const float* ws, const float* bias, float xs,
                                            long long m, int n, int end) {
   if (m >= p.M) return;
@@ -133,11 +190,11 @@ __device__ __forceinline__ void finish_row(const kda_linear_args& p, float (&v)[
   if (p.residual) {
     const Y* r = static_cast<const Y*>(p.residual) + m * p.ld_residual + n;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      float u[8];
-      if (n + 8 * b < end) load_block(r + 8 * b, u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) res[8 * b + j] = u[j];
+    for (int b = 0; b < 32; b += 8 * ACCESS) {
+      if (n + b < end) {
+        if (ACCESS == kRows32) load16(r + b, res + b);
+        else load8(r + b, res + b);
+      }
     }
   }
 #pragma unroll
@@ -155,18 +212,18 @@ __device__ __forceinline__ void finish_row(const kda_linear_args& p, float (&v)[
   }
   Y* y = static_cast<Y*>(p.y) + m * p.ldy + n;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    float u[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = v[8 * b + j];
-    if (n + 8 * b < end) store_block(y + 8 * b, u);
+  for (int b = 0; b < 32; b += 8 * ACCESS) {
+    if (n + b < end) {
+      if (ACCESS == kRows32) store16(y + b, v + b);
+      else store8(y + b, v + b);
+    }
   }
 }
 
-template <typename E, typename Y, int CTAS>
+template <typename E, typename Y, int CTAS, int ACCESS>
 __global__ void __launch_bounds__(kWideThreads, 1)
     kda_linear_wide_kernel(const kda_linear_args p, const __grid_constant__ CUtensorMap wmap,
-                           const __grid_constant__ CUtensorMap xmap, int mt, int nt, int NT, int stages, bool vec) {
+                           const __grid_constant__ CUtensorMap xmap, int mt, int nt, int NT, int stages) {
   extern __shared__ unsigned char raw[];
   __shared__ WideHead sm;
   constexpr int EPB = kKBytes / sizeof(E);
@@ -283,7 +340,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const long long m0 = (static_cast<long long>(mi) * CTAS + rank) * kRows + 32 * quarter;
       float* ws = sm.col[buf][0];
       float* bias = sm.col[buf][1];
-      if (vec) {
+      if (ACCESS != kRowsAny) {
         // (the tile before the last that used these has been finished by every warp:
         // each passed the named barrier of the tile in between afterwards)
         const int n = n0 + tid;
@@ -308,8 +365,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
         }
         if (!ok) continue;
-        if (vec) {
-          finish_row<Y>(p, v, ws + 32 * c, bias + 32 * c, xs, m0 + lane, n0 + 32 * c, end);
+        if constexpr (ACCESS != kRowsAny) {
+          finish_row<Y, ACCESS>(p, v, ws + 32 * c, bias + 32 * c, xs, m0 + lane, n0 + 32 * c, end);
         } else {
           // rows of any alignment: 16 tokens x 32 outputs at a time through shared
           // memory, so that a warp's accesses are 32 consecutive outputs of a token
@@ -349,12 +406,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
 }
 
-// Whether rows of y (and of the residual) allow 16-byte accesses.
-bool rows_aligned(const void* p, int64_t ld, size_t elem) {
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * static_cast<int64_t>(elem) % 16 == 0);
+// Whether rows of N values at p can be accessed `bytes` at a time.
+bool rows_allow(const void* p, int64_t ld, int N, size_t elem, int64_t bytes) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * static_cast<int64_t>(elem) % bytes == 0 &&
+                          N % (bytes / 2) == 0);  // (16 or 8 values at a time, of either type)
 }
 
-template <typename E, typename Y, int CTAS>
+template <typename E, typename Y, int CTAS, int ACCESS>
 cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
   constexpr int kUnits = 152 / CTAS;
   const long long mt = (static_cast<long long>(a.M) + CTAS * kRows - 1) / (CTAS * kRows);
@@ -375,14 +433,13 @@ cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
   CUtensorMap wmap, xmap;
   if (!encode_rows(&wmap, a.w, sizeof(E), a.K, a.N, a.ldw, NT / CTAS) || !encode_rows(&xmap, a.x, sizeof(E), a.K, a.M, a.ldx, kRows))
     return cudaErrorInvalidValue;
-  const bool vec = a.N % 8 == 0 && rows_aligned(a.y, a.ldy, sizeof(Y)) && rows_aligned(a.residual, a.ld_residual, sizeof(Y));
   const size_t stage = kXBytes + ((static_cast<size_t>(NT / CTAS) * kKBytes + 1023) & ~size_t{1023});
   constexpr size_t kStaged = kEpiWarps * 16 * kStageCols * sizeof(float);
   constexpr size_t kMost = kRingBytes + kStaged + 1024;
   const int stages = static_cast<int>(kRingBytes / stage) < kMaxStages ? static_cast<int>(kRingBytes / stage) : kMaxStages;
-  const size_t smem = stages * stage + kStaged + 1024;
+  const size_t smem = stages * stage + (ACCESS == kRowsAny ? kStaged : 0) + 1024;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = set_smem_limit_once(kda_linear_wide_kernel<E, Y, CTAS>, kMost, smem_set);
+  const cudaError_t e = set_smem_limit_once(kda_linear_wide_kernel<E, Y, CTAS, ACCESS>, kMost, smem_set);
   if (e != cudaSuccess) return e;
   const long long units = mt * nt < kUnits ? mt * nt : kUnits;
   cudaLaunchConfig_t cfg = {};
@@ -396,13 +453,22 @@ cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kda_linear_wide_kernel<E, Y, CTAS>, a, wmap, xmap, static_cast<int>(mt), static_cast<int>(nt),
-                            NT, stages, vec);
+  return cudaLaunchKernelEx(&cfg, kda_linear_wide_kernel<E, Y, CTAS, ACCESS>, a, wmap, xmap, static_cast<int>(mt), static_cast<int>(nt),
+                            NT, stages);
+}
+
+template <typename E, typename Y, int CTAS>
+cudaError_t launch_access(const kda_linear_args& a, cudaStream_t s) {
+  auto allow = [&](int64_t bytes) {
+    return rows_allow(a.y, a.ldy, a.N, sizeof(Y), bytes) && rows_allow(a.residual, a.ld_residual, a.N, sizeof(Y), bytes);
+  };
+  if (allow(32)) return launch<E, Y, CTAS, kRows32>(a, s);
+  return allow(16) ? launch<E, Y, CTAS, kRows16>(a, s) : launch<E, Y, CTAS, kRowsAny>(a, s);
 }
 
 template <typename E, typename Y>
 cudaError_t launch_ctas(const kda_linear_args& a, cudaStream_t s) {
-  return a.M <= kRows ? launch<E, Y, 1>(a, s) : launch<E, Y, 2>(a, s);
+  return a.M <= kRows ? launch_access<E, Y, 1>(a, s) : launch_access<E, Y, 2>(a, s);
 }
 
 }  // namespace
