@@ -150,16 +150,14 @@ struct Raw2<__nv_bfloat16> {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
   }
   __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
-    const uint32_t lo = p ? *reinterpret_cast<const uint16_t*>(p) : 0u;
-    const uint32_t hi = q ? *reinterpret_cast<const uint16_t*>(q) : 0u;
-    v = lo | (hi << 16);
+    v = *reinterpret_cast<const uint16_t*>(p) | (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(q)) << 16);
   }
 };
 template <>
 struct Raw2<float> {
   float2 v;
   __device__ __forceinline__ float2 get() const { return v; }
-  __device__ __forceinline__ void load(const float* p, const float* q) { v = make_float2(p ? *p : 0.f, q ? *q : 0.f); }
+  __device__ __forceinline__ void load(const float* p, const float* q) { v = make_float2(*p, *q); }
 };
 
 __device__ __forceinline__ void load4(const float* p, float* v) {
@@ -228,11 +226,14 @@ struct Tile {
       for (int i = 0; i < kScanChunk; ++i, src += stride)
         if (i < m) cp_async_bytes<2 * sizeof(T)>(pairs + i * 32 + lane, src);
     } else {
+      // tokens and channels that do not exist read the last that do: 32 loads without
+      // a condition stay in flight together
+      const T *p0 = rows + min(l.c0, D - 1), *p1 = rows + min(l.c1, D - 1);
       Raw2<T> r[kScanChunk];
 #pragma unroll
       for (int i = 0; i < kScanChunk; ++i) {
-        const T* row = rows + i * stride;
-        r[i].load(i < m && l.p0 ? row + l.c0 : nullptr, i < m && l.p1 ? row + l.c1 : nullptr);
+        const long long at = min(i, m - 1) * stride;
+        r[i].load(p0 + at, p1 + at);
       }
 #pragma unroll
       for (int i = 0; i < kScanChunk; ++i) pairs[i * 32 + lane] = r[i];
