@@ -351,6 +351,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         named_bar_sync(1, 32 * kEpiWarps);
       }
       const float xs = p.x_scale && m0 + lane < p.M ? p.x_scale[m0 + lane] : 1.f;
+      // the residual into L2 while the products run: from HBM each of a warp's blocks
+      // would wait 1.2 us for it after they are done
+      if (p.residual && m0 + lane < p.M) {
+        for (int c = half; c < chunks; c += 2) {
+          const Y* r = static_cast<const Y*>(p.residual) + (m0 + lane) * p.ld_residual + n0 + 32 * c;
+          if (n0 + 32 * c < end) asm volatile("prefetch.global.L2 [%0];" ::"l"(r));
+        }
+      }
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sm.acc_full[buf]), (k / 2) & 1, kLinearWaitNs));
       tc05::fence_after_sync();
       for (int c = half; c < chunks; c += 2) {
