@@ -440,7 +440,10 @@ typedef enum {
  *   h_t = a_t h_{t-1} + u_t,   u_t = x_t, or (1 - a_t) x_t with KDA_SCAN_FLAG_COMPLEMENT
  *   y_t = h_t
  *   x, y        [B, T, D]  dtype (bf16 or fp32)
- *   gate        [B, T, D]  gate_dtype (fp32, or bf16 when dtype is bf16)
+ *   gate        [B, T, D]  gate_dtype (fp32, or bf16 when dtype is bf16); log decays
+ *                          are meant to be <= 0 (-inf resets the state): products of
+ *                          16 and more positive ones are formed on the way and may
+ *                          leave fp32's range
  *   h0, hT      [N, D]     fp32, either may be NULL
  *   cu_seqlens  [N + 1]    as for kda_chunk_fwd (N = B without it)
  *   h_chunks    [chunks, D] fp32 or NULL: the state entering every 16-token

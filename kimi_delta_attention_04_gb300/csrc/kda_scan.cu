@@ -8,10 +8,15 @@
 // no token is read twice. Each warp reduces its chunk to the pair (A, B) of
 // h_out = A h_in + B (A the product of the decays, B the state from zero); the
 // pairs meet in shared memory, the CTAs' totals in every CTA of the cluster
-// (distributed shared memory), and each warp composes the pairs before it with
-// the carried state and runs its chunk again from the state that enters it.
-// Nothing waits on memory flags: two barriers per advance, in a fixed order, so
-// results do not vary from run to run.
+// (remote asynchronous stores, counted on a barrier), and each warp composes the
+// pairs before it with the carried state and runs its chunk again from the state
+// that enters it. The next advances' tiles are on their way meanwhile (asynchronous
+// copies, a ring of two or three tiles a warp). Sums have one fixed order, so results
+// do not vary from run to run.
+//
+// HBM traffic is the bound to come to: 8192 x 4096 bf16 runs at 4.3 TB/s forward (48
+// us; the rest is the latency of the exchange and 22 instructions an element) and 5.2
+// TB/s backward, 4 x 4096 x 2048 with fp32 gates at 5.5 and 6.2 TB/s.
 #include <algorithm>
 
 #include "kda_cluster.cuh"

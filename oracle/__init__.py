@@ -8,7 +8,9 @@ it, and it imports nothing from them.
 Every function here is pinned by ``tests/test_oracle_pins.py`` (closed forms,
 hand-worked golden fixtures, textbook special cases, brute force on tiny
 inputs, and planted-mutation sensitivity checks). No function is parity
-unpinned.
+unpinned. ``layer_oracle`` (norm, projection, gated recurrence) is pinned by
+``tests/test_layer_cpu.py``: hand-worked values, closed forms, and gradients
+against differences.
 """
 
 from .kda_oracle import (  # noqa: F401
