@@ -36,12 +36,14 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // The decay, to about an fp32 step. Long memories multiply hundreds of decays near
 // 1, so exp keeps expf's accuracy; in the sigmoid the error of e^-f is scaled by
 // 1 - a, and the special-function unit's ex2 and rcp do. (e^-f = inf gives 0.)
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 template <int MODE>
 __device__ __forceinline__ float decay_of(float f) {
-  if (MODE == KDA_SCAN_LOG_DECAY) return expf(f);
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-1.44269504f * f)));
-  return r;
+  return MODE == KDA_SCAN_LOG_DECAY ? expf(f) : rcp_approx(1.f + ex2_approx(-1.44269504f * f));
 }
 
 // A CTA's sequences, one after another.
@@ -310,8 +312,9 @@ __device__ __forceinline__ void decays(float2 (&a)[kScanChunk], const Tile<T, AC
   } else {
 #pragma unroll
     for (int i = 0; i < kScanChunk; ++i) {
-      const float2 f = gate.get(i);
-      a[i] = make_float2(decay_of<KDA_SCAN_LOGITS>(f.x), decay_of<KDA_SCAN_LOGITS>(f.y));
+      const float2 z = mul2(gate.get(i), make_float2(-1.44269504f, -1.44269504f));
+      const float2 e = add2(make_float2(ex2_approx(z.x), ex2_approx(z.y)), make_float2(1.f, 1.f));
+      a[i] = make_float2(rcp_approx(e.x), rcp_approx(e.y));
     }
   }
 }
@@ -354,7 +357,9 @@ __device__ __forceinline__ float2 enter_state(ScanSmem& sm, const Map& mine, flo
   sm.warp[parity][warp][lane] = mine;
   __syncthreads();
   Map before = identity_map();
-  for (int w = 0; w < warp; ++w) before = then(before, sm.warp[parity][w][lane]);
+#pragma unroll
+  for (int w = 0; w < kWarps - 1; ++w)
+    if (w < warp) before = then(before, sm.warp[parity][w][lane]);
   if (S == 1) {
     Map total = then(before, mine);
     for (int w = warp + 1; w < kWarps; ++w) total = then(total, sm.warp[parity][w][lane]);
@@ -413,28 +418,29 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_fwd_kernel(const kda_sca
   for (; more; more = next_sequence(p, pos)) {
     const int len = pos.end - pos.start;
     // the tiles of advance j, whose first token for this warp is first(j)
-    auto tile_x = [&](int j) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + (j % kStages) * kStage)}; };
-    auto tile_g = [&](int j) { return Tile<G, ACC>{reinterpret_cast<Raw2<G>*>(mine_ring + (j % kStages) * kStage + tile_bytes<X>())}; };
+    auto tile_x = [&](int slot) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + slot * kStage)}; };
+    auto tile_g = [&](int slot) { return Tile<G, ACC>{reinterpret_cast<Raw2<G>*>(mine_ring + slot * kStage + tile_bytes<X>())}; };
     auto first = [&](int j) { return j * advance + (rank * kWarps + warp) * kScanChunk; };
-    auto fetch = [&](int j) {
+    auto fetch = [&](int j, int slot) {
       const int i0 = first(j);
       if (i0 < len) {
         const long long t0 = pos.start + static_cast<long long>(i0);
-        tile_x(j).fetch(static_cast<const X*>(p.x) + t0 * p.x_stride, p.x_stride, len - i0, l, p.D);
-        tile_g(j).fetch(static_cast<const G*>(p.gate) + t0 * p.gate_stride, p.gate_stride, len - i0, l, p.D);
+        tile_x(slot).fetch(static_cast<const X*>(p.x) + t0 * p.x_stride, p.x_stride, len - i0, l, p.D);
+        tile_g(slot).fetch(static_cast<const G*>(p.gate) + t0 * p.gate_stride, p.gate_stride, len - i0, l, p.D);
       }
       cp_async_commit();
     };
     float2 carry = load_state(p.h0, pos.n, p.D, l);
-    for (int j = 0; j < kStages - 1; ++j) fetch(j);
-    for (int j = 0; j * static_cast<long long>(advance) < len; ++j, ++it) {
-      fetch(j + kStages - 1);
+    for (int j = 0; j < kStages - 1; ++j) fetch(j, j);
+    int slot = 0;  // of advance j; its stage before is the one to fill
+    for (int j = 0; j * static_cast<long long>(advance) < len; ++j, ++it, slot = slot + 1 == kStages ? 0 : slot + 1) {
+      fetch(j + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
       cp_async_wait<kStages - 1>();
       __syncwarp();
       const int i0 = first(j), m = len - i0;
       float2 a[kScanChunk], u[kScanChunk];
-      decays(a, tile_g(j), p.gate_mode);
-      const Tile<X, ACC> tx = tile_x(j);
+      decays(a, tile_g(slot), p.gate_mode);
+      const Tile<X, ACC> tx = tile_x(slot);
 #pragma unroll
       for (int i = 0; i < kScanChunk; ++i) {
         u[i] = tx.get(i);
@@ -498,19 +504,19 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_sca
   bool more = first_sequence(p, pos, reinterpret_cast<int*>(sm.warp));
   for (; more; more = next_sequence(p, pos)) {
     const int len = pos.end - pos.start, chunks = (len + kScanChunk - 1) / kScanChunk;
-    auto tile_x = [&](int j) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + (j % kStages) * kStage)}; };
-    auto tile_d = [&](int j) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + (j % kStages) * kStage + tile_bytes<X>())}; };
-    auto tile_g = [&](int j) { return Tile<G, ACC>{reinterpret_cast<Raw2<G>*>(mine_ring + (j % kStages) * kStage + 2 * tile_bytes<X>())}; };
+    auto tile_x = [&](int slot) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + slot * kStage)}; };
+    auto tile_d = [&](int slot) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + slot * kStage + tile_bytes<X>())}; };
+    auto tile_g = [&](int slot) { return Tile<G, ACC>{reinterpret_cast<Raw2<G>*>(mine_ring + slot * kStage + 2 * tile_bytes<X>())}; };
     // this warp's chunk of advance j (negative: none left)
     auto chunk_of = [&](int j) { return chunks - 1 - ((j * S + rank) * kWarps + warp); };
-    auto fetch = [&](int j) {
+    auto fetch = [&](int j, int slot) {
       const int k = chunk_of(j);
       if (k >= 0) {
         const int m = len - k * kScanChunk;
         const long long t0 = pos.start + static_cast<long long>(k) * kScanChunk;
-        tile_x(j).fetch(static_cast<const X*>(p.x) + t0 * p.x_stride, p.x_stride, m, l, p.D);
-        tile_g(j).fetch(static_cast<const G*>(p.gate) + t0 * p.gate_stride, p.gate_stride, m, l, p.D);
-        tile_d(j).fetch(static_cast<const X*>(q.dy) + t0 * q.dy_stride, q.dy_stride, m, l, p.D);
+        tile_x(slot).fetch(static_cast<const X*>(p.x) + t0 * p.x_stride, p.x_stride, m, l, p.D);
+        tile_g(slot).fetch(static_cast<const G*>(p.gate) + t0 * p.gate_stride, p.gate_stride, m, l, p.D);
+        tile_d(slot).fetch(static_cast<const X*>(q.dy) + t0 * q.dy_stride, q.dy_stride, m, l, p.D);
       }
       cp_async_commit();
     };
@@ -519,17 +525,18 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_sca
       return k >= 0 ? load_state(p.h_chunks, pos.chunk_base + k, p.D, l) : make_float2(0.f, 0.f);
     };
     float2 carry = load_state(q.dhT, pos.n, p.D, l), next_h = chunk_state(0);
-    for (int j = 0; j < kStages - 1; ++j) fetch(j);
-    for (int j = 0; j * S * kWarps < chunks; ++j, ++it) {
+    for (int j = 0; j < kStages - 1; ++j) fetch(j, j);
+    int slot = 0;  // of advance j; its stage before is the one to fill
+    for (int j = 0; j * S * kWarps < chunks; ++j, ++it, slot = slot + 1 == kStages ? 0 : slot + 1) {
       const int k = chunk_of(j), m = k < 0 ? 0 : len - k * kScanChunk;
       float2 h = next_h;
       next_h = chunk_state(j + 1);
-      fetch(j + kStages - 1);
+      fetch(j + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
       cp_async_wait<kStages - 1>();
       __syncwarp();
-      const Tile<X, ACC> tx = tile_x(j), td = tile_d(j);
+      const Tile<X, ACC> tx = tile_x(slot), td = tile_d(slot);
       float2 a[kScanChunk], w[kScanChunk];  // decay; what d multiplies in the decay's gradient
-      decays(a, tile_g(j), p.gate_mode);
+      decays(a, tile_g(slot), p.gate_mode);
       if (comp) {
 #pragma unroll
         for (int i = 0; i < kScanChunk; ++i) {  // a h + (1 - a) x = x + a (h - x)
