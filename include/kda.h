@@ -406,6 +406,9 @@ typedef enum {
  * dtype is bf16 or e4m3 (both operands); products and sums are fp32, everything
  * after them is fp32, and y is rounded once. M = 0 does nothing; N, K >= 1.
  * y overlaps neither x nor w.
+ * Resources: the kernels hold tensor memory while they run, for more than 64 tokens
+ * all 512 columns of each SM they are on. A kernel on another stream that holds some
+ * on the same SM only delays them (their allocation waits), and the other way round.
  * A bounded wait that runs out writes KDA_ERR_TIMEOUT to err.
  */
 typedef struct kda_linear_args {

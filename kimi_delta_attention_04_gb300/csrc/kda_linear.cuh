@@ -91,7 +91,8 @@ struct Epilogue {
   // values, and all reads are issued before anything is stored (y may be the
   // residual, so no load passes a store): 32 reads one by one had made the epilogue
   // of 8192 x 4096 outputs 5 times the products' time.
-  template <int C>
+  // SCALED: the tokens' scales have been multiplied in already.
+  template <bool SCALED = false, int C>
   __device__ __forceinline__ void operator()(float (&v)[C], long long m) const {
     const int live = n < p.N ? static_cast<int>(p.M - m < C ? p.M - m : C) : 0;
     if (live <= 0) return;
@@ -104,7 +105,10 @@ struct Epilogue {
 #pragma unroll
       for (int j = 0; j < C; ++j) res[j] = 0.f;
     }
-    if (p.x_scale) {
+    if (SCALED) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] *= ws;
+    } else if (p.x_scale) {
 #pragma unroll
       for (int j = 0; j < C; ++j) v[j] *= p.x_scale[m + (j < live ? j : 0)] * ws;
     }

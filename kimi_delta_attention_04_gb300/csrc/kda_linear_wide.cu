@@ -47,7 +47,7 @@ struct WideHead {
   uint64_t acc_empty[2];    // leader: the epilogue warps of all CTAs have read it
   uint32_t tmem_base;
   int failed;
-  float col[2][2][kMaxN];   // by accumulator: weight scales and biases of its outputs
+  alignas(16) float col[2][2][kMaxN];  // by accumulator: weight scales and biases of its outputs
 };
 
 template <int CTAS>
@@ -186,7 +186,7 @@ enum { kRows32 = 2, kRows16 = 1, kRowsAny = 0 };
 
 // Finishes 32 consecutive outputs n .. of one token: those below `end` (a multiple
 // of the access's values).
-template <typename Y, int ACCESS>
+template <typename Y, int ACCESS, bool SCALED>
 __device__ __forceinline__ void finish_row(const kda_linear_args& p, float (&v)[32], const float* ws, const float* bias, float xs,
                                            long long m, int n, int end) {
   if (m >= p.M) return;
@@ -201,8 +201,20 @@ __device__ __forceinline__ void finish_row(const kda_linear_args& p, float (&v)[
       }
     }
   }
+  if (SCALED) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], xs * ws[j], bias[j]);
+    for (int j = 0; j < 32; j += 4) {
+      const float4 s = *reinterpret_cast<const float4*>(ws + j);
+      v[j] *= xs * s.x, v[j + 1] *= xs * s.y, v[j + 2] *= xs * s.z, v[j + 3] *= xs * s.w;
+    }
+  }
+  if (p.bias) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(bias + j);
+      v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
+    }
+  }
   switch (p.activation) {
     case KDA_ACT_SILU: activate_all<KDA_ACT_SILU>(v); break;
     case KDA_ACT_GELU: activate_all<KDA_ACT_GELU>(v); break;
@@ -378,7 +390,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         if (!ok) continue;
         if constexpr (ACCESS != kRowsAny) {
-          finish_row<Y, ACCESS>(p, v, ws + 32 * c, bias + 32 * c, xs, m0 + lane, n0 + 32 * c, end);
+          finish_row<Y, ACCESS, sizeof(E) == 1>(p, v, ws + 32 * c, bias + 32 * c, xs, m0 + lane, n0 + 32 * c, end);
         } else {
           // rows of any alignment: 16 tokens x 32 outputs at a time through shared
           // memory, so that a warp's accesses are 32 consecutive outputs of a token
@@ -389,13 +401,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             __syncwarp();
             if (lane / 16 == h) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) staged[(lane % 16) * kStageCols + j] = v[j];
+              for (int j = 0; j < 32; ++j) staged[(lane % 16) * kStageCols + j] = sizeof(E) == 1 ? v[j] * xs : v[j];
             }
             __syncwarp();
             float u[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) u[j] = staged[j * kStageCols + lane];
-            finish(u, m0 + 16 * h);
+            finish.template operator()<sizeof(E) == 1>(u, m0 + 16 * h);
           }
         }
       }
