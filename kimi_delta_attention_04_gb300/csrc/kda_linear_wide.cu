@@ -9,9 +9,9 @@
 //
 // Each CTA stages 128 rows of x and NT / CTAS rows of w per 128-byte block of K, as
 // many stages as 200 KB hold (6 at NT = 256, up to 12: a load takes 3000 cycles under
-// way, and narrow tiles use a stage up in a fraction of the 512 of a wide one); in a pair an operand byte that reaches shared memory feeds twice the
-// products of a tile that one SM works on alone, and the leader CTA issues the MMAs
-// for both. CTA c's tensor memory holds tokens 128 c .. 128 c + 127 (lanes) of all NT
+// way, and narrow tiles use a stage up in a fraction of the 512 of a wide one); in a
+// pair an operand byte that reaches shared memory feeds twice the products of a tile
+// that one SM works on alone, and the leader CTA issues the MMAs for both. CTA c's tensor memory holds tokens 128 c .. 128 c + 127 (lanes) of all NT
 // outputs (columns), twice: while the epilogue warps read one accumulator the next
 // tile's products fill the other.
 //
@@ -19,9 +19,10 @@
 // 4096 -> 4096 e4m3 with bias, silu and residual at 3.3 (83 us), 256 x 4096 -> 12288 at
 // 25 us, where loads bring each SM about 45 bytes a cycle.
 //
-// Roles: warps 0-7 the epilogue (lane quarter w % 4, alternate blocks of 32 columns),
-// warp 8 issues the MMAs (leader only), warps 9 and 10 the TMA loads of x and of w for
-// their own CTA, counted on the leader's barrier.
+// Roles: warps 0-11 the epilogue (lane quarter w % 4, every third block of 32 columns;
+// with eight warps gelu on 4691 x 312 -> 8608 took 57 us instead of 54), warp 12 issues
+// the MMAs (leader only), warps 13 and 14 the TMA loads of x and of w for their own
+// CTA, counted on the leader's barrier.
 #include "kda_linear.cuh"
 
 namespace kda {
@@ -33,7 +34,8 @@ constexpr int kRows = 128;       // tokens of a CTA
 constexpr int kMaxN = 256;       // outputs of a tile, at most
 constexpr int kMaxStages = 12;
 constexpr size_t kRingBytes = 6 * 32768;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 12;
+constexpr int kParts = kEpiWarps / 4;  // warps that share a lane quarter
 constexpr int kWideThreads = 32 * (kEpiWarps + 3);
 constexpr uint32_t kXBytes = kRows * kKBytes;
 constexpr uint32_t kCols = 512;  // two accumulators of 256 columns
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (!ok) sm.failed = 1;
     }
   } else {
-    const int quarter = warp & 3, half = warp >> 2;
+    const int quarter = warp & 3, part = warp >> 2;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     float* staged = reinterpret_cast<float*>(ring + stages * stage) + warp * 16 * kStageCols;
     const int chunks = (NT + 31) / 32;  // blocks of 32 columns (the last may be half)
@@ -370,17 +372,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // the residual into L2 while the products run: from HBM each of a warp's blocks
       // would wait 1.2 us for it after they are done
       if (p.residual && m0 + lane < p.M) {
-        for (int c = half; c < chunks; c += 2) {
+        for (int c = part; c < chunks; c += kParts) {
           const Y* r = static_cast<const Y*>(p.residual) + (m0 + lane) * p.ld_residual + n0 + 32 * c;
           if (n0 + 32 * c < end) asm volatile("prefetch.global.L2 [%0];" ::"l"(r));
         }
       }
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sm.acc_full[buf]), (k / 2) & 1, kLinearWaitNs));
       tc05::fence_after_sync();
-      for (int c = half; c < chunks; c += 2) {
+      for (int c = part; c < chunks; c += kParts) {
         float v[32];
         tc05::ld32_wait(lane_base + buf * kMaxN + 32 * c, v);
-        if (c + 2 >= chunks) {  // this warp has read its share: the next but one tile may start
+        if (c + kParts >= chunks) {  // this warp has read its share: the next but one tile may start
           tc05::fence_before_sync();
           __syncwarp();
           if (lane == 0) {
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
         }
       }
-      if (half >= chunks && lane == 0) {  // a tile of one block of columns: no share to read
+      if (part >= chunks && lane == 0) {  // a tile of one block of columns: no share to read
         if (CTAS == 1) mbar_arrive_local(&sm.acc_empty[buf]);
         else mbar_arrive_cluster(mapa_shared(smem_u32(&sm.acc_empty[buf]), 0));
       }
