@@ -133,18 +133,12 @@ struct Epilogue {
   }
 };
 
-template <int C>
-__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[C]);
-template <>
-__device__ __forceinline__ void tmem_load<16>(uint32_t addr, float (&v)[16]) {
+// 16 columns of this warp's 32 lanes of tensor memory.
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[16]) {
   uint32_t r[16];
   tc05::ld16_wait(addr, r);
 #pragma unroll
   for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-}
-template <>
-__device__ __forceinline__ void tmem_load<32>(uint32_t addr, float (&v)[32]) {
-  tc05::ld32_wait(addr, v);
 }
 
 }  // namespace linear
