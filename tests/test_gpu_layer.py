@@ -565,3 +565,37 @@ def test_layer_calls_on_a_side_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# --- sizes past 32 bits ---
+
+def test_layer_offsets_past_32_bits():
+    """More than 2^31 elements in each tensor: the last rows against the same rows alone."""
+    T, D, tail = 2 ** 19 + 1000, 4104, 64
+    x = torch.ones(1, T, D, dtype=BF, device="cuda")
+    gate = torch.zeros(1, T, D, dtype=BF, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    x[:, -tail:] = torch.randn(1, tail, D, generator=gen, device="cuda")
+    gate[:, -tail:] = torch.randn(1, tail, D, generator=gen, device="cuda")
+    how = dict(gate_mode="logits", complement=True)  # a = 1/2 of ones before the tail: the state there is 1
+    states = torch.empty(kda.chunk_count(1, T), D, device="cuda")
+    y, hT = kda.kda_scan_fwd(x, gate, h_chunks=states, **how)
+    one = torch.ones(1, D, device="cuda")
+    xt, gt = x[:, -tail:].contiguous(), gate[:, -tail:].contiguous()
+    states_t = torch.empty(kda.chunk_count(1, tail), D, device="cuda")
+    yt, hTt = kda.kda_scan_fwd(xt, gt, h0=one, h_chunks=states_t, **how)
+    # 64 tokens of decays <= 1 from the same state, composed in other groups
+    assert torch.allclose(hT, hTt, rtol=0, atol=64 * PER_TOKEN * E24 * 8)
+    assert torch.allclose(y[:, -tail:].float(), yt.float(), rtol=2 * half_step(BF), atol=1e-4)
+    dx, dg, _ = kda.kda_scan_bwd(x, gate, y, states, **how)
+    dxt, dgt, _ = kda.kda_scan_bwd(xt, gt, y[:, -tail:].contiguous(), states_t, **how)
+    assert torch.allclose(dx[:, -tail:].float(), dxt.float(), rtol=2 * half_step(BF), atol=1e-4)
+    assert torch.allclose(dg[:, -tail:].float(), dgt.float(), rtol=2 * half_step(BF), atol=1e-4)
+    del y, dx, dg, states
+    w = torch.ones(D, device="cuda")
+    for a, b in zip(kda.kda_add_rmsnorm(x, w, eps=1e-6, residual=gate, out_dtype=E4),
+                    kda.kda_add_rmsnorm(xt, w, eps=1e-6, residual=gt, out_dtype=E4)):
+        assert torch.equal(a[:, -tail:].contiguous().view(torch.uint8), b.view(torch.uint8))
+    wide = torch.randn(24, D, generator=gen, device="cuda").to(BF)
+    # (the same 24 outputs of a token, whatever its place: one order of sums)
+    assert torch.equal(kda.kda_linear(x, wide)[:, -200:], kda.kda_linear(x[:, -200:], wide))
