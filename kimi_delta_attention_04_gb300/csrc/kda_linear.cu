@@ -15,7 +15,7 @@
 // over the operand costs less than loads that shift every row on its way into every
 // tile (777 x 1001 -> 1111: 27 us in the best such form).
 //
-// Few tiles (small M) leave most SMs without work, so a cluster of S CTAs splits
+// Few tiles (few tokens, or few outputs and a long K) leave most SMs without work, so a cluster of S CTAs splits
 // K of one tile: each sums its share, puts it into its own shared memory, and
 // finishes 1/S of the tokens from all S (distributed shared memory), in the
 // order of the ranks, so results do not vary from run to run. 16 x 4096 -> 4096 e4m3
@@ -195,6 +195,14 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// CTAs that share a tile's K: as many as still fit the SMs (two on each), with four
+// blocks of K or more for each.
+int split_of(long long tiles, long long blocks, int tokens) {
+  int S = 1;
+  while (S < kMaxSplit && 2 * S <= tokens && tiles * S * 2 <= 2 * 152 && blocks >= 2 * S * 4) S *= 2;
+  return S;
+}
+
 template <typename E, typename Y, int TOK>
 cudaError_t launch_tile(const kda_linear_args& a, cudaStream_t s) {
   constexpr size_t stage = (kOut + TOK) * kKBytes;
@@ -205,10 +213,7 @@ cudaError_t launch_tile(const kda_linear_args& a, cudaStream_t s) {
   constexpr int kFit = static_cast<int>(100 * 1024 / stage);
   constexpr int stages = kFit < kMaxStages ? kFit : kMaxStages;
   static_assert(stages * stage >= TOK * kOut * sizeof(float), "the ring holds a CTA's sums");
-  // split K while the CTAs still fit the SMs (two on each) and each keeps four blocks of K
-  const long long blocks = (a.K + EPB - 1) / EPB;
-  int S = 1;
-  while (S < kMaxSplit && 2 * S <= TOK && gx * gy * S * 2 <= 2 * 152 && blocks >= 2 * S * 4) S *= 2;
+  const int S = split_of(gx * gy, (a.K + EPB - 1) / EPB, TOK);
   CUtensorMap wmap, xmap;
   if (!encode_rows(&wmap, a.w, sizeof(E), a.K, a.N, a.ldw, kOut) || !encode_rows(&xmap, a.x, sizeof(E), a.K, a.M, a.ldx, TOK))
     return cudaErrorInvalidValue;
@@ -235,6 +240,17 @@ cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
   if (a.M <= 16) return launch_tile<E, Y, 16>(a, s);
   if (a.M <= 32) return launch_tile<E, Y, 32>(a, s);
   if (a.M <= 64) return launch_tile<E, Y, 64>(a, s);
+  // More tokens: whole K on tiles that share it between few SMs' loads, or, where a
+  // long K meets few tiles, K split over clusters. In units of one block of K on the
+  // wide kernel (0.23 us): a round there costs its blocks and 17, here a CTA's share
+  // of the blocks, 1.5 each and slowed by its neighbours, and 40 for the cluster's
+  // sums. 128 x 4096 -> 4096 bf16: 18.6 us wide, 14.6 split; 256 x 4096 -> 512: 19.5
+  // and 10.7; e4m3 (half the blocks) 128 x 4096 -> 4096: 11.8 and 13.5.
+  const long long blocks = (static_cast<long long>(a.K) * sizeof(E) + kKBytes - 1) / kKBytes;
+  const long long tiles = (static_cast<long long>(a.N) + kOut - 1) / kOut * ((static_cast<long long>(a.M) + 127) / 128);
+  const int S = split_of(tiles, blocks, 128);
+  const double crowd = static_cast<double>(tiles * S) / 152;
+  if (S > 1 && 40 + 1.5 * (crowd > 1 ? crowd : 1) * blocks / S < 17 + blocks) return launch_tile<E, Y, 128>(a, s);
   return launch_linear_wide(a, s);
 }
 

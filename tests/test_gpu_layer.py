@@ -242,9 +242,10 @@ def test_linear_repeats_bit_for_bit():
 
 @pytest.mark.parametrize("dtype", [BF, E4])
 @pytest.mark.parametrize("M,N,K", [(100, 1024, 512), (128, 30000, 80), (3000, 5008, 64), (2500, 4999, 144), (200, 12288, 48),
-                                   (70, 20000, 33), (1300, 2100, 65)])
+                                   (70, 20000, 33), (1300, 2100, 65), (130, 200, 6000), (70, 300, 8005)])
 def test_linear_many_tiles(dtype, M, N, K):
-    """Several tiles for each SM (both accumulators in turn), widths that divide nothing."""
+    """Several tiles for each SM (both accumulators in turn), widths that divide nothing,
+    and few tiles with a long K, split over clusters."""
     gen = torch.Generator().manual_seed(M + N + K)
     x, w, xs, ws = linear_inputs(gen, M, N, K, dtype)
     res = randn(gen, M, N, dtype=BF)
