@@ -218,6 +218,27 @@ def test_linear_workspace_of_the_caller():
         kda.kda_linear(x.cuda(), w.cuda(), workspace=ws[:256])
 
 
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("start", [0, 1, 2, 3, 5])
+@pytest.mark.parametrize("M,N,K", [(3, 5, 1), (9, 140, 2), (20, 130, 3), (70, 129, 61), (16, 300, 259), (130, 200, 1030)])
+def test_linear_rows_at_any_byte(dtype, start, M, N, K):
+    """Contiguous rows of any pitch from an operand that starts at any element."""
+    gen = torch.Generator().manual_seed(M * K + start)
+    x, w, xs, ws = linear_inputs(gen, M, N, K, dtype)
+
+    def moved(t):
+        buf = torch.full((t.numel() + start + 8,), float("nan"), device="cuda").to(t.dtype)
+        buf[start:start + t.numel()] = t.cuda().flatten()
+        return buf[start:start + t.numel()].view(t.shape)
+
+    cuda = lambda t: None if t is None else t.cuda()  # noqa: E731
+    cn = Canary()
+    y = cn.empty((M, N), BF, name="y")
+    kda.kda_linear(moved(x), moved(w), x_scale=cuda(xs), w_scale=cuda(ws), out=y)
+    cn.check()
+    check_linear(y, x, w, xs, ws)
+
+
 def test_linear_nan_and_inf_stay_in_their_rows():
     gen = torch.Generator().manual_seed(6)
     for M in (20, 300):
