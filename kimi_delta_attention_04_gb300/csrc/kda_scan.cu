@@ -77,11 +77,13 @@ __device__ __forceinline__ bool first_sequence(const kda_scan_args& p, Sequences
     q.chunk_base = static_cast<long long>(y) * ((p.T + kScanChunk - 1) / kScanChunk);
     return true;
   }
-  __shared__ unsigned long long base, total;  // chunks before the sequence, of all
+  // chunks before the sequence, of all (ends in order give at most T / 16 + N; the
+  // sums of others may wrap, but those are refused whatever they come to)
+  __shared__ unsigned base, total;
   __shared__ int chosen;
   if (tid == 0) base = total = 0;
   bool bad = false;
-  unsigned long long mine = 0, all = 0;
+  unsigned mine = 0, all = 0;
   int n;
   if (p.N <= kThreads) {
     for (int i = tid; i <= p.N; i += kThreads) scratch[i] = p.cu_seqlens[i];
@@ -117,10 +119,14 @@ __device__ __forceinline__ bool first_sequence(const kda_scan_args& p, Sequences
     __syncthreads();  // base and total are 0
   }
   if (p.h_chunks != nullptr) {
-    if (mine != 0) atomicAdd(&base, mine);
-    if (all != 0) atomicAdd(&total, all);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (tid % 32 == 0 && all != 0) {
+      atomicAdd(&base, mine);
+      atomicAdd(&total, all);
+    }
     __syncthreads();
-    bad |= total > static_cast<unsigned long long>(p.h_chunks_rows);
+    bad |= total > p.h_chunks_rows;
   }
   if (__syncthreads_or(bad)) {
     if (tid == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
