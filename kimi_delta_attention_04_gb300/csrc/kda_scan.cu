@@ -31,6 +31,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kBlockCh = 64;      // channels of a CTA
 constexpr int kMaxCluster = 8;
 constexpr int kStepThreads = 128;
+constexpr int kKeysAt = kThreads + 4;  // ints before the keys that order packed sequences: a multiple of 4
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // The decay, to about an fp32 step. Long memories multiply hundreds of decays near
@@ -61,8 +62,8 @@ __device__ __forceinline__ unsigned chunks_of(int s, int e, int T, bool& bad) {
 }
 
 // The first sequence of a CTA, checking the whole of cu_seqlens on the way (all
-// threads of the CTA call it; scratch: kThreads + 1 ints of shared memory that
-// nothing else uses meanwhile). Up to kThreads packed sequences take a CTA (or
+// threads of the CTA call it; scratch: kKeysAt + kThreads ints of shared memory
+// that nothing else uses meanwhile). Up to kThreads packed sequences take a CTA (or
 // cluster) each, longest first, so that no long one starts when the others are done
 // (16 sequences of 512 to 8192 tokens: 133 -> 116 us forward); more of them are
 // shared out in runs of neighbours, so that the check of all N is made once a CTA.
@@ -86,19 +87,30 @@ __device__ __forceinline__ bool first_sequence(const kda_scan_args& p, Sequences
   unsigned mine = 0, all = 0;
   int n;
   if (p.N <= kThreads) {
-    for (int i = tid; i <= p.N; i += kThreads) scratch[i] = p.cu_seqlens[i];
+    // one key orders by length (up to 2^24 chunks) and then by place, so that a
+    // sequence's rank is the number of larger keys: 256 sequences of 16 tokens,
+    // 1024 channels, 4096 CTAs: 65 us forward instead of 93 with lengths and places
+    // compared by themselves
+    unsigned* keys = reinterpret_cast<unsigned*>(scratch + kKeysAt);
+    unsigned key = 0;
+    if (tid < p.N) {
+      const int s = p.cu_seqlens[tid], e = p.cu_seqlens[tid + 1];
+      scratch[tid] = s;
+      if (tid == p.N - 1) scratch[p.N] = e;
+      all = chunks_of(s, e, p.T, bad);
+      bad |= (tid == 0 && s != 0) || (tid == p.N - 1 && e != p.T);
+      key = (all < 0xffffffu ? all : 0xffffffu) << 8 | (kThreads - 1 - tid);
+    }
+    keys[tid] = key;
     __syncthreads();
     if (tid < p.N) {
-      const int s = scratch[tid], e = scratch[tid + 1];
-      all = chunks_of(s, e, p.T, bad);
-      int rank = 0;  // longer ones, and equal ones before
-      for (int i = 0; i < p.N; ++i) {
-        const int len = scratch[i + 1] - scratch[i];
-        rank += len > e - s || (len == e - s && i < tid);
+      int rank = 0;
+      for (int i = 0; i < p.N; i += 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+        rank += (k.x > key) + (k.y > key) + (k.z > key) + (k.w > key);
       }
       if (rank == y) chosen = tid;
     }
-    bad |= tid == 0 && (scratch[0] != 0 || scratch[p.N] != p.T);
     __syncthreads();
     n = chosen;
     if (tid < n) mine = all;
@@ -340,6 +352,7 @@ struct __align__(128) ScanSmem {  // a map travels between CTAs as one word of 1
   uint64_t bar[2];              // all CTAs' maps of the advance have arrived
 };
 
+static_assert(sizeof(ScanSmem::warp) >= (kKeysAt + kThreads) * sizeof(int) && kThreads <= 256 && kKeysAt % 4 == 0, "");
 static_assert(sizeof(Map) == 16 && alignof(ScanSmem) % 16 == 0 && offsetof(ScanSmem, cta) % 16 == 0, "");
 
 // A lane's map into another CTA's shared memory, counted in bytes on its barrier.
