@@ -28,6 +28,7 @@ namespace {
 constexpr int kScanChunk = 16;    // tokens between the states of h_chunks, and of a warp's tile
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kShortWarps = 4;    // most warps of a CTA of the kernels for short sequences
 constexpr int kBlockCh = 64;      // channels of a CTA
 constexpr int kMaxCluster = 8;
 constexpr int kStepThreads = 128;
@@ -68,9 +69,10 @@ __device__ __forceinline__ unsigned chunks_of(int s, int e, int T, bool& bad) {
 // (16 sequences of 512 to 8192 tokens: 133 -> 116 us forward); more of them are
 // shared out in runs of neighbours, so that the check of all N is made once a CTA.
 // Returns false, after reporting, where the array is bad.
+template <int W>
 __device__ __forceinline__ bool first_sequence(const kda_scan_args& p, Sequences& q, int* scratch) {
   const int y = blockIdx.y, rows = gridDim.y, tid = threadIdx.x;
-  if (p.cu_seqlens == nullptr) {
+  if (W != kWarps || p.cu_seqlens == nullptr) {
     q.n = y;
     q.last = p.N - 1;
     q.start = y * p.T;
@@ -346,14 +348,21 @@ __device__ __forceinline__ Map then(const Map& first, const Map& second) {
 }
 __device__ __forceinline__ Map identity_map() { return Map{make_float2(1.f, 1.f), make_float2(0.f, 0.f)}; }
 
+// Warps of a CTA of a kernel made for up to W of them: kWarps always, or those launched.
+template <int W>
+__device__ __forceinline__ int cta_warps() {
+  return W == kWarps ? kWarps : blockDim.x >> 5;
+}
+
+template <int W>
 struct __align__(128) ScanSmem {  // a map travels between CTAs as one word of 16 bytes
-  Map warp[2][kWarps][32];      // the warps' maps of an advance, by parity of the advance
-  Map cta[2][kMaxCluster][32];  // the CTAs' maps
+  Map warp[2][W][32];           // the warps' maps of an advance, by parity of the advance
+  Map cta[2][W == kWarps ? kMaxCluster : 1][32];  // the CTAs' maps
   uint64_t bar[2];              // all CTAs' maps of the advance have arrived
 };
 
-static_assert(sizeof(ScanSmem::warp) >= (kKeysAt + kThreads) * sizeof(int) && kThreads <= 256 && kKeysAt % 4 == 0, "");
-static_assert(sizeof(Map) == 16 && alignof(ScanSmem) % 16 == 0 && offsetof(ScanSmem, cta) % 16 == 0, "");
+static_assert(sizeof(ScanSmem<kWarps>::warp) >= (kKeysAt + kThreads) * sizeof(int) && kThreads <= 256 && kKeysAt % 4 == 0, "");
+static_assert(sizeof(Map) == 16 && alignof(ScanSmem<kWarps>) % 16 == 0 && offsetof(ScanSmem<kWarps>, cta) % 16 == 0, "");
 
 // A lane's map into another CTA's shared memory, counted in bytes on its barrier.
 __device__ __forceinline__ void st_async_map(uint32_t addr, const Map& m, uint32_t bar) {
@@ -371,23 +380,24 @@ __device__ __forceinline__ void st_async_map(uint32_t addr, const Map& m, uint32
 // those of it. A wait for the other CTAs that runs out clears `ok`; the thread then
 // goes on through the same barriers without waiting for them again, so that all
 // threads still reach the end (with results that the error word disowns).
-__device__ __forceinline__ float2 enter_state(ScanSmem& sm, const Map& mine, float2& carry, bool& ok, int it, int S, int rank) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, parity = it & 1;
+template <int W>
+__device__ __forceinline__ float2 enter_state(ScanSmem<W>& sm, const Map& mine, float2& carry, bool& ok, int it, int S, int rank) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, parity = it & 1, warps = cta_warps<W>();
   sm.warp[parity][warp][lane] = mine;
   __syncthreads();
   Map before = identity_map();
 #pragma unroll
-  for (int w = 0; w < kWarps - 1; ++w)
+  for (int w = 0; w < W - 1; ++w)
     if (w < warp) before = then(before, sm.warp[parity][w][lane]);
-  if (S == 1) {
+  if (W != kWarps || S == 1) {
     Map total = then(before, mine);
-    for (int w = warp + 1; w < kWarps; ++w) total = then(total, sm.warp[parity][w][lane]);
+    for (int w = warp + 1; w < warps; ++w) total = then(total, sm.warp[parity][w][lane]);
     const float2 in = fma2(before.A, carry, before.B);
     carry = fma2(total.A, carry, total.B);
     return in;
   }
   const uint32_t bar = smem_u32(&sm.bar[parity]);
-  if (warp == kWarps - 1) {
+  if (warp == warps - 1) {
     const Map total = then(before, mine);
     if (lane == 0) mbar_arrive_expect_tx_local(&sm.bar[parity], S * 32 * sizeof(Map));
     const uint32_t at = smem_u32(&sm.cta[parity][rank][lane]);
@@ -405,11 +415,12 @@ __device__ __forceinline__ float2 enter_state(ScanSmem& sm, const Map& mine, flo
 }
 
 // Stages of the ring of tiles: what leaves two CTAs on an SM (about 100 KB each),
-// at least two.
-constexpr int stages_for(size_t stage) { return 100 * 1024 / (kWarps * stage) >= 3 ? 3 : 2; }
+// at least two; one for short sequences, which are one advance.
+constexpr int stages_for(size_t stage, int W) { return W != kWarps ? 1 : 100 * 1024 / (kWarps * stage) >= 3 ? 3 : 2; }
 
-__device__ __forceinline__ void scan_prologue(ScanSmem& sm, int S) {
-  if (S == 1) return;
+template <int W>
+__device__ __forceinline__ void scan_prologue(ScanSmem<W>& sm, int S) {
+  if (W != kWarps || S == 1) return;
   if (threadIdx.x == 0) {
     mbar_init(&sm.bar[0], 1);
     mbar_init(&sm.bar[1], 1);
@@ -418,14 +429,16 @@ __device__ __forceinline__ void scan_prologue(ScanSmem& sm, int S) {
   cluster_sync_all();  // every CTA of the cluster runs before its shared memory is written
 }
 
-// Forward. Grid (S * channel blocks, sequences), cluster (S, 1, 1).
-template <typename X, typename G, int ACC>
-__global__ void __launch_bounds__(kThreads, 2) kda_scan_fwd_kernel(const kda_scan_args p, int S) {
+// Forward. Grid (S * channel blocks, sequences), cluster (S, 1, 1). W is kWarps, or
+// kShortWarps for batches of equal sequences of up to that many chunks, with as many
+// warps as they have chunks and S = 1.
+template <typename X, typename G, int ACC, int W>
+__global__ void __launch_bounds__(32 * W, 2 * kWarps / W) kda_scan_fwd_kernel(const kda_scan_args p, int S) {
   extern __shared__ __align__(128) unsigned char ring[];
-  __shared__ ScanSmem sm;
+  __shared__ ScanSmem<W> sm;
   constexpr size_t kStage = tile_bytes<X>() + tile_bytes<G>();  // of one warp
-  constexpr int kStages = stages_for(kStage);
-  const int warp = threadIdx.x >> 5, rank = blockIdx.x % S, advance = S * kWarps * kScanChunk;
+  constexpr int kStages = stages_for(kStage, W);
+  const int warp = threadIdx.x >> 5, rank = blockIdx.x % S, warps = cta_warps<W>(), advance = S * warps * kScanChunk;
   const Lane l = lane_channels<ACC>(blockIdx.x / S * kBlockCh, p.D);
   const bool comp = p.flags & KDA_SCAN_FLAG_COMPLEMENT;
   unsigned char* mine_ring = ring + warp * kStages * kStage;
@@ -433,13 +446,13 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_fwd_kernel(const kda_sca
   int it = 0;
   bool ok = true;
   Sequences pos;
-  bool more = first_sequence(p, pos, reinterpret_cast<int*>(sm.warp));  // (the same answer in every CTA)
+  bool more = first_sequence<W>(p, pos, reinterpret_cast<int*>(sm.warp));  // (the same answer in every CTA)
   for (; more; more = next_sequence(p, pos)) {
     const int len = pos.end - pos.start;
     // the tiles of advance j, whose first token for this warp is first(j)
     auto tile_x = [&](int slot) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + slot * kStage)}; };
     auto tile_g = [&](int slot) { return Tile<G, ACC>{reinterpret_cast<Raw2<G>*>(mine_ring + slot * kStage + tile_bytes<X>())}; };
-    auto first = [&](int j) { return j * advance + (rank * kWarps + warp) * kScanChunk; };
+    auto first = [&](int j) { return j * advance + (rank * warps + warp) * kScanChunk; };
     auto fetch = [&](int j, int slot) {
       const int i0 = first(j);
       if (i0 < len) {
@@ -505,14 +518,14 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_fwd_kernel(const kda_sca
 // Backward: the same over the chunks from the last to the first, with the map of
 // d (the gradient of a state) over a chunk; the states within a chunk come from
 // h_chunks, so the forward direction needs no exchange.
-template <typename X, typename G, int ACC>
-__global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_scan_bwd_args q, int S) {
+template <typename X, typename G, int ACC, int W>
+__global__ void __launch_bounds__(32 * W, 2 * kWarps / W) kda_scan_bwd_kernel(const kda_scan_bwd_args q, int S) {
   extern __shared__ __align__(128) unsigned char ring[];
-  __shared__ ScanSmem sm;
+  __shared__ ScanSmem<W> sm;
   constexpr size_t kStage = 2 * tile_bytes<X>() + tile_bytes<G>();
-  constexpr int kStages = stages_for(kStage);
+  constexpr int kStages = stages_for(kStage, W);
   const kda_scan_args& p = q.fwd;
-  const int warp = threadIdx.x >> 5, rank = blockIdx.x % S;
+  const int warp = threadIdx.x >> 5, rank = blockIdx.x % S, warps = cta_warps<W>();
   const Lane l = lane_channels<ACC>(blockIdx.x / S * kBlockCh, p.D);
   const bool comp = p.flags & KDA_SCAN_FLAG_COMPLEMENT, logits = p.gate_mode == KDA_SCAN_LOGITS;
   unsigned char* mine_ring = ring + warp * kStages * kStage;
@@ -520,14 +533,14 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_sca
   int it = 0;
   bool ok = true;
   Sequences pos;
-  bool more = first_sequence(p, pos, reinterpret_cast<int*>(sm.warp));
+  bool more = first_sequence<W>(p, pos, reinterpret_cast<int*>(sm.warp));
   for (; more; more = next_sequence(p, pos)) {
     const int len = pos.end - pos.start, chunks = (len + kScanChunk - 1) / kScanChunk;
     auto tile_x = [&](int slot) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + slot * kStage)}; };
     auto tile_d = [&](int slot) { return Tile<X, ACC>{reinterpret_cast<Raw2<X>*>(mine_ring + slot * kStage + tile_bytes<X>())}; };
     auto tile_g = [&](int slot) { return Tile<G, ACC>{reinterpret_cast<Raw2<G>*>(mine_ring + slot * kStage + 2 * tile_bytes<X>())}; };
     // this warp's chunk of advance j (negative: none left)
-    auto chunk_of = [&](int j) { return chunks - 1 - ((j * S + rank) * kWarps + warp); };
+    auto chunk_of = [&](int j) { return chunks - 1 - ((j * S + rank) * warps + warp); };
     auto fetch = [&](int j, int slot) {
       const int k = chunk_of(j);
       if (k >= 0) {
@@ -546,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_bwd_kernel(const kda_sca
     float2 carry = load_state(q.dhT, pos.n, p.D, l), next_h = chunk_state(0);
     for (int j = 0; j < kStages - 1; ++j) fetch(j, j);
     int slot = 0;  // of advance j; its stage before is the one to fill
-    for (int j = 0; j * S * kWarps < chunks; ++j, ++it, slot = slot + 1 == kStages ? 0 : slot + 1) {
+    for (int j = 0; j * S * warps < chunks; ++j, ++it, slot = slot + 1 == kStages ? 0 : slot + 1) {
       const int k = chunk_of(j), m = k < 0 ? 0 : len - k * kScanChunk;
       float2 h = next_h;
       next_h = chunk_state(j + 1);
@@ -668,14 +681,15 @@ struct Instance {
   std::atomic<int> resident[kMaxCluster + 1] = {};
 };
 
-template <typename Args>
-cudaError_t launch_clusters(void (*kernel)(Args, int), Instance& inst, size_t smem, const Args& a, const kda_scan_args& f,
+template <int W, typename Args>
+cudaError_t launch_clusters(void (*kernel)(Args, int), Instance& inst, size_t warp_smem, const Args& a, const kda_scan_args& f,
                             cudaStream_t s) {
-  cudaError_t e = set_smem_limit_once(kernel, smem, inst.smem_set);
+  cudaError_t e = set_smem_limit_once(kernel, W * warp_smem, inst.smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  const int warps = W == kWarps ? kWarps : std::max(1, (f.T + kScanChunk - 1) / kScanChunk);
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = warps * warp_smem;
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -713,27 +727,38 @@ cudaError_t launch_clusters(void (*kernel)(Args, int), Instance& inst, size_t sm
   return cudaLaunchKernelEx(&cfg, kernel, a, S);
 }
 
-template <typename X, typename G, int ACC>
-cudaError_t launch_fwd(const kda_scan_args& a, cudaStream_t s) {
+// Equal sequences of up to kShortWarps chunks get a warp for each and one stage of
+// tiles, so that an SM holds many of them: 256 of 16 tokens, 1024 channels: 9 us
+// forward and 11 backward, 32 and 68 with the eight warps and the ring that long ones
+// need. How short the sequences of a packed batch are only the GPU knows.
+inline bool short_sequences(const kda_scan_args& a) { return !a.cu_seqlens && a.T <= kShortWarps * kScanChunk; }
+
+template <typename X, typename G, int ACC, int W>
+cudaError_t launch_warps(const kda_scan_args& a, cudaStream_t s) {
   static Instance inst;
   constexpr size_t stage = tile_bytes<X>() + tile_bytes<G>();
-  return launch_clusters(kda_scan_fwd_kernel<X, G, ACC>, inst, stages_for(stage) * kWarps * stage, a, a, s);
+  return launch_clusters<W>(kda_scan_fwd_kernel<X, G, ACC, W>, inst, stages_for(stage, W) * stage, a, a, s);
 }
 
-template <typename X, typename G, int ACC>
-cudaError_t launch_bwd(const kda_scan_bwd_args& a, cudaStream_t s) {
+template <typename X, typename G, int ACC, int W>
+cudaError_t launch_warps(const kda_scan_bwd_args& a, cudaStream_t s) {
   static Instance inst;
   constexpr size_t stage = 2 * tile_bytes<X>() + tile_bytes<G>();
-  return launch_clusters(kda_scan_bwd_kernel<X, G, ACC>, inst, stages_for(stage) * kWarps * stage, a, a.fwd, s);
+  return launch_clusters<W>(kda_scan_bwd_kernel<X, G, ACC, W>, inst, stages_for(stage, W) * stage, a, a.fwd, s);
 }
 
-template <typename X, typename G>
-cudaError_t launch_any(const kda_scan_args& a, int acc, cudaStream_t s) {
-  return acc == kWide ? launch_fwd<X, G, kWide>(a, s) : acc == kPair ? launch_fwd<X, G, kPair>(a, s) : launch_fwd<X, G, kSingle>(a, s);
+inline const kda_scan_args& fwd_of(const kda_scan_args& a) { return a; }
+inline const kda_scan_args& fwd_of(const kda_scan_bwd_args& a) { return a.fwd; }
+
+template <typename X, typename G, int ACC, typename Args>
+cudaError_t launch_acc(const Args& a, cudaStream_t s) {
+  return short_sequences(fwd_of(a)) ? launch_warps<X, G, ACC, kShortWarps>(a, s) : launch_warps<X, G, ACC, kWarps>(a, s);
 }
-template <typename X, typename G>
-cudaError_t launch_any(const kda_scan_bwd_args& a, int acc, cudaStream_t s) {
-  return acc == kWide ? launch_bwd<X, G, kWide>(a, s) : acc == kPair ? launch_bwd<X, G, kPair>(a, s) : launch_bwd<X, G, kSingle>(a, s);
+template <typename X, typename G, typename Args>
+cudaError_t launch_any(const Args& a, int acc, cudaStream_t s) {
+  return acc == kWide   ? launch_acc<X, G, kWide>(a, s)
+         : acc == kPair ? launch_acc<X, G, kPair>(a, s)
+                        : launch_acc<X, G, kSingle>(a, s);
 }
 
 // The instance for a call's types: x bf16 with a bf16 or fp32 gate, or both fp32.

@@ -409,6 +409,27 @@ def test_scan_many_sequences(N, D):
     check_scan_grad(dx, dg, dh0, x, gate, dy, "logits", False, h0, dhT, cu)
 
 
+@pytest.mark.parametrize("dtype,gate_dtype", TYPES)
+@pytest.mark.parametrize("D", [33, 66, 72])
+@pytest.mark.parametrize("T", [1, 16, 17, 31, 33, 48, 63, 64, 65, 128, 129])
+def test_scan_short_sequences(T, D, dtype, gate_dtype):
+    """Lengths around those at which the number of warps and the kernel change."""
+    gen = torch.Generator().manual_seed(T * D)
+    N = 5
+    x, gate = scan_inputs(gen, N, T, D, dtype, gate_dtype, "logits")
+    h0, dhT, dy = randn(gen, N, D), randn(gen, N, D), randn(gen, N, T, D, dtype=dtype)
+    how = dict(gate_mode="logits", complement=True)
+    cn = Canary()
+    states = cn.empty((N * -(-T // 16), D), F32, name="states")
+    y, dx = cn.empty((N, T, D), dtype, name="y"), cn.empty((N, T, D), dtype, name="dx")
+    dg = cn.empty((N, T, D), gate_dtype, name="dgate")
+    _, hT = kda.kda_scan_fwd(x.cuda(), gate.cuda(), h0=h0.cuda(), h_chunks=states, y=y, **how)
+    _, _, dh0 = kda.kda_scan_bwd(x.cuda(), gate.cuda(), dy.cuda(), states, dhT=dhT.cuda(), dx=dx, dgate=dg, **how)
+    cn.check()
+    check_scan(y, hT, x, gate, "logits", True, h0)
+    check_scan_grad(dx, dg, dh0, x, gate, dy, "logits", True, h0, dhT)
+
+
 def test_scan_many_rows():
     """More sequences of a batch, and more single tokens, than a grid's second axis."""
     N, D = 65535 + 300, 4
