@@ -106,7 +106,8 @@ struct RmsNormCall {
 cudaError_t launch_add_rmsnorm(const kda_add_rmsnorm_args& a, cudaStream_t s);
 size_t linear_workspace_bytes(const kda_linear_args& a);  // aligned copies of operands that TMA cannot describe
 cudaError_t launch_linear(kda_linear_args a, void* workspace, cudaStream_t s);
-cudaError_t launch_linear_wide(const kda_linear_args& a, cudaStream_t s);  // many tokens, rows that TMA describes
+// many tokens, rows that TMA describes; after_copy: the launch before on the stream is the copy of an operand
+cudaError_t launch_linear_wide(const kda_linear_args& a, bool after_copy, cudaStream_t s);
 cudaError_t launch_scan_fwd(const kda_scan_args& a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const kda_scan_bwd_args& a, cudaStream_t s);
 cudaError_t launch_scan_step(const kda_scan_step_args& a, cudaStream_t s);

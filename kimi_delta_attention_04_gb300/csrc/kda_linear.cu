@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kThreads)
     }
   } else if (warp == 5) {
     if (lane == 0) {
+      wait_for_copy();
       bool ok = true;
       int i = 0;
       for (; i < nkb; ++i) {
@@ -204,7 +205,7 @@ int split_of(long long tiles, long long blocks, int tokens) {
 }
 
 template <typename E, typename Y, int TOK>
-cudaError_t launch_tile(const kda_linear_args& a, cudaStream_t s) {
+cudaError_t launch_tile(const kda_linear_args& a, bool after_copy, cudaStream_t s) {
   constexpr size_t stage = (kOut + TOK) * kKBytes;
   constexpr int EPB = kKBytes / sizeof(E);
   const long long gx = (static_cast<long long>(a.N) + kOut - 1) / kOut, gy = (static_cast<long long>(a.M) + TOK - 1) / TOK;
@@ -226,20 +227,16 @@ cudaError_t launch_tile(const kda_linear_args& a, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = S;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attrs[2];
+  set_attributes(cfg, attrs, S, after_copy);
   return cudaLaunchKernelEx(&cfg, kda_linear_kernel<E, Y, TOK>, a, wmap, xmap, S, stages);
 }
 
 template <typename E, typename Y>
-cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
-  if (a.M <= 16) return launch_tile<E, Y, 16>(a, s);
-  if (a.M <= 32) return launch_tile<E, Y, 32>(a, s);
-  if (a.M <= 64) return launch_tile<E, Y, 64>(a, s);
+cudaError_t launch(const kda_linear_args& a, bool after_copy, cudaStream_t s) {
+  if (a.M <= 16) return launch_tile<E, Y, 16>(a, after_copy, s);
+  if (a.M <= 32) return launch_tile<E, Y, 32>(a, after_copy, s);
+  if (a.M <= 64) return launch_tile<E, Y, 64>(a, after_copy, s);
   // More tokens: whole K on tiles that share it between few SMs' loads, or, where a
   // long K meets few tiles, K split over clusters. In units of one block of K on the
   // wide kernel (0.23 us): a round there costs its blocks and 17, here a CTA's share
@@ -250,8 +247,8 @@ cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
   const long long tiles = (static_cast<long long>(a.N) + kOut - 1) / kOut * ((static_cast<long long>(a.M) + 127) / 128);
   const int S = split_of(tiles, blocks, 128);
   const double crowd = static_cast<double>(tiles * S) / 152;
-  if (S > 1 && 40 + 1.5 * (crowd > 1 ? crowd : 1) * blocks / S < 17 + blocks) return launch_tile<E, Y, 128>(a, s);
-  return launch_linear_wide(a, s);
+  if (S > 1 && 40 + 1.5 * (crowd > 1 ? crowd : 1) * blocks / S < 17 + blocks) return launch_tile<E, Y, 128>(a, after_copy, s);
+  return launch_linear_wide(a, after_copy, s);
 }
 
 // ---- rows to a pitch that TMA describes ----
@@ -268,6 +265,7 @@ struct Repitch {
 // element. Bytes of the new pitch past the row are not written: no map reaches them.
 template <typename E>
 __global__ void __launch_bounds__(256) kda_linear_repitch_kernel(const Repitch x, const Repitch w) {
+  asm volatile("griddepcontrol.launch_dependents;");  // the product's CTAs set themselves up meanwhile
   const int lane = threadIdx.x & 31;
   const long long total = static_cast<long long>(x.rows) + w.rows;
   for (long long r = (blockIdx.x * 256LL + threadIdx.x) >> 5; r < total; r += gridDim.x * 8LL) {
@@ -313,7 +311,6 @@ size_t copy_bytes(const kda_linear_args& a, const void* p, long long rows, long 
 // Operands that need it into the workspace; `a` then refers to the copies.
 cudaError_t repitch(kda_linear_args& a, void* workspace, cudaStream_t s) {
   const size_t e = elem_of(a), pitch = pitch_of(a), xb = copy_bytes(a, a.x, a.M, a.ldx), wb = copy_bytes(a, a.w, a.N, a.ldw);
-  if (xb == 0 && wb == 0) return cudaSuccess;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   const long long bytes = static_cast<long long>(a.K) * e, dst_pitch = static_cast<long long>(pitch);
   const Repitch x = {static_cast<const unsigned char*>(a.x), ws, a.ldx * static_cast<long long>(e), dst_pitch, bytes, xb ? a.M : 0};
@@ -338,11 +335,12 @@ cudaError_t repitch(kda_linear_args& a, void* workspace, cudaStream_t s) {
 size_t linear_workspace_bytes(const kda_linear_args& a) { return copy_bytes(a, a.x, a.M, a.ldx) + copy_bytes(a, a.w, a.N, a.ldw); }
 
 cudaError_t launch_linear(kda_linear_args a, void* workspace, cudaStream_t s) {
-  const cudaError_t e = repitch(a, workspace, s);
+  const bool copied = linear_workspace_bytes(a) != 0;
+  const cudaError_t e = copied ? repitch(a, workspace, s) : cudaSuccess;
   if (e != cudaSuccess) return e;
   if (a.dtype == KDA_DTYPE_BF16)
-    return a.y_dtype == KDA_DTYPE_BF16 ? launch<uint16_t, __nv_bfloat16>(a, s) : launch<uint16_t, float>(a, s);
-  return a.y_dtype == KDA_DTYPE_BF16 ? launch<uint8_t, __nv_bfloat16>(a, s) : launch<uint8_t, float>(a, s);
+    return a.y_dtype == KDA_DTYPE_BF16 ? launch<uint16_t, __nv_bfloat16>(a, copied, s) : launch<uint16_t, float>(a, copied, s);
+  return a.y_dtype == KDA_DTYPE_BF16 ? launch<uint8_t, __nv_bfloat16>(a, copied, s) : launch<uint8_t, float>(a, copied, s);
 }
 
 }  // namespace kda

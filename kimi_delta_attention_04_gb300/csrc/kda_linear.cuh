@@ -37,6 +37,23 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// Until the copy of an operand, if the launch before was one, has ended and its writes
+// can be read.
+__device__ __forceinline__ void wait_for_copy() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Clusters of `cluster` CTAs; after the copy of an operand, a launch while the copy
+// still runs: barriers and tensor memory are set up meanwhile, and only the loads wait
+// (777 x 1001 -> 1111 bf16: 12.4 us instead of 13.4; 40 x 51 -> 30: 5.2 instead of 6.7).
+inline void set_attributes(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attrs)[2], int cluster, bool after_copy) {
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = cluster;
+  attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = after_copy ? 2 : 1;
+}
+
 // 1 / (1 + e^-v) from the special-function unit (ex2, rcp: a few units in the last
 // place of fp32); e^-v = inf gives 0.
 __device__ __forceinline__ float fast_sigmoid(float v) {

@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     // cycles a block, more than a narrow tile's products take.
     const bool of_x = warp == kEpiWarps + 1;
     if (lane == 0) {
+      wait_for_copy();
       bool ok = true;
       int loaded = 0, s = 0;  // blocks so far, stage
       uint32_t phase = 1;     // of the stage's previous use
@@ -439,7 +440,7 @@ bool rows_allow(const void* p, int64_t ld, int N, size_t elem, int64_t bytes) {
 }
 
 template <typename E, typename Y, int CTAS, int ACCESS>
-cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
+cudaError_t launch(const kda_linear_args& a, bool after_copy, cudaStream_t s) {
   constexpr int kUnits = 152 / CTAS;
   const long long mt = (static_cast<long long>(a.M) + CTAS * kRows - 1) / (CTAS * kRows);
   // (One CTA on a tile stages all of its outputs' rows: at most 128 of them.)
@@ -473,36 +474,32 @@ cudaError_t launch(const kda_linear_args& a, cudaStream_t s) {
   cfg.blockDim = dim3(kWideThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = CTAS;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attrs[2];
+  set_attributes(cfg, attrs, CTAS, after_copy);
   return cudaLaunchKernelEx(&cfg, kda_linear_wide_kernel<E, Y, CTAS, ACCESS>, a, wmap, xmap, static_cast<int>(mt), static_cast<int>(nt),
                             NT, stages);
 }
 
 template <typename E, typename Y, int CTAS>
-cudaError_t launch_access(const kda_linear_args& a, cudaStream_t s) {
+cudaError_t launch_access(const kda_linear_args& a, bool after_copy, cudaStream_t s) {
   auto allow = [&](int64_t bytes) {
     return rows_allow(a.y, a.ldy, a.N, sizeof(Y), bytes) && rows_allow(a.residual, a.ld_residual, a.N, sizeof(Y), bytes);
   };
-  if (allow(32)) return launch<E, Y, CTAS, kRows32>(a, s);
-  return allow(16) ? launch<E, Y, CTAS, kRows16>(a, s) : launch<E, Y, CTAS, kRowsAny>(a, s);
+  if (allow(32)) return launch<E, Y, CTAS, kRows32>(a, after_copy, s);
+  return allow(16) ? launch<E, Y, CTAS, kRows16>(a, after_copy, s) : launch<E, Y, CTAS, kRowsAny>(a, after_copy, s);
 }
 
 template <typename E, typename Y>
-cudaError_t launch_ctas(const kda_linear_args& a, cudaStream_t s) {
-  return a.M <= kRows ? launch_access<E, Y, 1>(a, s) : launch_access<E, Y, 2>(a, s);
+cudaError_t launch_ctas(const kda_linear_args& a, bool after_copy, cudaStream_t s) {
+  return a.M <= kRows ? launch_access<E, Y, 1>(a, after_copy, s) : launch_access<E, Y, 2>(a, after_copy, s);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_wide(const kda_linear_args& a, cudaStream_t s) {
+cudaError_t launch_linear_wide(const kda_linear_args& a, bool after_copy, cudaStream_t s) {
   if (a.dtype == KDA_DTYPE_BF16)
-    return a.y_dtype == KDA_DTYPE_BF16 ? launch_ctas<uint16_t, __nv_bfloat16>(a, s) : launch_ctas<uint16_t, float>(a, s);
-  return a.y_dtype == KDA_DTYPE_BF16 ? launch_ctas<uint8_t, __nv_bfloat16>(a, s) : launch_ctas<uint8_t, float>(a, s);
+    return a.y_dtype == KDA_DTYPE_BF16 ? launch_ctas<uint16_t, __nv_bfloat16>(a, after_copy, s) : launch_ctas<uint16_t, float>(a, after_copy, s);
+  return a.y_dtype == KDA_DTYPE_BF16 ? launch_ctas<uint8_t, __nv_bfloat16>(a, after_copy, s) : launch_ctas<uint8_t, float>(a, after_copy, s);
 }
 
 }  // namespace kda

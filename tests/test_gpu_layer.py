@@ -239,6 +239,26 @@ def test_linear_rows_at_any_byte(dtype, start, M, N, K):
     check_linear(y, x, w, xs, ws)
 
 
+@pytest.mark.parametrize("M,N,K", [(9, 140, 515), (300, 260, 129)])
+def test_linear_calls_in_turn_share_a_workspace(M, N, K):
+    """Copies of one call's operands after the products of the call before, eager and captured."""
+    gen = torch.Generator().manual_seed(M)
+    ops = [tuple(t.cuda() for t in (randn(gen, M, K, dtype=BF), randn(gen, N, K, dtype=BF))) for _ in range(4)]
+    alone = [kda.kda_linear(x, w) for x, w in ops]
+    scratch = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        got = [kda.kda_linear(x, w, workspace=scratch) for x, w in ops]
+        assert all(torch.equal(a, b) for a, b in zip(alone, got))
+    out = [torch.empty_like(y) for y in alone]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for (x, w), y in zip(ops, out):
+            kda.kda_linear(x, w, workspace=scratch, out=y)
+    for _ in range(20):
+        graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(alone, out))
+
+
 def test_linear_nan_and_inf_stay_in_their_rows():
     gen = torch.Generator().manual_seed(6)
     for M in (20, 300):
