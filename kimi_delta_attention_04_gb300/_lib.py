@@ -556,6 +556,14 @@ def _device_of(x):
     return x.get_device()
 
 
+_I32_MAX = 2 ** 31 - 1
+
+
+def _past_32_bits(**sizes):
+    """Refuses what the C structs' 32-bit counts would be assigned cut short."""
+    raise ValueError("sizes must fit 32 bits: " + ", ".join(f"{k} = {v}" for k, v in sizes.items() if v > _I32_MAX))
+
+
 def _refuse(t, name, dev, dtype, shape):
     """Says what is wrong with a tensor that is not as expected (_rows and _vec ask)."""
     if not isinstance(t, torch.Tensor):
@@ -670,6 +678,8 @@ def kda_add_rmsnorm(x, weight, *, eps, residual=None, residual_out=None, out=Non
     dev = _device_of(x)
     shape, dtype = x.shape, x.dtype
     lead, D = shape[:-1], shape[-1]
+    if D > _I32_MAX:
+        _past_32_bits(D=D)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out: expected {out_dtype}, got {out.dtype}")
     out_dtype = out.dtype if out is not None else (out_dtype or x.dtype)
@@ -707,7 +717,9 @@ def kda_linear(x, w, *, bias=None, activation="none", residual=None, x_scale=Non
     dtype, lead, K = x.dtype, x.shape[:-1], x.shape[-1]
     if w.dim() != 2:
         raise ValueError("w: expected [N, K]")
-    N = w.shape[0]
+    M, N = x.numel() // max(K, 1), w.shape[0]
+    if M > _I32_MAX or N > _I32_MAX or K > _I32_MAX:
+        _past_32_bits(M=M, N=N, K=K)
     shape = lead + (N,)
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out: expected {out_dtype}, got {out.dtype}")
@@ -715,7 +727,7 @@ def kda_linear(x, w, *, bias=None, activation="none", residual=None, x_scale=Non
     args = LinearArgs()
     args.x, args.ldx = _rows(x, "x", dev, dtype, x.shape)
     args.w, args.ldw = _rows(w, "w", dev, dtype, (N, K))
-    args.M, args.N, args.K = x.numel() // max(K, 1), N, K
+    args.M, args.N, args.K = M, N, K
     args.dtype, args.y_dtype = _code(dtype), _code(out_dtype)
     args.activation = KDA_ACTIVATIONS[activation]
     args.x_scale, args.w_scale = _vec(x_scale, "x_scale", dev, lead), _vec(w_scale, "w_scale", dev, (N,))
@@ -738,12 +750,14 @@ def _scan_args(x, gate, gate_mode, complement, h0, cu_seqlens, h_chunks, err, de
     if len(x.shape) != 3:
         raise ValueError("x: expected [B, T, D]")
     B, T, D = shape = x.shape
+    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    if B > _I32_MAX or T > _I32_MAX or D > _I32_MAX or N > _I32_MAX:
+        _past_32_bits(B=B, T=T, D=D, N=N)
     args = ScanArgs()
     args.x, args.x_stride = _rows(x, "x", dev, x.dtype, shape)
     args.gate, args.gate_stride = _rows(gate, "gate", dev, gate.dtype, shape)
     args.dtype, args.gate_dtype = _code(x.dtype), _code(gate.dtype)
-    args.B, args.T, args.D = B, T, D
-    args.N = N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    args.B, args.T, args.D, args.N = B, T, D, N
     args.gate_mode, args.flags = KDA_SCAN_GATES[gate_mode], KDA_SCAN_FLAG_COMPLEMENT if complement else 0
     args.h0 = _vec(h0, "h0", dev, (N, D))
     args.cu_seqlens = _vec(cu_seqlens, "cu_seqlens", dev, (N + 1,), torch.int32)
@@ -814,6 +828,8 @@ def kda_scan_step(x, gate, state_pool, indices, *, gate_mode="log", complement=F
         raise ValueError("x: expected [B, D]")
     B, D = shape = x.shape
     slots = state_pool.shape[0]
+    if B > _I32_MAX or D > _I32_MAX or slots > _I32_MAX:
+        _past_32_bits(B=B, D=D, slots=slots)
     args = ScanStepArgs()
     args.dtype, args.gate_dtype, args.B, args.D = _code(x.dtype), _code(gate.dtype), B, D
     args.num_slots, args.gate_mode = slots, KDA_SCAN_GATES[gate_mode]
