@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % S;
   const int n0 = blockIdx.x / S * kOut, m0 = blockIdx.y * TOK;
-  const int blocks = (p.K + EPB - 1) / EPB;
+  const int blocks = (p.K - 1) / EPB + 1;  // (K + EPB may pass 2^31)
   const int kb0 = static_cast<int>(static_cast<long long>(blocks) * rank / S);
   const int nkb = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / S) - kb0;
 
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncwarp();
 
   bool ok = true;
-  if (warp < 4) ok = mbar_wait_bounded(smem_u32(&sm.acc), 0, kLinearWaitNs);
+  if (warp < 4) ok = mbar_wait_bounded(smem_u32(&sm.acc), 0, tile_wait_ns(nkb));
   if (!ok) sm.failed = 1;
   tc05::fence_after_sync();
   const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
@@ -214,7 +214,7 @@ cudaError_t launch_tile(const kda_linear_args& a, bool after_copy, cudaStream_t 
   constexpr int kFit = static_cast<int>(100 * 1024 / stage);
   constexpr int stages = kFit < kMaxStages ? kFit : kMaxStages;
   static_assert(stages * stage >= TOK * kOut * sizeof(float), "the ring holds a CTA's sums");
-  const int S = split_of(gx * gy, (a.K + EPB - 1) / EPB, TOK);
+  const int S = split_of(gx * gy, (a.K - 1) / EPB + 1, TOK);
   CUtensorMap wmap, xmap;
   if (!encode_rows(&wmap, a.w, sizeof(E), a.K, a.N, a.ldw, kOut) || !encode_rows(&xmap, a.x, sizeof(E), a.K, a.M, a.ldx, TOK))
     return cudaErrorInvalidValue;

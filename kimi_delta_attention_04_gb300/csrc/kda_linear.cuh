@@ -15,6 +15,9 @@ constexpr int kOut = 128;       // outputs per CTA (tensor-memory lanes)
 constexpr int kKBytes = 128;    // bytes of K per block: one row of the swizzle atom
 constexpr uint64_t kLinearWaitNs = 2000000000ull;
 
+// The wait for a whole tile's sum: a block takes 0.2 to 0.4 us (K = 2^31 is 2^25 of them).
+__device__ __forceinline__ uint64_t tile_wait_ns(int blocks) { return kLinearWaitNs + 2000ull * blocks; }
+
 // One MMA of the 8-bit kind (e4m3 x e4m3, 32 values of K); its instruction
 // descriptor is kind::f16's with operand formats 0 (e4m3).
 __device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,

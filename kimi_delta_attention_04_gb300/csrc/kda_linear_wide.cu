@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = CTAS == 1 ? 0 : static_cast<int>(cluster_ctarank());
   const int unit = blockIdx.x / CTAS, units = gridDim.x / CTAS, tiles = mt * nt;
-  const int blocks = (p.K + EPB - 1) / EPB;
+  const int blocks = (p.K - 1) / EPB + 1;  // (K + EPB may pass 2^31)
 
   if (warp == kEpiWarps + 1 && lane == 0) {
     prefetch_map(&xmap);
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (n0 + 32 * c < end) asm volatile("prefetch.global.L2 [%0];" ::"l"(r));
         }
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sm.acc_full[buf]), (k / 2) & 1, kLinearWaitNs));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&sm.acc_full[buf]), (k / 2) & 1, tile_wait_ns(blocks)));
       tc05::fence_after_sync();
       for (int c = part; c < chunks; c += kParts) {
         float v[32];
@@ -449,13 +449,13 @@ cudaError_t launch(const kda_linear_args& a, bool after_copy, cudaStream_t s) {
   int NT = 0;
   long long best = 0;
   for (int w = CTAS == 1 ? kMaxN / 2 : kMaxN; w >= 32; w -= 16) {
-    const long long tiles = mt * ((a.N + w - 1) / w), cost = (tiles + kUnits - 1) / kUnits * (w + 24);
+    const long long tiles = mt * ((a.N - 1) / w + 1), cost = (tiles + kUnits - 1) / kUnits * (w + 24);
     if (NT == 0 || cost < best) {
       NT = w;
       best = cost;
     }
   }
-  const long long nt = (a.N + NT - 1) / NT;
+  const long long nt = (a.N - 1) / NT + 1;
   if (mt * nt > INT32_MAX / 2) return cudaErrorNotSupported;
   CUtensorMap wmap, xmap;
   if (!encode_rows(&wmap, a.w, sizeof(E), a.K, a.N, a.ldw, NT / CTAS) || !encode_rows(&xmap, a.x, sizeof(E), a.K, a.M, a.ldx, kRows))

@@ -125,10 +125,10 @@ __device__ __forceinline__ bool first_sequence(const kda_scan_args& p, Sequences
     q.last = static_cast<int>(static_cast<long long>(p.N) * (y + 1) / rows) - 1;
     q.start = p.cu_seqlens[n];
     q.end = p.cu_seqlens[n + 1];
-    for (int i = tid; i < p.N; i += kThreads) {
+    for (unsigned i = tid; i < static_cast<unsigned>(p.N); i += kThreads) {  // (N + kThreads may pass 2^31)
       const unsigned chunks = chunks_of(p.cu_seqlens[i], p.cu_seqlens[i + 1], p.T, bad);
       all += chunks;
-      if (i < n) mine += chunks;
+      if (i < static_cast<unsigned>(n)) mine += chunks;
     }
     bad |= tid == 0 && (p.cu_seqlens[0] != 0 || p.cu_seqlens[p.N] != p.T);
     __syncthreads();  // base and total are 0
@@ -627,8 +627,8 @@ __global__ void __launch_bounds__(32 * W, 2 * kWarps / W) kda_scan_bwd_kernel(co
 // the batch strided over the grid.
 template <typename X, typename G, int C>
 __global__ void __launch_bounds__(kStepThreads) kda_scan_step_kernel(const kda_scan_step_args p) {
-  const int c = (blockIdx.x * kStepThreads + threadIdx.x) * C;
-  if (c >= p.D) return;
+  const unsigned c = (blockIdx.x * kStepThreads + threadIdx.x) * C;  // (may pass 2^31)
+  if (c >= static_cast<unsigned>(p.D)) return;
   for (long long b = blockIdx.y; b < p.B; b += gridDim.y) {
     const int slot = p.indices[b];
     const bool live = slot >= 0 && slot < p.num_slots;
@@ -705,7 +705,7 @@ cudaError_t launch_clusters(void (*kernel)(Args, int), Instance& inst, size_t wa
   // lengths out (16 of 512 to 8192 tokens, 1000 channels: 250 us forward and backward
   // with clusters of 2, 260 with 4, 290 with 1).
   const long long blocks = (f.D + kBlockCh - 1) / kBlockCh, work = blocks * f.N;
-  const long long mean = f.cu_seqlens ? (f.T + f.N - 1) / f.N : f.T;
+  const long long mean = f.cu_seqlens ? (static_cast<long long>(f.T) + f.N - 1) / f.N : f.T;
   const int rounds = f.cu_seqlens && f.N > 1 ? 2 : 1;
   int S = kMaxCluster;
   for (; S > 1; --S) {
@@ -801,7 +801,7 @@ cudaError_t launch_step(const kda_scan_step_args& a, cudaStream_t s) {
   const bool four = a.D % 4 == 0 && fours(a.x, a.x_stride, sizeof(X)) && fours(a.gate, a.gate_stride, sizeof(G)) &&
                     fours(a.y, a.y_stride, sizeof(X)) && fours(a.state_in, 0, 4) && fours(a.state_out, 0, 4);
   const int per = kStepThreads * (four ? 4 : 1);
-  const dim3 grid(static_cast<unsigned>((a.D + per - 1) / per), static_cast<unsigned>(std::min(a.B, 65535)));
+  const dim3 grid(static_cast<unsigned>((a.D - 1) / per + 1), static_cast<unsigned>(std::min(a.B, 65535)));
   if (four) kda_scan_step_kernel<X, G, 4><<<grid, kStepThreads, 0, s>>>(a);
   else kda_scan_step_kernel<X, G, 1><<<grid, kStepThreads, 0, s>>>(a);
   return cudaGetLastError();
