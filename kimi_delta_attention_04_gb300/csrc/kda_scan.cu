@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(32 * W, 2 * kWarps / W) kda_scan_fwd_kernel(co
 #pragma unroll
       for (int i = 0; i < kScanChunk; ++i) {
         u[i] = tx.get(i);
-        if (comp) u[i] = make_float2(fmaf(-a[i].x, u[i].x, u[i].x), fmaf(-a[i].y, u[i].y, u[i].y));
+        if (comp) u[i] = mul2(make_float2(1.f - a[i].x, 1.f - a[i].y), u[i]);  // (x - a x would be NaN for an infinite x)
       }
       __syncwarp();  // the slots are free for the fetch of the next iteration
       Map mine = identity_map();
@@ -572,10 +572,10 @@ __global__ void __launch_bounds__(32 * W, 2 * kWarps / W) kda_scan_bwd_kernel(co
       decays(a, tile_g(slot), p.gate_mode);
       if (comp) {
 #pragma unroll
-        for (int i = 0; i < kScanChunk; ++i) {  // a h + (1 - a) x = x + a (h - x)
+        for (int i = 0; i < kScanChunk; ++i) {  // (x + a (h - x) would be NaN for an infinite x)
           const float2 xv = tx.get(i);
           w[i] = make_float2(h.x - xv.x, h.y - xv.y);
-          h = fma2(a[i], w[i], xv);
+          h = fma2(a[i], h, mul2(make_float2(1.f - a[i].x, 1.f - a[i].y), xv));
         }
       } else {
 #pragma unroll
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kStepThreads) kda_scan_step_kernel(const kda_s
 #pragma unroll
       for (int j = 0; j < C; ++j) {
         const float a = p.gate_mode == KDA_SCAN_LOG_DECAY ? decay_of<KDA_SCAN_LOG_DECAY>(f[j]) : decay_of<KDA_SCAN_LOGITS>(f[j]);
-        h[j] = fmaf(a, h[j], p.flags & KDA_SCAN_FLAG_COMPLEMENT ? fmaf(-a, u[j], u[j]) : u[j]);
+        h[j] = fmaf(a, h[j], p.flags & KDA_SCAN_FLAG_COMPLEMENT ? (1.f - a) * u[j] : u[j]);
       }
       if (C == 4) store4(p.state_out + at, h);
       else p.state_out[at] = h[0];

@@ -56,3 +56,49 @@ def test_scan_step_channels_next_to_2_31(D):
     y = kda.kda_scan_step(x, gate, pool, torch.zeros(1, dtype=torch.int32, device="cuda"))
     assert y[0, 0] == 2 and y[0, D - 1] == 8 and pool[0, 0] == 2 and pool[0, D - 1] == 8
     assert torch.count_nonzero(y) == 2
+
+
+# --- infinite inputs ---
+
+def infinite_inputs(mode):
+    gen = torch.Generator().manual_seed(21)
+    T, D = 12, 70
+    x, f = randn(gen, 1, T, D), randn(gen, 1, T, D)
+    gate = f if mode == "logits" else torch.nn.functional.logsigmoid(f)
+    x[0, 3, 5], x[0, 7, 6], x[0, 0, 66], x[0, 11, 69] = float("inf"), float("-inf"), float("-inf"), float("inf")
+    return x, gate, randn(gen, 1, D), randn(gen, 1, T, D), randn(gen, 1, D)
+
+
+@pytest.mark.parametrize("mode", ["log", "logits"])
+def test_scan_infinite_inputs(mode):
+    """An infinite x under the weight 1 - a: the states are infinite from there on, its channel alone."""
+    x, gate, h0, dy, dhT = infinite_inputs(mode)
+    T, D = x.shape[1:]
+    how = dict(gate_mode=mode, complement=True)
+    states = torch.empty(kda.chunk_count(1, T), D, device="cuda")
+    y, hT = kda.kda_scan_fwd(x.cuda(), gate.cuda(), h0=h0.cuda(), h_chunks=states, **how)
+    ref, last, _ = lo.scan(np64(x[0]), np64(gate[0]), h0=np64(h0[0]), **how)
+    assert np.isinf(ref[3:, 5]).all() and np.isfinite(ref[:3, 5]).all() and np.isinf(last).sum() == 4
+    # 12 tokens of weights <= 1 on values below 6: at most 12 roundings of 12 steps each
+    same_or_within(y[0], ref, 12 * 12 * E24 * 6)
+    same_or_within(hT[0], last, 12 * 12 * E24 * 6)
+    dx, dg, dh0 = kda.kda_scan_bwd(x.cuda(), gate.cuda(), dy.cuda(), states, dhT=dhT.cuda(), **how)
+    rx, rg, r0 = lo.scan_grad(np64(x[0]), np64(gate[0]), np64(dy[0]), h0=np64(h0[0]), dhT=np64(dhT[0]), **how)
+    same_or_within(dx[0], rx, 12 * 12 * E24 * 6)
+    same_or_within(dh0[0], r0, 12 * 12 * E24 * 6)
+    same_or_within(dg[0], rg, 2 * 12 * 12 * E24 * 36)
+
+
+@pytest.mark.parametrize("mode", ["log", "logits"])
+def test_scan_step_infinite_inputs(mode):
+    x, gate, h0, _, _ = infinite_inputs(mode)
+    pool = h0.cuda()
+    idx = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for D in (70, 68):  # one channel an access, and four
+        pool = h0[:, :D].contiguous().cuda()
+        y = kda.kda_scan_step(x[0, 3:4, :D].contiguous().cuda(), gate[0, 3:4, :D].contiguous().cuda(), pool, idx,
+                              gate_mode=mode, complement=True)
+        ref, _, _ = lo.scan(np64(x[0, 3:4, :D]), np64(gate[0, 3:4, :D]), gate_mode=mode, complement=True, h0=np64(h0[0, :D]))
+        assert np.isinf(ref).sum() == 1
+        same_or_within(y, ref, 12 * E24 * 6)
+        same_or_within(pool, ref, 12 * E24 * 6)
