@@ -447,6 +447,8 @@ typedef enum {
  *                          are meant to be <= 0 (-inf resets the state): products of
  *                          16 and more positive ones are formed on the way and may
  *                          leave fp32's range
+ *                          (an infinite state stays infinite under decays above 0, as
+ *                          the definition has it, and is NaN after one of 0)
  *   h0, hT      [N, D]     fp32, either may be NULL
  *   cu_seqlens  [N + 1]    as for kda_chunk_fwd (N = B without it)
  *   h_chunks    [chunks, D] fp32 or NULL: the state entering every 16-token

@@ -349,6 +349,33 @@ __device__ __forceinline__ Map then(const Map& first, const Map& second) {
 }
 __device__ __forceinline__ Map identity_map() { return Map{make_float2(1.f, 1.f), make_float2(0.f, 0.f)}; }
 
+// A state may be infinite, and then a product of decays that has rounded to 0 makes it
+// NaN where one token after the other leaves it infinite. So maps that are handed on
+// have A = 0 only where one of their decays is 0: other products are held at the
+// smallest fp32 (which adds 2^-149 of a state at most, as much as rounding there does).
+// The factors are looked at again only where it matters, so the cost is a comparison.
+constexpr float kSmallest = 1.40129846e-45f;
+__device__ __forceinline__ void keep_nonzero(Map& map, const float2 (&a)[kScanChunk], int m) {
+  if (map.A.x != 0.f && map.A.y != 0.f) return;
+  float2 least = make_float2(kSmallest, kSmallest);
+#pragma unroll
+  for (int i = 0; i < kScanChunk; ++i)
+    if (i < m) least = make_float2(fminf(least.x, a[i].x), fminf(least.y, a[i].y));
+  map.A = make_float2(fmaxf(map.A.x, least.x), fmaxf(map.A.y, least.y));
+}
+// The same for the product of the first n warps' maps.
+__device__ __forceinline__ float2 nonzero_product(float2 A, const Map (*maps)[32], int n) {
+  float2 least = make_float2(kSmallest, kSmallest);
+  const int lane = threadIdx.x & 31;
+  for (int w = 0; w < n; ++w) least = make_float2(fminf(least.x, maps[w][lane].A.x), fminf(least.y, maps[w][lane].A.y));
+  return make_float2(fmaxf(A.x, least.x), fmaxf(A.y, least.y));
+}
+__device__ __forceinline__ bool any_infinite(float2 h) { return fabsf(h.x) + fabsf(h.y) > 3.40282347e+38f; }
+// A h + B where A is the product of the first n warps' maps.
+__device__ __forceinline__ float2 apply(const Map& map, float2 h, const Map (*maps)[32], int n) {
+  return fma2(any_infinite(h) ? nonzero_product(map.A, maps, n) : map.A, h, map.B);
+}
+
 // Warps of a CTA of a kernel made for up to W of them: kWarps always, or those launched.
 template <int W>
 __device__ __forceinline__ int cta_warps() {
@@ -393,13 +420,14 @@ __device__ __forceinline__ float2 enter_state(ScanSmem<W>& sm, const Map& mine, 
   if (W != kWarps || S == 1) {
     Map total = then(before, mine);
     for (int w = warp + 1; w < warps; ++w) total = then(total, sm.warp[parity][w][lane]);
-    const float2 in = fma2(before.A, carry, before.B);
-    carry = fma2(total.A, carry, total.B);
+    const float2 in = apply(before, carry, sm.warp[parity], warp);
+    carry = apply(total, carry, sm.warp[parity], warps);
     return in;
   }
   const uint32_t bar = smem_u32(&sm.bar[parity]);
   if (warp == warps - 1) {
-    const Map total = then(before, mine);
+    Map total = then(before, mine);
+    if (total.A.x == 0.f || total.A.y == 0.f) total.A = nonzero_product(total.A, sm.warp[parity], warps);
     if (lane == 0) mbar_arrive_expect_tx_local(&sm.bar[parity], S * 32 * sizeof(Map));
     const uint32_t at = smem_u32(&sm.cta[parity][rank][lane]);
     for (int r = 0; r < S; ++r) st_async_map(mapa_shared(at, r), total, mapa_shared(bar, r));
@@ -412,7 +440,7 @@ __device__ __forceinline__ float2 enter_state(ScanSmem<W>& sm, const Map& mine, 
     h = fma2(m.A, h, m.B);
   }
   carry = h;
-  return fma2(before.A, start, before.B);
+  return apply(before, start, sm.warp[parity], warp);
 }
 
 // Stages of the ring of tiles: what leaves two CTAs on an SM (about 100 KB each),
@@ -489,6 +517,7 @@ __global__ void __launch_bounds__(32 * W, 2 * kWarps / W) kda_scan_fwd_kernel(co
         for (int i = 0; i < kScanChunk; ++i)
           if (i < m) mine = then(mine, Map{a[i], u[i]});
       }
+      keep_nonzero(mine, a, m);
       float2 h = enter_state(sm, mine, carry, ok, it, S, rank);
       if (m > 0 && p.h_chunks) store_state(p.h_chunks, pos.chunk_base + i0 / kScanChunk, p.D, l, h);
       X* y = static_cast<X*>(p.y) + (pos.start + static_cast<long long>(i0)) * p.y_stride;
@@ -593,6 +622,7 @@ __global__ void __launch_bounds__(32 * W, 2 * kWarps / W) kda_scan_bwd_kernel(co
         for (int i = kScanChunk - 1; i >= 0; --i)
           if (i < m) mine = then(mine, Map{a[i], mul2(a[i], td.get(i))});
       }
+      keep_nonzero(mine, a, m);
       float2 d = enter_state(sm, mine, carry, ok, it, S, rank);
       const long long last = pos.start + static_cast<long long>(k) * kScanChunk + kScanChunk - 1;
       X* dx = static_cast<X*>(q.dx) + last * q.dx_stride;

@@ -102,3 +102,53 @@ def test_scan_step_infinite_inputs(mode):
         assert np.isinf(ref).sum() == 1
         same_or_within(y, ref, 12 * E24 * 6)
         same_or_within(pool, ref, 12 * E24 * 6)
+
+
+# --- infinite states over products of decays that leave fp32's range ---
+
+@pytest.mark.parametrize("comp", [False, True])
+@pytest.mark.parametrize("T", [40, 64, 200, 1500])
+def test_scan_infinite_states_stay(T, comp):
+    """h0 (and dhT) infinite, decays of e^-5 to e^-8 a token: 0 < a, so the state stays infinite,
+    although the product of 32 of them is below the smallest fp32."""
+    gen = torch.Generator().manual_seed(T)
+    D = 70
+    x, dy = randn(gen, 1, T, D), randn(gen, 1, T, D)
+    gate = -5 - 3 * torch.rand(1, T, D, generator=gen)
+    h0, dhT = randn(gen, 1, D), randn(gen, 1, D)
+    h0[0, 7], h0[0, 40], dhT[0, 9], dhT[0, 69] = float("inf"), float("-inf"), float("-inf"), float("inf")
+    x[0, T // 2, 60] = float("inf")
+    h0[0, 11] = 3e38   # a finite one decays away
+    how = dict(gate_mode="log", complement=comp)
+    states = torch.empty(kda.chunk_count(1, T), D, device="cuda")
+    y, hT = kda.kda_scan_fwd(x.cuda(), gate.cuda(), h0=h0.cuda(), h_chunks=states, **how)
+    ref, last, before = lo.scan(np64(x[0]), np64(gate[0]), h0=np64(h0[0]), **how)
+    assert np.isinf(ref[:, [7, 40]]).all() and np.isinf(ref[T // 2:, 60]).all()
+    # decays below 1/100: a state is off by some roundings of itself and its last input; a product that
+    # ends at the smallest fp32 (2^-149) is off by up to that
+    err = 16 * E24 * (np.abs(np.where(np.isfinite(ref), ref, 0)) + 6) + 2.0 ** -149 * 3e38
+    same_or_within(y[0], ref, err)
+    same_or_within(hT[0], last, err[-1])
+    dx, dg, dh0 = kda.kda_scan_bwd(x.cuda(), gate.cuda(), dy.cuda(), states, dhT=dhT.cuda(), **how)
+    rx, rg, r0 = lo.scan_grad(np64(x[0]), np64(gate[0]), np64(dy[0]), h0=np64(h0[0]), dhT=np64(dhT[0]), **how)
+    assert np.isinf(rx[:, [9, 69]]).all() and np.isinf(r0[[9, 69]]).all()
+    fin = lambda v: np.abs(np.where(np.isfinite(v), v, 0))  # noqa: E731
+    same_or_within(dx[0], rx, 16 * E24 * (fin(rx) + 6))
+    same_or_within(dh0[0], r0, 16 * E24 * (fin(r0) + 6))
+    same_or_within(dg[0], rg, 48 * E24 * (fin(rg) + 6 * (fin(before) + 6)))
+
+
+def test_scan_resets_stay_exact():
+    """A decay of exactly 0 lets nothing finite through, wherever it stands in its chunk, next to
+    decays whose product alone leaves fp32's range."""
+    gen = torch.Generator().manual_seed(2)
+    T, D = 700, 66
+    x = randn(gen, 1, T, D)
+    gate = torch.full((1, T, D), -6.0)
+    reset = torch.rand(T, D, generator=gen) < 0.05
+    gate[0][reset] = float("-inf")
+    x[0, ::3] = 0
+    h0 = torch.full((1, D), 3e38)
+    y, _ = kda.kda_scan_fwd(x.cuda(), gate.cuda(), h0=h0.cuda())
+    y = y[0].cpu()
+    assert torch.equal(y[reset], x[0][reset])
