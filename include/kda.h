@@ -367,7 +367,8 @@ kda_status kda_head_rmsnorm(const kda_rmsnorm_args* args, kda_stream_t stream);
  *   y                          [R, D]  y_dtype (bf16, fp32 or e4m3)
  *   y_scale                    [R]     fp32, e4m3 only
  * residual_out may be residual or x, and y may be x (same dtype and stride):
- * a row is read whole before any of it is written. A NaN in a row makes that
+ * a row is read whole before any of it is written. Finite rows may have squares
+ * outside fp32's range (eps = 0 is fine for small ones). A NaN in a row makes that
  * row's y NaN. 1 <= D <= KDA_NORM_MAX_D (KDA_ERR_UNSUPPORTED above). R = 0 is
  * accepted and does nothing.
  */

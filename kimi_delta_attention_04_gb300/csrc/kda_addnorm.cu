@@ -10,6 +10,10 @@
 // take a warp each and no barrier: 8192 x 4096 bf16 with residual to e4m3 in 37 us, 6.3
 // TB/s; 256 rows in 3.2 us. Rows whose pitch or address is off the 16-byte
 // grid are read one value at a time, lane-contiguous.
+//
+// A finite row can have squares beyond fp32's range (values above 1e19, or all below
+// 1e-15 without an eps to speak of); its sum is formed again from values scaled by a
+// power of two, which scales the root likewise and costs other rows one comparison.
 #include "kda_elem.cuh"
 
 namespace kda {
@@ -82,6 +86,14 @@ __device__ __forceinline__ void store8(__nv_fp8_storage_t* p, const float (&v)[k
                                             pack_e4m3x2(v[4], v[5]) | (pack_e4m3x2(v[6], v[7]) << 16));
 }
 
+// What a row's values are scaled by where the sum of their squares, ss, tells too little:
+// inf, or so small that some squares may have rounded away (above 2^-100 what those of
+// 32768 values lose is below 2^-34 of it; beside an eps of 2^-80 it is nothing). Sums of
+// squares of scaled values lie between 2^-98 and 2^120.
+__device__ __forceinline__ float range_scale(float ss, float eps) {
+  return ss > 3.40282347e+38f ? 0x1p-80f : ss < 0x1p-100f && eps < 0x1p-80f ? 0x1p100f : 1.f;
+}
+
 // Column of a thread's value j in step s. WIDE: 8 consecutive columns a thread;
 // otherwise consecutive threads hold consecutive columns.
 template <bool WIDE, int THREADS>
@@ -129,7 +141,7 @@ __global__ void __launch_bounds__(32 * WARPS * ROWS, min_ctas<32 * WARPS * ROWS,
   constexpr int THREADS = 32 * WARPS;
   constexpr bool KEEP = STEPS <= 2;  // weights in registers, next row on its way
   using Raw = typename RawOf<X>::type;
-  __shared__ float2 part[2][WARPS];
+  __shared__ float2 part[3][WARPS];  // by parity of the row; of a scaled row
   const int t = threadIdx.x % THREADS;
   const long long stride = static_cast<long long>(gridDim.x) * ROWS;
   long long row = static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / THREADS;
@@ -168,7 +180,25 @@ __global__ void __launch_bounds__(32 * WARPS * ROWS, min_ctas<32 * WARPS * ROWS,
       }
     }
     row_reduce<sizeof(Y) == 1, WARPS>(ss, top, part[parity]);
-    const float rstd = rsqrtf(ss / static_cast<float>(p.D) + p.eps);
+    float eps = p.eps;
+    const float by = range_scale(ss, eps);  // (the same in all threads of the row)
+    if (by != 1.f) {
+      ss = top = 0.f;
+      eps *= by;
+      eps *= by;
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        if (!KEEP && sizeof(Y) == 1) load_step<WIDE, THREADS>(p.weight, s, t, p.D, w[0]);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const float u = v[s][j] * by;
+          ss += u * u;
+          if (sizeof(Y) == 1) top = max_nan(top, fabsf(u * w[KEEP ? s : 0].w[j]));
+        }
+      }
+      row_reduce<sizeof(Y) == 1, WARPS>(ss, top, part[2]);
+    }
+    const float rstd = rsqrtf(ss / static_cast<float>(p.D) + eps);
     float inv = 1.f;
     if (sizeof(Y) == 1) {
       const float m = rstd * top;
@@ -180,6 +210,12 @@ __global__ void __launch_bounds__(32 * WARPS * ROWS, min_ctas<32 * WARPS * ROWS,
       X* ro = static_cast<X*>(p.residual_out) + row * p.residual_out_stride;
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) store_step<WIDE, THREADS>(ro, s, t, p.D, v[s]);
+    }
+    if (by != 1.f) {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[s][j] *= by;
     }
     Y* y = static_cast<Y*>(p.y) + row * p.y_stride;
 #pragma unroll

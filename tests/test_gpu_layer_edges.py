@@ -152,3 +152,30 @@ def test_scan_resets_stay_exact():
     y, _ = kda.kda_scan_fwd(x.cuda(), gate.cuda(), h0=h0.cuda())
     y = y[0].cpu()
     assert torch.equal(y[reset], x[0][reset])
+
+
+# --- norm: rows outside the range of a sum of squares ---
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("out_dtype", [BF, F32, E4])
+@pytest.mark.parametrize("D", [96, 101, 600, 4096, 9001])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+def test_add_rmsnorm_large_and_small_rows(dtype, out_dtype, D, eps):
+    """Finite rows whose squares leave fp32's range on either side."""
+    gen = torch.Generator().manual_seed(D)
+    size = torch.tensor([1e20, 6e37, 1.0, 1e-18, 1e-21, 1e-30, 1e-36, 3e18])
+    x = (randn(gen, len(size), D).clamp(-4, 4) * size[:, None]).to(dtype)
+    res = (randn(gen, len(size), D).clamp(-1, 1) * size[:, None] / 4).to(dtype)
+    w = 1 + 0.2 * randn(gen, D)
+    y, s, r = kda.kda_add_rmsnorm(x.cuda(), w.cuda(), eps=eps, residual=res.cuda(), out_dtype=out_dtype)
+    check_norm(y, s, r, x, res, w, eps, out_dtype)
+
+
+def test_add_rmsnorm_smallest_rows():
+    """Rows of fp32's smallest values, and a single one among zeros."""
+    x = torch.zeros(3, 200)
+    x[0], x[1, 17], x[2, :2] = 2.0 ** -149, 2.0 ** -149, torch.tensor([2.0 ** -127, 3e38])
+    w = torch.ones(200)
+    y, _, _ = kda.kda_add_rmsnorm(x.cuda(), w.cuda(), eps=0.0)
+    ref, _ = lo.add_rmsnorm(np64(x), None, np64(w), 0.0)
+    within(y, ref, F32, np.abs(ref) * E24 * 40)
