@@ -179,3 +179,55 @@ def test_add_rmsnorm_smallest_rows():
     y, _, _ = kda.kda_add_rmsnorm(x.cuda(), w.cuda(), eps=0.0)
     ref, _ = lo.add_rmsnorm(np64(x), None, np64(w), 0.0)
     within(y, ref, F32, np.abs(ref) * E24 * 40)
+
+
+# --- gates far from zero ---
+
+FAR = torch.linspace(-30, 30, 241)
+
+
+def one_token(f, x, h0, mode, comp, dy):
+    """(y, h, dx, dgate, dh0) of one token on every path that takes one."""
+    D = f.numel()
+    t = lambda v: v.reshape(1, 1, D).cuda()  # noqa: E731
+    how = dict(gate_mode=mode, complement=comp)
+    states = torch.empty(1, D, device="cuda")
+    y, hT = kda.kda_scan_fwd(t(x), t(f), h0=t(h0)[0], h_chunks=states, **how)
+    g = kda.kda_scan_bwd(t(x), t(f), t(dy), states, **how)
+    pool = t(h0)[0].clone()
+    ys = kda.kda_scan_step(t(x)[0], t(f)[0], pool, torch.zeros(1, dtype=torch.int32, device="cuda"), **how)
+    # the same token as the last of 101: zero inputs and logits that keep the state before it
+    T = 101
+    xl, fl = torch.zeros(1, T, D), torch.full((1, T, D), 200.0 if mode == "logits" else 0.0)
+    dl = torch.zeros(1, T, D)
+    xl[0, -1], fl[0, -1], dl[0, -1] = x, f, dy
+    states = torch.empty(kda.chunk_count(1, T), D, device="cuda")
+    yl, hl = kda.kda_scan_fwd(xl.cuda(), fl.cuda(), h0=t(h0)[0], h_chunks=states, **how)
+    gl = kda.kda_scan_bwd(xl.cuda(), fl.cuda(), dl.cuda(), states, **how)
+    return [(y[0], hT, g[0][0], g[1][0], g[2]), (ys, pool, None, None, None), (yl[0, -1:], hl, gl[0][0, -1:], gl[1][0, -1:], gl[2])]
+
+
+def test_scan_decays_far_from_zero():
+    """a = sigmoid(f) to fp32, relative: exponential 4 half steps, sum 1, reciprocal 2, products 1 each."""
+    f = FAR
+    x, h0 = torch.zeros_like(f), 1 + torch.rand(f.numel(), generator=torch.Generator().manual_seed(1))
+    ref, _, _ = lo.scan(np64(x)[None], np64(f)[None], gate_mode="logits", complement=False, h0=np64(h0))
+    for y, h, _, _, dh0 in one_token(f, x, h0, "logits", False, torch.ones_like(f)):
+        within(y, ref, F32, 9 * E24 * ref)
+        within(h, ref, F32, 9 * E24 * ref)
+        if dh0 is not None:
+            within(dh0, 1 / (1 + np.exp(-np64(f)))[None], F32, 9 * E24)
+            assert np.all(np.abs(np64(dh0)[0] * (1 + np.exp(-np64(f))) - 1) <= 10 * E24)
+
+
+def test_scan_decays_of_bf16_gates_far_from_zero():
+    """Their exponential's argument is rounded once: 1.3 |f| half steps more (the states are fp32)."""
+    f = FAR.to(BF)
+    h0 = 1 + torch.rand(1, f.numel(), generator=torch.Generator().manual_seed(1))
+    a = 1 / (1 + np.exp(-np64(f)))
+    x = torch.zeros(1, 1, f.numel(), dtype=BF, device="cuda")
+    states = torch.empty(1, f.numel(), device="cuda")
+    _, hT = kda.kda_scan_fwd(x, f.view(1, 1, -1).cuda(), gate_mode="logits", h0=h0.cuda(), h_chunks=states)
+    _, _, dh0 = kda.kda_scan_bwd(x, f.view(1, 1, -1).cuda(), x + 1, states, gate_mode="logits")
+    err = (10 + 1.3 * np.abs(np64(f))) * E24 * a
+    assert np.all(np.abs(np64(hT)[0] - a * np64(h0)[0]) <= err * np64(h0)[0]) and np.all(np.abs(np64(dh0)[0] - a) <= err)
