@@ -443,6 +443,8 @@ typedef enum {
  * Gated linear recurrence, one fp32 state h per sequence and channel:
  *   h_t = a_t h_{t-1} + u_t,   u_t = x_t, or (1 - a_t) x_t with KDA_SCAN_FLAG_COMPLEMENT
  *   y_t = h_t
+ * in fp32, with 1 - a_t formed by itself, not as a difference: decays next to 1 and
+ * next to 0 keep fp32's relative accuracy (of bf16 logits f, to some |f| fp32 steps).
  *   x, y        [B, T, D]  dtype (bf16 or fp32)
  *   gate        [B, T, D]  gate_dtype (fp32, or bf16 when dtype is bf16); log decays
  *                          are meant to be <= 0 (-inf resets the state): products of

@@ -319,36 +319,119 @@ __device__ __forceinline__ float rcp_approx(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// e^-f of bf16 gates, e^-|f| of fp32 ones.
 template <typename G>
-__device__ __forceinline__ float2 sigmoid2(float2 f) {
+__device__ __forceinline__ float2 exp_neg(float2 f) {
   constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
-  if (sizeof(G) == 2) {  // (e = inf gives 0)
+  if (sizeof(G) == 2) {
     const float2 z = mul2(f, make_float2(-kLog2e, -kLog2e));
-    const float2 q = add2(make_float2(ex2_approx(z.x), ex2_approx(z.y)), make_float2(1.f, 1.f));
-    return make_float2(rcp_approx(q.x), rcp_approx(q.y));
+    return make_float2(ex2_approx(z.x), ex2_approx(z.y));
   }
   // (e is 0 from |f| = 88 on; an infinite v would make d NaN)
   const float2 v = make_float2(max_nan(-fabsf(f.x), -128.f), max_nan(-fabsf(f.y), -128.f));
   const float2 z = mul2(v, make_float2(kLog2e, kLog2e)), d = fma2(z, make_float2(-kLn2, -kLn2), v);
-  float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-  e = fma2(e, d, e);
-  const float2 q = add2(e, make_float2(1.f, 1.f)), r = make_float2(rcp_approx(q.x), rcp_approx(q.y)), s = mul2(e, r);
-  return make_float2(f.x < 0.f ? s.x : r.x, f.y < 0.f ? s.y : r.y);
+  const float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+  return fma2(e, d, e);
 }
 template <int MODE, typename G>
-__device__ __forceinline__ float2 decays_of(float2 f) {
-  return MODE == KDA_SCAN_LOG_DECAY ? make_float2(expf(f.x), expf(f.y)) : sigmoid2<G>(f);
+__device__ __forceinline__ float2 decay_of(float2 f) {
+  if (MODE == KDA_SCAN_LOG_DECAY) return make_float2(expf(f.x), expf(f.y));
+  const float2 e = exp_neg<G>(f), q = add2(e, make_float2(1.f, 1.f)), r = make_float2(rcp_approx(q.x), rcp_approx(q.y));
+  if (sizeof(G) == 2) return r;  // (e = inf gives 0)
+  const float2 s = mul2(e, r);
+  return make_float2(f.x < 0.f ? s.x : r.x, f.y < 0.f ? s.y : r.y);
+}
+// 1 - a to a few steps of itself: from f = 17 on a rounds to 1, and at f = 10 the
+// difference has three digits, with one sign for a given gate. e a is 1 - a exactly; below
+// f = 0 the difference is good, and e may be infinite. With log decays it is 1 - e^g, near 0
+// by a polynomial in g (fitted to (e^g - 1) / g for the least relative error on [-0.7,
+// 0.7]: 3e-8).
+template <int MODE, typename G>
+__device__ __forceinline__ float2 rest_of(float2 f, float2 a) {
+  float2 near;
+  bool x, y;
+  if (MODE == KDA_SCAN_LOG_DECAY) {
+    auto both = [](float c) { return make_float2(c, c); };
+    near = fma2(both(1.98409674e-04f), f, both(1.41012878e-03f));
+    near = fma2(near, f, both(8.33449047e-03f));
+    near = fma2(near, f, both(4.16615158e-02f));
+    near = fma2(near, f, both(1.66666389e-01f));
+    near = fma2(near, f, both(5.00000298e-01f));
+    near = mul2(fma2(near, f, both(1.f)), make_float2(-f.x, -f.y));
+    x = fabsf(f.x) > 0.7f, y = fabsf(f.y) > 0.7f;
+  } else {
+    near = mul2(exp_neg<G>(f), a);
+    x = f.x < 0.f, y = f.y < 0.f;
+  }
+  return make_float2(x ? 1.f - a.x : near.x, y ? 1.f - a.y : near.y);
 }
 
-// The decays of a tile; the mode is looked at once.
-template <typename T, int ACC>
-__device__ __forceinline__ void decays(float2 (&a)[kScanChunk], const Tile<T, ACC>& gate, int mode) {
-  if (mode == KDA_SCAN_LOG_DECAY) {
+// A tile's gates and inputs, all read before anything is written to its slots.
+template <typename X, typename G, int ACC>
+__device__ __forceinline__ void read_tiles(float2 (&f)[kScanChunk], float2 (&u)[kScanChunk], const Tile<G, ACC>& gate,
+                                           const Tile<X, ACC>& x) {
 #pragma unroll
-    for (int i = 0; i < kScanChunk; ++i) a[i] = decays_of<KDA_SCAN_LOG_DECAY, T>(gate.get(i));
-  } else {
+  for (int i = 0; i < kScanChunk; ++i) f[i] = gate.get(i);
 #pragma unroll
-    for (int i = 0; i < kScanChunk; ++i) a[i] = decays_of<KDA_SCAN_LOGITS, T>(gate.get(i));
+  for (int i = 0; i < kScanChunk; ++i) u[i] = x.get(i);
+}
+// Decays in the place of the gates, and inputs as they enter the states.
+template <int MODE, bool COMP, typename G>
+__device__ __forceinline__ void weigh(float2 (&a)[kScanChunk], float2 (&u)[kScanChunk]) {
+#pragma unroll
+  for (int i = 0; i < kScanChunk; ++i) {
+    const float2 f = a[i];
+    a[i] = decay_of<MODE, G>(f);
+    if (COMP) u[i] = mul2(rest_of<MODE, G>(f, a[i]), u[i]);
+  }
+}
+// Four bytes a value in the slots of tiles that have been read: the gate's, or with bf16
+// the gate's and the input's, a half each.
+template <int ACC>
+__device__ __forceinline__ void put_pair(const Tile<float, ACC>& gate, const Tile<float, ACC>&, int i, float2 b) {
+  gate.pairs[i * 32 + (threadIdx.x & 31)].v = b;
+}
+template <int ACC>
+__device__ __forceinline__ void put_pair(const Tile<float, ACC>& gate, const Tile<__nv_bfloat16, ACC>&, int i, float2 b) {
+  gate.pairs[i * 32 + (threadIdx.x & 31)].v = b;
+}
+template <int ACC>
+__device__ __forceinline__ void put_pair(const Tile<__nv_bfloat16, ACC>& gate, const Tile<__nv_bfloat16, ACC>& x, int i, float2 b) {
+  const int at = i * 32 + (threadIdx.x & 31);
+  gate.pairs[at].v = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x7632);
+  x.pairs[at].v = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x5410);
+}
+template <typename X, int ACC>
+__device__ __forceinline__ float2 get_pair(const Tile<float, ACC>& gate, const Tile<X, ACC>&, int i) {
+  return gate.get(i);
+}
+template <int ACC>
+__device__ __forceinline__ float2 get_pair(const Tile<__nv_bfloat16, ACC>& gate, const Tile<__nv_bfloat16, ACC>& x, int i) {
+  const int at = i * 32 + (threadIdx.x & 31);
+  const uint32_t hi = gate.pairs[at].v, lo = x.pairs[at].v;
+  return make_float2(__uint_as_float(__byte_perm(lo, hi, 0x5410)), __uint_as_float(__byte_perm(lo, hi, 0x7632)));
+}
+
+// Decays in the place of the gates, and in the place of the inputs what each decay's
+// gradient is a multiple of: the state before the token (h before the first), less the input
+// where that has the weight 1 - a. 1 - a itself, where it is needed, is left in the tiles'
+// slots for the gradients (64 registers hold the other two, and forming it again there
+// made every backward pass a third longer).
+template <int MODE, bool COMP, typename X, typename G, int ACC>
+__device__ __forceinline__ void run_through(float2 (&a)[kScanChunk], float2 (&w)[kScanChunk], float2 h, const Tile<G, ACC>& gate,
+                                            const Tile<X, ACC>& x) {
+#pragma unroll
+  for (int i = 0; i < kScanChunk; ++i) {
+    const float2 f = a[i];
+    float2 u = w[i];
+    a[i] = decay_of<MODE, G>(f);
+    w[i] = COMP ? make_float2(h.x - u.x, h.y - u.y) : h;
+    if (COMP || MODE == KDA_SCAN_LOGITS) {
+      const float2 b = rest_of<MODE, G>(f, a[i]);
+      put_pair(gate, x, i, b);
+      if (COMP) u = mul2(b, u);
+    }
+    h = fma2(a[i], h, u);
   }
 }
 
@@ -512,12 +595,15 @@ __global__ void __launch_bounds__(32 * W, 2 * kWarps / W) kda_scan_fwd_kernel(co
       __syncwarp();
       const int i0 = first(j), m = len - i0;
       float2 a[kScanChunk], u[kScanChunk];
-      decays(a, tile_g(slot), p.gate_mode);
       const Tile<X, ACC> tx = tile_x(slot);
-#pragma unroll
-      for (int i = 0; i < kScanChunk; ++i) {
-        u[i] = tx.get(i);
-        if (comp) u[i] = mul2(make_float2(1.f - a[i].x, 1.f - a[i].y), u[i]);  // (x - a x would be NaN for an infinite x)
+      const Tile<G, ACC> tg = tile_g(slot);
+      read_tiles(a, u, tg, tx);
+      if (p.gate_mode == KDA_SCAN_LOG_DECAY) {
+        if (comp) weigh<KDA_SCAN_LOG_DECAY, true, G>(a, u);
+        else weigh<KDA_SCAN_LOG_DECAY, false, G>(a, u);
+      } else {
+        if (comp) weigh<KDA_SCAN_LOGITS, true, G>(a, u);
+        else weigh<KDA_SCAN_LOGITS, false, G>(a, u);
       }
       __syncwarp();  // the slots are free for the fetch of the next iteration
       Map mine = identity_map();
@@ -603,27 +689,21 @@ __global__ void __launch_bounds__(32 * W, 2 * kWarps / W) kda_scan_bwd_kernel(co
     int slot = 0;  // of advance j; its stage before is the one to fill
     for (int j = 0; j * S * warps < chunks; ++j, ++it, slot = slot + 1 == kStages ? 0 : slot + 1) {
       const int k = chunk_of(j), m = k < 0 ? 0 : len - k * kScanChunk;
-      float2 h = next_h;
+      const float2 h = next_h;
       next_h = chunk_state(j + 1);
       fetch(j + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
       cp_async_wait<kStages - 1>();
       __syncwarp();
       const Tile<X, ACC> tx = tile_x(slot), td = tile_d(slot);
       float2 a[kScanChunk], w[kScanChunk];  // decay; what d multiplies in the decay's gradient
-      decays(a, tile_g(slot), p.gate_mode);
-      if (comp) {
-#pragma unroll
-        for (int i = 0; i < kScanChunk; ++i) {  // (x + a (h - x) would be NaN for an infinite x)
-          const float2 xv = tx.get(i);
-          w[i] = make_float2(h.x - xv.x, h.y - xv.y);
-          h = fma2(a[i], h, mul2(make_float2(1.f - a[i].x, 1.f - a[i].y), xv));
-        }
+      const Tile<G, ACC> tg = tile_g(slot);
+      read_tiles(a, w, tg, tx);
+      if (logits) {
+        if (comp) run_through<KDA_SCAN_LOGITS, true>(a, w, h, tg, tx);
+        else run_through<KDA_SCAN_LOGITS, false>(a, w, h, tg, tx);
       } else {
-#pragma unroll
-        for (int i = 0; i < kScanChunk; ++i) {
-          w[i] = h;
-          h = fma2(a[i], h, tx.get(i));
-        }
+        if (comp) run_through<KDA_SCAN_LOG_DECAY, true>(a, w, h, tg, tx);
+        else run_through<KDA_SCAN_LOG_DECAY, false>(a, w, h, tg, tx);
       }
       Map mine = identity_map();  // d -> a (d + dy), last token first
       if (m >= kScanChunk) {
@@ -640,7 +720,8 @@ __global__ void __launch_bounds__(32 * W, 2 * kWarps / W) kda_scan_bwd_kernel(co
       X* dx = static_cast<X*>(q.dx) + last * q.dx_stride;
       G* dg = static_cast<G*>(q.dgate) + last * q.dgate_stride;
       auto token = [&](int i) {
-        const float2 b = make_float2(1.f - a[i].x, 1.f - a[i].y);
+        float2 b = make_float2(1.f, 1.f);  // 1 - a, where it is needed
+        if (logits || comp) b = get_pair(tg, tx, i);
         d = add2(d, td.get(i));
         store_pair<ACC>(dx, l, comp ? mul2(b, d) : d);
         d = mul2(a[i], d);
@@ -695,8 +776,11 @@ __global__ void __launch_bounds__(kStepThreads) kda_scan_step_kernel(const kda_s
 #pragma unroll
       for (int j = 0; j < C; ++j) {
         const float2 pair = make_float2(f[j], f[j]);
-        const float a = (p.gate_mode == KDA_SCAN_LOG_DECAY ? decays_of<KDA_SCAN_LOG_DECAY, G>(pair) : decays_of<KDA_SCAN_LOGITS, G>(pair)).x;
-        h[j] = fmaf(a, h[j], p.flags & KDA_SCAN_FLAG_COMPLEMENT ? (1.f - a) * u[j] : u[j]);
+        const bool log = p.gate_mode == KDA_SCAN_LOG_DECAY;
+        const float2 a = log ? decay_of<KDA_SCAN_LOG_DECAY, G>(pair) : decay_of<KDA_SCAN_LOGITS, G>(pair);
+        if (p.flags & KDA_SCAN_FLAG_COMPLEMENT)
+          u[j] *= (log ? rest_of<KDA_SCAN_LOG_DECAY, G>(pair, a) : rest_of<KDA_SCAN_LOGITS, G>(pair, a)).x;
+        h[j] = fmaf(a.x, h[j], u[j]);
       }
       if (C == 4) store4(p.state_out + at, h);
       else p.state_out[at] = h[0];

@@ -231,3 +231,32 @@ def test_scan_decays_of_bf16_gates_far_from_zero():
     _, _, dh0 = kda.kda_scan_bwd(x, f.view(1, 1, -1).cuda(), x + 1, states, gate_mode="logits")
     err = (10 + 1.3 * np.abs(np64(f))) * E24 * a
     assert np.all(np.abs(np64(hT)[0] - a * np64(h0)[0]) <= err * np64(h0)[0]) and np.all(np.abs(np64(dh0)[0] - a) <= err)
+
+
+# --- 1 - a ---
+
+@pytest.mark.parametrize("mode", ["log", "logits"])
+@pytest.mark.parametrize("comp", [False, True])
+def test_scan_complement_far_from_zero(mode, comp):
+    """1 - a to fp32, relative: as an input's weight, in dx and in a logit's gradient."""
+    f = FAR if mode == "logits" else -torch.logspace(-8, 2, 241)
+    gen = torch.Generator().manual_seed(4)
+    n = f.numel()
+    x, h0, dy = 1 + torch.rand(n, generator=gen), torch.zeros(n), 1 + torch.rand(n, generator=gen)
+    how = dict(gate_mode=mode, complement=comp)
+    for grad_only in (False, True):
+        if grad_only:  # a state beside the input, so that the decay's gradient is of one product
+            h0 = 4 + torch.rand(n, generator=gen)
+        ref, _, _ = lo.scan(np64(x)[None], np64(f)[None], h0=np64(h0), **how)
+        b = -np.expm1(np64(f)) if mode == "log" else 1 / (1 + np.exp(np64(f)))
+        a = np.exp(np64(f)) if mode == "log" else 1 / (1 + np.exp(-np64(f)))
+        want = (b if comp else 1) * np64(x)
+        rx = (b if comp else 1) * np64(dy)
+        rg = a * np64(dy) * (np64(h0) - np64(x) if comp else np64(h0)) * (b if mode == "logits" else 1)
+        for y, h, dx, dg, _ in one_token(f, x, h0, mode, comp, dy):
+            if not grad_only:
+                within(y, want[None], F32, 12 * E24 * want)
+                within(h, want[None], F32, 12 * E24 * want)
+            if dx is not None:
+                within(dx, rx[None], F32, 12 * E24 * rx)
+                within(dg, rg[None], F32, 24 * E24 * np.abs(rg))
