@@ -405,7 +405,8 @@ typedef enum {
  *   residual  [M, N]  y_dtype, row stride ld_residual, or NULL; may be y (same stride)
  *   y         [M, N]  y_dtype (bf16 or fp32), row stride ldy
  * dtype is bf16 or e4m3 (both operands); products and sums are fp32, everything
- * after them is fp32, and y is rounded once. M = 0 does nothing; N, K >= 1.
+ * after them is fp32 (activations to 20 half steps of their result and 1.5 times what half
+ * a step of their argument comes to), and y is rounded once. M = 0 does nothing; N, K >= 1.
  * y overlaps neither x nor w.
  * Resources: the kernels hold tensor memory while they run, for more than 64 tokens
  * all 512 columns of each SM they are on. A kernel on another stream that holds some

@@ -281,33 +281,6 @@ __device__ __forceinline__ void store_state(float* base, long long row, int D, c
   if (l.p1) base[l.c1] = v.y;
 }
 
-// Two fp32 operations in one instruction (PTX f32x2).
-__device__ __forceinline__ uint64_t bits2(float2 v) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
-  return r;
-}
-__device__ __forceinline__ float2 floats2(uint64_t b) {
-  float2 v;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(b));
-  return v;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-  return floats2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return floats2(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return floats2(r);
-}
-
 // The decays: expf(g), or the sigmoid. e^v is 2^z (1 + d) with z = v / ln 2 rounded and d =
 // v - z ln 2 what that lost. fp32 gates take d with it, and e = e^-|f| <= 1 (1 / (1 + e)
 // for f >= 0, e / (1 + e) below), so that a decay is good to a few fp32 steps of itself over

@@ -2,6 +2,8 @@
 and states, rows outside the range of a sum of squares, gates far from zero, sizes
 next to 2^31. Against the fp64 oracle; E24 is half a step of fp32, relative."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -260,3 +262,30 @@ def test_scan_complement_far_from_zero(mode, comp):
             if dx is not None:
                 within(dx, rx[None], F32, 12 * E24 * rx)
                 within(dg, rg[None], F32, 24 * E24 * np.abs(rg))
+
+
+# --- activations ---
+
+VALUES = torch.cat([torch.linspace(-12, 12, 449), torch.logspace(-6, 0, 25), -torch.logspace(-6, 0, 25), torch.tensor([0.0, 60.0, -60.0, 80.0, -80.0])]).to(BF)
+
+
+def activated(act, v):
+    """act of v and the steps that half a step of v itself costs, both in 64 bits without cancellation."""
+    if act == "gelu":
+        return 0.5 * v * np.array([math.erfc(-u / math.sqrt(2)) for u in v]), v * v
+    s = np.where(v < 0, np.exp(-np.abs(v)), 1) / (1 + np.exp(-np.abs(v)))
+    return s if act == "sigmoid" else v * s, np.abs(v)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "sigmoid"])
+@pytest.mark.parametrize("rows", [3, 100, 300])
+def test_linear_activations_alone(act, rows):
+    """Every value as an output of its own (K = 1, ones against the values): 20 half steps of the
+    result, and 1.5 times what half a step of the argument comes to, its square or product being rounded."""
+    x = torch.ones(rows, 1, dtype=BF, device="cuda")
+    ref, slope = activated(act, np64(VALUES))
+    for out_dtype in (F32, BF):
+        for n in (VALUES.numel(), VALUES.numel() // 16 * 16, VALUES.numel() // 16 * 16 - 8):  # any rows, 32 and 16 bytes
+            y = kda.kda_linear(x, VALUES[:n, None].contiguous().cuda(), activation=act, out_dtype=out_dtype)
+            assert torch.equal(y, y[:1].expand_as(y))
+            within(y[0], ref[:n], out_dtype, (20 + 1.5 * slope[:n]) * E24 * np.abs(ref[:n]))
