@@ -21,6 +21,7 @@
 #include <algorithm>
 
 #include "kda_cluster.cuh"
+#include "kda_device_counts.h"
 #include "kda_elem.cuh"
 
 namespace kda {
@@ -774,12 +775,11 @@ int access_of(const void* p, int64_t stride, int D, int32_t dt) {
   return D % 2 == 0 && stride % 2 == 0 && at % (2 * e) == 0 ? kPair : kSingle;
 }
 
-// What one instance of a kernel remembers of the device: where its shared-memory
-// limit has been raised, and how many of its clusters of each size are resident at
-// once (0: not asked yet).
+// What one instance of a kernel remembers of each device: whether its shared-memory
+// limit has been raised, and how many of its clusters of each size are resident at once.
 struct Instance {
   std::atomic<uint64_t> smem_set{0};
-  std::atomic<int> resident[kMaxCluster + 1] = {};
+  DeviceCounts<kMaxCluster + 1> resident;
 };
 
 template <int W, typename Args>
@@ -807,17 +807,19 @@ cudaError_t launch_clusters(void (*kernel)(Args, int), Instance& inst, size_t wa
   const long long blocks = (f.D + kBlockCh - 1) / kBlockCh, work = blocks * f.N;
   const long long mean = f.cu_seqlens ? (static_cast<long long>(f.T) + f.N - 1) / f.N : f.T;
   const int rounds = f.cu_seqlens && f.N > 1 ? 2 : 1;
+  int device = 0;
+  e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
   int S = kMaxCluster;
   for (; S > 1; --S) {
     if (mean <= static_cast<long long>(S - 1) * kWarps * kScanChunk) continue;
-    int fit = inst.resident[S].load(std::memory_order_relaxed);
-    if (fit == 0) {
+    int fit = 0;
+    e = static_cast<cudaError_t>(inst.resident.get(device, S, &fit, [&](int* count) {
       attr.val.clusterDim.x = S;
       cfg.gridDim = dim3(S);
-      e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
-      if (e != cudaSuccess) return e;
-      inst.resident[S].store(fit > 0 ? fit : -1, std::memory_order_relaxed);
-    }
+      return static_cast<int>(cudaOccupancyMaxActiveClusters(count, kernel, &cfg));
+    }));
+    if (e != cudaSuccess) return e;
     if (work <= static_cast<long long>(fit) * rounds) break;
   }
   attr.val.clusterDim.x = S;
