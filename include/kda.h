@@ -408,8 +408,9 @@ typedef enum {
  * after them is fp32 (activations to 20 half steps of their result and 1.5 times what half
  * a step of their argument comes to), and y is rounded once. M = 0 does nothing; N, K >= 1.
  * y overlaps neither x nor w.
- * Resources: the kernels hold tensor memory while they run, for more than 64 tokens
- * all 512 columns of each SM they are on. A kernel on another stream that holds some
+ * Resources: the kernels hold tensor memory while they run: for more than 64 tokens
+ * all 512 columns of each SM they are on, but where few tiles share a long K, and for fewer
+ * tokens, 32 to 128 columns for each of up to two CTAs on an SM. A kernel on another stream that holds some
  * on the same SM only delays them (their allocation waits), and the other way round.
  * A bounded wait that runs out writes KDA_ERR_TIMEOUT to err.
  */
@@ -445,7 +446,8 @@ typedef enum {
  *   h_t = a_t h_{t-1} + u_t,   u_t = x_t, or (1 - a_t) x_t with KDA_SCAN_FLAG_COMPLEMENT
  *   y_t = h_t
  * in fp32, with 1 - a_t formed by itself, not as a difference: decays next to 1 and
- * next to 0 keep fp32's relative accuracy (of bf16 logits f, to some |f| fp32 steps).
+ * next to 0 keep fp32's relative accuracy (of bf16 logits f, to some |f| fp32 steps);
+ * a decay, or 1 - a, of a logit that leaves fp32's normal range (2^-126) is 0.
  *   x, y        [B, T, D]  dtype (bf16 or fp32)
  *   gate        [B, T, D]  gate_dtype (fp32, or bf16 when dtype is bf16); log decays
  *                          are meant to be <= 0 (-inf resets the state): products of

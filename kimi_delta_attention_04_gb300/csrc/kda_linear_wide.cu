@@ -15,9 +15,9 @@
 // outputs (columns), twice: while the epilogue warps read one accumulator the next
 // tile's products fill the other.
 //
-// 8192 x 4096 -> 12288 bf16 runs at 1.98 PFLOP/s (416 us, tensor pipe 95 % busy), 8192 x
-// 4096 -> 4096 e4m3 with bias, silu and residual at 3.3 (83 us), 256 x 4096 -> 12288 at
-// 25 us, where loads bring each SM about 45 bytes a cycle.
+// 8192 x 4096 -> 12288 bf16 runs at 1.95 PFLOP/s (424 us, tensor pipe 95 % busy), 8192 x
+// 4096 -> 4096 e4m3 with bias, silu and residual at 3.1 (88 us), 256 x 4096 -> 12288 in
+// 25 us, in which loads bring each SM 1.77 MB, 36 bytes a cycle from launch to end.
 //
 // Roles: warps 0-11 the epilogue (lane quarter w % 4, every third block of 32 columns;
 // with eight warps gelu on 4691 x 312 -> 8608 took 57 us instead of 54), warp 12 issues

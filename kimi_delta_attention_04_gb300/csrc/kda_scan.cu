@@ -15,9 +15,9 @@
 // do not vary from run to run. Batches of short equal sequences have kernels of their
 // own, with no more warps than a sequence has chunks and no ring.
 //
-// HBM traffic is the bound to come to: 8192 x 4096 bf16 runs at 4.6 TB/s forward (43
-// us; the rest is the latency of the exchange and 22 instructions an element) and 5.2
-// TB/s backward, 4 x 4096 x 2048 with fp32 gates at 5.5 and 6.2 TB/s.
+// HBM traffic is the bound to come to: 8192 x 4096 bf16 runs at 4.6 TB/s forward (44
+// us; the rest is the latency of the exchange and 23 instructions an element) and 5.1
+// TB/s backward, 4 x 4096 x 2048 with fp32 gates at 5.7 and 6.3 TB/s.
 #include <algorithm>
 
 #include "kda_cluster.cuh"
@@ -286,8 +286,8 @@ __device__ __forceinline__ void store_state(float* base, long long row, int D, c
 // v - z ln 2 what that lost. fp32 gates take d with it, and e = e^-|f| <= 1 (1 / (1 + e)
 // for f >= 0, e / (1 + e) below), so that a decay is good to a few fp32 steps of itself over
 // the whole range. Without them a small decay is off by |f| / 2 steps; bf16 gates, whose
-// gradients are rounded at 2^-9, do without (8192 x 4096 forward: 47.2 us with both, 43.6
-// with neither).
+// gradients are rounded at 2^-9, do without (with both, 8192 x 4096 forward took 8 %
+// longer).
 __device__ __forceinline__ float rcp_approx(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -831,9 +831,9 @@ cudaError_t launch_clusters(void (*kernel)(Args, int), Instance& inst, size_t wa
 }
 
 // Equal sequences of up to kShortWarps chunks get a warp for each and one stage of
-// tiles, so that an SM holds many of them: 256 of 16 tokens, 1024 channels: 9 us
-// forward and 11 backward, 32 and 68 with the eight warps and the ring that long ones
-// need. How short the sequences of a packed batch are only the GPU knows.
+// tiles, so that an SM holds many of them: 256 of 16 tokens, 1024 channels: 10 us
+// forward and 15 backward, three to six times that with the eight warps and the ring that
+// long ones need. How short the sequences of a packed batch are only the GPU knows.
 inline bool short_sequences(const kda_scan_args& a) { return !a.cu_seqlens && a.T <= kShortWarps * kScanChunk; }
 
 template <typename X, typename G, int ACC, int W>
