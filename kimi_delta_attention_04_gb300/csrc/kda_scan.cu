@@ -439,7 +439,7 @@ __device__ __forceinline__ float2 nonzero_product(float2 A, const Map (*maps)[32
   for (int w = 0; w < n; ++w) least = make_float2(fminf(least.x, maps[w][lane].A.x), fminf(least.y, maps[w][lane].A.y));
   return make_float2(fmaxf(A.x, least.x), fmaxf(A.y, least.y));
 }
-__device__ __forceinline__ bool any_infinite(float2 h) { return fabsf(h.x) + fabsf(h.y) > 3.40282347e+38f; }
+__device__ __forceinline__ bool any_infinite(float2 h) { return fmaxf(fabsf(h.x), fabsf(h.y)) > 3.40282347e+38f; }  // (beside a NaN too)
 // A h + B where A is the product of the first n warps' maps.
 __device__ __forceinline__ float2 apply(const Map& map, float2 h, const Map (*maps)[32], int n) {
   return fma2(any_infinite(h) ? nonzero_product(map.A, maps, n) : map.A, h, map.B);

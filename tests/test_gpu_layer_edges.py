@@ -140,6 +140,21 @@ def test_scan_infinite_states_stay(T, comp):
     same_or_within(dg[0], rg, 48 * E24 * (fin(rg) + 6 * (fin(before) + 6)))
 
 
+@pytest.mark.parametrize("D", [70, 71, 72])
+def test_scan_infinite_states_beside_nan(D):
+    """An infinite channel next to one of NaN, in the same thread's pair and in the next."""
+    T = 200
+    h0 = torch.ones(1, D)
+    h0[0, [7, 12, 20, 21]] = float("inf")
+    h0[0, [6, 13, 39, 44, 52, 53]] = float("nan")  # (a thread holds 2 l and 2 l + 1, or l and l + 32)
+    x, gate = torch.zeros(1, T, D), torch.full((1, T, D), -6.0)
+    y, hT = kda.kda_scan_fwd(x.cuda(), gate.cuda(), h0=h0.cuda())
+    states = torch.zeros(kda.chunk_count(1, T), D, device="cuda")
+    _, _, dh0 = kda.kda_scan_bwd(x.cuda(), gate.cuda(), x.cuda(), states, dhT=h0.cuda())
+    for v in (y[0, -1].cpu(), hT[0].cpu(), dh0[0].cpu()):
+        assert torch.equal(torch.isinf(v), torch.isinf(h0[0])) and torch.equal(torch.isnan(v), torch.isnan(h0[0]))
+
+
 def test_scan_resets_stay_exact():
     """A decay of exactly 0 lets nothing finite through, wherever it stands in its chunk, next to
     decays whose product alone leaves fp32's range."""
