@@ -440,11 +440,6 @@ __device__ __forceinline__ float2 nonzero_product(float2 A, const Map (*maps)[32
   return make_float2(fmaxf(A.x, least.x), fmaxf(A.y, least.y));
 }
 __device__ __forceinline__ bool any_infinite(float2 h) { return fmaxf(fabsf(h.x), fabsf(h.y)) > 3.40282347e+38f; }  // (beside a NaN too)
-// A h + B where A is the product of the first n warps' maps.
-__device__ __forceinline__ float2 apply(const Map& map, float2 h, const Map (*maps)[32], int n) {
-  return fma2(any_infinite(h) ? nonzero_product(map.A, maps, n) : map.A, h, map.B);
-}
-
 // Warps of a CTA of a kernel made for up to W of them: kWarps always, or those launched.
 template <int W>
 __device__ __forceinline__ int cta_warps() {
@@ -489,8 +484,12 @@ __device__ __forceinline__ float2 enter_state(ScanSmem<W>& sm, const Map& mine, 
   if (W != kWarps || S == 1) {
     Map total = then(before, mine);
     for (int w = warp + 1; w < warps; ++w) total = then(total, sm.warp[parity][w][lane]);
-    const float2 in = apply(before, carry, sm.warp[parity], warp);
-    carry = apply(total, carry, sm.warp[parity], warps);
+    if (any_infinite(carry)) {
+      before.A = nonzero_product(before.A, sm.warp[parity], warp);
+      total.A = nonzero_product(total.A, sm.warp[parity], warps);
+    }
+    const float2 in = fma2(before.A, carry, before.B);
+    carry = fma2(total.A, carry, total.B);
     return in;
   }
   const uint32_t bar = smem_u32(&sm.bar[parity]);
@@ -509,7 +508,8 @@ __device__ __forceinline__ float2 enter_state(ScanSmem<W>& sm, const Map& mine, 
     h = fma2(m.A, h, m.B);
   }
   carry = h;
-  return apply(before, start, sm.warp[parity], warp);
+  if (any_infinite(start)) before.A = nonzero_product(before.A, sm.warp[parity], warp);
+  return fma2(before.A, start, before.B);
 }
 
 // Stages of the ring of tiles: what leaves two CTAs on an SM (about 100 KB each),
