@@ -13,6 +13,9 @@
  *   kda_linear                matrix product with scales, bias, activation and residual in its epilogue
  *   kda_scan_fwd / _bwd       gated linear recurrence (one state per channel) and its gradients
  *   kda_scan_step             the recurrence's single-token step on a slot pool
+ *   kda_kv_append             rotary positions, and keys and values into a paged cache (bf16 or 8 bits)
+ *   kda_attn_fwd              softmax attention over whole prompts (causal, grouped heads, packed, paged)
+ *   kda_attn_step             its single-token step on the cache, with a prefix that all rows share
  *   kda_chunk_fwd_noalloc     kda_chunk_fwd on a library-owned scratch buffer (no allocation)
  *   kda_version               library version string
  *   kda_selftest_*            diagnostics: bounded-wait failure path, tcgen05 round trip
@@ -71,7 +74,8 @@ typedef enum {
   KDA_DTYPE_BF16 = 0,  /* q, k, v, beta/b and o in bfloat16; tensor-core path */
   KDA_DTYPE_FP32 = 1,  /* q, k, v, beta/b and o in float32; CUDA-core fp32 path */
   KDA_DTYPE_E4M3 = 2   /* 8-bit floats (4 exponent, 3 mantissa bits, largest 448, no inf):
-                          kda_add_rmsnorm's output and kda_linear's operands only */
+                          kda_add_rmsnorm's output, kda_linear's operands and the
+                          attention's cache only */
 } kda_dtype;
 
 typedef enum {
@@ -533,6 +537,158 @@ typedef struct kda_scan_step_args {
   int32_t* err;               /* optional device status word */
 } kda_scan_step_args;
 kda_status kda_scan_step(const kda_scan_step_args* args, kda_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Softmax attention with a paged cache: the layers that hybrid models put between
+ * recurrent ones. No counterpart in the method's description; plain definitions.
+ *
+ * The cache. k_cache and v_cache are [pages, HKV, page_size, D], contiguous and
+ * 16-byte aligned, bf16 or e4m3; page_size is 16, 32, 64 or 128. Token t of a
+ * sequence lies at place t % page_size of page table[t / page_size] of the
+ * sequence's row of an int32 table (entries behind its last page are not read).
+ * With e4m3, k_scale and v_scale, fp32 [pages, HKV, page_size], hold a factor for
+ * each token and head (value ~ stored * scale); kda_kv_append writes powers of two.
+ * A page index outside 0 .. pages - 1 writes KDA_ERR_INVALID_ARG to err, and the
+ * tokens on it are left out.
+ *
+ * Heads: query head h uses key head h / (HQ / HKV); HQ is a multiple of HKV and at most
+ * KDA_ATTN_MAX_HEADS (KDA_ERR_UNSUPPORTED above). D is 64 or 128. Rows of q, k, v and outputs (a token's heads, contiguous) start on
+ * 16-byte boundaries; their strides are in elements.
+ * ------------------------------------------------------------------------- */
+
+#define KDA_ATTN_MAX_HEADS 1024
+
+/*
+ * Rotary positions, and the append to the cache. For every token t with
+ * p = positions[t] and its row [cos (rot / 2) | sin (rot / 2)] of cos_sin, each head
+ * x of q and k turns its first rot channels (rot even, 0 <= rot <= D) in pairs
+ *   (x_a, x_b) -> (x_a cos_i - x_b sin_i, x_b cos_i + x_a sin_i)
+ * with a = i, b = i + rot / 2, or a = 2i, b = 2i + 1 with KDA_KV_FLAG_INTERLEAVED.
+ * In fp32; q_out and k_out receive the result in bf16, and the cache at place
+ * slots[t] = page * page_size + offset the turned k and v, in bf16, or in e4m3 as
+ *   scale = the smallest power of two with max |x| <= 448 scale over the head (at
+ *           least 2^-110; 1 for zeros; NaN where the head has an infinity or a NaN)
+ *   stored = x / scale rounded to e4m3
+ *   q, q_out   [tokens, HQ, D]   bf16; both NULL (HQ is then ignored), or both given
+ *   k, v       [tokens, HKV, D]  bf16
+ *   k_out      [tokens, HKV, D]  bf16 or NULL
+ *   slots      [tokens]          int32, negative = padding (nothing is appended)
+ *   positions  [tokens]          int32 and cos_sin [max_positions, rot] fp32, 16-byte
+ *                                aligned; both NULL without rotation (rot = 0)
+ * q_out may be q and k_out may be k (same stride). A slot past the last page, or a
+ * position outside 0 .. max_positions - 1 of a token that is not padding, writes
+ * KDA_ERR_INVALID_ARG to err; such a token is not appended, and without a valid
+ * position its rows of q_out and k_out become zeros. Valid slots must be distinct
+ * (KDA_FLAG_CHECK_INDICES checks it, and needs err).
+ */
+#define KDA_KV_FLAG_INTERLEAVED 0x1u
+typedef struct kda_kv_append_args {
+  int32_t tokens, HQ, HKV, D;
+  int32_t pages, page_size;
+  int32_t cache_dtype;     /* KDA_DTYPE_BF16 or KDA_DTYPE_E4M3 */
+  int32_t rot, max_positions;
+  uint32_t flags;          /* KDA_KV_FLAG_INTERLEAVED, KDA_FLAG_CHECK_INDICES */
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* slots;
+  const int32_t* positions;
+  const float* cos_sin;
+  void* q_out;
+  void* k_out;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;          /* e4m3 only */
+  float* v_scale;
+  int32_t* err;            /* optional device status word */
+} kda_kv_append_args;
+kda_status kda_kv_append(const kda_kv_append_args* args, kda_stream_t stream);
+
+/*
+ * Softmax attention over whole prompts:
+ *   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i . k_j) / sum_j' exp(scale q_i . k_j')
+ * over the keys j that query i sees: all S_n of its sequence n, or, with
+ * KDA_ATTN_FLAG_CAUSAL, those up to i + S_n - T_n (the last query sees every key). A
+ * query that sees none gives o = 0 and lse = -inf.
+ *   q, o       [B, T, HQ, D]     bf16
+ *   lse        [B, T, HQ]        fp32 or NULL: log sum_j exp(scale q_i . k_j)
+ *   k, v       [B, S, HKV, D]    bf16, or, with block_table, the cache (bf16)
+ *   cu_seqlens, cu_seqlens_k [N + 1]  int32 device arrays, or NULL
+ *   block_table [N, table_width] int32 and seq_lens_k [N] int32, or NULL
+ * Without cu_seqlens there are N = B sequences of T queries (and S keys). With it,
+ * B is 1 and sequence n has the queries cu_seqlens[n] .. cu_seqlens[n + 1] - 1, and the
+ * keys that cu_seqlens_k gives in the same way (NULL: cu_seqlens for both, S = T). With
+ * block_table, sequence n has the first seq_lens_k[n] tokens of its pages as keys;
+ * cu_seqlens_k is NULL, and S and the strides of k and v are ignored. Each array starts
+ * at 0, never decreases and ends at T (or S) or before, and lengths are within
+ * 0 .. table_width * page_size; otherwise KDA_ERR_INVALID_ARG goes to err and the call
+ * does nothing. Rows of o and lse behind the last sequence are left as they were, and
+ * what stands behind a sequence's last key or in keys a query does not see, infinities
+ * and NaN among it, has no effect on that query. o overlaps no input.
+ * Products of bf16 on the tensor cores with fp32 sums; softmax in fp32; the weights
+ * p are rounded to bf16 for their product with v. scale is finite and > 0.
+ * Resources: 512 columns of tensor memory on each SM while the kernel runs.
+ */
+#define KDA_ATTN_FLAG_CAUSAL 0x1u
+typedef struct kda_attn_fwd_args {
+  int32_t B, T, S, N, HQ, HKV, D;
+  int32_t pages, page_size, table_width;  /* with block_table */
+  uint32_t flags;          /* KDA_ATTN_FLAG_CAUSAL */
+  float scale;
+  int64_t q_stride, k_stride, v_stride, o_stride;
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* cu_seqlens;
+  const int32_t* cu_seqlens_k;
+  const int32_t* block_table;
+  const int32_t* seq_lens_k;
+  void* o;
+  float* lse;
+  int32_t* err;            /* optional device status word */
+} kda_attn_fwd_args;
+kda_status kda_attn_fwd(const kda_attn_fwd_args* args, kda_stream_t stream);
+
+/*
+ * The single-token step: row b attends to the prefix_len tokens on the pages of
+ * prefix_table, which all rows share and which are read once for all of them, and to
+ * the seq_lens[b] tokens on the pages of its own row of block_table (its newest token
+ * among them; order does not matter to the sum).
+ *   q, o         [B, HQ, D]          bf16
+ *   lse          [B, HQ]             fp32 or NULL, as for kda_attn_fwd
+ *   k_cache, v_cache, k_scale, v_scale  the cache, bf16 or e4m3
+ *   block_table  [B, table_width]    int32
+ *   seq_lens     [B]                 int32; negative = padding row: o = 0, lse = -inf
+ *   prefix_table [prefix_pages]      int32, NULL without a prefix
+ * A row without any token gives o = 0, lse = -inf. A length above table_width *
+ * page_size writes KDA_ERR_INVALID_ARG to err and makes the row a padding row.
+ * o does not overlap q.
+ */
+typedef struct kda_attn_step_args {
+  int32_t B, HQ, HKV, D;
+  int32_t pages, page_size, table_width;
+  int32_t cache_dtype;     /* KDA_DTYPE_BF16 or KDA_DTYPE_E4M3 */
+  int32_t prefix_len, prefix_pages;
+  float scale;
+  int64_t q_stride, o_stride;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;    /* e4m3 only */
+  const float* v_scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* prefix_table;
+  void* o;
+  float* lse;
+  int32_t* err;            /* optional device status word */
+} kda_attn_step_args;
+/* Bytes of device scratch kda_attn_step needs: 0 without a prefix (also for arguments
+ * it refuses). */
+size_t kda_attn_step_workspace_size(const kda_attn_step_args* args);
+/* `workspace` is device memory of at least that size, 256-byte aligned (NULL for 0). */
+kda_status kda_attn_step(const kda_attn_step_args* args, void* workspace, size_t workspace_bytes, kda_stream_t stream);
 
 /*
  * Chunk forward for callers that cannot allocate device memory.

@@ -12,12 +12,15 @@ from ._lib import (  # noqa: F401
     chunk_count,
     chunk_workspace_size,
     kda_add_rmsnorm,
+    kda_attn_fwd,
+    kda_attn_step,
     kda_chunk_fwd,
     kda_chunk_output,
     kda_chunk_fwd_noalloc,
     kda_decode_conv_step,
     kda_decode_step,
     kda_head_rmsnorm,
+    kda_kv_append,
     kda_linear,
     kda_recurrent_step,
     kda_scan_bwd,

@@ -40,6 +40,9 @@ KDA_NORM_MAX_D = 32768
 KDA_ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "sigmoid": 3, "relu": 4}
 KDA_SCAN_GATES = {"log": 0, "logits": 1}
 KDA_SCAN_FLAG_COMPLEMENT = 0x1
+KDA_KV_FLAG_INTERLEAVED = 0x1
+KDA_ATTN_FLAG_CAUSAL = 0x1
+KDA_ATTN_MAX_HEADS = 1024
 
 
 class KdaError(RuntimeError):
@@ -150,6 +153,41 @@ class ScanStepArgs(ctypes.Structure):
     ]
 
 
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int32), ("HQ", ctypes.c_int32), ("HKV", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("cache_dtype", ctypes.c_int32), ("rot", ctypes.c_int32),
+        ("max_positions", ctypes.c_int32), ("flags", ctypes.c_uint32), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64), ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("cos_sin", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("err", ctypes.c_void_p),
+    ]
+
+
+class AttnFwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("S", ctypes.c_int32), ("N", ctypes.c_int32), ("HQ", ctypes.c_int32),
+        ("HKV", ctypes.c_int32), ("D", ctypes.c_int32), ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("table_width", ctypes.c_int32), ("flags", ctypes.c_uint32), ("scale", ctypes.c_float), ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64), ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("seq_lens_k", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("err", ctypes.c_void_p),
+    ]
+
+
+class AttnStepArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("HQ", ctypes.c_int32), ("HKV", ctypes.c_int32), ("D", ctypes.c_int32), ("pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("table_width", ctypes.c_int32), ("cache_dtype", ctypes.c_int32),
+        ("prefix_len", ctypes.c_int32), ("prefix_pages", ctypes.c_int32), ("scale", ctypes.c_float), ("q_stride", ctypes.c_int64),
+        ("o_stride", ctypes.c_int64), ("q", ctypes.c_void_p), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("prefix_table", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("err", ctypes.c_void_p),
+    ]
+
+
 class Tcgen05ProbeArgs(ctypes.Structure):
     _fields_ = [
         ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("layout", ctypes.c_int32), ("a_from_tmem", ctypes.c_int32),
@@ -161,7 +199,8 @@ class Tcgen05ProbeArgs(ctypes.Structure):
 EXPORTS = ("kda_chunk_fwd", "kda_chunk_output", "kda_chunk_fwd_noalloc", "kda_chunk_workspace_size", "kda_decode_step",
            "kda_decode_conv_step", "kda_recurrent_step", "kda_head_rmsnorm", "kda_add_rmsnorm", "kda_linear",
            "kda_linear_workspace_size", "kda_scan_fwd",
-           "kda_scan_bwd", "kda_scan_step", "kda_version",
+           "kda_scan_bwd", "kda_scan_step", "kda_kv_append", "kda_attn_fwd", "kda_attn_step", "kda_attn_step_workspace_size",
+           "kda_version",
            "kda_selftest_bounded_wait", "kda_selftest_tcgen05")
 
 
@@ -194,13 +233,18 @@ def load() -> ctypes.CDLL:
         lib.kda_decode_conv_step.argtypes = [ctypes.POINTER(DecodeConvArgs), ctypes.c_void_p]
         lib.kda_head_rmsnorm.restype = ctypes.c_int
         lib.kda_head_rmsnorm.argtypes = [ctypes.POINTER(RmsNormArgs), ctypes.c_void_p]
-        for name, struct in (("kda_add_rmsnorm", AddRmsNormArgs), ("kda_scan_fwd", ScanArgs), ("kda_scan_bwd", ScanBwdArgs), ("kda_scan_step", ScanStepArgs)):
+        for name, struct in (("kda_add_rmsnorm", AddRmsNormArgs), ("kda_scan_fwd", ScanArgs), ("kda_scan_bwd", ScanBwdArgs), ("kda_scan_step", ScanStepArgs),
+                             ("kda_kv_append", KvAppendArgs), ("kda_attn_fwd", AttnFwdArgs)):
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = [ctypes.POINTER(struct), ctypes.c_void_p]
         lib.kda_linear.restype = ctypes.c_int
         lib.kda_linear.argtypes = [ctypes.POINTER(LinearArgs), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
         lib.kda_linear_workspace_size.restype = ctypes.c_size_t
         lib.kda_linear_workspace_size.argtypes = [ctypes.POINTER(LinearArgs)]
+        lib.kda_attn_step.restype = ctypes.c_int
+        lib.kda_attn_step.argtypes = [ctypes.POINTER(AttnStepArgs), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        lib.kda_attn_step_workspace_size.restype = ctypes.c_size_t
+        lib.kda_attn_step_workspace_size.argtypes = [ctypes.POINTER(AttnStepArgs)]
         lib.kda_chunk_fwd_noalloc.restype = ctypes.c_int
         lib.kda_chunk_fwd_noalloc.argtypes = [ctypes.POINTER(ChunkArgs), ctypes.c_void_p]
         lib.kda_version.restype = ctypes.c_char_p
@@ -842,3 +886,200 @@ def kda_scan_step(x, gate, state_pool, indices, *, gate_mode="log", complement=F
     args.indices, args.err = _vec(indices, "indices", dev, (B,), torch.int32), _err_word(err, dev)
     _call(lib.kda_scan_step, args, dev, stream)
     return y
+
+
+# --- softmax attention with a paged cache ---
+
+
+def _head_rows(t, name, dev, dtype, shape):
+    """(pointer, row stride) of a tensor [..., heads, D] taken as rows of a token's heads:
+    the last two axes contiguous, the leading ones evenly spaced. None gives (None, 0)."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        _refuse(t, name, dev, dtype, shape)
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-2] * shape[-1]
+    if t.numel() and ((shape[-1] > 1 and t.stride(-1) != 1) or (shape[-2] > 1 and t.stride(-2) != shape[-1])):
+        raise ValueError(f"{name}: the last two axes must be contiguous")
+    ptr, step = _spaced_rows(t.select(-2, 0) if shape[-2] else t.flatten(-2), name)
+    return ptr, max(step, shape[-2] * shape[-1]) if t.numel() // max(1, shape[-2] * shape[-1]) <= 1 else step
+
+
+def _head_output(t, name, x, stream, shape):
+    """(tensor, pointer, row stride) of a bf16 output [..., heads, D]: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=torch.bfloat16, device=x.device) if stream is None else _empty(x, stream, shape, torch.bfloat16)
+        return t, t.data_ptr(), shape[-2] * shape[-1]
+    return t, *_head_rows(t, name, x.get_device(), torch.bfloat16, shape)
+
+
+def _cache(args, k_cache, v_cache, dev):
+    """Checks a cache [pages, HKV, page_size, D] and fills the struct's part on it. Returns its shape."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache: expected [pages, HKV, page_size, D]")
+    shape = k_cache.shape
+    if max(shape) > _I32_MAX:
+        _past_32_bits(**dict(zip(("pages", "HKV", "page_size", "D"), shape)))
+    args.pages, args.page_size = shape[0], shape[2]
+    return shape, _vec(k_cache, "k_cache", dev, shape, k_cache.dtype), _vec(v_cache, "v_cache", dev, shape, k_cache.dtype)
+
+
+def _cache_scales(args, k_scale, v_scale, dtype, shape, dev):
+    if (dtype == torch.float8_e4m3fn) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go with an 8-bit cache")
+    args.cache_dtype = _code(dtype)
+    args.k_scale, args.v_scale = _vec(k_scale, "k_scale", dev, shape[:3]), _vec(v_scale, "v_scale", dev, shape[:3])
+
+
+def kda_kv_append(k, v, slots, k_cache, v_cache, *, q=None, positions=None, cos_sin=None, interleaved=False, q_out=None,
+                  k_out=None, k_scale=None, v_scale=None, err=None, stream=None, check_indices=False):
+    """Rotary positions, and the append of keys and values to a paged cache.
+
+    k, v bf16 [..., HKV, D] and q (optional) bf16 [..., HQ, D], a token a leading index
+    (views of one packed projection will do); slots int32 [...] = page * page_size +
+    offset, negative for padding. k_cache, v_cache [pages, HKV, page_size, D], bf16 or
+    torch.float8_e4m3fn with k_scale, v_scale fp32 [pages, HKV, page_size], are updated in
+    place. positions int32 [...] and cos_sin fp32 [positions, rot] (cosines, then sines)
+    turn the first rot channels of q and k, in halves or in neighbouring pairs
+    (interleaved). q_out may be q; k_out, filled when given, may be k. check_indices (needs
+    err): a debug check that the valid slots are distinct. Returns (q_out or None, k_out)."""
+    lib = _lib or load()
+    dev = _device_of(k)
+    if k.dim() < 2:
+        raise ValueError("k: expected [..., HKV, D]")
+    args = KvAppendArgs()
+    cache, args.k_cache, args.v_cache = _cache(args, k_cache, v_cache, dev)
+    _cache_scales(args, k_scale, v_scale, k_cache.dtype, cache, dev)
+    lead, HKV, D = k.shape[:-2], cache[1], cache[3]
+    shape = lead + (HKV, D)
+    tokens = lead.numel()
+    if tokens > _I32_MAX:
+        _past_32_bits(tokens=tokens)
+    args.tokens, args.HKV, args.D = tokens, HKV, D
+    args.flags = (KDA_KV_FLAG_INTERLEAVED if interleaved else 0) | (KDA_FLAG_CHECK_INDICES if check_indices else 0)
+    args.k, args.k_stride = _head_rows(k, "k", dev, torch.bfloat16, shape)
+    args.v, args.v_stride = _head_rows(v, "v", dev, torch.bfloat16, shape)
+    args.slots, args.err = _vec(slots, "slots", dev, lead, torch.int32), _err_word(err, dev)
+    if (positions is None) != (cos_sin is None):
+        raise ValueError("positions and cos_sin go together")
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.shape[0] > _I32_MAX:
+            raise ValueError("cos_sin: expected [positions, rot]")
+        args.max_positions, args.rot = cos_sin.shape
+        args.cos_sin = _vec(cos_sin, "cos_sin", dev, cos_sin.shape)
+        if args.rot:
+            args.positions = _vec(positions, "positions", dev, lead, torch.int32)
+        else:
+            args.cos_sin = None
+    if q is not None:
+        if q.dim() < 2:
+            raise ValueError("q: expected [..., HQ, D]")
+        qshape = lead + (q.shape[-2], D)
+        args.HQ = q.shape[-2]
+        args.q, args.q_stride = _head_rows(q, "q", dev, torch.bfloat16, qshape)
+        q_out, args.q_out, args.q_out_stride = _head_output(q_out, "q_out", k, stream, qshape)
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    args.k_out, args.k_out_stride = _head_rows(k_out, "k_out", dev, torch.bfloat16, shape)
+    _call(lib.kda_kv_append, args, dev, stream)
+    return q_out, k_out
+
+
+def kda_attn_fwd(q, k, v, *, scale, causal=True, cu_seqlens=None, cu_seqlens_k=None, block_table=None, seq_lens_k=None,
+                 o=None, lse=None, err=None, stream=None):
+    """Softmax attention over whole prompts: q bf16 [B, T, HQ, D] on keys and values bf16
+    [B, S, HKV, D] (HQ a multiple of HKV, D 64 or 128), or on a bf16 cache [pages, HKV,
+    page_size, D] with block_table int32 [N, width] and seq_lens_k int32 [N].
+
+    cu_seqlens int32 [N + 1] packs N sequences along T (B = 1), cu_seqlens_k their keys
+    (default: the same). causal: query i of a sequence of T sees keys up to i + S - T.
+    lse (fp32 [B, T, HQ]) receives the logarithm of the sums when given. Rows of o and
+    lse behind the last sequence are left as they were. Returns o [B, T, HQ, D]."""
+    lib = _lib or load()
+    dev = _device_of(q)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k: expected [B, T, heads, D]")
+    B, T, HQ, D = shape = q.shape
+    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    args = AttnFwdArgs()
+    if block_table is not None:
+        if block_table.dim() != 2:
+            raise ValueError("block_table: expected [N, width]")
+        kshape, args.k, args.v = _cache(args, k, v, dev)
+        if k.dtype != torch.bfloat16:
+            raise ValueError(f"k: expected {torch.bfloat16}, got {k.dtype}")
+        HKV, S, width = kshape[1], 0, block_table.shape[1]
+        if kshape[3] != D:
+            raise ValueError(f"k: expected heads of {D}, got {kshape[3]}")
+        if width > _I32_MAX:
+            _past_32_bits(width=width)
+        args.table_width = width
+        args.block_table = _vec(block_table, "block_table", dev, (N, width), torch.int32)
+        args.seq_lens_k = _vec(seq_lens_k, "seq_lens_k", dev, (N,), torch.int32)
+        if seq_lens_k is None:
+            raise ValueError("seq_lens_k goes with block_table")
+    else:
+        if seq_lens_k is not None:
+            raise ValueError("seq_lens_k goes with block_table")
+        S, HKV = k.shape[1], k.shape[2]
+        args.k, args.k_stride = _head_rows(k, "k", dev, torch.bfloat16, (B, S, HKV, D))
+        args.v, args.v_stride = _head_rows(v, "v", dev, torch.bfloat16, (B, S, HKV, D))
+    if max(B, T, S, N, HQ, HKV) > _I32_MAX:
+        _past_32_bits(B=B, T=T, S=S, N=N, HQ=HQ, HKV=HKV)
+    args.B, args.T, args.S, args.N, args.HQ, args.HKV, args.D = B, T, S, N, HQ, HKV, D
+    args.flags, args.scale = KDA_ATTN_FLAG_CAUSAL if causal else 0, scale
+    args.q, args.q_stride = _head_rows(q, "q", dev, torch.bfloat16, shape)
+    args.cu_seqlens = _vec(cu_seqlens, "cu_seqlens", dev, (N + 1,), torch.int32)
+    args.cu_seqlens_k = _vec(cu_seqlens_k, "cu_seqlens_k", dev, (N + 1,), torch.int32)
+    o, args.o, args.o_stride = _head_output(o, "o", q, stream, shape)
+    args.lse, args.err = _vec(lse, "lse", dev, (B, T, HQ)), _err_word(err, dev)
+    _call(lib.kda_attn_fwd, args, dev, stream)
+    return o
+
+
+def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, *, scale, k_scale=None, v_scale=None, prefix_table=None,
+                  prefix_len=0, o=None, lse=None, workspace=None, err=None, stream=None):
+    """One token of each row, q bf16 [B, HQ, D], against a paged cache [pages, HKV,
+    page_size, D] (bf16, or torch.float8_e4m3fn with k_scale, v_scale fp32 [pages, HKV,
+    page_size]): row b attends to the first prefix_len tokens on the pages of prefix_table
+    (int32, shared by all rows and read once for them) and to its own seq_lens[b] tokens
+    (int32; negative = padding, o = 0) on the pages of block_table[b] (int32 [B, width]).
+
+    lse (fp32 [B, HQ]) receives the logarithm of the sums when given. With a prefix,
+    workspace (a CUDA uint8 tensor of kda_attn_step_workspace_size bytes) is made here
+    unless given. Returns o [B, HQ, D]."""
+    lib = _lib or load()
+    dev = _device_of(q)
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q: expected [B, HQ, D]; block_table: expected [B, width]")
+    B, HQ, D = shape = q.shape
+    args = AttnStepArgs()
+    cache, args.k_cache, args.v_cache = _cache(args, k_cache, v_cache, dev)
+    if cache[3] != D:
+        raise ValueError(f"k_cache: expected heads of {D}, got {cache[3]}")
+    _cache_scales(args, k_scale, v_scale, k_cache.dtype, cache, dev)
+    width = block_table.shape[1]
+    pages = 0 if prefix_table is None else prefix_table.numel()
+    if max(B, HQ, width, pages, prefix_len) > _I32_MAX:
+        _past_32_bits(B=B, HQ=HQ, width=width, prefix_pages=pages, prefix_len=prefix_len)
+    if prefix_len > 0 and pages * cache[2] < prefix_len:
+        raise ValueError(f"prefix_table: {pages} pages of {cache[2]} for {prefix_len} tokens")
+    args.B, args.HQ, args.HKV, args.D, args.table_width = B, HQ, cache[1], D, width
+    args.prefix_len, args.prefix_pages, args.scale = prefix_len, pages, scale
+    args.q, args.q_stride = _head_rows(q, "q", dev, torch.bfloat16, shape)
+    args.block_table = _vec(block_table, "block_table", dev, (B, width), torch.int32)
+    args.seq_lens = _vec(seq_lens, "seq_lens", dev, (B,), torch.int32)
+    args.prefix_table = _vec(prefix_table, "prefix_table", dev, (pages,), torch.int32)
+    o, args.o, args.o_stride = _head_output(o, "o", q, stream, shape)
+    args.lse, args.err = _vec(lse, "lse", dev, (B, HQ)), _err_word(err, dev)
+    if prefix_len <= 0:
+        _call(lib.kda_attn_step, args, dev, stream, None, 0)
+        return o
+    need = lib.kda_attn_step_workspace_size(args)
+    if need and workspace is None:
+        workspace = _empty(q, stream, (need,), torch.uint8)
+    elif need:
+        _vec(workspace, "workspace", dev, (max(need, workspace.numel()),), torch.uint8)
+    _call(lib.kda_attn_step, args, dev, stream, workspace.data_ptr() if need else None, need)
+    return o

@@ -1,0 +1,222 @@
+// Rotary positions and the append of keys and values to the paged cache.
+//
+// Bound by memory: each value is read once and written once (twice for the keys where
+// k_out is asked for). Lanes of D / 8 take a head with 8 channels (16 bytes) each; a
+// group of them keeps its channels' cosines and sines in registers and goes through
+// several heads of its token, all loads first. The pairs that a rotation turns are in
+// one lane (neighbours), or in two lanes of the group (halves, exchanged by shuffles)
+// where rot allows whole 8-channel pieces; other rot go through a per-channel path.
+#include "kda_elem.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHeadsAtOnce = 4;  // heads of a group whose loads are in flight together
+
+__device__ __forceinline__ void unpack8(const uint4& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3]), Bf16::pack(v[4], v[5]), Bf16::pack(v[6], v[7]));
+}
+
+// The smallest power of two s with m <= 448 s (448 = 1.75 * 2^8), at least 2^-110; 1
+// for 0, NaN for infinities and NaN. Division by it, and the product that gives a
+// stored value back, are exact.
+__device__ __forceinline__ float power_scale(float m) {
+  const uint32_t b = __float_as_uint(m);
+  if (b >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+  if (b == 0) return 1.f;
+  const int e = static_cast<int>(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __uint_as_float(static_cast<uint32_t>(e > 17 ? e : 17) << 23);  // (17: 2^-110)
+}
+
+// How a lane's 8 channels are turned.
+enum { kPlain = 0, kHalves = 1, kNeighbours = 2, kAny = 3 };
+
+template <int D, int MODE, bool E4>
+__global__ void __launch_bounds__(kThreads) kda_kv_append_kernel(const kda_kv_append_args p, int groups, int heads) {
+  constexpr int L = D / 8;  // lanes of a head
+  const int lane = threadIdx.x % L, c = 8 * lane;
+  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
+  const long long token = unit / groups;
+  const int group = static_cast<int>(unit % groups);
+  const bool live = token < p.tokens;
+  const long long t = live ? token : 0;
+
+  const int HQ = p.q ? p.HQ : 0;
+  int slot = live ? p.slots[t] : -1;
+  bool turn = true;
+  int pos = 0;
+  if (MODE != kPlain && live) {
+    pos = p.positions[t];
+    turn = pos >= 0 && pos < p.max_positions;
+    if (!turn) {
+      if (slot >= 0 && lane == 0 && group == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
+      pos = 0;
+      slot = -1;
+    }
+  }
+  if (slot >= p.pages * p.page_size) {
+    if (lane == 0 && group == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
+    slot = -1;
+  }
+  const int rot = MODE == kPlain ? 0 : p.rot, half = rot / 2;
+  const float* row = p.cos_sin + static_cast<long long>(pos) * rot;
+  const bool table = MODE != kPlain && p.max_positions > 0;
+
+  // value of channel c + i: x cs[i] + partner sn[i]
+  float cs[8], sn[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cs[i] = turn ? 1.f : 0.f, sn[i] = 0.f;
+  if (turn && table && c < rot) {
+    if (MODE == kHalves) {
+      const int at = c < half ? c : c - half;
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(row + at + i), b = *reinterpret_cast<const float4*>(row + half + at + i);
+        const float s = c < half ? -1.f : 1.f;
+        cs[i] = a.x, cs[i + 1] = a.y, cs[i + 2] = a.z, cs[i + 3] = a.w;
+        sn[i] = s * b.x, sn[i + 1] = s * b.y, sn[i + 2] = s * b.z, sn[i + 3] = s * b.w;
+      }
+    } else if (MODE == kNeighbours) {
+      const float4 a = *reinterpret_cast<const float4*>(row + c / 2), b = *reinterpret_cast<const float4*>(row + half + c / 2);
+      cs[0] = cs[1] = a.x, cs[2] = cs[3] = a.y, cs[4] = cs[5] = a.z, cs[6] = cs[7] = a.w;
+      sn[0] = -b.x, sn[1] = b.x, sn[2] = -b.y, sn[3] = b.y, sn[4] = -b.z, sn[5] = b.z, sn[6] = -b.w, sn[7] = b.w;
+    } else if (MODE == kAny) {
+      const bool pairs = p.flags & KDA_KV_FLAG_INTERLEAVED;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d = c + i;
+        if (d >= rot) continue;
+        const int at = pairs ? d / 2 : d < half ? d : d - half;
+        cs[i] = row[at];
+        sn[i] = (pairs ? d % 2 == 0 : d < half) ? -row[half + at] : row[half + at];
+      }
+    }
+  }
+  const int other = MODE == kHalves ? (c >= rot ? lane : c < half ? lane + half / 8 : lane - half / 8) : lane;
+
+  const int page = slot >= 0 ? slot / p.page_size : 0, off = slot >= 0 ? slot % p.page_size : 0;
+  for (int base = 0; base < heads; base += groups * kHeadsAtOnce) {  // (the same for a warp's lanes: they shuffle)
+    const int h0 = base + group;
+    uint4 raw[kHeadsAtOnce];
+    float partner[MODE == kAny ? kHeadsAtOnce : 1][8];
+    // all of a group's loads come before its stores: q_out may be q, and k_out k
+#pragma unroll
+    for (int u = 0; u < kHeadsAtOnce; ++u) {
+      const int h = h0 + u * groups;
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (live && h < heads) {
+        const __nv_bfloat16* x = h < HQ ? static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride + static_cast<long long>(h) * D
+                                 : h < HQ + p.HKV
+                                     ? static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride + static_cast<long long>(h - HQ) * D
+                                     : static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride + static_cast<long long>(h - HQ - p.HKV) * D;
+        raw[u] = *reinterpret_cast<const uint4*>(x + c);
+        if (MODE == kAny) {
+          const bool pairs = p.flags & KDA_KV_FLAG_INTERLEAVED;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int d = c + i;
+            const int q = d >= rot ? d : pairs ? (d ^ 1) : d < half ? d + half : d - half;
+            partner[u][i] = __bfloat162float(x[q]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < kHeadsAtOnce; ++u) {
+      const int h = h0 + u * groups;
+      const bool valid = live && h < heads, is_v = h >= HQ + p.HKV;
+      float x[8], y[8];
+      unpack8(raw[u], x);
+      if (MODE == kHalves) {
+        uint4 r;
+        r.x = __shfl_sync(0xffffffffu, raw[u].x, other, L);
+        r.y = __shfl_sync(0xffffffffu, raw[u].y, other, L);
+        r.z = __shfl_sync(0xffffffffu, raw[u].z, other, L);
+        r.w = __shfl_sync(0xffffffffu, raw[u].w, other, L);
+        unpack8(r, y);
+      } else if (MODE == kNeighbours) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+      } else if (MODE == kAny) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = partner[u][i];
+      }
+      // channels that are not turned keep their bits (infinities too: no 0 * partner)
+      if (MODE != kPlain && !is_v && (c < rot || !turn)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (!turn) x[i] = 0.f;
+          else if (c + i < rot) x[i] = x[i] * cs[i] + y[i] * sn[i];
+        }
+      }
+      if (valid && h < HQ) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.q_out) + t * p.q_out_stride + static_cast<long long>(h) * D + c;
+        *reinterpret_cast<uint4*>(o) = pack8(x);
+      } else if (valid && !is_v && p.k_out) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.k_out) + t * p.k_out_stride + static_cast<long long>(h - HQ) * D + c;
+        *reinterpret_cast<uint4*>(o) = pack8(x);
+      }
+      if (E4) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (valid && h >= HQ && slot >= 0) {
+          const float s = power_scale(m), inv = 1.f / s;
+          const long long at = (static_cast<long long>(page) * p.HKV + (is_v ? h - HQ - p.HKV : h - HQ)) * p.page_size + off;
+          uint2 b;
+          b.x = pack_e4m3x2(x[0] * inv, x[1] * inv) | pack_e4m3x2(x[2] * inv, x[3] * inv) << 16;
+          b.y = pack_e4m3x2(x[4] * inv, x[5] * inv) | pack_e4m3x2(x[6] * inv, x[7] * inv) << 16;
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + at * D + c) = b;
+          if (lane == 0) (is_v ? p.v_scale : p.k_scale)[at] = s;
+        }
+      } else if (valid && h >= HQ && slot >= 0) {
+        const long long at = (static_cast<long long>(page) * p.HKV + (is_v ? h - HQ - p.HKV : h - HQ)) * p.page_size + off;
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.v_cache : p.k_cache) + at * D + c) = pack8(x);
+      }
+    }
+  }
+}
+
+template <int D, int MODE>
+cudaError_t launch(const kda_kv_append_args& a, cudaStream_t s) {
+  const int heads = (a.q ? a.HQ : 0) + 2 * a.HKV;
+  // Groups of a token: each has up to kHeadsAtOnce heads, unless that is more groups
+  // than a CTA holds.
+  int groups = 1;
+  while (groups < kThreads / (D / 8) && groups * kHeadsAtOnce < heads) groups *= 2;
+  const long long units = static_cast<long long>(a.tokens) * groups, per = kThreads / (D / 8);
+  const long long grid = (units + per - 1) / per;
+  if (grid > INT32_MAX) return cudaErrorNotSupported;
+  if (a.cache_dtype == KDA_DTYPE_E4M3) kda_kv_append_kernel<D, MODE, true><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, groups, heads);
+  else kda_kv_append_kernel<D, MODE, false><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, groups, heads);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_mode(const kda_kv_append_args& a, cudaStream_t s) {
+  if (a.rot == 0) return launch<D, kPlain>(a, s);
+  const bool pairs = a.flags & KDA_KV_FLAG_INTERLEAVED;
+  if (pairs && a.rot % 8 == 0) return launch<D, kNeighbours>(a, s);
+  if (!pairs && a.rot % 16 == 0) return launch<D, kHalves>(a, s);
+  return launch<D, kAny>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const kda_kv_append_args& a, cudaStream_t s) {
+  return a.D == 64 ? launch_mode<64>(a, s) : launch_mode<128>(a, s);
+}
+
+}  // namespace kda

@@ -1,0 +1,452 @@
+// The single-token step of the softmax attention on a paged cache.
+//
+// A row's keys and values are read once, 2 D bytes of 8 bits or twice that of bf16 for
+// each token and key head, and serve the HQ / HKV query heads of the group: the bound is
+// HBM. The heads of a group (up to 16) are the rows of a warp-level tensor-core product
+// of m16n8k16, whose 16 tokens a step lie in one page: a warp loads them (4 KB of keys,
+// 4 KB of values at D = 128 in bf16) with 16-byte asynchronous copies, several steps
+// ahead, into shared memory of its own, keeps its own running maximum and sum, and no
+// barrier stands in its loop. The warps of a CTA, and the CTAs of a cluster that split
+// a row's tokens between them, join their results at the end, in a fixed order.
+//
+// 8-bit values become bf16 exactly (bits moved into place, times 2^120); a token's key
+// scale multiplies its scores and its value scale its weights, both in fp32. The weights
+// are rounded to bf16 for their product with the values; their sum is not.
+#include "kda_attn.cuh"
+#include "kda_cluster.cuh"
+
+namespace kda {
+namespace {
+
+using namespace attn;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kGroup = 16;       // tokens of a warp's step; divides every page
+constexpr int kMaxSplits = 16;
+constexpr float kTiny = 1.1754944e-38f;
+
+struct Params {
+  kda_attn_step_args a;
+  int G, head_tiles, splits;
+  const float* part_o;    // [parts, B, HQ, D]: the prefix's results, normalised
+  const float* part_lse;  // [parts, B, HQ], in powers of two
+  int parts;
+};
+
+template <int D, bool E4>
+struct Shape {
+  static constexpr int kRow = D * (E4 ? 1 : 2);                        // bytes of a token
+  static constexpr int kStage = 2 * kGroup * kRow + (E4 ? 128 : 0);    // keys, values, scales
+  static constexpr int kStages = E4 ? (D == 128 ? 5 : 6) : (D == 128 ? 3 : 6);
+  static constexpr int kWarpBytes = kStages * kStage > (D + 4) * 64 ? kStages * kStage : (D + 4) * 64;
+  static constexpr int kSmem = kWarps * kWarpBytes;
+};
+
+// 16-byte piece c of token row r: the pieces of 8 rows that an access takes together lie
+// in different banks.
+template <int ROW>
+__device__ __forceinline__ int piece(int r, int c) {
+  return r * ROW + ((ROW >= 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void copy16(unsigned char* dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 16 : 0));
+}
+
+// The even (low) and odd bytes of four e4m3 values as two bf16 each: the exponent and
+// mantissa bits in bf16's places stand for the value times 2^-120, subnormals included.
+__device__ __forceinline__ uint32_t times_2_120(uint32_t x) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7b807b80u));
+  return r;
+}
+__device__ __forceinline__ uint32_t even_bf16(uint32_t r) { return times_2_120(((r << 8) & 0x80008000u) | ((r << 4) & 0x07f007f0u)); }
+__device__ __forceinline__ uint32_t odd_bf16(uint32_t r) { return times_2_120((r & 0x80008000u) | ((r >> 4) & 0x07f007f0u)); }
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// One partial result (maximum m in powers of two, sum l, weighted values o) joined to
+// another. A part without keys has m = -inf and l = 0 and changes nothing.
+struct Joined {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float pm, float pl, float4 po) {
+    if (pm == -INFINITY && pl == 0.f) return;
+    const float top = pm > m ? pm : m;
+    const float a = m == -INFINITY ? 0.f : fmaxf(exp2f(m - top), kTiny);
+    const float b = pm == -INFINITY ? 0.f : pm == top ? 1.f : pm != pm ? pm : fmaxf(exp2f(pm - top), kTiny);
+    m = top;
+    l = l * a + pl * b;
+    o.x = o.x * a + po.x * b, o.y = o.y * a + po.y * b, o.z = o.z * a + po.z * b, o.w = o.w * a + po.w * b;
+  }
+};
+
+template <int D, bool E4>
+__global__ void __launch_bounds__(kThreads) kda_attn_step_kernel(const Params p) {
+  using Sh = Shape<D, E4>;
+  extern __shared__ __align__(128) unsigned char raw[];
+  __shared__ __align__(16) float cta_o[16][D];
+  __shared__ float cta_m[16], cta_l[16];
+  __shared__ float warp_m[kWarps][16], warp_l[kWarps][16];
+  __shared__ int cta_used;
+
+  const kda_attn_step_args& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int rank = static_cast<int>(blockIdx.x % p.splits);
+  long long unit = blockIdx.x / p.splits;
+  const int tile = static_cast<int>(unit % p.head_tiles);
+  unit /= p.head_tiles;
+  const int h = static_cast<int>(unit % a.HKV);
+  const int b = static_cast<int>(unit / a.HKV);
+  const int head0 = h * p.G + tile * 16, heads = min(16, p.G - tile * 16);
+
+  int len = a.seq_lens[b];
+  const bool row = len >= 0 && len <= a.table_width * a.page_size;
+  if (!row) {
+    if (len >= 0 && tid == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
+    len = 0;
+  }
+  if (tid == 0) cta_used = 0;
+
+  // queries as the products' A operand: heads g and g + 8; channels 16 k + 2 t, + 1 and
+  // + 8, + 9 for bf16 keys, the 4 from 16 k + 4 t for 8-bit ones (an order of the sum
+  // that gives a lane four consecutive bytes of a key)
+  uint32_t q[D / 16][4];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int head = g + 8 * r;
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_stride + static_cast<long long>(head0 + head) * D;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t lo = 0, hi = 0;
+      if (head < heads) {
+        if (E4) {
+          const uint2 w = *reinterpret_cast<const uint2*>(x + 16 * k + 4 * t);
+          lo = __byte_perm(w.x, w.y, 0x5410);  // channels 4t, 4t + 2 (even bytes of a key)
+          hi = __byte_perm(w.x, w.y, 0x7632);  // 4t + 1, 4t + 3
+        } else {
+          lo = *reinterpret_cast<const uint32_t*>(x + 16 * k + 2 * t);
+          hi = *reinterpret_cast<const uint32_t*>(x + 16 * k + 2 * t + 8);
+        }
+      }
+      q[k][r] = lo;
+      q[k][2 + r] = hi;
+    }
+  }
+
+  unsigned char* ring = raw + warp * Sh::kWarpBytes;
+  const int groups = (len + kGroup - 1) / kGroup;  // of 16 tokens; this warp has every (4 splits)-th
+  const int first = rank * kWarps + warp, step = p.splits * kWarps;
+  const int steps = groups > first ? (groups - first + step - 1) / step : 0;
+  const int32_t* table = a.block_table + static_cast<long long>(b) * a.table_width;
+  const float scale2 = a.scale * kLog2e;
+
+  // pages of the next 32 steps, one a lane
+  int pages = 0;
+  uint32_t bad = 0;  // by stage: its page is out of range
+  bool any_bad = false;
+  auto load = [&](int i) {
+    if (i % 32 == 0) {
+      const int at = i + lane;
+      pages = at < steps ? table[(first + at * step) * kGroup / a.page_size] : 0;
+    }
+    const int page = __shfl_sync(0xffffffffu, pages, i % 32), s = i % Sh::kStages;
+    const int tok = (first + i * step) * kGroup;
+    const bool good = page >= 0 && page < a.pages;
+    bad = good ? bad & ~(1u << s) : bad | 1u << s;
+    any_bad |= !good;
+    const long long at = good ? (static_cast<long long>(page) * a.HKV + h) * a.page_size + tok % a.page_size : 0;
+    const int real = good ? min(kGroup, len - tok) : 0;
+    unsigned char* dst = ring + s * Sh::kStage;
+    const unsigned char* ks = static_cast<const unsigned char*>(a.k_cache) + at * Sh::kRow;
+    const unsigned char* vs = static_cast<const unsigned char*>(a.v_cache) + at * Sh::kRow;
+    constexpr int C = Sh::kRow / 16;
+#pragma unroll
+    for (int j = 0; j < kGroup * C / 32; ++j) {
+      const int u = 32 * j + lane, r = u / C, c = u % C;
+      copy16(dst + piece<Sh::kRow>(r, c), ks + (r < real ? 16 * u : 0), r < real);
+      copy16(dst + kGroup * Sh::kRow + piece<Sh::kRow>(r, c), vs + (r < real ? 16 * u : 0), r < real);
+    }
+    if (E4 && lane < 8)
+      copy16(dst + 2 * kGroup * Sh::kRow + 16 * lane, (lane < 4 ? a.k_scale : a.v_scale) + at + (good ? 4 * (lane & 3) : 0), good);
+  };
+
+  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  bool used = false;
+
+#pragma unroll
+  for (int i = 0; i < Sh::kStages - 1; ++i) {
+    if (i < steps) load(i);
+    cp_async_commit();
+  }
+  for (int i = 0; i < steps; ++i) {
+    cp_async_wait<Sh::kStages - 2>();
+    __syncwarp();
+    const int s = i % Sh::kStages;
+    const unsigned char* ks = ring + s * Sh::kStage;
+    const unsigned char* vs = ks + kGroup * Sh::kRow;
+    const int real = (bad >> s & 1u) ? 0 : min(kGroup, len - (first + i * step) * kGroup);
+    used |= real > 0;
+
+    float sc[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+    if (E4) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(ks + piece<Sh::kRow>(8 * n + g, k) + 4 * t);
+          mma16816<Bf16>(sc[n], q[k], even_bf16(w), odd_bf16(w));
+        }
+      }
+    } else {
+      const int r = (lane & 7) + (lane >> 4) * 8, c = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t w[4];
+        ldsm_x4(w, ks + piece<Sh::kRow>(r, 2 * k + c));
+        mma16816<Bf16>(sc[0], q[k], w[0], w[1]);
+        mma16816<Bf16>(sc[1], q[k], w[2], w[3]);
+      }
+    }
+    // scores in powers of two; tokens that are not there weigh nothing
+    const float* scales = reinterpret_cast<const float*>(vs + kGroup * Sh::kRow);
+    float top[2] = {m[0], m[1]};
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int tok = 8 * n + 2 * t + (e & 1);
+        const float x = sc[n][e] * (E4 ? scales[tok] * scale2 : scale2);
+        sc[n][e] = tok < real ? x : -INFINITY;
+        top[e >> 1] = fmaxf(top[e >> 1], sc[n][e]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+    }
+    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+      float keep[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        keep[r] = m[r] == top[r] ? 1.f : m[r] == -INFINITY ? 0.f : fmaxf(ex2_approx(m[r] - top[r]), kTiny);
+        m[r] = top[r];
+        l[r] *= keep[r];
+      }
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) o[j][0] *= keep[0], o[j][1] *= keep[0], o[j][2] *= keep[1], o[j][3] *= keep[1];
+    }
+    float pr[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int tok = 8 * n + 2 * t + (e & 1);
+        const float x = sc[n][e], top_r = m[e >> 1];
+        // (a weight of a finite score stays above 0: an infinite value stays one)
+        float w = ex2_approx(x - (top_r == -INFINITY ? 0.f : top_r));
+        w = x == -INFINITY ? 0.f : w < kTiny ? kTiny : w;
+        l[e >> 1] += w;
+        pr[n][e] = E4 ? (tok < real ? w * scales[16 + tok] : 0.f) : w;
+      }
+    }
+    const uint32_t pa[4] = {Bf16::pack(pr[0][0], pr[0][1]), Bf16::pack(pr[0][2], pr[0][3]), Bf16::pack(pr[1][0], pr[1][1]),
+                            Bf16::pack(pr[1][2], pr[1][3])};
+    const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
+    if (E4) {
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {  // 32 channels: even and odd ones of each 16 in tiles of their own
+        uint32_t w[4];
+        ldsm_x4_trans(w, vs + piece<Sh::kRow>(r, 2 * j + c));
+        mma16816<Bf16>(o[4 * j], pa, even_bf16(w[0]), even_bf16(w[1]));
+        mma16816<Bf16>(o[4 * j + 1], pa, odd_bf16(w[0]), odd_bf16(w[1]));
+        mma16816<Bf16>(o[4 * j + 2], pa, even_bf16(w[2]), even_bf16(w[3]));
+        mma16816<Bf16>(o[4 * j + 3], pa, odd_bf16(w[2]), odd_bf16(w[3]));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t w[4];
+        ldsm_x4_trans(w, vs + piece<Sh::kRow>(r, 2 * j + c));
+        mma16816<Bf16>(o[2 * j], pa, w[0], w[1]);
+        mma16816<Bf16>(o[2 * j + 1], pa, w[2], w[3]);
+      }
+    }
+    __syncwarp();
+    if (i + Sh::kStages - 1 < steps) load(i + Sh::kStages - 1);
+    cp_async_commit();
+  }
+  cp_async_wait<0>();
+  if (any_bad && lane == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
+
+  // this warp's result: its ring now holds the weighted values [16][D + 4]
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+  }
+  __syncwarp();
+  float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int d = E4 ? 16 * (j / 2) + 4 * t + 2 * (e & 1) + (j & 1) : 8 * j + 2 * t + (e & 1);
+      mine[(g + 8 * (e >> 1)) * (D + 4) + d] = o[j][e];
+    }
+  }
+  if (t == 0) {
+    warp_m[warp][g] = m[0], warp_m[warp][g + 8] = m[1];
+    warp_l[warp][g] = l[0], warp_l[warp][g + 8] = l[1];
+  }
+  __syncthreads();
+  if (used && lane == 0) cta_used = 1;
+  constexpr int Q = D / 4;  // 4 channels at a time
+  for (int u = tid; u < heads * Q; u += kThreads) {
+    const int r = u / Q, d = 4 * (u % Q);
+    Joined j;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      j.add(warp_m[w][r], warp_l[w][r], *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(raw + w * Sh::kWarpBytes) + r * (D + 4) + d));
+    *reinterpret_cast<float4*>(&cta_o[r][d]) = j.o;
+    if (d == 0) cta_m[r] = j.m, cta_l[r] = j.l;
+  }
+  if (p.splits > 1) cluster_sync_all();
+  else __syncthreads();
+
+  // the splits' results and the prefix's, in order
+  for (int u = rank * kThreads + tid; u < heads * Q; u += p.splits * kThreads) {
+    const int r = u / Q, d = 4 * (u % Q), head = head0 + r;
+    Joined j;
+    int any = 0;
+    if (p.splits > 1) {
+      for (int s = 0; s < p.splits; ++s) {
+        any |= ld_shared_cluster_s32(mapa_shared(smem_u32(&cta_used), s));
+        j.add(ld_cluster(mapa_shared(smem_u32(&cta_m[r]), s)), ld_cluster(mapa_shared(smem_u32(&cta_l[r]), s)),
+              ld_cluster4(mapa_shared(smem_u32(&cta_o[r][d]), s)));
+      }
+    } else {
+      any = cta_used;
+      j.add(cta_m[r], cta_l[r], *reinterpret_cast<const float4*>(&cta_o[r][d]));
+    }
+    if (row) {
+      for (int s = 0; s < p.parts; ++s) {
+        const long long at = (static_cast<long long>(s) * a.B + b) * a.HQ + head;
+        const float lse = p.part_lse[at];
+        if (lse == -INFINITY) continue;  // no key
+        any = 1;
+        j.add(lse, 1.f, *reinterpret_cast<const float4*>(p.part_o + at * D + d));
+      }
+    }
+    // (keys whose scores are all -inf: 0 / 0, as the definition has it)
+    const float inv = 1.f / j.l;
+    uint2 w = make_uint2(0u, 0u);
+    if (any) w = make_uint2(Bf16::pack(j.o.x * inv, j.o.y * inv), Bf16::pack(j.o.z * inv, j.o.w * inv));
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + b * a.o_stride + static_cast<long long>(head) * D + d) = w;
+    if (a.lse && d == 0) a.lse[static_cast<long long>(b) * a.HQ + head] = any ? (j.m + log2f(j.l)) * kLn2 : -INFINITY;
+  }
+  if (p.splits > 1) cluster_sync_all();  // no CTA ends while another may read its results
+}
+
+template <int D, bool E4>
+cudaError_t launch(const Params& p, cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set{0};
+  auto kernel = kda_attn_step_kernel<D, E4>;
+  cudaError_t e = set_smem_limit_once(kernel, Shape<D, E4>::kSmem, smem_set);
+  if (e != cudaSuccess) return e;
+  if (p.splits > 8) {
+    static std::atomic<uint64_t> wide_set{0};
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+    if (bit == 0 || (wide_set.load(std::memory_order_acquire) & bit) == 0) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      wide_set.fetch_or(bit, std::memory_order_acq_rel);
+    }
+  }
+  const long long grid = static_cast<long long>(p.a.B) * p.a.HKV * p.head_tiles * p.splits;
+  if (grid > INT32_MAX) return cudaErrorNotSupported;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<D, E4>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(p.splits);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// The prefix, a warp for each row and query head.
+template <int D, bool E4>
+__global__ void __launch_bounds__(256) kda_attn_prefix_rows_kernel(const kda_attn_step_args a, float* part_o, float* part_lse) {
+  const int lane = threadIdx.x % 32;
+  const long long unit = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 32;
+  if (unit >= static_cast<long long>(a.B) * a.HQ) return;
+  const long long b = unit / a.HQ;
+  const int h = static_cast<int>(unit % a.HQ);
+  const Keys keys = {a.k_cache, a.v_cache, a.k_scale, a.v_scale, a.prefix_table, a.pages, a.page_size, a.HKV, 0, 0, 0};
+  float q[D / 32], o[D / 32], m, l;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c)
+    q[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[b * a.q_stride + static_cast<long long>(h) * D + lane + 32 * c]);
+  const int used = attend_row<D, E4>(q, keys, h / (a.HQ / a.HKV), a.prefix_len, a.scale * kLog2e, lane, a.err, m, l, o);
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) part_o[unit * D + lane + 32 * c] = used == 0 ? 0.f : o[c] / l;
+  if (lane == 0) part_lse[unit] = used == 0 ? -INFINITY : l == 0.f ? __uint_as_float(0x7fc00000u) : m + log2f(l);
+}
+
+template <int D, bool E4>
+cudaError_t launch_all(Params p, void* workspace, cudaStream_t s) {
+  if (p.a.prefix_len > 0) {
+    const long long rows = static_cast<long long>(p.a.B) * p.a.HQ;
+    float* lse = static_cast<float*>(workspace);
+    float* o = lse + (rows + 63) / 64 * 64;
+    kda_attn_prefix_rows_kernel<D, E4><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(p.a, o, lse);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    p.part_o = o, p.part_lse = lse, p.parts = 1;
+  }
+  return launch<D, E4>(p, s);
+}
+
+}  // namespace
+
+size_t attn_step_workspace_bytes(const kda_attn_step_args& a) {
+  const size_t rows = static_cast<size_t>(a.B) * a.HQ;
+  return ((rows + 63) / 64 * 64 + rows * a.D) * sizeof(float);
+}
+
+cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaStream_t s) {
+  Params p = {a, a.HQ / a.HKV, (a.HQ / a.HKV + 15) / 16, 1, nullptr, nullptr, 0};
+  // A cluster for each row and key head: enough CTAs for two on each of the 152 SMs, as
+  // long as a warp has 64 tokens or more of what the table has room for.
+  const long long units = static_cast<long long>(a.B) * a.HKV * p.head_tiles;
+  const long long room = static_cast<long long>(a.table_width) * a.page_size;
+  while (p.splits < kMaxSplits && units * p.splits < 2 * 152 && room >= 2 * p.splits * kWarps * 64) p.splits *= 2;
+  const bool e4 = a.cache_dtype == KDA_DTYPE_E4M3;
+  if (a.D == 64) return e4 ? launch_all<64, true>(p, workspace, s) : launch_all<64, false>(p, workspace, s);
+  return e4 ? launch_all<128, true>(p, workspace, s) : launch_all<128, false>(p, workspace, s);
+}
+
+}  // namespace kda

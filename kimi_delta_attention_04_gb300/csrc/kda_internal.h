@@ -112,6 +112,11 @@ cudaError_t launch_scan_fwd(const kda_scan_args& a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const kda_scan_bwd_args& a, cudaStream_t s);
 cudaError_t launch_scan_step(const kda_scan_step_args& a, cudaStream_t s);
 
+cudaError_t launch_kv_append(const kda_kv_append_args& a, cudaStream_t s);
+cudaError_t launch_attn_fwd(const kda_attn_fwd_args& a, cudaStream_t s);
+size_t attn_step_workspace_bytes(const kda_attn_step_args& a);  // the prefix's partial results
+cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaStream_t s);
+
 // Bytes of one (chunk, head) prep record.
 size_t record_bytes_tc(int d);           // bf16 tensor-core path, dk = dv = d
 size_t record_bytes_f32(int dk, int dv);  // fp32 path
