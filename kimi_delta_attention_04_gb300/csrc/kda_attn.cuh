@@ -27,20 +27,20 @@ __device__ __forceinline__ float e4m3_to_float(uint8_t b) {
   return __half2float(__half(h));
 }
 
-// Attention of one row of queries over keys [0, n), one warp, each key in turn with a
+// Attention of one row of queries over keys [begin, end), one warp, each key in turn with a
 // running maximum: lane l holds channels l + 32 i. Reads only what the row sees, and
 // follows the definition where infinities and NaN take part: a weight of a finite score
 // is held above 0 (2^-126), so that an infinite value stays one, and a score of -inf
 // weighs 0. q is the row already in fp32; scale2 = scale * log2(e). Returns how many
 // keys there were (those on pages out of range are left out).
 template <int D, bool E4>
-__device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& s, int h, int n, float scale2, int lane, int32_t* err,
+__device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& s, int h, int begin, int end, float scale2, int lane, int32_t* err,
                                            float& m, float& l, float (&o)[D / 32]) {
   m = -INFINITY, l = 0.f;
   int used = 0;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-  for (int j = 0; j < n; ++j) {
+  for (int j = begin; j < end; ++j) {
     long long ka, va;
     float kscale = 1.f, vscale = 1.f;
     if (s.table != nullptr) {

@@ -18,7 +18,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 bool rows_ok(const void* p, int64_t rows, int64_t cols, int64_t stride) {
   if (p == nullptr || !aligned(p, 16)) return false;
   if (rows > 1 && (stride < cols || stride % 8 != 0)) return false;
-  return stride >= 0 && stride <= (INT64_C(1) << 40) && rows <= (INT64_C(1) << 52) / (stride > cols ? stride : cols);
+  return stride >= 0 && stride < (INT64_C(1) << 39) && rows <= (INT64_C(1) << 52) / (stride > cols ? stride : cols);
 }
 
 kda_status done(cudaError_t e) {

@@ -1,82 +1,531 @@
-// Softmax attention over whole prompts: a warp for each query and head.
+// Softmax attention over whole prompts on the 5th-generation tensor cores, and the
+// shared prefix of the single-token step.
+//
+// A CTA takes 256 rows of queries, as two tiles of 128 that share every block of 128 keys
+// it loads. The rows of a tile are tokens x query heads of one key head (the largest
+// power of two of them that divides the group), so that a causal tile covers few tokens
+// and a group's heads share their keys' loads. For each tile and block
+//   S = Q K^T     128 x 128 into tensor memory (tcgen05.mma, both operands in shared memory)
+//   P = 2^(S c - m c)   a thread for each row: running maximum m and sum l in registers
+//   O += P V      P from tensor memory, where it takes S's place; V as it lies, MN-major
+// While one tile's rows are in the exponentials, the other's products run. O stays in
+// tensor memory and is scaled again only when a row's maximum has grown by more than
+// 2^8 (the weights stay below that, in bf16 and in the sums' fp32), which after the first
+// blocks is rare. P is rounded to bf16, as V is; l adds the unrounded weights.
+//
+// Roles: warps 0-3 and 4-7 the rows of the two tiles (200 registers a thread: a row's 128
+// scores are held at once), warp 8 issues the products, warp 9 the TMA loads.
+//
+// What a row does not see must not reach it: its scores are replaced before the maximum,
+// and the places behind a sequence's last key in the last block of V are zeroed in shared
+// memory (they may hold anything). A NaN or an infinity in the values of a key that some
+// rows of a tile see and others do not still meets a weight of 0 in the product; rows
+// whose result is not finite are therefore computed again by attend_row, which reads only
+// what the row sees.
 #include "kda_attn.cuh"
+#include "kda_attn_fwd.h"
+#include "kda_cluster.cuh"
+#include "kda_tcgen05.cuh"
+#include "kda_tma.h"
 
 namespace kda {
 namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 256;
-
-// Whether the arrays of lengths are as the contract has them (the whole block asks).
-__device__ __forceinline__ bool lengths_ok(const kda_attn_fwd_args& p) {
-  bool ok = true;
-  for (int i = threadIdx.x; i <= p.N; i += blockDim.x) {
-    if (p.cu_seqlens) ok &= i == 0 ? p.cu_seqlens[0] == 0 : p.cu_seqlens[i] >= p.cu_seqlens[i - 1] && p.cu_seqlens[i] <= p.T;
-    if (p.cu_seqlens_k) ok &= i == 0 ? p.cu_seqlens_k[0] == 0 : p.cu_seqlens_k[i] >= p.cu_seqlens_k[i - 1] && p.cu_seqlens_k[i] <= p.S;
-    if (p.seq_lens_k && i < p.N) ok &= p.seq_lens_k[i] >= 0 && p.seq_lens_k[i] <= p.table_width * p.page_size;
-  }
-  return __syncthreads_and(ok);
-}
+constexpr int kThreads = 384;
+constexpr int kRows = 128;            // rows of a tile; keys of a block
+constexpr int kHalf = kRows * 128;    // bytes of a block's 64 channels
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kGrow = 8.f;          // how far, in powers of two, a row's maximum may pass the one in use
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kda_attn_rows_kernel(const kda_attn_fwd_args p) {
-  if (!lengths_ok(p)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
+struct Shape {
+  static constexpr int kTile = kRows * D * 2;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kSmem = (2 + kStages) * kTile + 1024;
+  static constexpr uint32_t kO = 256;  // columns: S and P of the tiles at 0 and 128, O at 256 and 256 + D
+};
+
+struct Params {
+  kda_attn_fwd_args a;
+  AttnParts parts;
+  int G, Gp, lg, sub, heads;  // Gp = 2^lg query heads to a tile, sub such sets a key head, heads sets in all
+  int slots;                  // places for query tiles
+};
+
+struct Head {
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t full[8], empty[8];
+  uint32_t bad[8];            // by block, of the last 8: keys on pages that are out of range, a bit for each 16
+  uint32_t tmem_base;
+  int failed;
+};
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(smem_u32(bar), parity, kWaitNs); }
+
+// What one CTA works on.
+struct Item {
+  int n, hk, h0;            // sequence, key head, first query head
+  long long q0, k0;         // its first query and key
+  int T, S, shift;          // queries and keys; query i sees keys up to i + shift
+  int t0;                   // first query token of the CTA
+  int split, first, count[2];  // key blocks: first, and how many for each tile
+};
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+    kda_attn_fwd_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap) {
+  using Sh = Shape<D>;
+  extern __shared__ unsigned char raw[];
+  __shared__ Head sm;
+  const kda_attn_fwd_args& a = p.a;
+  unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
+  unsigned char* ring = tiles + 2 * Sh::kTile;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile_tokens = kRows >> p.lg, cta_tokens = 2 * tile_tokens;
+  const bool causal = a.flags & KDA_ATTN_FLAG_CAUSAL;
+
+  // The item: places in falling order, so that a causal prompt's long tiles start first.
+  Item it;
+  long long index = blockIdx.x;
+  it.split = static_cast<int>(index % p.parts.splits);
+  index /= p.parts.splits;
+  const int set = static_cast<int>(index % p.heads);
+  const int slot = p.slots - 1 - static_cast<int>(index / p.heads);
+  it.hk = set / p.sub;
+  it.h0 = it.hk * p.G + set % p.sub * p.Gp;
+
+  // The arrays of lengths: checked whole by every CTA, so that a call with bad ones does
+  // nothing. Sequence n's tiles have the places from cu_seqlens[n] / cta_tokens + n on,
+  // of which there are enough for it before the next sequence's.
+  bool ok = true;
+  int before = 0;  // sequences whose places start at this one or before it
+  const int entries = a.cu_seqlens || a.seq_lens_k ? a.N + 1 : 0;
+  for (int i0 = 0; i0 < entries; i0 += kThreads) {
+    const int i = i0 + tid;
+    bool starts = false;
+    if (i <= a.N) {
+      if (a.cu_seqlens) {
+        const int c = a.cu_seqlens[i];
+        ok &= i == 0 ? c == 0 : c >= a.cu_seqlens[i - 1] && c <= a.T;
+        starts = i < a.N && c >= 0 && c / cta_tokens + i <= slot;
+      }
+      if (a.cu_seqlens_k) ok &= i == 0 ? a.cu_seqlens_k[0] == 0 : a.cu_seqlens_k[i] >= a.cu_seqlens_k[i - 1] && a.cu_seqlens_k[i] <= a.S;
+      if (a.seq_lens_k && i < a.N) ok &= a.seq_lens_k[i] >= 0 && a.seq_lens_k[i] <= a.table_width * a.page_size;
+    }
+    before += __syncthreads_count(starts);
+  }
+  if (entries > 0 && !__syncthreads_and(ok)) {
+    if (blockIdx.x == 0 && tid == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
     return;
   }
-  const int lane = threadIdx.x % 32;
-  const long long unit = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / 32;
-  const long long tok = unit / p.HQ;
-  const int h = static_cast<int>(unit % p.HQ);
-  if (tok >= static_cast<long long>(p.B) * p.T) return;
-  int n, i, T, S;
-  Keys keys = {p.k, p.v, nullptr, nullptr, nullptr, p.pages, p.page_size, p.HKV, p.k_stride, p.v_stride, 0};
-  if (p.cu_seqlens) {
-    if (tok >= p.cu_seqlens[p.N]) return;
-    int lo = 0, hi = p.N - 1;  // the last n that starts at tok or before it
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (p.cu_seqlens[mid] <= tok) lo = mid; else hi = mid - 1;
-    }
-    n = lo;
-    i = static_cast<int>(tok) - p.cu_seqlens[n];
-    T = p.cu_seqlens[n + 1] - p.cu_seqlens[n];
-    const int32_t* ck = p.cu_seqlens_k ? p.cu_seqlens_k : p.cu_seqlens;
-    keys.first = ck[n];
-    S = ck[n + 1] - ck[n];
+  int tile;
+  if (a.cu_seqlens) {
+    it.n = before - 1;
+    it.q0 = a.cu_seqlens[it.n];
+    it.T = a.cu_seqlens[it.n + 1] - static_cast<int>(it.q0);
+    tile = slot - (static_cast<int>(it.q0) / cta_tokens + it.n);
+    const int32_t* ck = a.cu_seqlens_k ? a.cu_seqlens_k : a.cu_seqlens;
+    it.k0 = ck[it.n];
+    it.S = ck[it.n + 1] - static_cast<int>(it.k0);
   } else {
-    n = static_cast<int>(tok / p.T);
-    i = static_cast<int>(tok % p.T);
-    T = p.T;
-    S = p.S;
-    keys.first = static_cast<long long>(n) * S;
+    it.n = slot % a.N;
+    tile = slot / a.N;
+    it.T = a.T;
+    it.S = a.S;
+    it.q0 = static_cast<long long>(it.n) * it.T;
+    it.k0 = static_cast<long long>(it.n) * it.S;
   }
-  if (p.block_table) {
-    keys.table = p.block_table + static_cast<long long>(n) * p.table_width;
-    S = p.seq_lens_k[n];
+  if (PAGED) it.S = a.seq_lens_k ? a.seq_lens_k[it.n] : p.parts.keys;
+  if (static_cast<long long>(tile) * cta_tokens >= it.T) return;  // a place that no tile has
+  it.t0 = tile * cta_tokens;
+  it.shift = it.S - it.T;
+  const int blocks = (it.S + kRows - 1) / kRows, per = (blocks + p.parts.splits - 1) / p.parts.splits;
+  it.first = min(blocks, it.split * per);
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const int t = it.t0 + m * tile_tokens, last = min(t + tile_tokens, it.T) - 1;
+    const int seen = t >= it.T ? 0 : causal ? min(it.S, last + it.shift + 1) : it.S;
+    it.count[m] = max(0, min((max(seen, 0) + kRows - 1) / kRows, it.first + per) - it.first);
   }
-  const int seen = p.flags & KDA_ATTN_FLAG_CAUSAL ? min(S, i + S - T + 1) : S;
-  float q[D / 32], o[D / 32], m, l;
+  const int most = max(it.count[0], it.count[1]);
+
+  if (warp == 0) {
+    tc05::tmem_alloc(&sm.tmem_base, 512);
+    tc05::tmem_relinquish();
+  }
+  if (tid == 8 * 32) {
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(&sm.q_full[m], 1);
+      mbar_init(&sm.s_full[m], 1);
+      mbar_init(&sm.p_full[m], 4);
+      mbar_init(&sm.o_full[m], 1);
+    }
+    for (int s = 0; s < Sh::kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.failed = 0;
+    fence_mbarrier_init_cluster();
+  }
+  if (warp == 9 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&qmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+  }
+  __syncwarp();
+  tc05::fence_before_sync();
+  __syncthreads();
+  tc05::fence_after_sync();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 9) {
+      // ---- loads: the tiles' queries, then keys and values block by block ----
+      if (lane == 0) {
+        for (int m = 0; m < 2; ++m) {
+          if (it.count[m] == 0) continue;
+          mbar_arrive_expect_tx_local(&sm.q_full[m], Sh::kTile);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(tiles + m * Sh::kTile + c * kHalf, &qmap, 64 * c, it.h0, static_cast<int>(it.q0) + it.t0 + m * tile_tokens, &sm.q_full[m]);
+        }
+      }
+      const int box_keys = PAGED ? a.page_size : kRows;
+      const int boxes = kRows / box_keys * (D / 64), part = lane / (D / 64), half = lane % (D / 64);
+      bool going = true;
+      int loaded = 0;
+      for (int j = it.first; j < it.first + most && going; ++j) {
+        int y = it.hk, z = static_cast<int>(it.k0) + j * kRows;
+        uint32_t bad = 0;
+        if (PAGED) {
+          // a page that is out of range, or behind the last key, reads as zeros
+          const int tok = j * kRows + part * box_keys;
+          int page = -1;
+          if (lane < boxes && tok < it.S) {
+            page = a.block_table[static_cast<long long>(it.n) * a.table_width + tok / box_keys];
+            if (page >= a.pages) page = -1;
+          }
+          bad = __ballot_sync(0xffffffffu, lane < boxes && tok < it.S && page < 0);
+          if (bad != 0) {
+            if (lane == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
+            // a bit for each box to one for each 16 keys
+            bad = __ballot_sync(0xffffffffu, lane < 8 && (bad >> (lane * 16 / box_keys * (D / 64)) & 1u));
+          }
+          y = 0;
+          z = page < 0 ? -1 : page * a.HKV + it.hk;
+        }
+        for (int kv = 0; kv < 2 && going; ++kv, ++loaded) {
+          const int s = loaded % Sh::kStages;
+          if (loaded >= Sh::kStages) going = __all_sync(0xffffffffu, wait(&sm.empty[s], (loaded / Sh::kStages - 1) & 1));
+          if (!going) break;
+          if (lane == 0) {
+            // (the loads are at most 4 blocks ahead of the weights, which read this)
+            if (PAGED && kv == 0) sm.bad[(j - it.first) & 7] = bad;
+            mbar_arrive_expect_tx_local(&sm.full[s], Sh::kTile);
+          }
+          __syncwarp();
+          if (lane < boxes)
+            tma_load_3d(ring + s * Sh::kTile + half * kHalf + part * box_keys * 128, kv == 0 ? &kmap : &vmap, 64 * half, y, z, &sm.full[s]);
+        }
+      }
+      // no copy is left in flight when the CTA ends
+      for (int m = 0; m < 2; ++m)
+        if (it.count[m] > 0) going &= wait(&sm.q_full[m], 0);
+      for (int i = max(0, loaded - Sh::kStages); i < loaded; ++i) going &= wait(&sm.full[i % Sh::kStages], (i / Sh::kStages) & 1);
+      if (!going) sm.failed = 1;
+    } else if (warp == 8) {
+      // ---- products ----
+      const uint32_t qk = tc05::idesc_f16kind(kRows, kRows, true), pv = tc05::idesc_f16kind(kRows, D, true) | tc05::kIdescBMnMajor;
+      auto scores = [&](int m, int s) {  // S = Q K^T
+        const uint64_t q = tc05::smem_desc(smem_u32(tiles + m * Sh::kTile), 16, 1024, tc05::kSwizzle128B);
+        const uint64_t k = tc05::smem_desc(smem_u32(ring + s * Sh::kTile), 16, 1024, tc05::kSwizzle128B);
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c)
-    q[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[tok * p.q_stride + static_cast<long long>(h) * D + lane + 32 * c]);
-  const int used = attend_row<D, false>(q, keys, h / (p.HQ / p.HKV), seen, p.scale * kLog2e, lane, p.err, m, l, o);
+        for (int c = 0; c < D / 16; ++c) {
+          const uint32_t at = (c / 4 * kHalf + c % 4 * 32) >> 4;
+          tc05::mma_ss(tmem + m * kRows, q + at, k + at, qk, c > 0);
+        }
+        tc05::commit(&sm.s_full[m]);
+      };
+      auto values = [&](int m, int s, bool add) {  // O (+)= P V, 16 keys at a time
+        const uint64_t v = tc05::smem_desc(smem_u32(ring + s * Sh::kTile), kHalf, 1024, tc05::kSwizzle128B);
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c)
-    static_cast<__nv_bfloat16*>(p.o)[tok * p.o_stride + static_cast<long long>(h) * D + lane + 32 * c] =
-        __float2bfloat16_rn(used == 0 ? 0.f : o[c] / l);
-  if (p.lse && lane == 0) p.lse[tok * p.HQ + h] = used == 0 ? -INFINITY : (m + log2f(l)) * kLn2;
+        for (int c = 0; c < kRows / 16; ++c)
+          tc05::mma_ts(tmem + Sh::kO + m * D, tmem + m * kRows + 8 * c, v + ((c * 16 * 128) >> 4), pv, add || c > 0);
+      };
+      bool going = true;
+      if (most > 0) {
+        going = wait(&sm.full[0], 0);
+        for (int m = 0; m < 2; ++m) {
+          if (it.count[m] == 0) continue;
+          going = going && wait(&sm.q_full[m], 0);
+          going = __all_sync(0xffffffffu, going);
+          tc05::fence_after_sync();
+          if (going && lane == 0) scores(m, 0);
+        }
+        if (going && lane == 0) tc05::commit(&sm.empty[0]);
+      }
+      for (int i = 0; i < most && going; ++i) {
+        const int vi = 2 * i + 1, vs = vi % Sh::kStages, ki = 2 * i + 2, ks = ki % Sh::kStages;
+        bool v_there = false, k_there = false;
+        for (int m = 0; m < 2 && going; ++m) {
+          if (i >= it.count[m]) continue;
+          if (!v_there) {
+            going = __all_sync(0xffffffffu, wait(&sm.full[vs], (vi / Sh::kStages) & 1));
+            v_there = true;
+            const int live = it.S - (it.first + i) * kRows;  // keys there are in the block
+            if (going && live < kRows) {
+              // what stands behind the last key may be anything: zeros in its place
+              unsigned char* v = ring + vs * Sh::kTile;
+              for (int c = 0; c < D / 64; ++c)
+                for (int u = live * 8 + lane; u < kRows * 8; u += 32) *reinterpret_cast<uint4*>(v + c * kHalf + u * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          if (going) going = __all_sync(0xffffffffu, wait(&sm.p_full[m], i & 1));
+          if (!going) break;
+          tc05::fence_after_sync();
+          const bool both = m == 0 && i < it.count[1];           // the other tile still needs this block
+          const bool next = i + 1 < it.count[m], next_both = m == 0 && i + 1 < it.count[1];
+          if (lane == 0) {
+            values(m, vs, i > 0);
+            if (!next) tc05::commit(&sm.o_full[m]);
+            if (!both) tc05::commit(&sm.empty[vs]);
+          }
+          if (next) {
+            if (!k_there) {
+              going = __all_sync(0xffffffffu, wait(&sm.full[ks], (ki / Sh::kStages) & 1));
+              k_there = true;
+            }
+            tc05::fence_after_sync();
+            if (going && lane == 0) {
+              scores(m, ks);
+              if (!next_both) tc05::commit(&sm.empty[ks]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (!going) {  // products in flight end before their tensor memory is given back
+        if (lane == 0) {
+          sm.failed = 1;
+          tc05::commit(&sm.drain);
+        }
+        __syncwarp();
+        wait(&sm.drain, 0);
+      }
+    }
+  } else {
+    // ---- rows ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    const int m = warp >> 2, r = tid & (kRows - 1);
+    const int ti = it.t0 + m * tile_tokens + (r >> p.lg);
+    const bool valid = ti < it.T;
+    const int limit = !valid ? 0 : causal ? max(0, min(it.S, ti + it.shift + 1)) : it.S;  // keys this row sees
+    // blocks below this end need no mask (the tile's first row sees all of them)
+    const int open = causal ? min(it.S, it.t0 + m * tile_tokens + it.shift + 1) : it.S;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t s_at = lanes + m * kRows, o_at = lanes + Sh::kO + m * D;
+    const float c2 = a.scale * kLog2e;
+    float top = -INFINITY, sum = 0.f;
+    bool going = true;
+    for (int i = 0; i < it.count[m] && going; ++i) {
+      going = __all_sync(0xffffffffu, wait(&sm.s_full[m], i & 1));
+      if (!going) break;
+      tc05::fence_after_sync();
+      float s[128];
+      tc05::ld128_wait(s_at, s);
+      const int k0 = (it.first + i) * kRows;
+      const uint32_t bad = PAGED ? sm.bad[i & 7] : 0;
+      if (k0 + kRows > open || (PAGED && bad != 0)) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) s[j] = k0 + j < limit ? s[j] : -INFINITY;
+        if (PAGED && bad != 0) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (bad >> (j / 16) & 1u) s[j] = -INFINITY;
+        }
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int j = 4; j < 128; j += 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[j + e]);
+      }
+      const float high = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if (i == 0) {
+        top = high;
+      } else {
+        const bool grew = (high - top) * c2 > kGrow || (top == -INFINITY && high > top);
+        if (__any_sync(0xffffffffu, grew)) {
+          // (S of this block is there, so the product that last changed O is done)
+          const float now = grew ? high : top;
+          const float keep = grew ? ex2_approx((top - now) * c2) : 1.f;
+          top = now;
+          sum *= keep;
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tc05::ld32_wait(o_at + c, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] *= keep;
+            tc05::st32_wait(o_at + c, o);
+          }
+        }
+      }
+      const float base = top == -INFINITY ? 0.f : -top * c2;
+      const float2 c22 = make_float2(c2, c2), base2 = make_float2(base, base);
+      float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int h = 0; h < 128; h += 64) {
+        float w[32];  // weights in bf16 pairs
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float2 x = fma2(make_float2(s[h + 2 * j], s[h + 2 * j + 1]), c22, base2);
+          x.x = ex2_approx(x.x);
+          x.y = ex2_approx(x.y);
+          sum2[j & 1] = add2(sum2[j & 1], x);
+          w[j] = __uint_as_float(Bf16::pack(x.x, x.y));
+        }
+        tc05::st32(s_at + h / 2, w);
+      }
+      tc05::wait_st();
+      tc05::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(&sm.p_full[m]);
+      sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+    }
+    if (going && it.count[m] > 0) {
+      going = __all_sync(0xffffffffu, wait(&sm.o_full[m], 0));
+      tc05::fence_after_sync();
+    }
+    if (!going) {
+      if (lane == 0) sm.failed = 1;
+    } else {
+      const long long tok = it.q0 + ti, row = tok * a.HQ + it.h0 + (r & (p.Gp - 1));
+      const bool part = p.parts.o != nullptr;
+      const long long part_row = static_cast<long long>(it.split) * a.B * a.T * a.HQ + row;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + tok * a.o_stride + static_cast<long long>(it.h0 + (r & (p.Gp - 1))) * D;
+      const bool some = it.count[m] > 0 && limit > it.first * kRows;  // this row has keys here
+      const float inv = 1.f / sum;
+      bool finite = true;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (it.count[m] > 0) tc05::ld32_wait(o_at + c, o);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          o[j] = some ? o[j] * inv : 0.f;
+          finite &= fabsf(o[j]) < INFINITY;
+        }
+        if (!valid) continue;
+        if (part) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(p.parts.o + part_row * D + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+            *reinterpret_cast<uint4*>(out + c + j) = make_uint4(Bf16::pack(o[j], o[j + 1]), Bf16::pack(o[j + 2], o[j + 3]),
+                                                                Bf16::pack(o[j + 4], o[j + 5]), Bf16::pack(o[j + 6], o[j + 7]));
+        }
+      }
+      const float lse2 = some ? top * c2 + log2f(sum) : -INFINITY;
+      if (valid && part) p.parts.lse[part_row] = lse2;
+      if (valid && !part && a.lse) a.lse[row] = lse2 * kLn2;
+      // rows that infinities or NaN took part in, one by one
+      uint32_t again = __ballot_sync(0xffffffffu, valid && some && !finite);
+      while (again != 0) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        const long long stok = __shfl_sync(0xffffffffu, tok, src);
+        const int shead = __shfl_sync(0xffffffffu, it.h0 + (r & (p.Gp - 1)), src);
+        const int end = min(__shfl_sync(0xffffffffu, limit, src), (it.first + it.count[m]) * kRows);
+        const Keys keys = {a.k, a.v, nullptr, nullptr, PAGED ? a.block_table + static_cast<long long>(it.n) * a.table_width : nullptr,
+                           a.pages, a.page_size, a.HKV, a.k_stride, a.v_stride, it.k0};
+        float q[D / 32], o[D / 32], rm, rl;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          q[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[stok * a.q_stride + static_cast<long long>(shead) * D + lane + 32 * c]);
+        const int used = attend_row<D, false>(q, keys, it.hk, it.first * kRows, end, c2, lane, a.err, rm, rl, o);
+        const long long srow = stok * a.HQ + shead;
+        const long long spart = static_cast<long long>(it.split) * a.B * a.T * a.HQ + srow;
+        const float l2 = used == 0 ? -INFINITY : rl == 0.f ? __uint_as_float(0x7fc00000u) : rm + log2f(rl);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const float x = used == 0 ? 0.f : o[c] / rl;
+          if (part) p.parts.o[spart * D + lane + 32 * c] = x;
+          else static_cast<__nv_bfloat16*>(a.o)[stok * a.o_stride + static_cast<long long>(shead) * D + lane + 32 * c] = __float2bfloat16_rn(x);
+        }
+        if (lane == 0 && part) p.parts.lse[spart] = l2;
+        if (lane == 0 && !part && a.lse) a.lse[srow] = l2 * kLn2;
+      }
+    }
+  }
+  __syncwarp();
+  tc05::fence_before_sync();
+  __syncthreads();
+  tc05::fence_after_sync();
+  if (tid == 0 && sm.failed) set_err(a.err, KDA_ERR_TIMEOUT);
+  if (warp == 0) tc05::tmem_dealloc(tmem, 512);
+}
+
+// The largest power of two that divides the group, as its exponent, up to 128 heads.
+int group_bits(int group) {
+  int lg = 0;
+  while (lg < 7 && group % (2 << lg) == 0) ++lg;
+  return lg;
+}
+
+template <int D, bool PAGED>
+cudaError_t launch(const Params& p, cudaStream_t s) {
+  const kda_attn_fwd_args& a = p.a;
+  CUtensorMap qmap, kmap, vmap;
+  const long long queries = static_cast<long long>(a.B) * a.T;
+  bool ok = encode_heads(&qmap, a.q, D, a.HQ, D, queries, a.q_stride, static_cast<unsigned>(p.Gp), static_cast<unsigned>(kRows >> p.lg));
+  if (PAGED) {
+    // a cache without pages is never read (every page is out of range): any map will do
+    const long long rows = static_cast<long long>(a.pages) * a.HKV, page = static_cast<long long>(a.page_size) * D;
+    const bool none = a.pages == 0;
+    ok = ok && encode_heads(&kmap, none ? a.q : a.k, D, a.page_size, D, none ? 1 : rows, page, static_cast<unsigned>(a.page_size), 1) &&
+         encode_heads(&vmap, none ? a.q : a.v, D, a.page_size, D, none ? 1 : rows, page, static_cast<unsigned>(a.page_size), 1);
+  } else {
+    const long long keys = static_cast<long long>(a.B) * a.S;
+    const bool none = keys == 0;
+    ok = ok && encode_heads(&kmap, none ? a.q : a.k, D, a.HKV, D, none ? 1 : keys, a.k_stride, 1, kRows) &&
+         encode_heads(&vmap, none ? a.q : a.v, D, a.HKV, D, none ? 1 : keys, a.v_stride, 1, kRows);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  const long long grid = static_cast<long long>(p.slots) * p.heads * p.parts.splits;
+  if (grid > INT32_MAX) return cudaErrorNotSupported;
+  static std::atomic<uint64_t> smem_set{0};
+  const cudaError_t e = set_smem_limit_once(kda_attn_fwd_kernel<D, PAGED>, Shape<D>::kSmem, smem_set);
+  if (e != cudaSuccess) return e;
+  kda_attn_fwd_kernel<D, PAGED><<<static_cast<unsigned>(grid), kThreads, Shape<D>::kSmem, s>>>(p, qmap, kmap, vmap);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_fwd(const kda_attn_fwd_args& a, cudaStream_t s) {
-  const long long units = static_cast<long long>(a.B) * a.T * a.HQ, grid = (units + kThreads / 32 - 1) / (kThreads / 32);
-  if (grid > INT32_MAX) return cudaErrorNotSupported;
-  if (a.D == 64) kda_attn_rows_kernel<64><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
-  else kda_attn_rows_kernel<128><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+int attn_tile_tokens(int group) { return 2 * kRows >> group_bits(group); }
+
+cudaError_t launch_attn_prompts(const kda_attn_fwd_args& a, const AttnParts& parts, cudaStream_t s) {
+  Params p = {a, parts, a.HQ / a.HKV, 0, 0, 0, 0, 0};
+  p.lg = group_bits(p.G);
+  p.Gp = 1 << p.lg;
+  p.sub = p.G / p.Gp;
+  p.heads = a.HKV * p.sub;
+  const int tokens = 2 * kRows >> p.lg;
+  const long long slots = a.cu_seqlens ? static_cast<long long>(a.T) / tokens + a.N : (static_cast<long long>(a.T) + tokens - 1) / tokens * a.N;
+  if (slots > INT32_MAX) return cudaErrorNotSupported;
+  p.slots = static_cast<int>(slots);
+  if (a.block_table) return a.D == 64 ? launch<64, true>(p, s) : launch<128, true>(p, s);
+  return a.D == 64 ? launch<64, false>(p, s) : launch<128, false>(p, s);
 }
+
+cudaError_t launch_attn_fwd(const kda_attn_fwd_args& a, cudaStream_t s) { return launch_attn_prompts(a, AttnParts{nullptr, nullptr, 1, 0}, s); }
 
 }  // namespace kda

@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(256) kda_attn_prefix_rows_kernel(const kda_att
 #pragma unroll
   for (int c = 0; c < D / 32; ++c)
     q[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[b * a.q_stride + static_cast<long long>(h) * D + lane + 32 * c]);
-  const int used = attend_row<D, E4>(q, keys, h / (a.HQ / a.HKV), a.prefix_len, a.scale * kLog2e, lane, a.err, m, l, o);
+  const int used = attend_row<D, E4>(q, keys, h / (a.HQ / a.HKV), 0, a.prefix_len, a.scale * kLog2e, lane, a.err, m, l, o);
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) part_o[unit * D + lane + 32 * c] = used == 0 ? 0.f : o[c] / l;
   if (lane == 0) part_lse[unit] = used == 0 ? -INFINITY : l == 0.f ? __uint_as_float(0x7fc00000u) : m + log2f(l);

@@ -50,6 +50,19 @@ bool encode_rows(CUtensorMap* m, const void* base, size_t elem, long long cols, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_heads(CUtensorMap* m, const void* base, int D, long long heads, long long head_stride, long long rows, long long row_stride,
+                  unsigned box_heads, unsigned box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const long long pitch = rows == 1 ? heads * head_stride : row_stride;  // (one row has no stride to get wrong)
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(pitch) * 2};
+  const cuuint32_t box[3] = {64u, box_heads, box_rows};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t encode_input_maps(const ChunkCall& c, TmaInputMaps* m) {
   const long long tokens = c.geo.cu_seqlens ? static_cast<long long>(c.geo.T)
                                             : static_cast<long long>(c.geo.N) * c.geo.T;

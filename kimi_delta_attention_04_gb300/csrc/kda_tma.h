@@ -25,4 +25,10 @@ cudaError_t encode_input_maps(const ChunkCall& c, TmaInputMaps* m);
 bool encode_rows(CUtensorMap* m, const void* base, size_t elem, long long cols, long long rows, long long ld,
                  unsigned box_rows);
 
+// Host: a 3-D map [rows][heads][D] of bf16 (strides in elements; base and strides 16-byte
+// aligned), box box_rows x box_heads x 64 channels in the 128-byte swizzle; places past
+// the ends read as zero.
+bool encode_heads(CUtensorMap* m, const void* base, int D, long long heads, long long head_stride, long long rows, long long row_stride,
+                  unsigned box_heads, unsigned box_rows);
+
 }  // namespace kda
