@@ -15,17 +15,10 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 struct Keys {
   const void* k;
   const void* v;
-  const float* k_scale;  // [pages, HKV, page_size], 8-bit caches only
-  const float* v_scale;
   const int32_t* table;  // nullptr: rows
   int pages, page_size, HKV;
   long long k_stride, v_stride, first;
 };
-
-__device__ __forceinline__ float e4m3_to_float(uint8_t b) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(b, __NV_E4M3);
-  return __half2float(__half(h));
-}
 
 // Attention of one row of queries over keys [begin, end), one warp, each key in turn with a
 // running maximum: lane l holds channels l + 32 i. Reads only what the row sees, and
@@ -33,7 +26,7 @@ __device__ __forceinline__ float e4m3_to_float(uint8_t b) {
 // is held above 0 (2^-126), so that an infinite value stays one, and a score of -inf
 // weighs 0. q is the row already in fp32; scale2 = scale * log2(e). Returns how many
 // keys there were (those on pages out of range are left out).
-template <int D, bool E4>
+template <int D>
 __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& s, int h, int begin, int end, float scale2, int lane, int32_t* err,
                                            float& m, float& l, float (&o)[D / 32]) {
   m = -INFINITY, l = 0.f;
@@ -42,7 +35,6 @@ __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& 
   for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
   for (int j = begin; j < end; ++j) {
     long long ka, va;
-    float kscale = 1.f, vscale = 1.f;
     if (s.table != nullptr) {
       const int page = s.table[j / s.page_size];
       if (page < 0 || page >= s.pages) {
@@ -51,7 +43,6 @@ __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& 
       }
       const long long at = (static_cast<long long>(page) * s.HKV + h) * s.page_size + j % s.page_size;
       ka = va = at * D;
-      if (E4) kscale = s.k_scale[at], vscale = s.v_scale[at];
     } else {
       ka = (s.first + j) * s.k_stride + static_cast<long long>(h) * D;
       va = (s.first + j) * s.v_stride + static_cast<long long>(h) * D;
@@ -61,15 +52,10 @@ __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& 
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const int d = lane + 32 * i;
-      if (E4) {
-        x += q[i] * e4m3_to_float(static_cast<const uint8_t*>(s.k)[ka + d]);
-        v[i] = e4m3_to_float(static_cast<const uint8_t*>(s.v)[va + d]) * vscale;
-      } else {
-        x += q[i] * __bfloat162float(static_cast<const __nv_bfloat16*>(s.k)[ka + d]);
-        v[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(s.v)[va + d]);
-      }
+      x += q[i] * __bfloat162float(static_cast<const __nv_bfloat16*>(s.k)[ka + d]);
+      v[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(s.v)[va + d]);
     }
-    x = warp_sum(x) * (kscale * scale2);
+    x = warp_sum(x) * scale2;
     const float top = x > m ? x : m;  // (a NaN leaves m and makes p and l NaN)
     const float keep = m == top ? 1.f : m == -INFINITY ? 0.f : fmaxf(exp2f(m - top), 1.1754944e-38f);
     float p = exp2f(x - (top == -INFINITY ? 0.f : top));

@@ -444,13 +444,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long stok = __shfl_sync(0xffffffffu, tok, src);
         const int shead = __shfl_sync(0xffffffffu, it.h0 + (r & (p.Gp - 1)), src);
         const int end = min(__shfl_sync(0xffffffffu, limit, src), (it.first + it.count[m]) * kRows);
-        const Keys keys = {a.k, a.v, nullptr, nullptr, PAGED ? a.block_table + static_cast<long long>(it.n) * a.table_width : nullptr,
+        const Keys keys = {a.k, a.v, PAGED ? a.block_table + static_cast<long long>(it.n) * a.table_width : nullptr,
                            a.pages, a.page_size, a.HKV, a.k_stride, a.v_stride, it.k0};
         float q[D / 32], o[D / 32], rm, rl;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
           q[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[stok * a.q_stride + static_cast<long long>(shead) * D + lane + 32 * c]);
-        const int used = attend_row<D, false>(q, keys, it.hk, it.first * kRows, end, c2, lane, a.err, rm, rl, o);
+        const int used = attend_row<D>(q, keys, it.hk, it.first * kRows, end, c2, lane, a.err, rm, rl, o);
         const long long srow = stok * a.HQ + shead;
         const long long spart = static_cast<long long>(it.split) * a.B * a.T * a.HQ + srow;
         const float l2 = used == 0 ? -INFINITY : rl == 0.f ? __uint_as_float(0x7fc00000u) : rm + log2f(rl);

@@ -13,6 +13,7 @@
 // scale multiplies its scores and its value scale its weights, both in fp32. The weights
 // are rounded to bf16 for their product with the values; their sum is not.
 #include "kda_attn.cuh"
+#include "kda_attn_fwd.h"
 #include "kda_cluster.cuh"
 
 namespace kda {
@@ -397,45 +398,99 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// The prefix, a warp for each row and query head.
-template <int D, bool E4>
-__global__ void __launch_bounds__(256) kda_attn_prefix_rows_kernel(const kda_attn_step_args a, float* part_o, float* part_lse) {
-  const int lane = threadIdx.x % 32;
-  const long long unit = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 32;
-  if (unit >= static_cast<long long>(a.B) * a.HQ) return;
-  const long long b = unit / a.HQ;
-  const int h = static_cast<int>(unit % a.HQ);
-  const Keys keys = {a.k_cache, a.v_cache, a.k_scale, a.v_scale, a.prefix_table, a.pages, a.page_size, a.HKV, 0, 0, 0};
-  float q[D / 32], o[D / 32], m, l;
+// ---- the prefix ----
+// Its keys meet the queries of all rows: products of 128 rows, which the prompt kernel
+// computes as one sequence of B queries that sees every key, split over its blocks.
+
+// An 8-bit prefix in bf16 (exact with scales that are powers of two), as pages 0, 1, ...
+// of a cache of its own; table[i] is i, or -1 where the prefix's page is out of range.
+template <int D>
+__global__ void __launch_bounds__(256) kda_attn_prefix_bf16_kernel(const kda_attn_step_args a, __nv_bfloat16* k, __nv_bfloat16* v, int32_t* table) {
+  const int page = a.prefix_table[blockIdx.x], h = blockIdx.y;
+  const bool good = page >= 0 && page < a.pages;
+  if (h == 0 && threadIdx.x == 0) table[blockIdx.x] = good ? static_cast<int>(blockIdx.x) : -1;
+  if (!good) return;
+  const long long from = (static_cast<long long>(page) * a.HKV + h) * a.page_size, to = (static_cast<long long>(blockIdx.x) * a.HKV + h) * a.page_size;
+  for (int u = threadIdx.x; u < 2 * a.page_size * (D / 8); u += 256) {
+    const bool of_v = u >= a.page_size * (D / 8);
+    const int w = of_v ? u - a.page_size * (D / 8) : u, t = w / (D / 8), c = w % (D / 8) * 8;
+    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(of_v ? a.v_cache : a.k_cache) + (from + t) * D + c);
+    const float s = (of_v ? a.v_scale : a.k_scale)[from + t];
+    const uint32_t in[2] = {x.x, x.y};
+    uint32_t out[4];
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c)
-    q[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[b * a.q_stride + static_cast<long long>(h) * D + lane + 32 * c]);
-  const int used = attend_row<D, E4>(q, keys, h / (a.HQ / a.HKV), 0, a.prefix_len, a.scale * kLog2e, lane, a.err, m, l, o);
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) part_o[unit * D + lane + 32 * c] = used == 0 ? 0.f : o[c] / l;
-  if (lane == 0) part_lse[unit] = used == 0 ? -INFINITY : l == 0.f ? __uint_as_float(0x7fc00000u) : m + log2f(l);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t e = even_bf16(in[i]), o = odd_bf16(in[i]);  // values 0 and 2, 1 and 3
+      out[2 * i] = Bf16::pack(__uint_as_float(e << 16) * s, __uint_as_float(o << 16) * s);
+      out[2 * i + 1] = Bf16::pack(__uint_as_float(e & 0xffff0000u) * s, __uint_as_float(o & 0xffff0000u) * s);
+    }
+    *reinterpret_cast<uint4*>((of_v ? v : k) + (to + t) * D + c) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
 }
 
-template <int D, bool E4>
-cudaError_t launch_all(Params p, void* workspace, cudaStream_t s) {
-  if (p.a.prefix_len > 0) {
-    const long long rows = static_cast<long long>(p.a.B) * p.a.HQ;
-    float* lse = static_cast<float*>(workspace);
-    float* o = lse + (rows + 63) / 64 * 64;
-    kda_attn_prefix_rows_kernel<D, E4><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(p.a, o, lse);
+// How the prefix's work is laid out, and where its results lie in the workspace.
+struct Prefix {
+  int splits = 0, pages = 0;
+  size_t lse = 0, o = 0, table = 0, k = 0, v = 0, bytes = 0;
+};
+
+Prefix prefix_of(const kda_attn_step_args& a) {
+  Prefix x;
+  if (a.prefix_len == 0) return x;
+  // Splits that keep the 152 SMs busy: rounds of CTAs, each with its share of the blocks
+  // and 4 blocks' time for what a CTA does besides.
+  const int G = a.HQ / a.HKV, tokens = attn_tile_tokens(G), packed = tokens > 256 ? 1 : 256 / tokens;
+  const long long tiles = (static_cast<long long>(a.B) + tokens - 1) / tokens * a.HKV * (G / packed);
+  const int blocks = (a.prefix_len + 127) / 128;
+  long long best = 0;
+  for (int s = 1; s <= 32 && s <= blocks; ++s) {
+    const long long cost = (tiles * s + 151) / 152 * ((blocks + s - 1) / s + 4);
+    if (x.splits == 0 || cost < best) {
+      x.splits = s;
+      best = cost;
+    }
+  }
+  x.pages = (a.prefix_len - 1) / a.page_size + 1;
+  const size_t rows = static_cast<size_t>(a.B) * a.HQ * x.splits;
+  const auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
+  x.o = up(rows * sizeof(float));
+  x.table = x.o + up(rows * a.D * sizeof(float));
+  x.bytes = x.table;
+  if (a.cache_dtype == KDA_DTYPE_E4M3) {
+    const size_t cache = static_cast<size_t>(x.pages) * a.HKV * a.page_size * a.D * 2;
+    x.k = x.table + up(x.pages * sizeof(int32_t));
+    x.v = x.k + cache;
+    x.bytes = x.v + cache;
+  }
+  return x;
+}
+
+cudaError_t launch_prefix(const kda_attn_step_args& a, const Prefix& x, unsigned char* w, cudaStream_t s) {
+  kda_attn_fwd_args f = {};
+  f.B = f.N = 1;
+  f.T = a.B, f.HQ = a.HQ, f.HKV = a.HKV, f.D = a.D;
+  f.page_size = a.page_size, f.table_width = x.pages;
+  f.scale = a.scale;
+  f.q = a.q, f.q_stride = a.q_stride, f.err = a.err;
+  f.pages = a.pages, f.k = a.k_cache, f.v = a.v_cache, f.block_table = a.prefix_table;
+  if (a.cache_dtype == KDA_DTYPE_E4M3) {
+    if (a.HKV > 65535) return cudaErrorNotSupported;
+    __nv_bfloat16 *k = reinterpret_cast<__nv_bfloat16*>(w + x.k), *v = reinterpret_cast<__nv_bfloat16*>(w + x.v);
+    int32_t* table = reinterpret_cast<int32_t*>(w + x.table);
+    const dim3 grid(static_cast<unsigned>(x.pages), static_cast<unsigned>(a.HKV));
+    if (a.D == 64) kda_attn_prefix_bf16_kernel<64><<<grid, 256, 0, s>>>(a, k, v, table);
+    else kda_attn_prefix_bf16_kernel<128><<<grid, 256, 0, s>>>(a, k, v, table);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    p.part_o = o, p.part_lse = lse, p.parts = 1;
+    f.pages = x.pages, f.k = k, f.v = v, f.block_table = table;
   }
-  return launch<D, E4>(p, s);
+  const AttnParts parts = {reinterpret_cast<float*>(w + x.o), reinterpret_cast<float*>(w + x.lse), x.splits, a.prefix_len};
+  return launch_attn_prompts(f, parts, s);
 }
 
 }  // namespace
 
-size_t attn_step_workspace_bytes(const kda_attn_step_args& a) {
-  const size_t rows = static_cast<size_t>(a.B) * a.HQ;
-  return ((rows + 63) / 64 * 64 + rows * a.D) * sizeof(float);
-}
+size_t attn_step_workspace_bytes(const kda_attn_step_args& a) { return prefix_of(a).bytes; }
 
 cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaStream_t s) {
   Params p = {a, a.HQ / a.HKV, (a.HQ / a.HKV + 15) / 16, 1, nullptr, nullptr, 0};
@@ -444,9 +499,16 @@ cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaS
   const long long units = static_cast<long long>(a.B) * a.HKV * p.head_tiles;
   const long long room = static_cast<long long>(a.table_width) * a.page_size;
   while (p.splits < kMaxSplits && units * p.splits < 2 * 152 && room >= 2 * p.splits * kWarps * 64) p.splits *= 2;
+  const Prefix x = prefix_of(a);
+  if (x.splits > 0) {
+    unsigned char* w = static_cast<unsigned char*>(workspace);
+    const cudaError_t e = launch_prefix(a, x, w, s);
+    if (e != cudaSuccess) return e;
+    p.part_o = reinterpret_cast<const float*>(w + x.o), p.part_lse = reinterpret_cast<const float*>(w + x.lse), p.parts = x.splits;
+  }
   const bool e4 = a.cache_dtype == KDA_DTYPE_E4M3;
-  if (a.D == 64) return e4 ? launch_all<64, true>(p, workspace, s) : launch_all<64, false>(p, workspace, s);
-  return e4 ? launch_all<128, true>(p, workspace, s) : launch_all<128, false>(p, workspace, s);
+  if (a.D == 64) return e4 ? launch<64, true>(p, s) : launch<64, false>(p, s);
+  return e4 ? launch<128, true>(p, s) : launch<128, false>(p, s);
 }
 
 }  // namespace kda
