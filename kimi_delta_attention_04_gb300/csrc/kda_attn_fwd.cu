@@ -35,6 +35,7 @@ using namespace attn;
 
 constexpr int kThreads = 384;
 constexpr int kRows = 128;            // rows of a tile; keys of a block
+constexpr int kFirst = 64;            // keys of a block whose products start before the others' weights are there
 constexpr int kHalf = kRows * 128;    // bytes of a block's 64 channels
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 8.f;          // how far, in powers of two, a row's maximum may pass the one in use
@@ -55,14 +56,46 @@ struct Params {
 };
 
 struct Head {
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], tail_there, tail_zero, drain;  // p_full: a block's first kFirst keys, and the rest
   uint64_t full[8], empty[8];
   uint32_t bad[8];            // by block, of the last 8: keys on pages that are out of range, a bit for each 16
   uint32_t tmem_base;
   int failed;
 };
 
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(smem_u32(bar), parity, kWaitNs); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// One lane of the warp, which all enter.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e != 0;
+}
+
+// Waits for a phase, for a limited time. (Without the hint of mbar_try_wait, which lets the
+// thread sleep: 8192 tokens, 32 heads of 128 took 407 us with it and 395 without.)
+__device__ __forceinline__ bool try_now(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t b = smem_u32(bar);
+  if (try_now(b, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!try_now(b, parity)) {
+    if (global_timer_ns() - t0 > kWaitNs) return false;
+  }
+  return true;
+}
 
 // What one CTA works on.
 struct Item {
@@ -72,6 +105,82 @@ struct Item {
   int t0;                   // first query token of the CTA
   int split, first, count[2];  // key blocks: first, and how many for each tile
 };
+
+// The products of both tiles, issued by one thread. (It is elected: operands are then as
+// the tensor core's instructions want them and an issue takes the products' own time, 64
+// cycles each, where a thread chosen by its lane took 140. A warp for each tile's products
+// interleaves them, and each waits longer for its own: 444 us instead of 395 for 8192
+// tokens and 32 heads of 128.)
+template <int D>
+__device__ __forceinline__ void issue_products(Head& sm, const Item& it, unsigned char* tiles) {
+  using Sh = Shape<D>;
+  constexpr uint32_t qk = tc05::idesc_f16kind(kRows, kRows, true), pv = tc05::idesc_f16kind(kRows, D, true) | tc05::kIdescBMnMajor;
+  const int count0 = it.count[0], count1 = it.count[1], blocks = max(count0, count1), keys = it.S - it.first * kRows;
+  const uint64_t desc = tc05::smem_desc(0, 16, 1024, tc05::kSwizzle128B), desc_mn = tc05::smem_desc(0, kHalf, 1024, tc05::kSwizzle128B);
+  const uint32_t q_base = smem_u32(tiles) >> 4, r_base = q_base + (2 * Sh::kTile >> 4);
+  auto scores = [&](int m, int s) {  // S = Q K^T
+    const uint64_t q = desc + (q_base + m * (Sh::kTile >> 4)), k = desc + (r_base + s * (Sh::kTile >> 4));
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      const uint32_t at = (c / 4 * kHalf + c % 4 * 32) >> 4;
+      tc05::mma_ss(m * kRows, q + at, k + at, qk, c > 0);
+    }
+    tc05::commit(&sm.s_full[m]);
+  };
+  auto values = [&](int m, int s, int from, int to, bool add) {  // O (+)= P V over keys 16 from .. 16 to - 1
+    const uint64_t v = desc_mn + (r_base + s * (Sh::kTile >> 4));
+#pragma unroll
+    for (int c = from; c < to; ++c) tc05::mma_ts(Sh::kO + m * D, m * kRows + 8 * c, v + ((c * 16 * 128) >> 4), pv, add || c > 0);
+  };
+  bool going = true;
+  if (blocks > 0) {
+    going = wait(&sm.full[0], 0);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if ((m == 0 ? count0 : count1) == 0) continue;
+      going = going && wait(&sm.q_full[m], 0);
+      tc05::fence_after_sync();
+      if (going) scores(m, 0);
+    }
+    tc05::commit(&sm.empty[0]);
+  }
+  int vs = 1, v_phase = 0;  // stage and phase of the block's values; the next block's keys come after them
+  for (int i = 0; i < blocks && going; ++i) {
+    int ks = vs + 1, k_phase = v_phase;
+    if (ks == Sh::kStages) ks = 0, k_phase ^= 1;
+    going = wait(&sm.full[vs], v_phase);
+    if (i + 1 < blocks) going = going && wait(&sm.full[ks], k_phase);
+    const bool tail = keys < (i + 1) * kRows;  // the sequence's last block is not full: zeros behind its last key
+    if (tail && going) mbar_arrive_local(&sm.tail_there);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int count = m == 0 ? count0 : count1;
+      if (i >= count || !going) continue;
+      const bool last_v = m == 1 || i >= count1, last_k = m == 1 || i + 1 >= count1;  // no other tile needs the block
+      going = wait(&sm.p_full[m][0], i & 1);
+      if (tail) going = going && wait(&sm.tail_zero, 0);
+      tc05::fence_after_sync();
+      if (going) values(m, vs, 0, kFirst / 16, i > 0);
+      going = going && wait(&sm.p_full[m][1], i & 1);
+      tc05::fence_after_sync();
+      if (going) values(m, vs, kFirst / 16, kRows / 16, true);
+      if (i + 1 < count) {
+        if (going) scores(m, ks);
+        if (last_k) tc05::commit(&sm.empty[ks]);
+      } else {
+        tc05::commit(&sm.o_full[m]);
+      }
+      if (last_v) tc05::commit(&sm.empty[vs]);
+    }
+    vs = ks + 1, v_phase = k_phase;
+    if (vs == Sh::kStages) vs = 0, v_phase ^= 1;
+  }
+  if (!going) {  // products in flight end before their tensor memory is given back
+    sm.failed = 1;
+    tc05::commit(&sm.drain);
+    wait(&sm.drain, 0);
+  }
+}
 
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -160,13 +269,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int m = 0; m < 2; ++m) {
       mbar_init(&sm.q_full[m], 1);
       mbar_init(&sm.s_full[m], 1);
-      mbar_init(&sm.p_full[m], 4);
+      mbar_init(&sm.p_full[m][0], 4);
+      mbar_init(&sm.p_full[m][1], 4);
       mbar_init(&sm.o_full[m], 1);
     }
     for (int s = 0; s < Sh::kStages; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
     }
+    mbar_init(&sm.tail_there, 1);
+    mbar_init(&sm.tail_zero, 1);
     mbar_init(&sm.drain, 1);
     sm.failed = 0;
     fence_mbarrier_init_cluster();
@@ -180,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc05::fence_before_sync();
   __syncthreads();
   tc05::fence_after_sync();
-  const uint32_t tmem = sm.tmem_base;
+  // (all 512 columns: the allocation starts at 0)
+  const uint32_t tmem = 0;
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -238,85 +351,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, loaded - Sh::kStages); i < loaded; ++i) going &= wait(&sm.full[i % Sh::kStages], (i / Sh::kStages) & 1);
       if (!going) sm.failed = 1;
     } else if (warp == 8) {
-      // ---- products ----
-      const uint32_t qk = tc05::idesc_f16kind(kRows, kRows, true), pv = tc05::idesc_f16kind(kRows, D, true) | tc05::kIdescBMnMajor;
-      auto scores = [&](int m, int s) {  // S = Q K^T
-        const uint64_t q = tc05::smem_desc(smem_u32(tiles + m * Sh::kTile), 16, 1024, tc05::kSwizzle128B);
-        const uint64_t k = tc05::smem_desc(smem_u32(ring + s * Sh::kTile), 16, 1024, tc05::kSwizzle128B);
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint32_t at = (c / 4 * kHalf + c % 4 * 32) >> 4;
-          tc05::mma_ss(tmem + m * kRows, q + at, k + at, qk, c > 0);
-        }
-        tc05::commit(&sm.s_full[m]);
-      };
-      auto values = [&](int m, int s, bool add) {  // O (+)= P V, 16 keys at a time
-        const uint64_t v = tc05::smem_desc(smem_u32(ring + s * Sh::kTile), kHalf, 1024, tc05::kSwizzle128B);
-#pragma unroll
-        for (int c = 0; c < kRows / 16; ++c)
-          tc05::mma_ts(tmem + Sh::kO + m * D, tmem + m * kRows + 8 * c, v + ((c * 16 * 128) >> 4), pv, add || c > 0);
-      };
-      bool going = true;
-      if (most > 0) {
-        going = wait(&sm.full[0], 0);
-        for (int m = 0; m < 2; ++m) {
-          if (it.count[m] == 0) continue;
-          going = going && wait(&sm.q_full[m], 0);
-          going = __all_sync(0xffffffffu, going);
-          tc05::fence_after_sync();
-          if (going && lane == 0) scores(m, 0);
-        }
-        if (going && lane == 0) tc05::commit(&sm.empty[0]);
-      }
-      for (int i = 0; i < most && going; ++i) {
-        const int vi = 2 * i + 1, vs = vi % Sh::kStages, ki = 2 * i + 2, ks = ki % Sh::kStages;
-        bool v_there = false, k_there = false;
-        for (int m = 0; m < 2 && going; ++m) {
-          if (i >= it.count[m]) continue;
-          if (!v_there) {
-            going = __all_sync(0xffffffffu, wait(&sm.full[vs], (vi / Sh::kStages) & 1));
-            v_there = true;
-            const int live = it.S - (it.first + i) * kRows;  // keys there are in the block
-            if (going && live < kRows) {
-              // what stands behind the last key may be anything: zeros in its place
-              unsigned char* v = ring + vs * Sh::kTile;
-              for (int c = 0; c < D / 64; ++c)
-                for (int u = live * 8 + lane; u < kRows * 8; u += 32) *reinterpret_cast<uint4*>(v + c * kHalf + u * 16) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-          }
-          if (going) going = __all_sync(0xffffffffu, wait(&sm.p_full[m], i & 1));
-          if (!going) break;
-          tc05::fence_after_sync();
-          const bool both = m == 0 && i < it.count[1];           // the other tile still needs this block
-          const bool next = i + 1 < it.count[m], next_both = m == 0 && i + 1 < it.count[1];
-          if (lane == 0) {
-            values(m, vs, i > 0);
-            if (!next) tc05::commit(&sm.o_full[m]);
-            if (!both) tc05::commit(&sm.empty[vs]);
-          }
-          if (next) {
-            if (!k_there) {
-              going = __all_sync(0xffffffffu, wait(&sm.full[ks], (ki / Sh::kStages) & 1));
-              k_there = true;
-            }
-            tc05::fence_after_sync();
-            if (going && lane == 0) {
-              scores(m, ks);
-              if (!next_both) tc05::commit(&sm.empty[ks]);
-            }
-          }
-          __syncwarp();
-        }
-      }
-      if (!going) {  // products in flight end before their tensor memory is given back
-        if (lane == 0) {
-          sm.failed = 1;
-          tc05::commit(&sm.drain);
-        }
+      if (elect_one()) issue_products<D>(sm, it, tiles);
+    } else if (warp == 10) {
+      // ---- what stands behind the last key may be anything: zeros in its place ----
+      const int block = (it.S - 1) / kRows - it.first, live = it.S - (it.first + block) * kRows;
+      if (most > 0 && block == most - 1 && live < kRows) {
+        const int s = (2 * block + 1) % Sh::kStages;
+        if (!__all_sync(0xffffffffu, wait(&sm.tail_there, 0))) sm.failed = 1;
+        unsigned char* v = ring + s * Sh::kTile;
+        for (int c = 0; c < D / 64; ++c)
+          for (int u = live * 8 + lane; u < kRows * 8; u += 32) *reinterpret_cast<uint4*>(v + c * kHalf + u * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
         __syncwarp();
-        wait(&sm.drain, 0);
+        if (lane == 0) mbar_arrive_local(&sm.tail_zero);
       }
     }
   } else {
@@ -352,11 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int j = 4; j < 128; j += 4) {
+      for (int j = 4; j < 124; j += 8) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[j + e]);
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[j + 2 * e], s[j + 2 * e + 1]);
       }
-      const float high = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const float high = fmaxf(max3(max3(mx[0], s[124], s[125]), max3(mx[1], s[126], s[127]), mx[2]), mx[3]);
       if (i == 0) {
         top = high;
       } else {
@@ -381,22 +428,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 c22 = make_float2(c2, c2), base2 = make_float2(base, base);
       float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int h = 0; h < 128; h += 64) {
-        float w[32];  // weights in bf16 pairs
+      for (int h = 0; h < 128; h += 32) {
+        float w[16];  // weights in bf16 pairs
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < 16; ++j) {
           float2 x = fma2(make_float2(s[h + 2 * j], s[h + 2 * j + 1]), c22, base2);
           x.x = ex2_approx(x.x);
           x.y = ex2_approx(x.y);
           sum2[j & 1] = add2(sum2[j & 1], x);
           w[j] = __uint_as_float(Bf16::pack(x.x, x.y));
         }
-        tc05::st32(s_at + h / 2, w);
+        tc05::st16(s_at + h / 2, w);
+        if (h + 32 == kFirst || h + 32 == kRows) {  // the products of these keys may start
+          tc05::wait_st();
+          tc05::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(&sm.p_full[m][h + 32 == kRows]);
+        }
       }
-      tc05::wait_st();
-      tc05::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_local(&sm.p_full[m]);
       sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
     }
     if (going && it.count[m] > 0) {
