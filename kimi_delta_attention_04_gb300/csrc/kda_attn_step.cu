@@ -9,9 +9,10 @@
 // barrier stands in its loop. The warps of a CTA, and the CTAs of a cluster that split
 // a row's tokens between them, join their results at the end, in a fixed order.
 //
-// 8-bit values become bf16 exactly (bits moved into place, times 2^120); a token's key
-// scale multiplies its scores and its value scale its weights, both in fp32. The weights
-// are rounded to bf16 for their product with the values; their sum is not.
+// 8-bit keys and values become f16, exactly; a token's key scale multiplies its scores in
+// fp32, and the logarithm of its value scale is added to the score that its weight for the
+// product with the values comes from. These weights are rounded to f16, and to bf16 with a
+// bf16 cache; the sum takes unrounded ones.
 #include "kda_attn.cuh"
 #include "kda_attn_fwd.h"
 #include "kda_cluster.cuh"
@@ -21,10 +22,9 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;       // tokens of a warp's step; divides every page
 constexpr int kMaxSplits = 16;
+constexpr int kBusy = 304, kLong = 2048, kLeast = 64;
 constexpr float kTiny = 1.1754944e-38f;
 
 struct Params {
@@ -35,13 +35,13 @@ struct Params {
   int parts;
 };
 
-template <int D, bool E4>
+template <int D, bool E4, int WARPS>
 struct Shape {
   static constexpr int kRow = D * (E4 ? 1 : 2);                        // bytes of a token
   static constexpr int kStage = 2 * kGroup * kRow + (E4 ? 128 : 0);    // keys, values, scales
   static constexpr int kStages = E4 ? (D == 128 ? 5 : 6) : (D == 128 ? 3 : 6);
   static constexpr int kWarpBytes = kStages * kStage > (D + 4) * 64 ? kStages * kStage : (D + 4) * 64;
-  static constexpr int kSmem = kWarps * kWarpBytes;
+  static constexpr int kSmem = WARPS * kWarpBytes;
 };
 
 // 16-byte piece c of token row r: the pieces of 8 rows that an access takes together lie
@@ -55,15 +55,17 @@ __device__ __forceinline__ void copy16(unsigned char* dst, const void* src, bool
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 16 : 0));
 }
 
-// The even (low) and odd bytes of four e4m3 values as two bf16 each: the exponent and
-// mantissa bits in bf16's places stand for the value times 2^-120, subnormals included.
-__device__ __forceinline__ uint32_t times_2_120(uint32_t x) {
+// Two e4m3 values (the low or the high half of w) as f16, exactly; NaN stays NaN.
+__device__ __forceinline__ uint32_t low_f16(uint32_t w) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7b807b80u));
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(w));
   return r;
 }
-__device__ __forceinline__ uint32_t even_bf16(uint32_t r) { return times_2_120(((r << 8) & 0x80008000u) | ((r << 4) & 0x07f007f0u)); }
-__device__ __forceinline__ uint32_t odd_bf16(uint32_t r) { return times_2_120((r & 0x80008000u) | ((r >> 4) & 0x07f007f0u)); }
+__device__ __forceinline__ uint32_t high_f16(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
 
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   float4 v;
@@ -92,13 +94,27 @@ struct Joined {
   }
 };
 
-template <int D, bool E4>
-__global__ void __launch_bounds__(kThreads) kda_attn_step_kernel(const Params p) {
-  using Sh = Shape<D, E4>;
+// Two weights as an operand.
+template <bool E4>
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+  if (!E4) return Bf16::pack(lo, hi);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// What results under the maximum `was` are worth under `now`, at least 2^-126 (0 where there was none).
+__device__ __forceinline__ float factor(float was, float now) {
+  return was == now ? 1.f : was == -INFINITY ? 0.f : fmaxf(ex2_approx(was - now), kTiny);
+}
+
+template <int D, bool E4, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_constant__ Params p) {
+  using Sh = Shape<D, E4, WARPS>;
+  constexpr int kThreads = 32 * WARPS;
   extern __shared__ __align__(128) unsigned char raw[];
   __shared__ __align__(16) float cta_o[16][D];
   __shared__ float cta_m[16], cta_l[16];
-  __shared__ float warp_m[kWarps][16], warp_l[kWarps][16];
+  __shared__ float warp_m[WARPS][16], warp_l[WARPS][16];
   __shared__ int cta_used;
 
   const kda_attn_step_args& a = p.a;
@@ -121,36 +137,58 @@ __global__ void __launch_bounds__(kThreads) kda_attn_step_kernel(const Params p)
 
   // queries as the products' A operand: heads g and g + 8; channels 16 k + 2 t, + 1 and
   // + 8, + 9 for bf16 keys, the 4 from 16 k + 4 t for 8-bit ones (an order of the sum
-  // that gives a lane four consecutive bytes of a key)
+  // that gives a lane four consecutive bytes of a key). With 8-bit keys they are f16, as
+  // the keys are (e4m3 fits it), after a power of two of the head's own that brings the
+  // largest to 2^10 .. 2^11: what falls below f16's range is 2^-34 of that.
   uint32_t q[D / 16][4];
+  float c2[2] = {a.scale * kLog2e, a.scale * kLog2e};  // of the two heads: to scores in powers of two
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int head = g + 8 * r;
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_stride + static_cast<long long>(head0 + head) * D;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      uint32_t lo = 0, hi = 0;
+      uint2 w = make_uint2(0u, 0u);
       if (head < heads) {
-        if (E4) {
-          const uint2 w = *reinterpret_cast<const uint2*>(x + 16 * k + 4 * t);
-          lo = __byte_perm(w.x, w.y, 0x5410);  // channels 4t, 4t + 2 (even bytes of a key)
-          hi = __byte_perm(w.x, w.y, 0x7632);  // 4t + 1, 4t + 3
-        } else {
-          lo = *reinterpret_cast<const uint32_t*>(x + 16 * k + 2 * t);
-          hi = *reinterpret_cast<const uint32_t*>(x + 16 * k + 2 * t + 8);
+        if (E4) w = *reinterpret_cast<const uint2*>(x + 16 * k + 4 * t);
+        else w = make_uint2(*reinterpret_cast<const uint32_t*>(x + 16 * k + 2 * t), *reinterpret_cast<const uint32_t*>(x + 16 * k + 2 * t + 8));
+      }
+      q[k][r] = w.x;
+      q[k][2 + r] = w.y;
+    }
+    if (E4) {
+      float most = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+#pragma unroll
+        for (int u = r; u < 4; u += 2) {
+          most = max_nan(most, fabsf(__uint_as_float(q[k][u] << 16)));
+          most = max_nan(most, fabsf(__uint_as_float(q[k][u] & 0xffff0000u)));
         }
       }
-      q[k][r] = lo;
-      q[k][2 + r] = hi;
+      most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      // 2^(10 - e) of the largest's exponent e (as two factors: one may leave the range)
+      const int e = static_cast<int>(__float_as_uint(most) >> 23);
+      const int by = e == 0 || e == 255 ? 0 : 137 - e, b1 = by / 2, b2 = by - b1;
+      const float f1 = __uint_as_float(static_cast<uint32_t>(127 + b1) << 23), f2 = __uint_as_float(static_cast<uint32_t>(127 + b2) << 23);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+#pragma unroll
+        for (int u = r; u < 4; u += 2) {
+          const __half2 h = __floats2half2_rn(__uint_as_float(q[k][u] << 16) * f1 * f2, __uint_as_float(q[k][u] & 0xffff0000u) * f1 * f2);
+          q[k][u] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      c2[r] = c2[r] * (1.f / f1) * (1.f / f2);
     }
   }
 
   unsigned char* ring = raw + warp * Sh::kWarpBytes;
   const int groups = (len + kGroup - 1) / kGroup;  // of 16 tokens; this warp has every (4 splits)-th
-  const int first = rank * kWarps + warp, step = p.splits * kWarps;
+  const int first = rank * WARPS + warp, step = p.splits * WARPS;
   const int steps = groups > first ? (groups - first + step - 1) / step : 0;
   const int32_t* table = a.block_table + static_cast<long long>(b) * a.table_width;
-  const float scale2 = a.scale * kLog2e;
 
   // pages of the next 32 steps, one a lane
   int pages = 0;
@@ -182,7 +220,9 @@ __global__ void __launch_bounds__(kThreads) kda_attn_step_kernel(const Params p)
       copy16(dst + 2 * kGroup * Sh::kRow + 16 * lane, (lane < 4 ? a.k_scale : a.v_scale) + at + (good ? 4 * (lane & 3) : 0), good);
   };
 
-  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // running maximum and sum of the weights, and, with 8-bit values, the maximum of the
+  // weights times their values' scales, which o is relative to (its own otherwise)
+  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, mv[2] = {-INFINITY, -INFINITY};
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   bool used = false;
@@ -201,16 +241,19 @@ __global__ void __launch_bounds__(kThreads) kda_attn_step_kernel(const Params p)
     const int real = (bad >> s & 1u) ? 0 : min(kGroup, len - (first + i * step) * kGroup);
     used |= real > 0;
 
-    float sc[2][4];
+    float sc[2][4], sd[2][4];  // (two sums each: a product waits for the one before it)
 #pragma unroll
-    for (int n = 0; n < 2; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[n][e] = sd[n][e] = 0.f;
+    }
     if (E4) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const uint32_t w = *reinterpret_cast<const uint32_t*>(ks + piece<Sh::kRow>(8 * n + g, k) + 4 * t);
-          mma16816<Bf16>(sc[n], q[k], even_bf16(w), odd_bf16(w));
+          mma16816<F16>(k % 2 ? sd[n] : sc[n], q[k], low_f16(w), high_f16(w));
         }
       }
     } else {
@@ -219,65 +262,80 @@ __global__ void __launch_bounds__(kThreads) kda_attn_step_kernel(const Params p)
       for (int k = 0; k < D / 16; ++k) {
         uint32_t w[4];
         ldsm_x4(w, ks + piece<Sh::kRow>(r, 2 * k + c));
-        mma16816<Bf16>(sc[0], q[k], w[0], w[1]);
-        mma16816<Bf16>(sc[1], q[k], w[2], w[3]);
+        mma16816<Bf16>(k % 2 ? sd[0] : sc[0], q[k], w[0], w[1]);
+        mma16816<Bf16>(k % 2 ? sd[1] : sc[1], q[k], w[2], w[3]);
       }
     }
     // scores in powers of two; tokens that are not there weigh nothing
     const float* scales = reinterpret_cast<const float*>(vs + kGroup * Sh::kRow);
-    float top[2] = {m[0], m[1]};
+    float top[2] = {m[0], m[1]}, topv[2] = {mv[0], mv[1]}, lv[2][2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
 #pragma unroll
+      for (int e = 0; e < 2; ++e) lv[n][e] = E4 ? lg2_approx(scales[16 + 8 * n + 2 * t + e]) : 0.f;
+#pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int tok = 8 * n + 2 * t + (e & 1);
-        const float x = sc[n][e] * (E4 ? scales[tok] * scale2 : scale2);
+        const float x = (sc[n][e] + sd[n][e]) * (E4 ? scales[tok] * c2[e >> 1] : c2[e >> 1]);
         sc[n][e] = tok < real ? x : -INFINITY;
         top[e >> 1] = fmaxf(top[e >> 1], sc[n][e]);
+        if (E4) {
+          sd[n][e] = tok < real ? x + lv[n][e & 1] : -INFINITY;
+          topv[e >> 1] = fmaxf(topv[e >> 1], sd[n][e]);
+        }
       }
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+      if (E4) topv[r] = fmaxf(topv[r], __shfl_xor_sync(0xffffffffu, topv[r], 1));
       top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+      if (E4) topv[r] = fmaxf(topv[r], __shfl_xor_sync(0xffffffffu, topv[r], 2));
     }
-    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1] || (E4 && (topv[0] > mv[0] || topv[1] > mv[1])))) {
       float keep[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        keep[r] = m[r] == top[r] ? 1.f : m[r] == -INFINITY ? 0.f : fmaxf(ex2_approx(m[r] - top[r]), kTiny);
+        keep[r] = factor(m[r], top[r]);
         m[r] = top[r];
         l[r] *= keep[r];
+        if (E4) {
+          keep[r] = factor(mv[r], topv[r]);
+          mv[r] = topv[r];
+        }
       }
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) o[j][0] *= keep[0], o[j][1] *= keep[0], o[j][2] *= keep[1], o[j][3] *= keep[1];
     }
+    const float mz[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+    const float mvz[2] = {mv[0] == -INFINITY ? 0.f : mv[0], mv[1] == -INFINITY ? 0.f : mv[1]};
     float pr[2][4];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int tok = 8 * n + 2 * t + (e & 1);
-        const float x = sc[n][e], top_r = m[e >> 1];
+        const float x = sc[n][e];
         // (a weight of a finite score stays above 0: an infinite value stays one)
-        float w = ex2_approx(x - (top_r == -INFINITY ? 0.f : top_r));
+        float w = ex2_approx(x - mz[e >> 1]);
         w = x == -INFINITY ? 0.f : w < kTiny ? kTiny : w;
         l[e >> 1] += w;
-        pr[n][e] = E4 ? (tok < real ? w * scales[16 + tok] : 0.f) : w;
+        pr[n][e] = E4 ? ex2_approx(sd[n][e] - mvz[e >> 1]) : w;
       }
     }
-    const uint32_t pa[4] = {Bf16::pack(pr[0][0], pr[0][1]), Bf16::pack(pr[0][2], pr[0][3]), Bf16::pack(pr[1][0], pr[1][1]),
-                            Bf16::pack(pr[1][2], pr[1][3])};
+    const uint32_t pa[4] = {pack_weights<E4>(pr[0][0], pr[0][1]), pack_weights<E4>(pr[0][2], pr[0][3]), pack_weights<E4>(pr[1][0], pr[1][1]),
+                            pack_weights<E4>(pr[1][2], pr[1][3])};
     const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
     if (E4) {
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {  // 32 channels: even and odd ones of each 16 in tiles of their own
         uint32_t w[4];
         ldsm_x4_trans(w, vs + piece<Sh::kRow>(r, 2 * j + c));
-        mma16816<Bf16>(o[4 * j], pa, even_bf16(w[0]), even_bf16(w[1]));
-        mma16816<Bf16>(o[4 * j + 1], pa, odd_bf16(w[0]), odd_bf16(w[1]));
-        mma16816<Bf16>(o[4 * j + 2], pa, even_bf16(w[2]), even_bf16(w[3]));
-        mma16816<Bf16>(o[4 * j + 3], pa, odd_bf16(w[2]), odd_bf16(w[3]));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = __byte_perm(w[u], 0u, 0x3120);
+        mma16816<F16>(o[4 * j], pa, low_f16(w[0]), low_f16(w[1]));
+        mma16816<F16>(o[4 * j + 1], pa, high_f16(w[0]), high_f16(w[1]));
+        mma16816<F16>(o[4 * j + 2], pa, low_f16(w[2]), low_f16(w[3]));
+        mma16816<F16>(o[4 * j + 3], pa, high_f16(w[2]), high_f16(w[3]));
       }
     } else {
 #pragma unroll
@@ -293,6 +351,15 @@ __global__ void __launch_bounds__(kThreads) kda_attn_step_kernel(const Params p)
     cp_async_commit();
   }
   cp_async_wait<0>();
+  if (E4) {
+    // o relative to the weights' maximum again
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float by = mv[r] == -INFINITY ? (mv[r] == m[r] ? 1.f : 0.f) : exp2f(mv[r] - m[r]);
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) o[j][2 * r] *= by, o[j][2 * r + 1] *= by;
+    }
+  }
   if (any_bad && lane == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
 
   // this warp's result: its ring now holds the weighted values [16][D + 4]
@@ -322,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) kda_attn_step_kernel(const Params p)
     const int r = u / Q, d = 4 * (u % Q);
     Joined j;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
+    for (int w = 0; w < WARPS; ++w)
       j.add(warp_m[w][r], warp_l[w][r], *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(raw + w * Sh::kWarpBytes) + r * (D + 4) + d));
     *reinterpret_cast<float4*>(&cta_o[r][d]) = j.o;
     if (d == 0) cta_m[r] = j.m, cta_l[r] = j.l;
@@ -364,11 +431,12 @@ __global__ void __launch_bounds__(kThreads) kda_attn_step_kernel(const Params p)
   if (p.splits > 1) cluster_sync_all();  // no CTA ends while another may read its results
 }
 
-template <int D, bool E4>
+template <int D, bool E4, int WARPS>
 cudaError_t launch(const Params& p, cudaStream_t s) {
+  using Sh = Shape<D, E4, WARPS>;
   static std::atomic<uint64_t> smem_set{0};
-  auto kernel = kda_attn_step_kernel<D, E4>;
-  cudaError_t e = set_smem_limit_once(kernel, Shape<D, E4>::kSmem, smem_set);
+  auto kernel = kda_attn_step_kernel<D, E4, WARPS>;
+  cudaError_t e = set_smem_limit_once(kernel, Sh::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   if (p.splits > 8) {
     static std::atomic<uint64_t> wide_set{0};
@@ -386,8 +454,8 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   if (grid > INT32_MAX) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Shape<D, E4>::kSmem;
+  cfg.blockDim = dim3(32 * WARPS);
+  cfg.dynamicSmemBytes = Sh::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -398,6 +466,11 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <int D, bool E4>
+cudaError_t launch_warps(const Params& p, bool wide, cudaStream_t s) {
+  return wide ? launch<D, E4, 8>(p, s) : launch<D, E4, 4>(p, s);
+}
+
 // ---- the prefix ----
 // Its keys meet the queries of all rows: products of 128 rows, which the prompt kernel
 // computes as one sequence of B queries that sees every key, split over its blocks.
@@ -405,7 +478,7 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
 // An 8-bit prefix in bf16 (exact with scales that are powers of two), as pages 0, 1, ...
 // of a cache of its own; table[i] is i, or -1 where the prefix's page is out of range.
 template <int D>
-__global__ void __launch_bounds__(256) kda_attn_prefix_bf16_kernel(const kda_attn_step_args a, __nv_bfloat16* k, __nv_bfloat16* v, int32_t* table) {
+__global__ void __launch_bounds__(256) kda_attn_prefix_bf16_kernel(const kda_attn_step_args a, __nv_bfloat16* k, __nv_bfloat16* vals, int32_t* table) {
   const int page = a.prefix_table[blockIdx.x], h = blockIdx.y;
   const bool good = page >= 0 && page < a.pages;
   if (h == 0 && threadIdx.x == 0) table[blockIdx.x] = good ? static_cast<int>(blockIdx.x) : -1;
@@ -420,11 +493,12 @@ __global__ void __launch_bounds__(256) kda_attn_prefix_bf16_kernel(const kda_att
     uint32_t out[4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t e = even_bf16(in[i]), o = odd_bf16(in[i]);  // values 0 and 2, 1 and 3
-      out[2 * i] = Bf16::pack(__uint_as_float(e << 16) * s, __uint_as_float(o << 16) * s);
-      out[2 * i + 1] = Bf16::pack(__uint_as_float(e & 0xffff0000u) * s, __uint_as_float(o & 0xffff0000u) * s);
+      const uint32_t lo = low_f16(in[i]), hi = high_f16(in[i]);
+      const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&lo)), v = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+      out[2 * i] = Bf16::pack(u.x * s, u.y * s);
+      out[2 * i + 1] = Bf16::pack(v.x * s, v.y * s);
     }
-    *reinterpret_cast<uint4*>((of_v ? v : k) + (to + t) * D + c) = make_uint4(out[0], out[1], out[2], out[3]);
+    *reinterpret_cast<uint4*>((of_v ? vals : k) + (to + t) * D + c) = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
@@ -494,11 +568,11 @@ size_t attn_step_workspace_bytes(const kda_attn_step_args& a) { return prefix_of
 
 cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaStream_t s) {
   Params p = {a, a.HQ / a.HKV, (a.HQ / a.HKV + 15) / 16, 1, nullptr, nullptr, 0};
-  // A cluster for each row and key head: enough CTAs for two on each of the 152 SMs, as
-  // long as a warp has 64 tokens or more of what the table has room for.
+  // A cluster for each row and key head.
   const long long units = static_cast<long long>(a.B) * a.HKV * p.head_tiles;
   const long long room = static_cast<long long>(a.table_width) * a.page_size;
-  while (p.splits < kMaxSplits && units * p.splits < 2 * 152 && room >= 2 * p.splits * kWarps * 64) p.splits *= 2;
+  while (p.splits < kMaxSplits && (units * p.splits < kBusy || room > static_cast<long long>(p.splits) * kLong) && room > p.splits * kLeast) p.splits *= 2;
+  const bool wide = units * p.splits <= 152 && room >= p.splits * 2 * kLeast;
   const Prefix x = prefix_of(a);
   if (x.splits > 0) {
     unsigned char* w = static_cast<unsigned char*>(workspace);
@@ -507,8 +581,8 @@ cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaS
     p.part_o = reinterpret_cast<const float*>(w + x.o), p.part_lse = reinterpret_cast<const float*>(w + x.lse), p.parts = x.splits;
   }
   const bool e4 = a.cache_dtype == KDA_DTYPE_E4M3;
-  if (a.D == 64) return e4 ? launch<64, true>(p, s) : launch<64, false>(p, s);
-  return e4 ? launch<128, true>(p, s) : launch<128, false>(p, s);
+  if (a.D == 64) return e4 ? launch_warps<64, true>(p, wide, s) : launch_warps<64, false>(p, wide, s);
+  return e4 ? launch_warps<128, true>(p, wide, s) : launch_warps<128, false>(p, wide, s);
 }
 
 }  // namespace kda
