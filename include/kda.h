@@ -684,8 +684,10 @@ typedef struct kda_attn_step_args {
   float* lse;
   int32_t* err;            /* optional device status word */
 } kda_attn_step_args;
-/* Bytes of device scratch kda_attn_step needs: 0 without a prefix (also for arguments
- * it refuses). */
+/* Bytes of device scratch kda_attn_step needs: for the prefix, and for few rows on long
+ * tables; 0 without a prefix where the table has room for fewer than KDA_ATTN_LONG_TOKENS
+ * tokens a row (also for arguments it refuses). */
+#define KDA_ATTN_LONG_TOKENS 16384
 size_t kda_attn_step_workspace_size(const kda_attn_step_args* args);
 /* `workspace` is device memory of at least that size, 256-byte aligned (NULL for 0). */
 kda_status kda_attn_step(const kda_attn_step_args* args, void* workspace, size_t workspace_bytes, kda_stream_t stream);

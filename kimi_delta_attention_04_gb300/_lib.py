@@ -43,6 +43,7 @@ KDA_SCAN_FLAG_COMPLEMENT = 0x1
 KDA_KV_FLAG_INTERLEAVED = 0x1
 KDA_ATTN_FLAG_CAUSAL = 0x1
 KDA_ATTN_MAX_HEADS = 1024
+KDA_ATTN_LONG_TOKENS = 16384
 
 
 class KdaError(RuntimeError):
@@ -1046,9 +1047,9 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, *, scale, k_scale=
     (int32, shared by all rows and read once for them) and to its own seq_lens[b] tokens
     (int32; negative = padding, o = 0) on the pages of block_table[b] (int32 [B, width]).
 
-    lse (fp32 [B, HQ]) receives the logarithm of the sums when given. With a prefix,
-    workspace (a CUDA uint8 tensor of kda_attn_step_workspace_size bytes) is made here
-    unless given. Returns o [B, HQ, D]."""
+    lse (fp32 [B, HQ]) receives the logarithm of the sums when given. With a prefix, or a
+    table for KDA_ATTN_LONG_TOKENS tokens or more, workspace (a CUDA uint8 tensor of
+    kda_attn_step_workspace_size bytes) is made here unless given. Returns o [B, HQ, D]."""
     lib = _lib or load()
     dev = _device_of(q)
     if q.dim() != 3 or block_table.dim() != 2:
@@ -1073,7 +1074,7 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, *, scale, k_scale=
     args.prefix_table = _vec(prefix_table, "prefix_table", dev, (pages,), torch.int32)
     o, args.o, args.o_stride = _head_output(o, "o", q, stream, shape)
     args.lse, args.err = _vec(lse, "lse", dev, (B, HQ)), _err_word(err, dev)
-    if prefix_len <= 0:
+    if prefix_len <= 0 and width * cache[2] < KDA_ATTN_LONG_TOKENS:
         _call(lib.kda_attn_step, args, dev, stream, None, 0)
         return o
     need = lib.kda_attn_step_workspace_size(args)

@@ -129,13 +129,13 @@ kda_status kda_attn_fwd(const kda_attn_fwd_args* a, kda_stream_t stream) {
 }
 
 size_t kda_attn_step_workspace_size(const kda_attn_step_args* a) {
-  return check_step(a) == KDA_OK && a->B > 0 && a->prefix_len > 0 ? kda::attn_step_workspace_bytes(*a) : 0;
+  return check_step(a) == KDA_OK && a->B > 0 ? kda::attn_step_workspace_bytes(*a) : 0;
 }
 
 kda_status kda_attn_step(const kda_attn_step_args* a, void* workspace, size_t workspace_bytes, kda_stream_t stream) {
   const kda_status st = check_step(a);
   if (st != KDA_OK || a->B == 0) return st;
-  const size_t need = a->prefix_len > 0 ? kda::attn_step_workspace_bytes(*a) : 0;
+  const size_t need = kda::attn_step_workspace_bytes(*a);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))) return KDA_ERR_INVALID_ARG;
   return done(kda::launch_attn_step(*a, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }

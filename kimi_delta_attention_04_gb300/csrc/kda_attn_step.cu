@@ -22,25 +22,32 @@ namespace {
 
 using namespace attn;
 
-constexpr int kGroup = 16;       // tokens of a warp's step; divides every page
-constexpr int kMaxSplits = 16;
-constexpr int kBusy = 304, kLong = 2048, kLeast = 64;
+constexpr int kGroup = 16;       // tokens that the products take at once; divides every page
+constexpr int kMaxSplits = 8;    // CTAs of a cluster
 constexpr float kTiny = 1.1754944e-38f;
 
 struct Params {
   kda_attn_step_args a;
-  int G, head_tiles, splits;
-  const float* part_o;    // [parts, B, HQ, D]: the prefix's results, normalised
-  const float* part_lse;  // [parts, B, HQ], in powers of two
+  int G, head_tiles;
+  int splits, chunks;     // CTAs of a cluster and clusters on each row and key head (and tile of its heads)
+  const float* part_o;    // [parts, B, HQ, D]: results to join, normalised: the clusters' where a
+  const float* part_lse;  // row has several, and the prefix's; [parts, B, HQ], in powers of two
   int parts;
+  float* own_o;           // the clusters' part of them
+  float* own_lse;
 };
 
 template <int D, bool E4, int WARPS>
 struct Shape {
   static constexpr int kRow = D * (E4 ? 1 : 2);                        // bytes of a token
-  static constexpr int kStage = 2 * kGroup * kRow + (E4 ? 128 : 0);    // keys, values, scales
-  static constexpr int kStages = E4 ? (D == 128 ? 5 : 6) : (D == 128 ? 3 : 6);
-  static constexpr int kWarpBytes = kStages * kStage > (D + 4) * 64 ? kStages * kStage : (D + 4) * 64;
+  // Groups of a warp's step: two of 8-bit tokens (the same bytes as one of bf16; with one,
+  // what a step costs besides its products kept 256 rows of 2000 tokens at 262 us).
+  static constexpr int kSub = E4 ? 2 : 1;
+  static constexpr int kTokens = kSub * kGroup;
+  static constexpr int kStage = 2 * kTokens * kRow + (E4 ? 8 * kTokens : 0);  // keys, values, scales of both
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kResult = (D + 4) * 64 + 16 / WARPS * D * 4;  // a warp's result, and rows of the CTA's
+  static constexpr int kWarpBytes = kStages * kStage > kResult ? kStages * kStage : kResult;
   static constexpr int kSmem = WARPS * kWarpBytes;
 };
 
@@ -107,20 +114,55 @@ __device__ __forceinline__ float factor(float was, float now) {
   return was == now ? 1.f : was == -INFINITY ? 0.f : fmaxf(ex2_approx(was - now), kTiny);
 }
 
+// Adds the results in the workspace for a row and head, 4 channels from d.
+template <int D>
+__device__ __forceinline__ void join_parts(const Params& p, long long b, int head, int d, Joined& j, int& any) {
+  for (int s = 0; s < p.parts; ++s) {
+    const long long at = (static_cast<long long>(s) * p.a.B + b) * p.a.HQ + head;
+    const float lse = p.part_lse[at];
+    if (lse == -INFINITY) continue;  // no key
+    any = 1;
+    j.add(lse, 1.f, *reinterpret_cast<const float4*>(p.part_o + at * D + d));
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void store_row(const kda_attn_step_args& a, long long b, int head, int d, const Joined& j, int any) {
+  // (keys whose scores are all -inf: 0 / 0, as the definition has it)
+  const float inv = 1.f / j.l;
+  uint2 w = make_uint2(0u, 0u);
+  if (any) w = make_uint2(Bf16::pack(j.o.x * inv, j.o.y * inv), Bf16::pack(j.o.z * inv, j.o.w * inv));
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + b * a.o_stride + static_cast<long long>(head) * D + d) = w;
+  if (a.lse && d == 0) a.lse[b * a.HQ + head] = any ? (j.m + log2f(j.l)) * kLn2 : -INFINITY;
+}
+
+// Rows that several clusters, or the prefix and several clusters, worked on.
+template <int D>
+__global__ void __launch_bounds__(128) kda_attn_join_kernel(const __grid_constant__ Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long u = static_cast<long long>(blockIdx.x) * 128 + threadIdx.x, r = u / (D / 4);
+  if (r >= static_cast<long long>(p.a.B) * p.a.HQ) return;
+  const long long b = r / p.a.HQ;
+  const int head = static_cast<int>(r % p.a.HQ), d = static_cast<int>(u % (D / 4)) * 4, len = p.a.seq_lens[b];
+  Joined j;
+  int any = 0;
+  if (len >= 0 && len <= p.a.table_width * p.a.page_size) join_parts<D>(p, b, head, d, j, any);
+  store_row<D>(p.a, b, head, d, j, any);
+}
+
 template <int D, bool E4, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_constant__ Params p) {
   using Sh = Shape<D, E4, WARPS>;
   constexpr int kThreads = 32 * WARPS;
   extern __shared__ __align__(128) unsigned char raw[];
-  __shared__ __align__(16) float cta_o[16][D];
   __shared__ float cta_m[16], cta_l[16];
   __shared__ float warp_m[WARPS][16], warp_l[WARPS][16];
   __shared__ int cta_used;
 
   const kda_attn_step_args& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int rank = static_cast<int>(blockIdx.x % p.splits);
-  long long unit = blockIdx.x / p.splits;
+  const int rank = static_cast<int>(blockIdx.x % (p.splits * p.chunks)), in_cluster = rank % p.splits;  // of the row's CTAs
+  long long unit = blockIdx.x / (p.splits * p.chunks);
   const int tile = static_cast<int>(unit % p.head_tiles);
   unit /= p.head_tiles;
   const int h = static_cast<int>(unit % a.HKV);
@@ -185,39 +227,46 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
   }
 
   unsigned char* ring = raw + warp * Sh::kWarpBytes;
-  const int groups = (len + kGroup - 1) / kGroup;  // of 16 tokens; this warp has every (4 splits)-th
-  const int first = rank * WARPS + warp, step = p.splits * WARPS;
-  const int steps = groups > first ? (groups - first + step - 1) / step : 0;
+  constexpr int T = Sh::kTokens;
+  const int all = (len + T - 1) / T;  // steps of T tokens; this warp has every (CTAs of the row x WARPS)-th
+  const int first = rank * WARPS + warp, step = p.chunks * p.splits * WARPS;
+  const int steps = all > first ? (all - first + step - 1) / step : 0;
   const int32_t* table = a.block_table + static_cast<long long>(b) * a.table_width;
 
-  // pages of the next 32 steps, one a lane
+  // pages of the next 32 groups, one a lane
   int pages = 0;
-  uint32_t bad = 0;  // by stage: its page is out of range
+  uint32_t bad = 0;  // by stage and group: its page is out of range
   bool any_bad = false;
   auto load = [&](int i) {
-    if (i % 32 == 0) {
-      const int at = i + lane;
-      pages = at < steps ? table[(first + at * step) * kGroup / a.page_size] : 0;
-    }
-    const int page = __shfl_sync(0xffffffffu, pages, i % 32), s = i % Sh::kStages;
-    const int tok = (first + i * step) * kGroup;
-    const bool good = page >= 0 && page < a.pages;
-    bad = good ? bad & ~(1u << s) : bad | 1u << s;
-    any_bad |= !good;
-    const long long at = good ? (static_cast<long long>(page) * a.HKV + h) * a.page_size + tok % a.page_size : 0;
-    const int real = good ? min(kGroup, len - tok) : 0;
+    const int s = i % Sh::kStages;
     unsigned char* dst = ring + s * Sh::kStage;
-    const unsigned char* ks = static_cast<const unsigned char*>(a.k_cache) + at * Sh::kRow;
-    const unsigned char* vs = static_cast<const unsigned char*>(a.v_cache) + at * Sh::kRow;
-    constexpr int C = Sh::kRow / 16;
 #pragma unroll
-    for (int j = 0; j < kGroup * C / 32; ++j) {
-      const int u = 32 * j + lane, r = u / C, c = u % C;
-      copy16(dst + piece<Sh::kRow>(r, c), ks + (r < real ? 16 * u : 0), r < real);
-      copy16(dst + kGroup * Sh::kRow + piece<Sh::kRow>(r, c), vs + (r < real ? 16 * u : 0), r < real);
+    for (int u = 0; u < Sh::kSub; ++u) {
+      const int at0 = i * Sh::kSub + u;
+      if (at0 % 32 == 0) {
+        const int at = at0 + lane, tok = (first + at / Sh::kSub * step) * T + at % Sh::kSub * kGroup;
+        pages = at < steps * Sh::kSub && tok < len ? table[tok / a.page_size] : 0;
+      }
+      const int page = __shfl_sync(0xffffffffu, pages, at0 % 32), bit = s * Sh::kSub + u;
+      const int tok = (first + i * step) * T + u * kGroup;
+      const bool there = tok < len, good = there && page >= 0 && page < a.pages;
+      bad = good || !there ? bad & ~(1u << bit) : bad | 1u << bit;
+      any_bad |= there && !good;
+      const long long at = good ? (static_cast<long long>(page) * a.HKV + h) * a.page_size + tok % a.page_size : 0;
+      const int real = good ? min(kGroup, len - tok) : 0;
+      const unsigned char* ks = static_cast<const unsigned char*>(a.k_cache) + at * Sh::kRow;
+      const unsigned char* vs = static_cast<const unsigned char*>(a.v_cache) + at * Sh::kRow;
+      constexpr int C = Sh::kRow / 16;
+#pragma unroll
+      for (int j = 0; j < kGroup * C / 32; ++j) {
+        const int n = 32 * j + lane, r = n / C, c = n % C;
+        copy16(dst + piece<Sh::kRow>(u * kGroup + r, c), ks + (r < real ? 16 * n : 0), r < real);
+        copy16(dst + T * Sh::kRow + piece<Sh::kRow>(u * kGroup + r, c), vs + (r < real ? 16 * n : 0), r < real);
+      }
+      if (E4 && lane < 8)
+        copy16(dst + 2 * T * Sh::kRow + (lane / 4) * 4 * T + u * 4 * kGroup + 16 * (lane & 3),
+               (lane < 4 ? a.k_scale : a.v_scale) + at + (good ? 4 * (lane & 3) : 0), good);
     }
-    if (E4 && lane < 8)
-      copy16(dst + 2 * kGroup * Sh::kRow + 16 * lane, (lane < 4 ? a.k_scale : a.v_scale) + at + (good ? 4 * (lane & 3) : 0), good);
   };
 
   // running maximum and sum of the weights, and, with 8-bit values, the maximum of the
@@ -237,13 +286,18 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
     __syncwarp();
     const int s = i % Sh::kStages;
     const unsigned char* ks = ring + s * Sh::kStage;
-    const unsigned char* vs = ks + kGroup * Sh::kRow;
-    const int real = (bad >> s & 1u) ? 0 : min(kGroup, len - (first + i * step) * kGroup);
-    used |= real > 0;
-
-    float sc[2][4], sd[2][4];  // (two sums each: a product waits for the one before it)
+    const unsigned char* vs = ks + T * Sh::kRow;
+    constexpr int U = Sh::kSub, N = 2 * U;  // groups; products' 8 tokens
+    int real[U];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int u = 0; u < U; ++u) {
+      real[u] = (bad >> (s * U + u) & 1u) ? 0 : min(kGroup, len - (first + i * step) * T - u * kGroup);
+      used |= real[u] > 0;
+    }
+
+    float sc[N][4], sd[N][4];  // (two sums each: a product waits for the one before it)
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[n][e] = sd[n][e] = 0.f;
     }
@@ -251,7 +305,7 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < N; ++n) {
           const uint32_t w = *reinterpret_cast<const uint32_t*>(ks + piece<Sh::kRow>(8 * n + g, k) + 4 * t);
           mma16816<F16>(k % 2 ? sd[n] : sc[n], q[k], low_f16(w), high_f16(w));
         }
@@ -267,20 +321,21 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
       }
     }
     // scores in powers of two; tokens that are not there weigh nothing
-    const float* scales = reinterpret_cast<const float*>(vs + kGroup * Sh::kRow);
-    float top[2] = {m[0], m[1]}, topv[2] = {mv[0], mv[1]}, lv[2][2];
+    const float* scales = reinterpret_cast<const float*>(vs + T * Sh::kRow);
+    float top[2] = {m[0], m[1]}, topv[2] = {mv[0], mv[1]};
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < N; ++n) {
+      float lv[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) lv[n][e] = E4 ? lg2_approx(scales[16 + 8 * n + 2 * t + e]) : 0.f;
+      for (int e = 0; e < 2; ++e) lv[e] = E4 ? lg2_approx(scales[T + 8 * n + 2 * t + e]) : 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int tok = 8 * n + 2 * t + (e & 1);
         const float x = (sc[n][e] + sd[n][e]) * (E4 ? scales[tok] * c2[e >> 1] : c2[e >> 1]);
-        sc[n][e] = tok < real ? x : -INFINITY;
+        sc[n][e] = tok % kGroup < real[n / 2] ? x : -INFINITY;
         top[e >> 1] = fmaxf(top[e >> 1], sc[n][e]);
         if (E4) {
-          sd[n][e] = tok < real ? x + lv[n][e & 1] : -INFINITY;
+          sd[n][e] = tok % kGroup < real[n / 2] ? x + lv[e & 1] : -INFINITY;
           topv[e >> 1] = fmaxf(topv[e >> 1], sd[n][e]);
         }
       }
@@ -309,9 +364,8 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
     }
     const float mz[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
     const float mvz[2] = {mv[0] == -INFINITY ? 0.f : mv[0], mv[1] == -INFINITY ? 0.f : mv[1]};
-    float pr[2][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < N; ++n) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float x = sc[n][e];
@@ -319,31 +373,34 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
         float w = ex2_approx(x - mz[e >> 1]);
         w = x == -INFINITY ? 0.f : w < kTiny ? kTiny : w;
         l[e >> 1] += w;
-        pr[n][e] = E4 ? ex2_approx(sd[n][e] - mvz[e >> 1]) : w;
+        sc[n][e] = E4 ? ex2_approx(sd[n][e] - mvz[e >> 1]) : w;
       }
     }
-    const uint32_t pa[4] = {pack_weights<E4>(pr[0][0], pr[0][1]), pack_weights<E4>(pr[0][2], pr[0][3]), pack_weights<E4>(pr[1][0], pr[1][1]),
-                            pack_weights<E4>(pr[1][2], pr[1][3])};
-    const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
-    if (E4) {
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {  // 32 channels: even and odd ones of each 16 in tiles of their own
-        uint32_t w[4];
-        ldsm_x4_trans(w, vs + piece<Sh::kRow>(r, 2 * j + c));
+    for (int u = 0; u < U; ++u) {
+      const uint32_t pa[4] = {pack_weights<E4>(sc[2 * u][0], sc[2 * u][1]), pack_weights<E4>(sc[2 * u][2], sc[2 * u][3]),
+                              pack_weights<E4>(sc[2 * u + 1][0], sc[2 * u + 1][1]), pack_weights<E4>(sc[2 * u + 1][2], sc[2 * u + 1][3])};
+      const int r = u * kGroup + (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
+      if (E4) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) w[u] = __byte_perm(w[u], 0u, 0x3120);
-        mma16816<F16>(o[4 * j], pa, low_f16(w[0]), low_f16(w[1]));
-        mma16816<F16>(o[4 * j + 1], pa, high_f16(w[0]), high_f16(w[1]));
-        mma16816<F16>(o[4 * j + 2], pa, low_f16(w[2]), low_f16(w[3]));
-        mma16816<F16>(o[4 * j + 3], pa, high_f16(w[2]), high_f16(w[3]));
-      }
-    } else {
+        for (int j = 0; j < D / 32; ++j) {  // 32 channels: even and odd ones of each 16 in tiles of their own
+          uint32_t w[4];
+          ldsm_x4_trans(w, vs + piece<Sh::kRow>(r, 2 * j + c));
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        uint32_t w[4];
-        ldsm_x4_trans(w, vs + piece<Sh::kRow>(r, 2 * j + c));
-        mma16816<Bf16>(o[2 * j], pa, w[0], w[1]);
-        mma16816<Bf16>(o[2 * j + 1], pa, w[2], w[3]);
+          for (int x = 0; x < 4; ++x) w[x] = __byte_perm(w[x], 0u, 0x3120);
+          mma16816<F16>(o[4 * j], pa, low_f16(w[0]), low_f16(w[1]));
+          mma16816<F16>(o[4 * j + 1], pa, high_f16(w[0]), high_f16(w[1]));
+          mma16816<F16>(o[4 * j + 2], pa, low_f16(w[2]), low_f16(w[3]));
+          mma16816<F16>(o[4 * j + 3], pa, high_f16(w[2]), high_f16(w[3]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t w[4];
+          ldsm_x4_trans(w, vs + piece<Sh::kRow>(r, 2 * j + c));
+          mma16816<Bf16>(o[2 * j], pa, w[0], w[1]);
+          mma16816<Bf16>(o[2 * j + 1], pa, w[2], w[3]);
+        }
       }
     }
     __syncwarp();
@@ -385,20 +442,25 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
   __syncthreads();
   if (used && lane == 0) cta_used = 1;
   constexpr int Q = D / 4;  // 4 channels at a time
+  // the CTA's result lies behind its warps', some rows behind each
+  constexpr int kEach = 16 / WARPS;
+  const auto cta_o = [&](int r, int d) {
+    return reinterpret_cast<float*>(raw + r / kEach * Sh::kWarpBytes + (D + 4) * 64) + r % kEach * D + d;
+  };
   for (int u = tid; u < heads * Q; u += kThreads) {
     const int r = u / Q, d = 4 * (u % Q);
     Joined j;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w)
       j.add(warp_m[w][r], warp_l[w][r], *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(raw + w * Sh::kWarpBytes) + r * (D + 4) + d));
-    *reinterpret_cast<float4*>(&cta_o[r][d]) = j.o;
+    *reinterpret_cast<float4*>(cta_o(r, d)) = j.o;
     if (d == 0) cta_m[r] = j.m, cta_l[r] = j.l;
   }
   if (p.splits > 1) cluster_sync_all();
   else __syncthreads();
 
   // the splits' results and the prefix's, in order
-  for (int u = rank * kThreads + tid; u < heads * Q; u += p.splits * kThreads) {
+  for (int u = in_cluster * kThreads + tid; u < heads * Q; u += p.splits * kThreads) {
     const int r = u / Q, d = 4 * (u % Q), head = head0 + r;
     Joined j;
     int any = 0;
@@ -406,27 +468,22 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
       for (int s = 0; s < p.splits; ++s) {
         any |= ld_shared_cluster_s32(mapa_shared(smem_u32(&cta_used), s));
         j.add(ld_cluster(mapa_shared(smem_u32(&cta_m[r]), s)), ld_cluster(mapa_shared(smem_u32(&cta_l[r]), s)),
-              ld_cluster4(mapa_shared(smem_u32(&cta_o[r][d]), s)));
+              ld_cluster4(mapa_shared(smem_u32(cta_o(r, d)), s)));
       }
     } else {
       any = cta_used;
-      j.add(cta_m[r], cta_l[r], *reinterpret_cast<const float4*>(&cta_o[r][d]));
+      j.add(cta_m[r], cta_l[r], *reinterpret_cast<const float4*>(cta_o(r, d)));
     }
-    if (row) {
-      for (int s = 0; s < p.parts; ++s) {
-        const long long at = (static_cast<long long>(s) * a.B + b) * a.HQ + head;
-        const float lse = p.part_lse[at];
-        if (lse == -INFINITY) continue;  // no key
-        any = 1;
-        j.add(lse, 1.f, *reinterpret_cast<const float4*>(p.part_o + at * D + d));
-      }
+    if (p.chunks > 1) {
+      // one of several clusters on the row: kda_attn_join_kernel takes their results together
+      const long long at = (static_cast<long long>(rank / p.splits) * a.B + b) * a.HQ + head;
+      const float inv = any ? 1.f / j.l : 0.f;
+      *reinterpret_cast<float4*>(p.own_o + at * D + d) = make_float4(j.o.x * inv, j.o.y * inv, j.o.z * inv, j.o.w * inv);
+      if (d == 0) p.own_lse[at] = any ? (j.l == 0.f ? __uint_as_float(0x7fc00000u) : j.m + log2f(j.l)) : -INFINITY;
+      continue;
     }
-    // (keys whose scores are all -inf: 0 / 0, as the definition has it)
-    const float inv = 1.f / j.l;
-    uint2 w = make_uint2(0u, 0u);
-    if (any) w = make_uint2(Bf16::pack(j.o.x * inv, j.o.y * inv), Bf16::pack(j.o.z * inv, j.o.w * inv));
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + b * a.o_stride + static_cast<long long>(head) * D + d) = w;
-    if (a.lse && d == 0) a.lse[static_cast<long long>(b) * a.HQ + head] = any ? (j.m + log2f(j.l)) * kLn2 : -INFINITY;
+    if (row) join_parts<D>(p, b, head, d, j, any);
+    store_row<D>(a, b, head, d, j, any);
   }
   if (p.splits > 1) cluster_sync_all();  // no CTA ends while another may read its results
 }
@@ -438,19 +495,7 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   auto kernel = kda_attn_step_kernel<D, E4, WARPS>;
   cudaError_t e = set_smem_limit_once(kernel, Sh::kSmem, smem_set);
   if (e != cudaSuccess) return e;
-  if (p.splits > 8) {
-    static std::atomic<uint64_t> wide_set{0};
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
-    if (bit == 0 || (wide_set.load(std::memory_order_acquire) & bit) == 0) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return e;
-      wide_set.fetch_or(bit, std::memory_order_acq_rel);
-    }
-  }
-  const long long grid = static_cast<long long>(p.a.B) * p.a.HKV * p.head_tiles * p.splits;
+  const long long grid = static_cast<long long>(p.a.B) * p.a.HKV * p.head_tiles * p.splits * p.chunks;
   if (grid > INT32_MAX) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -502,48 +547,67 @@ __global__ void __launch_bounds__(256) kda_attn_prefix_bf16_kernel(const kda_att
   }
 }
 
-// How the prefix's work is laid out, and where its results lie in the workspace.
-struct Prefix {
-  int splits = 0, pages = 0;
+// How a call's work is laid out, and where its parts' results lie in the workspace.
+struct Plan {
+  int splits = 1, chunks = 1, parts = 0;  // of the rows' own tokens; all results to join
+  int prefix_splits = 0, prefix_pages = 0;
+  bool wide = false;                      // 8 warps to a CTA
   size_t lse = 0, o = 0, table = 0, k = 0, v = 0, bytes = 0;
 };
 
-Prefix prefix_of(const kda_attn_step_args& a) {
-  Prefix x;
-  if (a.prefix_len == 0) return x;
-  // Splits that keep the 152 SMs busy: rounds of CTAs, each with its share of the blocks
-  // and 4 blocks' time for what a CTA does besides.
-  const int G = a.HQ / a.HKV, tokens = attn_tile_tokens(G), packed = tokens > 256 ? 1 : 256 / tokens;
-  const long long tiles = (static_cast<long long>(a.B) + tokens - 1) / tokens * a.HKV * (G / packed);
-  const int blocks = (a.prefix_len + 127) / 128;
-  long long best = 0;
-  for (int s = 1; s <= 32 && s <= blocks; ++s) {
-    const long long cost = (tiles * s + 151) / 152 * ((blocks + s - 1) / s + 4);
-    if (x.splits == 0 || cost < best) {
-      x.splits = s;
-      best = cost;
-    }
+Plan plan_of(const kda_attn_step_args& a) {
+  Plan x;
+  const int G = a.HQ / a.HKV;
+  // A cluster for each row and key head (and 16 heads of its group): CTAs for two on each
+  // of the 152 SMs as far as their share stays at 64 tokens of what the table has room
+  // for, and enough that it is no more than 4096 (rows of unequal lengths leave SMs idle
+  // behind the longest: 64 rows of up to 8192 tokens took 223 us with one CTA each, 185
+  // with four; 256 of up to 2500 take 14 % longer with two).
+  const long long units = static_cast<long long>(a.B) * a.HKV * ((G + 15) / 16), room = static_cast<long long>(a.table_width) * a.page_size;
+  while (x.splits < kMaxSplits && (units * x.splits < 2 * 152 || room > 4096ll * x.splits) && room > 64ll * x.splits) x.splits *= 2;
+  // Few long rows: several clusters each, with a launch of its own to join their results.
+  // (Clusters of 16 leave SMs idle: one row of 131072 tokens took 140 us with them.)
+  if (units * x.splits <= 152 && room >= KDA_ATTN_LONG_TOKENS) {
+    const long long fill = 2 * 152 / (units * x.splits), each = room / (512 * x.splits);
+    x.chunks = static_cast<int>(fill < each ? fill : each);
   }
-  x.pages = (a.prefix_len - 1) / a.page_size + 1;
-  const size_t rows = static_cast<size_t>(a.B) * a.HQ * x.splits;
+  x.wide = units * x.splits * x.chunks <= 152 && room >= 128ll * x.splits * x.chunks;
+  if (a.prefix_len > 0) {
+    // Splits that keep the SMs busy: rounds of CTAs, each with its share of the blocks and
+    // 4 blocks' time for what a CTA does besides.
+    const int tokens = attn_tile_tokens(G), packed = 256 / tokens;
+    const long long tiles = (static_cast<long long>(a.B) + tokens - 1) / tokens * a.HKV * (G / packed);
+    const int blocks = (a.prefix_len - 1) / 128 + 1;
+    long long best = 0;
+    for (int s = 1; s <= 32 && s <= blocks; ++s) {
+      const long long cost = (tiles * s + 151) / 152 * ((blocks + s - 1) / s + 4);
+      if (x.prefix_splits == 0 || cost < best) {
+        x.prefix_splits = s;
+        best = cost;
+      }
+    }
+    x.prefix_pages = (a.prefix_len - 1) / a.page_size + 1;
+  }
+  x.parts = (x.chunks > 1 ? x.chunks : 0) + x.prefix_splits;
+  const size_t rows = static_cast<size_t>(a.B) * a.HQ * x.parts;
   const auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
   x.o = up(rows * sizeof(float));
   x.table = x.o + up(rows * a.D * sizeof(float));
   x.bytes = x.table;
-  if (a.cache_dtype == KDA_DTYPE_E4M3) {
-    const size_t cache = static_cast<size_t>(x.pages) * a.HKV * a.page_size * a.D * 2;
-    x.k = x.table + up(x.pages * sizeof(int32_t));
+  if (x.prefix_splits > 0 && a.cache_dtype == KDA_DTYPE_E4M3) {
+    const size_t cache = static_cast<size_t>(x.prefix_pages) * a.HKV * a.page_size * a.D * 2;
+    x.k = x.table + up(x.prefix_pages * sizeof(int32_t));
     x.v = x.k + cache;
     x.bytes = x.v + cache;
   }
   return x;
 }
 
-cudaError_t launch_prefix(const kda_attn_step_args& a, const Prefix& x, unsigned char* w, cudaStream_t s) {
+cudaError_t launch_prefix(const kda_attn_step_args& a, const Plan& x, unsigned char* w, const AttnParts& parts, cudaStream_t s) {
   kda_attn_fwd_args f = {};
   f.B = f.N = 1;
   f.T = a.B, f.HQ = a.HQ, f.HKV = a.HKV, f.D = a.D;
-  f.page_size = a.page_size, f.table_width = x.pages;
+  f.page_size = a.page_size, f.table_width = x.prefix_pages;
   f.scale = a.scale;
   f.q = a.q, f.q_stride = a.q_stride, f.err = a.err;
   f.pages = a.pages, f.k = a.k_cache, f.v = a.v_cache, f.block_table = a.prefix_table;
@@ -551,38 +615,44 @@ cudaError_t launch_prefix(const kda_attn_step_args& a, const Prefix& x, unsigned
     if (a.HKV > 65535) return cudaErrorNotSupported;
     __nv_bfloat16 *k = reinterpret_cast<__nv_bfloat16*>(w + x.k), *v = reinterpret_cast<__nv_bfloat16*>(w + x.v);
     int32_t* table = reinterpret_cast<int32_t*>(w + x.table);
-    const dim3 grid(static_cast<unsigned>(x.pages), static_cast<unsigned>(a.HKV));
+    const dim3 grid(static_cast<unsigned>(x.prefix_pages), static_cast<unsigned>(a.HKV));
     if (a.D == 64) kda_attn_prefix_bf16_kernel<64><<<grid, 256, 0, s>>>(a, k, v, table);
     else kda_attn_prefix_bf16_kernel<128><<<grid, 256, 0, s>>>(a, k, v, table);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    f.pages = x.pages, f.k = k, f.v = v, f.block_table = table;
+    f.pages = x.prefix_pages, f.k = k, f.v = v, f.block_table = table;
   }
-  const AttnParts parts = {reinterpret_cast<float*>(w + x.o), reinterpret_cast<float*>(w + x.lse), x.splits, a.prefix_len};
   return launch_attn_prompts(f, parts, s);
 }
 
 }  // namespace
 
-size_t attn_step_workspace_bytes(const kda_attn_step_args& a) { return prefix_of(a).bytes; }
+size_t attn_step_workspace_bytes(const kda_attn_step_args& a) { return plan_of(a).bytes; }
 
 cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaStream_t s) {
-  Params p = {a, a.HQ / a.HKV, (a.HQ / a.HKV + 15) / 16, 1, nullptr, nullptr, 0};
-  // A cluster for each row and key head.
-  const long long units = static_cast<long long>(a.B) * a.HKV * p.head_tiles;
-  const long long room = static_cast<long long>(a.table_width) * a.page_size;
-  while (p.splits < kMaxSplits && (units * p.splits < kBusy || room > static_cast<long long>(p.splits) * kLong) && room > p.splits * kLeast) p.splits *= 2;
-  const bool wide = units * p.splits <= 152 && room >= p.splits * 2 * kLeast;
-  const Prefix x = prefix_of(a);
-  if (x.splits > 0) {
-    unsigned char* w = static_cast<unsigned char*>(workspace);
-    const cudaError_t e = launch_prefix(a, x, w, s);
+  const Plan x = plan_of(a);
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  float *o = reinterpret_cast<float*>(w + x.o), *lse = reinterpret_cast<float*>(w + x.lse);
+  const Params p = {a, a.HQ / a.HKV, (a.HQ / a.HKV + 15) / 16, x.splits, x.chunks, o, lse, x.parts, o, lse};
+  const size_t own = x.chunks > 1 ? static_cast<size_t>(x.chunks) * a.B * a.HQ : 0;  // the prefix's results come behind these
+  if (x.prefix_splits > 0) {
+    const cudaError_t e = launch_prefix(a, x, w, AttnParts{o + own * a.D, lse + own, x.prefix_splits, a.prefix_len}, s);
     if (e != cudaSuccess) return e;
-    p.part_o = reinterpret_cast<const float*>(w + x.o), p.part_lse = reinterpret_cast<const float*>(w + x.lse), p.parts = x.splits;
   }
   const bool e4 = a.cache_dtype == KDA_DTYPE_E4M3;
-  if (a.D == 64) return e4 ? launch_warps<64, true>(p, wide, s) : launch_warps<64, false>(p, wide, s);
-  return e4 ? launch_warps<128, true>(p, wide, s) : launch_warps<128, false>(p, wide, s);
+  const cudaError_t e = a.D == 64 ? (e4 ? launch_warps<64, true>(p, x.wide, s) : launch_warps<64, false>(p, x.wide, s))
+                                  : (e4 ? launch_warps<128, true>(p, x.wide, s) : launch_warps<128, false>(p, x.wide, s));
+  if (e != cudaSuccess || x.chunks == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(a.B) * a.HQ * (a.D / 4) + 127) / 128));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;  // (launched while the step's last CTAs run; it waits for them)
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return a.D == 64 ? cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<64>, p) : cudaLaunchKernelEx(&cfg, kda_attn_join_kernel<128>, p);
 }
 
 }  // namespace kda

@@ -396,6 +396,15 @@ def test_step_split(dtype, P, lens):
 
 
 @pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_step_few_rows_on_long_tables(dtype, prefix):
+    """Rows that several clusters work on; padding and empty rows among them."""
+    gen = torch.Generator().manual_seed(31 + prefix)
+    run_step(gen, [17000, 3], 3, 1, 64, 64, dtype, prefix=prefix, spread=2.0)
+    run_step(gen, [5, -1, 0], 2, 2, 128, 16, dtype, prefix=prefix, width=1200)
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
 @pytest.mark.parametrize("prefix,HQ,HKV,D,P", [(1, 2, 1, 64, 16), (15, 8, 2, 128, 16), (128, 4, 4, 64, 32), (300, 14, 2, 128, 64), (1000, 32, 2, 128, 128)])
 def test_step_prefix(dtype, prefix, HQ, HKV, D, P):
     gen = torch.Generator().manual_seed(prefix + HQ)
