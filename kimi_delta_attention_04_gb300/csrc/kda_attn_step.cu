@@ -29,6 +29,7 @@ constexpr float kTiny = 1.1754944e-38f;
 struct Params {
   kda_attn_step_args a;
   int G, head_tiles;
+  int page_bits;          // page_size = 2^page_bits
   int splits, chunks;     // CTAs of a cluster and clusters on each row and key head (and tile of its heads)
   const float* part_o;    // [parts, B, HQ, D]: results to join, normalised: the clusters' where a
   const float* part_lse;  // row has several, and the prefix's; [parts, B, HQ], in powers of two
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(128) kda_attn_join_kernel(const __grid_constan
   store_row<D>(p.a, b, head, d, j, any);
 }
 
-template <int D, bool E4, int WARPS>
+template <int D, bool E4, int WARPS, int ROWS>
 __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_constant__ Params p) {
   using Sh = Shape<D, E4, WARPS>;
   constexpr int kThreads = 32 * WARPS;
@@ -245,27 +246,37 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
       const int at0 = i * Sh::kSub + u;
       if (at0 % 32 == 0) {
         const int at = at0 + lane, tok = (first + at / Sh::kSub * step) * T + at % Sh::kSub * kGroup;
-        pages = at < steps * Sh::kSub && tok < len ? table[tok / a.page_size] : 0;
+        pages = at < steps * Sh::kSub && tok < len ? table[tok >> p.page_bits] : 0;
       }
       const int page = __shfl_sync(0xffffffffu, pages, at0 % 32), bit = s * Sh::kSub + u;
       const int tok = (first + i * step) * T + u * kGroup;
       const bool there = tok < len, good = there && page >= 0 && page < a.pages;
       bad = good || !there ? bad & ~(1u << bit) : bad | 1u << bit;
       any_bad |= there && !good;
-      const long long at = good ? (static_cast<long long>(page) * a.HKV + h) * a.page_size + tok % a.page_size : 0;
+      const long long at = good ? ((static_cast<long long>(page) * a.HKV + h) << p.page_bits) + (tok & (a.page_size - 1)) : 0;
       const int real = good ? min(kGroup, len - tok) : 0;
-      const unsigned char* ks = static_cast<const unsigned char*>(a.k_cache) + at * Sh::kRow;
-      const unsigned char* vs = static_cast<const unsigned char*>(a.v_cache) + at * Sh::kRow;
       constexpr int C = Sh::kRow / 16;
+      const unsigned char* ks = static_cast<const unsigned char*>(a.k_cache) + at * Sh::kRow + 16 * lane;
+      const unsigned char* vs = static_cast<const unsigned char*>(a.v_cache) + at * Sh::kRow + 16 * lane;
+      unsigned char* to = dst + u * kGroup * Sh::kRow;
+      if (real == kGroup) {
 #pragma unroll
-      for (int j = 0; j < kGroup * C / 32; ++j) {
-        const int n = 32 * j + lane, r = n / C, c = n % C;
-        copy16(dst + piece<Sh::kRow>(u * kGroup + r, c), ks + (r < real ? 16 * n : 0), r < real);
-        copy16(dst + T * Sh::kRow + piece<Sh::kRow>(u * kGroup + r, c), vs + (r < real ? 16 * n : 0), r < real);
+        for (int j = 0; j < kGroup * C / 32; ++j) {
+          const int n = 32 * j + lane, at_piece = piece<Sh::kRow>(n / C, n % C);
+          cp_async16(to + at_piece, ks + 512 * j);
+          cp_async16(to + T * Sh::kRow + at_piece, vs + 512 * j);
+        }
+      } else {  // tokens that are not there become zeros
+#pragma unroll
+        for (int j = 0; j < kGroup * C / 32; ++j) {
+          const int n = 32 * j + lane, r = n / C, at_piece = piece<Sh::kRow>(r, n % C);
+          copy16(to + at_piece, r < real ? static_cast<const void*>(ks + 512 * j) : a.q, r < real);
+          copy16(to + T * Sh::kRow + at_piece, r < real ? static_cast<const void*>(vs + 512 * j) : a.q, r < real);
+        }
       }
       if (E4 && lane < 8)
         copy16(dst + 2 * T * Sh::kRow + (lane / 4) * 4 * T + u * 4 * kGroup + 16 * (lane & 3),
-               (lane < 4 ? a.k_scale : a.v_scale) + at + (good ? 4 * (lane & 3) : 0), good);
+               good ? static_cast<const void*>((lane < 4 ? a.k_scale : a.v_scale) + at + 4 * (lane & 3)) : a.q, good);
     }
   };
 
@@ -329,7 +340,7 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
 #pragma unroll
       for (int e = 0; e < 2; ++e) lv[e] = E4 ? lg2_approx(scales[T + 8 * n + 2 * t + e]) : 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 2 * ROWS; ++e) {
         const int tok = 8 * n + 2 * t + (e & 1);
         const float x = (sc[n][e] + sd[n][e]) * (E4 ? scales[tok] * c2[e >> 1] : c2[e >> 1]);
         sc[n][e] = tok % kGroup < real[n / 2] ? x : -INFINITY;
@@ -341,16 +352,16 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
       }
     }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
       top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
       if (E4) topv[r] = fmaxf(topv[r], __shfl_xor_sync(0xffffffffu, topv[r], 1));
       top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
       if (E4) topv[r] = fmaxf(topv[r], __shfl_xor_sync(0xffffffffu, topv[r], 2));
     }
-    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1] || (E4 && (topv[0] > mv[0] || topv[1] > mv[1])))) {
+    if (__any_sync(0xffffffffu, top[0] > m[0] || topv[0] > mv[0] || (ROWS > 1 && (top[1] > m[1] || topv[1] > mv[1])))) {
       float keep[2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < ROWS; ++r) {
         keep[r] = factor(m[r], top[r]);
         m[r] = top[r];
         l[r] *= keep[r];
@@ -360,14 +371,17 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
         }
       }
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) o[j][0] *= keep[0], o[j][1] *= keep[0], o[j][2] *= keep[1], o[j][3] *= keep[1];
+      for (int j = 0; j < D / 8; ++j) {
+        o[j][0] *= keep[0], o[j][1] *= keep[0];
+        if (ROWS > 1) o[j][2] *= keep[1], o[j][3] *= keep[1];
+      }
     }
     const float mz[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
     const float mvz[2] = {mv[0] == -INFINITY ? 0.f : mv[0], mv[1] == -INFINITY ? 0.f : mv[1]};
 #pragma unroll
     for (int n = 0; n < N; ++n) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 2 * ROWS; ++e) {
         const float x = sc[n][e];
         // (a weight of a finite score stays above 0: an infinite value stays one)
         float w = ex2_approx(x - mz[e >> 1]);
@@ -378,8 +392,9 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t pa[4] = {pack_weights<E4>(sc[2 * u][0], sc[2 * u][1]), pack_weights<E4>(sc[2 * u][2], sc[2 * u][3]),
-                              pack_weights<E4>(sc[2 * u + 1][0], sc[2 * u + 1][1]), pack_weights<E4>(sc[2 * u + 1][2], sc[2 * u + 1][3])};
+      const uint32_t pa[4] = {pack_weights<E4>(sc[2 * u][0], sc[2 * u][1]), ROWS == 1 ? 0u : pack_weights<E4>(sc[2 * u][2], sc[2 * u][3]),
+                              pack_weights<E4>(sc[2 * u + 1][0], sc[2 * u + 1][1]),
+                              ROWS == 1 ? 0u : pack_weights<E4>(sc[2 * u + 1][2], sc[2 * u + 1][3])};
       const int r = u * kGroup + (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
       if (E4) {
 #pragma unroll
@@ -488,11 +503,11 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
   if (p.splits > 1) cluster_sync_all();  // no CTA ends while another may read its results
 }
 
-template <int D, bool E4, int WARPS>
+template <int D, bool E4, int WARPS, int ROWS>
 cudaError_t launch(const Params& p, cudaStream_t s) {
   using Sh = Shape<D, E4, WARPS>;
   static std::atomic<uint64_t> smem_set{0};
-  auto kernel = kda_attn_step_kernel<D, E4, WARPS>;
+  auto kernel = kda_attn_step_kernel<D, E4, WARPS, ROWS>;
   cudaError_t e = set_smem_limit_once(kernel, Sh::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(p.a.B) * p.a.HKV * p.head_tiles * p.splits * p.chunks;
@@ -513,7 +528,9 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
 
 template <int D, bool E4>
 cudaError_t launch_warps(const Params& p, bool wide, cudaStream_t s) {
-  return wide ? launch<D, E4, 8>(p, s) : launch<D, E4, 4>(p, s);
+  // (A lane's scores are of heads g and g + 8: with up to 8 heads the second half is nothing.)
+  if (p.G <= 8) return wide ? launch<D, E4, 8, 1>(p, s) : launch<D, E4, 4, 1>(p, s);
+  return wide ? launch<D, E4, 8, 2>(p, s) : launch<D, E4, 4, 2>(p, s);
 }
 
 // ---- the prefix ----
@@ -633,7 +650,7 @@ cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaS
   const Plan x = plan_of(a);
   unsigned char* w = static_cast<unsigned char*>(workspace);
   float *o = reinterpret_cast<float*>(w + x.o), *lse = reinterpret_cast<float*>(w + x.lse);
-  const Params p = {a, a.HQ / a.HKV, (a.HQ / a.HKV + 15) / 16, x.splits, x.chunks, o, lse, x.parts, o, lse};
+  const Params p = {a, a.HQ / a.HKV, (a.HQ / a.HKV + 15) / 16, __builtin_ctz(a.page_size), x.splits, x.chunks, o, lse, x.parts, o, lse};
   const size_t own = x.chunks > 1 ? static_cast<size_t>(x.chunks) * a.B * a.HQ : 0;  // the prefix's results come behind these
   if (x.prefix_splits > 0) {
     const cudaError_t e = launch_prefix(a, x, w, AttnParts{o + own * a.D, lse + own, x.prefix_splits, a.prefix_len}, s);
