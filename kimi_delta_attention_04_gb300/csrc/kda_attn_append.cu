@@ -12,7 +12,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeadsAtOnce = 4;  // heads of a group whose loads are in flight together
+constexpr int kHeadsAtOnce = 3;  // heads of a group whose loads are in flight together
 
 __device__ __forceinline__ void unpack8(const uint4& r, float (&v)[8]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -41,7 +41,7 @@ __device__ __forceinline__ float power_scale(float m) {
 enum { kPlain = 0, kHalves = 1, kNeighbours = 2, kAny = 3 };
 
 template <int D, int MODE, bool E4>
-__global__ void __launch_bounds__(kThreads) kda_kv_append_kernel(const kda_kv_append_args p, int groups, int heads) {
+__global__ void __launch_bounds__(kThreads, MODE == kAny ? 2 : 4) kda_kv_append_kernel(const __grid_constant__ kda_kv_append_args p, int groups, int heads) {
   constexpr int L = D / 8;  // lanes of a head
   const int lane = threadIdx.x % L, c = 8 * lane;
   const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
@@ -49,83 +49,82 @@ __global__ void __launch_bounds__(kThreads) kda_kv_append_kernel(const kda_kv_ap
   const int group = static_cast<int>(unit % groups);
   const bool live = token < p.tokens;
   const long long t = live ? token : 0;
-
   const int HQ = p.q ? p.HQ : 0;
-  int slot = live ? p.slots[t] : -1;
-  bool turn = true;
-  int pos = 0;
-  if (MODE != kPlain && live) {
-    pos = p.positions[t];
-    turn = pos >= 0 && pos < p.max_positions;
-    if (!turn) {
-      if (slot >= 0 && lane == 0 && group == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
-      pos = 0;
-      slot = -1;
-    }
-  }
-  if (slot >= p.pages * p.page_size) {
-    if (lane == 0 && group == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
-    slot = -1;
-  }
   const int rot = MODE == kPlain ? 0 : p.rot, half = rot / 2;
-  const float* row = p.cos_sin + static_cast<long long>(pos) * rot;
-  const bool table = MODE != kPlain && p.max_positions > 0;
+  const bool pairs = MODE == kNeighbours || (MODE == kAny && (p.flags & KDA_KV_FLAG_INTERLEAVED));
 
-  // value of channel c + i: x cs[i] + partner sn[i]
-  float cs[8], sn[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = turn ? 1.f : 0.f, sn[i] = 0.f;
-  if (turn && table && c < rot) {
-    if (MODE == kHalves) {
-      const int at = c < half ? c : c - half;
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(row + at + i), b = *reinterpret_cast<const float4*>(row + half + at + i);
-        const float s = c < half ? -1.f : 1.f;
-        cs[i] = a.x, cs[i + 1] = a.y, cs[i + 2] = a.z, cs[i + 3] = a.w;
-        sn[i] = s * b.x, sn[i + 1] = s * b.y, sn[i + 2] = s * b.z, sn[i + 3] = s * b.w;
-      }
-    } else if (MODE == kNeighbours) {
-      const float4 a = *reinterpret_cast<const float4*>(row + c / 2), b = *reinterpret_cast<const float4*>(row + half + c / 2);
-      cs[0] = cs[1] = a.x, cs[2] = cs[3] = a.y, cs[4] = cs[5] = a.z, cs[6] = cs[7] = a.w;
-      sn[0] = -b.x, sn[1] = b.x, sn[2] = -b.y, sn[3] = b.y, sn[4] = -b.z, sn[5] = b.z, sn[6] = -b.w, sn[7] = b.w;
-    } else if (MODE == kAny) {
-      const bool pairs = p.flags & KDA_KV_FLAG_INTERLEAVED;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int d = c + i;
-        if (d >= rot) continue;
-        const int at = pairs ? d / 2 : d < half ? d : d - half;
-        cs[i] = row[at];
-        sn[i] = (pairs ? d % 2 == 0 : d < half) ? -row[half + at] : row[half + at];
-      }
-    }
-  }
+  const __nv_bfloat16* xq = static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride + c;
+  const __nv_bfloat16* xk = static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride + c;
+  const __nv_bfloat16* xv = static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride + c;
+  int slot = live ? p.slots[t] : -1;
+  int pos = MODE != kPlain && live ? p.positions[t] : 0;
+  bool turn = true, looked = false;
+  float cs[8], sn[8];  // value of channel c + i: x cs[i] + partner sn[i]
+  int page = 0, off = 0;
   const int other = MODE == kHalves ? (c >= rot ? lane : c < half ? lane + half / 8 : lane - half / 8) : lane;
 
-  const int page = slot >= 0 ? slot / p.page_size : 0, off = slot >= 0 ? slot % p.page_size : 0;
   for (int base = 0; base < heads; base += groups * kHeadsAtOnce) {  // (the same for a warp's lanes: they shuffle)
     const int h0 = base + group;
     uint4 raw[kHeadsAtOnce];
     float partner[MODE == kAny ? kHeadsAtOnce : 1][8];
-    // all of a group's loads come before its stores: q_out may be q, and k_out k
+    // all of a group's loads come before its stores (q_out may be q, and k_out k), and before
+    // what depends on the token's place and position
 #pragma unroll
     for (int u = 0; u < kHeadsAtOnce; ++u) {
       const int h = h0 + u * groups;
       raw[u] = make_uint4(0, 0, 0, 0);
       if (live && h < heads) {
-        const __nv_bfloat16* x = h < HQ ? static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride + static_cast<long long>(h) * D
-                                 : h < HQ + p.HKV
-                                     ? static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride + static_cast<long long>(h - HQ) * D
-                                     : static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride + static_cast<long long>(h - HQ - p.HKV) * D;
-        raw[u] = *reinterpret_cast<const uint4*>(x + c);
+        const __nv_bfloat16* x = h < HQ ? xq + h * D : h < HQ + p.HKV ? xk + (h - HQ) * D : xv + (h - HQ - p.HKV) * D;
+        raw[u] = *reinterpret_cast<const uint4*>(x);
         if (MODE == kAny) {
-          const bool pairs = p.flags & KDA_KV_FLAG_INTERLEAVED;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int d = c + i;
             const int q = d >= rot ? d : pairs ? (d ^ 1) : d < half ? d + half : d - half;
-            partner[u][i] = __bfloat162float(x[q]);
+            partner[u][i] = __bfloat162float(x[q - c]);
+          }
+        }
+      }
+    }
+    if (!looked) {
+      looked = true;
+      if (MODE != kPlain && live) {
+        turn = pos >= 0 && pos < p.max_positions;
+        if (!turn) {
+          if (slot >= 0 && lane == 0 && group == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
+          slot = -1;
+        }
+      }
+      if (slot >= p.pages * p.page_size) {
+        if (lane == 0 && group == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
+        slot = -1;
+      }
+      if (slot >= 0) page = slot / p.page_size, off = slot % p.page_size;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
+      if (MODE != kPlain && live && turn && c < rot) {
+        const float* row = p.cos_sin + static_cast<long long>(pos) * rot;
+        if (MODE == kHalves) {
+          const int at = c < half ? c : c - half;
+          const float sign = c < half ? -1.f : 1.f;
+#pragma unroll
+          for (int i = 0; i < 8; i += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(row + at + i), b = *reinterpret_cast<const float4*>(row + half + at + i);
+            cs[i] = a.x, cs[i + 1] = a.y, cs[i + 2] = a.z, cs[i + 3] = a.w;
+            sn[i] = sign * b.x, sn[i + 1] = sign * b.y, sn[i + 2] = sign * b.z, sn[i + 3] = sign * b.w;
+          }
+        } else if (MODE == kNeighbours) {
+          const float4 a = *reinterpret_cast<const float4*>(row + c / 2), b = *reinterpret_cast<const float4*>(row + half + c / 2);
+          cs[0] = cs[1] = a.x, cs[2] = cs[3] = a.y, cs[4] = cs[5] = a.z, cs[6] = cs[7] = a.w;
+          sn[0] = -b.x, sn[1] = b.x, sn[2] = -b.y, sn[3] = b.y, sn[4] = -b.z, sn[5] = b.z, sn[6] = -b.w, sn[7] = b.w;
+        } else if (MODE == kAny) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int d = c + i;
+            if (d >= rot) continue;
+            const int at = pairs ? d / 2 : d < half ? d : d - half;
+            cs[i] = row[at];
+            sn[i] = (pairs ? d % 2 == 0 : d < half) ? -row[half + at] : row[half + at];
           }
         }
       }
@@ -134,6 +133,7 @@ __global__ void __launch_bounds__(kThreads) kda_kv_append_kernel(const kda_kv_ap
 #pragma unroll
     for (int u = 0; u < kHeadsAtOnce; ++u) {
       const int h = h0 + u * groups;
+      if (base + u * groups >= heads) break;  // (no lane of the warp has a head here)
       const bool valid = live && h < heads, is_v = h >= HQ + p.HKV;
       float x[8], y[8];
       unpack8(raw[u], x);
@@ -156,24 +156,23 @@ __global__ void __launch_bounds__(kThreads) kda_kv_append_kernel(const kda_kv_ap
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (!turn) x[i] = 0.f;
-          else if (c + i < rot) x[i] = x[i] * cs[i] + y[i] * sn[i];
+          else if (MODE != kAny || c + i < rot) x[i] = x[i] * cs[i] + y[i] * sn[i];
         }
       }
       if (valid && h < HQ) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.q_out) + t * p.q_out_stride + static_cast<long long>(h) * D + c;
-        *reinterpret_cast<uint4*>(o) = pack8(x);
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.q_out) + t * p.q_out_stride + h * D + c) = pack8(x);
       } else if (valid && !is_v && p.k_out) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.k_out) + t * p.k_out_stride + static_cast<long long>(h - HQ) * D + c;
-        *reinterpret_cast<uint4*>(o) = pack8(x);
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_out) + t * p.k_out_stride + (h - HQ) * D + c) = pack8(x);
       }
       if (E4) {
+        if (base + (u + 1) * groups <= HQ) continue;  // (queries only in the whole warp)
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (valid && h >= HQ && slot >= 0) {
-          const float s = power_scale(m), inv = 1.f / s;
+          const float s = power_scale(m), inv = s == s ? __uint_as_float((254u << 23) - __float_as_uint(s)) : s;
           const long long at = (static_cast<long long>(page) * p.HKV + (is_v ? h - HQ - p.HKV : h - HQ)) * p.page_size + off;
           uint2 b;
           b.x = pack_e4m3x2(x[0] * inv, x[1] * inv) | pack_e4m3x2(x[2] * inv, x[3] * inv) << 16;
