@@ -190,6 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char raw[];
   __shared__ Head sm;
   const kda_attn_fwd_args& a = p.a;
+  // (a step that joins these results has work of its own to do before it)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
   unsigned char* ring = tiles + 2 * Sh::kTile;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

@@ -118,12 +118,22 @@ __device__ __forceinline__ float factor(float was, float now) {
 // Adds the results in the workspace for a row and head, 4 channels from d.
 template <int D>
 __device__ __forceinline__ void join_parts(const Params& p, long long b, int head, int d, Joined& j, int& any) {
-  for (int s = 0; s < p.parts; ++s) {
-    const long long at = (static_cast<long long>(s) * p.a.B + b) * p.a.HQ + head;
-    const float lse = p.part_lse[at];
-    if (lse == -INFINITY) continue;  // no key
-    any = 1;
-    j.add(lse, 1.f, *reinterpret_cast<const float4*>(p.part_o + at * D + d));
+  constexpr int kAtOnce = 4;  // loads in flight together
+  for (int s0 = 0; s0 < p.parts; s0 += kAtOnce) {
+    float lse[kAtOnce];
+    float4 o[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const long long at = (static_cast<long long>(min(s0 + i, p.parts - 1)) * p.a.B + b) * p.a.HQ + head;
+      lse[i] = s0 + i < p.parts ? __ldcg(p.part_lse + at) : -INFINITY;
+      o[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (lse[i] == -INFINITY) continue;  // no key
+      any = 1;
+      j.add(lse[i], 1.f, o[i]);
+    }
   }
 }
 
@@ -169,6 +179,17 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
   const int h = static_cast<int>(unit % a.HKV);
   const int b = static_cast<int>(unit / a.HKV);
   const int head0 = h * p.G + tile * 16, heads = min(16, p.G - tile * 16);
+
+  // pages of this warp's next 32 groups, one a lane; the first ones are asked for before the
+  // row's length is there (entries behind its last page are not used)
+  constexpr int T = Sh::kTokens;
+  const int first = rank * WARPS + warp, step = p.chunks * p.splits * WARPS;  // of the row's steps of T tokens
+  const int32_t* table = a.block_table + static_cast<long long>(b) * a.table_width;
+  int pages = 0;
+  {
+    const long long tok = static_cast<long long>(first + lane / Sh::kSub * step) * T + lane % Sh::kSub * kGroup;
+    if (tok < static_cast<long long>(a.table_width) << p.page_bits) pages = table[tok >> p.page_bits];
+  }
 
   int len = a.seq_lens[b];
   const bool row = len >= 0 && len <= a.table_width * a.page_size;
@@ -228,14 +249,8 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
   }
 
   unsigned char* ring = raw + warp * Sh::kWarpBytes;
-  constexpr int T = Sh::kTokens;
-  const int all = (len + T - 1) / T;  // steps of T tokens; this warp has every (CTAs of the row x WARPS)-th
-  const int first = rank * WARPS + warp, step = p.chunks * p.splits * WARPS;
+  const int all = (len + T - 1) / T;  // the row's steps; this warp has every (CTAs of the row x WARPS)-th
   const int steps = all > first ? (all - first + step - 1) / step : 0;
-  const int32_t* table = a.block_table + static_cast<long long>(b) * a.table_width;
-
-  // pages of the next 32 groups, one a lane
-  int pages = 0;
   uint32_t bad = 0;  // by stage and group: its page is out of range
   bool any_bad = false;
   auto load = [&](int i) {
@@ -244,7 +259,7 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
 #pragma unroll
     for (int u = 0; u < Sh::kSub; ++u) {
       const int at0 = i * Sh::kSub + u;
-      if (at0 % 32 == 0) {
+      if (at0 % 32 == 0 && at0 > 0) {
         const int at = at0 + lane, tok = (first + at / Sh::kSub * step) * T + at % Sh::kSub * kGroup;
         pages = at < steps * Sh::kSub && tok < len ? table[tok >> p.page_bits] : 0;
       }
@@ -474,7 +489,9 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
   if (p.splits > 1) cluster_sync_all();
   else __syncthreads();
 
-  // the splits' results and the prefix's, in order
+  // the splits' results and the prefix's, in order (the prefix's kernel may still have been
+  // running beside this one's loop)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int u = in_cluster * kThreads + tid; u < heads * Q; u += p.splits * kThreads) {
     const int r = u / Q, d = 4 * (u % Q), head = head0 + r;
     Joined j;
@@ -504,7 +521,7 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
 }
 
 template <int D, bool E4, int WARPS, int ROWS>
-cudaError_t launch(const Params& p, cudaStream_t s) {
+cudaError_t launch(const Params& p, bool after_prefix, cudaStream_t s) {
   using Sh = Shape<D, E4, WARPS>;
   static std::atomic<uint64_t> smem_set{0};
   auto kernel = kda_attn_step_kernel<D, E4, WARPS, ROWS>;
@@ -517,20 +534,38 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   cfg.blockDim = dim3(32 * WARPS);
   cfg.dynamicSmemBytes = Sh::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(p.splits);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  cudaLaunchAttribute attrs[2];
+  int n = 0;
+  if (p.splits > 1) {
+    attrs[n].id = cudaLaunchAttributeClusterDimension;
+    attrs[n].val.clusterDim.x = static_cast<unsigned>(p.splits);
+    attrs[n].val.clusterDim.y = attrs[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (after_prefix) {  // its CTAs start where the prefix's leave SMs free
+    attrs[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attrs;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// How a call's work is laid out, and where its parts' results lie in the workspace.
+struct Plan {
+  int splits = 1, chunks = 1, parts = 0;  // of the rows' own tokens; all results to join
+  int prefix_splits = 0, prefix_pages = 0;
+  bool wide = false;                      // 8 warps to a CTA
+  size_t lse = 0, o = 0, table = 0, k = 0, v = 0, bytes = 0;
+};
+
 template <int D, bool E4>
-cudaError_t launch_warps(const Params& p, bool wide, cudaStream_t s) {
+cudaError_t launch_warps(const Params& p, const Plan& x, cudaStream_t s) {
+  const bool wide = x.wide, after = x.prefix_splits > 0;
   // (A lane's scores are of heads g and g + 8: with up to 8 heads the second half is nothing.)
-  if (p.G <= 8) return wide ? launch<D, E4, 8, 1>(p, s) : launch<D, E4, 4, 1>(p, s);
-  return wide ? launch<D, E4, 8, 2>(p, s) : launch<D, E4, 4, 2>(p, s);
+  if (p.G <= 8) return wide ? launch<D, E4, 8, 1>(p, after, s) : launch<D, E4, 4, 1>(p, after, s);
+  return wide ? launch<D, E4, 8, 2>(p, after, s) : launch<D, E4, 4, 2>(p, after, s);
 }
 
 // ---- the prefix ----
@@ -563,14 +598,6 @@ __global__ void __launch_bounds__(256) kda_attn_prefix_bf16_kernel(const kda_att
     *reinterpret_cast<uint4*>((of_v ? vals : k) + (to + t) * D + c) = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
-
-// How a call's work is laid out, and where its parts' results lie in the workspace.
-struct Plan {
-  int splits = 1, chunks = 1, parts = 0;  // of the rows' own tokens; all results to join
-  int prefix_splits = 0, prefix_pages = 0;
-  bool wide = false;                      // 8 warps to a CTA
-  size_t lse = 0, o = 0, table = 0, k = 0, v = 0, bytes = 0;
-};
 
 Plan plan_of(const kda_attn_step_args& a) {
   Plan x;
@@ -657,8 +684,8 @@ cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaS
     if (e != cudaSuccess) return e;
   }
   const bool e4 = a.cache_dtype == KDA_DTYPE_E4M3;
-  const cudaError_t e = a.D == 64 ? (e4 ? launch_warps<64, true>(p, x.wide, s) : launch_warps<64, false>(p, x.wide, s))
-                                  : (e4 ? launch_warps<128, true>(p, x.wide, s) : launch_warps<128, false>(p, x.wide, s));
+  const cudaError_t e = a.D == 64 ? (e4 ? launch_warps<64, true>(p, x, s) : launch_warps<64, false>(p, x, s))
+                                  : (e4 ? launch_warps<128, true>(p, x, s) : launch_warps<128, false>(p, x, s));
   if (e != cudaSuccess || x.chunks == 1) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(a.B) * a.HQ * (a.D / 4) + 127) / 128));
