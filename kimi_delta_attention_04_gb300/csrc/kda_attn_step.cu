@@ -556,16 +556,24 @@ cudaError_t launch(const Params& p, bool after_prefix, cudaStream_t s) {
 struct Plan {
   int splits = 1, chunks = 1, parts = 0;  // of the rows' own tokens; all results to join
   int prefix_splits = 0, prefix_pages = 0;
-  bool wide = false;                      // 8 warps to a CTA
+  int warps = 4;                          // to a CTA: 2, 4 or 8
   size_t lse = 0, o = 0, table = 0, k = 0, v = 0, bytes = 0;
 };
 
+template <int D, bool E4, int ROWS>
+cudaError_t launch_rows(const Params& p, const Plan& x, cudaStream_t s) {
+  const bool after = x.prefix_splits > 0;
+  if (x.warps == 8) return launch<D, E4, 8, ROWS>(p, after, s);
+  if constexpr (!E4) {
+    if (x.warps == 2) return launch<D, E4, 2, ROWS>(p, after, s);
+  }
+  return launch<D, E4, 4, ROWS>(p, after, s);
+}
+
+// (A lane's scores are of heads g and g + 8: with up to 8 heads the second half is nothing.)
 template <int D, bool E4>
 cudaError_t launch_warps(const Params& p, const Plan& x, cudaStream_t s) {
-  const bool wide = x.wide, after = x.prefix_splits > 0;
-  // (A lane's scores are of heads g and g + 8: with up to 8 heads the second half is nothing.)
-  if (p.G <= 8) return wide ? launch<D, E4, 8, 1>(p, after, s) : launch<D, E4, 4, 1>(p, after, s);
-  return wide ? launch<D, E4, 8, 2>(p, after, s) : launch<D, E4, 4, 2>(p, after, s);
+  return p.G <= 8 ? launch_rows<D, E4, 1>(p, x, s) : launch_rows<D, E4, 2>(p, x, s);
 }
 
 // ---- the prefix ----
@@ -604,18 +612,25 @@ Plan plan_of(const kda_attn_step_args& a) {
   const int G = a.HQ / a.HKV;
   // A cluster for each row and key head (and 16 heads of its group): CTAs for two on each
   // of the 152 SMs as far as their share stays at 64 tokens of what the table has room
-  // for, and enough that it is no more than 4096 (rows of unequal lengths leave SMs idle
-  // behind the longest: 64 rows of up to 8192 tokens took 223 us with one CTA each, 185
-  // with four; 256 of up to 2500 take 14 % longer with two).
+  // for, and enough that a CTA's share is no more than 1 MB (rows of unequal lengths leave
+  // SMs idle behind the longest: 64 rows of up to 8192 tokens took 223 us with one CTA
+  // each, 178 with four).
   const long long units = static_cast<long long>(a.B) * a.HKV * ((G + 15) / 16), room = static_cast<long long>(a.table_width) * a.page_size;
-  while (x.splits < kMaxSplits && (units * x.splits < 2 * 152 || room > 4096ll * x.splits) && room > 64ll * x.splits) x.splits *= 2;
+  const bool e4 = a.cache_dtype == KDA_DTYPE_E4M3;
+  const long long share = (1 << 20) / (2 * a.D * (e4 ? 1 : 2));
+  while (x.splits < kMaxSplits && (units * x.splits < 2 * 152 || room > share * x.splits) && room > 64ll * x.splits) x.splits *= 2;
   // Few long rows: several clusters each, with a launch of its own to join their results.
   // (Clusters of 16 leave SMs idle: one row of 131072 tokens took 140 us with them.)
   if (units * x.splits <= 152 && room >= KDA_ATTN_LONG_TOKENS) {
     const long long fill = 2 * 152 / (units * x.splits), each = room / (512 * x.splits);
     x.chunks = static_cast<int>(fill < each ? fill : each);
   }
-  x.wide = units * x.splits * x.chunks <= 152 && room >= 128ll * x.splits * x.chunks;
+  // Many CTAs: two warps each, four of them on an SM, so that one's start and end pass under
+  // the others' loads (256 rows of up to 500 tokens with a prefix: 94 -> 89 us; with 8-bit
+  // keys, whose products take longer, 197 -> 203, so not there). Few: eight warps.
+  const long long ctas = units * x.splits * x.chunks;
+  if (ctas >= 4 * 152 && !e4) x.warps = 2;
+  if (ctas <= 152 && room >= 128ll * x.splits * x.chunks) x.warps = 8;
   if (a.prefix_len > 0) {
     // Splits that keep the SMs busy: rounds of CTAs, each with its share of the blocks and
     // 4 blocks' time for what a CTA does besides.
