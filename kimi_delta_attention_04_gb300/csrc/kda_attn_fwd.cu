@@ -51,13 +51,27 @@ struct Shape {
 struct Params {
   kda_attn_fwd_args a;
   AttnParts parts;
-  int G, Gp, lg, sub, heads;  // Gp = 2^lg query heads to a tile, sub such sets a key head, heads sets in all
+  int G, Gp, sub, heads;      // Gp query heads to a tile, sub such sets a key head, heads sets in all
+  int tile_tokens, per_token; // tokens to a tile; 65536 / Gp rounded up: row r is of token r per_token >> 16
   int slots;                  // places for query tiles
 };
 
+// What a CTA works on next.
+struct Item {
+  int n, hk, h0;         // sequence (-1: there is nothing left), key head, first query head
+  int q0, k0;            // its first query and key
+  int T, S, shift;       // queries and keys; query i sees keys up to i + shift
+  int t0;                // first query token of the CTA
+  int split, first;      // of the key blocks: which part of them, the first of these,
+  int count[2];          // and how many each tile has
+};
+
 struct Head {
-  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], tail_there, tail_zero, drain;  // p_full: a block's first kFirst keys, and the rest
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], tail_there, tail_zero, drain;  // p_full: a block's first kFirst keys, and the rest
   uint64_t full[8], empty[8];
+  uint64_t item_full[2], item_empty[2], next_there;
+  alignas(16) uint32_t next[4];  // the answer to the request for another CTA's place
+  Item items[2];
   uint32_t bad[8];            // by block, of the last 8: keys on pages that are out of range, a bit for each 16
   uint32_t tmem_base;
   int failed;
@@ -97,25 +111,15 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
-// What one CTA works on.
-struct Item {
-  int n, hk, h0;            // sequence, key head, first query head
-  long long q0, k0;         // its first query and key
-  int T, S, shift;          // queries and keys; query i sees keys up to i + shift
-  int t0;                   // first query token of the CTA
-  int split, first, count[2];  // key blocks: first, and how many for each tile
-};
-
 // The products of both tiles, issued by one thread. (It is elected: operands are then as
 // the tensor core's instructions want them and an issue takes the products' own time, 64
 // cycles each, where a thread chosen by its lane took 140. A warp for each tile's products
 // interleaves them, and each waits longer for its own: 444 us instead of 395 for 8192
 // tokens and 32 heads of 128.)
 template <int D>
-__device__ __forceinline__ void issue_products(Head& sm, const Item& it, unsigned char* tiles) {
+__device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* tiles) {
   using Sh = Shape<D>;
   constexpr uint32_t qk = tc05::idesc_f16kind(kRows, kRows, true), pv = tc05::idesc_f16kind(kRows, D, true) | tc05::kIdescBMnMajor;
-  const int count0 = it.count[0], count1 = it.count[1], blocks = max(count0, count1), keys = it.S - it.first * kRows;
   const uint64_t desc = tc05::smem_desc(0, 16, 1024, tc05::kSwizzle128B), desc_mn = tc05::smem_desc(0, kHalf, 1024, tc05::kSwizzle128B);
   const uint32_t q_base = smem_u32(tiles) >> 4, r_base = q_base + (2 * Sh::kTile >> 4);
   auto scores = [&](int m, int s) {  // S = Q K^T
@@ -133,53 +137,146 @@ __device__ __forceinline__ void issue_products(Head& sm, const Item& it, unsigne
     for (int c = from; c < to; ++c) tc05::mma_ts(Sh::kO + m * D, m * kRows + 8 * c, v + ((c * 16 * 128) >> 4), pv, add || c > 0);
   };
   bool going = true;
-  if (blocks > 0) {
-    going = wait(&sm.full[0], 0);
+  int s = 0, phase = 0;              // stage of the ring that comes next
+  int done[2] = {0, 0}, tiles_done[2] = {0, 0}, tails = 0;  // blocks and tiles so far, whose parities their barriers have
+  auto advance = [&]() {
+    if (++s == Sh::kStages) s = 0, phase ^= 1;
+  };
+  for (int k = 0; going; ++k) {
+    going = wait(&sm.item_full[k & 1], (k >> 1) & 1);
+    if (!going) break;
+    const Item& it = sm.items[k & 1];
+    if (it.n < 0) break;
+    const int count0 = it.count[0], count1 = it.count[1], blocks = max(count0, count1), keys = it.S - it.first * kRows;
+    if (blocks > 0) {
+      going = wait(&sm.full[s], phase);
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      if ((m == 0 ? count0 : count1) == 0) continue;
-      going = going && wait(&sm.q_full[m], 0);
-      tc05::fence_after_sync();
-      if (going) scores(m, 0);
-    }
-    tc05::commit(&sm.empty[0]);
-  }
-  int vs = 1, v_phase = 0;  // stage and phase of the block's values; the next block's keys come after them
-  for (int i = 0; i < blocks && going; ++i) {
-    int ks = vs + 1, k_phase = v_phase;
-    if (ks == Sh::kStages) ks = 0, k_phase ^= 1;
-    going = wait(&sm.full[vs], v_phase);
-    if (i + 1 < blocks) going = going && wait(&sm.full[ks], k_phase);
-    const bool tail = keys < (i + 1) * kRows;  // the sequence's last block is not full: zeros behind its last key
-    if (tail && going) mbar_arrive_local(&sm.tail_there);
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int count = m == 0 ? count0 : count1;
-      if (i >= count || !going) continue;
-      const bool last_v = m == 1 || i >= count1, last_k = m == 1 || i + 1 >= count1;  // no other tile needs the block
-      going = wait(&sm.p_full[m][0], i & 1);
-      if (tail) going = going && wait(&sm.tail_zero, 0);
-      tc05::fence_after_sync();
-      if (going) values(m, vs, 0, kFirst / 16, i > 0);
-      going = going && wait(&sm.p_full[m][1], i & 1);
-      tc05::fence_after_sync();
-      if (going) values(m, vs, kFirst / 16, kRows / 16, true);
-      if (i + 1 < count) {
-        if (going) scores(m, ks);
-        if (last_k) tc05::commit(&sm.empty[ks]);
-      } else {
-        tc05::commit(&sm.o_full[m]);
+      for (int m = 0; m < 2; ++m) {
+        const int count = m == 0 ? count0 : count1;
+        if (count == 0) continue;
+        going = going && wait(&sm.q_full[m], tiles_done[m]++ & 1);
+        tc05::fence_after_sync();
+        if (going) scores(m, s);
+        if (count == 1) tc05::commit(&sm.q_empty[m]);
       }
-      if (last_v) tc05::commit(&sm.empty[vs]);
+      tc05::commit(&sm.empty[s]);
+      advance();
     }
-    vs = ks + 1, v_phase = k_phase;
-    if (vs == Sh::kStages) vs = 0, v_phase ^= 1;
+    for (int i = 0; i < blocks && going; ++i) {
+      const int vs = s, v_phase = phase;  // the block's values; the next block's keys come after them
+      advance();
+      going = wait(&sm.full[vs], v_phase);
+      if (i + 1 < blocks) going = going && wait(&sm.full[s], phase);
+      const bool tail = keys < (i + 1) * kRows;  // the sequence's last block is not full: zeros behind its last key
+      if (tail && going) mbar_arrive_local(&sm.tail_there);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int count = m == 0 ? count0 : count1;
+        if (i >= count || !going) continue;
+        const bool last_v = m == 1 || i >= count1, last_k = m == 1 || i + 1 >= count1;  // no other tile needs the block
+        const int parity = done[m]++ & 1;
+        going = wait(&sm.p_full[m][0], parity);
+        if (tail) going = going && wait(&sm.tail_zero, tails & 1);
+        tc05::fence_after_sync();
+        if (going) values(m, vs, 0, kFirst / 16, i > 0);
+        going = going && wait(&sm.p_full[m][1], parity);
+        tc05::fence_after_sync();
+        if (going) values(m, vs, kFirst / 16, kRows / 16, true);
+        if (i + 1 < count) {
+          if (going) scores(m, s);
+          if (i + 2 == count) tc05::commit(&sm.q_empty[m]);
+          if (last_k) tc05::commit(&sm.empty[s]);
+        } else {
+          tc05::commit(&sm.o_full[m]);
+        }
+        if (last_v) tc05::commit(&sm.empty[vs]);
+      }
+      if (tail) ++tails;
+      if (i + 1 < blocks) advance();
+    }
+    mbar_arrive_local(&sm.item_empty[k & 1]);
   }
   if (!going) {  // products in flight end before their tensor memory is given back
-    sm.failed = 1;
     tc05::commit(&sm.drain);
     wait(&sm.drain, 0);
   }
+  return going;
+}
+
+// The item of a place in the grid: false where no tile has it. One warp.
+// Places in falling order, so that a causal prompt's long tiles start first. Sequence n's
+// tiles have the places from cu_seqlens[n] / (tokens of a CTA) + n on, of which there are
+// enough for it before the next sequence's.
+template <bool PAGED>
+__device__ __forceinline__ bool item_of(const Params& p, long long index, int lane, Item& it) {
+  const kda_attn_fwd_args& a = p.a;
+  const int cta_tokens = 2 * p.tile_tokens;
+  it.split = static_cast<int>(index % p.parts.splits);
+  index /= p.parts.splits;
+  const int set = static_cast<int>(index % p.heads);
+  const int slot = p.slots - 1 - static_cast<int>(index / p.heads);
+  it.hk = set / p.sub;
+  it.h0 = it.hk * p.G + set % p.sub * p.Gp;
+  int tile;
+  if (a.cu_seqlens) {
+    int lo = 0, n = a.N;  // the last sequence whose places start at this one or before it
+    while (n > 1) {
+      const int step = (n + 31) / 32, at = lane * step;
+      const bool before = at < n && a.cu_seqlens[lo + at] / cta_tokens + lo + at <= slot;
+      const int which = __popc(__ballot_sync(0xffffffffu, before)) - 1;
+      lo += which * step;
+      n = min(step, n - which * step);
+    }
+    it.n = lo;
+    it.q0 = a.cu_seqlens[lo];
+    it.T = a.cu_seqlens[lo + 1] - it.q0;
+    tile = slot - (it.q0 / cta_tokens + lo);
+    const int32_t* ck = a.cu_seqlens_k ? a.cu_seqlens_k : a.cu_seqlens;
+    it.k0 = ck[lo];
+    it.S = ck[lo + 1] - it.k0;
+  } else {
+    it.n = slot % a.N;
+    tile = slot / a.N;
+    it.T = a.T;
+    it.S = a.S;
+    it.q0 = it.n * it.T;
+    it.k0 = it.n * it.S;
+  }
+  if (PAGED) it.S = a.seq_lens_k ? a.seq_lens_k[it.n] : p.parts.keys;
+  if (static_cast<long long>(tile) * cta_tokens >= it.T) return false;
+  it.t0 = tile * cta_tokens;
+  it.shift = it.S - it.T;
+  const int blocks = (it.S + kRows - 1) / kRows, per = (blocks + p.parts.splits - 1) / p.parts.splits;
+  it.first = min(blocks, it.split * per);
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const int t = it.t0 + m * p.tile_tokens, last = min(t + p.tile_tokens, it.T) - 1;
+    const int seen = t >= it.T ? 0 : a.flags & KDA_ATTN_FLAG_CAUSAL ? min(it.S, last + it.shift + 1) : it.S;
+    it.count[m] = max(0, min((max(seen, 0) + kRows - 1) / kRows, it.first + per) - it.first);
+  }
+  return true;
+}
+
+// Asks for the place of a CTA of this grid that has not started yet; the answer comes to
+// sm.next and counts 16 bytes on sm.next_there.
+__device__ __forceinline__ void ask_for_place(Head& sm) {
+  mbar_arrive_expect_tx_local(&sm.next_there, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(sm.next)),
+               "r"(smem_u32(&sm.next_there))
+               : "memory");
+}
+// Whether the answer gives a place, and which.
+__device__ __forceinline__ bool place_given(const Head& sm, uint32_t& place) {
+  uint32_t given;
+  asm volatile(
+      "{\n .reg .b128 answer;\n .reg .pred p;\n .reg .b64 lo, hi;\n"
+      " ld.shared.v2.b64 {lo, hi}, [%2];\n mov.b128 answer, {lo, hi};\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, answer;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, answer;\n}\n"
+      : "=r"(given), "=r"(place)
+      : "r"(smem_u32(sm.next))
+      : "memory");
+  return given != 0;
 }
 
 template <int D, bool PAGED>
@@ -195,73 +292,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
   unsigned char* ring = tiles + 2 * Sh::kTile;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int tile_tokens = kRows >> p.lg, cta_tokens = 2 * tile_tokens;
   const bool causal = a.flags & KDA_ATTN_FLAG_CAUSAL;
 
-  // The item: places in falling order, so that a causal prompt's long tiles start first.
-  Item it;
-  long long index = blockIdx.x;
-  it.split = static_cast<int>(index % p.parts.splits);
-  index /= p.parts.splits;
-  const int set = static_cast<int>(index % p.heads);
-  const int slot = p.slots - 1 - static_cast<int>(index / p.heads);
-  it.hk = set / p.sub;
-  it.h0 = it.hk * p.G + set % p.sub * p.Gp;
-
-  // The arrays of lengths: checked whole by every CTA, so that a call with bad ones does
-  // nothing. Sequence n's tiles have the places from cu_seqlens[n] / cta_tokens + n on,
-  // of which there are enough for it before the next sequence's.
+  // The arrays of lengths: checked whole by every CTA, so that a call with bad ones does nothing.
   bool ok = true;
-  int before = 0;  // sequences whose places start at this one or before it
-  const int entries = a.cu_seqlens || a.seq_lens_k ? a.N + 1 : 0;
-  for (int i0 = 0; i0 < entries; i0 += kThreads) {
-    const int i = i0 + tid;
-    bool starts = false;
-    if (i <= a.N) {
-      if (a.cu_seqlens) {
-        const int c = a.cu_seqlens[i];
-        ok &= i == 0 ? c == 0 : c >= a.cu_seqlens[i - 1] && c <= a.T;
-        starts = i < a.N && c >= 0 && c / cta_tokens + i <= slot;
-      }
+  if (a.cu_seqlens || a.seq_lens_k) {
+    for (int i = tid; i <= a.N; i += kThreads) {
+      if (a.cu_seqlens) ok &= i == 0 ? a.cu_seqlens[0] == 0 : a.cu_seqlens[i] >= a.cu_seqlens[i - 1] && a.cu_seqlens[i] <= a.T;
       if (a.cu_seqlens_k) ok &= i == 0 ? a.cu_seqlens_k[0] == 0 : a.cu_seqlens_k[i] >= a.cu_seqlens_k[i - 1] && a.cu_seqlens_k[i] <= a.S;
       if (a.seq_lens_k && i < a.N) ok &= a.seq_lens_k[i] >= 0 && a.seq_lens_k[i] <= a.table_width * a.page_size;
     }
-    before += __syncthreads_count(starts);
+    if (!__syncthreads_and(ok)) {
+      if (blockIdx.x == 0 && tid == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
+      return;
+    }
   }
-  if (entries > 0 && !__syncthreads_and(ok)) {
-    if (blockIdx.x == 0 && tid == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
-    return;
-  }
-  int tile;
-  if (a.cu_seqlens) {
-    it.n = before - 1;
-    it.q0 = a.cu_seqlens[it.n];
-    it.T = a.cu_seqlens[it.n + 1] - static_cast<int>(it.q0);
-    tile = slot - (static_cast<int>(it.q0) / cta_tokens + it.n);
-    const int32_t* ck = a.cu_seqlens_k ? a.cu_seqlens_k : a.cu_seqlens;
-    it.k0 = ck[it.n];
-    it.S = ck[it.n + 1] - static_cast<int>(it.k0);
-  } else {
-    it.n = slot % a.N;
-    tile = slot / a.N;
-    it.T = a.T;
-    it.S = a.S;
-    it.q0 = static_cast<long long>(it.n) * it.T;
-    it.k0 = static_cast<long long>(it.n) * it.S;
-  }
-  if (PAGED) it.S = a.seq_lens_k ? a.seq_lens_k[it.n] : p.parts.keys;
-  if (static_cast<long long>(tile) * cta_tokens >= it.T) return;  // a place that no tile has
-  it.t0 = tile * cta_tokens;
-  it.shift = it.S - it.T;
-  const int blocks = (it.S + kRows - 1) / kRows, per = (blocks + p.parts.splits - 1) / p.parts.splits;
-  it.first = min(blocks, it.split * per);
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const int t = it.t0 + m * tile_tokens, last = min(t + tile_tokens, it.T) - 1;
-    const int seen = t >= it.T ? 0 : causal ? min(it.S, last + it.shift + 1) : it.S;
-    it.count[m] = max(0, min((max(seen, 0) + kRows - 1) / kRows, it.first + per) - it.first);
-  }
-  const int most = max(it.count[0], it.count[1]);
 
   if (warp == 0) {
     tc05::tmem_alloc(&sm.tmem_base, 512);
@@ -270,6 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 8 * 32) {
     for (int m = 0; m < 2; ++m) {
       mbar_init(&sm.q_full[m], 1);
+      mbar_init(&sm.q_empty[m], 1);
+      mbar_init(&sm.item_full[m], 1);
+      mbar_init(&sm.item_empty[m], 11);
       mbar_init(&sm.s_full[m], 1);
       mbar_init(&sm.p_full[m][0], 4);
       mbar_init(&sm.p_full[m][1], 4);
@@ -282,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.tail_there, 1);
     mbar_init(&sm.tail_zero, 1);
     mbar_init(&sm.drain, 1);
+    mbar_init(&sm.next_there, 1);
     sm.failed = 0;
     fence_mbarrier_init_cluster();
   }
@@ -301,95 +350,161 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 9) {
       // ---- loads: the tiles' queries, then keys and values block by block ----
-      if (lane == 0) {
-        for (int m = 0; m < 2; ++m) {
-          if (it.count[m] == 0) continue;
-          mbar_arrive_expect_tx_local(&sm.q_full[m], Sh::kTile);
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(tiles + m * Sh::kTile + c * kHalf, &qmap, 64 * c, it.h0, static_cast<int>(it.q0) + it.t0 + m * tile_tokens, &sm.q_full[m]);
-        }
-      }
       const int box_keys = PAGED ? a.page_size : kRows;
       const int boxes = kRows / box_keys * (D / 64), part = lane / (D / 64), half = lane % (D / 64);
+      const uint32_t q_bytes = static_cast<uint32_t>(p.Gp * p.tile_tokens) * D * 2;
       bool going = true;
-      int loaded = 0;
-      for (int j = it.first; j < it.first + most && going; ++j) {
-        int y = it.hk, z = static_cast<int>(it.k0) + j * kRows;
-        uint32_t bad = 0;
-        if (PAGED) {
-          // a page that is out of range, or behind the last key, reads as zeros
-          const int tok = j * kRows + part * box_keys;
-          int page = -1;
-          if (lane < boxes && tok < it.S) {
-            page = a.block_table[static_cast<long long>(it.n) * a.table_width + tok / box_keys];
-            if (page >= a.pages) page = -1;
-          }
-          bad = __ballot_sync(0xffffffffu, lane < boxes && tok < it.S && page < 0);
-          if (bad != 0) {
-            if (lane == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
-            // a bit for each box to one for each 16 keys
-            bad = __ballot_sync(0xffffffffu, lane < 8 && (bad >> (lane * 16 / box_keys * (D / 64)) & 1u));
-          }
-          y = 0;
-          z = page < 0 ? -1 : page * a.HKV + it.hk;
-        }
-        for (int kv = 0; kv < 2 && going; ++kv, ++loaded) {
-          const int s = loaded % Sh::kStages;
-          if (loaded >= Sh::kStages) going = __all_sync(0xffffffffu, wait(&sm.empty[s], (loaded / Sh::kStages - 1) & 1));
-          if (!going) break;
+      int loaded = 0, blocks_done = 0, tiles_done[2] = {0, 0};
+      for (int k = 0; going; ++k) {
+        going = __all_sync(0xffffffffu, wait(&sm.item_full[k & 1], (k >> 1) & 1));
+        if (!going) break;
+        const Item it = sm.items[k & 1];
+        if (it.n < 0) break;
+        const int most = max(it.count[0], it.count[1]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (it.count[m] == 0 || !going) continue;
+          if (tiles_done[m] > 0) going = __all_sync(0xffffffffu, wait(&sm.q_empty[m], (tiles_done[m] - 1) & 1));
+          if (!going) continue;
+          ++tiles_done[m];
           if (lane == 0) {
-            // (the loads are at most 4 blocks ahead of the weights, which read this)
-            if (PAGED && kv == 0) sm.bad[(j - it.first) & 7] = bad;
-            mbar_arrive_expect_tx_local(&sm.full[s], Sh::kTile);
+            mbar_arrive_expect_tx_local(&sm.q_full[m], q_bytes);
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(tiles + m * Sh::kTile + c * kHalf, &qmap, 64 * c, it.h0, it.q0 + it.t0 + m * p.tile_tokens, &sm.q_full[m]);
           }
-          __syncwarp();
-          if (lane < boxes)
-            tma_load_3d(ring + s * Sh::kTile + half * kHalf + part * box_keys * 128, kv == 0 ? &kmap : &vmap, 64 * half, y, z, &sm.full[s]);
         }
+        for (int j = it.first; j < it.first + most && going; ++j) {
+          int y = it.hk, z = it.k0 + j * kRows;
+          uint32_t bad = 0;
+          if (PAGED) {
+            // a page that is out of range, or behind the last key, reads as zeros
+            const int tok = j * kRows + part * box_keys;
+            int page = -1;
+            if (lane < boxes && tok < it.S) {
+              page = a.block_table[static_cast<long long>(it.n) * a.table_width + tok / box_keys];
+              if (page >= a.pages) page = -1;
+            }
+            bad = __ballot_sync(0xffffffffu, lane < boxes && tok < it.S && page < 0);
+            if (bad != 0) {
+              if (lane == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
+              // a bit for each box to one for each 16 keys
+              bad = __ballot_sync(0xffffffffu, lane < 8 && (bad >> (lane * 16 / box_keys * (D / 64)) & 1u));
+            }
+            y = 0;
+            z = page < 0 ? -1 : page * a.HKV + it.hk;
+          }
+          for (int kv = 0; kv < 2 && going; ++kv, ++loaded) {
+            const int s = loaded % Sh::kStages;
+            if (loaded >= Sh::kStages) going = __all_sync(0xffffffffu, wait(&sm.empty[s], (loaded / Sh::kStages - 1) & 1));
+            if (!going) break;
+            if (lane == 0) {
+              // (the loads are at most 4 blocks ahead of the weights, which read this)
+              if (PAGED && kv == 0) sm.bad[(blocks_done + j - it.first) & 7] = bad;
+              mbar_arrive_expect_tx_local(&sm.full[s], Sh::kTile);
+            }
+            __syncwarp();
+            if (lane < boxes)
+              tma_load_3d(ring + s * Sh::kTile + half * kHalf + part * box_keys * 128, kv == 0 ? &kmap : &vmap, 64 * half, y, z, &sm.full[s]);
+          }
+        }
+        blocks_done += most;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_local(&sm.item_empty[k & 1]);
       }
       // no copy is left in flight when the CTA ends
       for (int m = 0; m < 2; ++m)
-        if (it.count[m] > 0) going &= wait(&sm.q_full[m], 0);
+        if (tiles_done[m] > 0) going &= wait(&sm.q_full[m], (tiles_done[m] - 1) & 1);
       for (int i = max(0, loaded - Sh::kStages); i < loaded; ++i) going &= wait(&sm.full[i % Sh::kStages], (i / Sh::kStages) & 1);
       if (!going) sm.failed = 1;
     } else if (warp == 8) {
-      if (elect_one()) issue_products<D>(sm, it, tiles);
+      if (elect_one() && !issue_products<D>(sm, tiles)) sm.failed = 1;
     } else if (warp == 10) {
       // ---- what stands behind the last key may be anything: zeros in its place ----
-      const int block = (it.S - 1) / kRows - it.first, live = it.S - (it.first + block) * kRows;
-      if (most > 0 && block == most - 1 && live < kRows) {
-        const int s = (2 * block + 1) % Sh::kStages;
-        if (!__all_sync(0xffffffffu, wait(&sm.tail_there, 0))) sm.failed = 1;
-        unsigned char* v = ring + s * Sh::kTile;
-        for (int c = 0; c < D / 64; ++c)
-          for (int u = live * 8 + lane; u < kRows * 8; u += 32) *reinterpret_cast<uint4*>(v + c * kHalf + u * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
+      bool going = true;
+      int loaded = 0, tails = 0;
+      for (int k = 0; going; ++k) {
+        going = __all_sync(0xffffffffu, wait(&sm.item_full[k & 1], (k >> 1) & 1));
+        if (!going) break;
+        const Item it = sm.items[k & 1];
+        if (it.n < 0) break;
+        const int most = max(it.count[0], it.count[1]), live = it.S - (it.first + most - 1) * kRows;
+        if (most > 0 && live < kRows) {
+          const int s = (loaded + 2 * most - 1) % Sh::kStages;
+          going = __all_sync(0xffffffffu, wait(&sm.tail_there, tails++ & 1));
+          if (!going) break;
+          unsigned char* v = ring + s * Sh::kTile;
+          for (int c = 0; c < D / 64; ++c)
+            for (int u = live * 8 + lane; u < kRows * 8; u += 32) *reinterpret_cast<uint4*>(v + c * kHalf + u * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(&sm.tail_zero);
+        }
+        loaded += 2 * most;
         __syncwarp();
-        if (lane == 0) mbar_arrive_local(&sm.tail_zero);
+        if (lane == 0) mbar_arrive_local(&sm.item_empty[k & 1]);
+      }
+      if (!going) sm.failed = 1;
+    } else {
+      // ---- places: this CTA's own, then those of CTAs that have not started ----
+      bool going = true, more = true;
+      uint32_t place = blockIdx.x;
+      int k = 0, asked = 0;
+      while (going) {
+        // (the next answer travels while this place is worked out)
+        if (more && lane == 0) ask_for_place(sm);
+        asked += more;
+        Item it;
+        if (!more) it.n = -1;
+        if (!more || item_of<PAGED>(p, place, lane, it)) {
+          if (k >= 2) going = __all_sync(0xffffffffu, wait(&sm.item_empty[k & 1], ((k >> 1) - 1) & 1));
+          if (going && lane == 0) {
+            sm.items[k & 1] = it;
+            mbar_arrive_local(&sm.item_full[k & 1]);
+          }
+          ++k;
+        }
+        if (!more || !going) break;
+        going = __all_sync(0xffffffffu, wait(&sm.next_there, (asked - 1) & 1));
+        if (!going) break;
+        more = place_given(sm, place);
+        fence_proxy_async_smem();  // (the next answer is written after this one has been read)
+        __syncwarp();
+      }
+      if (!going) {
+        if (asked > 0) wait(&sm.next_there, (asked - 1) & 1);  // no answer is left under way
+        sm.failed = 1;
       }
     }
   } else {
     // ---- rows ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int m = warp >> 2, r = tid & (kRows - 1);
-    const int ti = it.t0 + m * tile_tokens + (r >> p.lg);
-    const bool valid = ti < it.T;
-    const int limit = !valid ? 0 : causal ? max(0, min(it.S, ti + it.shift + 1)) : it.S;  // keys this row sees
-    // blocks below this end need no mask (the tile's first row sees all of them)
-    const int open = causal ? min(it.S, it.t0 + m * tile_tokens + it.shift + 1) : it.S;
+    const int row_token = r * p.per_token >> 16, row_head = r - row_token * p.Gp;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const uint32_t s_at = lanes + m * kRows, o_at = lanes + Sh::kO + m * D;
     const float c2 = a.scale * kLog2e;
-    float top = -INFINITY, sum = 0.f;
     bool going = true;
-    for (int i = 0; i < it.count[m] && going; ++i) {
-      going = __all_sync(0xffffffffu, wait(&sm.s_full[m], i & 1));
+    int done = 0, tiles_done = 0, blocks_done = 0;
+    for (int k = 0; going; ++k) {
+    going = __all_sync(0xffffffffu, wait(&sm.item_full[k & 1], (k >> 1) & 1));
+    if (!going) break;
+    const Item& it = sm.items[k & 1];
+    if (it.n < 0) break;
+    const int first = it.first, count = it.count[m];
+    const int ti = it.t0 + m * p.tile_tokens + row_token;
+    const bool valid = row_token < p.tile_tokens && ti < it.T;
+    const int limit = !valid ? 0 : causal ? max(0, min(it.S, ti + it.shift + 1)) : it.S;  // keys this row sees
+    // blocks below this end need no mask (the tile's first row sees all of them)
+    const int open = causal ? min(it.S, it.t0 + m * p.tile_tokens + it.shift + 1) : it.S;
+    float top = -INFINITY, sum = 0.f;
+    for (int i = 0; i < count && going; ++i, ++done) {
+      going = __all_sync(0xffffffffu, wait(&sm.s_full[m], done & 1));
       if (!going) break;
       tc05::fence_after_sync();
       float s[128];
       tc05::ld128_wait(s_at, s);
-      const int k0 = (it.first + i) * kRows;
-      const uint32_t bad = PAGED ? sm.bad[i & 7] : 0;
+      const int k0 = (first + i) * kRows;
+      const uint32_t bad = PAGED ? sm.bad[(blocks_done + i) & 7] : 0;
       if (k0 + kRows > open || (PAGED && bad != 0)) {
 #pragma unroll
         for (int j = 0; j < 128; ++j) s[j] = k0 + j < limit ? s[j] : -INFINITY;
@@ -450,24 +565,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
     }
-    if (going && it.count[m] > 0) {
-      going = __all_sync(0xffffffffu, wait(&sm.o_full[m], 0));
+    if (going && count > 0) {
+      going = __all_sync(0xffffffffu, wait(&sm.o_full[m], tiles_done++ & 1));
       tc05::fence_after_sync();
     }
-    if (!going) {
-      if (lane == 0) sm.failed = 1;
-    } else {
-      const long long tok = it.q0 + ti, row = tok * a.HQ + it.h0 + (r & (p.Gp - 1));
+    if (going) {
+      const long long tok = it.q0 + ti, row = tok * a.HQ + it.h0 + row_head;
       const bool part = p.parts.o != nullptr;
       const long long part_row = static_cast<long long>(it.split) * a.B * a.T * a.HQ + row;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + tok * a.o_stride + static_cast<long long>(it.h0 + (r & (p.Gp - 1))) * D;
-      const bool some = it.count[m] > 0 && limit > it.first * kRows;  // this row has keys here
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + tok * a.o_stride + static_cast<long long>(it.h0 + row_head) * D;
+      const bool some = count > 0 && limit > first * kRows;  // this row has keys here
       const float inv = 1.f / sum;
       bool finite = true;
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
         float o[32];
-        if (it.count[m] > 0) tc05::ld32_wait(o_at + c, o);
+        if (count > 0) tc05::ld32_wait(o_at + c, o);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           o[j] = some ? o[j] * inv : 0.f;
@@ -493,15 +606,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int src = __ffs(again) - 1;
         again &= again - 1;
         const long long stok = __shfl_sync(0xffffffffu, tok, src);
-        const int shead = __shfl_sync(0xffffffffu, it.h0 + (r & (p.Gp - 1)), src);
-        const int end = min(__shfl_sync(0xffffffffu, limit, src), (it.first + it.count[m]) * kRows);
+        const int shead = __shfl_sync(0xffffffffu, it.h0 + row_head, src);
+        const int end = min(__shfl_sync(0xffffffffu, limit, src), (first + count) * kRows);
         const Keys keys = {a.k, a.v, PAGED ? a.block_table + static_cast<long long>(it.n) * a.table_width : nullptr,
                            a.pages, a.page_size, a.HKV, a.k_stride, a.v_stride, it.k0};
         float q[D / 32], o[D / 32], rm, rl;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
           q[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[stok * a.q_stride + static_cast<long long>(shead) * D + lane + 32 * c]);
-        const int used = attend_row<D>(q, keys, it.hk, it.first * kRows, end, c2, lane, a.err, rm, rl, o);
+        const int used = attend_row<D>(q, keys, it.hk, first * kRows, end, c2, lane, a.err, rm, rl, o);
         const long long srow = stok * a.HQ + shead;
         const long long spart = static_cast<long long>(it.split) * a.B * a.T * a.HQ + srow;
         const float l2 = used == 0 ? -INFINITY : rl == 0.f ? __uint_as_float(0x7fc00000u) : rm + log2f(rl);
@@ -515,6 +628,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0 && !part && a.lse) a.lse[srow] = l2 * kLn2;
       }
     }
+    blocks_done += max(it.count[0], it.count[1]);
+    // (O has been read: the next item's weights, and with them its products into O, come after this)
+    tc05::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_local(&sm.item_empty[k & 1]);
+    }
+    if (!going) sm.failed = 1;
   }
   __syncwarp();
   tc05::fence_before_sync();
@@ -524,11 +644,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tc05::tmem_dealloc(tmem, 512);
 }
 
-// The largest power of two that divides the group, as its exponent, up to 128 heads.
-int group_bits(int group) {
-  int lg = 0;
-  while (lg < 7 && group % (2 << lg) == 0) ++lg;
-  return lg;
+// Query heads of a tile's tokens: the largest divisor of the group that leaves no more
+// than 8 of the 128 rows without a token (14 heads on 2: 18 tokens of 7 heads).
+int heads_of_tile(int group) {
+  for (int h = group < kRows ? group : kRows; h > 1; --h)
+    if (group % h == 0 && kRows / h * h >= kRows - 8) return h;
+  return 1;
 }
 
 template <int D, bool PAGED>
@@ -536,7 +657,7 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   const kda_attn_fwd_args& a = p.a;
   CUtensorMap qmap, kmap, vmap;
   const long long queries = static_cast<long long>(a.B) * a.T;
-  bool ok = encode_heads(&qmap, a.q, D, a.HQ, D, queries, a.q_stride, static_cast<unsigned>(p.Gp), static_cast<unsigned>(kRows >> p.lg));
+  bool ok = encode_heads(&qmap, a.q, D, a.HQ, D, queries, a.q_stride, static_cast<unsigned>(p.Gp), static_cast<unsigned>(p.tile_tokens));
   if (PAGED) {
     // a cache without pages is never read (every page is out of range): any map will do
     const long long rows = static_cast<long long>(a.pages) * a.HKV, page = static_cast<long long>(a.page_size) * D;
@@ -561,15 +682,21 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
 
 }  // namespace
 
-int attn_tile_tokens(int group) { return 2 * kRows >> group_bits(group); }
+AttnTiles attn_tiles(int group) {
+  const int h = heads_of_tile(group);
+  return {2 * (kRows / h), h};
+}
 
 cudaError_t launch_attn_prompts(const kda_attn_fwd_args& a, const AttnParts& parts, cudaStream_t s) {
-  Params p = {a, parts, a.HQ / a.HKV, 0, 0, 0, 0, 0};
-  p.lg = group_bits(p.G);
-  p.Gp = 1 << p.lg;
+  Params p = {};
+  p.a = a, p.parts = parts;
+  p.G = a.HQ / a.HKV;
+  p.Gp = heads_of_tile(p.G);
   p.sub = p.G / p.Gp;
   p.heads = a.HKV * p.sub;
-  const int tokens = 2 * kRows >> p.lg;
+  p.tile_tokens = kRows / p.Gp;
+  p.per_token = (65536 + p.Gp - 1) / p.Gp;
+  const int tokens = 2 * p.tile_tokens;
   const long long slots = a.cu_seqlens ? static_cast<long long>(a.T) / tokens + a.N : (static_cast<long long>(a.T) + tokens - 1) / tokens * a.N;
   if (slots > INT32_MAX) return cudaErrorNotSupported;
   p.slots = static_cast<int>(slots);

@@ -13,8 +13,11 @@ struct AttnParts {
   int keys;        // paged keys of the one sequence, where no seq_lens_k gives them
 };
 
-// Query tokens that a CTA takes at once, for so many query heads a key head.
-int attn_tile_tokens(int group);
+// Query tokens that a CTA takes at once, and of how many query heads of a key head's group.
+struct AttnTiles {
+  int tokens, heads;
+};
+AttnTiles attn_tiles(int group);
 cudaError_t launch_attn_prompts(const kda_attn_fwd_args& a, const AttnParts& parts, cudaStream_t s);
 
 }  // namespace kda

@@ -634,8 +634,8 @@ Plan plan_of(const kda_attn_step_args& a) {
   if (a.prefix_len > 0) {
     // Splits that keep the SMs busy: rounds of CTAs, each with its share of the blocks and
     // 4 blocks' time for what a CTA does besides.
-    const int tokens = attn_tile_tokens(G), packed = 256 / tokens;
-    const long long tiles = (static_cast<long long>(a.B) + tokens - 1) / tokens * a.HKV * (G / packed);
+    const AttnTiles t = attn_tiles(G);
+    const long long tiles = (static_cast<long long>(a.B) + t.tokens - 1) / t.tokens * a.HKV * (G / t.heads);
     const int blocks = (a.prefix_len - 1) / 128 + 1;
     long long best = 0;
     for (int s = 1; s <= 32 && s <= blocks; ++s) {
