@@ -69,7 +69,7 @@ struct Item {
 struct Head {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], tail_there, tail_zero, drain;  // p_full: a block's first kFirst keys, and the rest
   uint64_t full[8], empty[8];
-  uint64_t item_full[2], item_empty[2], next_there;
+  uint64_t item_full[2], item_empty[2], item_near, next_there;  // item_near: the loads of an item are almost all under way
   alignas(16) uint32_t next[4];  // the answer to the request for another CTA's place
   Item items[2];
   uint32_t bad[8];            // by block, of the last 8: keys on pages that are out of range, a bit for each 16
@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.tail_there, 1);
     mbar_init(&sm.tail_zero, 1);
     mbar_init(&sm.drain, 1);
+    mbar_init(&sm.item_near, 1);
     mbar_init(&sm.next_there, 1);
     sm.failed = 0;
     fence_mbarrier_init_cluster();
@@ -373,7 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(tiles + m * Sh::kTile + c * kHalf, &qmap, 64 * c, it.h0, it.q0 + it.t0 + m * p.tile_tokens, &sm.q_full[m]);
           }
         }
+        if (lane == 0 && most <= 1) mbar_arrive_local(&sm.item_near);
         for (int j = it.first; j < it.first + most && going; ++j) {
+          if (lane == 0 && most > 1 && j == it.first + most - 2) mbar_arrive_local(&sm.item_near);
           int y = it.hk, z = it.k0 + j * kRows;
           uint32_t bad = 0;
           if (PAGED) {
@@ -445,14 +448,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!going) sm.failed = 1;
     } else {
-      // ---- places: this CTA's own, then those of CTAs that have not started ----
+      // ---- places: this CTA's own, then those of CTAs that have not started. One is asked
+      // for when the loads are two blocks from the end of the item before: earlier, the
+      // first CTAs of a grid of few would take the others' places from idle SMs. ----
       bool going = true, more = true;
       uint32_t place = blockIdx.x;
       int k = 0, asked = 0;
       while (going) {
-        // (the next answer travels while this place is worked out)
-        if (more && lane == 0) ask_for_place(sm);
-        asked += more;
         Item it;
         if (!more) it.n = -1;
         if (!more || item_of<PAGED>(p, place, lane, it)) {
@@ -461,9 +463,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             sm.items[k & 1] = it;
             mbar_arrive_local(&sm.item_full[k & 1]);
           }
+          if (more && going) going = __all_sync(0xffffffffu, wait(&sm.item_near, k & 1));
           ++k;
         }
         if (!more || !going) break;
+        if (lane == 0) ask_for_place(sm);
+        ++asked;
         going = __all_sync(0xffffffffu, wait(&sm.next_there, (asked - 1) & 1));
         if (!going) break;
         more = place_given(sm, place);
