@@ -83,6 +83,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// 32 bytes at once, on a 32-byte boundary.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // One lane of the warp, which all enter.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
@@ -581,27 +588,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + tok * a.o_stride + static_cast<long long>(it.h0 + row_head) * D;
       const bool some = count > 0 && limit > first * kRows;  // this row has keys here
       const float inv = 1.f / sum;
-      bool finite = true;
+      float2 total = make_float2(0.f, 0.f);  // not finite where a value is not (or where the values are next to that)
+      const bool wide = part || ((reinterpret_cast<uintptr_t>(a.o) | static_cast<uintptr_t>(a.o_stride * 2)) & 31) == 0;
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
         float o[32];
         if (count > 0) tc05::ld32_wait(o_at + c, o);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < 32; j += 2) {
           o[j] = some ? o[j] * inv : 0.f;
-          finite &= fabsf(o[j]) < INFINITY;
+          o[j + 1] = some ? o[j + 1] * inv : 0.f;
+          total = add2(total, make_float2(o[j], o[j + 1]));
         }
         if (!valid) continue;
+        // (32 bytes a store: a lane's rows are apart, and each store of a warp is 32 pieces
+        // whatever their width; in 16 bytes the two tiles' took 5000 cycles)
         if (part) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(p.parts.o + part_row * D + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          for (int j = 0; j < 32; j += 8) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[j + e]);
+            store32(p.parts.o + part_row * D + c + j, w);
+          }
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            *reinterpret_cast<uint4*>(out + c + j) = make_uint4(Bf16::pack(o[j], o[j + 1]), Bf16::pack(o[j + 2], o[j + 3]),
-                                                                Bf16::pack(o[j + 4], o[j + 5]), Bf16::pack(o[j + 6], o[j + 7]));
+          for (int j = 0; j < 32; j += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = Bf16::pack(o[j + 2 * e], o[j + 2 * e + 1]);
+            if (wide) {
+              store32(out + c + j, w);
+            } else {
+              *reinterpret_cast<uint4*>(out + c + j) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(out + c + j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
         }
       }
+      const bool finite = fabsf(total.x + total.y) < INFINITY;
       const float lse2 = some ? top * c2 + log2f(sum) : -INFINITY;
       if (valid && part) p.parts.lse[part_row] = lse2;
       if (valid && !part && a.lse) a.lse[row] = lse2 * kLn2;
