@@ -37,7 +37,6 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;            // rows of a tile; keys of a block
 constexpr int kFirst = 64;            // keys of a block whose products start before the others' weights are there
 constexpr int kHalf = kRows * 128;    // bytes of a block's 64 channels
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 8.f;          // how far, in powers of two, a row's maximum may pass the one in use
 
 template <int D>
@@ -97,25 +96,23 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-// Waits for a phase, for a limited time. (Without the hint of mbar_try_wait, which lets the
-// thread sleep: 8192 tokens, 32 heads of 128 took 407 us with it and 395 without.)
-__device__ __forceinline__ bool try_now(uint32_t bar, uint32_t parity) {
+// Waits for a phase, for at most two seconds; whether it came. (One statement, and callers
+// that look at the results seldom: with the loop and its exits in the compiler's hands each
+// wait of the thread that issues products left the tensor core idle for 140 cycles instead
+// of 40. No hint that lets the thread sleep: 395 us instead of 407 for 8192 tokens and 32
+// heads of 128.)
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p, q;\n .reg .b64 t0, t1;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n mov.u64 t0, %globaltimer;\n"
+      "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n mov.u64 t1, %globaltimer;\n"
+      " sub.u64 t1, t1, t0;\n setp.lt.u64 q, t1, 2000000000;\n @q bra AGAIN;\n mov.u32 %0, 0;\n bra END;\n"
+      "DONE:\n mov.u32 %0, 1;\nEND:\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-  const uint32_t b = smem_u32(bar);
-  if (try_now(b, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!try_now(b, parity)) {
-    if (global_timer_ns() - t0 > kWaitNs) return false;
-  }
-  return true;
 }
 
 // The products of both tiles, issued by one thread. (It is elected: operands are then as
@@ -169,7 +166,31 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
       tc05::commit(&sm.empty[s]);
       advance();
     }
-    for (int i = 0; i < blocks && going; ++i) {
+    int i = 0;
+    // blocks that both tiles use and that others follow: no conditions between the products
+    for (const int both = min(count0, count1) - 1; i < both && going; ++i) {
+      const int vs = s;
+      bool there = wait(&sm.full[vs], phase);
+      advance();
+      there &= wait(&sm.full[s], phase);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int parity = done[m]++ & 1;
+        there &= wait(&sm.p_full[m][0], parity);
+        tc05::fence_after_sync();
+        values(m, vs, 0, kFirst / 16, i > 0);
+        there &= wait(&sm.p_full[m][1], parity);
+        tc05::fence_after_sync();
+        values(m, vs, kFirst / 16, kRows / 16, true);
+        scores(m, s);
+        if (i + 2 == (m == 0 ? count0 : count1)) tc05::commit(&sm.q_empty[m]);
+      }
+      tc05::commit(&sm.empty[s]);
+      tc05::commit(&sm.empty[vs]);
+      advance();
+      going = there;
+    }
+    for (; i < blocks && going; ++i) {
       const int vs = s, v_phase = phase;  // the block's values; the next block's keys come after them
       advance();
       going = wait(&sm.full[vs], v_phase);
@@ -510,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int open = causal ? min(it.S, it.t0 + m * p.tile_tokens + it.shift + 1) : it.S;
     float top = -INFINITY, sum = 0.f;
     for (int i = 0; i < count && going; ++i, ++done) {
-      going = __all_sync(0xffffffffu, wait(&sm.s_full[m], done & 1));
-      if (!going) break;
+      const bool there = wait(&sm.s_full[m], done & 1);  // (looked at below, when nothing waits for it)
+      __syncwarp();
       tc05::fence_after_sync();
       float s[128];
       tc05::ld128_wait(s_at, s);
@@ -575,6 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_local(&sm.p_full[m][h + 32 == kRows]);
         }
       }
+      going = __all_sync(0xffffffffu, there);
       sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
     }
     if (going && count > 0) {
