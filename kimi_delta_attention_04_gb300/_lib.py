@@ -899,12 +899,19 @@ def _head_rows(t, name, dev, dtype, shape):
         return None, 0
     if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
         _refuse(t, name, dev, dtype, shape)
+    st, H, D = t.stride(), shape[-2], shape[-1]
+    n = len(st)
+    # [tokens, heads, D] and [1, tokens, heads, D], whole or as a view of a wider row
+    if st[-1] == 1 and st[-2] == D and (n == 3 or (n == 4 and shape[0] == 1)):
+        return t.data_ptr(), st[-3] if shape[-3] > 1 else H * D
     if t.is_contiguous():
-        return t.data_ptr(), shape[-2] * shape[-1]
-    if t.numel() and ((shape[-1] > 1 and t.stride(-1) != 1) or (shape[-2] > 1 and t.stride(-2) != shape[-1])):
+        return t.data_ptr(), H * D
+    if t.numel() == 0:
+        return t.data_ptr(), H * D
+    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
         raise ValueError(f"{name}: the last two axes must be contiguous")
-    ptr, step = _spaced_rows(t.select(-2, 0) if shape[-2] else t.flatten(-2), name)
-    return ptr, max(step, shape[-2] * shape[-1]) if t.numel() // max(1, shape[-2] * shape[-1]) <= 1 else step
+    ptr, step = _spaced_rows(t.select(-2, 0), name)
+    return ptr, step if t.numel() > H * D else H * D
 
 
 def _head_output(t, name, x, stream, shape):
