@@ -31,44 +31,63 @@ __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& 
                                            float& m, float& l, float (&o)[D / 32]) {
   m = -INFINITY, l = 0.f;
   int used = 0;
+  bool nan = false;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-  for (int j = begin; j < end; ++j) {
-    long long ka, va;
-    if (s.table != nullptr) {
-      const int page = s.table[j / s.page_size];
-      if (page < 0 || page >= s.pages) {
-        if (lane == 0) set_err(err, KDA_ERR_INVALID_ARG);
-        continue;
+  for (int i = 0; i < D / 32; ++i) o[i] = 0.f, nan |= q[i] != q[i];
+  const bool nan_row = __any_sync(0xffffffffu, nan);  // (padding that nothing has written, say)
+  constexpr int N = 4;  // keys whose loads and sums are under way together
+  for (int j0 = begin; j0 < end; j0 += N) {
+    float x[N], v[N][D / 32];
+    bool there[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int j = j0 + u;
+      there[u] = j < end;
+      x[u] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) v[u][i] = 0.f;
+      if (!there[u]) continue;
+      long long ka, va;
+      if (s.table != nullptr) {
+        const int page = s.table[j / s.page_size];
+        there[u] = page >= 0 && page < s.pages;
+        if (!there[u]) {
+          if (lane == 0) set_err(err, KDA_ERR_INVALID_ARG);
+          continue;
+        }
+        ka = va = ((static_cast<long long>(page) * s.HKV + h) * s.page_size + j % s.page_size) * D;
+      } else {
+        ka = (s.first + j) * s.k_stride + static_cast<long long>(h) * D;
+        va = (s.first + j) * s.v_stride + static_cast<long long>(h) * D;
       }
-      const long long at = (static_cast<long long>(page) * s.HKV + h) * s.page_size + j % s.page_size;
-      ka = va = at * D;
-    } else {
-      ka = (s.first + j) * s.k_stride + static_cast<long long>(h) * D;
-      va = (s.first + j) * s.v_stride + static_cast<long long>(h) * D;
-    }
-    ++used;
-    float x = 0.f, v[D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int d = lane + 32 * i;
-      x += q[i] * __bfloat162float(static_cast<const __nv_bfloat16*>(s.k)[ka + d]);
-      v[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(s.v)[va + d]);
+      for (int i = 0; i < D / 32; ++i) {
+        const int d = lane + 32 * i;
+        x[u] += q[i] * __bfloat162float(static_cast<const __nv_bfloat16*>(s.k)[ka + d]);
+        v[u][i] = __bfloat162float(static_cast<const __nv_bfloat16*>(s.v)[va + d]);
+      }
     }
-    x = warp_sum(x) * scale2;
-    const float top = x > m ? x : m;  // (a NaN leaves m and makes p and l NaN)
-    const float keep = m == top ? 1.f : m == -INFINITY ? 0.f : fmaxf(exp2f(m - top), 1.1754944e-38f);
-    float p = exp2f(x - (top == -INFINITY ? 0.f : top));
-    if (x != -INFINITY) p = p < 1.1754944e-38f ? 1.1754944e-38f : p;
-    m = top;
-    l = l * keep + p;
-    if (l != l) {  // every output is NaN from here on
+#pragma unroll
+    for (int u = 0; u < N; ++u) x[u] = warp_sum(x[u]) * scale2;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      if (!there[u]) continue;
+      ++used;
+      const float top = x[u] > m ? x[u] : m;  // (a NaN leaves m and makes p and l NaN)
+      const float keep = m == top ? 1.f : m == -INFINITY ? 0.f : fmaxf(exp2f(m - top), 1.1754944e-38f);
+      float p = exp2f(x[u] - (top == -INFINITY ? 0.f : top));
+      if (x[u] != -INFINITY) p = p < 1.1754944e-38f ? 1.1754944e-38f : p;
+      m = top;
+      l = l * keep + p;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) o[i] = o[i] * keep + p * v[u][i];
+    }
+    if (l != l || (nan_row && used > 0)) {  // every output is NaN from here on
+      l = __uint_as_float(0x7fc00000u);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) o[i] = l;
       return used;
     }
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = o[i] * keep + p * v[i];
   }
   return used;
 }

@@ -47,6 +47,11 @@ kda_status check_cache(int32_t pages, int32_t page_size, int32_t HKV, int32_t dt
   return aligned(ks, 16) && aligned(vs, 16) ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
 
+// An output in place of an input: the same rows, or none of them.
+bool place_ok(const void* out, int64_t out_stride, const void* in, int64_t in_stride, int64_t rows) {
+  return out != in || out_stride == in_stride || rows <= 1;
+}
+
 bool scale_ok(float scale) { return scale > 0.f && std::isfinite(scale); }
 
 kda_status check_step(const kda_attn_step_args* a) {
@@ -59,7 +64,7 @@ kda_status check_step(const kda_attn_step_args* a) {
   if (!aligned(a->err, 4) || !aligned(a->lse, 4)) return KDA_ERR_INVALID_ARG;
   if (a->B == 0) return KDA_OK;
   const int64_t cols = static_cast<int64_t>(a->HQ) * a->D;
-  if (!rows_ok(a->q, a->B, cols, a->q_stride) || !rows_ok(a->o, a->B, cols, a->o_stride)) return KDA_ERR_INVALID_ARG;
+  if (!rows_ok(a->q, a->B, cols, a->q_stride) || !rows_ok(a->o, a->B, cols, a->o_stride) || a->o == a->q) return KDA_ERR_INVALID_ARG;
   if (a->seq_lens == nullptr || !aligned(a->seq_lens, 4) || !aligned(a->block_table, 4)) return KDA_ERR_INVALID_ARG;
   if (a->table_width > 0 && a->block_table == nullptr) return KDA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(a->table_width) * a->page_size > INT32_MAX) return KDA_ERR_INVALID_ARG;
@@ -94,6 +99,8 @@ kda_status kda_kv_append(const kda_kv_append_args* a, kda_stream_t stream) {
   if (a->k_out && !rows_ok(a->k_out, a->tokens, kv, a->k_out_stride)) return KDA_ERR_INVALID_ARG;
   if (with_q && (!rows_ok(a->q, a->tokens, qn, a->q_stride) || !rows_ok(a->q_out, a->tokens, qn, a->q_out_stride)))
     return KDA_ERR_INVALID_ARG;
+  if (!place_ok(a->q_out, a->q_out_stride, a->q, a->q_stride, a->tokens) || !place_ok(a->k_out, a->k_out_stride, a->k, a->k_stride, a->tokens))
+    return KDA_ERR_INVALID_ARG;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (a->flags & KDA_FLAG_CHECK_INDICES) e = kda::launch_check_indices(a->slots, a->tokens, a->pages * a->page_size, a->err, s);
@@ -123,7 +130,7 @@ kda_status kda_attn_fwd(const kda_attn_fwd_args* a, kda_stream_t stream) {
     if (a->table_width < 0 || static_cast<int64_t>(a->table_width) * a->page_size > INT32_MAX) return KDA_ERR_INVALID_ARG;
   }
   if (queries == 0) return KDA_OK;
-  if (!rows_ok(a->q, queries, qn, a->q_stride) || !rows_ok(a->o, queries, qn, a->o_stride)) return KDA_ERR_INVALID_ARG;
+  if (!rows_ok(a->q, queries, qn, a->q_stride) || !rows_ok(a->o, queries, qn, a->o_stride) || a->o == a->q) return KDA_ERR_INVALID_ARG;
   if (!paged && keys > 0 && (!rows_ok(a->k, keys, kv, a->k_stride) || !rows_ok(a->v, keys, kv, a->v_stride))) return KDA_ERR_INVALID_ARG;
   return done(kda::launch_attn_fwd(*a, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -96,7 +96,8 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-// Waits for a phase, for at most two seconds; whether it came. (One statement, and callers
+// Waits for a phase, for at most ten seconds (rows computed again one by one
+// take most of a second at 10^6 keys); whether it came. (One statement, and callers
 // that look at the results seldom: with the loop and its exits in the compiler's hands each
 // wait of the thread that issues products left the tensor core idle for 140 cycles instead
 // of 40. No hint that lets the thread sleep: 395 us instead of 407 for 8192 tokens and 32
@@ -107,7 +108,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
       "{\n .reg .pred p, q;\n .reg .b64 t0, t1;\n"
       " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n mov.u64 t0, %globaltimer;\n"
       "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n mov.u64 t1, %globaltimer;\n"
-      " sub.u64 t1, t1, t0;\n setp.lt.u64 q, t1, 2000000000;\n @q bra AGAIN;\n mov.u32 %0, 0;\n bra END;\n"
+      " sub.u64 t1, t1, t0;\n setp.lt.u64 q, t1, 10000000000;\n @q bra AGAIN;\n mov.u32 %0, 0;\n bra END;\n"
       "DONE:\n mov.u32 %0, 1;\nEND:\n}\n"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)

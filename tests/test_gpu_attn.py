@@ -308,6 +308,22 @@ def test_prompts_hidden_values_have_no_effect(what, where, at):
                     check(got[0, i:i + 1, h:h + 1], None, r, T, D)
 
 
+def test_prompts_with_unwritten_padding():
+    """A right-padded equal batch whose padding holds NaN: the rows before it are as without it."""
+    gen = torch.Generator().manual_seed(16)
+    B, T, HQ, HKV, D, real = 3, 400, 4, 2, 128, (400, 250, 1)
+    q, k, v = randn(gen, B, T, HQ, D), randn(gen, B, T, HKV, D), randn(gen, B, T, HKV, D)
+    for b, n in enumerate(real):
+        for x in (q, k, v):
+            x[b, n:] = NAN
+    lse = torch.empty(B, T, HQ, device="cuda")
+    o = kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), scale=0.09, lse=lse)
+    for b, n in enumerate(real):
+        refs = ao.attend(np64(q[b, :n]), np64(k[b, :n]), np64(v[b, :n]), float(np.float32(0.09)), ao.seen_keys(n, n, True))
+        check(o[b, :n], lse[b, :n], refs, n, D)
+        assert torch.isnan(o[b, n:].float()).all() and torch.isnan(lse[b, n:]).all()
+
+
 def test_prompts_refuse_bad_lengths():
     T, HQ, HKV, D = 20, 2, 1, 64
     gen = torch.Generator().manual_seed(14)
