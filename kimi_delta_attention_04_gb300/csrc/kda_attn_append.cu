@@ -41,12 +41,13 @@ __device__ __forceinline__ float power_scale(float m) {
 enum { kPlain = 0, kHalves = 1, kNeighbours = 2, kAny = 3 };
 
 template <int D, int MODE, bool E4>
-__global__ void __launch_bounds__(kThreads, MODE == kAny ? 2 : 4) kda_kv_append_kernel(const __grid_constant__ kda_kv_append_args p, int groups, int heads) {
+__global__ void __launch_bounds__(kThreads, MODE == kAny ? 2 : 4) kda_kv_append_kernel(const __grid_constant__ kda_kv_append_args p, int group_bits, int page_bits, int heads) {
   constexpr int L = D / 8;  // lanes of a head
   const int lane = threadIdx.x % L, c = 8 * lane;
   const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-  const long long token = unit / groups;
-  const int group = static_cast<int>(unit % groups);
+  const int groups = 1 << group_bits;
+  const long long token = unit >> group_bits;
+  const int group = static_cast<int>(unit) & (groups - 1);
   const bool live = token < p.tokens;
   const long long t = live ? token : 0;
   const int HQ = p.q ? p.HQ : 0;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kAny ? 2 : 4) kda_kv_append_
         if (lane == 0 && group == 0) set_err(p.err, KDA_ERR_INVALID_ARG);
         slot = -1;
       }
-      if (slot >= 0) page = slot / p.page_size, off = slot % p.page_size;
+      if (slot >= 0) page = slot >> page_bits, off = slot & (p.page_size - 1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
       if (MODE != kPlain && live && turn && c < rot) {
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kAny ? 2 : 4) kda_kv_append_
         for (int o = L / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (valid && h >= HQ && slot >= 0) {
           const float s = power_scale(m), inv = s == s ? __uint_as_float((254u << 23) - __float_as_uint(s)) : s;
-          const long long at = (static_cast<long long>(page) * p.HKV + (is_v ? h - HQ - p.HKV : h - HQ)) * p.page_size + off;
+          const long long at = ((static_cast<long long>(page) * p.HKV + (is_v ? h - HQ - p.HKV : h - HQ)) << page_bits) + off;
           uint2 b;
           b.x = pack_e4m3x2(x[0] * inv, x[1] * inv) | pack_e4m3x2(x[2] * inv, x[3] * inv) << 16;
           b.y = pack_e4m3x2(x[4] * inv, x[5] * inv) | pack_e4m3x2(x[6] * inv, x[7] * inv) << 16;
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kAny ? 2 : 4) kda_kv_append_
           if (lane == 0) (is_v ? p.v_scale : p.k_scale)[at] = s;
         }
       } else if (valid && h >= HQ && slot >= 0) {
-        const long long at = (static_cast<long long>(page) * p.HKV + (is_v ? h - HQ - p.HKV : h - HQ)) * p.page_size + off;
+        const long long at = ((static_cast<long long>(page) * p.HKV + (is_v ? h - HQ - p.HKV : h - HQ)) << page_bits) + off;
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.v_cache : p.k_cache) + at * D + c) = pack8(x);
       }
     }
@@ -193,13 +194,14 @@ cudaError_t launch(const kda_kv_append_args& a, cudaStream_t s) {
   const int heads = (a.q ? a.HQ : 0) + 2 * a.HKV;
   // Groups of a token: each has up to kHeadsAtOnce heads, unless that is more groups
   // than a CTA holds.
-  int groups = 1;
-  while (groups < kThreads / (D / 8) && groups * kHeadsAtOnce < heads) groups *= 2;
-  const long long units = static_cast<long long>(a.tokens) * groups, per = kThreads / (D / 8);
+  int bits = 0;
+  while ((1 << bits) < kThreads / (D / 8) && (kHeadsAtOnce << bits) < heads) ++bits;
+  const int page_bits = __builtin_ctz(a.page_size);
+  const long long units = static_cast<long long>(a.tokens) << bits, per = kThreads / (D / 8);
   const long long grid = (units + per - 1) / per;
   if (grid > INT32_MAX) return cudaErrorNotSupported;
-  if (a.cache_dtype == KDA_DTYPE_E4M3) kda_kv_append_kernel<D, MODE, true><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, groups, heads);
-  else kda_kv_append_kernel<D, MODE, false><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, groups, heads);
+  if (a.cache_dtype == KDA_DTYPE_E4M3) kda_kv_append_kernel<D, MODE, true><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, bits, page_bits, heads);
+  else kda_kv_append_kernel<D, MODE, false><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, bits, page_bits, heads);
   return cudaGetLastError();
 }
 
