@@ -1,5 +1,6 @@
 """GB300-native Kimi Delta Attention: chunkwise forward, fused T=1 decode and the
-short-T recurrent step on a state pool.
+short-T recurrent step on a state pool, with the layer around it (norm, projection,
+gated recurrence) and softmax attention on a paged cache.
 
 The computation lives in libkda.so (hand-written sm_103a CUDA behind the C ABI
 of include/kda.h); this package is its thin Python binding. Importing the
