@@ -37,13 +37,16 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;            // rows of a tile; keys of a block
 constexpr int kFirst = 64;            // keys of a block whose products start before the others' weights are there
 constexpr int kHalf = kRows * 128;    // bytes of a block's 64 channels
+constexpr int kPairTokens = 2, kPairItems = 76;
 constexpr float kGrow = 8.f;          // how far, in powers of two, a row's maximum may pass the one in use
 
-template <int D>
+template <int D, int CTAS>
 struct Shape {
-  static constexpr int kTile = kRows * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr int kSmem = (2 + kStages) * kTile + 1024;
+  static constexpr int kQTile = kRows * D * 2;
+  static constexpr int kTile = kQTile / CTAS;       // this CTA's part of a block's keys, or of its values
+  static constexpr int kKeys = kRows / CTAS;        // of its keys
+  static constexpr int kStages = D == 128 ? 5 * CTAS : 8;
+  static constexpr int kSmem = 2 * kQTile + kStages * kTile + 1024;
   static constexpr uint32_t kO = 256;  // columns: S and P of the tiles at 0 and 128, O at 256 and 256 + D
 };
 
@@ -67,8 +70,8 @@ struct Item {
 
 struct Head {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], tail_there, tail_zero, drain;  // p_full: a block's first kFirst keys, and the rest
-  uint64_t full[8], empty[8];
-  uint64_t item_full[2], item_empty[2], item_near, next_there;  // item_near: the loads of an item are almost all under way
+  uint64_t full[10], empty[10];
+  uint64_t item_full[2], item_empty[2], item_near, ready, next_there;  // item_near: the loads of an item are almost all under way
   alignas(16) uint32_t next[4];  // the answer to the request for another CTA's place
   Item items[2];
   uint32_t bad[8];            // by block, of the last 8: keys on pages that are out of range, a bit for each 16
@@ -116,30 +119,90 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// ---- what differs where a pair of CTAs works on tiles of 256 rows ----
+
+// An arrival on the barrier at the same place in the pair's first CTA, whose thread issues
+// the products of both.
+template <int CTAS>
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  if (CTAS == 1) mbar_arrive_local(bar);
+  else mbar_arrive_cluster(mapa_shared(smem_u32(bar), 0));
+}
+
+// An arrival on the barrier at the same place in every CTA when the products issued before are done.
+template <int CTAS>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (CTAS == 1) {
+    tc05::commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  }
+}
+
+template <int CTAS>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  if (CTAS == 1) {
+    tc05::mma_ss(d, a, b, idesc, add);
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+  }
+}
+template <int CTAS>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  if (CTAS == 1) {
+    tc05::mma_ts(d, a, b, idesc, add);
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+  }
+}
+
+// A load into this CTA's shared memory, counted on a barrier of the pair's first CTA.
+template <int CTAS>
+__device__ __forceinline__ void load_tile(void* smem, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  if (CTAS == 1) {
+    tma_load_3d(smem, map, x, y, z, bar);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(mapa_shared(smem_u32(bar), 0))
+        : "memory");
+  }
+}
+
 // The products of both tiles, issued by one thread. (It is elected: operands are then as
 // the tensor core's instructions want them and an issue takes the products' own time, 64
 // cycles each, where a thread chosen by its lane took 140. A warp for each tile's products
 // interleaves them, and each waits longer for its own: 444 us instead of 395 for 8192
 // tokens and 32 heads of 128.)
-template <int D>
+template <int D, int CTAS>
 __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* tiles) {
-  using Sh = Shape<D>;
-  constexpr uint32_t qk = tc05::idesc_f16kind(kRows, kRows, true), pv = tc05::idesc_f16kind(kRows, D, true) | tc05::kIdescBMnMajor;
+  using Sh = Shape<D, CTAS>;
+  constexpr uint32_t qk = tc05::idesc_f16kind(CTAS * kRows, kRows, true), pv = tc05::idesc_f16kind(CTAS * kRows, D, true) | tc05::kIdescBMnMajor;
   const uint64_t desc = tc05::smem_desc(0, 16, 1024, tc05::kSwizzle128B), desc_mn = tc05::smem_desc(0, kHalf, 1024, tc05::kSwizzle128B);
-  const uint32_t q_base = smem_u32(tiles) >> 4, r_base = q_base + (2 * Sh::kTile >> 4);
+  const uint32_t q_base = smem_u32(tiles) >> 4, r_base = q_base + (2 * Sh::kQTile >> 4);
   auto scores = [&](int m, int s) {  // S = Q K^T
-    const uint64_t q = desc + (q_base + m * (Sh::kTile >> 4)), k = desc + (r_base + s * (Sh::kTile >> 4));
+    const uint64_t q = desc + (q_base + m * (Sh::kQTile >> 4)), k = desc + (r_base + s * (Sh::kTile >> 4));
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
-      const uint32_t at = (c / 4 * kHalf + c % 4 * 32) >> 4;
-      tc05::mma_ss(m * kRows, q + at, k + at, qk, c > 0);
+      mma_ss<CTAS>(m * kRows, q + ((c / 4 * kHalf + c % 4 * 32) >> 4), k + ((c / 4 * (Sh::kKeys * 128) + c % 4 * 32) >> 4), qk, c > 0);
     }
-    tc05::commit(&sm.s_full[m]);
+    commit<CTAS>(&sm.s_full[m]);
   };
   auto values = [&](int m, int s, int from, int to, bool add) {  // O (+)= P V over keys 16 from .. 16 to - 1
     const uint64_t v = desc_mn + (r_base + s * (Sh::kTile >> 4));
 #pragma unroll
-    for (int c = from; c < to; ++c) tc05::mma_ts(Sh::kO + m * D, m * kRows + 8 * c, v + ((c * 16 * 128) >> 4), pv, add || c > 0);
+    for (int c = from; c < to; ++c) mma_ts<CTAS>(Sh::kO + m * D, m * kRows + 8 * c, v + ((c * 16 * 128) >> 4), pv, add || c > 0);
   };
   bool going = true;
   int s = 0, phase = 0;              // stage of the ring that comes next
@@ -162,9 +225,9 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
         going = going && wait(&sm.q_full[m], tiles_done[m]++ & 1);
         tc05::fence_after_sync();
         if (going) scores(m, s);
-        if (count == 1) tc05::commit(&sm.q_empty[m]);
+        if (count == 1) commit<CTAS>(&sm.q_empty[m]);
       }
-      tc05::commit(&sm.empty[s]);
+      commit<CTAS>(&sm.empty[s]);
       advance();
     }
     int i = 0;
@@ -184,10 +247,10 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
         tc05::fence_after_sync();
         values(m, vs, kFirst / 16, kRows / 16, true);
         scores(m, s);
-        if (i + 2 == (m == 0 ? count0 : count1)) tc05::commit(&sm.q_empty[m]);
+        if (i + 2 == (m == 0 ? count0 : count1)) commit<CTAS>(&sm.q_empty[m]);
       }
-      tc05::commit(&sm.empty[s]);
-      tc05::commit(&sm.empty[vs]);
+      commit<CTAS>(&sm.empty[s]);
+      commit<CTAS>(&sm.empty[vs]);
       advance();
       going = there;
     }
@@ -197,7 +260,10 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
       going = wait(&sm.full[vs], v_phase);
       if (i + 1 < blocks) going = going && wait(&sm.full[s], phase);
       const bool tail = keys < (i + 1) * kRows;  // the sequence's last block is not full: zeros behind its last key
-      if (tail && going) mbar_arrive_local(&sm.tail_there);
+      if (tail && going) {
+        mbar_arrive_local(&sm.tail_there);
+        if (CTAS == 2) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.tail_there), 1));
+      }
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int count = m == 0 ? count0 : count1;
@@ -213,12 +279,12 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
         if (going) values(m, vs, kFirst / 16, kRows / 16, true);
         if (i + 1 < count) {
           if (going) scores(m, s);
-          if (i + 2 == count) tc05::commit(&sm.q_empty[m]);
-          if (last_k) tc05::commit(&sm.empty[s]);
+          if (i + 2 == count) commit<CTAS>(&sm.q_empty[m]);
+          if (last_k) commit<CTAS>(&sm.empty[s]);
         } else {
-          tc05::commit(&sm.o_full[m]);
+          commit<CTAS>(&sm.o_full[m]);
         }
-        if (last_v) tc05::commit(&sm.empty[vs]);
+        if (last_v) commit<CTAS>(&sm.empty[vs]);
       }
       if (tail) ++tails;
       if (i + 1 < blocks) advance();
@@ -226,7 +292,7 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
     mbar_arrive_local(&sm.item_empty[k & 1]);
   }
   if (!going) {  // products in flight end before their tensor memory is given back
-    tc05::commit(&sm.drain);
+    commit<CTAS>(&sm.drain);
     wait(&sm.drain, 0);
   }
   return going;
@@ -236,10 +302,10 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
 // Places in falling order, so that a causal prompt's long tiles start first. Sequence n's
 // tiles have the places from cu_seqlens[n] / (tokens of a CTA) + n on, of which there are
 // enough for it before the next sequence's.
-template <bool PAGED>
+template <bool PAGED, int CTAS>
 __device__ __forceinline__ bool item_of(const Params& p, long long index, int lane, Item& it) {
   const kda_attn_fwd_args& a = p.a;
-  const int cta_tokens = 2 * p.tile_tokens;
+  const int tile_tokens = CTAS * p.tile_tokens, cta_tokens = 2 * tile_tokens;
   it.split = static_cast<int>(index % p.parts.splits);
   index /= p.parts.splits;
   const int set = static_cast<int>(index % p.heads);
@@ -279,20 +345,28 @@ __device__ __forceinline__ bool item_of(const Params& p, long long index, int la
   it.first = min(blocks, it.split * per);
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    const int t = it.t0 + m * p.tile_tokens, last = min(t + p.tile_tokens, it.T) - 1;
+    const int t = it.t0 + m * tile_tokens, last = min(t + tile_tokens, it.T) - 1;
     const int seen = t >= it.T ? 0 : a.flags & KDA_ATTN_FLAG_CAUSAL ? min(it.S, last + it.shift + 1) : it.S;
     it.count[m] = max(0, min((max(seen, 0) + kRows - 1) / kRows, it.first + per) - it.first);
   }
   return true;
 }
 
-// Asks for the place of a CTA of this grid that has not started yet; the answer comes to
-// sm.next and counts 16 bytes on sm.next_there.
+// Asks for the place of a CTA (or pair) of this grid that has not started yet; the answer
+// comes to sm.next of every CTA of the pair and counts 16 bytes on its sm.next_there.
+template <int CTAS>
 __device__ __forceinline__ void ask_for_place(Head& sm) {
-  mbar_arrive_expect_tx_local(&sm.next_there, 16);
-  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(sm.next)),
-               "r"(smem_u32(&sm.next_there))
-               : "memory");
+  if (CTAS == 1) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_u32(sm.next)),
+                 "r"(smem_u32(&sm.next_there))
+                 : "memory");
+  } else {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 [%0], [%1];" ::"r"(
+            smem_u32(sm.next)),
+        "r"(smem_u32(&sm.next_there))
+        : "memory");
+  }
 }
 // Whether the answer gives a place, and which.
 __device__ __forceinline__ bool place_given(const Head& sm, uint32_t& place) {
@@ -308,18 +382,19 @@ __device__ __forceinline__ bool place_given(const Head& sm, uint32_t& place) {
   return given != 0;
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1)
     kda_attn_fwd_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
-  using Sh = Shape<D>;
+  using Sh = Shape<D, CTAS>;
   extern __shared__ unsigned char raw[];
   __shared__ Head sm;
   const kda_attn_fwd_args& a = p.a;
   // (a step that joins these results has work of its own to do before it)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
-  unsigned char* ring = tiles + 2 * Sh::kTile;
+  unsigned char* ring = tiles + 2 * Sh::kQTile;
+  const int rank = CTAS == 1 ? 0 : static_cast<int>(cluster_ctarank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool causal = a.flags & KDA_ATTN_FLAG_CAUSAL;
 
@@ -338,18 +413,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (warp == 0) {
-    tc05::tmem_alloc(&sm.tmem_base, 512);
-    tc05::tmem_relinquish();
+    if (CTAS == 1) {
+      tc05::tmem_alloc(&sm.tmem_base, 512);
+      tc05::tmem_relinquish();
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)), "r"(512) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
   }
   if (tid == 8 * 32) {
     for (int m = 0; m < 2; ++m) {
       mbar_init(&sm.q_full[m], 1);
       mbar_init(&sm.q_empty[m], 1);
       mbar_init(&sm.item_full[m], 1);
-      mbar_init(&sm.item_empty[m], 11);
+      mbar_init(&sm.item_empty[m], rank == 0 ? 11 : 10);
       mbar_init(&sm.s_full[m], 1);
-      mbar_init(&sm.p_full[m][0], 4);
-      mbar_init(&sm.p_full[m][1], 4);
+      mbar_init(&sm.p_full[m][0], 4 * CTAS);
+      mbar_init(&sm.p_full[m][1], 4 * CTAS);
       mbar_init(&sm.o_full[m], 1);
     }
     for (int s = 0; s < Sh::kStages; ++s) {
@@ -357,9 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.empty[s], 1);
     }
     mbar_init(&sm.tail_there, 1);
-    mbar_init(&sm.tail_zero, 1);
+    mbar_init(&sm.tail_zero, CTAS);
     mbar_init(&sm.drain, 1);
     mbar_init(&sm.item_near, 1);
+    mbar_init(&sm.ready, CTAS);
     mbar_init(&sm.next_there, 1);
     sm.failed = 0;
     fence_mbarrier_init_cluster();
@@ -372,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc05::fence_before_sync();
   __syncthreads();
+  if (CTAS > 1) cluster_sync_all();
   tc05::fence_after_sync();
   // (all 512 columns: the allocation starts at 0)
   const uint32_t tmem = 0;
@@ -380,8 +462,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 9) {
       // ---- loads: the tiles' queries, then keys and values block by block ----
-      const int box_keys = PAGED ? a.page_size : kRows;
-      const int boxes = kRows / box_keys * (D / 64), part = lane / (D / 64), half = lane % (D / 64);
+      // a block's keys and values in boxes of so many keys and 64 channels, one a lane
+      constexpr int kParts = D / 64;
+      const int box_keys = PAGED ? min(a.page_size, Sh::kKeys) : Sh::kKeys, v_box_keys = PAGED ? box_keys : kRows;
       const uint32_t q_bytes = static_cast<uint32_t>(p.Gp * p.tile_tokens) * D * 2;
       bool going = true;
       int loaded = 0, blocks_done = 0, tiles_done[2] = {0, 0};
@@ -398,58 +481,63 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!going) continue;
           ++tiles_done[m];
           if (lane == 0) {
-            mbar_arrive_expect_tx_local(&sm.q_full[m], q_bytes);
+            if (rank == 0) mbar_arrive_expect_tx_local(&sm.q_full[m], CTAS * q_bytes);
             for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(tiles + m * Sh::kTile + c * kHalf, &qmap, 64 * c, it.h0, it.q0 + it.t0 + m * p.tile_tokens, &sm.q_full[m]);
+              load_tile<CTAS>(tiles + m * Sh::kQTile + c * kHalf, &qmap, 64 * c, it.h0, it.q0 + it.t0 + (m * CTAS + rank) * p.tile_tokens, &sm.q_full[m]);
           }
         }
         if (lane == 0 && most <= 1) mbar_arrive_local(&sm.item_near);
         for (int j = it.first; j < it.first + most && going; ++j) {
           if (lane == 0 && most > 1 && j == it.first + most - 2) mbar_arrive_local(&sm.item_near);
-          int y = it.hk, z = it.k0 + j * kRows;
-          uint32_t bad = 0;
-          if (PAGED) {
-            // a page that is out of range, or behind the last key, reads as zeros
-            const int tok = j * kRows + part * box_keys;
-            int page = -1;
-            if (lane < boxes && tok < it.S) {
-              page = a.block_table[static_cast<long long>(it.n) * a.table_width + tok / box_keys];
-              if (page >= a.pages) page = -1;
-            }
-            bad = __ballot_sync(0xffffffffu, lane < boxes && tok < it.S && page < 0);
-            if (bad != 0) {
-              if (lane == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
-              // a bit for each box to one for each 16 keys
-              bad = __ballot_sync(0xffffffffu, lane < 8 && (bad >> (lane * 16 / box_keys * (D / 64)) & 1u));
-            }
-            y = 0;
-            z = page < 0 ? -1 : page * a.HKV + it.hk;
-          }
           for (int kv = 0; kv < 2 && going; ++kv, ++loaded) {
+            // keys: this CTA's share of them, all channels; values: all keys, its share of the channels
+            const int parts = kv == 0 ? kParts : kParts / CTAS, keys = kv == 0 ? box_keys : v_box_keys;
+            const int boxes = (kv == 0 ? Sh::kKeys : kRows) / keys * parts, part = lane / parts, half = lane % parts;
+            const int tok = j * kRows + part * keys + (kv == 0 ? rank * Sh::kKeys : 0);
+            int y = it.hk, z = it.k0 + tok;
+            uint32_t bad = 0;
+            if (PAGED) {
+              // a page that is out of range, or behind the last key, reads as zeros
+              int page = -1;
+              if (lane < boxes && tok < it.S) {
+                page = a.block_table[static_cast<long long>(it.n) * a.table_width + tok / a.page_size];
+                if (page >= a.pages) page = -1;
+              }
+              y = tok % a.page_size;
+              z = page < 0 ? -1 : page * a.HKV + it.hk;
+              bad = __ballot_sync(0xffffffffu, lane < boxes && tok < it.S && page < 0);
+              if (bad != 0) {
+                if (lane == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
+                // a bit for each box to one for each 16 keys
+                bad = __ballot_sync(0xffffffffu, lane < 8 && (bad >> (lane * 16 / keys * parts) & 1u));
+              }
+            }
             const int s = loaded % Sh::kStages;
             if (loaded >= Sh::kStages) going = __all_sync(0xffffffffu, wait(&sm.empty[s], (loaded / Sh::kStages - 1) & 1));
             if (!going) break;
             if (lane == 0) {
-              // (the loads are at most 4 blocks ahead of the weights, which read this)
-              if (PAGED && kv == 0) sm.bad[(blocks_done + j - it.first) & 7] = bad;
-              mbar_arrive_expect_tx_local(&sm.full[s], Sh::kTile);
+              // (the values', of all keys; the loads are at most 5 blocks ahead of the weights, which read this)
+              if (PAGED && kv == 1) sm.bad[(blocks_done + j - it.first) & 7] = bad;
+              if (rank == 0) mbar_arrive_expect_tx_local(&sm.full[s], CTAS * Sh::kTile);
             }
             __syncwarp();
             if (lane < boxes)
-              tma_load_3d(ring + s * Sh::kTile + half * kHalf + part * box_keys * 128, kv == 0 ? &kmap : &vmap, 64 * half, y, z, &sm.full[s]);
+              load_tile<CTAS>(ring + s * Sh::kTile + half * (kv == 0 ? Sh::kKeys * 128 : kHalf) + part * keys * 128, kv == 0 ? &kmap : &vmap,
+                              64 * (half + (kv == 0 ? 0 : rank * parts)), y, z, &sm.full[s]);
           }
         }
         blocks_done += most;
         __syncwarp();
         if (lane == 0) mbar_arrive_local(&sm.item_empty[k & 1]);
       }
-      // no copy is left in flight when the CTA ends
+      // every tile and stage has been used up: no copy and no arrival is left under way when
+      // the CTA ends
       for (int m = 0; m < 2; ++m)
-        if (tiles_done[m] > 0) going &= wait(&sm.q_full[m], (tiles_done[m] - 1) & 1);
-      for (int i = max(0, loaded - Sh::kStages); i < loaded; ++i) going &= wait(&sm.full[i % Sh::kStages], (i / Sh::kStages) & 1);
+        if (tiles_done[m] > 0) going &= wait(&sm.q_empty[m], (tiles_done[m] - 1) & 1);
+      for (int i = max(0, loaded - Sh::kStages); i < loaded; ++i) going &= wait(&sm.empty[i % Sh::kStages], (i / Sh::kStages) & 1);
       if (!going) sm.failed = 1;
     } else if (warp == 8) {
-      if (elect_one() && !issue_products<D>(sm, tiles)) sm.failed = 1;
+      if (rank == 0 && elect_one() && !issue_products<D, CTAS>(sm, tiles)) sm.failed = 1;
     } else if (warp == 10) {
       // ---- what stands behind the last key may be anything: zeros in its place ----
       bool going = true;
@@ -465,11 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           going = __all_sync(0xffffffffu, wait(&sm.tail_there, tails++ & 1));
           if (!going) break;
           unsigned char* v = ring + s * Sh::kTile;
-          for (int c = 0; c < D / 64; ++c)
+          for (int c = 0; c < D / 64 / CTAS; ++c)
             for (int u = live * 8 + lane; u < kRows * 8; u += 32) *reinterpret_cast<uint4*>(v + c * kHalf + u * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_local(&sm.tail_zero);
+          if (lane == 0) arrive_first<CTAS>(&sm.tail_zero);
         }
         loaded += 2 * most;
         __syncwarp();
@@ -486,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (going) {
         Item it;
         if (!more) it.n = -1;
-        if (!more || item_of<PAGED>(p, place, lane, it)) {
+        if (!more || item_of<PAGED, CTAS>(p, place / CTAS, lane, it)) {
           if (k >= 2) going = __all_sync(0xffffffffu, wait(&sm.item_empty[k & 1], ((k >> 1) - 1) & 1));
           if (going && lane == 0) {
             sm.items[k & 1] = it;
@@ -496,18 +584,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++k;
         }
         if (!more || !going) break;
-        if (lane == 0) ask_for_place(sm);
+        // (every CTA of a pair has read the last answer, and expects the next, before it is asked for)
+        if (lane == 0) {
+          mbar_arrive_expect_tx_local(&sm.next_there, 16);
+          arrive_first<CTAS>(&sm.ready);
+        }
+        if (rank == 0) going = __all_sync(0xffffffffu, wait(&sm.ready, asked & 1));
+        if (going && rank == 0 && lane == 0) ask_for_place<CTAS>(sm);
         ++asked;
+        if (!going) break;
         going = __all_sync(0xffffffffu, wait(&sm.next_there, (asked - 1) & 1));
         if (!going) break;
         more = place_given(sm, place);
         fence_proxy_async_smem();  // (the next answer is written after this one has been read)
         __syncwarp();
       }
-      if (!going) {
-        if (asked > 0) wait(&sm.next_there, (asked - 1) & 1);  // no answer is left under way
-        sm.failed = 1;
-      }
+      if (!going) sm.failed = 1;
     }
   } else {
     // ---- rows ----
@@ -525,11 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Item& it = sm.items[k & 1];
     if (it.n < 0) break;
     const int first = it.first, count = it.count[m];
-    const int ti = it.t0 + m * p.tile_tokens + row_token;
+    const int own = it.t0 + (m * CTAS + rank) * p.tile_tokens;  // the first token of this CTA's rows
+    const int ti = own + row_token;
     const bool valid = row_token < p.tile_tokens && ti < it.T;
     const int limit = !valid ? 0 : causal ? max(0, min(it.S, ti + it.shift + 1)) : it.S;  // keys this row sees
     // blocks below this end need no mask (the tile's first row sees all of them)
-    const int open = causal ? min(it.S, it.t0 + m * p.tile_tokens + it.shift + 1) : it.S;
+    const int open = causal ? min(it.S, own + it.shift + 1) : it.S;
     float top = -INFINITY, sum = 0.f;
     for (int i = 0; i < count && going; ++i, ++done) {
       const bool there = wait(&sm.s_full[m], done & 1);  // (looked at below, when nothing waits for it)
@@ -594,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc05::wait_st();
           tc05::fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive_local(&sm.p_full[m][h + 32 == kRows]);
+          if (lane == 0) arrive_first<CTAS>(&sm.p_full[m][h + 32 == kRows]);
         }
       }
       going = __all_sync(0xffffffffu, there);
@@ -694,7 +787,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc05::fence_after_sync();
   if (tid == 0 && sm.failed) set_err(a.err, KDA_ERR_TIMEOUT);
-  if (warp == 0) tc05::tmem_dealloc(tmem, 512);
+  if (CTAS > 1) cluster_sync_all();  // neither CTA ends while the other may still signal it or read its memory
+  if (warp == 0) {
+    if (CTAS == 1) tc05::tmem_dealloc(tmem, 512);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
 }
 
 // Query heads of a tile's tokens: the largest divisor of the group that leaves no more
@@ -705,32 +802,59 @@ int heads_of_tile(int group) {
   return 1;
 }
 
-template <int D, bool PAGED>
-cudaError_t launch(const Params& p, cudaStream_t s) {
+template <int D, bool PAGED, int CTAS>
+cudaError_t launch(Params p, cudaStream_t s) {
+  using Sh = Shape<D, CTAS>;
   const kda_attn_fwd_args& a = p.a;
+  const int tokens = 2 * CTAS * p.tile_tokens;
+  const long long slots = a.cu_seqlens ? static_cast<long long>(a.T) / tokens + a.N : (static_cast<long long>(a.T) + tokens - 1) / tokens * a.N;
+  if (slots > INT32_MAX) return cudaErrorNotSupported;
+  p.slots = static_cast<int>(slots);
   CUtensorMap qmap, kmap, vmap;
   const long long queries = static_cast<long long>(a.B) * a.T;
   bool ok = encode_heads(&qmap, a.q, D, a.HQ, D, queries, a.q_stride, static_cast<unsigned>(p.Gp), static_cast<unsigned>(p.tile_tokens));
   if (PAGED) {
     // a cache without pages is never read (every page is out of range): any map will do
     const long long rows = static_cast<long long>(a.pages) * a.HKV, page = static_cast<long long>(a.page_size) * D;
+    const unsigned box = static_cast<unsigned>(a.page_size < Sh::kKeys ? a.page_size : Sh::kKeys);
     const bool none = a.pages == 0;
-    ok = ok && encode_heads(&kmap, none ? a.q : a.k, D, a.page_size, D, none ? 1 : rows, page, static_cast<unsigned>(a.page_size), 1) &&
-         encode_heads(&vmap, none ? a.q : a.v, D, a.page_size, D, none ? 1 : rows, page, static_cast<unsigned>(a.page_size), 1);
+    ok = ok && encode_heads(&kmap, none ? a.q : a.k, D, a.page_size, D, none ? 1 : rows, page, box, 1) &&
+         encode_heads(&vmap, none ? a.q : a.v, D, a.page_size, D, none ? 1 : rows, page, box, 1);
   } else {
     const long long keys = static_cast<long long>(a.B) * a.S;
     const bool none = keys == 0;
-    ok = ok && encode_heads(&kmap, none ? a.q : a.k, D, a.HKV, D, none ? 1 : keys, a.k_stride, 1, kRows) &&
+    ok = ok && encode_heads(&kmap, none ? a.q : a.k, D, a.HKV, D, none ? 1 : keys, a.k_stride, 1, Sh::kKeys) &&
          encode_heads(&vmap, none ? a.q : a.v, D, a.HKV, D, none ? 1 : keys, a.v_stride, 1, kRows);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const long long grid = static_cast<long long>(p.slots) * p.heads * p.parts.splits;
+  const long long grid = slots * p.heads * p.parts.splits * CTAS;
   if (grid > INT32_MAX) return cudaErrorNotSupported;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = set_smem_limit_once(kda_attn_fwd_kernel<D, PAGED>, Shape<D>::kSmem, smem_set);
+  const cudaError_t e = set_smem_limit_once(kda_attn_fwd_kernel<D, PAGED, CTAS>, Sh::kSmem, smem_set);
   if (e != cudaSuccess) return e;
-  kda_attn_fwd_kernel<D, PAGED><<<static_cast<unsigned>(grid), kThreads, Shape<D>::kSmem, s>>>(p, qmap, kmap, vmap);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CTAS;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = CTAS > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kda_attn_fwd_kernel<D, PAGED, CTAS>, p, qmap, kmap, vmap);
+}
+
+template <bool PAGED>
+cudaError_t launch_width(const Params& p, cudaStream_t s) {
+  const kda_attn_fwd_args& a = p.a;
+  if (a.D == 64) return launch<64, PAGED, 1>(p, s);
+  // Pairs of CTAs where there are four rounds of them and sequences fill their tiles.
+  const int tokens = 4 * p.tile_tokens;
+  const long long each = a.cu_seqlens ? static_cast<long long>(a.T) / a.N : a.T, items = static_cast<long long>(a.B) * a.T / tokens * p.heads;
+  if (p.parts.o == nullptr && each >= kPairTokens * tokens && items >= kPairItems) return launch<128, PAGED, 2>(p, s);
+  return launch<128, PAGED, 1>(p, s);
 }
 
 }  // namespace
@@ -749,12 +873,7 @@ cudaError_t launch_attn_prompts(const kda_attn_fwd_args& a, const AttnParts& par
   p.heads = a.HKV * p.sub;
   p.tile_tokens = kRows / p.Gp;
   p.per_token = (65536 + p.Gp - 1) / p.Gp;
-  const int tokens = 2 * p.tile_tokens;
-  const long long slots = a.cu_seqlens ? static_cast<long long>(a.T) / tokens + a.N : (static_cast<long long>(a.T) + tokens - 1) / tokens * a.N;
-  if (slots > INT32_MAX) return cudaErrorNotSupported;
-  p.slots = static_cast<int>(slots);
-  if (a.block_table) return a.D == 64 ? launch<64, true>(p, s) : launch<128, true>(p, s);
-  return a.D == 64 ? launch<64, false>(p, s) : launch<128, false>(p, s);
+  return a.block_table ? launch_width<true>(p, s) : launch_width<false>(p, s);
 }
 
 cudaError_t launch_attn_fwd(const kda_attn_fwd_args& a, cudaStream_t s) { return launch_attn_prompts(a, AttnParts{nullptr, nullptr, 1, 0}, s); }

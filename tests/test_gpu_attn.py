@@ -234,6 +234,46 @@ def test_prompts_other_key_lengths(lens, lens_k, causal):
     run_prompts(gen, lens, lens_k, 3, 3, 128, causal)
 
 
+@pytest.mark.parametrize("P", [0, 16, 32, 64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_many_tiles(P, causal):
+    """Prompts long enough for the tiles that two CTAs share: first, last and border rows of tiles."""
+    gen = torch.Generator().manual_seed(41 + P)
+    HQ, HKV, D = 64, 4, 128
+    lens, lens_k = (701, 0, 1025, 3), (701, 9, 1400, 130)
+    if not P:
+        lens_k = (701, 9, 1025, 3)
+    T, S = sum(lens), sum(lens_k)
+    q, k, v = randn(gen, T, HQ, D), randn(gen, S, HKV, D), randn(gen, S, HKV, D)
+    offs, offs_k = np.cumsum([0] + list(lens)), np.cumsum([0] + list(lens_k))
+    ks, vs = ([x[a:b] for a, b in zip(offs_k[:-1], offs_k[1:])] for x in (k, v))
+    cn, err = Canary(), err_word()
+    o, lse = cn.empty((1, T, HQ, D), BF, name="o"), cn.empty((1, T, HQ), F32, name="lse")
+    kw = dict(scale=0.09, causal=causal, o=o, lse=lse, err=err, cu_seqlens=cu(lens).cuda())
+    if P:
+        cache = Cache(gen, ks, vs, P).cuda()
+        kda.kda_attn_fwd(q[None].cuda(), cache.k, cache.v, block_table=cache.table, seq_lens_k=cache.lens, **kw)
+    else:
+        kda.kda_attn_fwd(q[None].cuda(), k[None].cuda(), v[None].cuda(), cu_seqlens_k=cu(lens_k).cuda(), **kw)
+    cn.check()
+    assert int(err) == 0
+    for n in range(4):
+        seen = ao.seen_keys(lens[n], lens_k[n], causal)
+        for i in sorted({i for i in (0, 1, 7, 8, 15, 16, 31, 32, 33, 63, 64, 127, 128, 500, lens[n] - 2, lens[n] - 1) if 0 <= i < lens[n]}):
+            row = offs[n] + i
+            refs = ao.attend(np64(q[row:row + 1]), np64(ks[n]), np64(vs[n]), float(np.float32(0.09)), [seen[i]])
+            check(o[0, row:row + 1], lse[0, row:row + 1], refs, lens_k[n], D)
+    # and every row against the step's kernel, which shares nothing with it but the cache
+    if P:
+        rows = [(n, i) for n in (0, 2) for i in range(0, lens[n], 5)]
+        step = kda.kda_attn_step(q[[offs[n] + i for n, i in rows]].cuda(), cache.k, cache.v, cache.table[[n for n, _ in rows]].contiguous(),
+                                 torch.tensor([int(ao.seen_keys(lens[n], lens_k[n], causal)[i]) for n, i in rows], dtype=torch.int32).cuda(), scale=0.09)
+        got = o[0, [int(offs[n] + i) for n, i in rows]]
+        # both round the weights and the result to bf16
+        big = step.float().abs().max()
+        assert float((got.float() - step.float()).abs().max()) <= 2 * 2.0 ** -8 * float(big) + 2 * 2.0 ** -8 * float(v.float().abs().max())
+
+
 @pytest.mark.parametrize("P", [16, 32, 64, 128])
 @pytest.mark.parametrize("lens,lens_k", [((5, 1, 130), (5, 200, 259)), ((1, 1), (1, 128)), ((140, 0), (400, 7)), ((9,), (4,))])
 def test_prompts_paged(lens, lens_k, P):
