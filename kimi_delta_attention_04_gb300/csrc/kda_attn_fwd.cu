@@ -35,9 +35,7 @@ using namespace attn;
 
 constexpr int kThreads = 384;
 constexpr int kRows = 128;            // rows of a tile; keys of a block
-constexpr int kFirst = 64;            // keys of a block whose products start before the others' weights are there
 constexpr int kHalf = kRows * 128;    // bytes of a block's 64 channels
-constexpr int kPairTokens = 2, kPairItems = 76;
 constexpr float kGrow = 8.f;          // how far, in powers of two, a row's maximum may pass the one in use
 
 template <int D, int CTAS>
@@ -69,7 +67,7 @@ struct Item {
 };
 
 struct Head {
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], tail_there, tail_zero, drain;  // p_full: a block's first kFirst keys, and the rest
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], tail_there, tail_zero, drain;  // p_full: of each half of a block's keys
   uint64_t full[10], empty[10];
   uint64_t item_full[2], item_empty[2], item_near, ready, next_there;  // item_near: the loads of an item are almost all under way
   alignas(16) uint32_t next[4];  // the answer to the request for another CTA's place
@@ -242,10 +240,10 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
         const int parity = done[m]++ & 1;
         there &= wait(&sm.p_full[m][0], parity);
         tc05::fence_after_sync();
-        values(m, vs, 0, kFirst / 16, i > 0);
+        values(m, vs, 0, 4, i > 0);
         there &= wait(&sm.p_full[m][1], parity);
         tc05::fence_after_sync();
-        values(m, vs, kFirst / 16, kRows / 16, true);
+        values(m, vs, 4, kRows / 16, true);
         scores(m, s);
         if (i + 2 == (m == 0 ? count0 : count1)) commit<CTAS>(&sm.q_empty[m]);
       }
@@ -273,10 +271,10 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
         going = wait(&sm.p_full[m][0], parity);
         if (tail) going = going && wait(&sm.tail_zero, tails & 1);
         tc05::fence_after_sync();
-        if (going) values(m, vs, 0, kFirst / 16, i > 0);
+        if (going) values(m, vs, 0, 4, i > 0);
         going = going && wait(&sm.p_full[m][1], parity);
         tc05::fence_after_sync();
-        if (going) values(m, vs, kFirst / 16, kRows / 16, true);
+        if (going) values(m, vs, 4, kRows / 16, true);
         if (i + 1 < count) {
           if (going) scores(m, s);
           if (i + 2 == count) commit<CTAS>(&sm.q_empty[m]);
@@ -628,19 +626,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool there = wait(&sm.s_full[m], done & 1);  // (looked at below, when nothing waits for it)
       __syncwarp();
       tc05::fence_after_sync();
-      float s[128];
-      tc05::ld128_wait(s_at, s);
       const int k0 = (first + i) * kRows;
       const uint32_t bad = PAGED ? sm.bad[(blocks_done + i) & 7] : 0;
-      if (k0 + kRows > open || (PAGED && bad != 0)) {
+      float s[128];
+      auto load = [&]() {
+        tc05::ld128_wait(s_at, s);
+        if (k0 + kRows > open || (PAGED && bad != 0)) {
 #pragma unroll
-        for (int j = 0; j < 128; ++j) s[j] = k0 + j < limit ? s[j] : -INFINITY;
-        if (PAGED && bad != 0) {
+          for (int j = 0; j < 128; ++j) s[j] = k0 + j < limit ? s[j] : -INFINITY;
+          if (PAGED && bad != 0) {
 #pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (bad >> (j / 16) & 1u) s[j] = -INFINITY;
+            for (int j = 0; j < 128; ++j)
+              if (bad >> (j / 16) & 1u) s[j] = -INFINITY;
+          }
         }
-      }
+      };
+      load();
+      const float2 c22 = make_float2(c2, c2);
+      float2 base2, sum2[2];
+      float w[32];  // weights of half of the block's keys, in bf16 pairs
+      auto weigh = [&](int h) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float2 x = fma2(make_float2(s[h + 2 * j], s[h + 2 * j + 1]), c22, base2);
+          x.x = ex2_approx(x.x);
+          x.y = ex2_approx(x.y);
+          sum2[j & 1] = add2(sum2[j & 1], x);
+          w[j] = __uint_as_float(Bf16::pack(x.x, x.y));
+        }
+      };
+      auto restart = [&]() {
+        const float base = top == -INFINITY ? 0.f : -top * c2;
+        base2 = make_float2(base, base);
+        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+        weigh(0);
+      };
+      // With 128 channels, the first half's weights under the maximum in use, while this
+      // block's is found: it rarely changes after the first blocks (in pairs, 8192 tokens and
+      // 32 heads: 312 us instead of 337). With 64, where a block's products are half as long
+      // and short prompts are nothing but first blocks, after it (64 prompts of up to 333
+      // tokens: 33 us instead of 36).
+      constexpr bool kAhead = D == 128;
+      if (kAhead) restart();
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
       for (int j = 4; j < 124; j += 8) {
@@ -648,16 +675,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[j + 2 * e], s[j + 2 * e + 1]);
       }
       const float high = fmaxf(max3(max3(mx[0], s[124], s[125]), max3(mx[1], s[126], s[127]), mx[2]), mx[3]);
-      if (i == 0) {
-        top = high;
-      } else {
-        const bool grew = (high - top) * c2 > kGrow || (top == -INFINITY && high > top);
-        if (__any_sync(0xffffffffu, grew)) {
-          // (S of this block is there, so the product that last changed O is done)
-          const float now = grew ? high : top;
-          const float keep = grew ? ex2_approx((top - now) * c2) : 1.f;
-          top = now;
-          sum *= keep;
+      const bool grew = (high - top) * c2 > kGrow || (top == -INFINITY && high > top);
+      if (__any_sync(0xffffffffu, grew)) {
+        // (S of this block is there, so the product that last changed O is done)
+        const float now = grew ? high : top;
+        const float keep = grew ? ex2_approx((top - now) * c2) : 1.f;
+        top = now;
+        sum *= keep;
+        if (i > 0) {
 #pragma unroll
           for (int c = 0; c < D; c += 32) {
             float o[32];
@@ -667,28 +692,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc05::st32_wait(o_at + c, o);
           }
         }
+        if (kAhead) {
+          load();
+          restart();
+        }
       }
-      const float base = top == -INFINITY ? 0.f : -top * c2;
-      const float2 c22 = make_float2(c2, c2), base2 = make_float2(base, base);
-      float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      if (!kAhead) restart();
 #pragma unroll
-      for (int h = 0; h < 128; h += 32) {
-        float w[16];  // weights in bf16 pairs
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float2 x = fma2(make_float2(s[h + 2 * j], s[h + 2 * j + 1]), c22, base2);
-          x.x = ex2_approx(x.x);
-          x.y = ex2_approx(x.y);
-          sum2[j & 1] = add2(sum2[j & 1], x);
-          w[j] = __uint_as_float(Bf16::pack(x.x, x.y));
-        }
-        tc05::st16(s_at + h / 2, w);
-        if (h + 32 == kFirst || h + 32 == kRows) {  // the products of these keys may start
-          tc05::wait_st();
-          tc05::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) arrive_first<CTAS>(&sm.p_full[m][h + 32 == kRows]);
-        }
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1) weigh(64);
+        tc05::st32(s_at + 32 * h, w);
+        tc05::wait_st();
+        tc05::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_first<CTAS>(&sm.p_full[m][h]);  // the products of these keys may start
       }
       going = __all_sync(0xffffffffu, there);
       sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
@@ -850,10 +867,12 @@ template <bool PAGED>
 cudaError_t launch_width(const Params& p, cudaStream_t s) {
   const kda_attn_fwd_args& a = p.a;
   if (a.D == 64) return launch<64, PAGED, 1>(p, s);
-  // Pairs of CTAs where there are four rounds of them and sequences fill their tiles.
+  // Pairs of CTAs, each of which holds half of the keys and values, where there are four
+  // rounds of them on the 76 pairs of SMs and sequences of two tiles or more (4 x 512 tokens
+  // on 6512 keys, 128 pairs' work: 158 us with pairs, 149 without).
   const int tokens = 4 * p.tile_tokens;
   const long long each = a.cu_seqlens ? static_cast<long long>(a.T) / a.N : a.T, items = static_cast<long long>(a.B) * a.T / tokens * p.heads;
-  if (p.parts.o == nullptr && each >= kPairTokens * tokens && items >= kPairItems) return launch<128, PAGED, 2>(p, s);
+  if (p.parts.o == nullptr && each >= 2 * tokens && items >= 4 * 76) return launch<128, PAGED, 2>(p, s);
   return launch<128, PAGED, 1>(p, s);
 }
 
