@@ -2,9 +2,8 @@
 // shared prefix of the single-token step.
 //
 // A CTA takes 256 rows of queries, as two tiles of 128 that share every block of 128 keys
-// it loads. The rows of a tile are tokens x query heads of one key head (the largest
-// power of two of them that divides the group), so that a causal tile covers few tokens
-// and a group's heads share their keys' loads. For each tile and block
+// it loads. The rows of a tile are tokens x query heads of one key head, so that a causal
+// tile covers few tokens and a group's heads share their keys' loads. For each tile and block
 //   S = Q K^T     128 x 128 into tensor memory (tcgen05.mma, both operands in shared memory)
 //   P = 2^(S c - m c)   a thread for each row: running maximum m and sum l in registers
 //   O += P V      P from tensor memory, where it takes S's place; V as it lies, MN-major
@@ -13,8 +12,18 @@
 // 2^8 (the weights stay below that, in bf16 and in the sums' fp32), which after the first
 // blocks is rare. P is rounded to bf16, as V is; l adds the unrounded weights.
 //
+// Bound: the products, 1024 cycles of the tensor core for a tile and block of 128 channels.
+// Alone, a CTA's ring of five keys' or values' tiles (160 KB beside 64 KB of queries) is
+// short for what a load takes; a pair of CTAs (cta_group::2) makes each product 256 rows
+// wide, each CTA holds half of the keys (rows) and of the values (channels), and the ring
+// lasts twice as long. One 8192-token prompt, 32 heads of 128 on 8: 312 us, 1.76 PFLOP/s,
+// 93 % of the rate of a large matrix product; single CTAs 335.
+//
 // Roles: warps 0-3 and 4-7 the rows of the two tiles (200 registers a thread: a row's 128
-// scores are held at once), warp 8 issues the products, warp 9 the TMA loads.
+// scores are held at once), warp 8 issues the products (in a pair the first CTA's, for
+// both), warp 9 the TMA loads, warp 10 writes zeros behind the last key, warp 11 finds
+// what comes next. A CTA goes on with the places of CTAs that have not started (launch
+// control answers which), so that its start and the ends of its items overlap.
 //
 // What a row does not see must not reach it: its scores are replaced before the maximum,
 // and the places behind a sequence's last key in the last block of V are zeroed in shared
@@ -867,12 +876,14 @@ template <bool PAGED>
 cudaError_t launch_width(const Params& p, cudaStream_t s) {
   const kda_attn_fwd_args& a = p.a;
   if (a.D == 64) return launch<64, PAGED, 1>(p, s);
-  // Pairs of CTAs, each of which holds half of the keys and values, where there are four
-  // rounds of them on the 76 pairs of SMs and sequences of two tiles or more (4 x 512 tokens
-  // on 6512 keys, 128 pairs' work: 158 us with pairs, 149 without).
+  // Pairs of CTAs, each of which holds half of the keys and values, where there are two
+  // rounds of them on the 76 pairs of SMs and sequences fill a tile on the average (32 heads
+  // of 128 on 8: 64 prompts of up to 512 tokens 116 us with pairs, 130 without; 128 of 256
+  // 177 and 207; 512 of 64 312 and 195; 4 x 512 tokens on 6512 keys, 128 pairs' work, 158
+  // and 149).
   const int tokens = 4 * p.tile_tokens;
   const long long each = a.cu_seqlens ? static_cast<long long>(a.T) / a.N : a.T, items = static_cast<long long>(a.B) * a.T / tokens * p.heads;
-  if (p.parts.o == nullptr && each >= 2 * tokens && items >= 4 * 76) return launch<128, PAGED, 2>(p, s);
+  if (p.parts.o == nullptr && each >= tokens && items >= 2 * 76) return launch<128, PAGED, 2>(p, s);
   return launch<128, PAGED, 1>(p, s);
 }
 
