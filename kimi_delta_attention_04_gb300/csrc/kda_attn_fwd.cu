@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.o_full[m], 1);
     }
     for (int s = 0; s < Sh::kStages; ++s) {
-      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.full[s], PAGED ? CTAS : 1);
       mbar_init(&sm.empty[s], 1);
     }
     mbar_init(&sm.tail_there, 1);
@@ -505,27 +505,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t bad = 0;
             if (PAGED) {
               // a page that is out of range, or behind the last key, reads as zeros
+              const int32_t* table = a.block_table + static_cast<long long>(it.n) * a.table_width;
               int page = -1;
               if (lane < boxes && tok < it.S) {
-                page = a.block_table[static_cast<long long>(it.n) * a.table_width + tok / a.page_size];
+                page = table[tok / a.page_size];
                 if (page >= a.pages) page = -1;
               }
               y = tok % a.page_size;
               z = page < 0 ? -1 : page * a.HKV + it.hk;
-              bad = __ballot_sync(0xffffffffu, lane < boxes && tok < it.S && page < 0);
-              if (bad != 0) {
-                if (lane == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
-                // a bit for each box to one for each 16 keys
-                bad = __ballot_sync(0xffffffffu, lane < 8 && (bad >> (lane * 16 / keys * parts) & 1u));
+              if (kv == 0) {  // a bit for each 16 of the block's keys, those of the pair's other CTA among them
+                if (CTAS == 1) {
+                  bad = __ballot_sync(0xffffffffu, lane < boxes && tok < it.S && page < 0);
+                  if (bad != 0) bad = __ballot_sync(0xffffffffu, lane < 8 && (bad >> (lane * 16 / keys * parts) & 1u));
+                } else {
+                  const int at = j * kRows + 16 * lane;
+                  const bool there = lane < 8 && at < it.S;
+                  if (there) page = table[at / a.page_size];
+                  bad = __ballot_sync(0xffffffffu, there && (page < 0 || page >= a.pages));
+                }
+                if (bad != 0 && lane == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
               }
             }
             const int s = loaded % Sh::kStages;
             if (loaded >= Sh::kStages) going = __all_sync(0xffffffffu, wait(&sm.empty[s], (loaded / Sh::kStages - 1) & 1));
             if (!going) break;
             if (lane == 0) {
-              // (the values', of all keys; the loads are at most 5 blocks ahead of the weights, which read this)
-              if (PAGED && kv == 1) sm.bad[(blocks_done + j - it.first) & 7] = bad;
+              // (before the keys' arrival, and so before their scores; the loads are at most 5
+              // blocks ahead of the weights, which read this)
+              if (PAGED && kv == 0) sm.bad[(blocks_done + j - it.first) & 7] = bad;
               if (rank == 0) mbar_arrive_expect_tx_local(&sm.full[s], CTAS * Sh::kTile);
+              else if (PAGED) arrive_first<CTAS>(&sm.full[s]);
             }
             __syncwarp();
             if (lane < boxes)

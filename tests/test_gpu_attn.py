@@ -405,6 +405,29 @@ def test_prompts_leave_out_bad_pages():
     assert (o == 0).all() and torch.isinf(lse).all()
 
 
+@pytest.mark.parametrize("P", [16, 64, 128])
+def test_prompts_leave_out_bad_pages_of_many_tiles(P):
+    """Where two CTAs hold half of a block's keys each: pages of one half, of the other, of
+    both, and of the last blocks, which are not full."""
+    gen = torch.Generator().manual_seed(16)
+    T, HQ, HKV, D = 2500, 64, 4, 128
+    q, k, v = randn(gen, 1, T, HQ, D), randn(gen, T, HKV, D), randn(gen, T, HKV, D)
+    cache = Cache(gen, [k], [v], P)
+    gone = [t // P for t in (0, 200, 330, 640, 767, 1500, 2499)]
+    cache.table[0, gone] = torch.tensor([-1, len(cache.k), 2 ** 31 - 1, -2 ** 31, len(cache.k), -7, -1], dtype=torch.int32)
+    cache.cuda()
+    err = err_word()
+    o = kda.kda_attn_fwd(q.cuda(), cache.k, cache.v, scale=0.09, block_table=cache.table, seq_lens_k=cache.lens, err=err)
+    assert int(err) == 1
+    for i in (0, 17, 129, 255, 256, 400, 700, 801, 1024, 1600, 2047, 2490, 2499):
+        keys = [j for j in range(i + 1) if j // P not in gone]
+        if not keys:
+            assert (o[0, i] == 0).all()
+            continue
+        refs = ao.attend(np64(q[0, i:i + 1]), np64(k[keys]), np64(v[keys]), float(np.float32(0.09)), [len(keys)])
+        check(o[0, i:i + 1], None, refs, T, D)
+
+
 # --- the single-token step ---
 
 def run_step(gen, lens, HQ, HKV, D, P, dtype, prefix=0, spread=1.0, width=None):
