@@ -545,18 +545,22 @@ kda_status kda_scan_step(const kda_scan_step_args* args, kda_stream_t stream);
  * The cache. k_cache and v_cache are [pages, HKV, page_size, D], contiguous and
  * 16-byte aligned, bf16 or e4m3; page_size is 16, 32, 64 or 128. Token t of a
  * sequence lies at place t % page_size of page table[t / page_size] of the
- * sequence's row of an int32 table (entries behind its last page are not read).
+ * sequence's row of an int32 table (entries behind its last page are not used).
  * With e4m3, k_scale and v_scale, fp32 [pages, HKV, page_size], hold a factor for
- * each token and head (value ~ stored * scale); kda_kv_append writes powers of two.
+ * each token and head (value ~ stored * scale): above 0, or NaN. kda_kv_append writes
+ * powers of two; with others a prefix's keys and values are rounded to bf16.
  * A page index outside 0 .. pages - 1 writes KDA_ERR_INVALID_ARG to err, and the
  * tokens on it are left out.
  *
  * Heads: query head h uses key head h / (HQ / HKV); HQ is a multiple of HKV and at most
- * KDA_ATTN_MAX_HEADS (KDA_ERR_UNSUPPORTED above). D is 64 or 128. Rows of q, k, v and outputs (a token's heads, contiguous) start on
- * 16-byte boundaries; their strides are in elements.
+ * KDA_ATTN_MAX_HEADS (KDA_ERR_UNSUPPORTED above). D is 64 or 128. Rows of q, k, v and
+ * outputs (a token's heads, contiguous) start on 16-byte boundaries; their strides are in
+ * elements.
  * ------------------------------------------------------------------------- */
 
 #define KDA_ATTN_MAX_HEADS 1024
+/* Keys of a sequence, or tokens a row of a table has room for (KDA_ERR_UNSUPPORTED above). */
+#define KDA_ATTN_MAX_TOKENS (1 << 29)
 
 /*
  * Rotary positions, and the append to the cache. For every token t with
@@ -627,7 +631,10 @@ kda_status kda_kv_append(const kda_kv_append_args* args, kda_stream_t stream);
  * what stands behind a sequence's last key or in keys a query does not see, infinities
  * and NaN among it, has no effect on that query. o overlaps no input.
  * Products of bf16 on the tensor cores with fp32 sums; softmax in fp32; the weights
- * p are rounded to bf16 for their product with v. scale is finite and > 0.
+ * p are rounded to bf16 for their product with v. scale is finite and > 0. Rows that
+ * infinities or NaN of v, or scores that are not finite, reach are computed again one by
+ * one, at about 100 times the cost. Every wait in the kernel is bounded; one that runs out
+ * (after ten seconds) writes KDA_ERR_TIMEOUT to err and ends the call without its results.
  * Resources: 512 columns of tensor memory on each SM while the kernel runs.
  */
 #define KDA_ATTN_FLAG_CAUSAL 0x1u
@@ -662,8 +669,8 @@ kda_status kda_attn_fwd(const kda_attn_fwd_args* args, kda_stream_t stream);
  *   seq_lens     [B]                 int32; negative = padding row: o = 0, lse = -inf
  *   prefix_table [prefix_pages]      int32, NULL without a prefix
  * A row without any token gives o = 0, lse = -inf. A length above table_width *
- * page_size writes KDA_ERR_INVALID_ARG to err and makes the row a padding row.
- * o does not overlap q.
+ * page_size writes KDA_ERR_INVALID_ARG to err and makes the row a padding row. The prefix
+ * runs on kda_attn_fwd's kernel (its resources, and KDA_ERR_TIMEOUT). o does not overlap q.
  */
 typedef struct kda_attn_step_args {
   int32_t B, HQ, HKV, D;

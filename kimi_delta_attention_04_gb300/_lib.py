@@ -44,6 +44,7 @@ KDA_KV_FLAG_INTERLEAVED = 0x1
 KDA_ATTN_FLAG_CAUSAL = 0x1
 KDA_ATTN_MAX_HEADS = 1024
 KDA_ATTN_LONG_TOKENS = 16384
+KDA_ATTN_MAX_TOKENS = 1 << 29
 
 
 class KdaError(RuntimeError):

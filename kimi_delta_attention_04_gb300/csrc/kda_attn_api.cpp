@@ -47,6 +47,10 @@ kda_status check_cache(int32_t pages, int32_t page_size, int32_t HKV, int32_t dt
   return aligned(ks, 16) && aligned(vs, 16) ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
 
+// Tokens that a table has room for. At this limit counts of tokens past the last one stay
+// below 2^31, and a prompt kernel's longest wait, for an item's whole work, below ten seconds.
+bool room_ok(int32_t width, int32_t page_size) { return static_cast<int64_t>(width) * page_size <= KDA_ATTN_MAX_TOKENS; }
+
 // An output in place of an input: the same rows, or none of them.
 bool place_ok(const void* out, int64_t out_stride, const void* in, int64_t in_stride, int64_t rows) {
   return out != in || out_stride == in_stride || rows <= 1;
@@ -62,12 +66,12 @@ kda_status check_step(const kda_attn_step_args* a) {
   st = check_cache(a->pages, a->page_size, a->HKV, a->cache_dtype, a->k_cache, a->v_cache, a->k_scale, a->v_scale);
   if (st != KDA_OK) return st;
   if (!aligned(a->err, 4) || !aligned(a->lse, 4)) return KDA_ERR_INVALID_ARG;
+  if (!room_ok(a->table_width, a->page_size) || a->prefix_len > KDA_ATTN_MAX_TOKENS) return KDA_ERR_UNSUPPORTED;
   if (a->B == 0) return KDA_OK;
   const int64_t cols = static_cast<int64_t>(a->HQ) * a->D;
   if (!rows_ok(a->q, a->B, cols, a->q_stride) || !rows_ok(a->o, a->B, cols, a->o_stride) || a->o == a->q) return KDA_ERR_INVALID_ARG;
   if (a->seq_lens == nullptr || !aligned(a->seq_lens, 4) || !aligned(a->block_table, 4)) return KDA_ERR_INVALID_ARG;
   if (a->table_width > 0 && a->block_table == nullptr) return KDA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(a->table_width) * a->page_size > INT32_MAX) return KDA_ERR_INVALID_ARG;
   if (a->prefix_len > 0) {
     if (a->prefix_table == nullptr || !aligned(a->prefix_table, 4)) return KDA_ERR_INVALID_ARG;
     if (static_cast<int64_t>(a->prefix_pages) * a->page_size < a->prefix_len) return KDA_ERR_INVALID_ARG;
@@ -122,12 +126,14 @@ kda_status kda_attn_fwd(const kda_attn_fwd_args* a, kda_stream_t stream) {
     return KDA_ERR_INVALID_ARG;
   const int64_t queries = static_cast<int64_t>(a->B) * a->T, keys = static_cast<int64_t>(a->B) * a->S;
   if (queries > INT32_MAX / 2 || (!paged && keys > INT32_MAX / 2)) return KDA_ERR_INVALID_ARG;
+  if (!paged && a->S > KDA_ATTN_MAX_TOKENS) return KDA_ERR_UNSUPPORTED;
   if (packed && !paged && a->cu_seqlens_k == nullptr && a->S != a->T) return KDA_ERR_INVALID_ARG;
   const int64_t qn = static_cast<int64_t>(a->HQ) * a->D, kv = static_cast<int64_t>(a->HKV) * a->D;
   if (paged) {
     st = check_cache(a->pages, a->page_size, a->HKV, KDA_DTYPE_BF16, a->k, a->v, nullptr, nullptr);
     if (st != KDA_OK) return st;
-    if (a->table_width < 0 || static_cast<int64_t>(a->table_width) * a->page_size > INT32_MAX) return KDA_ERR_INVALID_ARG;
+    if (a->table_width < 0) return KDA_ERR_INVALID_ARG;
+    if (!room_ok(a->table_width, a->page_size)) return KDA_ERR_UNSUPPORTED;
   }
   if (queries == 0) return KDA_OK;
   if (!rows_ok(a->q, queries, qn, a->q_stride) || !rows_ok(a->o, queries, qn, a->o_stride) || a->o == a->q) return KDA_ERR_INVALID_ARG;

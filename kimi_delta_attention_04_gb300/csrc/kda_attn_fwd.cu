@@ -547,10 +547,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_local(&sm.item_empty[k & 1]);
       }
       // every tile and stage has been used up: no copy and no arrival is left under way when
-      // the CTA ends
+      // the CTA ends (after a wait that ran out: the copies have come, those of a pair both
+      // counted in its first CTA, and neither CTA ends before the other)
+      bool idle = going;
       for (int m = 0; m < 2; ++m)
-        if (tiles_done[m] > 0) going &= wait(&sm.q_empty[m], (tiles_done[m] - 1) & 1);
-      for (int i = max(0, loaded - Sh::kStages); i < loaded; ++i) going &= wait(&sm.empty[i % Sh::kStages], (i / Sh::kStages) & 1);
+        if (idle && tiles_done[m] > 0) idle = wait(&sm.q_empty[m], (tiles_done[m] - 1) & 1);
+      for (int i = max(0, loaded - Sh::kStages); i < loaded && idle; ++i) idle = wait(&sm.empty[i % Sh::kStages], (i / Sh::kStages) & 1);
+      if (!idle && rank == 0) {
+        bool there = true;
+        for (int m = 0; m < 2; ++m)
+          if (there && tiles_done[m] > 0) there = wait(&sm.q_full[m], (tiles_done[m] - 1) & 1);
+        for (int i = max(0, loaded - Sh::kStages); i < loaded && there; ++i) there = wait(&sm.full[i % Sh::kStages], (i / Sh::kStages) & 1);
+      }
+      going = idle;
       if (!going) sm.failed = 1;
     } else if (warp == 8) {
       if (rank == 0 && elect_one() && !issue_products<D, CTAS>(sm, tiles)) sm.failed = 1;

@@ -671,7 +671,6 @@ cudaError_t launch_prefix(const kda_attn_step_args& a, const Plan& x, unsigned c
   f.q = a.q, f.q_stride = a.q_stride, f.err = a.err;
   f.pages = a.pages, f.k = a.k_cache, f.v = a.v_cache, f.block_table = a.prefix_table;
   if (a.cache_dtype == KDA_DTYPE_E4M3) {
-    if (a.HKV > 65535) return cudaErrorNotSupported;
     __nv_bfloat16 *k = reinterpret_cast<__nv_bfloat16*>(w + x.k), *v = reinterpret_cast<__nv_bfloat16*>(w + x.v);
     int32_t* table = reinterpret_cast<int32_t*>(w + x.table);
     const dim3 grid(static_cast<unsigned>(x.prefix_pages), static_cast<unsigned>(a.HKV));

@@ -44,12 +44,12 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t smem_addr, uint32_t lbo_b
 
 // Instruction descriptor of kind::f16 with fp32 accumulation and K-major A and
 // B: bits 4-5 D format (1 = f32), 7-9 A format and 10-12 B format (0 = f16,
-// 1 = bf16), 17-22 N / 8, 24-28 M / 16.
-constexpr uint32_t kIdescBMnMajor = 1u << 16;  // B is MN-major (bit 15: A)
+// 1 = bf16), 15 and 16 A and B MN-major instead, 17-22 N / 8, 24-28 M / 16.
 __host__ __device__ constexpr uint32_t idesc_f16kind(int M, int N, bool bf16) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
+constexpr uint32_t kIdescBMnMajor = 1u << 16;  // added to it: B is MN-major
 
 // TMEM allocation: executed by one whole warp; the base address is written to
 // *dst (shared memory). ncols is a power of two, 32 .. 512.

@@ -42,7 +42,7 @@ def test_struct_layouts_match_c(tmp_path):
         for f, _ in st._fields_:
             lines.append(f'printf("{name}.{f} %zu\\n", offsetof({name}, {f}));')
             want[f"{name}.{f}"] = getattr(st, f).offset
-    for const in ("KDA_KV_FLAG_INTERLEAVED", "KDA_ATTN_FLAG_CAUSAL", "KDA_ATTN_MAX_HEADS", "KDA_ATTN_LONG_TOKENS"):
+    for const in ("KDA_KV_FLAG_INTERLEAVED", "KDA_ATTN_FLAG_CAUSAL", "KDA_ATTN_MAX_HEADS", "KDA_ATTN_LONG_TOKENS", "KDA_ATTN_MAX_TOKENS"):
         lines.append(f'printf("{const} %zu\\n", (size_t){const});')
         want[const] = getattr(_lib, const)
     src, exe = tmp_path / "layout.c", tmp_path / "layout"
@@ -110,9 +110,9 @@ PAGED = dict(block_table=FAKE, seq_lens_k=FAKE, pages=4, page_size=16, table_wid
     (PACKED | dict(S=9), INVALID),                                   # other keys, and no array for them
     (PACKED | dict(cu_seqlens_k=FAKE + 1, S=9), INVALID), (PACKED | PAGED | dict(cu_seqlens_k=FAKE), INVALID),
     (PAGED | dict(seq_lens_k=None), INVALID), (dict(seq_lens_k=FAKE), INVALID), (PAGED | dict(page_size=8), UNSUPPORTED),
-    (PAGED | dict(table_width=-1), INVALID), (PAGED | dict(table_width=2 ** 28), INVALID), (PAGED | dict(k=None), INVALID),
+    (PAGED | dict(table_width=-1), INVALID), (PAGED | dict(table_width=2 ** 25 + 1), UNSUPPORTED), (PAGED | dict(table_width=2 ** 31 - 1), UNSUPPORTED), (PAGED | dict(k=None), INVALID),
     (PAGED | dict(pages=-1), INVALID), (dict(lse=FAKE + 2), INVALID), (dict(err=FAKE + 1), INVALID),
-    (dict(T=2 ** 30, S=2 ** 30), INVALID), (dict(q_stride=2 ** 39), INVALID), (dict(o=FAKE), INVALID),
+    (dict(T=2 ** 30, S=2 ** 30), INVALID), (dict(B=1, N=1, S=2 ** 29 + 1), UNSUPPORTED), (dict(q_stride=2 ** 39), INVALID), (dict(o=FAKE), INVALID),
 ])
 def test_fwd_refuses(lib, over, status):
     assert lib.kda_attn_fwd(ctypes.byref(_fwd(**over)), None) == status
@@ -137,7 +137,8 @@ PREFIX = dict(prefix_len=33, prefix_pages=2, prefix_table=FAKE)
     (dict(cache_dtype=FP32), UNSUPPORTED), (dict(cache_dtype=E4M3), INVALID), (dict(k_cache=None), INVALID), (dict(v_cache=FAKE + 2), INVALID),
     (dict(page_size=20), UNSUPPORTED), (dict(q=None), INVALID), (dict(o=FAKE + 8), INVALID), (dict(q_stride=511), INVALID),
     (dict(o_stride=516), INVALID), (dict(block_table=None), INVALID), (dict(block_table=FAKE + 2), INVALID), (dict(seq_lens=None), INVALID),
-    (dict(seq_lens=FAKE + 1), INVALID), (dict(table_width=2 ** 27), INVALID), (dict(prefix_len=-1), INVALID), (dict(lse=FAKE + 1), INVALID),
+    (dict(seq_lens=FAKE + 1), INVALID), (dict(table_width=2 ** 27), UNSUPPORTED), (dict(table_width=2 ** 31 - 1), UNSUPPORTED), (dict(prefix_len=-1), INVALID),
+    (PREFIX | dict(prefix_len=2 ** 29 + 1, prefix_pages=2 ** 30), UNSUPPORTED), (dict(lse=FAKE + 1), INVALID),
     (dict(o=FAKE), INVALID), (PREFIX, INVALID),                      # no workspace
     (PREFIX | dict(prefix_table=None), INVALID), (PREFIX | dict(prefix_len=65), INVALID), (PREFIX | dict(prefix_table=FAKE + 2), INVALID),
     (dict(table_width=1024), INVALID),                               # few rows on long tables: no workspace
