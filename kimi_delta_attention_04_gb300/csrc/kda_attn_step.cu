@@ -34,7 +34,7 @@ struct Params {
   const float* part_o;    // [parts, B, HQ, D]: results to join, normalised: the clusters' where a
   const float* part_lse;  // row has several, and the prefix's; [parts, B, HQ], in powers of two
   int parts;
-  float* own_o;           // the clusters' part of them
+  float* own_o;           // the clusters' part of them; nullptr: the one cluster of a row writes o
   float* own_lse;
 };
 
@@ -489,9 +489,9 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
   if (p.splits > 1) cluster_sync_all();
   else __syncthreads();
 
-  // the splits' results and the prefix's, in order (the prefix's kernel may still have been
-  // running beside this one's loop)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the splits' results and the prefix's, in order (the prefix's kernel may still be running;
+  // where another launch joins the results, one CTA waits for it and the others make room)
+  if (p.own_o == nullptr || blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int u = in_cluster * kThreads + tid; u < heads * Q; u += p.splits * kThreads) {
     const int r = u / Q, d = 4 * (u % Q), head = head0 + r;
     Joined j;
@@ -506,8 +506,7 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
       any = cta_used;
       j.add(cta_m[r], cta_l[r], *reinterpret_cast<const float4*>(cta_o(r, d)));
     }
-    if (p.chunks > 1) {
-      // one of several clusters on the row: kda_attn_join_kernel takes their results together
+    if (p.own_o != nullptr) {  // kda_attn_join_kernel takes the results together
       const long long at = (static_cast<long long>(rank / p.splits) * a.B + b) * a.HQ + head;
       const float inv = any ? 1.f / j.l : 0.f;
       *reinterpret_cast<float4*>(p.own_o + at * D + d) = make_float4(j.o.x * inv, j.o.y * inv, j.o.z * inv, j.o.w * inv);
@@ -557,6 +556,7 @@ struct Plan {
   int splits = 1, chunks = 1, parts = 0;  // of the rows' own tokens; all results to join
   int prefix_splits = 0, prefix_pages = 0;
   int warps = 4;                          // to a CTA: 2, 4 or 8
+  bool join = false;                      // a launch of its own joins the results
   size_t lse = 0, o = 0, table = 0, k = 0, v = 0, bytes = 0;
 };
 
@@ -624,6 +624,7 @@ Plan plan_of(const kda_attn_step_args& a) {
   if (units * x.splits <= 152 && room >= KDA_ATTN_LONG_TOKENS) {
     const long long fill = 2 * 152 / (units * x.splits), each = room / (512 * x.splits);
     x.chunks = static_cast<int>(fill < each ? fill : each);
+    x.join = x.chunks > 1;
   }
   // Many CTAs: two warps each, four of them on an SM, so that one's start and end pass under
   // the others' loads (256 rows of up to 500 tokens with a prefix: 94 -> 89 us; with 8-bit
@@ -632,22 +633,35 @@ Plan plan_of(const kda_attn_step_args& a) {
   if (ctas >= 4 * 152 && !e4) x.warps = 2;
   if (ctas <= 152 && room >= 128ll * x.splits * x.chunks) x.warps = 8;
   if (a.prefix_len > 0) {
-    // Splits that keep the SMs busy: rounds of CTAs, each with its share of the blocks and
-    // 4 blocks' time for what a CTA does besides.
+    // The prefix's splits, by what they leave to the rows' own tokens, in units of a block's
+    // time on an SM (1.17 us): rounds of CTAs, each with its share of the blocks and 5 blocks'
+    // time for what a CTA does besides; own CTAs run on the SMs that these leave free, for half
+    // of the tokens that the table has room for and 6 units besides. Unless all fit at once,
+    // own CTAs must not wait for the prefix, which would keep the next ones out, and a
+    // launch joins the results. (256 rows, 32 heads on 8, prefix 8192, up to 500 own tokens: 2
+    // splits on 64 SMs 73 us, 4 splits on 128 SMs 87, and 89 with CTAs that wait; 32 rows 27
+    // and 38; 8 rows of up to 64 tokens, prefix 512, which fit, 10.8, and 12.4 with a join.)
     const AttnTiles t = attn_tiles(G);
     const long long tiles = (static_cast<long long>(a.B) + t.tokens - 1) / t.tokens * a.HKV * (G / t.heads);
     const int blocks = (a.prefix_len - 1) / 128 + 1;
-    long long best = 0;
+    const double own = static_cast<double>(units) * room / 2 * (2 * a.D * (e4 ? 1 : 2)) / 7e6 + 6;
+    const long long own_sms = (ctas * x.warps + 7) / 8;
+    double best = 0;
     for (int s = 1; s <= 32 && s <= blocks; ++s) {
-      const long long cost = (tiles * s + 151) / 152 * ((blocks + s - 1) / s + 4);
+      const long long n = tiles * s;
+      const double prefix = static_cast<double>((n + 151) / 152) * ((blocks + s - 1) / s + 5);
+      const bool fits = n + own_sms <= 152;
+      const double beside = n < 152 ? prefix * (152 - n) / 152 * 1.2 : 0;
+      const double cost = fits ? prefix : prefix + (own > beside ? own - beside : 0) + 2;
       if (x.prefix_splits == 0 || cost < best) {
         x.prefix_splits = s;
+        x.join = x.chunks > 1 || !fits;
         best = cost;
       }
     }
     x.prefix_pages = (a.prefix_len - 1) / a.page_size + 1;
   }
-  x.parts = (x.chunks > 1 ? x.chunks : 0) + x.prefix_splits;
+  x.parts = (x.join ? x.chunks : 0) + x.prefix_splits;
   const size_t rows = static_cast<size_t>(a.B) * a.HQ * x.parts;
   const auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
   x.o = up(rows * sizeof(float));
@@ -691,8 +705,8 @@ cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaS
   const Plan x = plan_of(a);
   unsigned char* w = static_cast<unsigned char*>(workspace);
   float *o = reinterpret_cast<float*>(w + x.o), *lse = reinterpret_cast<float*>(w + x.lse);
-  const Params p = {a, a.HQ / a.HKV, (a.HQ / a.HKV + 15) / 16, __builtin_ctz(a.page_size), x.splits, x.chunks, o, lse, x.parts, o, lse};
-  const size_t own = x.chunks > 1 ? static_cast<size_t>(x.chunks) * a.B * a.HQ : 0;  // the prefix's results come behind these
+  const Params p = {a, a.HQ / a.HKV, (a.HQ / a.HKV + 15) / 16, __builtin_ctz(a.page_size), x.splits, x.chunks, o, lse, x.parts, x.join ? o : nullptr, lse};
+  const size_t own = x.join ? static_cast<size_t>(x.chunks) * a.B * a.HQ : 0;  // the prefix's results come behind these
   if (x.prefix_splits > 0) {
     const cudaError_t e = launch_prefix(a, x, w, AttnParts{o + own * a.D, lse + own, x.prefix_splits, a.prefix_len}, s);
     if (e != cudaSuccess) return e;
@@ -700,7 +714,7 @@ cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaS
   const bool e4 = a.cache_dtype == KDA_DTYPE_E4M3;
   const cudaError_t e = a.D == 64 ? (e4 ? launch_warps<64, true>(p, x, s) : launch_warps<64, false>(p, x, s))
                                   : (e4 ? launch_warps<128, true>(p, x, s) : launch_warps<128, false>(p, x, s));
-  if (e != cudaSuccess || x.chunks == 1) return e;
+  if (e != cudaSuccess || !x.join) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(a.B) * a.HQ * (a.D / 4) + 127) / 128));
   cfg.blockDim = dim3(128);
