@@ -38,15 +38,16 @@ struct Params {
   float* own_lse;
 };
 
-template <int D, bool E4, int WARPS>
+template <int D, bool E4, int WARPS, bool MANY>
 struct Shape {
   static constexpr int kRow = D * (E4 ? 1 : 2);                        // bytes of a token
   // Groups of a warp's step: two of 8-bit tokens (the same bytes as one of bf16; with one,
-  // what a step costs besides its products kept 256 rows of 2000 tokens at 262 us).
-  static constexpr int kSub = E4 ? 2 : 1;
+  // what a step costs besides its products kept 256 rows of 2000 tokens at 262 us). MANY: one,
+  // so that three CTAs fit an SM (plan_of).
+  static constexpr int kSub = E4 && !MANY ? 2 : 1;
   static constexpr int kTokens = kSub * kGroup;
   static constexpr int kStage = 2 * kTokens * kRow + (E4 ? 8 * kTokens : 0);  // keys, values, scales of both
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = D == 128 ? (MANY ? 4 : 3) : 6;
   static constexpr int kResult = (D + 4) * 64 + 16 / WARPS * D * 4;  // a warp's result, and rows of the CTA's
   static constexpr int kWarpBytes = kStages * kStage > kResult ? kStages * kStage : kResult;
   static constexpr int kSmem = WARPS * kWarpBytes;
@@ -161,9 +162,9 @@ __global__ void __launch_bounds__(128) kda_attn_join_kernel(const __grid_constan
   store_row<D>(p.a, b, head, d, j, any);
 }
 
-template <int D, bool E4, int WARPS, int ROWS>
-__global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_constant__ Params p) {
-  using Sh = Shape<D, E4, WARPS>;
+template <int D, bool E4, int WARPS, bool MANY, int ROWS>
+__global__ void __launch_bounds__(32 * WARPS, MANY ? 3 : 1) kda_attn_step_kernel(const __grid_constant__ Params p) {
+  using Sh = Shape<D, E4, WARPS, MANY>;
   constexpr int kThreads = 32 * WARPS;
   extern __shared__ __align__(128) unsigned char raw[];
   __shared__ float cta_m[16], cta_l[16];
@@ -519,11 +520,11 @@ __global__ void __launch_bounds__(32 * WARPS) kda_attn_step_kernel(const __grid_
   if (p.splits > 1) cluster_sync_all();  // no CTA ends while another may read its results
 }
 
-template <int D, bool E4, int WARPS, int ROWS>
+template <int D, bool E4, int WARPS, bool MANY, int ROWS>
 cudaError_t launch(const Params& p, bool after_prefix, cudaStream_t s) {
-  using Sh = Shape<D, E4, WARPS>;
+  using Sh = Shape<D, E4, WARPS, MANY>;
   static std::atomic<uint64_t> smem_set{0};
-  auto kernel = kda_attn_step_kernel<D, E4, WARPS, ROWS>;
+  auto kernel = kda_attn_step_kernel<D, E4, WARPS, MANY, ROWS>;
   cudaError_t e = set_smem_limit_once(kernel, Sh::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(p.a.B) * p.a.HKV * p.head_tiles * p.splits * p.chunks;
@@ -556,6 +557,7 @@ struct Plan {
   int splits = 1, chunks = 1, parts = 0;  // of the rows' own tokens; all results to join
   int prefix_splits = 0, prefix_pages = 0;
   int warps = 4;                          // to a CTA: 2, 4 or 8
+  bool many = false;                      // CTAs: more of them on an SM
   bool join = false;                      // a launch of its own joins the results
   size_t lse = 0, o = 0, table = 0, k = 0, v = 0, bytes = 0;
 };
@@ -563,11 +565,13 @@ struct Plan {
 template <int D, bool E4, int ROWS>
 cudaError_t launch_rows(const Params& p, const Plan& x, cudaStream_t s) {
   const bool after = x.prefix_splits > 0;
-  if (x.warps == 8) return launch<D, E4, 8, ROWS>(p, after, s);
-  if constexpr (!E4) {
-    if (x.warps == 2) return launch<D, E4, 2, ROWS>(p, after, s);
+  if (x.warps == 8) return launch<D, E4, 8, false, ROWS>(p, after, s);
+  if constexpr (E4) {
+    if (x.many) return launch<D, E4, 4, true, ROWS>(p, after, s);
+  } else {
+    if (x.many) return launch<D, E4, 2, false, ROWS>(p, after, s);
   }
-  return launch<D, E4, 4, ROWS>(p, after, s);
+  return launch<D, E4, 4, false, ROWS>(p, after, s);
 }
 
 // (A lane's scores are of heads g and g + 8: with up to 8 heads the second half is nothing.)
@@ -626,11 +630,15 @@ Plan plan_of(const kda_attn_step_args& a) {
     x.chunks = static_cast<int>(fill < each ? fill : each);
     x.join = x.chunks > 1;
   }
-  // Many CTAs: two warps each, four of them on an SM, so that one's start and end pass under
-  // the others' loads (256 rows of up to 500 tokens with a prefix: 94 -> 89 us; with 8-bit
-  // keys, whose products take longer, 197 -> 203, so not there). Few: eight warps.
+  // Many CTAs: more and smaller ones on an SM, so that one's start and end pass under the
+  // others' loads. bf16: four of two warps (256 rows of up to 500 tokens with a prefix: 94 ->
+  // 89 us). 8 bits, whose products take longer: three of four warps, one group a step (256 rows
+  // of about 2000: 198 -> 192; of 64 channels 147 -> 125; two warps each 208). Not where they
+  // are few (16 rows of 2000 to 4000, 512 CTAs: 33 -> 37; 4 of 32768 to 65536: 94 -> 113).
+  // Few: eight warps.
   const long long ctas = units * x.splits * x.chunks;
-  if (ctas >= 4 * 152 && !e4) x.warps = 2;
+  x.many = ctas >= 4 * 152;
+  if (x.many && !e4) x.warps = 2;
   if (ctas <= 152 && room >= 128ll * x.splits * x.chunks) x.warps = 8;
   if (a.prefix_len > 0) {
     // The prefix's splits, by what they leave to the rows' own tokens, in units of a block's

@@ -495,6 +495,16 @@ def test_step_prefix_many_rows():
     run_step(gen, [int(n) for n in torch.randint(0, 40, (150,), generator=gen)], 4, 2, 64, 16, BF, prefix=333)
 
 
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("prefix", [0, 40])
+@pytest.mark.parametrize("HQ,HKV,D,P", [(8, 4, 128, 16), (40, 4, 64, 32)])
+def test_step_many_rows(dtype, prefix, HQ, HKV, D, P):
+    """More CTAs than three rounds of the SMs take: smaller ones, and results that a launch joins."""
+    gen = torch.Generator().manual_seed(HQ + prefix)
+    lens = [int(x) for x in torch.randint(1, 70, (156,), generator=gen)]
+    run_step(gen, lens + [0, -3, 1, 300], HQ, HKV, D, P, dtype, prefix=prefix)
+
+
 def test_step_equals_the_last_prompt_row():
     """The last query of a causal prompt and the step on the same cache: the same keys."""
     gen = torch.Generator().manual_seed(22)
