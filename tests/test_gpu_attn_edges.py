@@ -261,3 +261,52 @@ def test_python_refusals():
             (kda.KdaError, lambda: kda.kda_attn_step(q[0, :1], z(4, 2, 8, 64), z(4, 2, 8, 64), table, lens, scale=1.0))):
         with pytest.raises(error):
             call()
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_results_that_wait_for_a_long_prefix(dtype):
+    """Rows whose own tokens are done long before the prefix: run again and again, and captured,
+    on workspaces that held other results; every time the same, and right."""
+    gen = torch.Generator().manual_seed(31)
+    B, HQ, HKV, D, P, prefix, pages = 160, 16, 4, 128, 64, 20000, 330
+    own = [int(n) for n in torch.randint(1, 60, (B,), generator=gen)]
+    kv = [randn(gen, pages, HKV, P, D) for _ in range(2)]
+    scales = [None, None]
+    stored = [np64(x) for x in kv]
+    if dtype == E4:
+        kv, scales = (list(x) for x in zip(*(quantised(x) for x in kv)))
+        stored = [np64(x.float()) * np64(s)[..., None] for x, s in zip(kv, scales)]
+    kc, vc = (x.cuda() for x in kv)
+    ks, vs = (None if s is None else s.cuda() for s in scales)
+    pre = torch.randperm(pages, generator=gen)[:-(-prefix // P)]
+    rows = torch.randint(0, pages, (B, 1), generator=gen)
+    lens = i32(own)
+    q = randn(gen, B, HQ, D).cuda()
+    call = dict(scale=0.09, k_scale=ks, v_scale=vs, prefix_table=pre.int().cuda(), prefix_len=prefix)
+    table = rows.int().cuda()
+
+    def step(lse):
+        return kda.kda_attn_step(q, kc, vc, table, lens, lse=lse, **call)
+
+    lse = torch.zeros(B, HQ, device="cuda")
+    first = step(lse)
+    torch.cuda.synchronize()
+    for b in (0, 63, 64, 159):
+        tokens = [np.concatenate([np.concatenate([x[p] for p in pre.tolist()], 1)[:, :prefix], x[int(rows[b])][:, :own[b]]], 1).transpose(1, 0, 2)
+                  for x in stored]
+        refs = ao.attend(np64(q[b:b + 1]), *tokens, float(np.float32(0.09)), [prefix + own[b]])
+        check(first[b:b + 1], lse[b:b + 1], refs, prefix + own[b], D)
+    queries = [q.clone(), randn(gen, B, HQ, D).cuda()]
+    q.copy_(queries[1])
+    second_lse = torch.zeros_like(lse)
+    wanted = [(first, lse), (step(second_lse), second_lse)]
+    graph, held = torch.cuda.CUDAGraph(), torch.zeros_like(lse)
+    with torch.cuda.graph(graph):
+        again = step(held)
+    for i in range(20):
+        q.copy_(queries[i % 2])
+        graph.replay()
+        other = torch.zeros_like(lse)
+        eager = step(other)
+        for o, l in ((again, held), (eager, other)):
+            assert torch.equal(o, wanted[i % 2][0]) and torch.equal(l, wanted[i % 2][1])
