@@ -7,7 +7,9 @@
 // 4 KB of values at D = 128 in bf16) with 16-byte asynchronous copies, several steps
 // ahead, into shared memory of its own, keeps its own running maximum and sum, and no
 // barrier stands in its loop. The warps of a CTA, and the CTAs of a cluster that split
-// a row's tokens between them, join their results at the end, in a fixed order.
+// a row's tokens between them, join their results at the end, in a fixed order. So are, in
+// a workspace, the results of several clusters on a row and of the prefix that all rows
+// share, which the prompt kernel computes beside the rows' own tokens.
 //
 // 8-bit keys and values become f16, exactly; a token's key scale multiplies its scores in
 // fp32, and the logarithm of its value scale is added to the score that its weight for the

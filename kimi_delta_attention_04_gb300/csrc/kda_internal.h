@@ -114,7 +114,7 @@ cudaError_t launch_scan_step(const kda_scan_step_args& a, cudaStream_t s);
 
 cudaError_t launch_kv_append(const kda_kv_append_args& a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const kda_attn_fwd_args& a, cudaStream_t s);
-size_t attn_step_workspace_bytes(const kda_attn_step_args& a);  // the prefix's partial results
+size_t attn_step_workspace_bytes(const kda_attn_step_args& a);  // partial results that are joined, and an 8-bit prefix in bf16
 cudaError_t launch_attn_step(const kda_attn_step_args& a, void* workspace, cudaStream_t s);
 
 // Bytes of one (chunk, head) prep record.
