@@ -671,6 +671,12 @@ kda_status kda_attn_fwd(const kda_attn_fwd_args* args, kda_stream_t stream);
  * A row without any token gives o = 0, lse = -inf. A length above table_width *
  * page_size writes KDA_ERR_INVALID_ARG to err and makes the row a padding row. The prefix
  * runs on kda_attn_fwd's kernel (its resources, and KDA_ERR_TIMEOUT). o does not overlap q.
+ * Sums and softmax in fp32. For their product with v the weights p are rounded to bf16, and for
+ * a row's own tokens in an 8-bit cache, after v's factors, to f16: off by at most 2^-8 of
+ * themselves (2^-11 above 2^-29 of the row's largest), down to 2^-96 of the row's largest weight
+ * times factor; those below 2^-105 of it add nothing. With an 8-bit cache q is rounded to f16 after
+ * a power of two of the head's own: values of q down to 2^-27 of the head's largest are exact, those
+ * below 2^-36 lost.
  */
 typedef struct kda_attn_step_args {
   int32_t B, HQ, HKV, D;

@@ -14,7 +14,11 @@
 // 8-bit keys and values become f16, exactly; a token's key scale multiplies its scores in
 // fp32, and the logarithm of its value scale is added to the score that its weight for the
 // product with the values comes from. These weights are rounded to f16, and to bf16 with a
-// bf16 cache; the sum takes unrounded ones.
+// bf16 cache; the sum takes unrounded ones. f16 holds the largest weight times scale at 2^15;
+// tokens more than 2^32 below it have products of their own (a head of zeros has the scale 1,
+// far above others', and sets that maximum though it adds nothing). 256 rows of about 2000
+// tokens: 194 us, as without the look for such tokens; cold caches: 207 us, and 278 where a head
+// of zeros is 40 nats above all others of every row.
 #include "kda_attn.cuh"
 #include "kda_attn_fwd.h"
 #include "kda_cluster.cuh"
@@ -27,6 +31,12 @@ using namespace attn;
 constexpr int kGroup = 16;       // tokens that the products take at once; divides every page
 constexpr int kMaxSplits = 8;    // CTAs of a cluster
 constexpr float kTiny = 1.1754944e-38f;
+// The f16 weights of 8-bit values: 2^kTopWeight is the largest, and down to kWeightBits below it,
+// 2^-17, a rounding is at most 2^-8 (half of f16's smallest step, 2^-24). Smaller ones are taken in
+// kParts - 1 further parts, each kWeightBits wide, the last one open (its roundings grow below
+// 2^-96 of the largest, and nothing is left at 2^-105).
+constexpr float kTopWeight = 15.f;
+constexpr int kWeightBits = 32, kParts = 3;
 
 struct Params {
   kda_attn_step_args a;
@@ -299,7 +309,7 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? 3 : 1) kda_attn_step_kernel
   };
 
   // running maximum and sum of the weights, and, with 8-bit values, the maximum of the
-  // weights times their values' scales, which o is relative to (its own otherwise)
+  // weights times their values' scales, of which o is relative to 2^-kTopWeight (its own otherwise)
   float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, mv[2] = {-INFINITY, -INFINITY};
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -395,7 +405,12 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? 3 : 1) kda_attn_step_kernel
       }
     }
     const float mz[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-    const float mvz[2] = {mv[0] == -INFINITY ? 0.f : mv[0], mv[1] == -INFINITY ? 0.f : mv[1]};
+    const float mvz[2] = {mv[0] == -INFINITY ? 0.f : mv[0] - kTopWeight, mv[1] == -INFINITY ? 0.f : mv[1] - kTopWeight};
+    // by their bits, exponents of weights below the limit and above -inf: from the limit's own
+    // bits (0) up to those of -inf; all other values, NaN among them, come out larger
+    constexpr float kLimit = kTopWeight - kWeightBits;
+    const uint32_t limit = __float_as_uint(kLimit), past = __float_as_uint(-INFINITY) - limit;
+    uint32_t small = past;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
 #pragma unroll
@@ -405,36 +420,68 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? 3 : 1) kda_attn_step_kernel
         float w = ex2_approx(x - mz[e >> 1]);
         w = x == -INFINITY ? 0.f : w < kTiny ? kTiny : w;
         l[e >> 1] += w;
-        sc[n][e] = E4 ? ex2_approx(sd[n][e] - mvz[e >> 1]) : w;
+        if (E4) {
+          const float y = sd[n][e] - mvz[e >> 1];
+          small = min(small, __float_as_uint(y) - limit);
+          w = ex2_approx(y);
+        }
+        sc[n][e] = w;
       }
     }
+    // With weights below the limit: those in f16's reach first, then the next kWeightBits as if they
+    // were and what is summed so far lifted with them (by 2^64 at most, from 2^53: 2^15 * 448 for
+    // 2^29 tokens), and so on. In one loop: a second copy of the products took 40 registers more.
+    const int parts = E4 && __any_sync(0xffffffffu, small < past) ? kParts : 1;
+#pragma unroll 1
+    for (int part = 0;;) {
+      if (E4 && parts > 1) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t pa[4] = {pack_weights<E4>(sc[2 * u][0], sc[2 * u][1]), ROWS == 1 ? 0u : pack_weights<E4>(sc[2 * u][2], sc[2 * u][3]),
-                              pack_weights<E4>(sc[2 * u + 1][0], sc[2 * u + 1][1]),
-                              ROWS == 1 ? 0u : pack_weights<E4>(sc[2 * u + 1][2], sc[2 * u + 1][3])};
-      const int r = u * kGroup + (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
-      if (E4) {
+        for (int n = 0; n < N; ++n) {
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {  // 32 channels: even and odd ones of each 16 in tiles of their own
-          uint32_t w[4];
-          ldsm_x4_trans(w, vs + piece<Sh::kRow>(r, 2 * j + c));
-#pragma unroll
-          for (int x = 0; x < 4; ++x) w[x] = __byte_perm(w[x], 0u, 0x3120);
-          mma16816<F16>(o[4 * j], pa, low_f16(w[0]), low_f16(w[1]));
-          mma16816<F16>(o[4 * j + 1], pa, high_f16(w[0]), high_f16(w[1]));
-          mma16816<F16>(o[4 * j + 2], pa, low_f16(w[2]), low_f16(w[3]));
-          mma16816<F16>(o[4 * j + 3], pa, high_f16(w[2]), high_f16(w[3]));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          uint32_t w[4];
-          ldsm_x4_trans(w, vs + piece<Sh::kRow>(r, 2 * j + c));
-          mma16816<Bf16>(o[2 * j], pa, w[0], w[1]);
-          mma16816<Bf16>(o[2 * j + 1], pa, w[2], w[3]);
+          for (int e = 0; e < 2 * ROWS; ++e) {
+            const float y = sd[n][e] - mvz[e >> 1] + static_cast<float>(kWeightBits * part);
+            const bool here = part == 0 ? !(y < kLimit) : y < kTopWeight && (part == kParts - 1 || y >= kLimit);
+            sc[n][e] = here ? ex2_approx(y) : 0.f;
+          }
         }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t pa[4] = {pack_weights<E4>(sc[2 * u][0], sc[2 * u][1]), ROWS == 1 ? 0u : pack_weights<E4>(sc[2 * u][2], sc[2 * u][3]),
+                                pack_weights<E4>(sc[2 * u + 1][0], sc[2 * u + 1][1]),
+                                ROWS == 1 ? 0u : pack_weights<E4>(sc[2 * u + 1][2], sc[2 * u + 1][3])};
+        const int r = u * kGroup + (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
+        if (E4) {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {  // 32 channels: even and odd ones of each 16 in tiles of their own
+            uint32_t w[4];
+            ldsm_x4_trans(w, vs + piece<Sh::kRow>(r, 2 * j + c));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w[x] = __byte_perm(w[x], 0u, 0x3120);
+            mma16816<F16>(o[4 * j], pa, low_f16(w[0]), low_f16(w[1]));
+            mma16816<F16>(o[4 * j + 1], pa, high_f16(w[0]), high_f16(w[1]));
+            mma16816<F16>(o[4 * j + 2], pa, low_f16(w[2]), low_f16(w[3]));
+            mma16816<F16>(o[4 * j + 3], pa, high_f16(w[2]), high_f16(w[3]));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t w[4];
+            ldsm_x4_trans(w, vs + piece<Sh::kRow>(r, 2 * j + c));
+            mma16816<Bf16>(o[2 * j], pa, w[0], w[1]);
+            mma16816<Bf16>(o[2 * j + 1], pa, w[2], w[3]);
+          }
+        }
+      }
+      if (!E4 || parts == 1) break;
+      ++part;
+      const float by = __uint_as_float(static_cast<uint32_t>(127 + (part == kParts ? 1 - kParts : 1) * kWeightBits) << 23);
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2 * ROWS; ++e) o[j][e] *= by;
+      }
+      if (part == kParts) break;
     }
     __syncwarp();
     if (i + Sh::kStages - 1 < steps) load(i + Sh::kStages - 1);
@@ -445,7 +492,7 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? 3 : 1) kda_attn_step_kernel
     // o relative to the weights' maximum again
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const float by = mv[r] == -INFINITY ? (mv[r] == m[r] ? 1.f : 0.f) : exp2f(mv[r] - m[r]);
+      const float by = mv[r] == -INFINITY ? (mv[r] == m[r] ? 1.f : 0.f) : exp2f(mv[r] - kTopWeight - m[r]);
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) o[j][2 * r] *= by, o[j][2 * r + 1] *= by;
     }
