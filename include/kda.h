@@ -614,7 +614,8 @@ kda_status kda_kv_append(const kda_kv_append_args* args, kda_stream_t stream);
  *   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i . k_j) / sum_j' exp(scale q_i . k_j')
  * over the keys j that query i sees: all S_n of its sequence n, or, with
  * KDA_ATTN_FLAG_CAUSAL, those up to i + S_n - T_n (the last query sees every key). A
- * query that sees none gives o = 0 and lse = -inf.
+ * query that sees none gives o = 0 and lse = -inf; one whose keys all score -inf o = NaN (0 / 0)
+ * and lse = -inf; a score of +inf or NaN makes both NaN.
  *   q, o       [B, T, HQ, D]     bf16
  *   lse        [B, T, HQ]        fp32 or NULL: log sum_j exp(scale q_i . k_j)
  *   k, v       [B, S, HKV, D]    bf16, or, with block_table, the cache (bf16)

@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int used = attend_row<D>(q, keys, it.hk, first * kRows, end, c2, lane, a.err, rm, rl, o);
         const long long srow = stok * a.HQ + shead;
         const long long spart = static_cast<long long>(it.split) * a.B * a.T * a.HQ + srow;
-        const float l2 = used == 0 ? -INFINITY : rl == 0.f ? __uint_as_float(0x7fc00000u) : rm + log2f(rl);
+        const float l2 = used == 0 || rl == 0.f ? -INFINITY : rm + log2f(rl);  // (keys that all score -inf: o is 0 / 0)
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           const float x = used == 0 ? 0.f : o[c] / rl;

@@ -8,7 +8,7 @@ namespace kda {
 
 struct AttnParts {
   float* o;        // [splits, B * T, HQ, D] fp32, normalised; nullptr: the results go to the call's o
-  float* lse;      // [splits, B * T, HQ], in powers of two
+  float* lse;      // [splits, B * T, HQ], in powers of two; -inf without a key (o: 0), and with keys that all score -inf (o: NaN)
   int splits;      // the keys' blocks are split over this many results
   int keys;        // paged keys of the one sequence, where no seq_lens_k gives them
 };

@@ -128,7 +128,9 @@ __device__ __forceinline__ float factor(float was, float now) {
   return was == now ? 1.f : was == -INFINITY ? 0.f : fmaxf(ex2_approx(was - now), kTiny);
 }
 
-// Adds the results in the workspace for a row and head, 4 channels from d.
+// Adds the results in the workspace for a row and head, 4 channels from d. A logarithm of -inf
+// is a part without keys, or with keys that weigh nothing, which has NaN as its values: where
+// no other part has a weight the row is NaN (0 / 0), otherwise they change nothing.
 template <int D>
 __device__ __forceinline__ void join_parts(const Params& p, long long b, int head, int d, Joined& j, int& any) {
   constexpr int kAtOnce = 4;  // loads in flight together
@@ -143,7 +145,10 @@ __device__ __forceinline__ void join_parts(const Params& p, long long b, int hea
     }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      if (lse[i] == -INFINITY) continue;  // no key
+      if (lse[i] == -INFINITY) {
+        any |= o[i].x != o[i].x;
+        continue;
+      }
       any = 1;
       j.add(lse[i], 1.f, o[i]);
     }
@@ -556,11 +561,11 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? 3 : 1) kda_attn_step_kernel
       any = cta_used;
       j.add(cta_m[r], cta_l[r], *reinterpret_cast<const float4*>(cta_o(r, d)));
     }
-    if (p.own_o != nullptr) {  // kda_attn_join_kernel takes the results together
+    if (p.own_o != nullptr) {  // kda_attn_join_kernel takes the results together (keys without weight: 0 / 0, and -inf)
       const long long at = (static_cast<long long>(rank / p.splits) * a.B + b) * a.HQ + head;
       const float inv = any ? 1.f / j.l : 0.f;
       *reinterpret_cast<float4*>(p.own_o + at * D + d) = make_float4(j.o.x * inv, j.o.y * inv, j.o.z * inv, j.o.w * inv);
-      if (d == 0) p.own_lse[at] = any ? (j.l == 0.f ? __uint_as_float(0x7fc00000u) : j.m + log2f(j.l)) : -INFINITY;
+      if (d == 0) p.own_lse[at] = any && j.l != 0.f ? j.m + log2f(j.l) : -INFINITY;
       continue;
     }
     if (row) join_parts<D>(p, b, head, d, j, any);

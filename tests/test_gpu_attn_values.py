@@ -1,4 +1,5 @@
-"""Softmax attention on values far apart: cached heads of zeros beside others."""
+"""Softmax attention on values far apart: cached heads of zeros beside others, scores and
+values of infinity."""
 
 import numpy as np
 import pytest
@@ -7,10 +8,12 @@ import torch
 import kimi_delta_attention_04_gb300 as kda
 from oracle import attn_oracle as ao
 
-from attn_cases import BF, E4, F32, Cache, check, randn
+from attn_cases import BF, E4, F32, NAN, Cache, check, randn
 from kda_cases import np64
 
 pytestmark = pytest.mark.gpu
+
+INF = float("inf")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -75,3 +78,107 @@ def test_step_zero_heads_beside_others(layout, HQ, HKV, D, P, n, spread, nats):
     o, lse = steps(cache, n, q, scale, layout)
     for r in range(2):
         check(o[r:r + 1], lse[r:r + 1], refs, n, D)
+
+
+# --- scores of -inf weigh nothing, wherever a row's tokens are worked on ---
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("cut", [0, 16, 128, 256, 512, 1024, 1536])
+@pytest.mark.parametrize("first", [True, False])
+def test_step_scores_of_minus_infinity(layout, cut, first):
+    """Keys on one side of `cut` score -inf: as if they were not there; only they: NaN (0 / 0), and
+    a logarithm of -inf."""
+    gen = torch.Generator().manual_seed(cut)
+    n, HQ, HKV, D, P = 1601, 4, 2, 64, 16
+    q, k, v = randn(gen, 1, HQ, D), randn(gen, n, HKV, D), randn(gen, n, HKV, D)
+    q[..., 0] = 1.0
+    hidden = np.arange(n) < cut if first else np.arange(n) >= cut
+    k[torch.from_numpy(hidden)] = k[torch.from_numpy(hidden)].index_fill(2, torch.tensor([0]), -INF)
+    cache = Cache(gen, [k], [v], P).cuda()
+    o, lse = steps(cache, n, q, 0.125, layout)
+    if hidden.all():
+        assert torch.isnan(o.float()).all() and (lse == -INF).all()
+        return
+    keep = torch.from_numpy(~hidden)
+    refs = ao.attend(np64(q), np64(k[keep]), np64(v[keep]), 0.125, [int(keep.sum())])
+    for r in range(2):
+        check(o[r:r + 1], lse[r:r + 1], refs, n, D)
+
+
+@pytest.mark.parametrize("own", ["finite", "-inf", "none"])
+@pytest.mark.parametrize("cut", [0, 128, 256, 384])
+def test_step_prefix_scores_of_minus_infinity(own, cut):
+    """A prefix whose keys from `cut` on score -inf: a split of it may have no others."""
+    gen = torch.Generator().manual_seed(cut + 1)
+    prefix, HQ, HKV, D, P = 400, 2, 1, 128, 16
+    n = 0 if own == "none" else 20
+    q = randn(gen, 1, HQ, D)
+    q[..., 0] = 1.0
+    ks, vs = ([randn(gen, m, HKV, D) for m in (n, prefix)] for _ in range(2))
+    ks[1][cut:, :, 0] = -INF
+    if own == "-inf":
+        ks[0][:, :, 0] = -INF
+    cache = Cache(gen, ks, vs, P).cuda()
+    keys = np.concatenate([np64(ks[1][:cut]), np64(ks[0][:0 if own == "-inf" else n])])
+    values = np.concatenate([np64(vs[1][:cut]), np64(vs[0][:0 if own == "-inf" else n])])
+    for layout in ("few", "many"):
+        o, lse = steps(cache, n, q, 0.09, layout, prefix=prefix)
+        if len(keys) == 0:
+            assert torch.isnan(o.float()).all() and (lse == -INF).all()
+            continue
+        refs = ao.attend(np64(q), keys, values, float(np.float32(0.09)), [len(keys)])
+        for r in range(2):
+            check(o[r:r + 1], lse[r:r + 1], refs, n + prefix, D)
+
+
+def test_prompts_scores_of_minus_infinity():
+    """Only scores of -inf give NaN and a logarithm of -inf; with others they weigh nothing."""
+    gen = torch.Generator().manual_seed(2)
+    T, HQ, HKV, D = 200, 2, 1, 64
+    q, k, v = randn(gen, 1, T, HQ, D), randn(gen, 1, T, HKV, D), randn(gen, 1, T, HKV, D)
+    q[..., 0] = 1.0
+    k[:, :140, :, 0] = -INF
+    lse = torch.zeros(1, T, HQ, device="cuda")
+    o = kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), scale=0.125, lse=lse)
+    assert torch.isnan(o[0, :140].float()).all() and (lse[0, :140] == -INF).all()
+    refs = ao.attend(np64(q[0, 140:]), np64(k[0, 140:]), np64(v[0, 140:]), 0.125, ao.seen_keys(60, 60, True))
+    check(o[0, 140:], lse[0, 140:], refs, T, D)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("what", [INF, -INF, NAN])
+@pytest.mark.parametrize("at", [3, 700, 1600])
+def test_step_infinite_values(layout, what, at):
+    """An infinity in a value, however small its weight, is that channel's result; the others stay."""
+    gen = torch.Generator().manual_seed(at)
+    n, HQ, HKV, D, P = 1601, 4, 2, 64, 16
+    q, k, v = randn(gen, 1, HQ, D), randn(gen, n, HKV, D), randn(gen, n, HKV, D)
+    q[..., 0], k[at, :, 0] = 30.0, -100.0  # a weight of exp(-375) and less
+    v[at, 1, 17] = what
+    cache = Cache(gen, [k], [v], P).cuda()
+    o, lse = steps(cache, n, q, 0.125, layout)
+    v[at, 1, 17] = 0.0
+    refs = ao.attend(np64(q), np64(k), np64(v), 0.125, [n])
+    got = o.float().cpu()
+    want = torch.full((2, 2), what)
+    assert torch.equal(torch.nan_to_num(got[:, 2:, 17], nan=5.0, posinf=6.0, neginf=7.0), torch.nan_to_num(want, nan=5.0, posinf=6.0, neginf=7.0))
+    for r in range(2):
+        fixed = got[r:r + 1].clone()
+        fixed[:, 2:, 17] = torch.from_numpy(refs[0][:, 2:, 17]).float()
+        check(fixed, lse[r:r + 1], refs, n, D)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_step_infinite_scores(layout):
+    """A score of +inf gives NaN in its heads and leaves the others as they were."""
+    gen = torch.Generator().manual_seed(3)
+    n, HQ, HKV, D, P = 1601, 4, 2, 64, 16
+    q, k, v = randn(gen, 1, HQ, D), randn(gen, n, HKV, D), randn(gen, n, HKV, D)
+    q[..., 0] = 1.0
+    k[900, 1, 0] = INF
+    cache = Cache(gen, [k], [v], P).cuda()
+    o, lse = steps(cache, n, q, 0.125, layout)
+    assert torch.isnan(o[:, 2:].float()).all()
+    refs = ao.attend(np64(q[:, :2]), np64(k[:, :1]), np64(v[:, :1]), 0.125, [n])
+    for r in range(2):
+        check(o[r:r + 1, :2], lse[r:r + 1, :2], refs, n, D)
