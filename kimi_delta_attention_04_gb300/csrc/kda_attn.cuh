@@ -20,21 +20,28 @@ struct Keys {
   long long k_stride, v_stride, first;
 };
 
+// How far, in powers of two, the weights of n keys are held below 1: their sum stays below
+// 1 / 2, and with it a sum of weighted values below the largest value (four times 1e38 is
+// infinite, its mean is not).
+__device__ __forceinline__ float below_one(int n) { return static_cast<float>(33 - __clz(n)); }
+
 // Attention of one row of queries over keys [begin, end), one warp, each key in turn with a
 // running maximum: lane l holds channels l + 32 i. Reads only what the row sees, and
 // follows the definition where infinities and NaN take part: a weight of a finite score
 // is held above 0 (2^-126), so that an infinite value stays one, and a score of -inf
-// weighs 0. q is the row already in fp32; scale2 = scale * log2(e). Returns how many
+// weighs 0. The sum l and the values o are relative to 2^m. q is the row already in fp32; scale2 = scale * log2(e). Returns how many
 // keys there were (those on pages out of range are left out).
 template <int D>
 __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& s, int h, int begin, int end, float scale2, int lane, int32_t* err,
                                            float& m, float& l, float (&o)[D / 32]) {
   m = -INFINITY, l = 0.f;
+  float best = -INFINITY;  // the largest score; m is `below` above it
   int used = 0;
   bool nan = false;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = 0.f, nan |= q[i] != q[i];
   const bool nan_row = __any_sync(0xffffffffu, nan);  // (padding that nothing has written, say)
+  const float below = below_one(max(end - begin, 0));
   constexpr int N = 4;  // keys whose loads and sums are under way together
   for (int j0 = begin; j0 < end; j0 += N) {
     float x[N], v[N][D / 32];
@@ -73,11 +80,11 @@ __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& 
     for (int u = 0; u < N; ++u) {
       if (!there[u]) continue;
       ++used;
-      const float top = x[u] > m ? x[u] : m;  // (a NaN leaves m and makes p and l NaN)
-      const float keep = m == top ? 1.f : m == -INFINITY ? 0.f : fmaxf(exp2f(m - top), 1.1754944e-38f);
-      float p = exp2f(x[u] - (top == -INFINITY ? 0.f : top));
+      const float top = x[u] > best ? x[u] : best;  // (a NaN leaves it and makes p and l NaN)
+      const float keep = best == top ? 1.f : best == -INFINITY ? 0.f : fmaxf(exp2f(best - top), 1.1754944e-38f);
+      best = top, m = top + below;
+      float p = exp2f(x[u] - (top == -INFINITY ? 0.f : m));
       if (x[u] != -INFINITY) p = p < 1.1754944e-38f ? 1.1754944e-38f : p;
-      m = top;
       l = l * keep + p;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) o[i] = o[i] * keep + p * v[u][i];

@@ -1,5 +1,5 @@
 """Softmax attention on values far apart: cached heads of zeros beside others, scores and
-values of infinity."""
+values of infinity, values near the ends of bf16's range."""
 
 import numpy as np
 import pytest
@@ -182,3 +182,18 @@ def test_step_infinite_scores(layout):
     refs = ao.attend(np64(q[:, :2]), np64(k[:, :1]), np64(v[:, :1]), 0.125, [n])
     for r in range(2):
         check(o[r:r + 1, :2], lse[r:r + 1, :2], refs, n, D)
+
+
+# --- values near the end of the range: their mean is there, their sum is not ---
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_largest_values(D, causal):
+    gen = torch.Generator().manual_seed(D)
+    T, HQ, HKV = 300, 4, 2
+    q, k, v = randn(gen, 1, T, HQ, D) * 0.1, randn(gen, 1, T, HKV, D), (randn(gen, 1, T, HKV, D, dtype=F32).clamp(-1, 1) * 3.2e38).to(BF)
+    v[..., :5] = 3.2e38
+    lse = torch.zeros(1, T, HQ, device="cuda")
+    o = kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), scale=0.125, causal=causal, lse=lse)
+    refs = ao.attend(np64(q[0]), np64(k[0]), np64(v[0]), 0.125, ao.seen_keys(T, T, causal))
+    check(o[0], lse[0], refs, T, D)
