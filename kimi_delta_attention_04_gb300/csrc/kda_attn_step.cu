@@ -150,7 +150,8 @@ __device__ __forceinline__ void join_parts(const Params& p, long long b, int hea
         continue;
       }
       any = 1;
-      j.add(lse[i], 1.f, o[i]);
+      // (2^-8 each: with up to 70 parts, sums of weighted values stay below the largest)
+      j.add(lse[i] + 8.f, 0x1p-8f, make_float4(o[i].x * 0x1p-8f, o[i].y * 0x1p-8f, o[i].z * 0x1p-8f, o[i].w * 0x1p-8f));
     }
   }
 }
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? 3 : 1) kda_attn_step_kernel
     len = 0;
   }
   if (tid == 0) cta_used = 0;
+  const float below = below_one(len);
 
   // queries as the products' A operand: heads g and g + 8; channels 16 k + 2 t, + 1 and
   // + 8, + 9 for bf16 keys, the 4 from 16 k + 4 t for 8-bit ones (an order of the sum
@@ -313,7 +315,8 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? 3 : 1) kda_attn_step_kernel
     }
   };
 
-  // running maximum and sum of the weights, and, with 8-bit values, the maximum of the
+  // running maximum of the scores, sum of the weights (relative to 2^below times the maximum's: what is
+  // added up over the row stays below the largest value, also across warps and CTAs), and, with 8-bit values, the maximum of the
   // weights times their values' scales, of which o is relative to 2^-kTopWeight (its own otherwise)
   float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, mv[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? 3 : 1) kda_attn_step_kernel
         if (ROWS > 1) o[j][2] *= keep[1], o[j][3] *= keep[1];
       }
     }
-    const float mz[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+    const float mz[2] = {m[0] == -INFINITY ? 0.f : m[0] + below, m[1] == -INFINITY ? 0.f : m[1] + below};
     const float mvz[2] = {mv[0] == -INFINITY ? 0.f : mv[0] - kTopWeight, mv[1] == -INFINITY ? 0.f : mv[1] - kTopWeight};
     // by their bits, exponents of weights below the limit and above -inf: from the limit's own
     // bits (0) up to those of -inf; all other values, NaN among them, come out larger
@@ -494,12 +497,13 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? 3 : 1) kda_attn_step_kernel
   }
   cp_async_wait<0>();
   if (E4) {
-    // o relative to the weights' maximum again
+    // o relative to what the sum is relative to again (in two factors: one might leave the range)
+    const float down = exp2f(-kTopWeight - below);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const float by = mv[r] == -INFINITY ? (mv[r] == m[r] ? 1.f : 0.f) : exp2f(mv[r] - kTopWeight - m[r]);
+      const float by = mv[r] == -INFINITY ? (mv[r] == m[r] ? 1.f : 0.f) : exp2f(mv[r] - m[r]);
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) o[j][2 * r] *= by, o[j][2 * r + 1] *= by;
+      for (int j = 0; j < D / 8; ++j) o[j][2 * r] = o[j][2 * r] * down * by, o[j][2 * r + 1] = o[j][2 * r + 1] * down * by;
     }
   }
   if (any_bad && lane == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? 3 : 1) kda_attn_step_kernel
     }
   }
   if (t == 0) {
-    warp_m[warp][g] = m[0], warp_m[warp][g + 8] = m[1];
+    warp_m[warp][g] = m[0] + below, warp_m[warp][g + 8] = m[1] + below;
     warp_l[warp][g] = l[0], warp_l[warp][g + 8] = l[1];
   }
   __syncthreads();

@@ -197,3 +197,19 @@ def test_prompts_largest_values(D, causal):
     o = kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), scale=0.125, causal=causal, lse=lse)
     refs = ao.attend(np64(q[0]), np64(k[0]), np64(v[0]), 0.125, ao.seen_keys(T, T, causal))
     check(o[0], lse[0], refs, T, D)
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("n,big", [(2, 3.2e38), (4, 1e38), (70, 3.2e38), (3001, 1e38)])
+def test_step_largest_values(dtype, layout, n, big):
+    gen = torch.Generator().manual_seed(n)
+    HQ, HKV, D, P = 4, 2, 128, 16
+    q, k, v = randn(gen, 1, HQ, D), randn(gen, n, HKV, D), (randn(gen, n, HKV, D, dtype=F32).clamp(-1, 1) * big).to(BF)
+    v[..., :5] = big
+    v[..., 5:8] = -big
+    cache = Cache(gen, [k], [v], P, dtype)
+    refs = ao.attend(np64(q * 0.1), *cache.tokens(0), float(np.float32(0.09)), [n])
+    o, lse = steps(cache.cuda(), n, q * 0.1, 0.09, layout)
+    for r in range(2):
+        check(o[r:r + 1], lse[r:r + 1], refs, n, D)
