@@ -548,7 +548,8 @@ kda_status kda_scan_step(const kda_scan_step_args* args, kda_stream_t stream);
  * sequence's row of an int32 table (entries behind its last page are not used).
  * With e4m3, k_scale and v_scale, fp32 [pages, HKV, page_size], hold a factor for
  * each token and head (value ~ stored * scale): above 0, or NaN. kda_kv_append writes
- * powers of two; with others a prefix's keys and values are rounded to bf16.
+ * powers of two; with others a prefix's keys and values are rounded to bf16, whose
+ * largest value they are held to.
  * A page index outside 0 .. pages - 1 writes KDA_ERR_INVALID_ARG to err, and the
  * tokens on it are left out.
  *

@@ -642,6 +642,13 @@ cudaError_t launch_warps(const Params& p, const Plan& x, cudaStream_t s) {
 // Its keys meet the queries of all rows: products of 128 rows, which the prompt kernel
 // computes as one sequence of B queries that sees every key, split over its blocks.
 
+// fp32 held to bf16's largest value (an 8-bit head of bf16's last values may hold 256 times
+// 2^120, 2^-8 above it); NaN stays NaN.
+__device__ __forceinline__ float in_bf16(float x) {
+  constexpr float kMost = 3.3895313892515355e38f;
+  return x > kMost ? kMost : x < -kMost ? -kMost : x;
+}
+
 // An 8-bit prefix in bf16 (exact with scales that are powers of two), as pages 0, 1, ...
 // of a cache of its own; table[i] is i, or -1 where the prefix's page is out of range.
 template <int D>
@@ -662,8 +669,8 @@ __global__ void __launch_bounds__(256) kda_attn_prefix_bf16_kernel(const kda_att
     for (int i = 0; i < 2; ++i) {
       const uint32_t lo = low_f16(in[i]), hi = high_f16(in[i]);
       const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&lo)), v = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-      out[2 * i] = Bf16::pack(u.x * s, u.y * s);
-      out[2 * i + 1] = Bf16::pack(v.x * s, v.y * s);
+      out[2 * i] = Bf16::pack(in_bf16(u.x * s), in_bf16(u.y * s));
+      out[2 * i + 1] = Bf16::pack(in_bf16(v.x * s), in_bf16(v.y * s));
     }
     *reinterpret_cast<uint4*>((of_v ? vals : k) + (to + t) * D + c) = make_uint4(out[0], out[1], out[2], out[3]);
   }

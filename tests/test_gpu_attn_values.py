@@ -213,3 +213,21 @@ def test_step_largest_values(dtype, layout, n, big):
     o, lse = steps(cache.cuda(), n, q * 0.1, 0.09, layout)
     for r in range(2):
         check(o[r:r + 1], lse[r:r + 1], refs, n, D)
+
+
+def test_step_8bit_values_past_the_largest_of_bf16():
+    """A head of bf16's largest values is stored as 256 times 2^120, which bf16 does not hold: in the
+    prefix, which bf16 copies of are made, as among the row's own tokens."""
+    gen = torch.Generator().manual_seed(5)
+    n, HQ, HKV, D, P = 48, 2, 1, 64, 16
+    q, k, v = randn(gen, 1, HQ, D) * 0.1, randn(gen, n, HKV, D), torch.zeros(n, HKV, D, dtype=BF)
+    v[1::3, :, :9] = 3.38e38
+    v[2::3, :, 5:12] = -3.38e38
+    cache = Cache(gen, [k], [v], P, E4)
+    assert float(cache.v_scale[cache.v_scale == cache.v_scale].max()) == 2.0 ** 120
+    refs = ao.attend(np64(q), *cache.tokens(0), 0.125, [n])
+    cache.cuda()
+    for layout in LAYOUTS:
+        o, lse = steps(cache, n, q, 0.125, layout)
+        for r in range(2):
+            check(o[r:r + 1], lse[r:r + 1], refs, n, D)
