@@ -231,3 +231,45 @@ def test_step_8bit_values_past_the_largest_of_bf16():
         o, lse = steps(cache, n, q, 0.125, layout)
         for r in range(2):
             check(o[r:r + 1], lse[r:r + 1], refs, n, D)
+
+
+# --- long rows ---
+
+def repeated(q, k, v, scale, seen):
+    """ao.attend of queries q [T, HQ, D] on the keys of one page, k and v [P, D], over and over: of
+    `seen` [T] keys in all."""
+    P = len(k)
+    q, k, v = np64(q), np64(k), np64(v)
+    count = np.asarray(seen)[:, None] // P + (np.arange(P)[None] < np.asarray(seen)[:, None] % P)
+    s = np.einsum("thd,pd->thp", q, k) * scale + np.log(count)[:, None]
+    m = s.max(-1, keepdims=True)
+    e = np.exp(s - m)
+    p = e / e.sum(-1, keepdims=True)
+    return p @ v, (m + np.log(e.sum(-1, keepdims=True)))[..., 0], p @ np.abs(v), (np.abs(q) @ np.abs(k).T).max(-1) * scale
+
+
+@pytest.mark.parametrize("T,D", [(32, 64), (512, 128)])
+def test_prompts_rows_computed_again_for_long(T, D):
+    """32 rows of 10^6 keys with an infinity among their values take longer to compute again than a
+    wait may last, while the next tile of their CTA (of 512 rows and 128 channels: their pair of CTAs)
+    is under way: the call ends with its results. (About 15 s each.)"""
+    gen = torch.Generator().manual_seed(7)
+    P, N, S = 128, 400 if T == 32 else 200, 2 ** 20 + (2 ** 18 if D == 64 else 0)
+    k, v = (randn(gen, 1, 1, P, D).expand(2, -1, -1, -1).contiguous() for _ in range(2))
+    v[1, 0, P - 32, 5] = INF  # in the last page of one sequence: of its last 32 queries only
+    q = randn(gen, N * T, 1, D)
+    table = torch.zeros(N, S // P, dtype=torch.int32, device="cuda")
+    table[N - 1, -1] = 1  # (the last sequence starts first)
+    err, lse = i32([0]), torch.zeros(1, N * T, 1, device="cuda")
+    o = kda.kda_attn_fwd(q[None].cuda(), k.cuda(), v.cuda(), scale=0.09, cu_seqlens=i32([n * T for n in range(N + 1)]), block_table=table,
+                         seq_lens_k=i32([S] * N), lse=lse, err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    bad = o[0, -32:, 0, 5].clone()
+    assert (bad == INF).all() and torch.isinf(o).sum() == 32
+    for a in (0, (N - 2) * T, (N - 1) * T):
+        refs = repeated(q[a:a + T], k[0, 0], v[0, 0], float(np.float32(0.09)), S - T + 1 + np.arange(T))
+        got = o[0, a:a + T].float().cpu()
+        if a == (N - 1) * T:
+            got[-32:, 0, 5] = torch.from_numpy(refs[0][-32:, 0, 5]).float()
+        check(got, lse[0, a:a + T], refs, S, D)
