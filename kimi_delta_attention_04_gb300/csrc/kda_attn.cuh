@@ -30,11 +30,10 @@ __device__ __forceinline__ float below_one(int n) { return static_cast<float>(33
 // follows the definition where infinities and NaN take part: a weight of a finite score
 // is held above 0 (2^-126), so that an infinite value stays one, and a score of -inf
 // weighs 0. The sum l and the values o are relative to 2^m. q is the row already in fp32; scale2 = scale * log2(e). Returns how many
-// keys there were (those on pages out of range are left out). alive() is called by one
-// lane every 1024 keys (about half a millisecond).
-template <int D, typename Alive>
+// keys there were (those on pages out of range are left out).
+template <int D>
 __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& s, int h, int begin, int end, float scale2, int lane, int32_t* err,
-                                           const Alive& alive, float& m, float& l, float (&o)[D / 32]) {
+                                           float& m, float& l, float (&o)[D / 32]) {
   m = -INFINITY, l = 0.f;
   float best = -INFINITY;  // the largest score; m is `below` above it
   int used = 0;
@@ -45,7 +44,6 @@ __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& 
   const float below = below_one(max(end - begin, 0));
   constexpr int N = 4;  // keys whose loads and sums are under way together
   for (int j0 = begin; j0 < end; j0 += N) {
-    if (lane == 0 && (j0 - begin) % 1024 == 0) alive();
     float x[N], v[N][D / 32];
     bool there[N];
 #pragma unroll

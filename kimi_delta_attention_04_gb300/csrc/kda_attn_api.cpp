@@ -49,7 +49,7 @@ kda_status check_cache(int32_t pages, int32_t page_size, int32_t HKV, int32_t dt
 
 // Tokens that a table has room for. At this limit counts of tokens past the last one stay
 // below 2^31, and a prompt kernel's longest wait, for an item's whole work, below ten seconds
-// (rows that are computed again say that they go on, which the waits look at).
+// (rows that are computed again take longer, which its limit counts in).
 bool room_ok(int32_t width, int32_t page_size) { return static_cast<int64_t>(width) * page_size <= KDA_ATTN_MAX_TOKENS; }
 
 // An output in place of an input: the same rows, or none of them.

@@ -63,6 +63,7 @@ struct Params {
   int G, Gp, sub, heads;      // Gp query heads to a tile, sub such sets a key head, heads sets in all
   int tile_tokens, per_token; // tokens to a tile; 65536 / Gp rounded up: row r is of token r per_token >> 16
   int slots;                  // places for query tiles
+  unsigned long long limit;   // how long a wait may last, in ns
 };
 
 // What a CTA works on next.
@@ -84,7 +85,6 @@ struct Head {
   uint32_t bad[8];            // by block, of the last 8: keys on pages that are out of range, a bit for each 16
   uint32_t tmem_base;
   int failed;
-  unsigned long long alive;   // when a row was last known to be computed again, in ns
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -107,33 +107,22 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-// Waits for a phase, for at most ten seconds in which no row is computed again (32 rows of a
-// warp take 10 to 15 s at 10^6 keys, and say in Head::alive that they go on); whether it came. (One
-// statement, and callers that look at the results seldom: with the loop and its exits in the
-// compiler's hands each wait of the thread that issues products left the tensor core idle for 140
-// cycles instead of 40. No hint that lets the thread sleep: 395 us instead of 407 for 8192 tokens
-// and 32 heads of 128.)
-__device__ __forceinline__ bool wait(Head& sm, uint64_t* bar, uint32_t parity) {
+// Waits for a phase, for at most `limit` ns; whether it came. (One statement, and callers that look
+// at the results seldom: with the loop and its exits in the compiler's hands each wait of the
+// thread that issues products left the tensor core idle for 140 cycles instead of 40. No hint that
+// lets the thread sleep: 395 us instead of 407 for 8192 tokens and 32 heads of 128.)
+__device__ __forceinline__ bool wait(unsigned long long limit, uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 t0, t1, t2;\n"
+      "{\n .reg .pred p, q;\n .reg .b64 t0, t1;\n"
       " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n mov.u64 t0, %globaltimer;\n"
       "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n mov.u64 t1, %globaltimer;\n"
-      " ld.volatile.shared.u64 t2, [%3];\n max.u64 t2, t2, t0;\n"
-      " sub.s64 t1, t1, t2;\n setp.lt.s64 q, t1, 10000000000;\n @q bra AGAIN;\n mov.u32 %0, 0;\n bra END;\n"
+      " sub.u64 t1, t1, t0;\n setp.lt.u64 q, t1, %3;\n @q bra AGAIN;\n mov.u32 %0, 0;\n bra END;\n"
       "DONE:\n mov.u32 %0, 1;\nEND:\n}\n"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(&sm.alive))
+      : "r"(smem_u32(bar)), "r"(parity), "l"(limit)
       : "memory");
   return ok != 0;
-}
-
-// The time, where the waits of this CTA, and of the pair's other one, look for it.
-template <int CTAS>
-__device__ __forceinline__ void say_alive(Head& sm, int rank) {
-  const unsigned long long now = global_timer_ns();
-  asm volatile("st.volatile.shared.u64 [%0], %1;" ::"r"(smem_u32(&sm.alive)), "l"(now) : "memory");
-  if (CTAS == 2) asm volatile("st.relaxed.cluster.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(&sm.alive), rank ^ 1)), "l"(now) : "memory");
 }
 
 // ---- what differs where a pair of CTAs works on tiles of 256 rows ----
@@ -203,7 +192,7 @@ __device__ __forceinline__ void load_tile(void* smem, const CUtensorMap* map, in
 // interleaves them, and each waits longer for its own: 444 us instead of 395 for 8192
 // tokens and 32 heads of 128.)
 template <int D, int CTAS>
-__device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* tiles) {
+__device__ __forceinline__ bool issue_products(const Params& p, Head& sm, const unsigned char* tiles) {
   using Sh = Shape<D, CTAS>;
   constexpr uint32_t qk = tc05::idesc_f16kind(CTAS * kRows, kRows, true), pv = tc05::idesc_f16kind(CTAS * kRows, D, true) | tc05::kIdescBMnMajor;
   const uint64_t desc = tc05::smem_desc(0, 16, 1024, tc05::kSwizzle128B), desc_mn = tc05::smem_desc(0, kHalf, 1024, tc05::kSwizzle128B);
@@ -228,18 +217,18 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
     if (++s == Sh::kStages) s = 0, phase ^= 1;
   };
   for (int k = 0; going; ++k) {
-    going = wait(sm, &sm.item_full[k & 1], (k >> 1) & 1);
+    going = wait(p.limit, &sm.item_full[k & 1], (k >> 1) & 1);
     if (!going) break;
     const Item& it = sm.items[k & 1];
     if (it.n < 0) break;
     const int count0 = it.count[0], count1 = it.count[1], blocks = max(count0, count1), keys = it.S - it.first * kRows;
     if (blocks > 0) {
-      going = wait(sm, &sm.full[s], phase);
+      going = wait(p.limit, &sm.full[s], phase);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int count = m == 0 ? count0 : count1;
         if (count == 0) continue;
-        going = going && wait(sm, &sm.q_full[m], tiles_done[m]++ & 1);
+        going = going && wait(p.limit, &sm.q_full[m], tiles_done[m]++ & 1);
         tc05::fence_after_sync();
         if (going) scores(m, s);
         if (count == 1) commit<CTAS>(&sm.q_empty[m]);
@@ -251,16 +240,16 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
     // blocks that both tiles use and that others follow: no conditions between the products
     for (const int both = min(count0, count1) - 1; i < both && going; ++i) {
       const int vs = s;
-      bool there = wait(sm, &sm.full[vs], phase);
+      bool there = wait(p.limit, &sm.full[vs], phase);
       advance();
-      there &= wait(sm, &sm.full[s], phase);
+      there &= wait(p.limit, &sm.full[s], phase);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int parity = done[m]++ & 1;
-        there &= wait(sm, &sm.p_full[m][0], parity);
+        there &= wait(p.limit, &sm.p_full[m][0], parity);
         tc05::fence_after_sync();
         values(m, vs, 0, 4, i > 0);
-        there &= wait(sm, &sm.p_full[m][1], parity);
+        there &= wait(p.limit, &sm.p_full[m][1], parity);
         tc05::fence_after_sync();
         values(m, vs, 4, kRows / 16, true);
         scores(m, s);
@@ -274,8 +263,8 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
     for (; i < blocks && going; ++i) {
       const int vs = s, v_phase = phase;  // the block's values; the next block's keys come after them
       advance();
-      going = wait(sm, &sm.full[vs], v_phase);
-      if (i + 1 < blocks) going = going && wait(sm, &sm.full[s], phase);
+      going = wait(p.limit, &sm.full[vs], v_phase);
+      if (i + 1 < blocks) going = going && wait(p.limit, &sm.full[s], phase);
       const bool tail = keys < (i + 1) * kRows;  // the sequence's last block is not full: zeros behind its last key
       if (tail && going) {
         mbar_arrive_local(&sm.tail_there);
@@ -287,11 +276,11 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
         if (i >= count || !going) continue;
         const bool last_v = m == 1 || i >= count1, last_k = m == 1 || i + 1 >= count1;  // no other tile needs the block
         const int parity = done[m]++ & 1;
-        going = wait(sm, &sm.p_full[m][0], parity);
-        if (tail) going = going && wait(sm, &sm.tail_zero, tails & 1);
+        going = wait(p.limit, &sm.p_full[m][0], parity);
+        if (tail) going = going && wait(p.limit, &sm.tail_zero, tails & 1);
         tc05::fence_after_sync();
         if (going) values(m, vs, 0, 4, i > 0);
-        going = going && wait(sm, &sm.p_full[m][1], parity);
+        going = going && wait(p.limit, &sm.p_full[m][1], parity);
         tc05::fence_after_sync();
         if (going) values(m, vs, 4, kRows / 16, true);
         if (i + 1 < count) {
@@ -310,7 +299,7 @@ __device__ __forceinline__ bool issue_products(Head& sm, const unsigned char* ti
   }
   if (!going) {  // products in flight end before their tensor memory is given back
     commit<CTAS>(&sm.drain);
-    wait(sm, &sm.drain, 0);
+    wait(p.limit, &sm.drain, 0);
   }
   return going;
 }
@@ -459,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.item_near, 1);
     mbar_init(&sm.ready, CTAS);
     mbar_init(&sm.next_there, 1);
-    sm.failed = 0, sm.alive = 0;
+    sm.failed = 0;
     fence_mbarrier_init_cluster();
   }
   if (warp == 9 && lane == 0) {
@@ -486,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool going = true;
       int loaded = 0, blocks_done = 0, tiles_done[2] = {0, 0};
       for (int k = 0; going; ++k) {
-        going = __all_sync(0xffffffffu, wait(sm, &sm.item_full[k & 1], (k >> 1) & 1));
+        going = __all_sync(0xffffffffu, wait(p.limit, &sm.item_full[k & 1], (k >> 1) & 1));
         if (!going) break;
         const Item it = sm.items[k & 1];
         if (it.n < 0) break;
@@ -494,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           if (it.count[m] == 0 || !going) continue;
-          if (tiles_done[m] > 0) going = __all_sync(0xffffffffu, wait(sm, &sm.q_empty[m], (tiles_done[m] - 1) & 1));
+          if (tiles_done[m] > 0) going = __all_sync(0xffffffffu, wait(p.limit, &sm.q_empty[m], (tiles_done[m] - 1) & 1));
           if (!going) continue;
           ++tiles_done[m];
           if (lane == 0) {
@@ -537,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const int s = loaded % Sh::kStages;
-            if (loaded >= Sh::kStages) going = __all_sync(0xffffffffu, wait(sm, &sm.empty[s], (loaded / Sh::kStages - 1) & 1));
+            if (loaded >= Sh::kStages) going = __all_sync(0xffffffffu, wait(p.limit, &sm.empty[s], (loaded / Sh::kStages - 1) & 1));
             if (!going) break;
             if (lane == 0) {
               // (before the keys' arrival, and so before their scores; the loads are at most 5
@@ -561,31 +550,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       // counted in its first CTA, and neither CTA ends before the other)
       bool idle = going;
       for (int m = 0; m < 2; ++m)
-        if (idle && tiles_done[m] > 0) idle = wait(sm, &sm.q_empty[m], (tiles_done[m] - 1) & 1);
-      for (int i = max(0, loaded - Sh::kStages); i < loaded && idle; ++i) idle = wait(sm, &sm.empty[i % Sh::kStages], (i / Sh::kStages) & 1);
+        if (idle && tiles_done[m] > 0) idle = wait(p.limit, &sm.q_empty[m], (tiles_done[m] - 1) & 1);
+      for (int i = max(0, loaded - Sh::kStages); i < loaded && idle; ++i) idle = wait(p.limit, &sm.empty[i % Sh::kStages], (i / Sh::kStages) & 1);
       if (!idle && rank == 0) {
         bool there = true;
         for (int m = 0; m < 2; ++m)
-          if (there && tiles_done[m] > 0) there = wait(sm, &sm.q_full[m], (tiles_done[m] - 1) & 1);
-        for (int i = max(0, loaded - Sh::kStages); i < loaded && there; ++i) there = wait(sm, &sm.full[i % Sh::kStages], (i / Sh::kStages) & 1);
+          if (there && tiles_done[m] > 0) there = wait(p.limit, &sm.q_full[m], (tiles_done[m] - 1) & 1);
+        for (int i = max(0, loaded - Sh::kStages); i < loaded && there; ++i) there = wait(p.limit, &sm.full[i % Sh::kStages], (i / Sh::kStages) & 1);
       }
       going = idle;
       if (!going) sm.failed = 1;
     } else if (warp == 8) {
-      if (rank == 0 && elect_one() && !issue_products<D, CTAS>(sm, tiles)) sm.failed = 1;
+      if (rank == 0 && elect_one() && !issue_products<D, CTAS>(p, sm, tiles)) sm.failed = 1;
     } else if (warp == 10) {
       // ---- what stands behind the last key may be anything: zeros in its place ----
       bool going = true;
       int loaded = 0, tails = 0;
       for (int k = 0; going; ++k) {
-        going = __all_sync(0xffffffffu, wait(sm, &sm.item_full[k & 1], (k >> 1) & 1));
+        going = __all_sync(0xffffffffu, wait(p.limit, &sm.item_full[k & 1], (k >> 1) & 1));
         if (!going) break;
         const Item it = sm.items[k & 1];
         if (it.n < 0) break;
         const int most = max(it.count[0], it.count[1]), live = it.S - (it.first + most - 1) * kRows;
         if (most > 0 && live < kRows) {
           const int s = (loaded + 2 * most - 1) % Sh::kStages;
-          going = __all_sync(0xffffffffu, wait(sm, &sm.tail_there, tails++ & 1));
+          going = __all_sync(0xffffffffu, wait(p.limit, &sm.tail_there, tails++ & 1));
           if (!going) break;
           unsigned char* v = ring + s * Sh::kTile;
           for (int c = 0; c < D / 64 / CTAS; ++c)
@@ -610,12 +599,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it;
         if (!more) it.n = -1;
         if (!more || item_of<PAGED, CTAS>(p, place / CTAS, lane, it)) {
-          if (k >= 2) going = __all_sync(0xffffffffu, wait(sm, &sm.item_empty[k & 1], ((k >> 1) - 1) & 1));
+          if (k >= 2) going = __all_sync(0xffffffffu, wait(p.limit, &sm.item_empty[k & 1], ((k >> 1) - 1) & 1));
           if (going && lane == 0) {
             sm.items[k & 1] = it;
             mbar_arrive_local(&sm.item_full[k & 1]);
           }
-          if (more && going) going = __all_sync(0xffffffffu, wait(sm, &sm.item_near, k & 1));
+          if (more && going) going = __all_sync(0xffffffffu, wait(p.limit, &sm.item_near, k & 1));
           ++k;
         }
         if (!more || !going) break;
@@ -624,11 +613,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx_local(&sm.next_there, 16);
           arrive_first<CTAS>(&sm.ready);
         }
-        if (rank == 0) going = __all_sync(0xffffffffu, wait(sm, &sm.ready, asked & 1));
+        if (rank == 0) going = __all_sync(0xffffffffu, wait(p.limit, &sm.ready, asked & 1));
         if (going && rank == 0 && lane == 0) ask_for_place<CTAS>(sm);
         ++asked;
         if (!going) break;
-        going = __all_sync(0xffffffffu, wait(sm, &sm.next_there, (asked - 1) & 1));
+        going = __all_sync(0xffffffffu, wait(p.limit, &sm.next_there, (asked - 1) & 1));
         if (!going) break;
         more = place_given(sm, place);
         fence_proxy_async_smem();  // (the next answer is written after this one has been read)
@@ -647,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool going = true;
     int done = 0, tiles_done = 0, blocks_done = 0;
     for (int k = 0; going; ++k) {
-    going = __all_sync(0xffffffffu, wait(sm, &sm.item_full[k & 1], (k >> 1) & 1));
+    going = __all_sync(0xffffffffu, wait(p.limit, &sm.item_full[k & 1], (k >> 1) & 1));
     if (!going) break;
     const Item& it = sm.items[k & 1];
     if (it.n < 0) break;
@@ -660,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int open = causal ? min(it.S, own + it.shift + 1) : it.S;
     float top = -INFINITY, sum = 0.f;
     for (int i = 0; i < count && going; ++i, ++done) {
-      const bool there = wait(sm, &sm.s_full[m], done & 1);  // (looked at below, when nothing waits for it)
+      const bool there = wait(p.limit, &sm.s_full[m], done & 1);  // (looked at below, when nothing waits for it)
       __syncwarp();
       tc05::fence_after_sync();
       const int k0 = (first + i) * kRows;
@@ -748,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
     }
     if (going && count > 0) {
-      going = __all_sync(0xffffffffu, wait(sm, &sm.o_full[m], tiles_done++ & 1));
+      going = __all_sync(0xffffffffu, wait(p.limit, &sm.o_full[m], tiles_done++ & 1));
       tc05::fence_after_sync();
     }
     if (going) {
@@ -814,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
           q[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[stok * a.q_stride + static_cast<long long>(shead) * D + lane + 32 * c]);
-        const int used = attend_row<D>(q, keys, it.hk, first * kRows, end, c2, lane, a.err, [&] { say_alive<CTAS>(sm, rank); }, rm, rl, o);
+        const int used = attend_row<D>(q, keys, it.hk, first * kRows, end, c2, lane, a.err, rm, rl, o);
         const long long srow = stok * a.HQ + shead;
         const long long spart = static_cast<long long>(it.split) * a.B * a.T * a.HQ + srow;
         const float l2 = used == 0 || rl == 0.f ? -INFINITY : rm + log2f(rl);  // (keys that all score -inf: o is 0 / 0)
@@ -931,6 +920,12 @@ cudaError_t launch_attn_prompts(const kda_attn_fwd_args& a, const AttnParts& par
   p.heads = a.HKV * p.sub;
   p.tile_tokens = kRows / p.Gp;
   p.per_token = (65536 + p.Gp - 1) / p.Gp;
+  // Ten seconds, and what 32 rows that a warp computes again may take beside others that do: 2 us
+  // a key and row, four times what one warp alone needs (0.3 us with 64 channels, 0.46 with 128).
+  // (A limit that starts again while such rows go on cost every wait some instructions, and
+  // prompt tiles of two blocks 4 %: 32.3 -> 33.4 us for 64 prompts of up to 333 tokens.)
+  const long long most = a.block_table == nullptr ? a.S : a.seq_lens_k ? static_cast<long long>(a.table_width) * a.page_size : parts.keys;
+  p.limit = 10000000000ull + 64000ull * static_cast<unsigned long long>(most);
   return a.block_table ? launch_width<true>(p, s) : launch_width<false>(p, s);
 }
 
