@@ -29,13 +29,15 @@ __device__ __forceinline__ float below_one(int n) { return static_cast<float>(33
 // running maximum: lane l holds channels l + 32 i. Reads only what the row sees, and
 // follows the definition where infinities and NaN take part: a weight of a finite score
 // is held above 0 (2^-126), so that an infinite value stays one, and a score of -inf
-// weighs 0. The sum l and the values o are relative to 2^m. q is the row already in fp32; scale2 = scale * log2(e). Returns how many
+// weighs 0. The sum l and the values o are relative to 2^m; 1024 keys are added up at a time
+// (one sum would stop growing at 2^24 equal weights). q is the row already in fp32; scale2 = scale * log2(e). Returns how many
 // keys there were (those on pages out of range are left out).
 template <int D>
 __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& s, int h, int begin, int end, float scale2, int lane, int32_t* err,
                                            float& m, float& l, float (&o)[D / 32]) {
   m = -INFINITY, l = 0.f;
   float best = -INFINITY;  // the largest score; m is `below` above it
+  float sum = 0.f, total[D / 32] = {};  // of the 1024s before
   int used = 0;
   bool nan = false;
 #pragma unroll
@@ -43,7 +45,13 @@ __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& 
   const bool nan_row = __any_sync(0xffffffffu, nan);  // (padding that nothing has written, say)
   const float below = below_one(max(end - begin, 0));
   constexpr int N = 4;  // keys whose loads and sums are under way together
+  const auto add = [&]() {
+    sum += l, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) total[i] += o[i], o[i] = 0.f;
+  };
   for (int j0 = begin; j0 < end; j0 += N) {
+    if ((j0 - begin) % 1024 == 0) add();
     float x[N], v[N][D / 32];
     bool there[N];
 #pragma unroll
@@ -81,13 +89,19 @@ __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& 
       if (!there[u]) continue;
       ++used;
       const float top = x[u] > best ? x[u] : best;  // (a NaN leaves it and makes p and l NaN)
-      const float keep = best == top ? 1.f : best == -INFINITY ? 0.f : fmaxf(exp2f(best - top), 1.1754944e-38f);
-      best = top, m = top + below;
+      if (top != best) {  // (in all lanes)
+        const float keep = best == -INFINITY ? 0.f : fmaxf(exp2f(best - top), 1.1754944e-38f);
+        best = top;
+        l *= keep, sum *= keep;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] *= keep, total[i] *= keep;
+      }
+      m = top + below;
       float p = exp2f(x[u] - (top == -INFINITY ? 0.f : m));
       if (x[u] != -INFINITY) p = p < 1.1754944e-38f ? 1.1754944e-38f : p;
-      l = l * keep + p;
+      l += p;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = o[i] * keep + p * v[u][i];
+      for (int i = 0; i < D / 32; ++i) o[i] += p * v[u][i];
     }
     if (l != l || (nan_row && used > 0)) {  // every output is NaN from here on
       l = __uint_as_float(0x7fc00000u);
@@ -96,6 +110,10 @@ __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& 
       return used;
     }
   }
+  add();
+  l = sum;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = total[i];
   return used;
 }
 

@@ -273,3 +273,23 @@ def test_prompts_rows_computed_again_for_long(T, D):
         if a == (N - 1) * T:
             got[-32:, 0, 5] = torch.from_numpy(refs[0][-32:, 0, 5]).float()
         check(got, lse[0, a:a + T], refs, S, D)
+
+
+def test_prompts_long_rows_computed_again():
+    """More equal weights than fp32 can count one by one, in a row that is computed again (7 s)."""
+    P, S, D = 128, 2 ** 24 + 2 ** 23, 64
+    k, v = torch.zeros(3, 1, P, D, dtype=BF), torch.ones(3, 1, P, D, dtype=BF)
+    v[1:] = 2.0
+    v[2, 0, 0, 5] = INF
+    table = torch.zeros(1, S // P, dtype=torch.int32, device="cuda")
+    table[:, S // P // 3:] = 1
+    table[:, -1] = 2
+    lse = torch.zeros(1, 1, 1, device="cuda")
+    o = kda.kda_attn_fwd(torch.zeros(1, 1, 1, D, dtype=BF, device="cuda"), k.cuda(), v.cuda(), scale=0.125, block_table=table,
+                         seq_lens_k=i32([S]), lse=lse)
+    o = o[0, 0, 0].float().cpu()
+    assert o[5] == INF
+    # a third of the values are 1: half a bf16 step, and 2 (2^10 + S / 2^10) fp32 additions
+    bound = (2.0 ** -8 + 2 * (2 ** 10 + S / 2 ** 10) * 2.0 ** -24) * 5 / 3
+    assert (o[torch.arange(D) != 5] - 5 / 3).abs().max() <= bound and bound < 0.02
+    assert abs(float(lse) - np.log(S)) <= (2 ** 10 + S / 2 ** 10) * 2.0 ** -24 + 2.0 ** -20 * np.log(S)
