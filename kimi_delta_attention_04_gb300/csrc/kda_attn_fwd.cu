@@ -46,6 +46,11 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;            // rows of a tile; keys of a block
 constexpr int kHalf = kRows * 128;    // bytes of a block's 64 channels
 constexpr float kGrow = 8.f;          // how far, in powers of two, a row's maximum may pass the one in use
+// The tensor core truncates what it adds to O, by half an ulp of O on the average for each 16 keys:
+// values of one sign came out 0.08 % low at 131072 keys, 0.66 % at 2^20, 10 % at 2^24. After every
+// kHold blocks a row's O is therefore rounded to bf16 into the row's place of the output, and
+// the tensor memory keeps the rest.
+constexpr int kHold = 256;
 
 template <int D, int CTAS>
 struct Shape {
@@ -63,6 +68,7 @@ struct Params {
   int G, Gp, sub, heads;      // Gp query heads to a tile, sub such sets a key head, heads sets in all
   int tile_tokens, per_token; // tokens to a tile; 65536 / Gp rounded up: row r is of token r per_token >> 16
   int slots;                  // places for query tiles
+  long long keys;             // that a sequence may have
   unsigned long long limit;   // how long a wait may last, in ns
 };
 
@@ -83,6 +89,7 @@ struct Head {
   alignas(16) uint32_t next[4];  // the answer to the request for another CTA's place
   Item items[2];
   uint32_t bad[8];            // by block, of the last 8: keys on pages that are out of range, a bit for each 16
+  float held_top[2 * kRows];  // by row: the maximum in use when its O was last held (not in a register: it is rarely looked at)
   uint32_t tmem_base;
   int failed;
 };
@@ -388,7 +395,58 @@ __device__ __forceinline__ bool place_given(const Head& sm, uint32_t& place) {
   return given != 0;
 }
 
-template <int D, bool PAGED, int CTAS>
+// Where a row's rounded part of O is held: its place of the output, or the second half of its
+// (fp32) place among the results to join, which the results are written to from the front.
+template <int D>
+__device__ __forceinline__ __nv_bfloat16* held_row(const Params& p, const Item& it, int ti, int row_head) {
+  const kda_attn_fwd_args& a = p.a;
+  const long long tok = it.q0 + ti;
+  if (p.parts.o == nullptr) return static_cast<__nv_bfloat16*>(a.o) + tok * a.o_stride + static_cast<long long>(it.h0 + row_head) * D;
+  const long long row = static_cast<long long>(it.split) * a.B * a.T * a.HQ + tok * a.HQ + it.h0 + row_head;
+  return reinterpret_cast<__nv_bfloat16*>(p.parts.o + row * D + D / 2);
+}
+
+// What values held under the maximum `was` are worth under `now`.
+__device__ __forceinline__ float held_keep(float was, float now, float c2) { return was == now ? 1.f : ex2_approx((was - now) * c2); }
+
+// Adds what is held, times `keep` (0: there is nothing yet), to a row of O in tensor memory, and, with
+// `out`, holds the sum's bf16 part instead. `held`: nullptr for rows that are not there. A warp.
+// (Rolled up and apart: beside the loop's other instructions it took prompt tiles of two blocks
+// from 32.3 to 34.3 us.)
+template <int D>
+__device__ __forceinline__ void hold(uint32_t o_at, __nv_bfloat16* held, float keep, bool out) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
+    tc05::ld32_wait(o_at + c, o);
+    if (held != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        uint4* at = reinterpret_cast<uint4*>(held + c + j);
+        uint4 r = keep != 0.f ? *at : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float &x = o[j + 2 * e], &y = o[j + 2 * e + 1];
+          x += keep * __uint_as_float(w[e] << 16);
+          y += keep * __uint_as_float(w[e] & 0xffff0000u);
+          if (!out) continue;
+          w[e] = Bf16::pack(x, y);
+          x -= __uint_as_float(w[e] << 16);
+          y -= __uint_as_float(w[e] & 0xffff0000u);
+        }
+        if (out) *at = r;
+      }
+    }
+    __syncwarp();
+    tc05::st32_wait(o_at + c, o);
+  }
+}
+
+// LONG: rows may have more than kHold blocks. (With 64 channels shorter ones have kernels without
+// what these need: 64 prompts of up to 333 tokens 32.9 us instead of 34.3. With 128 it makes no
+// difference.)
+template <int D, bool PAGED, int CTAS, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
     kda_attn_fwd_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
@@ -648,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // blocks below this end need no mask (the tile's first row sees all of them)
     const int open = causal ? min(it.S, own + it.shift + 1) : it.S;
     float top = -INFINITY, sum = 0.f;
-    for (int i = 0; i < count && going; ++i, ++done) {
+    for (int i = 0;;) {
+    for (const int end = LONG ? min(count, i + kHold) : count; i < end && going; ++i, ++done) {
       const bool there = wait(p.limit, &sm.s_full[m], done & 1);  // (looked at below, when nothing waits for it)
       __syncwarp();
       tc05::fence_after_sync();
@@ -736,9 +795,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       going = __all_sync(0xffffffffu, there);
       sum += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
     }
+    if (!LONG || i == count || !going) break;
+    // (S of the next block is there when the product that last changed O is done)
+    going = __all_sync(0xffffffffu, wait(p.limit, &sm.s_full[m], done & 1));
+    if (!going) break;
+    tc05::fence_after_sync();
+    hold<D>(o_at, valid ? held_row<D>(p, it, ti, row_head) : nullptr, i > kHold ? held_keep(sm.held_top[m * kRows + r], top, c2) : 0.f, true);
+    sm.held_top[m * kRows + r] = top;
+    }
     if (going && count > 0) {
       going = __all_sync(0xffffffffu, wait(p.limit, &sm.o_full[m], tiles_done++ & 1));
       tc05::fence_after_sync();
+      if (LONG && count > kHold) hold<D>(o_at, valid ? held_row<D>(p, it, ti, row_head) : nullptr, held_keep(sm.held_top[m * kRows + r], top, c2), false);
     }
     if (going) {
       const long long tok = it.q0 + ti, row = tok * a.HQ + it.h0 + row_head;
@@ -845,7 +913,7 @@ int heads_of_tile(int group) {
   return 1;
 }
 
-template <int D, bool PAGED, int CTAS>
+template <int D, bool PAGED, int CTAS, bool LONG>
 cudaError_t launch(Params p, cudaStream_t s) {
   using Sh = Shape<D, CTAS>;
   const kda_attn_fwd_args& a = p.a;
@@ -873,7 +941,7 @@ cudaError_t launch(Params p, cudaStream_t s) {
   const long long grid = slots * p.heads * p.parts.splits * CTAS;
   if (grid > INT32_MAX) return cudaErrorNotSupported;
   static std::atomic<uint64_t> smem_set{0};
-  const cudaError_t e = set_smem_limit_once(kda_attn_fwd_kernel<D, PAGED, CTAS>, Sh::kSmem, smem_set);
+  const cudaError_t e = set_smem_limit_once(kda_attn_fwd_kernel<D, PAGED, CTAS, LONG>, Sh::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -886,13 +954,13 @@ cudaError_t launch(Params p, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = CTAS > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kda_attn_fwd_kernel<D, PAGED, CTAS>, p, qmap, kmap, vmap);
+  return cudaLaunchKernelEx(&cfg, kda_attn_fwd_kernel<D, PAGED, CTAS, LONG>, p, qmap, kmap, vmap);
 }
 
 template <bool PAGED>
 cudaError_t launch_width(const Params& p, cudaStream_t s) {
   const kda_attn_fwd_args& a = p.a;
-  if (a.D == 64) return launch<64, PAGED, 1>(p, s);
+  if (a.D == 64) return p.keys > kHold * kRows ? launch<64, PAGED, 1, true>(p, s) : launch<64, PAGED, 1, false>(p, s);
   // Pairs of CTAs, each of which holds half of the keys and values, where there are two
   // rounds of them on the 76 pairs of SMs and sequences fill a tile on the average (32 heads
   // of 128 on 8: 64 prompts of up to 512 tokens 116 us with pairs, 130 without; 128 of 256
@@ -900,8 +968,8 @@ cudaError_t launch_width(const Params& p, cudaStream_t s) {
   // and 149).
   const int tokens = 4 * p.tile_tokens;
   const long long each = a.cu_seqlens ? static_cast<long long>(a.T) / a.N : a.T, items = static_cast<long long>(a.B) * a.T / tokens * p.heads;
-  if (p.parts.o == nullptr && each >= tokens && items >= 2 * 76) return launch<128, PAGED, 2>(p, s);
-  return launch<128, PAGED, 1>(p, s);
+  if (p.parts.o == nullptr && each >= tokens && items >= 2 * 76) return launch<128, PAGED, 2, true>(p, s);
+  return launch<128, PAGED, 1, true>(p, s);
 }
 
 }  // namespace
@@ -924,8 +992,8 @@ cudaError_t launch_attn_prompts(const kda_attn_fwd_args& a, const AttnParts& par
   // a key and row, four times what one warp alone needs (0.3 us with 64 channels, 0.46 with 128).
   // (A limit that starts again while such rows go on cost every wait some instructions, and
   // prompt tiles of two blocks 4 %: 32.3 -> 33.4 us for 64 prompts of up to 333 tokens.)
-  const long long most = a.block_table == nullptr ? a.S : a.seq_lens_k ? static_cast<long long>(a.table_width) * a.page_size : parts.keys;
-  p.limit = 10000000000ull + 64000ull * static_cast<unsigned long long>(most);
+  p.keys = a.block_table == nullptr ? a.S : a.seq_lens_k ? static_cast<long long>(a.table_width) * a.page_size : parts.keys;
+  p.limit = 10000000000ull + 64000ull * static_cast<unsigned long long>(p.keys);
   return a.block_table ? launch_width<true>(p, s) : launch_width<false>(p, s);
 }
 

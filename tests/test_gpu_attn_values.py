@@ -293,3 +293,82 @@ def test_prompts_long_rows_computed_again():
     bound = (2.0 ** -8 + 2 * (2 ** 10 + S / 2 ** 10) * 2.0 ** -24) * 5 / 3
     assert (o[torch.arange(D) != 5] - 5 / 3).abs().max() <= bound and bound < 0.02
     assert abs(float(lse) - np.log(S)) <= (2 ** 10 + S / 2 ** 10) * 2.0 ** -24 + 2.0 ** -20 * np.log(S)
+
+
+def weighted(q, k, v, scale, count):
+    """ao.attend of queries q [T, HQ, D] on keys k, v [S, HKV, D] of which each is there count [S] times."""
+    T, HQ, D = q.shape
+    S, G = len(k), HQ // k.shape[1]
+    o, a, lse, top = np.zeros((T, HQ, D)), np.zeros((T, HQ, D)), np.zeros((T, HQ)), np.zeros((T, HQ))
+    for h in range(HQ):
+        kh, vh = np64(k[:, h // G]), np64(v[:, h // G])
+        s = np64(q[:, h]) @ kh.T * scale + np.log(count)
+        m = s.max(-1, keepdims=True)
+        e = np.exp(s - m)
+        p = e / e.sum(-1, keepdims=True)
+        o[:, h], a[:, h], lse[:, h] = p @ vh, p @ np.abs(vh), (m + np.log(e.sum(-1, keepdims=True)))[:, 0]
+        top[:, h] = (np.abs(np64(q[:, h])) @ np.abs(kh).T).max(-1) * scale
+    return o, lse, a, top
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("S", [2 ** 15, 2 ** 15 + 128, 2 ** 16 + 1, 2 ** 20, 2 ** 22])
+@pytest.mark.parametrize("equal", [True, False])
+def test_prompts_long_rows(S, D, equal):
+    """Values of one sign in long rows, whose sum the tensor core truncates with every product."""
+    gen = torch.Generator().manual_seed(S % 1000 + D)
+    P, T, HQ = 128, 45, 3
+    q, k, v = randn(gen, T, HQ, D) * (0.0 if equal else 0.5), randn(gen, 1, 1, P, D), randn(gen, 1, 1, P, D).abs() + 0.5
+    table = torch.zeros(1, -(-S // P), dtype=torch.int32, device="cuda")
+    lse = torch.zeros(1, T, HQ, device="cuda")
+    o = kda.kda_attn_fwd(q[None].cuda(), k.cuda(), v.cuda(), scale=0.125, causal=False, block_table=table, seq_lens_k=i32([S]), lse=lse)
+    refs = weighted(q, k[0].transpose(0, 1), v[0].transpose(0, 1), 0.125, S // P + (np.arange(P) < S % P) + 0.0)
+    # 2^15 keys are 2^11 truncated additions, of up to 2^-23 of the sum, and one of parts in fp32. Equal
+    # weights are exact, and so is their sum; others are off as in attn_cases.errors
+    sums = (2 ** 11 + S / 2 ** 15) * 2.0 ** -23
+    each = 0.0 if equal else 2 * (np.expm1((D / 8 + 6) * 2.0 ** -23 * refs[3]) + 2.0 ** -21 + sums)[..., None] + 2.0 ** -8
+    e = refs[2] * (each + sums)
+    off = np.abs(np64(o[0]) - refs[0])
+    assert (off <= e + 2.0 ** -8 * (np.abs(refs[0]) + e)).all(), f"worst {(off / np.abs(refs[0])).max():.1e}"
+    assert np.abs(np64(lse[0]) - refs[1]).max() <= (0.0 if equal else each.max()) + 2.0 ** -20 * (1 + np.abs(refs[1]).max())
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,T", [(64, 200), (128, 40), (128, 512)])
+def test_prompts_long_rows_whose_maximum_grows(D, T, causal):
+    """Scores that grow after parts of a row's sum were put aside, and earlier keys that still count;
+    512 rows of 128 channels, in 200 sequences: pairs of CTAs."""
+    gen = torch.Generator().manual_seed(D + T)
+    P, N, HQ = 128, 200 if T == 512 else 2, 1
+    S = P * 820 + 31
+    q, k, v = randn(gen, N * T, HQ, D) * 0.5, randn(gen, 3, 1, P, D), randn(gen, 3, 1, P, D).abs() + 0.5
+    q[..., 0] = 8.0
+    for page, score in enumerate((-7.0, 0.0, 6.5)):
+        k[page, ..., 0] = score / (8.0 * 0.125)
+    pages = torch.tensor([0] * 300 + [1] * 500 + [2] * 21, dtype=torch.int32)
+    lse = torch.zeros(1, N * T, HQ, device="cuda")
+    o = kda.kda_attn_fwd(q[None].cuda(), k.cuda(), v.cuda(), scale=0.125, causal=causal, cu_seqlens=i32([n * T for n in range(N + 1)]),
+                         block_table=pages.cuda().repeat(N, 1), seq_lens_k=i32([S] * N), lse=lse)
+    for n in (0, N - 1):
+        for t in sorted({0, 1, 31, 127, 128, T // 2, T - 1} & set(range(T))):
+            r = n * T + t
+            seen = S - T + t + 1 if causal else S
+            count = np.concatenate([[300.0] * P, [500.0] * P, (seen - 800 * P) // P + (np.arange(P) < (seen - 800 * P) % P)])
+            keep = count > 0
+            keys, values = (x.reshape(-1, 1, D)[torch.from_numpy(keep)] for x in (k.transpose(1, 2), v.transpose(1, 2)))
+            refs = weighted(q[r:r + 1], keys, values, 0.125, count[keep])
+            check(o[0, r:r + 1], lse[0, r:r + 1], refs, 2 ** 15, D)
+
+
+def test_step_long_prefix():
+    """Splits of a prefix that are long rows themselves."""
+    gen = torch.Generator().manual_seed(9)
+    P, B, HQ, HKV, D, prefix = 128, 640, 32, 8, 64, 2 ** 20 + 77
+    q, k, v = randn(gen, B, HQ, D) * 0.5, randn(gen, 1, HKV, P, D), randn(gen, 1, HKV, P, D).abs() + 0.5
+    lse = torch.zeros(B, HQ, device="cuda")
+    o = kda.kda_attn_step(q.cuda(), k.cuda(), v.cuda(), torch.zeros(B, 1, dtype=torch.int32, device="cuda"), i32([0] * B), scale=0.125,
+                          prefix_table=torch.zeros(-(-prefix // P), dtype=torch.int32, device="cuda"), prefix_len=prefix, lse=lse)
+    rows = [0, 1, 63, 64, 300, 639]
+    count = prefix // P + (np.arange(P) < prefix % P) + 0.0
+    refs = weighted(q[rows], k[0].transpose(0, 1), v[0].transpose(0, 1), 0.125, count)
+    check(o[rows], lse[rows], refs, 2 ** 15, D)
