@@ -1,5 +1,6 @@
 """Softmax attention on values far apart: cached heads of zeros beside others, scores and
-values of infinity, values near the ends of bf16's range."""
+values of infinity, values near the ends of bf16's range; long rows; and every row of
+prompts that pairs of CTAs work on."""
 
 import numpy as np
 import pytest
@@ -372,3 +373,93 @@ def test_step_long_prefix():
     count = prefix // P + (np.arange(P) < prefix % P) + 0.0
     refs = weighted(q[rows], k[0].transpose(0, 1), v[0].transpose(0, 1), 0.125, count)
     check(o[rows], lse[rows], refs, 2 ** 15, D)
+
+
+# --- prompts that pairs of CTAs work on: every row ---
+
+def exact(q, k, v, scale, seen):
+    """ao.attend on the GPU in 64 bits: q [T, HQ, D], k and v [S, HKV, D], seen [T] keys a query sees."""
+    q, k, v = (x.cuda().double() for x in (q, k, v))
+    T, HQ, D = q.shape
+    S, G = len(k), q.shape[1] // k.shape[1]
+    o, a, lse, top = (torch.zeros(T, HQ, *n, dtype=torch.float64, device="cuda") for n in ((D,), (D,), (), ()))
+    hidden = torch.arange(S, device="cuda")[None] >= torch.as_tensor(seen, device="cuda")[:, None]
+    for h in range(HQ):
+        kh, vh = k[:, h // G], v[:, h // G]
+        s = (q[:, h] @ kh.T * scale).masked_fill(hidden, -INF)
+        lse[:, h] = torch.logsumexp(s, 1)
+        p = torch.nan_to_num(torch.softmax(s, 1))
+        o[:, h], a[:, h] = p @ vh, p @ vh.abs()
+        if S:
+            top[:, h] = (q[:, h].abs() @ kh.abs().T * scale).masked_fill(hidden, 0.0).amax(1)
+    return tuple(x.cpu().numpy() for x in (o, lse, a, top))
+
+
+@pytest.mark.parametrize("P", [0, 16, 64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_every_row_of_many_tiles(P, causal):
+    """Outputs and logarithms of all rows: one key of 1400 too many or too few moves a logarithm by 7e-4."""
+    gen = torch.Generator().manual_seed(43 + P)
+    HQ, HKV, D = 64, 4, 128
+    lens, lens_k = (701, 0, 1025, 3), (701, 9, 1400, 130)
+    if not P:
+        lens_k = (701, 9, 1025, 3)
+    T, S = sum(lens), sum(lens_k)
+    q, k, v = randn(gen, T, HQ, D), randn(gen, S, HKV, D), randn(gen, S, HKV, D)
+    offs, offs_k = np.cumsum([0] + list(lens)), np.cumsum([0] + list(lens_k))
+    ks, vs = ([x[a:b] for a, b in zip(offs_k[:-1], offs_k[1:])] for x in (k, v))
+    lse = torch.zeros(1, T, HQ, device="cuda")
+    kw = dict(scale=0.09, causal=causal, lse=lse, cu_seqlens=i32(offs.tolist()))
+    if P:
+        cache = Cache(gen, ks, vs, P).cuda()
+        o = kda.kda_attn_fwd(q[None].cuda(), cache.k, cache.v, block_table=cache.table, seq_lens_k=cache.lens, **kw)
+    else:
+        o = kda.kda_attn_fwd(q[None].cuda(), k[None].cuda(), v[None].cuda(), cu_seqlens_k=i32(offs_k.tolist()), **kw)
+    for n in range(4):
+        a, b = offs[n], offs[n + 1]
+        if a == b:
+            continue
+        refs = exact(q[a:b], ks[n], vs[n], float(np.float32(0.09)), ao.seen_keys(lens[n], lens_k[n], causal))
+        check(o[0, a:b], lse[0, a:b], refs, lens_k[n], D)
+
+
+@pytest.mark.parametrize("what", [INF, -INF, NAN])
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("at,channel", [(300, 17), (300, 100), (460, 17), (460, 100), (2499, 64)])
+def test_prompts_hidden_values_of_many_tiles(what, where, at, channel):
+    """A bad key or value in each half of a block's keys and of the channels, which two CTAs hold: only
+    the queries that see it change, and those to what the definition gives."""
+    gen = torch.Generator().manual_seed(at)
+    T, HQ, HKV, D = 2500, 64, 4, 128
+    q, k, v = randn(gen, T, HQ, D), randn(gen, T, HKV, D), randn(gen, T, HKV, D)
+    own = slice(16, 32)  # the heads on key head 1
+    clean_lse, lse = torch.zeros(1, T, HQ, device="cuda"), torch.zeros(1, T, HQ, device="cuda")
+    clean = kda.kda_attn_fwd(q[None].cuda(), k[None].cuda(), v[None].cuda(), scale=0.09, lse=clean_lse)
+    (k if where == "k" else v)[at, 1, channel] = what
+    got = kda.kda_attn_fwd(q[None].cuda(), k[None].cuda(), v[None].cuda(), scale=0.09, lse=lse)
+    others = [h for h in range(HQ) if not 16 <= h < 32]
+    assert torch.equal(got[0][:, others], clean[0][:, others]) and torch.equal(lse[0][:, others], clean_lse[0][:, others])
+    bad = (k if where == "k" else v)[:, 1:2].clone()
+    (k if where == "k" else v)[at, 1, channel] = 0.0
+    seen = ao.seen_keys(T, T, True)
+    scale = float(np.float32(0.09))
+    refs = exact(q[:, own], k[:, 1:2], v[:, 1:2], scale, seen)
+    before, rest = got[0, :at, own], got[0, at:, own].float().cpu()
+    # rows that do not see it: as if it were not there
+    check(before, lse[0, :at, own], tuple(r[:at] for r in refs), T, D)
+    if where == "v":
+        want = torch.full((T - at, 16), what)
+        assert torch.equal(torch.nan_to_num(rest[..., channel], nan=5.0, posinf=6.0, neginf=7.0), torch.nan_to_num(want, nan=5.0, posinf=6.0, neginf=7.0))
+        keep = [d for d in range(D) if d != channel]
+        check(rest[..., keep], lse[0, at:, own], tuple(r[at:][..., keep] if r.ndim == 3 else r[at:] for r in refs), T, D)
+    elif what != what:
+        assert torch.isnan(rest).all()
+    else:  # scores of +inf or -inf by the sign of q: NaN, or the key left out
+        pos = q[at:, own, channel].float() * what > 0
+        assert torch.isnan(rest[pos]).all()
+        without = [j for j in range(T) if j != at]
+        refs = exact(q[at:, own], k[without, 1:2], v[without, 1:2], scale, seen[at:] - 1)
+        fixed, fixed_lse = rest.clone(), lse[0, at:, own].cpu().clone()
+        fixed[pos], fixed_lse[pos] = torch.from_numpy(refs[0]).float()[pos], torch.from_numpy(refs[1]).float()[pos]
+        check(fixed, fixed_lse, refs, T, D)
+    assert torch.isfinite(bad.float()).sum() == bad.numel() - 1
