@@ -862,6 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (again != 0) {
         const int src = __ffs(again) - 1;
         again &= again - 1;
+        __syncwarp();  // (the row's own lane has stored what all lanes store again)
         const long long stok = __shfl_sync(0xffffffffu, tok, src);
         const int shead = __shfl_sync(0xffffffffu, it.h0 + row_head, src);
         const int end = min(__shfl_sync(0xffffffffu, limit, src), (first + count) * kRows);
