@@ -637,7 +637,7 @@ kda_status kda_kv_append(const kda_kv_append_args* args, kda_stream_t stream);
  * infinities and NaN of v, or scores that are not finite, reach are computed again one by
  * one, at about 1000 times the cost (a warp takes 0.3 to 0.5 us a key). Every wait in the
  * kernel is bounded; one that runs out (after ten seconds and 64 us for each key that a sequence
- * may have: S, or what the table has room for) writes KDA_ERR_TIMEOUT to err and ends the call
+ * may have: S, or what the table has room for, at least 32768) writes KDA_ERR_TIMEOUT to err and ends the call
  * without its results.
  * Resources: 512 columns of tensor memory on each SM while the kernel runs.
  */

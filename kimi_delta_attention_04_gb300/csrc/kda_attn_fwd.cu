@@ -69,7 +69,7 @@ struct Params {
   int tile_tokens, per_token; // tokens to a tile; 65536 / Gp rounded up: row r is of token r per_token >> 16
   int slots;                  // places for query tiles
   long long keys;             // that a sequence may have
-  unsigned long long limit;   // how long a wait may last, in ns
+  unsigned long long limit;   // how long a wait may last, in ns, in the kernels for long rows
 };
 
 // What a CTA works on next.
@@ -114,11 +114,19 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-// Waits for a phase, for at most `limit` ns; whether it came. (One statement, and callers that look
+// How long a wait may last where a sequence may have so many keys: ten seconds, and what 32 rows
+// that a warp computes again may take beside others that do, 2 us a key and row (four times what
+// one warp alone needs: 0.3 us with 64 channels, 0.46 with 128). (A limit that starts again while
+// such rows go on cost every wait some instructions, and prompt tiles of two blocks 4 %: 32.3 ->
+// 33.4 us for 64 prompts of up to 333 tokens; one that is not a constant 0.6 %.)
+__host__ __device__ constexpr unsigned long long wait_limit(long long keys) { return 10000000000ull + 64000ull * static_cast<unsigned long long>(keys); }
+
+// Waits for a phase, for a limited time; whether it came. (One statement, and callers that look
 // at the results seldom: with the loop and its exits in the compiler's hands each wait of the
 // thread that issues products left the tensor core idle for 140 cycles instead of 40. No hint that
 // lets the thread sleep: 395 us instead of 407 for 8192 tokens and 32 heads of 128.)
-__device__ __forceinline__ bool wait(unsigned long long limit, uint64_t* bar, uint32_t parity) {
+template <bool LONG>
+__device__ __forceinline__ bool wait(const Params& p, uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .b64 t0, t1;\n"
@@ -127,7 +135,7 @@ __device__ __forceinline__ bool wait(unsigned long long limit, uint64_t* bar, ui
       " sub.u64 t1, t1, t0;\n setp.lt.u64 q, t1, %3;\n @q bra AGAIN;\n mov.u32 %0, 0;\n bra END;\n"
       "DONE:\n mov.u32 %0, 1;\nEND:\n}\n"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "l"(limit)
+      : "r"(smem_u32(bar)), "r"(parity), "l"(LONG ? p.limit : wait_limit(kHold * kRows))
       : "memory");
   return ok != 0;
 }
@@ -198,7 +206,7 @@ __device__ __forceinline__ void load_tile(void* smem, const CUtensorMap* map, in
 // cycles each, where a thread chosen by its lane took 140. A warp for each tile's products
 // interleaves them, and each waits longer for its own: 444 us instead of 395 for 8192
 // tokens and 32 heads of 128.)
-template <int D, int CTAS>
+template <int D, int CTAS, bool LONG>
 __device__ __forceinline__ bool issue_products(const Params& p, Head& sm, const unsigned char* tiles) {
   using Sh = Shape<D, CTAS>;
   constexpr uint32_t qk = tc05::idesc_f16kind(CTAS * kRows, kRows, true), pv = tc05::idesc_f16kind(CTAS * kRows, D, true) | tc05::kIdescBMnMajor;
@@ -224,18 +232,18 @@ __device__ __forceinline__ bool issue_products(const Params& p, Head& sm, const 
     if (++s == Sh::kStages) s = 0, phase ^= 1;
   };
   for (int k = 0; going; ++k) {
-    going = wait(p.limit, &sm.item_full[k & 1], (k >> 1) & 1);
+    going = wait<LONG>(p, &sm.item_full[k & 1], (k >> 1) & 1);
     if (!going) break;
     const Item& it = sm.items[k & 1];
     if (it.n < 0) break;
     const int count0 = it.count[0], count1 = it.count[1], blocks = max(count0, count1), keys = it.S - it.first * kRows;
     if (blocks > 0) {
-      going = wait(p.limit, &sm.full[s], phase);
+      going = wait<LONG>(p, &sm.full[s], phase);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int count = m == 0 ? count0 : count1;
         if (count == 0) continue;
-        going = going && wait(p.limit, &sm.q_full[m], tiles_done[m]++ & 1);
+        going = going && wait<LONG>(p, &sm.q_full[m], tiles_done[m]++ & 1);
         tc05::fence_after_sync();
         if (going) scores(m, s);
         if (count == 1) commit<CTAS>(&sm.q_empty[m]);
@@ -247,16 +255,16 @@ __device__ __forceinline__ bool issue_products(const Params& p, Head& sm, const 
     // blocks that both tiles use and that others follow: no conditions between the products
     for (const int both = min(count0, count1) - 1; i < both && going; ++i) {
       const int vs = s;
-      bool there = wait(p.limit, &sm.full[vs], phase);
+      bool there = wait<LONG>(p, &sm.full[vs], phase);
       advance();
-      there &= wait(p.limit, &sm.full[s], phase);
+      there &= wait<LONG>(p, &sm.full[s], phase);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int parity = done[m]++ & 1;
-        there &= wait(p.limit, &sm.p_full[m][0], parity);
+        there &= wait<LONG>(p, &sm.p_full[m][0], parity);
         tc05::fence_after_sync();
         values(m, vs, 0, 4, i > 0);
-        there &= wait(p.limit, &sm.p_full[m][1], parity);
+        there &= wait<LONG>(p, &sm.p_full[m][1], parity);
         tc05::fence_after_sync();
         values(m, vs, 4, kRows / 16, true);
         scores(m, s);
@@ -270,8 +278,8 @@ __device__ __forceinline__ bool issue_products(const Params& p, Head& sm, const 
     for (; i < blocks && going; ++i) {
       const int vs = s, v_phase = phase;  // the block's values; the next block's keys come after them
       advance();
-      going = wait(p.limit, &sm.full[vs], v_phase);
-      if (i + 1 < blocks) going = going && wait(p.limit, &sm.full[s], phase);
+      going = wait<LONG>(p, &sm.full[vs], v_phase);
+      if (i + 1 < blocks) going = going && wait<LONG>(p, &sm.full[s], phase);
       const bool tail = keys < (i + 1) * kRows;  // the sequence's last block is not full: zeros behind its last key
       if (tail && going) {
         mbar_arrive_local(&sm.tail_there);
@@ -283,11 +291,11 @@ __device__ __forceinline__ bool issue_products(const Params& p, Head& sm, const 
         if (i >= count || !going) continue;
         const bool last_v = m == 1 || i >= count1, last_k = m == 1 || i + 1 >= count1;  // no other tile needs the block
         const int parity = done[m]++ & 1;
-        going = wait(p.limit, &sm.p_full[m][0], parity);
-        if (tail) going = going && wait(p.limit, &sm.tail_zero, tails & 1);
+        going = wait<LONG>(p, &sm.p_full[m][0], parity);
+        if (tail) going = going && wait<LONG>(p, &sm.tail_zero, tails & 1);
         tc05::fence_after_sync();
         if (going) values(m, vs, 0, 4, i > 0);
-        going = going && wait(p.limit, &sm.p_full[m][1], parity);
+        going = going && wait<LONG>(p, &sm.p_full[m][1], parity);
         tc05::fence_after_sync();
         if (going) values(m, vs, 4, kRows / 16, true);
         if (i + 1 < count) {
@@ -306,7 +314,7 @@ __device__ __forceinline__ bool issue_products(const Params& p, Head& sm, const 
   }
   if (!going) {  // products in flight end before their tensor memory is given back
     commit<CTAS>(&sm.drain);
-    wait(p.limit, &sm.drain, 0);
+    wait<LONG>(p, &sm.drain, 0);
   }
   return going;
 }
@@ -533,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool going = true;
       int loaded = 0, blocks_done = 0, tiles_done[2] = {0, 0};
       for (int k = 0; going; ++k) {
-        going = __all_sync(0xffffffffu, wait(p.limit, &sm.item_full[k & 1], (k >> 1) & 1));
+        going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.item_full[k & 1], (k >> 1) & 1));
         if (!going) break;
         const Item it = sm.items[k & 1];
         if (it.n < 0) break;
@@ -541,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           if (it.count[m] == 0 || !going) continue;
-          if (tiles_done[m] > 0) going = __all_sync(0xffffffffu, wait(p.limit, &sm.q_empty[m], (tiles_done[m] - 1) & 1));
+          if (tiles_done[m] > 0) going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.q_empty[m], (tiles_done[m] - 1) & 1));
           if (!going) continue;
           ++tiles_done[m];
           if (lane == 0) {
@@ -584,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const int s = loaded % Sh::kStages;
-            if (loaded >= Sh::kStages) going = __all_sync(0xffffffffu, wait(p.limit, &sm.empty[s], (loaded / Sh::kStages - 1) & 1));
+            if (loaded >= Sh::kStages) going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.empty[s], (loaded / Sh::kStages - 1) & 1));
             if (!going) break;
             if (lane == 0) {
               // (before the keys' arrival, and so before their scores; the loads are at most 5
@@ -608,31 +616,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       // counted in its first CTA, and neither CTA ends before the other)
       bool idle = going;
       for (int m = 0; m < 2; ++m)
-        if (idle && tiles_done[m] > 0) idle = wait(p.limit, &sm.q_empty[m], (tiles_done[m] - 1) & 1);
-      for (int i = max(0, loaded - Sh::kStages); i < loaded && idle; ++i) idle = wait(p.limit, &sm.empty[i % Sh::kStages], (i / Sh::kStages) & 1);
+        if (idle && tiles_done[m] > 0) idle = wait<LONG>(p, &sm.q_empty[m], (tiles_done[m] - 1) & 1);
+      for (int i = max(0, loaded - Sh::kStages); i < loaded && idle; ++i) idle = wait<LONG>(p, &sm.empty[i % Sh::kStages], (i / Sh::kStages) & 1);
       if (!idle && rank == 0) {
         bool there = true;
         for (int m = 0; m < 2; ++m)
-          if (there && tiles_done[m] > 0) there = wait(p.limit, &sm.q_full[m], (tiles_done[m] - 1) & 1);
-        for (int i = max(0, loaded - Sh::kStages); i < loaded && there; ++i) there = wait(p.limit, &sm.full[i % Sh::kStages], (i / Sh::kStages) & 1);
+          if (there && tiles_done[m] > 0) there = wait<LONG>(p, &sm.q_full[m], (tiles_done[m] - 1) & 1);
+        for (int i = max(0, loaded - Sh::kStages); i < loaded && there; ++i) there = wait<LONG>(p, &sm.full[i % Sh::kStages], (i / Sh::kStages) & 1);
       }
       going = idle;
       if (!going) sm.failed = 1;
     } else if (warp == 8) {
-      if (rank == 0 && elect_one() && !issue_products<D, CTAS>(p, sm, tiles)) sm.failed = 1;
+      if (rank == 0 && elect_one() && !issue_products<D, CTAS, LONG>(p, sm, tiles)) sm.failed = 1;
     } else if (warp == 10) {
       // ---- what stands behind the last key may be anything: zeros in its place ----
       bool going = true;
       int loaded = 0, tails = 0;
       for (int k = 0; going; ++k) {
-        going = __all_sync(0xffffffffu, wait(p.limit, &sm.item_full[k & 1], (k >> 1) & 1));
+        going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.item_full[k & 1], (k >> 1) & 1));
         if (!going) break;
         const Item it = sm.items[k & 1];
         if (it.n < 0) break;
         const int most = max(it.count[0], it.count[1]), live = it.S - (it.first + most - 1) * kRows;
         if (most > 0 && live < kRows) {
           const int s = (loaded + 2 * most - 1) % Sh::kStages;
-          going = __all_sync(0xffffffffu, wait(p.limit, &sm.tail_there, tails++ & 1));
+          going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.tail_there, tails++ & 1));
           if (!going) break;
           unsigned char* v = ring + s * Sh::kTile;
           for (int c = 0; c < D / 64 / CTAS; ++c)
@@ -657,12 +665,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it;
         if (!more) it.n = -1;
         if (!more || item_of<PAGED, CTAS>(p, place / CTAS, lane, it)) {
-          if (k >= 2) going = __all_sync(0xffffffffu, wait(p.limit, &sm.item_empty[k & 1], ((k >> 1) - 1) & 1));
+          if (k >= 2) going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.item_empty[k & 1], ((k >> 1) - 1) & 1));
           if (going && lane == 0) {
             sm.items[k & 1] = it;
             mbar_arrive_local(&sm.item_full[k & 1]);
           }
-          if (more && going) going = __all_sync(0xffffffffu, wait(p.limit, &sm.item_near, k & 1));
+          if (more && going) going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.item_near, k & 1));
           ++k;
         }
         if (!more || !going) break;
@@ -671,11 +679,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx_local(&sm.next_there, 16);
           arrive_first<CTAS>(&sm.ready);
         }
-        if (rank == 0) going = __all_sync(0xffffffffu, wait(p.limit, &sm.ready, asked & 1));
+        if (rank == 0) going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.ready, asked & 1));
         if (going && rank == 0 && lane == 0) ask_for_place<CTAS>(sm);
         ++asked;
         if (!going) break;
-        going = __all_sync(0xffffffffu, wait(p.limit, &sm.next_there, (asked - 1) & 1));
+        going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.next_there, (asked - 1) & 1));
         if (!going) break;
         more = place_given(sm, place);
         fence_proxy_async_smem();  // (the next answer is written after this one has been read)
@@ -694,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool going = true;
     int done = 0, tiles_done = 0, blocks_done = 0;
     for (int k = 0; going; ++k) {
-    going = __all_sync(0xffffffffu, wait(p.limit, &sm.item_full[k & 1], (k >> 1) & 1));
+    going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.item_full[k & 1], (k >> 1) & 1));
     if (!going) break;
     const Item& it = sm.items[k & 1];
     if (it.n < 0) break;
@@ -708,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float top = -INFINITY, sum = 0.f;
     for (int i = 0;;) {
     for (const int end = LONG ? min(count, i + kHold) : count; i < end && going; ++i, ++done) {
-      const bool there = wait(p.limit, &sm.s_full[m], done & 1);  // (looked at below, when nothing waits for it)
+      const bool there = wait<LONG>(p, &sm.s_full[m], done & 1);  // (looked at below, when nothing waits for it)
       __syncwarp();
       tc05::fence_after_sync();
       const int k0 = (first + i) * kRows;
@@ -750,8 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // block's is found: it rarely changes after the first blocks (in pairs, 8192 tokens and
       // 32 heads: 312 us instead of 337). With 64, where a block's products are half as long
       // and short prompts are nothing but first blocks, after it (64 prompts of up to 333
-      // tokens: 33 us instead of 36).
-      constexpr bool kAhead = D == 128;
+      // tokens: 33 us instead of 36; 64 of 512: 184 and 200; 8192 tokens, 32 heads: 279 and
+      // 278), but in the kernels for long rows (40000 tokens, 8 heads: 1560 and 1420).
+      constexpr bool kAhead = D == 128 || LONG;
       if (kAhead) restart();
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -797,14 +806,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!LONG || i == count || !going) break;
     // (S of the next block is there when the product that last changed O is done)
-    going = __all_sync(0xffffffffu, wait(p.limit, &sm.s_full[m], done & 1));
+    going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.s_full[m], done & 1));
     if (!going) break;
     tc05::fence_after_sync();
     hold<D>(o_at, valid ? held_row<D>(p, it, ti, row_head) : nullptr, i > kHold ? held_keep(sm.held_top[m * kRows + r], top, c2) : 0.f, true);
     sm.held_top[m * kRows + r] = top;
     }
     if (going && count > 0) {
-      going = __all_sync(0xffffffffu, wait(p.limit, &sm.o_full[m], tiles_done++ & 1));
+      going = __all_sync(0xffffffffu, wait<LONG>(p, &sm.o_full[m], tiles_done++ & 1));
       tc05::fence_after_sync();
       if (LONG && count > kHold) hold<D>(o_at, valid ? held_row<D>(p, it, ti, row_head) : nullptr, held_keep(sm.held_top[m * kRows + r], top, c2), false);
     }
@@ -989,12 +998,8 @@ cudaError_t launch_attn_prompts(const kda_attn_fwd_args& a, const AttnParts& par
   p.heads = a.HKV * p.sub;
   p.tile_tokens = kRows / p.Gp;
   p.per_token = (65536 + p.Gp - 1) / p.Gp;
-  // Ten seconds, and what 32 rows that a warp computes again may take beside others that do: 2 us
-  // a key and row, four times what one warp alone needs (0.3 us with 64 channels, 0.46 with 128).
-  // (A limit that starts again while such rows go on cost every wait some instructions, and
-  // prompt tiles of two blocks 4 %: 32.3 -> 33.4 us for 64 prompts of up to 333 tokens.)
   p.keys = a.block_table == nullptr ? a.S : a.seq_lens_k ? static_cast<long long>(a.table_width) * a.page_size : parts.keys;
-  p.limit = 10000000000ull + 64000ull * static_cast<unsigned long long>(p.keys);
+  p.limit = wait_limit(p.keys);
   return a.block_table ? launch_width<true>(p, s) : launch_width<false>(p, s);
 }
 
