@@ -25,16 +25,21 @@ struct Keys {
 // infinite, its mean is not).
 __device__ __forceinline__ float below_one(int n) { return static_cast<float>(33 - __clz(n)); }
 
-// Attention of one row of queries over keys [begin, end), one warp, each key in turn with a
-// running maximum: lane l holds channels l + 32 i. Reads only what the row sees, and
-// follows the definition where infinities and NaN take part: a weight of a finite score
-// is held above 0 (2^-126), so that an infinite value stays one, and a score of -inf
-// weighs 0. The sum l and the values o are relative to 2^m; 1024 keys are added up at a time
-// (one sum would stop growing at 2^24 equal weights). q is the row already in fp32; scale2 = scale * log2(e). Returns how many
-// keys there were (those on pages out of range are left out).
-template <int D>
-__device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& s, int h, int begin, int end, float scale2, int lane, int32_t* err,
-                                           float& m, float& l, float (&o)[D / 32]) {
+// A value times a weight that may have left fp32's range downwards: infinities stay.
+__device__ __forceinline__ float weighed(float v, float w) { return fabsf(v) == INFINITY ? v : v * w; }
+
+// Attention of one row of queries over `count` keys, the tokens token(0), token(1), ..; one
+// warp, each key in turn with a running maximum: lane l holds channels l + 32 i. Reads only
+// what the row sees, and follows the definition where infinities and NaN take part: a score of
+// -inf weighs 0, a finite one always more than that, so that an infinite value stays one (and
+// a finite one adds what fp32 has of its weight, which may be nothing). The sum l and the
+// values o are relative to 2^m, which is 2^below above the largest score; 1024 keys are added
+// up at a time (one sum would stop growing at 2^24 equal weights). q is the row already in
+// fp32; scale2 = scale * log2(e). Returns how many keys there were (those on pages out of range
+// are left out).
+template <int D, typename Token>
+__device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& s, int h, int count, const Token& token, float below, float scale2,
+                                           int lane, int32_t* err, float& m, float& l, float (&o)[D / 32]) {
   m = -INFINITY, l = 0.f;
   float best = -INFINITY;  // the largest score; m is `below` above it
   float sum = 0.f, total[D / 32] = {};  // of the 1024s before
@@ -43,25 +48,24 @@ __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& 
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = 0.f, nan |= q[i] != q[i];
   const bool nan_row = __any_sync(0xffffffffu, nan);  // (padding that nothing has written, say)
-  const float below = below_one(max(end - begin, 0));
   constexpr int N = 4;  // keys whose loads and sums are under way together
   const auto add = [&]() {
     sum += l, l = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) total[i] += o[i], o[i] = 0.f;
   };
-  for (int j0 = begin; j0 < end; j0 += N) {
-    if ((j0 - begin) % 1024 == 0) add();
+  for (int j0 = 0; j0 < count; j0 += N) {
+    if (j0 % 1024 == 0) add();
     float x[N], v[N][D / 32];
     bool there[N];
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-      const int j = j0 + u;
-      there[u] = j < end;
+      there[u] = j0 + u < count;
       x[u] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) v[u][i] = 0.f;
       if (!there[u]) continue;
+      const int j = token(j0 + u);
       long long ka, va;
       if (s.table != nullptr) {
         const int page = s.table[j / s.page_size];
@@ -90,18 +94,17 @@ __device__ __forceinline__ int attend_row(const float (&q)[D / 32], const Keys& 
       ++used;
       const float top = x[u] > best ? x[u] : best;  // (a NaN leaves it and makes p and l NaN)
       if (top != best) {  // (in all lanes)
-        const float keep = best == -INFINITY ? 0.f : fmaxf(exp2f(best - top), 1.1754944e-38f);
+        const float keep = best == -INFINITY ? 0.f : exp2f(best - top);
         best = top;
         l *= keep, sum *= keep;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] *= keep, total[i] *= keep;
+        for (int i = 0; i < D / 32; ++i) o[i] = weighed(o[i], keep), total[i] = weighed(total[i], keep);
       }
       m = top + below;
-      float p = exp2f(x[u] - (top == -INFINITY ? 0.f : m));
-      if (x[u] != -INFINITY) p = p < 1.1754944e-38f ? 1.1754944e-38f : p;
+      const float p = exp2f(x[u] - (top == -INFINITY ? 0.f : m));
       l += p;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] += p * v[u][i];
+      for (int i = 0; i < D / 32; ++i) o[i] += x[u] == -INFINITY ? 0.f * v[u][i] : weighed(v[u][i], p);
     }
     if (l != l || (nan_row && used > 0)) {  // every output is NaN from here on
       l = __uint_as_float(0x7fc00000u);

@@ -881,7 +881,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
           q[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[stok * a.q_stride + static_cast<long long>(shead) * D + lane + 32 * c]);
-        const int used = attend_row<D>(q, keys, it.hk, first * kRows, end, c2, lane, a.err, rm, rl, o);
+        const int begin = first * kRows, seen = max(end - begin, 0);
+        const int used = attend_row<D>(q, keys, it.hk, seen, [begin](int j) { return begin + j; }, below_one(seen), c2, lane, a.err, rm, rl, o);
         const long long srow = stok * a.HQ + shead;
         const long long spart = static_cast<long long>(it.split) * a.B * a.T * a.HQ + srow;
         const float l2 = used == 0 || rl == 0.f ? -INFINITY : rm + log2f(rl);  // (keys that all score -inf: o is 0 / 0)

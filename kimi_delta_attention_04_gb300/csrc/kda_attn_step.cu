@@ -30,7 +30,6 @@ using namespace attn;
 
 constexpr int kGroup = 16;       // tokens that the products take at once; divides every page
 constexpr int kMaxSplits = 8;    // CTAs of a cluster
-constexpr float kTiny = 1.1754944e-38f;
 // The f16 weights of 8-bit values: 2^kTopWeight is the largest, and down to kWeightBits below it,
 // 2^-17, a rounding is at most 2^-8 (half of f16's smallest step, 2^-24). Smaller ones are taken in
 // kParts - 1 further parts, each kWeightBits wide, the last one open (its roundings grow below
@@ -99,19 +98,20 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   return v;
 }
 
-// One partial result (maximum m in powers of two, sum l, weighted values o) joined to
-// another. A part without keys has m = -inf and l = 0 and changes nothing.
+// One partial result (sum l and weighted values o, relative to 2^m) joined to another. A part
+// without keys has m = -inf and l = 0 and changes nothing.
 struct Joined {
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   __device__ __forceinline__ void add(float pm, float pl, float4 po) {
     if (pm == -INFINITY && pl == 0.f) return;
     const float top = pm > m ? pm : m;
-    const float a = m == -INFINITY ? 0.f : fmaxf(exp2f(m - top), kTiny);
-    const float b = pm == -INFINITY ? 0.f : pm == top ? 1.f : pm != pm ? pm : fmaxf(exp2f(pm - top), kTiny);
+    const float a = m == -INFINITY ? 0.f : exp2f(m - top);
+    const float b = pm == -INFINITY ? 0.f : pm == top ? 1.f : exp2f(pm - top);
     m = top;
     l = l * a + pl * b;
-    o.x = o.x * a + po.x * b, o.y = o.y * a + po.y * b, o.z = o.z * a + po.z * b, o.w = o.w * a + po.w * b;
+    o.x = weighed(o.x, a) + weighed(po.x, b), o.y = weighed(o.y, a) + weighed(po.y, b);
+    o.z = weighed(o.z, a) + weighed(po.z, b), o.w = weighed(o.w, a) + weighed(po.w, b);
   }
 };
 
@@ -123,10 +123,8 @@ __device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// What results under the maximum `was` are worth under `now`, at least 2^-126 (0 where there was none).
-__device__ __forceinline__ float factor(float was, float now) {
-  return was == now ? 1.f : was == -INFINITY ? 0.f : fmaxf(ex2_approx(was - now), kTiny);
-}
+// What results under the maximum `was` are worth under `now`.
+__device__ __forceinline__ float factor(float was, float now) { return was == now ? 1.f : was == -INFINITY ? 0.f : ex2_approx(was - now); }
 
 // Adds the results in the workspace for a row and head, 4 channels from d. A logarithm of -inf
 // is a part without keys, or with keys that weigh nothing, which has NaN as its values: where
@@ -181,7 +179,7 @@ __global__ void __launch_bounds__(128) kda_attn_join_kernel(const __grid_constan
 }
 
 // (Where there are many CTAs, as many fit an SM as the registers can be held to without spills: with
-// 64 channels and up to 8 heads four, 256 rows of about 2000 tokens 138 us, cold; 148 with three.)
+// 64 channels and up to 8 heads four, 256 rows of about 2000 tokens 134 us, cold; 148 with three.)
 template <int D, bool E4, int WARPS, bool MANY, int ROWS>
 __global__ void __launch_bounds__(32 * WARPS, MANY ? (D == 64 && ROWS == 1 ? 4 : 3) : 1) kda_attn_step_kernel(const __grid_constant__ Params p) {
   using Sh = Shape<D, E4, WARPS, MANY>;
@@ -317,8 +315,7 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? (D == 64 && ROWS == 1 ? 4 :
     }
   };
 
-  // running maximum of the scores, sum of the weights (relative to 2^below times the maximum's: what is
-  // added up over the row stays below the largest value, also across warps and CTAs), and, with 8-bit values, the maximum of the
+  // running maximum of the scores, sum of the weights, and, with 8-bit values, the maximum of the
   // weights times their values' scales, of which o is relative to 2^-kTopWeight (its own otherwise)
   float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, mv[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -414,7 +411,7 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? (D == 64 && ROWS == 1 ? 4 :
         if (ROWS > 1) o[j][2] *= keep[1], o[j][3] *= keep[1];
       }
     }
-    const float mz[2] = {m[0] == -INFINITY ? 0.f : m[0] + below, m[1] == -INFINITY ? 0.f : m[1] + below};
+    const float mz[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
     const float mvz[2] = {mv[0] == -INFINITY ? 0.f : mv[0] - kTopWeight, mv[1] == -INFINITY ? 0.f : mv[1] - kTopWeight};
     // by their bits, exponents of weights below the limit and above -inf: from the limit's own
     // bits (0) up to those of -inf; all other values, NaN among them, come out larger
@@ -425,10 +422,7 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? (D == 64 && ROWS == 1 ? 4 :
     for (int n = 0; n < N; ++n) {
 #pragma unroll
       for (int e = 0; e < 2 * ROWS; ++e) {
-        const float x = sc[n][e];
-        // (a weight of a finite score stays above 0: an infinite value stays one)
-        float w = ex2_approx(x - mz[e >> 1]);
-        w = x == -INFINITY ? 0.f : w < kTiny ? kTiny : w;
+        float w = ex2_approx(sc[n][e] - mz[e >> 1]);
         l[e >> 1] += w;
         if (E4) {
           const float y = sd[n][e] - mvz[e >> 1];
@@ -498,15 +492,25 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? (D == 64 && ROWS == 1 ? 4 :
     cp_async_commit();
   }
   cp_async_wait<0>();
-  if (E4) {
-    // o relative to what the sum is relative to again (in two factors: one might leave the range)
-    const float down = exp2f(-kTopWeight - below);
+  // Results relative to 2^below times the maximum's weight: what the joins add up over the row stays
+  // below the largest value. (8 bits: o is relative to the maximum of its own so far. In two factors:
+  // one might leave the range.)
+  const float down = exp2f(-below);
+  bool redo[2] = {false, false};
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float by = mv[r] == -INFINITY ? (mv[r] == m[r] ? 1.f : 0.f) : exp2f(mv[r] - m[r]);
+  for (int r = 0; r < ROWS; ++r) {
+    const float by = !E4 || mv[r] == m[r] ? 1.f : mv[r] == -INFINITY ? 0.f : exp2f(mv[r] - m[r]), f = E4 ? down * exp2f(-kTopWeight) : down;
+    float finite = 0.f;
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) o[j][2 * r] = o[j][2 * r] * down * by, o[j][2 * r + 1] = o[j][2 * r + 1] * down * by;
+    for (int j = 0; j < D / 8; ++j) {
+#pragma unroll
+      for (int e = 2 * r; e < 2 * r + 2; ++e) {
+        finite = fmaf(o[j][e], 0.f, finite);
+        o[j][e] = o[j][e] * f * by;
+      }
     }
+    redo[r] = !E4 && finite != finite;
+    l[r] *= down;
   }
   if (any_bad && lane == 0) set_err(a.err, KDA_ERR_INVALID_ARG);
 
@@ -529,6 +533,31 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? (D == 64 && ROWS == 1 ? 4 :
   if (t == 0) {
     warp_m[warp][g] = m[0] + below, warp_m[warp][g + 8] = m[1] + below;
     warp_l[warp][g] = l[0], warp_l[warp][g + 8] = l[1];
+  }
+  if (!E4) {
+    // Heads that an infinity, or a sum past fp32, is in, again, one by one: a weight that rounds to 0
+    // made NaN of an infinite value. (Weights held above 0 instead gave values of 1e38 weights that
+    // they do not have.) Where the sum of the weights is NaN the results are.
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      uint32_t again = __ballot_sync(0xffffffffu, redo[r] && l[r] == l[r] && g + 8 * r < heads);
+      while (again != 0) {
+        const int head = (__ffs(again) - 1) / 4;
+        again &= ~(0xfu << (4 * head));
+        const int row = head + 8 * r;
+        const Keys keys = {a.k_cache, a.v_cache, table, a.pages, a.page_size, a.HKV, 0, 0, 0};
+        const int last = (first + (steps - 1) * step) * T, count = (steps - 1) * T + min(T, len - last);  // of this warp's tokens
+        float x[D / 32], y[D / 32], rm, rl;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          x[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[b * a.q_stride + static_cast<long long>(head0 + row) * D + lane + 32 * c]);
+        attend_row<D>(x, keys, h, count, [first, step](int j) { return (first + j / T * step) * T + j % T; }, below, a.scale * kLog2e, lane, a.err, rm, rl, y);
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) mine[row * (D + 4) + lane + 32 * c] = y[c];
+        if (lane == 0) warp_m[warp][row] = rm, warp_l[warp][row] = rl;
+      }
+    }
   }
   __syncthreads();
   if (used && lane == 0) cta_used = 1;

@@ -62,7 +62,7 @@ def steps(cache, n, q, scale, layout, prefix=None):
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("HQ,HKV,D,P", [(4, 1, 128, 16), (10, 1, 128, 64), (4, 2, 64, 16)])
 @pytest.mark.parametrize("n,spread,nats", [
-    (32, 1e-6, 0), (1000, 0.1, 10), (2100, 0.02, 12), (2100, 1.0, 12), (700, 0.02, 25), (700, 1e-6, 40), (40, 1e-24, 3), (700, 3e30, 30)])
+    (32, 1e-6, 0), (1000, 0.1, 10), (2100, 0.02, 12), (2100, 1.0, 12), (700, 0.02, 25), (700, 1e-6, 40), (40, 1e-24, 3), (700, 3e30, 30), (700, 1e-31, 20)])
 def test_step_zero_heads_beside_others(layout, HQ, HKV, D, P, n, spread, nats):
     """A head of zeros with a large score takes most of the weight and adds nothing: what the
     others give comes out as exactly as without it."""
@@ -183,6 +183,55 @@ def test_step_infinite_scores(layout):
     refs = ao.attend(np64(q[:, :2]), np64(k[:, :1]), np64(v[:, :1]), 0.125, [n])
     for r in range(2):
         check(o[r:r + 1, :2], lse[r:r + 1, :2], refs, n, D)
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("n", [5, 700, 1601])
+@pytest.mark.parametrize("infinite", [False, True])
+def test_step_large_values_without_weight(dtype, layout, n, infinite):
+    """Values of 1e38 with weights of exp(-400) add nothing, in other tokens' parts of the row or beside
+    them, also where an infinity makes the row one of a kind."""
+    if infinite and dtype == E4:
+        pytest.skip("8-bit values have no infinity")
+    gen = torch.Generator().manual_seed(n)
+    HQ, HKV, D, P = 4, 2, 64, 16
+    q, k, v = randn(gen, 1, HQ, D), randn(gen, n, HKV, D), randn(gen, n, HKV, D)
+    q[..., 0], k[..., 0] = 32.0, 0.0
+    for at in (0, n // 2, n - 2):
+        k[at, :, 0], v[at, :, 20:30] = -100.0, 1e38
+    if infinite:
+        v[n // 2, :, 3] = INF
+    cache = Cache(gen, [k], [v], P, dtype)
+    tokens = cache.tokens(0)
+    if infinite:
+        tokens[1][n // 2, :, 3] = 0.0
+    refs = ao.attend(np64(q), *tokens, 0.125, [n])
+    o, lse = steps(cache.cuda(), n, q, 0.125, layout)
+    got = o.float().cpu()
+    if infinite:
+        assert (got[..., 3] == INF).all()
+        got[..., 3] = torch.from_numpy(refs[0][..., 3]).float()
+    for r in range(2):
+        check(got[r:r + 1], lse[r:r + 1], refs, n, D)
+
+
+def test_prompts_large_values_without_weight():
+    """The same in rows of a prompt that are computed again."""
+    gen = torch.Generator().manual_seed(8)
+    T, HQ, HKV, D = 300, 4, 2, 128
+    q, k, v = randn(gen, T, HQ, D), randn(gen, T, HKV, D), randn(gen, T, HKV, D)
+    q[..., 0], k[..., 0] = 32.0, 0.0
+    k[100, :, 0], v[100, :, 20:30] = -100.0, 1e38
+    v[7, :, 3], v[100, :, 4] = INF, -INF
+    lse = torch.zeros(1, T, HQ, device="cuda")
+    o = kda.kda_attn_fwd(q[None].cuda(), k[None].cuda(), v[None].cuda(), scale=0.125, lse=lse)
+    got = o[0].float().cpu()
+    assert (got[7:, :, 3] == INF).all() and (got[100:, :, 4] == -INF).all()
+    v[7, :, 3], v[100, :, 4] = 0.0, 0.0
+    refs = ao.attend(np64(q), np64(k), np64(v), 0.125, ao.seen_keys(T, T, True))
+    got[7:, :, 3], got[100:, :, 4] = (torch.from_numpy(refs[0][a:, :, c]).float() for a, c in ((7, 3), (100, 4)))
+    check(got, lse[0], refs, T, D)
 
 
 # --- values near the end of the range: their mean is there, their sum is not ---
