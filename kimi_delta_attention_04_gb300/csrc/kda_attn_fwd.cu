@@ -451,9 +451,9 @@ __device__ __forceinline__ void hold(uint32_t o_at, __nv_bfloat16* held, float k
   }
 }
 
-// LONG: rows may have more than kHold blocks. (With 64 channels shorter ones have kernels without
-// what these need: 64 prompts of up to 333 tokens 32.9 us instead of 34.3. With 128 it makes no
-// difference.)
+// LONG: rows may have more than kHold blocks. Shorter ones have kernels without what these need (64
+// prompts of up to 333 tokens, heads of 64: 32.4 us instead of 34.3; 128 prompts of 256, heads of
+// 128: 179 instead of 181).
 template <int D, bool PAGED, int CTAS, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
     kda_attn_fwd_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -968,10 +968,10 @@ cudaError_t launch(Params p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kda_attn_fwd_kernel<D, PAGED, CTAS, LONG>, p, qmap, kmap, vmap);
 }
 
-template <bool PAGED>
+template <bool PAGED, bool LONG>
 cudaError_t launch_width(const Params& p, cudaStream_t s) {
   const kda_attn_fwd_args& a = p.a;
-  if (a.D == 64) return p.keys > kHold * kRows ? launch<64, PAGED, 1, true>(p, s) : launch<64, PAGED, 1, false>(p, s);
+  if (a.D == 64) return launch<64, PAGED, 1, LONG>(p, s);
   // Pairs of CTAs, each of which holds half of the keys and values, where there are two
   // rounds of them on the 76 pairs of SMs and sequences fill a tile on the average (32 heads
   // of 128 on 8: 64 prompts of up to 512 tokens 116 us with pairs, 130 without; 128 of 256
@@ -979,8 +979,8 @@ cudaError_t launch_width(const Params& p, cudaStream_t s) {
   // and 149).
   const int tokens = 4 * p.tile_tokens;
   const long long each = a.cu_seqlens ? static_cast<long long>(a.T) / a.N : a.T, items = static_cast<long long>(a.B) * a.T / tokens * p.heads;
-  if (p.parts.o == nullptr && each >= tokens && items >= 2 * 76) return launch<128, PAGED, 2, true>(p, s);
-  return launch<128, PAGED, 1, true>(p, s);
+  if (p.parts.o == nullptr && each >= tokens && items >= 2 * 76) return launch<128, PAGED, 2, LONG>(p, s);
+  return launch<128, PAGED, 1, LONG>(p, s);
 }
 
 }  // namespace
@@ -1001,7 +1001,8 @@ cudaError_t launch_attn_prompts(const kda_attn_fwd_args& a, const AttnParts& par
   p.per_token = (65536 + p.Gp - 1) / p.Gp;
   p.keys = a.block_table == nullptr ? a.S : a.seq_lens_k ? static_cast<long long>(a.table_width) * a.page_size : parts.keys;
   p.limit = wait_limit(p.keys);
-  return a.block_table ? launch_width<true>(p, s) : launch_width<false>(p, s);
+  if (p.keys > kHold * kRows) return a.block_table ? launch_width<true, true>(p, s) : launch_width<false, true>(p, s);
+  return a.block_table ? launch_width<true, false>(p, s) : launch_width<false, false>(p, s);
 }
 
 cudaError_t launch_attn_fwd(const kda_attn_fwd_args& a, cudaStream_t s) { return launch_attn_prompts(a, AttnParts{nullptr, nullptr, 1, 0}, s); }
