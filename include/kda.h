@@ -683,6 +683,8 @@ kda_status kda_attn_fwd(const kda_attn_fwd_args* args, kda_stream_t stream);
  * below 2^-36 lost. With a bf16 cache, heads of a row that an infinity or a NaN of v reaches, or
  * whose sum of weighted values passes fp32, are computed again token by token (a warp takes 0.3 to
  * 0.5 us for each of its tokens).
+ * How a row's tokens are split over CTAs goes by table_width * page_size, not by seq_lens: tables
+ * much wider than the rows cost time (most CTAs find nothing to do).
  */
 typedef struct kda_attn_step_args {
   int32_t B, HQ, HKV, D;

@@ -952,7 +952,8 @@ def kda_kv_append(k, v, slots, k_cache, v_cache, *, q=None, positions=None, cos_
     place. positions int32 [...] and cos_sin fp32 [positions, rot] (cosines, then sines)
     turn the first rot channels of q and k, in halves or in neighbouring pairs
     (interleaved). q_out may be q; k_out, filled when given, may be k. check_indices (needs
-    err): a debug check that the valid slots are distinct. Returns (q_out or None, k_out)."""
+    err): a debug check that the valid slots are distinct. Returns (q_out or None, k_out),
+    without gradients."""
     lib = _lib or load()
     dev = _device_of(k)
     if k.dim() < 2:
@@ -1004,7 +1005,8 @@ def kda_attn_fwd(q, k, v, *, scale, causal=True, cu_seqlens=None, cu_seqlens_k=N
     cu_seqlens int32 [N + 1] packs N sequences along T (B = 1), cu_seqlens_k their keys
     (default: the same). causal: query i of a sequence of T sees keys up to i + S - T.
     lse (fp32 [B, T, HQ]) receives the logarithm of the sums when given. Rows of o and
-    lse behind the last sequence are left as they were. Returns o [B, T, HQ, D]."""
+    lse behind the last sequence are left as they were. Returns o [B, T, HQ, D], without
+    gradients."""
     lib = _lib or load()
     dev = _device_of(q)
     if q.dim() != 4 or k.dim() != 4:
@@ -1057,7 +1059,9 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, *, scale, k_scale=
 
     lse (fp32 [B, HQ]) receives the logarithm of the sums when given. With a prefix, or a
     table for KDA_ATTN_LONG_TOKENS tokens or more, workspace (a CUDA uint8 tensor of
-    kda_attn_step_workspace_size bytes) is made here unless given. Returns o [B, HQ, D]."""
+    kda_attn_step_workspace_size bytes) is made here unless given. How rows are split goes by
+    the table's width: one much wider than the rows costs time. Returns o [B, HQ, D],
+    without gradients."""
     lib = _lib or load()
     dev = _device_of(q)
     if q.dim() != 3 or block_table.dim() != 2:

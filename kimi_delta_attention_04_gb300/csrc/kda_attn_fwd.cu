@@ -10,14 +10,17 @@
 // While one tile's rows are in the exponentials, the other's products run. O stays in
 // tensor memory and is scaled again only when a row's maximum has grown by more than
 // 2^8 (the weights stay below that, in bf16 and in the sums' fp32), which after the first
-// blocks is rare. P is rounded to bf16, as V is; l adds the unrounded weights.
+// blocks is rare. P is rounded to bf16, as V is (at most 2^-8 of a weight; outputs are 2.1e-3 to 2.3e-3
+// off in the mean square, 1.7e-3 by their own rounding); l adds the unrounded weights. (Two tiles in
+// turn, and scaling O again only for large growth, are published methods for fused attention on
+// these tensor cores, not this file's own.)
 //
 // Bound: the products, 1024 cycles of the tensor core for a tile and block of 128 channels.
 // Alone, a CTA's ring of five keys' or values' tiles (160 KB beside 64 KB of queries) is
 // short for what a load takes; a pair of CTAs (cta_group::2) makes each product 256 rows
 // wide, each CTA holds half of the keys (rows) and of the values (channels), and the ring
-// lasts twice as long. One 8192-token prompt, 32 heads of 128 on 8: 312 us, 1.76 PFLOP/s,
-// 93 % of the rate of a large matrix product; single CTAs 335.
+// lasts twice as long. One 8192-token prompt, 32 heads of 128 on 8: 311 to 315 us, 1.75 PFLOP/s,
+// 92 % of the rate of a large matrix product; single CTAs 335.
 //
 // Roles: warps 0-3 and 4-7 the rows of the two tiles (200 registers a thread: a row's 128
 // scores are held at once), warp 8 issues the products (in a pair the first CTA's, for
@@ -30,7 +33,7 @@
 // memory (they may hold anything). A NaN or an infinity in the values of a key that some
 // rows of a tile see and others do not still meets a weight of 0 in the product; rows
 // whose result is not finite are therefore computed again by attend_row, which reads only
-// what the row sees.
+// what the row sees (0.3 to 0.5 us a key for a row and warp, about 1000 times the cost).
 #include "kda_attn.cuh"
 #include "kda_attn_fwd.h"
 #include "kda_cluster.cuh"
@@ -756,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // With 128 channels, the first half's weights under the maximum in use, while this
       // block's is found: it rarely changes after the first blocks (in pairs, 8192 tokens and
-      // 32 heads: 312 us instead of 337). With 64, where a block's products are half as long
+      // 32 heads: 314 us instead of 337). With 64, where a block's products are half as long
       // and short prompts are nothing but first blocks, after it (64 prompts of up to 333
       // tokens: 33 us instead of 36; 64 of 512: 184 and 200; 8192 tokens, 32 heads: 279 and
       // 278), but in the kernels for long rows (40000 tokens, 8 heads: 1560 and 1420).

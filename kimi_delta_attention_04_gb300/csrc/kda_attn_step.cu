@@ -17,7 +17,7 @@
 // bf16 cache; the sum takes unrounded ones. f16 holds the largest weight times scale at 2^15;
 // tokens more than 2^32 below it have products of their own (a head of zeros has the scale 1,
 // far above others', and sets that maximum though it adds nothing). 256 rows of about 2000
-// tokens: 194 us, as without the look for such tokens; cold caches: 207 us, and 278 where a head
+// tokens: 191 us, as without the look for such tokens; cold caches: 205 us, and 278 where a head
 // of zeros is 40 nats above all others of every row.
 #include "kda_attn.cuh"
 #include "kda_attn_fwd.h"
