@@ -678,7 +678,8 @@ kda_status kda_attn_fwd(const kda_attn_fwd_args* args, kda_stream_t stream);
  * Sums and softmax in fp32. For their product with v the weights p are rounded to bf16, and for
  * a row's own tokens in an 8-bit cache, after v's factors, to f16: off by at most 2^-8 of
  * themselves (2^-11 above 2^-29 of the row's largest), down to 2^-96 of the row's largest weight
- * times factor; those below 2^-105 of it add nothing. With an 8-bit cache q is rounded to f16 after
+ * times factor, and to 2^-128 where a head's sums so far stay below 2^-25 of that times 448; those
+ * below add nothing. With an 8-bit cache q is rounded to f16 after
  * a power of two of the head's own: values of q down to 2^-27 of the head's largest are exact, those
  * below 2^-36 lost. With a bf16 cache, heads of a row that an infinity or a NaN of v reaches, or
  * whose sum of weighted values passes fp32, are computed again token by token (a warp takes 0.3 to

@@ -32,10 +32,9 @@ constexpr int kGroup = 16;       // tokens that the products take at once; divid
 constexpr int kMaxSplits = 8;    // CTAs of a cluster
 // The f16 weights of 8-bit values: 2^kTopWeight is the largest, and down to kWeightBits below it,
 // 2^-17, a rounding is at most 2^-8 (half of f16's smallest step, 2^-24). Smaller ones are taken in
-// kParts - 1 further parts, each kWeightBits wide, the last one open (its roundings grow below
-// 2^-96 of the largest, and nothing is left at 2^-105).
+// kParts - 1 further parts, each kWeightBits wide: to 2^-128 of the largest.
 constexpr float kTopWeight = 15.f;
-constexpr int kWeightBits = 32, kParts = 3;
+constexpr int kWeightBits = 32, kParts = 4;
 
 struct Params {
   kda_attn_step_args a;
@@ -433,9 +432,12 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? (D == 64 && ROWS == 1 ? 4 :
       }
     }
     // With weights below the limit: those in f16's reach first, then the next kWeightBits as if they
-    // were and what is summed so far lifted with them (by 2^64 at most, from 2^53: 2^15 * 448 for
-    // 2^29 tokens), and so on. In one loop: a second copy of the products took 40 registers more.
+    // were and what is summed so far lifted with them, and so on while the sums have room: they are
+    // up to 2^53 (2^15 * 448 for 2^29 tokens), which two lifts leave below 2^117. Heads that are all
+    // but zeros, whose small weights count, have room for the third. In one loop: a second copy
+    // of the products took 40 registers more.
     const int parts = E4 && __any_sync(0xffffffffu, small < past) ? kParts : 1;
+    float most = 0.f;  // of the sums
 #pragma unroll 1
     for (int part = 0;;) {
       if (E4 && parts > 1) {
@@ -444,7 +446,7 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? (D == 64 && ROWS == 1 ? 4 :
 #pragma unroll
           for (int e = 0; e < 2 * ROWS; ++e) {
             const float y = sd[n][e] - mvz[e >> 1] + static_cast<float>(kWeightBits * part);
-            const bool here = part == 0 ? !(y < kLimit) : y < kTopWeight && (part == kParts - 1 || y >= kLimit);
+            const bool here = part == 0 ? !(y < kLimit) : y < kTopWeight && y >= kLimit;
             sc[n][e] = here ? ex2_approx(y) : 0.f;
           }
         }
@@ -479,13 +481,15 @@ __global__ void __launch_bounds__(32 * WARPS, MANY ? (D == 64 && ROWS == 1 ? 4 :
       }
       if (!E4 || parts == 1) break;
       ++part;
-      const float by = __uint_as_float(static_cast<uint32_t>(127 + (part == kParts ? 1 - kParts : 1) * kWeightBits) << 23);
+      const bool more = part < kParts && __all_sync(0xffffffffu, most < 0x1p89f);  // (and this part's products below 2^54)
+      const float by = __uint_as_float(static_cast<uint32_t>(127 + (more ? 1 : 1 - part) * kWeightBits) << 23);
+      most = 0.f;
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
 #pragma unroll
-        for (int e = 0; e < 2 * ROWS; ++e) o[j][e] *= by;
+        for (int e = 0; e < 2 * ROWS; ++e) o[j][e] *= by, most = fmaxf(most, fabsf(o[j][e]));
       }
-      if (part == kParts) break;
+      if (!more) break;
     }
     __syncwarp();
     if (i + Sh::kStages - 1 < steps) load(i + Sh::kStages - 1);

@@ -62,7 +62,7 @@ def steps(cache, n, q, scale, layout, prefix=None):
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("HQ,HKV,D,P", [(4, 1, 128, 16), (10, 1, 128, 64), (4, 2, 64, 16)])
 @pytest.mark.parametrize("n,spread,nats", [
-    (32, 1e-6, 0), (1000, 0.1, 10), (2100, 0.02, 12), (2100, 1.0, 12), (700, 0.02, 25), (700, 1e-6, 40), (40, 1e-24, 3), (700, 3e30, 30), (700, 1e-31, 20)])
+    (32, 1e-6, 0), (1000, 0.1, 10), (2100, 0.02, 12), (2100, 1.0, 12), (700, 0.02, 25), (700, 1e-6, 40), (40, 1e-24, 3), (700, 3e30, 30), (700, 1e-31, 20), (700, 1e-3, 60), (40, 1e-28, 1)])
 def test_step_zero_heads_beside_others(layout, HQ, HKV, D, P, n, spread, nats):
     """A head of zeros with a large score takes most of the weight and adds nothing: what the
     others give comes out as exactly as without it."""
